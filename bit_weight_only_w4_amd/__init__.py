@@ -6,7 +6,8 @@ if the library is not built, every call raises ``RuntimeError``.
 
 Formats are named ``"nf4_f16"``, ``"nf4_bf16"``, ``"int4_f16"`` and ``"int4_bf16"`` (weight format
 x activation dtype).  Scales are fp32 ``[N, K/64]`` for NF4 and bf16 bit patterns stored in an
-int16 tensor ``[N, K/128]`` for INT4.
+int16 tensor ``[N, K/128]`` for INT4.  ``"fp4_*"`` (E2M1, NF4's layout), ``"int4a_*"`` (int32 words
+``[N, K/128]``) and ``"mxfp4_*"`` (E2M1, uint8 power-of-two scales ``[N, K/32]``) are the others.
 """
 from __future__ import annotations
 
@@ -17,7 +18,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libw4.so")
 
 FORMATS = {"nf4_f16": 1, "nf4_bf16": 2, "int4_f16": 3, "int4_bf16": 4, "fp4_f16": 5, "fp4_bf16": 6,
-           "int4a_f16": 7, "int4a_bf16": 8}
+           "int4a_f16": 7, "int4a_bf16": 8, "mxfp4_f16": 16, "mxfp4_bf16": 17}
 PATHS = {"auto": 0, "gemv": 1, "splitk": 2, "mfma": 3, "twopass": 4, "tiled": 5, "tiled_f16": 6}
 PATH_NAMES = {v: k for k, v in PATHS.items()}
 STATUS = {0: "OK", -1: "NULL", -2: "SHAPE", -3: "ALIGN", -4: "FORMAT", -5: "NONFINITE",
@@ -55,6 +56,7 @@ def lib() -> ctypes.CDLL:
         L.w4_quantize_int4.argtypes = [vp, i64, i64, vp, vp, vp]
         L.w4_quantize_fp4.argtypes = [vp, i64, i64, vp, vp, vp]
         L.w4_quantize_int4_asym.argtypes = [vp, i64, i64, vp, vp, vp]
+        L.w4_quantize_mxfp4.argtypes = [vp, i64, i64, vp, vp, vp]
         L.w4_gptq_block_update.argtypes = [vp, vp, vp, vp, i64, i64, i64, ci, ci, i64, i64, vp, vp,
                                            vp, vp]
         L.w4_gptq_lazy_update.argtypes = [vp, vp, vp, i64, i64, i64, i64, vp]
@@ -86,7 +88,7 @@ def lib() -> ctypes.CDLL:
         L.w4_get_path.argtypes = []
         L.w4_set_workspace.argtypes = [vp, sz]
         for name in ("w4_quantize_nf4", "w4_quantize_int4", "w4_quantize_fp4", "w4_quantize_int4_asym",
-                     "w4_gemv", "w4_gemm_smallbatch", "w4_matmul_ex", "w4_auto_path",
+                     "w4_quantize_mxfp4", "w4_gemv", "w4_gemm_smallbatch", "w4_matmul_ex", "w4_auto_path",
                      "w4_gemv_plan", "w4_version", "w4_probe_read", "w4_probe_copy",
                      "w4_gemv_grouped", "w4_gemv_grouped_plan", "w4_gemm_smallbatch_grouped",
                      "w4_gemm_prefill", "w4_gptq_block_update", "w4_gptq_lazy_update",
@@ -205,8 +207,24 @@ def quantize_int4_asym(w, stream=None):
     return packed, words
 
 
+def quantize_mxfp4(w, stream=None):
+    """fp32 [N, K] device weights -> (packed uint8 [N, K/2], scale uint8 [N, K/32]) in MXFP4: E2M1
+    codes, scale 2^(byte - 127) per block of 32."""
+    import torch
+
+    _need_cuda(w)
+    if w.dtype != torch.float32 or w.dim() != 2:
+        raise ValueError("w must be a 2-D float32 tensor")
+    n, k = w.shape
+    packed = torch.empty((n, k // 2), dtype=torch.uint8, device=w.device)
+    scale = torch.empty((n, max(k // 32, 1)), dtype=torch.uint8, device=w.device)
+    check(lib().w4_quantize_mxfp4(_ptr(w), n, k, _ptr(packed), _ptr(scale), _stream(stream)),
+          "w4_quantize_mxfp4")
+    return packed, scale
+
+
 def weight_format(fmt: str) -> str:
-    """"nf4", "int4", "int4a" or "fp4": the weight encoding of a format name such as "fp4_bf16"."""
+    """"nf4", "int4", "int4a", "fp4" or "mxfp4": the weight encoding of a format name such as "fp4_bf16"."""
     if fmt not in FORMATS:
         raise ValueError(f"unknown format {fmt!r}")
     return fmt.split("_")[0]
@@ -216,7 +234,7 @@ def quantize(fmt: str, w, stream=None):
     """Quantize fp32 [N, K] device weights in the weight encoding of `fmt` (activation type aside):
     the packed nibbles and the scales that the matmul entry points take for that format."""
     q = {"nf4": quantize_nf4, "int4": quantize_int4, "int4a": quantize_int4_asym,
-         "fp4": quantize_fp4}[weight_format(fmt)]
+         "fp4": quantize_fp4, "mxfp4": quantize_mxfp4}[weight_format(fmt)]
     return q(w, stream)
 
 

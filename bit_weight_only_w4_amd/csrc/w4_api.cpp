@@ -101,8 +101,12 @@ Steer current_steer() {
 bool valid_fmt(int fmt) {
   return fmt == W4_NF4_X_F16 || fmt == W4_NF4_X_BF16 || fmt == W4_INT4_X_F16 ||
          fmt == W4_INT4_X_BF16 || fmt == W4_FP4_X_F16 || fmt == W4_FP4_X_BF16 ||
-         fmt == W4_INT4A_X_F16 || fmt == W4_INT4A_X_BF16;
+         fmt == W4_INT4A_X_F16 || fmt == W4_INT4A_X_BF16 || fmt == W4_MXFP4_X_F16 ||
+         fmt == W4_MXFP4_X_BF16;
 }
+
+// MXFP4 has the fused GEMV and the MFMA kernel only.
+bool is_mxfp4(int fmt) { return fmt_weight(fmt) == kMXFP4; }
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -374,6 +378,7 @@ int run_tiled_f16(const void* x, const uint8_t* packed, const void* scales, int 
 
 int run_tiled(const void* x, const uint8_t* packed, const void* scales, int fmt, int64_t n,
               int64_t k, int64_t b, float* y, hipStream_t st, int splits = 1, void* ws = nullptr) {
+  if (is_mxfp4(fmt)) return W4_ERR_PATH;
   const hipError_t e = launch_gemm(fmt, reinterpret_cast<const uint16_t*>(x), packed, scales, n, k,
                                    b, y, st, splits, reinterpret_cast<float*>(ws));
   if (e == hipErrorNotSupported) return W4_ERR_PATH;
@@ -457,7 +462,7 @@ int validate_group(const void* x, int groups, const uint8_t* const* packed,
 int run_group(const void* x, int groups, const uint8_t* const* packed, const void* const* scales,
               const int64_t* n, float* const* y, int fmt, int64_t k, int64_t b, bool mfma,
               hipStream_t s) {
-  if (mfma && b >= W4_TILED_FROM_BATCH) {
+  if (mfma && b >= W4_TILED_FROM_BATCH && !is_mxfp4(fmt)) {
     const uint8_t* tp[kMaxGroup];
     const void* ts[kMaxGroup];
     int64_t tn[kMaxGroup];
@@ -570,6 +575,24 @@ int w4_quantize_fp4(const float* w, int64_t n, int64_t k, uint8_t* packed, float
   return flag ? W4_ERR_NONFINITE : W4_OK;
 }
 
+int w4_quantize_mxfp4(const float* w, int64_t n, int64_t k, uint8_t* packed, uint8_t* scale,
+                      void* stream) {
+  if (!w || !packed || !scale) return W4_ERR_NULL;
+  if (n < 1 || k < 64 || k % 64 != 0 || n >= kMaxDim || k >= kMaxDim) return W4_ERR_SHAPE;
+  if (!aligned(w, 8) || !aligned(packed, 16) || !aligned(scale, 2)) return W4_ERR_ALIGN;
+  if (overlaps(w, (size_t)(n * k) * 4, packed, (size_t)(n * k / 2)) ||
+      overlaps(w, (size_t)(n * k) * 4, scale, (size_t)(n * k / 32)) ||
+      overlaps(packed, (size_t)(n * k / 2), scale, (size_t)(n * k / 32)))
+    return W4_ERR_ALIAS;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  std::lock_guard<std::mutex> lock(g_flag_mu);
+  if (quantize_error_reset(s) != hipSuccess) return W4_ERR_HIP;
+  if (launch_quantize_mxfp4(w, n, k, packed, scale, s) != hipSuccess) return W4_ERR_HIP;
+  int flag = 0;
+  if (quantize_error_read(&flag, s) != hipSuccess) return W4_ERR_HIP;
+  return flag ? W4_ERR_NONFINITE : W4_OK;
+}
+
 int w4_quantize_int4_asym(const float* w, int64_t n, int64_t k, uint8_t* packed, uint32_t* words,
                           void* stream) {
   if (!w || !packed || !words) return W4_ERR_NULL;
@@ -614,6 +637,7 @@ size_t w4_workspace_bytes(int fmt, int64_t n, int64_t k, int64_t b, int path, in
     case W4_PATH_SPLITK: return splitk_bytes(n, b, split_k > 1 ? split_k : 4);
     case W4_PATH_MFMA: return split_k > 1 ? splitk_bytes(n, b, split_k) : 0;
     case W4_PATH_TILED: {
+      if (is_mxfp4(fmt)) return 0;
       const int ranges = split_k > 1 && split_k <= W4_MAX_SPLIT_K ? gemm_splits_used(k, split_k) : 1;
       return ranges > 1 ? splitk_bytes(n, b, ranges) : 0;
     }
@@ -623,7 +647,7 @@ size_t w4_workspace_bytes(int fmt, int64_t n, int64_t k, int64_t b, int path, in
           split_k > 1 && split_k <= W4_MAX_SPLIT_K ? gemm_fold_ranges(fmt, k, split_k, nullptr) : 1;
       return ranges > 1 ? splitk_bytes(n, b, ranges) : 0;
     }
-    case W4_PATH_TWOPASS: return (size_t)n * (size_t)k * 2;
+    case W4_PATH_TWOPASS: return is_mxfp4(fmt) ? 0 : (size_t)n * (size_t)k * 2;
     case W4_PATH_AUTO: {
       int sk = 1;
       const int p = w4_auto_path(fmt, n, k, b, SIZE_MAX, &sk);
@@ -682,11 +706,12 @@ int w4_auto_path(int fmt, int64_t n, int64_t k, int64_t b, size_t workspace_byte
   int s = 1;
   int path;
   GemvPlan p;
-  if (prefer_tiled(n, b)) {
+  const bool tiled = !is_mxfp4(fmt);
+  if (tiled && prefer_tiled(n, b)) {
     path = W4_PATH_TILED;
     int st = 1;
     if (prefer_tiled_split(fmt, n, k, b, workspace_bytes, &st)) s = st;
-  } else if (prefer_tiled_split(fmt, n, k, b, workspace_bytes, &s)) {
+  } else if (tiled && prefer_tiled_split(fmt, n, k, b, workspace_bytes, &s)) {
     path = W4_PATH_TILED;
   } else if (prefer_mfma(n, k, b) || !plan_gemv(n, k, (int)b, 1, &p)) {
     path = W4_PATH_MFMA;
@@ -742,6 +767,7 @@ int w4_matmul_ex(const void* x, const uint8_t* packed, const void* scales, int f
       return run_mfma(x, packed, scales, fmt, n, k, b, y, s, split_k, workspace);
     }
     case W4_PATH_TILED: {
+      if (is_mxfp4(fmt)) return W4_ERR_PATH;
       if (split_k <= 1) return run_tiled(x, packed, scales, fmt, n, k, b, y, s);
       if (split_k > W4_MAX_SPLIT_K) return W4_ERR_PATH;
       const int ranges = gemm_splits_used(k, split_k);
@@ -763,6 +789,7 @@ int w4_matmul_ex(const void* x, const uint8_t* packed, const void* scales, int f
       return run_tiled_f16(x, packed, scales, fmt, n, k, b, y, s, split_k, workspace);
     }
     case W4_PATH_TWOPASS: {
+      if (is_mxfp4(fmt)) return W4_ERR_PATH;  // 2^(e - 127) codes need not fit fp16
       const size_t used = (size_t)n * (size_t)k * 2;
       if (!workspace || workspace_bytes < used) return W4_ERR_WORKSPACE;
       if (workspace_overlaps_inputs(workspace, used, x, packed, scales, fmt, n, k, b))
@@ -861,7 +888,9 @@ int w4_gemm_prefill(const void* x, const uint8_t* packed, const void* scales, in
                     int64_t k, int64_t b, float* y, void* stream) {
   const int st = validate(x, packed, scales, fmt, n, k, b, y);
   if (st != W4_OK) return st;
-  return run_tiled(x, packed, scales, fmt, n, k, b, y, reinterpret_cast<hipStream_t>(stream));
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (is_mxfp4(fmt)) return run_mfma(x, packed, scales, fmt, n, k, b, y, s);
+  return run_tiled(x, packed, scales, fmt, n, k, b, y, s);
 }
 
 int w4_probe_read(const void* src, size_t bytes, uint32_t* sink, void* stream) {

@@ -83,8 +83,9 @@ __device__ inline uint32_t buffer_load16bit(__amdgpu_buffer_rsrc_t r, uint32_t o
 // 16-entry table; INT4 has groups of 128 with a bf16 scale; asymmetric INT4 (INT4A) has the same
 // groups with a 32-bit word per group (bf16 scale in bits 0-15, zero point z in bits 16-19).
 // INT4A decodes through INT4's table (codes q - 8), and the kernels subtract (z - 8) * s * sum(x)
-// per group: (q - z) s = (q - 8) s - (z - 8) s.
-enum Fmt { kNF4 = 0, kINT4 = 1, kFP4 = 2, kINT4A = 3 };
+// per group: (q - z) s = (q - 8) s - (z - 8) s.  MXFP4 has FP4's codes and one E8M0 byte per 32
+// weights; rows hold whole pairs of such blocks (K % 64 == 0), so its scales are 2 bytes per 64.
+enum Fmt { kNF4 = 0, kINT4 = 1, kFP4 = 2, kINT4A = 3, kMXFP4 = 4 };
 enum XType { kF16 = 0, kBF16 = 1 };
 
 // Formats with groups of 128 along K and a bf16 scale.
@@ -94,16 +95,26 @@ inline int fmt_weight(int fmt) {
   return (fmt == W4_NF4_X_F16 || fmt == W4_NF4_X_BF16)       ? kNF4
          : (fmt == W4_FP4_X_F16 || fmt == W4_FP4_X_BF16)     ? kFP4
          : (fmt == W4_INT4A_X_F16 || fmt == W4_INT4A_X_BF16) ? kINT4A
+         : (fmt == W4_MXFP4_X_F16 || fmt == W4_MXFP4_X_BF16) ? kMXFP4
                                                              : kINT4;
 }
 inline int fmt_xtype(int fmt) {
   return (fmt == W4_NF4_X_F16 || fmt == W4_INT4_X_F16 || fmt == W4_FP4_X_F16 ||
-          fmt == W4_INT4A_X_F16)
+          fmt == W4_INT4A_X_F16 || fmt == W4_MXFP4_X_F16)
              ? kF16
              : kBF16;
 }
 inline int64_t fmt_group(int fmt) { return is_g128(fmt_weight(fmt)) ? 128 : 64; }
-inline size_t fmt_scale_bytes(int fmt) { return fmt_weight(fmt) == kINT4 ? 2 : 4; }
+// Bytes of scale per fmt_group(fmt) weights (INT4: one bf16; MXFP4: two E8M0 bytes).
+inline size_t fmt_scale_bytes(int fmt) {
+  return fmt_weight(fmt) == kINT4 || fmt_weight(fmt) == kMXFP4 ? 2 : 4;
+}
+
+// The value of an E8M0 scale byte e: 2^(e - 127), the subnormal 2^-127 for e = 0, NaN for e = 255.
+__device__ inline float e8m0_value(uint32_t e) {
+  const uint32_t bits = e == 0u ? 0x00400000u : e << 23;
+  return __uint_as_float(e == 255u ? 0x7FC00000u : bits);
+}
 
 // Shape of one fused-GEMV launch (host-chosen; see plan_gemv in w4_api.cpp).
 struct GemvPlan {
@@ -124,6 +135,7 @@ constexpr int kMaxGroup = W4_MAX_GROUP;
 struct GemvMember {
   const uint8_t* packed;  // [N_g, K/2]
   const void* scales;     // NF4, FP4 float[N_g, K/64] | INT4 uint16[N_g, K/128] | INT4A uint32
+                          // | MXFP4 uint8[N_g, K/32]
   float* out;             // y [B, N_g] (splits == 1) or partials [splits, B, N_g]
   uint32_t n;             // rows N_g
   uint32_t nrb;           // row blocks of this member = ceil(N_g / rows per workgroup)
@@ -176,6 +188,8 @@ hipError_t launch_quantize_int4_asym(const float* w, int64_t n, int64_t k, uint8
                                      uint32_t* words, hipStream_t s);
 hipError_t launch_quantize_fp4(const float* w, int64_t n, int64_t k, uint8_t* packed, float* scale,
                                hipStream_t s);
+hipError_t launch_quantize_mxfp4(const float* w, int64_t n, int64_t k, uint8_t* packed,
+                                 uint8_t* scale, hipStream_t s);
 hipError_t quantize_error_reset(hipStream_t s);
 hipError_t quantize_error_read(int* flag, hipStream_t s);
 hipError_t launch_dequant_f16(int fmt, const uint8_t* packed, const void* scales, int64_t n,

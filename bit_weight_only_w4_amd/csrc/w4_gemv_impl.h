@@ -159,24 +159,30 @@ template <int FMT>
 __device__ inline uint32_t scale_pitch(int64_t k) {
   return FMT == kINT4A ? (uint32_t)(k >> 7) * 4u
          : FMT == kINT4 ? (uint32_t)(k >> 7) * 2u
-                        : (uint32_t)(k >> 6) * 4u;
+         : FMT == kMXFP4 ? (uint32_t)(k >> 5)
+                         : (uint32_t)(k >> 6) * 4u;
 }
 template <int FMT>
 __device__ inline uint32_t scale_offset(int chunk) {
   return FMT == kINT4A ? (uint32_t)(chunk >> 2) * 4u
          : FMT == kINT4 ? (uint32_t)(chunk >> 2) * 2u
-                        : (uint32_t)(chunk >> 1) * 4u;
+         : FMT == kMXFP4 ? (uint32_t)chunk
+                         : (uint32_t)(chunk >> 1) * 4u;
 }
 // The scale slot of a chunk as loaded: fp32 (NF4, FP4), the 32-bit word (INT4A, as float bits),
-// or the 16 bf16 bits (INT4), widened to fp32 only where the scale is used (scale_value).  Widened
+// the 16 bf16 bits (INT4) or the E8M0 byte (MXFP4, whose block is the chunk), widened to fp32 only where the scale is used (scale_value).  Widened
 // at load time, the conversion of every prefetched row block's scales waited for their loads
 // right away (0.2 us per small launch).
 template <int FMT>
-using ScaleSlot = typename std::conditional<FMT == kINT4, uint16_t, float>::type;
+using ScaleSlot =
+    typename std::conditional<FMT == kINT4, uint16_t,
+                              typename std::conditional<FMT == kMXFP4, uint8_t, float>::type>::type;
 template <int FMT>
 __device__ inline ScaleSlot<FMT> load_scale(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   if constexpr (FMT == kINT4) {
     return __builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, 0);
+  } else if constexpr (FMT == kMXFP4) {
+    return __builtin_amdgcn_raw_buffer_load_b8(r, (int)off, 0, 0);
   } else {
     return __uint_as_float(buffer_load32(r, off));
   }
@@ -185,12 +191,20 @@ template <int FMT>
 __device__ inline float scale_value(ScaleSlot<FMT> slot) {
   if constexpr (FMT == kINT4) {
     return __uint_as_float((uint32_t)slot << 16);  // bf16 -> fp32, exact
+  } else if constexpr (FMT == kMXFP4) {
+    return e8m0_value(slot);
   } else {
     return slot;
   }
 }
 
-// Launches decoded without the LDS table (no fill, no lookups): FP4, through gfx950's E2M1 ->
+// E2M1 codes, whatever their scales.
+template <int FMT>
+constexpr bool is_e2m1() {
+  return FMT == kFP4 || FMT == kMXFP4;
+}
+
+// Launches decoded without the LDS table (no fill, no lookups): E2M1 codes, through gfx950's E2M1 ->
 // 16-bit conversion (v_cvt_scalef32_pk_{f16,bf16}_fp4 with scale 1: exact, one instruction per
 // packed byte).  INT4 and asymmetric INT4 keep the table everywhere: a table-free INT4 decode
 // (nibbles placed in the mantissa of M + q, 1.75 VALU instructions per packed byte, the offset
@@ -199,7 +213,7 @@ __device__ inline float scale_value(ScaleSlot<FMT> slot) {
 // table against 492.3, asymmetric INT4 503.5 against 508.1, INT4 at B = 2 610.6 against 622.7).
 template <int FMT>
 constexpr bool table_free() {
-  return FMT == kFP4;
+  return is_e2m1<FMT>();
 }
 
 // The two FP4 weights of byte KB of packed dword w as one activation-type pair.  The conversion
@@ -328,7 +342,7 @@ gemv_kernel(GemvArgsT<GROUPED ? kMaxGroup : 1> a) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint4 v = buffer_load16(rx, xo + 16u * q);
-        if constexpr (FMT == kFP4) {
+        if constexpr (is_e2m1<FMT>()) {
           // the hardware FP4 conversion yields (odd k, even k) pairs: swap each activation pair
           v = make_uint4(__builtin_amdgcn_alignbit(v.x, v.x, 16), __builtin_amdgcn_alignbit(v.y, v.y, 16),
                          __builtin_amdgcn_alignbit(v.z, v.z, 16), __builtin_amdgcn_alignbit(v.w, v.w, 16));

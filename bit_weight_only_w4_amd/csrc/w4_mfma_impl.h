@@ -32,6 +32,11 @@
 //   * NF4 x bf16 uses the two-term bf16 split of each code (two MFMAs per step); INT4 codes q - 8
 //     are exact in both 16-bit types.  Asymmetric INT4 decodes q - 8 the same way and adds one
 //     MFMA per step whose A rows hold -(z - 8), which makes D the block's sum of (q - z) x.
+//   * MXFP4 moves through the registers as NF4's 64-weight blocks; one more swap of 16-lane rows
+//     (v_permlane16_swap) gathers the lane groups' dwords so that each MFMA step is one 32-weight
+//     block with one scale, applied in fp32 after the step.  Its codes come from the hardware
+//     E2M1 conversion (no table): the dword's nibbles swapped pairwise (3 operations), then one
+//     conversion per byte.
 #pragma once
 #include <string.h>
 
@@ -46,6 +51,7 @@ namespace w4 {
 struct MfmaMember {
   const uint8_t* packed;  // [N_g, K/2]
   const void* scales;     // NF4, FP4 float[N_g, K/64] | INT4 uint16 / INT4A uint32 [N_g, K/128]
+                          // | MXFP4 uint8[N_g, K/32]
   float* y;               // [B, N_g]
   uint32_t n;             // N_g
   uint32_t tile0;
@@ -94,8 +100,27 @@ template <int FMT>
 struct Quad {
   static constexpr int QC = is_g128(FMT) ? 2 : 4;  // scale blocks per quad
   uint32_t w[2][4];
-  uint32_t s[QC];  // fp32 bits (INT4: bf16 bits in the low half; INT4A: its word)
+  uint32_t s[QC];  // fp32 bits (INT4: bf16 bits in the low half; INT4A: its word; MXFP4: the
+                   // block pair's two E8M0 bytes)
 };
+
+// The four E2M1 pairs of a packed dword in memory order (high nibble first) as 16-bit pairs.  The
+// conversion returns a byte's low nibble in the low half, so the nibbles are swapped first.
+template <int XT>
+__device__ inline uint4 e2m1_pairs(uint32_t w) {
+  w = ((w >> 4) & 0x0F0F0F0Fu) | ((w << 4) & 0xF0F0F0F0u);
+  if constexpr (XT == kF16) {
+    return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3)));
+  } else {
+    return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3)));
+  }
+}
 
 // Waves per SIMD the kernel is compiled for: four (two workgroups per CU, <= 128 VGPRs) for one
 // batch tile, two above.
@@ -107,11 +132,12 @@ __global__ void __launch_bounds__(kThreads, min_waves(T)) mfma_kernel(MfmaArgs a
   constexpr int KC = is_g128(FMT) ? 128 : 64;  // weights per scale block
   constexpr int QC = kQuad / KC;              // blocks per quad
   constexpr int STEPS = KC / 32;              // MFMA steps per block
-  constexpr int SB = FMT == kINT4 ? 2 : 4;     // bytes per scale
+  constexpr bool kMX = FMT == kMXFP4;          // a scale per step, no table
+  constexpr int SB = FMT == kINT4 || kMX ? 2 : 4;  // bytes of scale per block
   constexpr bool kSplit = (FMT == kNF4 && XT == kBF16);
   // LDS: the decode table (static, at address 0, so a lookup address needs no base), then the
   // dynamic part: the K-group reduction area and the x window.
-  __shared__ __align__(16) uint32_t tab[kTableBytes / 4];
+  __shared__ __align__(16) uint32_t tab[kMX ? 4 : kTableBytes / 4];
   extern __shared__ __align__(16) uint8_t smem[];
   float4_t* red = reinterpret_cast<float4_t*>(smem);  // [KW - 1][RW][T][64 lanes]
   uint8_t* xs = smem + a.red_bytes;
@@ -205,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, min_waves(T)) mfma_kernel(MfmaArgs a
     // multiplied (inside the matrix their bytes are the next row's; zeroing them here would make
     // the loop wait for the load).  INT4: two bf16 scales, 2-byte aligned, two loads, moved to the
     // high half when multiplied (for the same reason).
-    if constexpr (!is_g128(FMT)) {
+    if constexpr (!is_g128(FMT) && !kMX) {
       const uint4 sv = buffer_load16(cur.rs, offset_or_oob(qb < nblocks, sbase));
       d.s[0] = sv.x;
       d.s[1] = sv.y;
@@ -274,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, min_waves(T)) mfma_kernel(MfmaArgs a
   advance(ld);
   load_quad(ld, P1);
   advance(ld);
-  fill_table<FMT, XT, kThreads>(tab);
+  if constexpr (!kMX) fill_table<FMT, XT, kThreads>(tab);
   if constexpr (R == 4) {
     load_quad(ld, P2);
     advance(ld);
@@ -293,7 +319,8 @@ __global__ void __launch_bounds__(kThreads, min_waves(T)) mfma_kernel(MfmaArgs a
   const uint8_t* xw = xs + (uint32_t)kg * (seg * 16u);  // this K group's part of the window
 
   // k offset (in the block) of the first of this lane's weights for MFMA step 0 (see Quad).
-  const int klane = !is_g128(FMT) ? 32 * (g & 1) + 16 * (g >> 1) : 32 * g;
+  // MXFP4: of the step's block, 8 weights per lane group.
+  const int klane = kMX ? 8 * g : !is_g128(FMT) ? 32 * (g & 1) + 16 * (g >> 1) : 32 * g;
   // INT4A: the lane holding the scale word of A row m (scale words sit with D rows 4 g + (m & 3)).
   const int zsrc = 16 * (m >> 2) + (m & 3);
 
@@ -319,6 +346,16 @@ __global__ void __launch_bounds__(kThreads, min_waves(T)) mfma_kernel(MfmaArgs a
         wb[2 * h][1] = s1[0];
         wb[2 * h + 1][0] = s0[1];
         wb[2 * h + 1][1] = s1[1];
+      }
+      if constexpr (kMX) {
+        // Lane groups 0 and 2 now hold dwords 0, 1 and 2, 3 of the first 32-weight block, groups 1
+        // and 3 those of the second: dword g of block s to lane group g, step s.
+#pragma unroll
+        for (int c = 0; c < QC; ++c) {
+          const auto t = __builtin_amdgcn_permlane16_swap(wb[c][0], wb[c][1], false, false);
+          wb[c][0] = t[0];
+          wb[c][1] = t[1];
+        }
       }
     } else {
 #pragma unroll
@@ -353,6 +390,21 @@ __global__ void __launch_bounds__(kThreads, min_waves(T)) mfma_kernel(MfmaArgs a
       }
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
+        if constexpr (kMX) {
+          const uint4 a1 = e2m1_pairs<XT>(wb[c][s]);
+          const uint32_t sraw = __float_as_uint(e8m0_value((d.s[c] >> (8 * s)) & 0xFFu));
+          const float sc[4] = {row_bcast<0>(sraw), row_bcast<1>(sraw), row_bcast<2>(sraw),
+                               row_bcast<3>(sraw)};
+#pragma unroll
+          for (int t = 0; t < T; ++t) {
+            const uint4 bv = *reinterpret_cast<const uint4*>(xq + xrowoff[t] + (c * KC + s * 32) * 2);
+            const float4_t one = mfma<XT>(a1, bv, float4_t{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(one[i], sc[i], acc[t][i]);
+          }
+          if constexpr (T == 8) __builtin_amdgcn_sched_barrier(0);
+          continue;
+        }
         uint32_t p1[4], p2[4];
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb) {
@@ -380,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, min_waves(T)) mfma_kernel(MfmaArgs a
         // step (they would not fit the registers left by the accumulators).
         if constexpr (T == 8) __builtin_amdgcn_sched_barrier(0);
       }
+      if constexpr (kMX) continue;  // scaled step by step above
       const uint32_t sraw = !is_g128(FMT) ? ((c > 0 && qb + c >= nblocks) ? 0u : d.s[c]) : d.s[c] << 16;
       const float sc[4] = {row_bcast<0>(sraw), row_bcast<1>(sraw), row_bcast<2>(sraw),
                            row_bcast<3>(sraw)};
@@ -560,7 +613,9 @@ hipError_t dispatch(int op, int fmt, const MfmaArgs& a, int tiles, int kw, int l
     case W4_FP4_X_F16: return dispatch_fx<kFP4, kF16, GROUPED>(op, a, tiles, kw, lds, grid, slices, out, s);
     case W4_FP4_X_BF16: return dispatch_fx<kFP4, kBF16, GROUPED>(op, a, tiles, kw, lds, grid, slices, out, s);
     case W4_INT4A_X_F16: return dispatch_fx<kINT4A, kF16, GROUPED>(op, a, tiles, kw, lds, grid, slices, out, s);
+    case W4_MXFP4_X_F16: return dispatch_fx<kMXFP4, kF16, GROUPED>(op, a, tiles, kw, lds, grid, slices, out, s);
     case W4_INT4A_X_BF16: return dispatch_fx<kINT4A, kBF16, GROUPED>(op, a, tiles, kw, lds, grid, slices, out, s);
+    case W4_MXFP4_X_BF16: return dispatch_fx<kMXFP4, kBF16, GROUPED>(op, a, tiles, kw, lds, grid, slices, out, s);
   }
   return hipErrorInvalidValue;
 }

@@ -25,10 +25,15 @@
 // ladder applied to the fp64 quotient |w| / s, sign bit = (w < 0); the thresholds are dyadic, so
 // the fp64 quotient of two fp32 values is on the same side of each as the exact ratio.
 //
+// MXFP4 (E2M1 codes as FP4, the block form of the OCP microscaling formats): blocks of 32, the
+// scale 2^e with e = floor(log2 absmax) - 2 (E2M1's largest exponent is 2), clamped to E8M0's
+// [-127, 127], stored as e + 127; the ladder applied to |w| 2^-e, exact in fp64, saturating at 6
+// (quotients reach just under 8).
+//
 // One lane handles one pair of weights (one output byte): element 2i goes to the high nibble.
 // Absmax is an integer max over |bits| (the order of non-negative floats), reduced across the 32
-// lanes of an NF4 block or the 64 lanes of an INT4 group with cross-lane shuffles (asymmetric
-// INT4: fp32 min and max the same way).
+// lanes of an NF4 block, the 64 lanes of an INT4 group or the 16 lanes of an MXFP4 block with
+// cross-lane shuffles (asymmetric INT4: fp32 min and max the same way).
 #include "w4_common.h"
 
 namespace w4 {
@@ -189,6 +194,32 @@ __global__ void __launch_bounds__(256) quant_fp4_kernel(const float* __restrict_
   }
 }
 
+__global__ void __launch_bounds__(256) quant_mxfp4_kernel(const float* __restrict__ w, int64_t pairs,
+                                                           uint8_t* __restrict__ packed,
+                                                           uint8_t* __restrict__ scale) {
+  const int64_t p = blockIdx.x * 256ll + threadIdx.x;
+  const bool valid = p < pairs;  // pairs is a multiple of 32: a whole block is valid or not
+  const float2 v = reinterpret_cast<const float2*>(w)[valid ? p : 0];
+  const uint32_t a0 = __float_as_uint(v.x) & 0x7FFFFFFFu;
+  const uint32_t a1 = __float_as_uint(v.y) & 0x7FFFFFFFu;
+  if (valid && (a0 >= 0x7F800000u || a1 >= 0x7F800000u)) g_w4_nonfinite = 1;
+  uint32_t m = a0 > a1 ? a0 : a1;
+#pragma unroll
+  for (int off = 1; off < 16; off <<= 1) {
+    const uint32_t o = (uint32_t)__shfl_xor((int)m, off);
+    m = o > m ? o : m;
+  }
+  // e + 127 = biased exponent of absmax - 2, at least 0 (an all-zero block too)
+  const int byte = (int)(m >> 23) > 2 ? (int)(m >> 23) - 2 : 0;
+  const double inv = ldexp(1.0, 127 - byte);
+  const uint32_t n0 = fp4_magnitude(fabs((double)v.x) * inv) | (v.x < 0.0f ? 8u : 0u);
+  const uint32_t n1 = fp4_magnitude(fabs((double)v.y) * inv) | (v.y < 0.0f ? 8u : 0u);
+  if (valid) {
+    packed[p] = (uint8_t)((n0 << 4) | n1);
+    if ((threadIdx.x & 15) == 0) scale[p >> 4] = (uint8_t)byte;
+  }
+}
+
 }  // namespace
 
 hipError_t quantize_error_reset(hipStream_t s) {
@@ -220,6 +251,22 @@ hipError_t launch_quantize_fp4(const float* w, int64_t n, int64_t k, uint8_t* pa
   hipLaunchKernelGGL(quant_fp4_kernel, dim3((unsigned)blocks), dim3(256), 0, s, w, pairs, packed,
                      scale);
   return hipGetLastError();
+}
+
+hipError_t launch_quantize_mxfp4(const float* w, int64_t n, int64_t k, uint8_t* packed,
+                                 uint8_t* scale, hipStream_t s) {
+  // Rows in slices of at most 2^32 weights (one row at least): a launch's threads, one per pair,
+  // have to number fewer than 2^32.
+  const int64_t slice = k >= ((int64_t)1 << 32) / 2 ? 1 : ((int64_t)1 << 32) / k;
+  for (int64_t r = 0; r < n; r += slice) {
+    const int64_t pairs = (n - r < slice ? n - r : slice) * (k / 2);
+    const int64_t blocks = (pairs + 255) / 256;
+    hipLaunchKernelGGL(quant_mxfp4_kernel, dim3((unsigned)blocks), dim3(256), 0, s, w + r * k, pairs,
+                       packed + r * (k / 2), scale + r * (k / 32));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_quantize_int4_asym(const float* w, int64_t n, int64_t k, uint8_t* packed,

@@ -57,7 +57,14 @@ extern "C" {
  *         quotient plus the zero point, clamped and rounded; "What those numbers leave out":
  *         INT4 in symmetric and asymmetric grouped forms): nibble = unsigned code q in 0..15, groups of 128 along K,
  *         scales = uint32[N, K/128] words, bf16 scale bits in bits 0-15 and the zero point z
- *         (0..15) in bits 16-19, bits 20-31 zero; decoded weight = (q - z) * scale. */
+ *         (0..15) in bits 16-19, bits 20-31 zero; decoded weight = (q - z) * scale.
+ *   MXFP4: the FP4 codes in blocks of 32 along K with one E8M0 byte e per block (the block form
+ *         of the OCP microscaling formats), scales = uint8[N, K/32], 2-byte aligned, K a multiple
+ *         of 64; decoded weight = table[nibble] * 2^(e - 127), NaN for e = 255.  Both 16-bit types
+ *         hold the codes exactly and each block's sum is scaled in fp32, so y differs from the
+ *         exact product by fp32 accumulation alone.  Runs on W4_PATH_GEMV, W4_PATH_SPLITK and
+ *         W4_PATH_MFMA (W4_PATH_AUTO and w4_gemm_prefill choose among these); the two-pass and
+ *         tiled paths return W4_ERR_PATH. */
 typedef enum {
   W4_NF4_X_F16 = 1,
   W4_NF4_X_BF16 = 2,
@@ -66,13 +73,15 @@ typedef enum {
   W4_FP4_X_F16 = 5,
   W4_FP4_X_BF16 = 6,
   W4_INT4A_X_F16 = 7,
-  W4_INT4A_X_BF16 = 8
+  W4_INT4A_X_BF16 = 8,
+  W4_MXFP4_X_F16 = 16, /* 9-15 are not formats */
+  W4_MXFP4_X_BF16 = 17
 } w4_format_t;
 
 typedef enum {
   W4_OK = 0,
   W4_ERR_NULL = -1,      /* a required pointer is NULL                                        */
-  W4_ERR_SHAPE = -2,     /* N, K or B out of range, or K not a multiple of 64 (NF4, FP4) / 128 (INT4, INT4A) */
+  W4_ERR_SHAPE = -2,     /* N, K or B out of range, or K not a multiple of 64 (NF4, FP4, MXFP4) / 128 (INT4, INT4A) */
   W4_ERR_ALIGN = -3,     /* packed or x not 16-byte aligned, scales or y not element aligned  */
   W4_ERR_FORMAT = -4,    /* unknown w4_format_t                                               */
   W4_ERR_NONFINITE = -5, /* quantize met a NaN or Inf weight (outputs are then meaningless)   */
@@ -210,6 +219,18 @@ int w4_quantize_int4_asym(const float* w, int64_t N, int64_t K, uint8_t* packed,
 int w4_quantize_fp4(const float* w, int64_t N, int64_t K, uint8_t* packed, float* scale,
                     void* stream);
 
+/* w4_quantize_mxfp4: MXFP4 quantization, blocks of 32 along K.  Per block with A = max |w|: the scale
+ * is 2^e, e = floor(log2 A) - 2 clamped to [-127, 127], stored as e + 127 (an all-zero block
+ * stores 0); nibble of w: sign bit (w < 0) | the FP4 ladder's index of |w| / 2^e (ties to even
+ * codes, 6 and above to the last).
+ *   w      device float[N, K] (fp32), read only; 8-byte aligned
+ *   N, K   N >= 1, K a positive multiple of 64
+ *   packed device uint8[N, K/2], written; 16-byte aligned; element 2i in the high nibble
+ *   scale  device uint8[N, K/32], written; 2-byte aligned
+ * Synchronizes `stream`.  Returns W4_ERR_NONFINITE if any weight is NaN or Inf. */
+int w4_quantize_mxfp4(const float* w, int64_t N, int64_t K, uint8_t* packed, uint8_t* scale,
+                      void* stream);
+
 /* -------------------------------------------------------------------------- matmul --------- */
 
 /* ---------------------------------------------------------------- settings ----------------- */
@@ -248,7 +269,7 @@ int w4_set_workspace(void* workspace, size_t bytes);
  * RTX 4060, "Kernel Implementation": unpack, codebook, block scale, fp32 accumulation).
  *   x       device [B, K] fp16 or bf16 (per fmt) bit patterns; 16-byte aligned
  *   packed  device uint8[N, K/2]; 16-byte aligned
- *   scales  device float[N, K/64] (NF4) or uint16 bf16 bits [N, K/128] (INT4)
+ *   scales  device scales of the format (see w4_format_t): float[N, K/64] (NF4), ...
  *   fmt     w4_format_t
  *   N, K, B N >= 1; K as for the format; 1 <= B <= 8
  *   y       device float[B, N]; fully overwritten, never accumulated into; must not overlap inputs

@@ -22,6 +22,8 @@ What it computes (all in numpy fp64 unless a storage format fixes the precision)
   absmax / 6, the pages' threshold rounding with exact ties on even codes (LLM Compressor 0.14,
   section "Details worth knowing"; the FP4-named fused kernel of My Triton Kernel Ties
   bitsandbytes, section "The kernels").
+* ``quantize_mxfp4`` -- the E2M1 codes in blocks of 32 with one power-of-two scale byte per block
+  (module ``oracle.mxfp4``; the block form of the OCP microscaling formats).
 * ``gptq``           -- GPTQ's column loop with lazy blocks (module ``oracle.gptq``): dampening, the
   upper Cholesky factor of H^-1, per-column quantize with error feedback, the lazy update (LLM
   Compressor 0.14, sections "The problem GPTQ solves" to "The fused kernel"), in fp64 for the
@@ -44,6 +46,7 @@ from .nf4 import NF4_BLOCK, dequant_nf4, nf4_codebook, nf4_midpoints, quantize_n
 from .int4 import INT4_GROUP, dequant_int4, quantize_int4
 from .int4_asym import INT4A_GROUP, dequant_int4_asym, int4_asym_scale_zero, quantize_int4_asym
 from .fp4 import FP4_BLOCK, FP4_GRID, dequant_fp4, fp4_codebook, fp4_magnitude_index, quantize_fp4
+from .mxfp4 import MXFP4_BLOCK, dequant_mxfp4, quantize_mxfp4
 from .gemv import accept, dequant, gemv_reference, unpack_nibbles, violation_ratio
 
 __all__ = [
@@ -52,6 +55,7 @@ __all__ = [
     "quantize_int4", "dequant_int4",
     "INT4A_GROUP", "int4_asym_scale_zero", "quantize_int4_asym", "dequant_int4_asym",
     "FP4_BLOCK", "FP4_GRID", "fp4_codebook", "fp4_magnitude_index", "quantize_fp4", "dequant_fp4",
+    "MXFP4_BLOCK", "quantize_mxfp4", "dequant_mxfp4",
     "unpack_nibbles", "dequant", "gemv_reference", "accept", "violation_ratio",
     "f16_bits_to_f64", "bf16_bits_to_f64", "x_bits_to_f64", "f32_to_bf16_rne_bits",
 ]

@@ -34,7 +34,7 @@ def unpack_nibbles(packed: np.ndarray) -> np.ndarray:
 
 
 def dequant(fmt: str, packed: np.ndarray, scales: np.ndarray) -> np.ndarray:
-    """Decoded fp64 weights for ``fmt`` in {"nf4", "int4", "int4a", "fp4"}."""
+    """Decoded fp64 weights for ``fmt`` in {"nf4", "int4", "int4a", "fp4", "mxfp4"}."""
     if fmt == "nf4":
         from .nf4 import dequant_nf4
 
@@ -51,6 +51,10 @@ def dequant(fmt: str, packed: np.ndarray, scales: np.ndarray) -> np.ndarray:
         from .fp4 import dequant_fp4
 
         return dequant_fp4(packed, scales)
+    if fmt == "mxfp4":
+        from .mxfp4 import dequant_mxfp4
+
+        return dequant_mxfp4(packed, scales)
     raise ValueError(f"unknown weight format {fmt!r}")
 
 
