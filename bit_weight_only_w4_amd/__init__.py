@@ -64,6 +64,10 @@ def lib() -> ctypes.CDLL:
         L.w4_sparse24_compress.argtypes = [vp, i64, i64, ci, vp, vp, vp]
         L.w4_sparse24_gemv.argtypes = [vp, vp, vp, ci, i64, i64, i64, vp, vp]
         L.w4_sparse24_gemv_grouped.argtypes = [vp, ci, vp, vp, vp, ci, i64, i64, vp, vp]
+        L.w4_moe_route.argtypes = [vp, ci, i64, i64, i64, ci, vp, vp, vp]
+        L.w4_moe.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, i64, i64, i64, i64, i64, vp, vp, sz, vp]
+        L.w4_moe_workspace_bytes.argtypes = [ci, i64, i64, i64, i64, i64]
+        L.w4_moe_workspace_bytes.restype = sz
         L.w4_gemv.argtypes = [vp, vp, vp, ci, i64, i64, i64, vp, vp]
         L.w4_gemm_smallbatch.argtypes = [vp, vp, vp, ci, i64, i64, i64, vp, vp]
         L.w4_gemm_prefill.argtypes = [vp, vp, vp, ci, i64, i64, i64, vp, vp]
@@ -95,7 +99,7 @@ def lib() -> ctypes.CDLL:
                      "w4_gptq_quantize", "w4_sparse24_compress", "w4_sparse24_gemv",
                      "w4_sparse24_gemv_grouped", "w4_set_path", "w4_get_path",
                      "w4_matmul_splitk_noalloc",
-                     "w4_set_workspace"):
+                     "w4_set_workspace", "w4_moe_route", "w4_moe"):
             getattr(L, name).restype = ci
         _lib = L
     return _lib
@@ -518,3 +522,101 @@ def sparse24_gemv_grouped(x, values, meta, ys=None, stream=None):
         (ctypes.c_int64 * g)(*ns), S24_TYPES[xtype], k, b, arr(*[y.data_ptr() for y in ys]),
         _stream(stream)), "w4_sparse24_gemv_grouped")
     return ys
+
+
+MOE_MAX_EXPERTS = 1024
+MOE_MAX_TOPK = 16
+_MOE_SCALES = {"nf4": ("float32", 64), "fp4": ("float32", 64), "int4": ("int16", 128),
+               "int4a": ("int32", 128), "mxfp4": ("uint8", 32)}
+
+
+def _on_device_of(t, stream):
+    """A context in which allocations and launches go to `stream` (or the current stream) of t's
+    device."""
+    import torch
+
+    if stream is None:
+        return torch.cuda.device(t.device)
+    if stream.device != t.device:
+        raise ValueError("stream and tensors must be on one device")
+    return torch.cuda.stream(stream)
+
+
+def moe_route(logits, top_k, renormalize=True, ids=None, weights=None, stream=None):
+    """The top_k experts of each token and their softmax weights from router logits [T, E] (fp32, fp16
+    or bf16): (ids int32 [T, top_k], weights fp32 [T, top_k]).  Descending, ties to the lowest expert; the
+    weights are normalized over the chosen experts, or over all of them (renormalize=False).  NaN
+    and -inf logits are never chosen: slots left over get id -1 and weight 0."""
+    import torch
+
+    kind = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(logits.dtype)
+    if kind is None or logits.dim() != 2:
+        raise ValueError("logits must be a 2-D float32, float16 or bfloat16 tensor")
+    _need_cuda(logits, ids, weights)
+    t, e = logits.shape
+    top_k = int(top_k)
+    with _on_device_of(logits, stream):
+        if ids is None:
+            ids = torch.empty((t, max(top_k, 0)), dtype=torch.int32, device=logits.device)
+        if weights is None:
+            weights = torch.empty((t, max(top_k, 0)), dtype=torch.float32, device=logits.device)
+        if tuple(ids.shape) != (t, top_k) or ids.dtype != torch.int32 or ids.device != logits.device:
+            raise ValueError("ids must be int32 [T, top_k] on the logits' device")
+        if tuple(weights.shape) != (t, top_k) or weights.dtype != torch.float32 or \
+                weights.device != logits.device:
+            raise ValueError("weights must be float32 [T, top_k] on the logits' device")
+        check(lib().w4_moe_route(_ptr(logits), kind, t, e, top_k, int(bool(renormalize)), _ptr(ids),
+                                 _ptr(weights), _stream(stream)), "w4_moe_route")
+    return ids, weights
+
+
+def moe_workspace_bytes(fmt, tokens, hidden, inter, experts, top_k) -> int:
+    return int(lib().w4_moe_workspace_bytes(_fmt(fmt), tokens, hidden, inter, experts, top_k))
+
+
+def moe(x, ids, weights, gate_up, gate_up_scales, down, down_scales, fmt, y=None, workspace=None,
+        stream=None):
+    """A mixture-of-experts layer over 4-bit experts: y [T, H] fp32 with
+    y[t] = sum_j weights[t, j] * Down_e(silu(Gate_e x[t]) * (Up_e x[t])), e = ids[t, j].
+
+    x [T, H] of the format's activation type; ids int32 and weights fp32 [T, top_k] (as moe_route gives
+    them; ids outside [0, E) are absent slots); gate_up uint8 [E, 2 I, H/2] (gate rows, then up
+    rows) and down uint8 [E, H, I/2] with the format's scales [E, 2 I, H/g] and [E, H, I/g].
+    `workspace` is a uint8 tensor of moe_workspace_bytes(...), allocated by the call if not given."""
+    import torch
+
+    if fmt not in FORMATS:
+        raise ValueError(f"unknown format {fmt!r}; expected one of {sorted(FORMATS)}")
+    weight, xtype = fmt.split("_")
+    _need_cuda(x, ids, weights, gate_up, gate_up_scales, down, down_scales, y, workspace)
+    if x.dim() != 2 or x.dtype != (torch.float16 if xtype == "f16" else torch.bfloat16):
+        raise ValueError(f"x must be a 2-D tensor of the activation type of {fmt!r}")
+    if ids.dim() != 2 or gate_up.dim() != 3 or down.dim() != 3:
+        raise ValueError("ids must be [T, top_k], gate_up [E, 2 I, H/2] and down [E, H, I/2]")
+    t, h = x.shape
+    k = ids.shape[1]
+    e, i = gate_up.shape[0], down.shape[2] * 2
+    dtype, group = _MOE_SCALES[weight]
+    dtype = getattr(torch, dtype)
+    for name, v, shape, kind in (
+            ("ids", ids, (t, k), torch.int32), ("weights", weights, (t, k), torch.float32),
+            ("gate_up", gate_up, (e, 2 * i, h // 2), torch.uint8), ("down", down, (e, h, i // 2), torch.uint8),
+            ("gate_up_scales", gate_up_scales, (e, 2 * i, h // group), dtype),
+            ("down_scales", down_scales, (e, h, i // group), dtype)):
+        if v.shape != shape or v.dtype != kind or v.device != x.device:
+            raise ValueError(f"{name} must be {kind} {list(shape)} on x's device")
+    with _on_device_of(x, stream):
+        if y is None:
+            y = torch.empty((t, h), dtype=torch.float32, device=x.device)
+        elif y.shape != (t, h) or y.dtype != torch.float32 or y.device != x.device:
+            raise ValueError("y must be float32 [T, H] on x's device")
+        if workspace is None:
+            workspace = torch.empty(moe_workspace_bytes(fmt, t, h, i, e, k), dtype=torch.uint8,
+                                    device=x.device)
+        elif workspace.device != x.device:
+            raise ValueError("workspace must be on x's device")
+        check(lib().w4_moe(_ptr(x), _ptr(ids), _ptr(weights), _ptr(gate_up), _ptr(gate_up_scales),
+                           _ptr(down), _ptr(down_scales), FORMATS[fmt], t, h, i, e, k, _ptr(y),
+                           _ptr(workspace), workspace.numel() * workspace.element_size(),
+                           _stream(stream)), "w4_moe")
+    return y

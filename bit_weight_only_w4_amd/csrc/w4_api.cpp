@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "w4_common.h"
+#include "w4_moe.h"
 
 namespace w4 {
 
@@ -1084,6 +1085,81 @@ int w4_gptq_quantize(float* w, const float* u, const float* scale, const float* 
   }
   if (pending && hipStreamWaitEvent(s, h->join, 0) != hipSuccess) return W4_ERR_HIP;
   return W4_OK;
+}
+
+int w4_moe_route(const void* logits, int logits_type, int64_t tokens, int64_t experts, int64_t top_k,
+                 int renormalize, int32_t* ids, float* weights, void* stream) {
+  if (!logits || !ids || !weights) return W4_ERR_NULL;
+  if (logits_type != W4_LOGITS_F32 && logits_type != W4_LOGITS_F16 && logits_type != W4_LOGITS_BF16)
+    return W4_ERR_FORMAT;
+  if (tokens < 1 || tokens >= ((int64_t)1 << 26) || experts < 1 || experts > W4_MOE_MAX_EXPERTS ||
+      top_k < 1 || top_k > W4_MOE_MAX_TOPK || top_k > experts)
+    return W4_ERR_SHAPE;
+  const size_t lsz = logits_type == W4_LOGITS_F32 ? 4 : 2;
+  if (!aligned(logits, lsz) || !aligned(ids, 4) || !aligned(weights, 4)) return W4_ERR_ALIGN;
+  const size_t lb = (size_t)(tokens * experts) * lsz, ob = (size_t)(tokens * top_k) * 4;
+  if (overlaps(ids, ob, logits, lb) || overlaps(weights, ob, logits, lb) || overlaps(ids, ob, weights, ob))
+    return W4_ERR_ALIAS;
+  return launch_moe_route(logits, logits_type, tokens, experts, top_k, renormalize != 0, ids, weights,
+                          reinterpret_cast<hipStream_t>(stream)) == hipSuccess
+             ? W4_OK
+             : W4_ERR_HIP;
+}
+
+namespace {
+
+// Sizes of a w4_moe call: the limits keep the 32-bit offsets of the kernels in range.
+int moe_shape(int fmt, int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k) {
+  if (!valid_fmt(fmt)) return W4_ERR_FORMAT;
+  const int64_t g = fmt_group(fmt);
+  if (tokens < 1 || tokens > W4_MAX_BATCH || experts < 1 || experts > W4_MOE_MAX_EXPERTS || top_k < 1 ||
+      top_k > W4_MOE_MAX_TOPK)
+    return W4_ERR_SHAPE;
+  if (hidden < g || hidden % g || inter < g || inter % g || hidden >= ((int64_t)1 << 22) ||
+      inter >= ((int64_t)1 << 22))
+    return W4_ERR_SHAPE;
+  const int64_t limit = ((int64_t)1 << 31) - 256;
+  if (tokens * hidden * 2 > limit || tokens * top_k * inter * 6 > limit) return W4_ERR_SHAPE;
+  return W4_OK;
+}
+
+}  // namespace
+
+size_t w4_moe_workspace_bytes(int fmt, int64_t tokens, int64_t hidden, int64_t inter, int64_t experts,
+                              int64_t top_k) {
+  if (moe_shape(fmt, tokens, hidden, inter, experts, top_k) != W4_OK) return 0;
+  return moe_workspace(tokens * top_k, hidden, inter);
+}
+
+int w4_moe(const void* x, const int32_t* ids, const float* weights, const uint8_t* gate_up,
+           const void* gate_up_scales, const uint8_t* down, const void* down_scales, int fmt,
+           int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k, float* y,
+           void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = moe_shape(fmt, tokens, hidden, inter, experts, top_k);
+  if (st == W4_ERR_FORMAT) return st;
+  if (!x || !ids || !weights || !gate_up || !gate_up_scales || !down || !down_scales || !y)
+    return W4_ERR_NULL;
+  if (st != W4_OK) return st;
+  const size_t sa = fmt_scale_bytes(fmt), sdiv = (size_t)fmt_group(fmt);
+  if (!aligned(x, 16) || !aligned(gate_up, 16) || !aligned(down, 16) || !aligned(gate_up_scales, sa) ||
+      !aligned(down_scales, sa) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(y, 4))
+    return W4_ERR_ALIGN;
+  const size_t used = moe_workspace(tokens * top_k, hidden, inter);
+  if (!workspace || workspace_bytes < used) return W4_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return W4_ERR_ALIGN;
+  const size_t pairs = (size_t)(tokens * top_k), per = (size_t)hidden * (size_t)inter;  // weights a matrix
+  const size_t gb = (size_t)experts * per, db = gb / 2, yb = (size_t)(tokens * hidden) * 4;
+  const void* in[7] = {x, ids, weights, gate_up, gate_up_scales, down, down_scales};
+  const size_t bytes[7] = {(size_t)(tokens * hidden) * 2, pairs * 4, pairs * 4, gb, 2 * gb / sdiv * sa, db,
+                           gb / sdiv * sa};
+  for (int i = 0; i < 7; ++i)
+    if (overlaps(y, yb, in[i], bytes[i]) || overlaps(workspace, used, in[i], bytes[i])) return W4_ERR_ALIAS;
+  if (overlaps(y, yb, workspace, used)) return W4_ERR_ALIAS;
+  return launch_moe(fmt, reinterpret_cast<const uint16_t*>(x), ids, weights, gate_up, gate_up_scales, down,
+                    down_scales, tokens, hidden, inter, experts, top_k, y, workspace,
+                    reinterpret_cast<hipStream_t>(stream)) == hipSuccess
+             ? W4_OK
+             : W4_ERR_HIP;
 }
 
 int w4_sparse24_compress(const float* w, int64_t n, int64_t k, int xtype, uint16_t* values,

@@ -1,0 +1,44 @@
+// Internal interface of the mixture-of-experts kernels (w4_moe*.hip).
+#pragma once
+#include "w4_common.h"
+
+namespace w4 {
+
+// One launch of an expert product.  Up: gate and up rows of one expert on the token rows of x.
+// Down: rows of one expert on the rows of h.
+struct MoeArgs {
+  const uint8_t* packed;   // [E, N, K/2]; up: N = 2 inter, gate rows first
+  const void* scales;      // [E, N, scales of K]
+  const uint16_t* cols;    // up: x [tokens, K]; down: the three planes of h [3, pairs, K]
+  const int32_t* ids;      // [pairs], pair = token * top_k + slot; outside [0, experts): absent
+  uint16_t* h;             // up: planes of h [3, pairs, inter]
+  float* part;             // down: [pairs, N]
+  uint32_t n;              // rows of one expert matrix
+  uint32_t k;
+  uint32_t experts;
+  uint32_t pairs;
+  uint32_t top_k;
+  uint32_t units;          // row units: up 16 gate + 16 up rows, down 32 rows
+  uint32_t qpk;            // quads (256 weights) per K group
+};
+
+constexpr int kMoeThreads = 512;   // 8 waves
+constexpr int kMoePacked = 5;      // tokens of a down chunk whose three planes share one column tile
+
+// kw K groups (1, 2, 4, 8) in a workgroup of 8 / kw row units; down also: column tiles (1: up to
+// kMoePacked tokens a chunk, 3: up to 16).  grid.y = slots (see moe_kernel).
+hipError_t launch_moe_up_f16(int weight, int kw, const MoeArgs& a, uint32_t slots, hipStream_t s);
+hipError_t launch_moe_up_bf16(int weight, int kw, const MoeArgs& a, uint32_t slots, hipStream_t s);
+hipError_t launch_moe_down(int weight, int kw, int tiles, const MoeArgs& a, uint32_t slots,
+                           hipStream_t s);
+
+// The layer (arguments as w4_moe, already validated).
+hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const float* weights,
+                      const uint8_t* gate_up, const void* gate_up_scales, const uint8_t* down,
+                      const void* down_scales, int64_t tokens, int64_t hidden, int64_t inter,
+                      int64_t experts, int64_t top_k, float* y, void* ws, hipStream_t s);
+size_t moe_workspace(int64_t pairs, int64_t hidden, int64_t inter);
+hipError_t launch_moe_route(const void* logits, int type, int64_t tokens, int64_t experts, int64_t top_k,
+                            bool renormalize, int32_t* ids, float* weights, hipStream_t s);
+
+}  // namespace w4

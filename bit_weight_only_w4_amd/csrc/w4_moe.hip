@@ -1,0 +1,215 @@
+// Mixture-of-experts layer: the router's choice, the combination of a token's experts, and the
+// launch rules of the expert products (w4_moe_impl.h).
+#include <algorithm>
+
+#include "w4_moe.h"
+
+namespace w4 {
+namespace {
+
+// Router: the top_k largest of a token's expert logits and their softmax weights.  One wave per
+// token, expert i in lane i % 64, register i / 64.  A logit becomes an unsigned key that orders
+// like it (-0 as +0), 0 for one that is never chosen (NaN, -inf); a round takes the largest key
+// (maximum over the wave) of the lowest expert (first register, first lane of a ballot).  The
+// weights are exp(v - max) over their sum, in fp32; a logit of +inf counts as its maximum's equal.
+// Bound by latency: one wave's chain of top_k reductions.
+template <int TYPE>
+__device__ inline float load_logit(const void* p, size_t i) {
+  if constexpr (TYPE == W4_LOGITS_F32) return reinterpret_cast<const float*>(p)[i];
+  if constexpr (TYPE == W4_LOGITS_F16) return (float)reinterpret_cast<const _Float16*>(p)[i];
+  return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << 16);
+}
+
+__device__ inline uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const uint32_t o = (uint32_t)__shfl_xor((int)v, off);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+
+__device__ inline float wave_sum(float v) {
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) v += __shfl_xor(v, off);
+  return v;
+}
+
+__device__ inline float key_value(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+
+__device__ inline float exp_from(float v, float top) { return v == top ? 1.0f : expf(v - top); }
+
+template <int TYPE, int NV>
+__global__ void __launch_bounds__(256) route_kernel(const void* __restrict__ logits, uint32_t tokens,
+                                                    uint32_t experts, uint32_t top_k, int renormalize,
+                                                    int32_t* __restrict__ ids, float* __restrict__ weights) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t t = blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
+  if (t >= tokens) return;
+  uint32_t key[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const uint32_t i = (uint32_t)lane + 64u * j;
+    key[j] = 0;
+    if (i < experts) {
+      const float v = load_logit<TYPE>(logits, (size_t)t * experts + i) + 0.0f;
+      const uint32_t u = __float_as_uint(v);
+      const bool never = v != v || u == 0xFF800000u;
+      key[j] = never ? 0u : u & 0x80000000u ? ~u : u ^ 0x80000000u;
+    }
+  }
+  float all = 0.0f, top = 0.0f, mine = 0.0f;
+  int mine_id = -1;
+  float chosen = 0.0f;
+  for (uint32_t r = 0; r < top_k; ++r) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) best = key[j] > best ? key[j] : best;
+    best = wave_max(best);
+    if (best == 0) break;  // nothing left to choose: the remaining slots stay absent
+    if (r == 0) {
+      top = key_value(best);
+      if (!renormalize) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (key[j] != 0) all += exp_from(key_value(key[j]), top);
+        all = wave_sum(all);
+      }
+    }
+    int id = -1;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const uint64_t mask = __ballot(key[j] == best);
+      if (id < 0 && mask != 0) {
+        const int at = __builtin_ctzll(mask);
+        id = 64 * j + at;
+        if (lane == at) key[j] = 0;
+      }
+    }
+    const float w = exp_from(key_value(best), top);
+    chosen += w;
+    if ((uint32_t)lane == r) {
+      mine = w;
+      mine_id = id;
+    }
+  }
+  if ((uint32_t)lane < top_k) {
+    const float sum = renormalize ? chosen : all;
+    ids[(size_t)t * top_k + lane] = mine_id;
+    weights[(size_t)t * top_k + lane] = mine_id < 0 ? 0.0f : mine / sum;
+  }
+}
+
+template <int TYPE>
+hipError_t route_type(const void* logits, uint32_t tokens, uint32_t experts, uint32_t top_k,
+                      int renorm, int32_t* ids, float* weights, hipStream_t s) {
+  const uint32_t waves = tokens < 4 ? tokens : 4;
+  const dim3 grid((tokens + waves - 1) / waves), block(64 * waves);
+#define W4_ROUTE(NV)                                                                              \
+  if (experts <= 64 * NV) {                                                                       \
+    hipLaunchKernelGGL((route_kernel<TYPE, NV>), grid, block, 0, s, logits, tokens, experts, top_k, \
+                       renorm, ids, weights);                                                     \
+    return hipGetLastError();                                                                     \
+  }
+  W4_ROUTE(1)
+  W4_ROUTE(2)
+  W4_ROUTE(4)
+  W4_ROUTE(8)
+  W4_ROUTE(16)
+#undef W4_ROUTE
+  return hipErrorInvalidValue;
+}
+
+// y[t] = sum over slots j, in order, of weights[t, j] * part[t * top_k + j]; absent slots add
+// nothing (their rows of `part` were never written), a token without experts gets zeros.
+__global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ part,
+                                                      const int32_t* __restrict__ ids,
+                                                      const float* __restrict__ weights, uint32_t hidden,
+                                                      uint32_t experts, uint32_t top_k,
+                                                      float* __restrict__ y) {
+  const uint32_t t = blockIdx.y;
+  const uint32_t n = blockIdx.x * 256 + threadIdx.x;
+  if (n >= hidden) return;
+  float v = 0.0f;
+  for (uint32_t j = 0; j < top_k; ++j) {
+    const uint32_t p = t * top_k + j;
+    if ((uint32_t)ids[p] < experts) v = __builtin_fmaf(weights[p], part[(size_t)p * hidden + n], v);
+  }
+  y[(size_t)t * hidden + n] = v;
+}
+
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
+// K groups: the fewest whose workgroups give every CU two, at most one per quad.
+int moe_kw(int64_t units, int64_t slots, int64_t k) {
+  const int64_t quads = (k + 255) / 256;
+  int kw = 1;
+  while (kw < 8 && 2 * kw <= quads && (units + 8 / kw - 1) / (8 / kw) * slots < 2 * device_cu_count())
+    kw *= 2;
+  return kw;
+}
+
+}  // namespace
+
+hipError_t launch_moe_route(const void* logits, int type, int64_t tokens, int64_t experts, int64_t top_k,
+                            bool renormalize, int32_t* ids, float* weights, hipStream_t s) {
+  const uint32_t t = (uint32_t)tokens, e = (uint32_t)experts, k = (uint32_t)top_k;
+  switch (type) {
+    case W4_LOGITS_F32: return route_type<W4_LOGITS_F32>(logits, t, e, k, renormalize, ids, weights, s);
+    case W4_LOGITS_F16: return route_type<W4_LOGITS_F16>(logits, t, e, k, renormalize, ids, weights, s);
+    case W4_LOGITS_BF16: return route_type<W4_LOGITS_BF16>(logits, t, e, k, renormalize, ids, weights, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+// The planes of h (three bf16 values per pair and row), then the partial results.
+size_t moe_workspace(int64_t pairs, int64_t hidden, int64_t inter) {
+  return align256((size_t)pairs * (size_t)inter * 6) + (size_t)pairs * (size_t)hidden * 4;
+}
+
+hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const float* weights,
+                      const uint8_t* gate_up, const void* gate_up_scales, const uint8_t* down,
+                      const void* down_scales, int64_t tokens, int64_t hidden, int64_t inter,
+                      int64_t experts, int64_t top_k, float* y, void* ws, hipStream_t s) {
+  const int64_t pairs = tokens * top_k;
+  const uint32_t slots = (uint32_t)std::min(pairs, experts);
+  const int weight = fmt_weight(fmt);
+  MoeArgs a{};
+  a.ids = ids;
+  a.h = reinterpret_cast<uint16_t*>(ws);
+  a.part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + align256((size_t)pairs * (size_t)inter * 6));
+  a.experts = (uint32_t)experts;
+  a.pairs = (uint32_t)pairs;
+  a.top_k = (uint32_t)top_k;
+
+  a.packed = gate_up;
+  a.scales = gate_up_scales;
+  a.cols = x;
+  a.n = (uint32_t)(2 * inter);
+  a.k = (uint32_t)hidden;
+  a.units = (uint32_t)(inter / 16);
+  int kw = moe_kw(a.units, slots, hidden);
+  a.qpk = (uint32_t)(((hidden + 255) / 256 + kw - 1) / kw);
+  hipError_t e = fmt_xtype(fmt) == kF16 ? launch_moe_up_f16(weight, kw, a, slots, s)
+                                        : launch_moe_up_bf16(weight, kw, a, slots, s);
+  if (e != hipSuccess) return e;
+
+  a.packed = down;
+  a.scales = down_scales;
+  a.cols = a.h;
+  a.n = (uint32_t)hidden;
+  a.k = (uint32_t)inter;
+  a.units = (uint32_t)(hidden / 32);
+  kw = moe_kw(a.units, slots, inter);
+  a.qpk = (uint32_t)(((inter + 255) / 256 + kw - 1) / kw);
+  e = launch_moe_down(weight, kw, pairs <= 2 * experts ? 1 : 3, a, slots, s);
+  if (e != hipSuccess) return e;
+
+  hipLaunchKernelGGL(combine_kernel, dim3((unsigned)((hidden + 255) / 256), (unsigned)tokens), dim3(256), 0,
+                     s, a.part, ids, weights, (uint32_t)hidden, (uint32_t)experts, (uint32_t)top_k, y);
+  return hipGetLastError();
+}
+
+}  // namespace w4

@@ -511,6 +511,66 @@ int w4_sparse24_gemv_grouped(const uint16_t* x, int groups, const uint16_t* cons
                              const uint8_t* const* meta, const int64_t* N, int xtype, int64_t K,
                              int64_t B, float* const* y, void* stream);
 
+/* ------------------------------------------------------------------ mixture of experts ----- */
+
+#define W4_MOE_MAX_EXPERTS 1024
+#define W4_MOE_MAX_TOPK 16
+
+typedef enum { W4_LOGITS_F32 = 0, W4_LOGITS_F16 = 1, W4_LOGITS_BF16 = 2 } w4_logits_type_t;
+
+/* w4_moe_route: the experts of each token and their routing weights, from the router's logits.
+ * Per token: the top_k largest logits in descending order, the lower expert first among equals; the
+ * weight of a chosen expert is exp(logit) over the sum of exp(logit) of the chosen experts
+ * (renormalize != 0) or of all experts (renormalize == 0).  A logit that is NaN or -inf is never
+ * chosen and adds nothing; where fewer than top_k are left, the remaining slots get id -1 and
+ * weight 0 (all of them in a row that is masked whole).  Logits of +inf share their weight
+ * equally.
+ *   logits       device [tokens, experts] of logits_type, read only; aligned to its element
+ *   tokens       1 <= tokens < 2^26
+ *   experts      1 <= experts <= W4_MOE_MAX_EXPERTS
+ *   top_k        1 <= top_k <= min(experts, W4_MOE_MAX_TOPK)
+ *   ids          device int32[tokens, top_k], written; 4-byte aligned
+ *   weights      device float[tokens, top_k], written; 4-byte aligned
+ * No output may overlap the logits or the other output.  Asynchronous on `stream`; no
+ * workspace. */
+int w4_moe_route(const void* logits, int logits_type, int64_t tokens, int64_t experts, int64_t top_k,
+                 int renormalize, int32_t* ids, float* weights, void* stream);
+
+/* w4_moe: a mixture-of-experts layer over 4-bit expert weights,
+ *   y[t] = sum_j weights[t, j] * Down_e (silu(Gate_e x[t]) * (Up_e x[t])),   e = ids[t, j],
+ * silu(v) = v / (1 + exp(-v)).  Made for a few tokens at a time (decode, drafted tokens, short
+ * prompts); any number up to W4_MAX_BATCH.
+ *   x        device [tokens, hidden] fp16 or bf16 (per fmt); 16-byte aligned
+ *   ids      device int32[tokens, top_k]; a slot whose id is outside [0, experts) is absent: it adds
+ *            nothing whatever its weight (experts on another device, masked slots); a token whose
+ *            slots are all absent gets y[t] = 0; an expert may appear in several slots of a token
+ *   weights  device float[tokens, top_k]
+ *   gate_up  device uint8[experts, 2 * inter, hidden / 2]: an expert's gate rows, then its up
+ *            rows, each row packed as for w4_gemv; 16-byte aligned
+ *   gate_up_scales  the format's scales of gate_up, [experts, 2 * inter, ...]
+ *   down     device uint8[experts, hidden, inter / 2]; 16-byte aligned
+ *   down_scales     the format's scales of down, [experts, hidden, ...]
+ *   fmt      any w4_format_t
+ *   tokens   1 <= tokens <= W4_MAX_BATCH, tokens * hidden * 2 < 2^31 - 256
+ *   hidden, inter   multiples of 64 (NF4, FP4, MXFP4) or 128 (INT4, INT4A), below 2^22
+ *   experts  1 <= experts <= W4_MOE_MAX_EXPERTS
+ *   top_k    1 <= top_k <= W4_MOE_MAX_TOPK, tokens * top_k * inter * 6 < 2^31 - 256
+ *   y        device float[tokens, hidden], fully overwritten; 4-byte aligned; must not overlap an
+ *            input or the workspace
+ *   workspace  device memory of at least w4_moe_workspace_bytes(...) bytes, 16-byte aligned; scratch
+ *            on entry and exit; must not overlap an input; two calls in flight must not share it
+ * fp32 accumulation; the products between the two matrices are kept to 24 bits, so y is exact up
+ * to fp32 sums (NF4: codes to 4e-7 of their rms).  The order of every sum is fixed: the same call
+ * gives the same bits.  Asynchronous on `stream`. */
+int w4_moe(const void* x, const int32_t* ids, const float* weights, const uint8_t* gate_up,
+           const void* gate_up_scales, const uint8_t* down, const void* down_scales, int fmt,
+           int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k, float* y,
+           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace w4_moe needs for these sizes; 0 for invalid ones. */
+size_t w4_moe_workspace_bytes(int fmt, int64_t tokens, int64_t hidden, int64_t inter, int64_t experts,
+                              int64_t top_k);
+
 /* ------------------------------------------------------------------ measurement probes ------ */
 
 /* Streaming-read ceiling probe: reads `bytes` (multiple of 16) from device `src` with 128-bit
