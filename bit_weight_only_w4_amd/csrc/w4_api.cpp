@@ -1141,8 +1141,8 @@ int w4_moe(const void* x, const int32_t* ids, const float* weights, const uint8_
     return W4_ERR_NULL;
   if (st != W4_OK) return st;
   const size_t sa = fmt_scale_bytes(fmt), sdiv = (size_t)fmt_group(fmt);
-  if (!aligned(x, 16) || !aligned(gate_up, 16) || !aligned(down, 16) || !aligned(gate_up_scales, sa) ||
-      !aligned(down_scales, sa) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(y, 4))
+  if (!aligned(x, 16) || !aligned(gate_up, 16) || !aligned(down, 16) || !aligned(gate_up_scales, 4) ||
+      !aligned(down_scales, 4) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(y, 4))
     return W4_ERR_ALIGN;
   const size_t used = moe_workspace(tokens * top_k, hidden, inter);
   if (!workspace || workspace_bytes < used) return W4_ERR_WORKSPACE;

@@ -9,7 +9,7 @@ namespace w4 {
 struct MoeArgs {
   const uint8_t* packed;   // [E, N, K/2]; up: N = 2 inter, gate rows first
   const void* scales;      // [E, N, scales of K]
-  const uint16_t* cols;    // up: x [tokens, K]; down: the three planes of h [3, pairs, K]
+  const uint16_t* x;       // up: x [tokens, K]; down: the three planes of h [3, pairs, K]
   const int32_t* ids;      // [pairs], pair = token * top_k + slot; outside [0, experts): absent
   uint16_t* h;             // up: planes of h [3, pairs, inter]
   float* part;             // down: [pairs, N]
@@ -18,15 +18,20 @@ struct MoeArgs {
   uint32_t experts;
   uint32_t pairs;
   uint32_t top_k;
-  uint32_t units;          // row units: up 16 gate + 16 up rows, down 32 rows
+  uint32_t tiles;          // row tiles of 16 rows, even; up: gate and up tiles alternate
   uint32_t qpk;            // quads (256 weights) per K group
+  uint32_t qpw;            // quads per activation window, a multiple of the K groups
+  uint32_t cols;           // pairs of a chunk: at most 16 per column tile (down with one tile: 4)
+  uint32_t grid;           // workgroups of a slot, at most one per group of tiles
+  uint32_t win_bytes;      // LDS bytes of a window: rows * qpw * 512
 };
 
 constexpr int kMoeThreads = 512;   // 8 waves
-constexpr int kMoePacked = 5;      // tokens of a down chunk whose three planes share one column tile
+constexpr uint32_t kMoeMaxWindow = 81920;  // LDS bytes of a window
+constexpr int kMoePacked = 4;      // pairs of a down chunk whose three planes share one tile
 
-// kw K groups (1, 2, 4, 8) in a workgroup of 8 / kw row units; down also: column tiles (1: up to
-// kMoePacked tokens a chunk, 3: up to 16).  grid.y = slots (see moe_kernel).
+// kw K groups (1, 2, 4) in a workgroup of 8 / kw row tiles; down also: tiles (1: up to kMoePacked
+// pairs a chunk, 3: up to 16, a tile per plane).  grid.y = slots (see moe_kernel).
 hipError_t launch_moe_up_f16(int weight, int kw, const MoeArgs& a, uint32_t slots, hipStream_t s);
 hipError_t launch_moe_up_bf16(int weight, int kw, const MoeArgs& a, uint32_t slots, hipStream_t s);
 hipError_t launch_moe_down(int weight, int kw, int tiles, const MoeArgs& a, uint32_t slots,

@@ -142,13 +142,36 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
-// K groups: the fewest whose workgroups give every CU two, at most one per quad.
-int moe_kw(int64_t units, int64_t slots, int64_t k) {
+// Workgroups of a slot (MoeArgs::grid): as many as give the possible experts in use two per CU together,
+// what fits; each then walks the expert's tile groups with its loads running ahead and one window
+// of activations.  Measured on MI355X (32 tokens, 8 of 128 experts, 2048 x 768, MXFP4): 4 workgroups of each expert
+// and direction 83.5 us, one per tile group 92.
+// K groups: the fewest whose workgroups give every CU two, at most one per quad, and two quads of
+// `rows` window rows for each inside the largest window.
+int moe_kw(int64_t tiles, int64_t slots, int64_t k, int64_t rows) {
   const int64_t quads = (k + 255) / 256;
   int kw = 1;
-  while (kw < 8 && 2 * kw <= quads && (units + 8 / kw - 1) / (8 / kw) * slots < 2 * device_cu_count())
+  while (kw < 4 && 2 * kw <= quads && rows * 1024 * 2 * kw <= kMoeMaxWindow &&
+         (tiles + 8 / kw - 1) / (8 / kw) * slots < 2 * device_cu_count())
     kw *= 2;
   return kw;
+}
+
+// Quads, window and chunk of a product over K with kw K groups: `cols` pairs a chunk of `planes`
+// rows each, and as many quads a window as fit kWindowBytes (all of K if it fits).
+constexpr int64_t kWindowBytes = 65536;
+
+void moe_window(int64_t k, int kw, uint32_t cols, uint32_t planes, MoeArgs* a) {
+  const int64_t qpk = ((k + 255) / 256 + kw - 1) / kw;
+  const int64_t rows = (int64_t)cols * planes;
+  const int64_t fit = std::max<int64_t>(1, kWindowBytes / (rows * 512 * kw));
+  // (windows of an even number of quads of a K group: the loop takes two at a time)
+  const int64_t windows = (qpk + fit - 1) / fit;
+  const int64_t per = windows == 1 ? qpk : std::max<int64_t>(2, ((qpk + windows - 1) / windows + 1) / 2 * 2);
+  a->qpk = (uint32_t)qpk;
+  a->qpw = (uint32_t)(per * kw);
+  a->cols = cols;
+  a->win_bytes = (uint32_t)rows * a->qpw * 512u;
 }
 
 }  // namespace
@@ -186,25 +209,29 @@ hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const floa
 
   a.packed = gate_up;
   a.scales = gate_up_scales;
-  a.cols = x;
+  a.x = x;
   a.n = (uint32_t)(2 * inter);
   a.k = (uint32_t)hidden;
-  a.units = (uint32_t)(inter / 16);
-  int kw = moe_kw(a.units, slots, hidden);
-  a.qpk = (uint32_t)(((hidden + 255) / 256 + kw - 1) / kw);
+  a.tiles = (uint32_t)(inter / 8);
+  uint32_t cols = (uint32_t)std::min<int64_t>(16, tokens);
+  int kw = moe_kw(a.tiles, slots, hidden, cols);
+  a.grid = (uint32_t)std::max<int64_t>(1, 2 * device_cu_count() / slots);
+  moe_window(hidden, kw, cols, 1, &a);
   hipError_t e = fmt_xtype(fmt) == kF16 ? launch_moe_up_f16(weight, kw, a, slots, s)
                                         : launch_moe_up_bf16(weight, kw, a, slots, s);
   if (e != hipSuccess) return e;
 
   a.packed = down;
   a.scales = down_scales;
-  a.cols = a.h;
+  a.x = a.h;
   a.n = (uint32_t)hidden;
   a.k = (uint32_t)inter;
-  a.units = (uint32_t)(hidden / 32);
-  kw = moe_kw(a.units, slots, inter);
-  a.qpk = (uint32_t)(((inter + 255) / 256 + kw - 1) / kw);
-  e = launch_moe_down(weight, kw, pairs <= 2 * experts ? 1 : 3, a, slots, s);
+  a.tiles = (uint32_t)(hidden / 16);
+  const int tiles = pairs <= 2 * experts ? 1 : 3;
+  cols = (uint32_t)std::min<int64_t>(tiles == 1 ? kMoePacked : 16, tokens);
+  kw = moe_kw(a.tiles, slots, inter, 3 * cols);
+  moe_window(inter, kw, cols, 3, &a);
+  e = launch_moe_down(weight, kw, tiles, a, slots, s);
   if (e != hipSuccess) return e;
 
   hipLaunchKernelGGL(combine_kernel, dim3((unsigned)((hidden + 255) / 256), (unsigned)tokens), dim3(256), 0,

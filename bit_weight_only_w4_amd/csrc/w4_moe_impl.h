@@ -12,23 +12,34 @@
 // its expert's pairs itself, 64 ids at a time (a ballot, and a lane permutation that hands the r-th
 // pair to lane r): no launch, memory or barrier for a sorted list.
 //
-// Inside a workgroup 8 waves are RW row units x KW K groups.  A unit is two 16-row tiles that share
-// every activation fragment: a gate tile and its up tile (the product silu(g) u then needs no
-// exchange), or two adjacent row tiles of the down matrix.  A wave streams its unit's quads (256
-// weights of each row, two 16-byte loads per lane and tile, whole 128-byte lines) and activations
-// into one of two register sets while it multiplies the other:
-//   * v_mfma_f32_16x16x32, A = 16 weight rows x 32 k, B = 32 k x 16 columns, the k order inside a
-//     block permuted alike on both sides (see load_quad); fp32 accumulation per scale block, then
-//     acc += scale[row] * D.
-//   * Weight codes are exact 16-bit values (E2M1 through the hardware conversion; q - 8 through a
-//     byte -> pair LDS table, asymmetric INT4 with one more MFMA whose rows hold -(z - 8)).  NF4's codes
-//     are not: they are held as two 16-bit terms, after a factor of 1.4376 (taken off the sums)
-//     that leaves the two bf16 terms an rms error of 4.2e-7 over normal weights (2.5e-6 without it).
+// Inside a workgroup 8 waves are RT row tiles (16 weight rows each) x KW K groups; the tiles of the
+// up direction alternate between a gate tile and the up tile of the same rows.  K runs in quads (256
+// weights of a row), in KW contiguous ranges.  A workgroup walks several groups of RT tiles of its
+// expert, its loads running ahead across them.
+//   * v_mfma_f32_16x16x32, A = 16 columns of the chunk x 32 k from LDS, B = 32 k x 16 weight rows
+//     decoded in registers, the k order inside a block permuted alike on both sides.  A lane's
+//     results all belong to one weight row, so the block scale is the lane's own: fp32 accumulation
+//     per scale block, then acc += scale * D.
+//   * A lane's weights arrive in two 16-byte loads per quad (whole 128-byte lines), two quads ahead of
+//     the one being multiplied.
+//   * The chunk's activations are copied into LDS once per window (all of K where it fits), 16-byte
+//     pieces at position piece ^ (row mod 16): the 16 lanes that an LDS cycle serves read
+//     16 different rows at one k, and the exclusive or puts them in different banks.
+//   * Weight codes are exact 16-bit values, decoded without a table: E2M1 through the hardware
+//     conversion, integers as q + 16 (two operations a pair) with one more MFMA whose columns
+//     hold -(16 + z) taking the offset off.  The activations are put into the decoder's order on their
+//     way into the window.  NF4's codes are not exact: they are held as two 16-bit terms in a byte
+//     -> pair LDS table, after a factor of 1.4376 (taken off the sums) that leaves the two bf16
+//     terms an rms error of 4.2e-7 over normal weights (2.5e-6 without it).
 //   * h has fp32's 24 bits as three bf16 planes (the value cut after 8 bits, then the rest, then
-//     what is left), which keeps bf16's range for either activation type.  The planes are
-//     columns of the same product: up to five tokens' planes fill one 16-column tile, so keeping
-//     24 bits costs a few tokens nothing; from six tokens on a plane is a column tile of its own.
+//     what is left), which keeps bf16's range for either activation type.  The planes are rows of
+//     the same product: four tokens' planes share one 16-row tile, so keeping 24 bits costs a few
+//     tokens nothing; from five tokens on a plane is a tile of its own.
+//   * A group's sums go through LDS, where every thread takes its share of the results: the K groups
+//     are added in group order, gate meets up, and a row's values are stored side by side.
 #pragma once
+#include <type_traits>
+
 #include "w4_mfma_common.h"
 #include "w4_moe.h"
 
@@ -38,452 +49,565 @@ namespace {
 constexpr int kUp = 0, kDown = 1;
 constexpr float kNf4Factor = 1.4376f;
 
-// Byte -> decoded pair table: 32 copies of each 4-byte entry, or 16 of each 8-byte NF4 entry
-// (first terms, second terms), 128 bytes per entry.
-template <int FMT, int XT>
+// NF4's byte -> decoded pair table: 16 copies of each 8-byte entry (first terms, second terms), lane L
+// reading copy L % 16.
+template <int XT>
 __device__ inline void fill_moe_table(uint32_t* tab) {
-  uint32_t v1, v2 = 0;
-  if (FMT == kNF4) {
-    const float c = __uint_as_float(codes_in_lanes<kNF4>()) * kNf4Factor;
-    if (XT == kF16) {
-      const _Float16 hi = (_Float16)c;
-      v1 = f16_bits((float)hi);
-      v2 = f16_bits(c - (float)hi);
-    } else {
-      v1 = bf16_rne_bits(c);
-      v2 = bf16_rne_bits(c - __uint_as_float(v1 << 16));
-    }
+  const float c = __uint_as_float(codes_in_lanes<kNF4>()) * kNf4Factor;
+  uint32_t v1, v2;
+  if (XT == kF16) {
+    const _Float16 hi = (_Float16)c;
+    v1 = f16_bits((float)hi);
+    v2 = f16_bits(c - (float)hi);
   } else {
-    const float v = (float)((int)(threadIdx.x & 15u) - 8);
-    v1 = XT == kF16 ? f16_bits(v) : (__float_as_uint(v) >> 16);
+    v1 = bf16_rne_bits(c);
+    v2 = bf16_rne_bits(c - __uint_as_float(v1 << 16));
   }
   uint4* t4 = reinterpret_cast<uint4*>(tab);
   const int tid = threadIdx.x;
   const uint32_t lo1 = (uint32_t)__shfl((int)v1, (tid >> 3) & 15) << 16;
-  const uint32_t lo2 = FMT == kNF4 ? (uint32_t)__shfl((int)v2, (tid >> 3) & 15) << 16 : 0u;
+  const uint32_t lo2 = (uint32_t)__shfl((int)v2, (tid >> 3) & 15) << 16;
 #pragma unroll
   for (int j = 0; j < kTableBytes / 16 / kMoeThreads; ++j) {
     const int i = tid + kMoeThreads * j;
     const int hi = __builtin_amdgcn_readfirstlane(i >> 7);
     const uint32_t p1 = (uint32_t)__builtin_amdgcn_readlane((int)v1, hi) | lo1;
-    if (FMT == kNF4) {
-      const uint32_t p2 = (uint32_t)__builtin_amdgcn_readlane((int)v2, hi) | lo2;
-      t4[i] = make_uint4(p1, p2, p1, p2);
-    } else {
-      t4[i] = make_uint4(p1, p1, p1, p1);
-    }
+    const uint32_t p2 = (uint32_t)__builtin_amdgcn_readlane((int)v2, hi) | lo2;
+    t4[i] = make_uint4(p1, p2, p1, p2);
   }
 }
 
-// The four E2M1 pairs of a packed dword in memory order (high nibble first) as 16-bit pairs.  The
-// conversion returns a byte's low nibble in the low half, so the nibbles are swapped first.
-template <int XT>
-__device__ inline uint4 e2m1_pairs(uint32_t w) {
-  w = ((w >> 4) & 0x0F0F0F0Fu) | ((w << 4) & 0xF0F0F0F0u);
-  if constexpr (XT == kF16) {
-    return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0)),
-                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1)),
-                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2)),
-                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3)));
+// Eight weights of a packed dword as 16-bit pairs, without a table.  Each decoder gives its own order of
+// the eight, and `arranged` puts an activation piece (8 values in memory order) into that order.
+//   E2M1: one conversion per byte, the low nibble (odd k) first.
+//   q + 16 (integers): the nibble of each half placed in the mantissa of 16.0, two operations a pair:
+//   nibbles 0, 1, 2, 3 of the halves, which are k = (1, 5), (0, 4), (3, 7), (2, 6).
+template <int FMT, int XT>
+__device__ inline uint4 decode8(uint32_t w) {
+  if constexpr (FMT == kFP4 || FMT == kMXFP4) {
+    if constexpr (XT == kF16) {
+      return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0)),
+                        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1)),
+                        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2)),
+                        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3)));
+    } else {
+      return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0)),
+                        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1)),
+                        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2)),
+                        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3)));
+    }
+  } else if constexpr (XT == kF16) {  // 16.0 = 0x4C00, one unit = 1 << 6
+    constexpr uint32_t kMask = 0x03C003C0u, kOne = 0x4C004C00u;
+    return make_uint4(((w << 6) & kMask) | kOne, ((w << 2) & kMask) | kOne, ((w >> 2) & kMask) | kOne,
+                      ((w >> 6) & kMask) | kOne);
+  } else {  // 16.0 = 0x4180, one unit = 1 << 3
+    constexpr uint32_t kMask = 0x00780078u, kOne = 0x41804180u;
+    return make_uint4(((w << 3) & kMask) | kOne, ((w >> 1) & kMask) | kOne, ((w >> 5) & kMask) | kOne,
+                      ((w >> 9) & kMask) | kOne);
+  }
+}
+
+template <int FMT>
+__device__ inline uint4 arranged(uint4 v) {
+  if constexpr (FMT == kFP4 || FMT == kMXFP4) {
+    return make_uint4(__builtin_amdgcn_alignbit(v.x, v.x, 16), __builtin_amdgcn_alignbit(v.y, v.y, 16),
+                      __builtin_amdgcn_alignbit(v.z, v.z, 16), __builtin_amdgcn_alignbit(v.w, v.w, 16));
+  } else if constexpr (is_g128(FMT)) {
+    constexpr uint32_t kHi = 0x07060302u, kLo = 0x05040100u;  // (second, first) operand's halves
+    return make_uint4(__builtin_amdgcn_perm(v.z, v.x, kHi), __builtin_amdgcn_perm(v.z, v.x, kLo),
+                      __builtin_amdgcn_perm(v.w, v.y, kHi), __builtin_amdgcn_perm(v.w, v.y, kLo));
   } else {
-    return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0)),
-                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1)),
-                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2)),
-                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3)));
+    return v;
   }
 }
 
 // The pairs of expert e in pair order: returns their number and the first of them, and in lane r
-// (r < ncol <= 63) the pair of rank c0 + r, or -1.  Every lane of the wave takes part.
-__device__ inline uint32_t scan_pairs(const int32_t* __restrict__ ids, uint32_t pairs, int e,
+// (r < ncol <= 63) the pair of rank c0 + r, or -1.  `id0` holds the first 64 ids, one a lane (-1 past
+// the last).  Every lane of the wave takes part.
+__device__ inline uint32_t scan_pairs(const int32_t* __restrict__ ids, uint32_t pairs, int id0, int e,
                                       uint32_t c0, uint32_t ncol, int lane, uint32_t& first, int& mine) {
   uint32_t total = 0;
   first = 0xFFFFFFFFu;
   mine = -1;
-  for (uint32_t base = 0; base < pairs; base += 64) {
-    const uint32_t i = base + (uint32_t)lane;
-    const int id = i < pairs ? ids[i] : -1;
+  auto batch = [&](uint32_t base, int id) __attribute__((always_inline)) {
     const bool match = id == e;
     const uint64_t mask = __ballot(match);
+    if (mask == 0) return;
     const uint32_t rank = total + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
                                                             __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
     // lanes without a pair of this chunk send to lane 63, which is no column
-    const uint32_t to = match && rank >= c0 && rank - c0 < ncol ? rank - c0 : 63u;
-    const int got = __builtin_amdgcn_ds_permute((int)(to * 4u), (int)(i + 1u));
+    const uint32_t to = match && rank - c0 < ncol ? rank - c0 : 63u;
+    const int got = __builtin_amdgcn_ds_permute((int)(to * 4u), (int)(base + (uint32_t)lane + 1u));
     if (lane < (int)ncol && got > 0) mine = got - 1;
-    if (first == 0xFFFFFFFFu && mask != 0) first = base + (uint32_t)__builtin_ctzll(mask);
+    if (first == 0xFFFFFFFFu) first = base + (uint32_t)__builtin_ctzll(mask);
     total += (uint32_t)__builtin_popcountll(mask);
+  };
+  batch(0, id0);
+  // then eight batches at a time: their loads are in flight together
+  for (uint32_t base = 64; base < pairs; base += 512) {
+    int id[8];
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      const uint32_t i = base + 64u * b + (uint32_t)lane;
+      id[b] = i < pairs ? ids[i] : -1;
+    }
+#pragma unroll
+    for (int b = 0; b < 8; ++b) batch(base + 64u * b, id[b]);
   }
   return total;
 }
 
-template <int FMT>
+// A quad of this lane's tile: load h.
 struct MoeQuad {
-  static constexpr int QC = is_g128(FMT) ? 2 : 4;  // scale blocks (MXFP4: block pairs) per quad
-  uint32_t w[2][2][4];  // [tile][load][dword]
-  uint32_t s[2][QC];    // as loaded, for one D row of each tile
+  uint32_t w[2][4];
+};
+
+// Block scales.  The scales of 16 rows lie together in memory, a few bytes of each row per quad, so they
+// are loaded for eight quads at a time: lane 4 r + p takes those of quads 2 p, 2 p + 1 of row r, and a
+// quad's scales reach the 4 lanes of their row by lane permutations.  (Loaded quad by quad, each load
+// touched 16 cache lines for a few bytes of each, and re-fetched them from L2 at every quad.)
+template <int FMT>
+struct MoeScales {
+  static constexpr uint32_t kQuads = 8;
+  static constexpr int kPer = FMT == kMXFP4 ? 2 : FMT == kINT4 ? 1 : FMT == kINT4A ? 2 : 4;  // dwords a quad
+  // 2-byte rows: one dword more, loaded from the aligned address below and shifted into place
+  static constexpr bool kShift = FMT == kMXFP4 || FMT == kINT4;
+  static constexpr int kRaw = 2 * kPer + (kShift ? 1 : 0);
+  uint32_t v[kRaw];
 };
 
 template <int DIR, int FMT, int XT, int NT, int KW>
-__global__ void __launch_bounds__(kMoeThreads, 2) moe_kernel(MoeArgs a) {
-  constexpr int RW = 8 / KW;
+__global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 4 : 2) moe_kernel(MoeArgs a) {
+  constexpr uint32_t RT = 8 / KW;
   constexpr int KC = is_g128(FMT) ? 128 : 64;  // weights per block
-  constexpr int QC = 256 / KC;
+  constexpr uint32_t QC = 256 / KC;
   constexpr int STEPS = KC / 32;
   constexpr bool kMX = FMT == kMXFP4;
-  constexpr bool kTable = FMT != kFP4 && !kMX;
-  constexpr bool kSplit = FMT == kNF4;
-  constexpr int SB = FMT == kINT4 || kMX ? 2 : 4;
-  constexpr uint32_t kCols = DIR == kUp ? 16u * NT : NT == 1 ? (uint32_t)kMoePacked : 16u * (NT / 3);
+  constexpr bool kTable = FMT == kNF4;
+  constexpr uint32_t SB = FMT == kINT4 || kMX ? 2 : 4;
   __shared__ __align__(16) uint32_t tab[kTable ? kTableBytes / 4 : 4];
-  __shared__ float4_t red[KW > 1 ? (KW - 1) * RW * 2 * NT * 64 : 1];
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint8_t* win = smem;                                          // the window of activations
+  float* sums = reinterpret_cast<float*>(smem + a.win_bytes);  // two buffers of [8 waves][NT][4][64]
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int rg = wave % RW, kg = wave / RW;
+  const uint32_t rt = (uint32_t)wave % RT, kg = (uint32_t)wave / RT;
   const int g = lane >> 4, m = lane & 15;
 
-  // This slot's expert.
+  // This slot's expert, and the first 64 ids, before any other vector load: loads complete in order,
+  // and what waits for the ids must not wait for weights.
   const bool by_pair = a.pairs < a.experts;
-  const int e = by_pair ? a.ids[blockIdx.y] : (int)blockIdx.y;
+  const int id0 = (uint32_t)lane < a.pairs ? a.ids[lane] : -1;
+  if constexpr (kTable) fill_moe_table<XT>(tab);
+  const int e = !by_pair ? (int)blockIdx.y
+                : blockIdx.y < 64 ? __builtin_amdgcn_readlane(id0, (int)blockIdx.y) : a.ids[blockIdx.y];
   if ((uint32_t)e >= a.experts) return;
+  const uint32_t cols = a.cols;  // pairs of a chunk
 
+  const uint32_t qpk = a.qpk;
   const uint32_t pitch = a.k >> 1;
   const uint32_t nblocks = a.k / KC;
   const uint32_t spitch = nblocks * SB;
-  const uint32_t unit = blockIdx.x * RW + (uint32_t)rg;
-  const uint32_t live = unit < a.units ? 16u : 0u;  // a wave past the last unit reads zeros
-  const uint32_t row0 = DIR == kUp ? unit * 16u : unit * 32u;
-  const uint32_t row1 = DIR == kUp ? (a.n >> 1) + unit * 16u : unit * 32u + 16u;
-  __amdgpu_buffer_rsrc_t rw[2], rs[2];
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const size_t row = (size_t)e * a.n + (live ? (r ? row1 : row0) : 0u);
-    rw[r] = make_rsrc(a.packed + row * pitch, live * pitch);
-    rs[r] = make_rsrc(reinterpret_cast<const char*>(a.scales) + row * spitch, live * spitch);
-  }
+  const uint32_t ngroups = (a.tiles + RT - 1) / RT;
+  // First weight row of tile `tile` (tiles past the last: none, they read zeros).
+  auto tile_rsrc = [&](const void* base, uint32_t tile, uint32_t bytes) __attribute__((always_inline)) {
+    const bool live = tile < a.tiles;
+    const uint32_t row0 = DIR == kUp ? (tile & 1u) * (a.n >> 1) + (tile >> 1) * 16u : tile * 16u;
+    const size_t row = (size_t)e * a.n + (live ? row0 : 0u);
+    return make_rsrc(reinterpret_cast<const char*>(base) + row * bytes, live ? 16u * bytes : 0u);
+  };
 
-  // Weight loads of lane (g, m): load h covers rows 8 h .. 8 h + 7 with 8 lanes on the 128 bytes of
-  // each row's quad: the lane's own row m when m >> 3 == h, else its partner row m ^ 8; rotating by
-  // 8 lanes later gives lane (g, m) chunks g and g + 4 (16 bytes each) of row m.
-  const uint32_t chunk0 = m < 8 ? g : g + 4, chunk1 = m < 8 ? g + 4 : g;
-  const uint32_t wl0 = (uint32_t)(m & 7) * pitch + chunk0 * 16u;
-  const uint32_t wl1 = (uint32_t)(8 + (m & 7)) * pitch + chunk1 * 16u;
-  const uint32_t slane = (uint32_t)(4 * g + (m & 3)) * spitch;
+  // The load cursor: quad lj of tile lt.
+  uint32_t lt, lj;
+  __amdgpu_buffer_rsrc_t rw;
+  // Weight loads of lane (g, m): load h covers rows 8 h .. 8 h + 7, whole 128-byte lines with 8 lanes
+  // each: the lane takes row 8 h + (m & 7), chunk (16 bytes) g + 4 (m >> 3).
+  const uint32_t chunk = (uint32_t)g + 4u * (uint32_t)(m >> 3);
+  const uint32_t wlane = (uint32_t)(m & 7) * pitch + chunk * 16u;
   const uint32_t nchunks = a.k >> 5;
-
-  auto load_weights = [&](uint32_t q, bool in, MoeQuad<FMT>& d) __attribute__((always_inline)) {
-    const uint32_t qb = q * QC;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const uint4 v0 = buffer_load16_stream(rw[r], offset_or_oob(in && q * 8 + chunk0 < nchunks, wl0 + q * 128u));
-      const uint4 v1 = buffer_load16_stream(rw[r], offset_or_oob(in && q * 8 + chunk1 < nchunks, wl1 + q * 128u));
-      d.w[r][0][0] = v0.x; d.w[r][0][1] = v0.y; d.w[r][0][2] = v0.z; d.w[r][0][3] = v0.w;
-      d.w[r][1][0] = v1.x; d.w[r][1][1] = v1.y; d.w[r][1][2] = v1.z; d.w[r][1][3] = v1.w;
-      if constexpr (!is_g128(FMT) && !kMX) {
-        // blocks past K hold the next row's scales here; they are zeroed when used
-        const uint4 sv = buffer_load16(rs[r], offset_or_oob(in && qb < nblocks, slane + qb * SB));
-        d.s[r][0] = sv.x; d.s[r][1] = sv.y; d.s[r][2] = sv.z; d.s[r][3] = sv.w;
-      } else {
-#pragma unroll
-        for (int c = 0; c < QC; ++c) {
-          const uint32_t off = offset_or_oob(in && qb + c < nblocks, slane + (qb + c) * SB);
-          d.s[r][c] = FMT == kINT4A ? buffer_load32(rs[r], off) : buffer_load16bit(rs[r], off);
-        }
-      }
+  // The quad at the cursor (past K everything reads as zero), and the cursor's step: tiles of an even
+  // number of quads, the last of an odd count left out.
+  auto load_quad = [&](MoeQuad& d) __attribute__((always_inline)) {
+    if (lj < qpk) {
+      const uint32_t q = kg * qpk + lj;
+      const bool in = q * 8 + chunk < nchunks;
+      const uint4 v0 = buffer_load16_stream(rw, offset_or_oob(in, wlane + q * 128u));
+      const uint4 v1 = buffer_load16_stream(rw, offset_or_oob(in, wlane + q * 128u + 8u * pitch));
+      d.w[0][0] = v0.x; d.w[0][1] = v0.y; d.w[0][2] = v0.z; d.w[0][3] = v0.w;
+      d.w[1][0] = v1.x; d.w[1][1] = v1.y; d.w[1][2] = v1.z; d.w[1][3] = v1.w;
+    }
+    if (++lj >= ((qpk + 1u) & ~1u)) {
+      lj = 0;
+      lt += gridDim.x * RT;
+      rw = tile_rsrc(a.packed, lt, pitch);
     }
   };
 
-  const uint32_t qpk = a.qpk, q0 = (uint32_t)kg * qpk;
-  MoeQuad<FMT> W0, W1;
-  load_weights(q0, true, W0);
-  load_weights(q0 + 1, 1 < qpk, W1);
+  // The scale cursor, window sj (eight quads) of tile st, one window ahead of the multiplication.
+  using Sc = MoeScales<FMT>;
+  uint32_t st, sj;
+  const uint32_t nsw = (qpk + Sc::kQuads - 1) / Sc::kQuads;
+  auto load_scales = [&](Sc& d) __attribute__((always_inline)) {
+    const uint32_t q = kg * qpk + sj * Sc::kQuads;
+    const uint32_t at = (uint32_t)(lane >> 2) * spitch + (q + 2u * (uint32_t)(lane & 3)) * (QC * SB);
+    const uint32_t off = offset_or_oob(q * QC < nblocks, at & ~3u);
+    const __amdgpu_buffer_rsrc_t rs = tile_rsrc(a.scales, st, spitch);
+    if constexpr (FMT == kINT4) {
+      const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, (int)off, 0, 0);
+      d.v[0] = v[0];
+      d.v[1] = v[1];
+      d.v[2] = buffer_load32(rs, off + 8u);
+    } else {
+      const uint4 v = buffer_load16(rs, off);
+      d.v[0] = v.x; d.v[1] = v.y; d.v[2] = v.z; d.v[3] = v.w;
+      if constexpr (kMX) d.v[4] = buffer_load32(rs, off + 16u);
+      if constexpr (Sc::kPer == 4) {
+        const uint4 u = buffer_load16(rs, off + 16u);
+        d.v[4] = u.x; d.v[5] = u.y; d.v[6] = u.z; d.v[7] = u.w;
+      }
+    }
+    if (++sj == nsw) {
+      sj = 0;
+      st += gridDim.x * RT;
+    }
+  };
+  // bits by which this lane's 2-byte rows start inside their first dword (rows of every tile alike:
+  // a tile starts on a multiple of 32 bytes)
+  const uint32_t sshift = ((uint32_t)(lane >> 2) * spitch & 2u) * 8u;
 
-  if constexpr (kTable) fill_moe_table<FMT, XT>(tab);
-  uint32_t first, count;
-  int list;
-  count = scan_pairs(a.ids, a.pairs, e, 0, kCols, lane, first, list);
-  // without pairs, or another slot has this expert: every wave sees the same count
-  if (count == 0 || (by_pair && first != blockIdx.y)) return;
-  if constexpr (kTable) __syncthreads();
-
-  const uint32_t laneoff = kSplit ? (uint32_t)(lane & 15) * 16u : (uint32_t)(lane & 31) * 8u;
+  const uint32_t laneoff = (uint32_t)(lane & 15) * 16u;
   const char* tabc = reinterpret_cast<const char*>(tab);
-  // k of this lane's first weight of a block's first step, and the step's stride
-  const uint32_t klane = kMX ? 8 * g : is_g128(FMT) ? 32 * g : 32 * (g & 1) + 16 * (g >> 1);
-  constexpr uint32_t kstep = kMX ? 32 : 8;
-  const int zsrc = 16 * (m >> 2) + (m & 3);  // lane holding the scale word of A row m
+  const uint32_t rpitch = a.qpw * 512u;  // bytes of a window row: its quads
+  const uint32_t per = a.qpw / KW;       // quads of a K group per window
+  // This lane's A row in each column tile, as its window offset, and its piece of a block's first
+  // step with the row's exclusive or.
+  uint32_t arow[NT], apiece[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const uint32_t last = cols - 1u;
+    const uint32_t r = DIR == kUp ? min((uint32_t)(16 * t + m), last)
+                       : NT == 1  ? (uint32_t)min(m >> 2, 2) * cols + min((uint32_t)(m & 3), last)
+                                  : (uint32_t)t * cols + min((uint32_t)m, last);
+    const uint32_t piece = kMX ? g : is_g128(FMT) ? 4 * g : 4 * (g & 1) + 2 * (g >> 1);
+    arow[t] = r * rpitch + kg * per * 512u;
+    apiece[t] = (piece ^ (r & 15u)) * 16u;
+  }
   const __amdgpu_buffer_rsrc_t rx =
-      make_rsrc(a.cols, (DIR == kUp ? a.pairs / a.top_k : 3u * a.pairs) * a.k * 2u);
+      make_rsrc(a.x, (DIR == kUp ? a.pairs / a.top_k : 3u * a.pairs) * a.k * 2u);
 
-  for (uint32_t c0 = 0; c0 < count; c0 += kCols) {
-    if (c0 > 0) {
-      scan_pairs(a.ids, a.pairs, e, c0, kCols, lane, first, list);
-      load_weights(q0, true, W0);
-      load_weights(q0 + 1, 1 < qpk, W1);
-    }
-    // The row of `cols` behind this lane's column of each tile, as a byte offset.
-    uint32_t coff[NT];
-    bool chave[NT];
-    int pair[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if constexpr (DIR == kUp) {
-        pair[t] = __shfl(list, 16 * t + m);
-        coff[t] = (uint32_t)max(pair[t], 0) / a.top_k * a.k * 2u;
-      } else {
-        const int plane = NT == 1 ? m / kMoePacked : t % 3;
-        pair[t] = __shfl(list, NT == 1 ? m % kMoePacked : 16 * (t / 3) + m);
-        if (plane > 2) pair[t] = -1;
-        coff[t] = ((uint32_t)plane * a.pairs + (uint32_t)max(pair[t], 0)) * a.k * 2u;
-      }
-      chave[t] = pair[t] >= 0;
-    }
-    auto load_cols = [&](uint32_t q, bool in, uint4 (&x)[NT][8]) __attribute__((always_inline)) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-#pragma unroll
-        for (int c = 0; c < QC; ++c) {
-#pragma unroll
-          for (int s = 0; s < STEPS; ++s) {
-            const uint32_t kpos = q * 256u + c * KC + klane + s * kstep;
-            x[t][c * STEPS + s] = buffer_load16(rx, offset_or_oob(in && chave[t] && kpos < a.k, coff[t] + kpos * 2u));
-          }
-        }
-      }
-    };
+  MoeQuad W0, W1;
+  Sc held_scales, next_scales;
+  uint32_t count = 1;
+  for (uint32_t c0 = 0; c0 < count; c0 += cols) {
+    uint32_t first;
+    int list;
+    count = scan_pairs(a.ids, a.pairs, id0, e, c0, cols, lane, first, list);
+    // without pairs, or another slot has this expert: every wave sees the same count
+    if (count == 0 || (by_pair && first != blockIdx.y)) return;
+    const uint32_t have = min(cols, count - c0);
+    lt = st = blockIdx.x * RT + rt;
+    lj = sj = 0;
+    rw = tile_rsrc(a.packed, lt, pitch);
 
-    float4_t acc[2][NT];
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int t = 0; t < NT; ++t) acc[r][t] = float4_t{0.f, 0.f, 0.f, 0.f};
-
-    auto compute = [&](uint32_t q, const MoeQuad<FMT>& d, const uint4 (&x)[NT][8]) __attribute__((always_inline)) {
-      const uint32_t qb = q * QC;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        uint32_t wh[2][4], wb[QC][STEPS];
+    // Copies the window that starts at quad j0 of each K group (`per` quads of each, one group after the
+    // other) of the chunk's rows: a unit is 64 pieces (two quads) of a row, each wave takes every eighth
+    // unit and keeps four in flight.  At the start of a chunk the first weights are requested behind
+    // the first of these loads.
+    auto load_window = [&](uint32_t j0, bool start) __attribute__((always_inline)) {
+      // (opaque copies: the divisions below are recomputed by each call, not held across the loop)
+      uint32_t nseg = (a.qpw + 1u) / 2u, top_k = a.top_k, pl = cols, rows = have;
+      asm volatile("" : "+s"(nseg), "+s"(top_k), "+s"(rows), "+s"(pl));
+      const uint32_t total = (DIR == kUp ? rows : 3u * rows) * nseg;
+      uint32_t u0 = (uint32_t)wave;
+      do {
+        uint4 v[4];
+        uint32_t at[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t send = m < 8 ? d.w[r][1][i] : d.w[r][0][i];
-          wh[0][i] = m < 8 ? d.w[r][0][i] : d.w[r][1][i];
-          wh[1][i] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)send, 0x128, 0xF, 0xF, false);  // row_ror:8
+          at[i] = 0xFFFFFFFFu;
+          const uint32_t u = u0 + 8u * i;
+          if (u < total) {
+            const uint32_t row = u / nseg, seg = u - row * nseg;
+            const uint32_t plane = DIR == kUp ? 0u : row / rows, j = DIR == kUp ? row : row - plane * rows;
+            const uint32_t p = (uint32_t)__builtin_amdgcn_readlane(list, (int)j);
+            const uint32_t base = (DIR == kUp ? p / top_k : plane * a.pairs + p) * a.k * 2u;
+            const uint32_t r = plane * pl + j;                             // window row
+            const uint32_t sl = seg * 64u + (uint32_t)lane, ql = sl >> 5;  // slot and quad in the row
+            // (all of K in the window, per == qpk: quads in order; else quads past the group's last
+            // belong to the next one, and are left out)
+            const uint32_t gr = per == qpk ? 0u : ql / per;
+            const uint32_t jq = per == qpk ? 0u : j0 + ql - gr * per;
+            const uint32_t quad = per == qpk ? ql : gr * qpk + jq;
+            const uint32_t kpos = quad * 256u + (((sl & 31u) ^ (r & 15u)) * 8u);
+            v[i] = buffer_load16(rx, offset_or_oob(kpos < a.k && jq < qpk, base + kpos * 2u));
+            if (ql < a.qpw) at[i] = r * rpitch + sl * 16u;
+          }
         }
-        if constexpr (is_g128(FMT)) {
+        // (the stores stand in both branches: behind a join they would wait for the weights too)
+        if (start) {
+          load_scales(next_scales);
+          load_quad(W0);
+          load_quad(W1);
+          start = false;
 #pragma unroll
-          for (int c = 0; c < QC; ++c)
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) wb[c][s] = wh[c][s];
+          for (int i = 0; i < 4; ++i)
+            if (at[i] != 0xFFFFFFFFu) *reinterpret_cast<uint4*>(win + at[i]) = arranged<FMT>(v[i]);
         } else {
-          // 64-weight blocks: chunks 2 c, 2 c + 1 of the half quad to every lane group, two dwords
-          // each; MXFP4: one more swap gives step s the dwords of the 32-weight block s.
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const auto s0 = __builtin_amdgcn_permlane32_swap(wh[h][0], wh[h][2], false, false);
-            const auto s1 = __builtin_amdgcn_permlane32_swap(wh[h][1], wh[h][3], false, false);
-            wb[2 * h][0] = s0[0];
-            wb[2 * h][1] = s1[0];
-            wb[2 * h + 1][0] = s0[1];
-            wb[2 * h + 1][1] = s1[1];
-          }
-          if constexpr (kMX) {
-#pragma unroll
-            for (int c = 0; c < QC; ++c) {
-              const auto t = __builtin_amdgcn_permlane16_swap(wb[c][0], wb[c][1], false, false);
-              wb[c][0] = t[0];
-              wb[c][1] = t[1];
-            }
-          }
+          for (int i = 0; i < 4; ++i)
+            if (at[i] != 0xFFFFFFFFu) *reinterpret_cast<uint4*>(win + at[i]) = arranged<FMT>(v[i]);
         }
-#pragma unroll
-        for (int c = 0; c < QC; ++c) {
-          float4_t dd[NT];
-#pragma unroll
-          for (int t = 0; t < NT; ++t) dd[t] = float4_t{0.f, 0.f, 0.f, 0.f};
-          uint4 zrow = make_uint4(0u, 0u, 0u, 0u);
-          if constexpr (FMT == kINT4A) {
-            const uint32_t word = (uint32_t)__shfl((int)d.s[r][c], zsrc);
-            const float zn = (float)(8 - (int)((word >> 16) & 15u));
-            const uint32_t h = XT == kF16 ? f16_bits(zn) : (__float_as_uint(zn) >> 16);
-            zrow = make_uint4(h | (h << 16), h | (h << 16), h | (h << 16), h | (h << 16));
-          }
-#pragma unroll
-          for (int s = 0; s < STEPS; ++s) {
-            uint4 a1, a2;
-            if constexpr (!kTable) {
-              a1 = e2m1_pairs<XT>(wb[c][s]);
-            } else {
-              uint32_t p1[4], p2[4];
-#pragma unroll
-              for (int kb = 0; kb < 4; ++kb) {
-                const uint32_t addr =
-                    __builtin_amdgcn_perm(wb[c][s], laneoff, 0x0C0C0000u | ((4u + (uint32_t)kb) << 8)) >> 1;
-                if (kSplit) {
-                  const uint2 tv = *reinterpret_cast<const uint2*>(tabc + addr);
-                  p1[kb] = tv.x;
-                  p2[kb] = tv.y;
-                } else {
-                  p1[kb] = *reinterpret_cast<const uint32_t*>(tabc + addr);
-                }
-              }
-              a1 = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-              if (kSplit) a2 = make_uint4(p2[0], p2[1], p2[2], p2[3]);
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const uint4 bv = x[t][c * STEPS + s];
-              dd[t] = mfma<XT>(a1, bv, dd[t]);
-              if constexpr (kSplit) dd[t] = mfma<XT>(a2, bv, dd[t]);
-              if constexpr (FMT == kINT4A) dd[t] = mfma<XT>(zrow, bv, dd[t]);
-            }
-            if constexpr (kMX) {
-              const uint32_t sraw = __float_as_uint(e8m0_value((d.s[r][c] >> (8 * s)) & 0xFFu));
-              const float sc[4] = {row_bcast<0>(sraw), row_bcast<1>(sraw), row_bcast<2>(sraw),
-                                   row_bcast<3>(sraw)};
-#pragma unroll
-              for (int t = 0; t < NT; ++t) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[r][t][i] = __builtin_fmaf(dd[t][i], sc[i], acc[r][t][i]);
-                dd[t] = float4_t{0.f, 0.f, 0.f, 0.f};
-              }
-            }
-          }
-          if constexpr (!kMX) {
-            const uint32_t sraw = is_g128(FMT) ? d.s[r][c] << 16 : c > 0 && qb + c >= nblocks ? 0u : d.s[r][c];
-            const float sc[4] = {row_bcast<0>(sraw), row_bcast<1>(sraw), row_bcast<2>(sraw),
-                                 row_bcast<3>(sraw)};
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[r][t][i] = __builtin_fmaf(dd[t][i], sc[i], acc[r][t][i]);
-          }
-        }
-      }
+        u0 += 32u;
+      } while (u0 < total);
     };
 
-    // Activations two quads ahead like the weights for one column tile; more tiles leave registers
-    // for one set.
-    uint4 X0[NT][8], X1[NT][8];
-    load_cols(q0, true, X0);
-    if constexpr (NT == 1) load_cols(q0 + 1, 1 < qpk, X1);
-    for (uint32_t q = 0; q < qpk; q += 2) {
-      compute(q0 + q, W0, X0);
-      load_weights(q0 + q + 2, q + 2 < qpk, W0);
-      if constexpr (NT == 1) {
-        load_cols(q0 + q + 2, q + 2 < qpk, X0);
-      } else {
-        load_cols(q0 + q + 1, q + 1 < qpk, X0);
+    float4_t acc[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+
+    // Multiply the quad held in d: quad j of this K group, at window quad wq (of this K group).
+    auto compute = [&](uint32_t j, uint32_t wq, const MoeQuad& d) __attribute__((always_inline)) {
+      // The quad's scales of row m: from lane 4 m + (pair of quads), the quad's half of its dwords.  Those
+      // of blocks past K are the next row's: zeros instead.
+      const uint32_t jw = j % Sc::kQuads, qb = (kg * qpk + j) * QC;
+      const int from = (4 * m + (int)(jw >> 1)) * 4;
+      uint32_t sw[Sc::kPer];
+#pragma unroll
+      for (int i = 0; i < Sc::kPer; ++i)
+        sw[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)(jw & 1u ? held_scales.v[Sc::kPer + i] : held_scales.v[i]));
+      if (qb + QC > nblocks) {
+        const uint32_t left = qb < nblocks ? (nblocks - qb) * SB : 0u;  // bytes of scales inside K
+#pragma unroll
+        for (int i = 0; i < Sc::kPer; ++i)
+          sw[i] = 4u * i + 4u <= left ? sw[i] : 4u * i < left ? sw[i] & 0xFFFFu : 0u;
       }
-      if (q + 1 < qpk) {
-        if constexpr (NT == 1) {
-          compute(q0 + q + 1, W1, X1);
-          load_weights(q0 + q + 3, q + 3 < qpk, W1);
-          load_cols(q0 + q + 3, q + 3 < qpk, X1);
-        } else {
-          compute(q0 + q + 1, W1, X0);
-          load_weights(q0 + q + 3, q + 3 < qpk, W1);
-          load_cols(q0 + q + 2, q + 2 < qpk, X0);
+      // (Opaque copies: offsets derived from these are recomputed per quad, an operation each, instead of
+      // being held across the loop in registers that the loads in flight need.)
+      uint32_t ap[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        ap[t] = apiece[t];
+        asm volatile("" : "+v"(ap[t]));
+      }
+      const uint8_t* wbase = win + wq * 512u;
+      // chunks g and g + 4 of row m: lanes m < 8 hold (row m, g) in load 0 and need (row m, g + 4) of
+      // lane m + 8; lanes m >= 8 hold (row m, g + 4) in load 1 and need (row m, g) of lane m - 8
+      uint32_t wh[2][4], wb[QC][STEPS];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        wh[0][i] = (uint32_t)__builtin_amdgcn_update_dpp((int)d.w[0][i], (int)d.w[1][i], 0x118, 0xF, 0xC, false);
+        wh[1][i] = (uint32_t)__builtin_amdgcn_update_dpp((int)d.w[1][i], (int)d.w[0][i], 0x108, 0xF, 0x3, false);
+      }
+      if constexpr (is_g128(FMT)) {
+#pragma unroll
+        for (int c = 0; c < (int)QC; ++c)
+#pragma unroll
+          for (int s = 0; s < STEPS; ++s) wb[c][s] = wh[c][s];
+      } else {
+        // 64-weight blocks: chunks 2 c, 2 c + 1 of the half quad to every lane group, two dwords
+        // each; MXFP4: one more swap gives step s the dwords of the 32-weight block s.
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const auto s0 = __builtin_amdgcn_permlane32_swap(wh[h][0], wh[h][2], false, false);
+          const auto s1 = __builtin_amdgcn_permlane32_swap(wh[h][1], wh[h][3], false, false);
+          wb[2 * h][0] = s0[0];
+          wb[2 * h][1] = s1[0];
+          wb[2 * h + 1][0] = s0[1];
+          wb[2 * h + 1][1] = s1[1];
+        }
+        if constexpr (kMX) {
+#pragma unroll
+          for (int c = 0; c < (int)QC; ++c) {
+            const auto t = __builtin_amdgcn_permlane16_swap(wb[c][0], wb[c][1], false, false);
+            wb[c][0] = t[0];
+            wb[c][1] = t[1];
+          }
         }
       }
-    }
-
-    if constexpr (KW > 1) {
-      if (c0 > 0) __syncthreads();  // the previous chunk's sums have been read
-      if (kg > 0) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+      for (int c = 0; c < (int)QC; ++c) {
+        float4_t dd[NT];
 #pragma unroll
-          for (int t = 0; t < NT; ++t) red[((((kg - 1) * RW + rg) * 2 + r) * NT + t) * 64 + lane] = acc[r][t];
-      }
-      __syncthreads();
-      if (kg > 0) continue;
-      for (int j = 1; j < KW; ++j) {
+        for (int t = 0; t < NT; ++t) dd[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+        // Integer codes decode as q + 16; a column of -(16 + z) takes the offset off (z = 8: INT4).
+        uint4 zcol = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (is_g128(FMT)) {
+          const float zn = FMT == kINT4 ? -24.0f : -16.0f - (float)((sw[c % Sc::kPer] >> 16) & 15u);
+          const uint32_t h = XT == kF16 ? f16_bits(zn) : (__float_as_uint(zn) >> 16);
+          zcol = make_uint4(h | (h << 16), h | (h << 16), h | (h << 16), h | (h << 16));
+        }
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int s = 0; s < STEPS; ++s) {
+          constexpr uint32_t kPieces = KC / 8;  // of a block
+          const uint32_t at = (c * kPieces + s * (kMX ? 4u : 1u)) * 16u;
+          uint4 xv[NT];
+#pragma unroll
+          for (int t = 0; t < NT; ++t) xv[t] = *reinterpret_cast<const uint4*>(wbase + arow[t] + (ap[t] ^ at));
+          uint4 b1, b2;
+          if constexpr (kTable) {
+            uint2 tv[4];
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) {
+              // LDS byte address = byte * 128 + lane offset: byte * 256 + 2 * lane offset, halved
+              const uint32_t addr =
+                  __builtin_amdgcn_perm(wb[c][s], laneoff, 0x0C0C0000u | ((4u + (uint32_t)kb) << 8)) >> 1;
+              tv[kb] = *reinterpret_cast<const uint2*>(tabc + addr);
+            }
+            b1 = make_uint4(tv[0].x, tv[1].x, tv[2].x, tv[3].x);
+            b2 = make_uint4(tv[0].y, tv[1].y, tv[2].y, tv[3].y);
+          } else {
+            b1 = decode8<FMT, XT>(wb[c][s]);
+          }
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            const float4_t v = red[((((j - 1) * RW + rg) * 2 + r) * NT + t) * 64 + lane];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[r][t][i] += v[i];
+            dd[t] = mfma<XT>(xv[t], b1, dd[t]);
+            if constexpr (kTable) dd[t] = mfma<XT>(xv[t], b2, dd[t]);
+            if constexpr (is_g128(FMT)) dd[t] = mfma<XT>(xv[t], zcol, dd[t]);
           }
+          if constexpr (kMX) {
+            // 2^(e - 127); e = 255 gives an infinity here, which `finish` tells apart
+            const float sc = ldexpf(__uint_as_float(0x00400000u), (int)((sw[c >> 1] >> (16 * (c & 1) + 8 * s)) & 0xFFu));
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(dd[t][i], sc, acc[t][i]);
+              dd[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+            }
+          }
+        }
+        if constexpr (!kMX) {
+          const float sc = __uint_as_float(FMT == kINT4    ? (c == 0 ? sw[0] << 16 : sw[0] & 0xFFFF0000u)
+                                           : FMT == kINT4A ? sw[c % Sc::kPer] << 16 : sw[c % Sc::kPer]);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(dd[t][i], sc, acc[t][i]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-    }
-    if constexpr (kSplit) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[r][t][i] *= 1.0f / kNf4Factor;
-    }
-    if (!live) continue;
+    };
 
-    if constexpr (DIR == kUp) {
-      const uint32_t inter = a.n >> 1;
+    // A tile's value for (row n, A row 4 g + i of column tile t): its K groups' sums, in group order.
+    // Waves hold theirs as [t][i][16 g + n].  An MXFP4 scale byte of 255 is NaN: it made its row's
+    // sums infinite or NaN, so a row is looked through for it only then.
+    auto tile_value = [&](const float* buf, uint32_t tile, uint32_t n, uint32_t t, uint32_t r)
+                          __attribute__((always_inline)) {
+      float v = 0.0f;
+      const uint32_t at = (t * 4u + (r & 3u)) * 64u + (r >> 2) * 16u + n;
+#pragma unroll
+      for (uint32_t w = 0; w < (uint32_t)KW; ++w) v += buf[(w * RT + tile % RT) * (NT * 256u) + at];
+      return kTable ? v * (1.0f / kNf4Factor) : v;
+    };
+    auto with_nan = [&](float v, uint32_t row) __attribute__((always_inline)) {
+      if constexpr (kMX) {
+        if (!__builtin_isfinite(v)) {
+          const uint8_t* sp = reinterpret_cast<const uint8_t*>(a.scales) + ((size_t)e * a.n + row) * spitch;
+          for (uint32_t i = 0; i < spitch; ++i)
+            if (sp[i] == 255u) v = __uint_as_float(0x7FC00000u);
+        }
+      }
+      return v;
+    };
+
+    uint32_t held = 0xFFFFFFFFu;  // first quad (of each K group) of the window in LDS
+    uint32_t buffer = 0;
+    for (uint32_t ug = blockIdx.x; ug < ngroups; ug += gridDim.x) {
+      for (uint32_t j = 0; j < qpk; j += 2) {
+        const uint32_t w0 = per == qpk ? 0u : j / per * per;
+        if (w0 != held) {
+          __syncthreads();  // every wave is done with the old window (or has written its table entries)
+          load_window(w0, held == 0xFFFFFFFFu);
+          held = w0;
+          __syncthreads();
+        }
+        if (j % Sc::kQuads == 0) {  // the next scale window: shifted into place, the one after it requested
+#pragma unroll
+          for (int i = 0; i < 2 * Sc::kPer; ++i) {
+            if constexpr (Sc::kShift) {
+              held_scales.v[i] = __builtin_amdgcn_alignbit(next_scales.v[i + 1], next_scales.v[i], sshift);
+            } else {
+              held_scales.v[i] = next_scales.v[i];
+            }
+          }
+          load_scales(next_scales);
+        }
+        compute(j, j - w0, W0);
+        load_quad(W0);
+        if (j + 1 < qpk) compute(j + 1, j + 1 - w0, W1);
+        load_quad(W1);
+      }
+
+      // The group's sums into this buffer; the other one is read until the next group's barrier.
+      float* buf = sums + buffer * (8u * NT * 256u);
+      buffer ^= 1u;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        uint32_t p[3][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float gate = acc[0][t][i];
-          const float v = gate / (1.0f + expf(-gate)) * acc[1][t][i];
+        for (int i = 0; i < 4; ++i) buf[((uint32_t)wave * NT + t) * 256u + i * 64u + lane] = acc[t][i];
+        acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+      }
+      __syncthreads();
+      const uint32_t tile0 = ug * RT, tiles = min(RT, a.tiles - tile0);
+      if constexpr (DIR == kUp) {
+        const uint32_t inter = a.n >> 1, row0 = tile0 * 8u, rows = tiles * 8u;  // rows of h in this group
+        for (uint32_t i = (uint32_t)tid; i < rows * have; i += kMoeThreads) {
+          const uint32_t j = i / rows, row = i - j * rows, tile = row / 16u * 2u, n = row & 15u;
+          const int pair = __shfl(list, (int)j);  // (rows * have is a multiple of 16: lanes 0 .. 15 take part)
+          const float gate = with_nan(tile_value(buf, tile, n, j / 16u, j & 15u), row0 + row);
+          const float up = with_nan(tile_value(buf, tile + 1u, n, j / 16u, j & 15u), inter + row0 + row);
+          const float v = gate / (1.0f + expf(-gate)) * up;
           const uint32_t b1 = __float_as_uint(v) & 0xFFFF0000u;
           const float r1 = __builtin_isinf(v) ? 0.0f : v - __uint_as_float(b1);
           const uint32_t b2 = __float_as_uint(r1) & 0xFFFF0000u;
-          p[0][i] = b1;
-          p[1][i] = b2;
-          // (r1 may be the remainder of the unrounded product, a contracted multiply-subtract: cut)
-          p[2][i] = __float_as_uint(r1 - __uint_as_float(b2)) & 0xFFFF0000u;
+          const float r2 = r1 - __uint_as_float(b2);  // cut: a contracted r1 may be longer
+          const size_t at = (size_t)(uint32_t)pair * inter + row0 + row, plane = (size_t)a.pairs * inter;
+          a.h[at] = (uint16_t)(b1 >> 16);
+          a.h[at + plane] = (uint16_t)(b2 >> 16);
+          a.h[at + 2 * plane] = (uint16_t)(__float_as_uint(r2) >> 16);
         }
-        if (chave[t]) {
-#pragma unroll
-          for (int pl = 0; pl < 3; ++pl) {
-            const size_t at = ((size_t)pl * a.pairs + (uint32_t)pair[t]) * inter + row0 + 4u * g;
-            *reinterpret_cast<uint2*>(a.h + at) =
-                make_uint2(p[pl][0] >> 16 | p[pl][1], p[pl][2] >> 16 | p[pl][3]);
+      } else {
+        const uint32_t row0 = tile0 * 16u, rows = tiles * 16u;
+        for (uint32_t i = (uint32_t)tid; i < rows * have; i += kMoeThreads) {
+          const uint32_t j = i / rows, row = i - j * rows, tile = row / 16u, n = row & 15u;
+          const int pair = __shfl(list, (int)j);  // (rows * have is a multiple of 16: lanes 0 .. 15 take part)
+          float v;
+          if constexpr (NT == 1) {  // planes in rows 4 p + j
+            v = tile_value(buf, tile, n, 0, j) + (tile_value(buf, tile, n, 0, 4u + j) + tile_value(buf, tile, n, 0, 8u + j));
+          } else {
+            v = tile_value(buf, tile, n, 0, j) + (tile_value(buf, tile, n, 1, j) + tile_value(buf, tile, n, 2, j));
           }
-        }
-      }
-    } else {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        if constexpr (NT == 1) {
-          float4_t v;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float v2 = __shfl(acc[r][0][i], lane + kMoePacked), v3 = __shfl(acc[r][0][i], lane + 2 * kMoePacked);
-            v[i] = acc[r][0][i] + (v2 + v3);
-          }
-          if (m < kMoePacked && chave[0])
-            *reinterpret_cast<float4_t*>(a.part + (size_t)pair[0] * a.n + (r ? row1 : row0) + 4u * g) = v;
-        } else {
-#pragma unroll
-          for (int t = 0; t < NT; t += 3) {
-            float4_t v;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = acc[r][t][i] + (acc[r][t + 1][i] + acc[r][t + 2][i]);
-            if (chave[t])
-              *reinterpret_cast<float4_t*>(a.part + (size_t)pair[t] * a.n + (r ? row1 : row0) + 4u * g) = v;
-          }
+          a.part[(size_t)(uint32_t)pair * a.n + row0 + row] = with_nan(v, row0 + row);
         }
       }
     }
+    if (c0 + cols < count) __syncthreads();  // the window and the sums have been read
   }
+}
+
+template <int DIR, int FMT, int XT, int NT, int KW>
+hipError_t launch_moe_one(const MoeArgs& a, uint32_t slots, hipStream_t s) {
+  constexpr uint32_t RT = 8 / KW, kSums = 2 * 8 * NT * 1024;
+  // the limit on dynamic LDS, raised once per instantiation and process
+  static const hipError_t raised = hipFuncSetAttribute(
+      reinterpret_cast<const void*>(&moe_kernel<DIR, FMT, XT, NT, KW>),
+      hipFuncAttributeMaxDynamicSharedMemorySize, kMoeMaxWindow + kSums);
+  if (raised != hipSuccess) return raised;
+  if (a.win_bytes > kMoeMaxWindow) return hipErrorInvalidValue;
+  const uint32_t ngroups = (a.tiles + RT - 1) / RT;
+  hipLaunchKernelGGL((moe_kernel<DIR, FMT, XT, NT, KW>), dim3(a.grid < ngroups ? a.grid : ngroups, slots),
+                     dim3(kMoeThreads), a.win_bytes + kSums, s, a);
+  return hipGetLastError();
 }
 
 template <int DIR, int FMT, int XT, int NT>
 hipError_t launch_moe_kw(int kw, const MoeArgs& a, uint32_t slots, hipStream_t s) {
-  const uint32_t rw = 8u / (uint32_t)kw;
-  const dim3 grid((a.units + rw - 1) / rw, slots, 1);
   switch (kw) {
-    case 1: hipLaunchKernelGGL((moe_kernel<DIR, FMT, XT, NT, 1>), grid, dim3(kMoeThreads), 0, s, a); break;
-    case 2: hipLaunchKernelGGL((moe_kernel<DIR, FMT, XT, NT, 2>), grid, dim3(kMoeThreads), 0, s, a); break;
-    case 4: hipLaunchKernelGGL((moe_kernel<DIR, FMT, XT, NT, 4>), grid, dim3(kMoeThreads), 0, s, a); break;
-    case 8: hipLaunchKernelGGL((moe_kernel<DIR, FMT, XT, NT, 8>), grid, dim3(kMoeThreads), 0, s, a); break;
-    default: return hipErrorInvalidValue;
+    case 1: return launch_moe_one<DIR, FMT, XT, NT, 1>(a, slots, s);
+    case 2: return launch_moe_one<DIR, FMT, XT, NT, 2>(a, slots, s);
+    case 4: return launch_moe_one<DIR, FMT, XT, NT, 4>(a, slots, s);
   }
-  return hipGetLastError();
+  return hipErrorInvalidValue;
 }
 
 template <int DIR, int XT, int NT>

@@ -547,9 +547,9 @@ int w4_moe_route(const void* logits, int logits_type, int64_t tokens, int64_t ex
  *   weights  device float[tokens, top_k]
  *   gate_up  device uint8[experts, 2 * inter, hidden / 2]: an expert's gate rows, then its up
  *            rows, each row packed as for w4_gemv; 16-byte aligned
- *   gate_up_scales  the format's scales of gate_up, [experts, 2 * inter, ...]
+ *   gate_up_scales  the format's scales of gate_up, [experts, 2 * inter, ...]; 4-byte aligned
  *   down     device uint8[experts, hidden, inter / 2]; 16-byte aligned
- *   down_scales     the format's scales of down, [experts, hidden, ...]
+ *   down_scales     the format's scales of down, [experts, hidden, ...]; 4-byte aligned
  *   fmt      any w4_format_t
  *   tokens   1 <= tokens <= W4_MAX_BATCH, tokens * hidden * 2 < 2^31 - 256
  *   hidden, inter   multiples of 64 (NF4, FP4, MXFP4) or 128 (INT4, INT4A), below 2^22

@@ -4,8 +4,8 @@ The bound is the sum of the layer's roundings, each taken at its largest.  With 
 
 * a sum over K of one matrix: |d| <= eps(K) T, eps(K) = (K/32 + 64) u and T the sum of the
   magnitudes of its terms (32 additions inside a block, K/32 block additions, 32 for the sums over
-  waves and column planes); asymmetric INT4 adds (q - 8) x and (8 - z) x apart, so its terms
-  are |x| s (|q - 8| + |z - 8|).  Products are exact in fp32 except the scale's (2 u, inside the
+  waves and column planes); the integer formats add (16 + q) x and -(16 + z) x (z = 8 for INT4)
+  apart, so their terms are |x| s (32 + q + z).  Products are exact in fp32 except the scale's (2 u, inside the
   64), NF4's codes are two 16-bit terms, off by at most 2^-18 |code|;
 * silu has |silu'| <= 1.1; exp, the division and two products are off by at most 2^-20 |h|;
 * h is kept whole; the sum over slots adds (top_k + 2) u of its magnitudes;
@@ -27,10 +27,10 @@ def quantize_experts(weight, w):
     p, s = q(w.reshape(e * n, k))
     hat = oracle.dequant(weight, p, s).reshape(e, n, k)
     mag = np.abs(hat)
-    if weight == "int4a":
+    if weight in ("int4", "int4a"):
         sc = np.repeat(oracle.bf16_bits_to_f64((s & 0xFFFF).astype(np.uint16)), 128, axis=1).reshape(e, n, k)
-        z = np.repeat((s >> 16) & 15, 128, axis=1).astype(np.float64).reshape(e, n, k)
-        mag = np.abs(hat + (z - 8) * sc) + np.abs(z - 8) * sc
+        z = np.repeat((s >> 16) & 15, 128, axis=1).astype(np.float64).reshape(e, n, k) if weight == "int4a" else 8.0
+        mag = hat + (32 + 2 * z) * sc  # s (16 + q) + s (16 + z), hat = s (q - z)
     return p.reshape(e, n, k // 2), s.reshape(e, n, -1), hat, mag
 
 
