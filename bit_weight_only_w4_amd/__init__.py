@@ -134,14 +134,16 @@ def _fmt(fmt) -> int:
 
 
 def _stream(stream=None) -> int:
-    import torch
+    if stream is None:
+        import torch
 
-    s = torch.cuda.current_stream() if stream is None else stream
-    return int(s.cuda_stream)
+        # the current stream's handle without building a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return int(stream.cuda_stream)
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need_cuda(*ts):
@@ -530,16 +532,22 @@ _MOE_SCALES = {"nf4": ("float32", 64), "fp4": ("float32", 64), "int4": ("int16",
                "int4a": ("int32", 128), "mxfp4": ("uint8", 32)}
 
 
-def _on_device_of(t, stream):
-    """A context in which allocations and launches go to `stream` (or the current stream) of t's
-    device."""
+def _expect(name, t, shape, dtype, index):
+    """Refuse a tensor that is not contiguous, of this shape and type, on GPU `index`."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on the first tensor's GPU")
+
+
+def _on_device(index, stream):
+    """None where the call can go ahead on the current device and stream, else a context to make it in:
+    allocations and launches go to `stream`, or to the current stream of the tensors' device."""
     import torch
 
-    if stream is None:
-        return torch.cuda.device(t.device)
-    if stream.device != t.device:
-        raise ValueError("stream and tensors must be on one device")
-    return torch.cuda.stream(stream)
+    if stream is not None:
+        if stream.device.index != index:
+            raise ValueError("stream and tensors must be on one device")
+        return torch.cuda.stream(stream)
+    return None if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
 def moe_route(logits, top_k, renormalize=True, ids=None, weights=None, stream=None):
@@ -549,24 +557,30 @@ def moe_route(logits, top_k, renormalize=True, ids=None, weights=None, stream=No
     and -inf logits are never chosen: slots left over get id -1 and weight 0."""
     import torch
 
-    kind = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(logits.dtype)
-    if kind is None or logits.dim() != 2:
-        raise ValueError("logits must be a 2-D float32, float16 or bfloat16 tensor")
-    _need_cuda(logits, ids, weights)
+    kind = 0 if logits.dtype is torch.float32 else 1 if logits.dtype is torch.float16 else \
+        2 if logits.dtype is torch.bfloat16 else None
+    index = logits.get_device()
+    if kind is None or logits.dim() != 2 or index < 0 or not logits.is_contiguous():
+        raise ValueError("logits must be a contiguous 2-D float32, float16 or bfloat16 tensor on the GPU")
     t, e = logits.shape
-    top_k = int(top_k)
-    with _on_device_of(logits, stream):
-        if ids is None:
-            ids = torch.empty((t, max(top_k, 0)), dtype=torch.int32, device=logits.device)
-        if weights is None:
-            weights = torch.empty((t, max(top_k, 0)), dtype=torch.float32, device=logits.device)
-        if tuple(ids.shape) != (t, top_k) or ids.dtype != torch.int32 or ids.device != logits.device:
-            raise ValueError("ids must be int32 [T, top_k] on the logits' device")
-        if tuple(weights.shape) != (t, top_k) or weights.dtype != torch.float32 or \
-                weights.device != logits.device:
-            raise ValueError("weights must be float32 [T, top_k] on the logits' device")
-        check(lib().w4_moe_route(_ptr(logits), kind, t, e, top_k, int(bool(renormalize)), _ptr(ids),
-                                 _ptr(weights), _stream(stream)), "w4_moe_route")
+    if top_k < 1:
+        raise ValueError("top_k must be at least 1")
+    context = _on_device(index, stream)
+    if context is not None:
+        with context:
+            return moe_route(logits, top_k, renormalize, ids, weights)
+    if ids is None:
+        ids = torch.empty((t, top_k), dtype=torch.int32, device=logits.device)
+    else:
+        _expect("ids", ids, (t, top_k), torch.int32, index)
+    if weights is None:
+        weights = torch.empty((t, top_k), dtype=torch.float32, device=logits.device)
+    else:
+        _expect("weights", weights, (t, top_k), torch.float32, index)
+    status = lib().w4_moe_route(logits.data_ptr(), kind, t, e, top_k, 1 if renormalize else 0, ids.data_ptr(),
+                                weights.data_ptr(), torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        check(status, "w4_moe_route")
     return ids, weights
 
 
@@ -585,12 +599,14 @@ def moe(x, ids, weights, gate_up, gate_up_scales, down, down_scales, fmt, y=None
     `workspace` is a uint8 tensor of moe_workspace_bytes(...), allocated by the call if not given."""
     import torch
 
-    if fmt not in FORMATS:
+    code = FORMATS.get(fmt)
+    if code is None:
         raise ValueError(f"unknown format {fmt!r}; expected one of {sorted(FORMATS)}")
     weight, xtype = fmt.split("_")
-    _need_cuda(x, ids, weights, gate_up, gate_up_scales, down, down_scales, y, workspace)
-    if x.dim() != 2 or x.dtype != (torch.float16 if xtype == "f16" else torch.bfloat16):
-        raise ValueError(f"x must be a 2-D tensor of the activation type of {fmt!r}")
+    index = x.get_device()
+    if x.dim() != 2 or index < 0 or not x.is_contiguous() or \
+            x.dtype is not (torch.float16 if xtype == "f16" else torch.bfloat16):
+        raise ValueError(f"x must be a contiguous 2-D GPU tensor of the activation type of {fmt!r}")
     if ids.dim() != 2 or gate_up.dim() != 3 or down.dim() != 3:
         raise ValueError("ids must be [T, top_k], gate_up [E, 2 I, H/2] and down [E, H, I/2]")
     t, h = x.shape
@@ -598,25 +614,31 @@ def moe(x, ids, weights, gate_up, gate_up_scales, down, down_scales, fmt, y=None
     e, i = gate_up.shape[0], down.shape[2] * 2
     dtype, group = _MOE_SCALES[weight]
     dtype = getattr(torch, dtype)
-    for name, v, shape, kind in (
-            ("ids", ids, (t, k), torch.int32), ("weights", weights, (t, k), torch.float32),
-            ("gate_up", gate_up, (e, 2 * i, h // 2), torch.uint8), ("down", down, (e, h, i // 2), torch.uint8),
-            ("gate_up_scales", gate_up_scales, (e, 2 * i, h // group), dtype),
-            ("down_scales", down_scales, (e, h, i // group), dtype)):
-        if v.shape != shape or v.dtype != kind or v.device != x.device:
-            raise ValueError(f"{name} must be {kind} {list(shape)} on x's device")
-    with _on_device_of(x, stream):
-        if y is None:
-            y = torch.empty((t, h), dtype=torch.float32, device=x.device)
-        elif y.shape != (t, h) or y.dtype != torch.float32 or y.device != x.device:
-            raise ValueError("y must be float32 [T, H] on x's device")
-        if workspace is None:
-            workspace = torch.empty(moe_workspace_bytes(fmt, t, h, i, e, k), dtype=torch.uint8,
-                                    device=x.device)
-        elif workspace.device != x.device:
-            raise ValueError("workspace must be on x's device")
-        check(lib().w4_moe(_ptr(x), _ptr(ids), _ptr(weights), _ptr(gate_up), _ptr(gate_up_scales),
-                           _ptr(down), _ptr(down_scales), FORMATS[fmt], t, h, i, e, k, _ptr(y),
-                           _ptr(workspace), workspace.numel() * workspace.element_size(),
-                           _stream(stream)), "w4_moe")
+    _expect("ids", ids, (t, k), torch.int32, index)
+    _expect("weights", weights, (t, k), torch.float32, index)
+    _expect("gate_up", gate_up, (e, 2 * i, h // 2), torch.uint8, index)
+    _expect("gate_up_scales", gate_up_scales, (e, 2 * i, h // group), dtype, index)
+    _expect("down", down, (e, h, i // 2), torch.uint8, index)
+    _expect("down_scales", down_scales, (e, h, i // group), dtype, index)
+    context = _on_device(index, stream)
+    if context is not None:
+        with context:
+            return moe(x, ids, weights, gate_up, gate_up_scales, down, down_scales, fmt, y, workspace)
+    L = lib()
+    if y is None:
+        y = torch.empty((t, h), dtype=torch.float32, device=x.device)
+    else:
+        _expect("y", y, (t, h), torch.float32, index)
+    if workspace is None:
+        size = L.w4_moe_workspace_bytes(code, t, h, i, e, k)
+        workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
+    else:
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on x's GPU")
+        size = workspace.numel() * workspace.element_size()
+    status = L.w4_moe(x.data_ptr(), ids.data_ptr(), weights.data_ptr(), gate_up.data_ptr(),
+                      gate_up_scales.data_ptr(), down.data_ptr(), down_scales.data_ptr(), code, t, h, i, e,
+                      k, y.data_ptr(), workspace.data_ptr(), size, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        check(status, "w4_moe")
     return y
