@@ -13,6 +13,8 @@ struct MoeArgs {
   const int32_t* ids;      // [pairs], pair = token * top_k + slot; outside [0, experts): absent
   uint16_t* h;             // up: planes of h [3, pairs, inter]
   float* part;             // down: [pairs, N]
+  const float* weights;    // down with the combination: [pairs]
+  float* y;                // ... and its result [tokens, N]
   uint32_t n;              // rows of one expert matrix
   uint32_t k;
   uint32_t experts;
@@ -34,6 +36,7 @@ constexpr int kMoePacked = 4;      // pairs of a down chunk whose three planes s
 // pairs a chunk, 3: up to 16, a tile per plane).  grid.y = slots (see moe_kernel).
 hipError_t launch_moe_up_f16(int weight, int kw, const MoeArgs& a, uint32_t slots, hipStream_t s);
 hipError_t launch_moe_up_bf16(int weight, int kw, const MoeArgs& a, uint32_t slots, hipStream_t s);
+hipError_t launch_moe_token(int weight, int kw, const MoeArgs& a, uint32_t tokens, hipStream_t s);
 hipError_t launch_moe_down(int weight, int kw, int tiles, const MoeArgs& a, uint32_t slots,
                            hipStream_t s);
 

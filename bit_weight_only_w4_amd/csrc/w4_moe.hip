@@ -4,6 +4,9 @@
 
 #include "w4_moe.h"
 
+#ifndef MOE_TOKEN_PAIRS
+#define MOE_TOKEN_PAIRS 64
+#endif
 namespace w4 {
 namespace {
 
@@ -227,6 +230,15 @@ hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const floa
   a.n = (uint32_t)hidden;
   a.k = (uint32_t)inter;
   a.tiles = (uint32_t)(hidden / 16);
+  // A few tokens, mostly with experts of their own: the combination inside the down launch.
+  if (tokens == 1 || (pairs <= MOE_TOKEN_PAIRS && 2 * pairs <= experts)) {
+    a.weights = weights;
+    a.y = y;
+    kw = top_k > 4 ? 1 : top_k > 2 ? 2 : 4;
+    while (kw > 1 && kw > (inter + 255) / 256) kw /= 2;
+    a.qpk = (uint32_t)(((inter + 255) / 256 + kw - 1) / kw);
+    return launch_moe_token(weight, kw, a, (uint32_t)tokens, s);
+  }
   const int tiles = pairs <= 2 * experts ? 1 : 3;
   cols = (uint32_t)std::min<int64_t>(tiles == 1 ? kMoePacked : 16, tokens);
   kw = moe_kw(a.tiles, slots, inter, 3 * cols);

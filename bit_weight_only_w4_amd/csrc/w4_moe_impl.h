@@ -176,12 +176,191 @@ struct MoeScales {
   uint32_t v[kRaw];
 };
 
+// acc += the product of the quad held in d (B) and 256 k of the window (A).  The quad is the jw-th of the
+// scales' eight, ODD its parity; `left` is the bytes of its row's scales that lie inside K; its first piece of A row r
+// of column tile t stands at wbase + arow[t].
+template <int FMT, int XT, int NT, int ODD>
+__device__ __attribute__((always_inline)) inline void quad_product(
+    float4_t (&acc)[NT], const MoeQuad& d, const MoeScales<FMT>& scales, uint32_t jw, uint32_t left,
+    const uint8_t* wbase, const uint32_t (&arow)[NT], const uint32_t (&apiece)[NT], const uint32_t* tab, int lane) {
+  using Sc = MoeScales<FMT>;
+  constexpr int KC = is_g128(FMT) ? 128 : 64;  // weights per block
+  constexpr uint32_t QC = 256 / KC;
+  constexpr int STEPS = KC / 32;
+  constexpr bool kMX = FMT == kMXFP4;
+  constexpr bool kTable = FMT == kNF4;
+  constexpr uint32_t SB = FMT == kINT4 || kMX ? 2 : 4;
+  const int m = lane & 15;
+  const uint32_t laneoff = (uint32_t)m * 16u;
+  const char* tabc = reinterpret_cast<const char*>(tab);
+  // The quad's scales of row m: from lane 4 m + (pair of quads), the quad's half of its dwords.  Those of
+  // blocks past K are the next row's: zeros instead.
+  const int from = (4 * m + (int)(jw >> 1)) * 4;
+  uint32_t sw[Sc::kPer];
+#pragma unroll
+  for (int i = 0; i < Sc::kPer; ++i)
+    sw[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)scales.v[ODD * Sc::kPer + i]);
+  if (left < QC * SB) {
+#pragma unroll
+    for (int i = 0; i < Sc::kPer; ++i)
+      sw[i] = 4u * i + 4u <= left ? sw[i] : 4u * i < left ? sw[i] & 0xFFFFu : 0u;
+  }
+  // (Opaque copies: offsets derived from these are recomputed per quad, an operation each, instead of
+  // being held across the loop in registers that the loads in flight need.)
+  uint32_t ap[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    ap[t] = apiece[t];
+    asm volatile("" : "+v"(ap[t]));
+  }
+  // chunks g and g + 4 of row m: lanes m < 8 hold (row m, g) in load 0 and need (row m, g + 4) of
+  // lane m + 8; lanes m >= 8 hold (row m, g + 4) in load 1 and need (row m, g) of lane m - 8
+  uint32_t wh[2][4], wb[QC][STEPS];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    wh[0][i] = (uint32_t)__builtin_amdgcn_update_dpp((int)d.w[0][i], (int)d.w[1][i], 0x118, 0xF, 0xC, false);
+    wh[1][i] = (uint32_t)__builtin_amdgcn_update_dpp((int)d.w[1][i], (int)d.w[0][i], 0x108, 0xF, 0x3, false);
+  }
+  if constexpr (is_g128(FMT)) {
+#pragma unroll
+    for (int c = 0; c < (int)QC; ++c)
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) wb[c][s] = wh[c][s];
+  } else {
+    // 64-weight blocks: chunks 2 c, 2 c + 1 of the half quad to every lane group, two dwords
+    // each; MXFP4: one more swap gives step s the dwords of the 32-weight block s.
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const auto s0 = __builtin_amdgcn_permlane32_swap(wh[h][0], wh[h][2], false, false);
+      const auto s1 = __builtin_amdgcn_permlane32_swap(wh[h][1], wh[h][3], false, false);
+      wb[2 * h][0] = s0[0];
+      wb[2 * h][1] = s1[0];
+      wb[2 * h + 1][0] = s0[1];
+      wb[2 * h + 1][1] = s1[1];
+    }
+    if constexpr (kMX) {
+#pragma unroll
+      for (int c = 0; c < (int)QC; ++c) {
+        const auto t = __builtin_amdgcn_permlane16_swap(wb[c][0], wb[c][1], false, false);
+        wb[c][0] = t[0];
+        wb[c][1] = t[1];
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < (int)QC; ++c) {
+    float4_t dd[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) dd[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+    // Integer codes decode as q + 16; a column of -(16 + z) takes the offset off (z = 8: INT4).
+    uint4 zcol = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (is_g128(FMT)) {
+      const float zn = FMT == kINT4 ? -24.0f : -16.0f - (float)((sw[c % Sc::kPer] >> 16) & 15u);
+      const uint32_t h = XT == kF16 ? f16_bits(zn) : (__float_as_uint(zn) >> 16);
+      zcol = make_uint4(h | (h << 16), h | (h << 16), h | (h << 16), h | (h << 16));
+    }
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      constexpr uint32_t kPieces = KC / 8;  // of a block
+      const uint32_t at = (c * kPieces + s * (kMX ? 4u : 1u)) * 16u;
+      uint4 xv[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) xv[t] = *reinterpret_cast<const uint4*>(wbase + arow[t] + (ap[t] ^ at));
+      uint4 b1, b2;
+      if constexpr (kTable) {
+        uint2 tv[4];
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+          // LDS byte address = byte * 128 + lane offset: byte * 256 + 2 * lane offset, halved
+          const uint32_t addr =
+              __builtin_amdgcn_perm(wb[c][s], laneoff, 0x0C0C0000u | ((4u + (uint32_t)kb) << 8)) >> 1;
+          tv[kb] = *reinterpret_cast<const uint2*>(tabc + addr);
+        }
+        b1 = make_uint4(tv[0].x, tv[1].x, tv[2].x, tv[3].x);
+        b2 = make_uint4(tv[0].y, tv[1].y, tv[2].y, tv[3].y);
+      } else {
+        b1 = decode8<FMT, XT>(wb[c][s]);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        dd[t] = mfma<XT>(xv[t], b1, dd[t]);
+        if constexpr (kTable) dd[t] = mfma<XT>(xv[t], b2, dd[t]);
+        if constexpr (is_g128(FMT)) dd[t] = mfma<XT>(xv[t], zcol, dd[t]);
+      }
+      if constexpr (kMX) {
+        // 2^(e - 127); e = 255 gives an infinity here, which `finish` tells apart
+        const float sc = ldexpf(__uint_as_float(0x00400000u), (int)((sw[c >> 1] >> (16 * (c & 1) + 8 * s)) & 0xFFu));
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(dd[t][i], sc, acc[t][i]);
+          dd[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+        }
+      }
+    }
+    if constexpr (!kMX) {
+      const float sc = __uint_as_float(FMT == kINT4    ? (c == 0 ? sw[0] << 16 : sw[0] & 0xFFFF0000u)
+                                       : FMT == kINT4A ? sw[c % Sc::kPer] << 16 : sw[c % Sc::kPer]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(dd[t][i], sc, acc[t][i]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// The scales of eight quads as loaded (see MoeScales), from byte `off` of the tile's.
+template <int FMT>
+__device__ inline void load_scale_window(MoeScales<FMT>& d, __amdgpu_buffer_rsrc_t rs, uint32_t off) {
+  if constexpr (FMT == kINT4) {
+    const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, (int)off, 0, 0);
+    d.v[0] = v[0];
+    d.v[1] = v[1];
+    d.v[2] = buffer_load32(rs, off + 8u);
+  } else {
+    const uint4 v = buffer_load16(rs, off);
+    d.v[0] = v.x; d.v[1] = v.y; d.v[2] = v.z; d.v[3] = v.w;
+    if constexpr (FMT == kMXFP4) d.v[4] = buffer_load32(rs, off + 16u);
+    if constexpr (MoeScales<FMT>::kPer == 4) {
+      const uint4 u = buffer_load16(rs, off + 16u);
+      d.v[4] = u.x; d.v[5] = u.y; d.v[6] = u.z; d.v[7] = u.w;
+    }
+  }
+}
+
+// ... and moved into place; `sshift`: the bits by which a 2-byte row starts inside its first dword.
+template <int FMT>
+__device__ inline void place_scales(MoeScales<FMT>& held, const MoeScales<FMT>& raw, uint32_t sshift) {
+#pragma unroll
+  for (int i = 0; i < 2 * MoeScales<FMT>::kPer; ++i) {
+    if constexpr (MoeScales<FMT>::kShift) {
+      held.v[i] = __builtin_amdgcn_alignbit(raw.v[i + 1], raw.v[i], sshift);
+    } else {
+      held.v[i] = raw.v[i];
+    }
+  }
+}
+
+// v, or NaN if the MXFP4 row at `scales` (bytes of them) holds a scale byte of 255.  Such a byte makes
+// its row's sums infinite or NaN, so a row is looked through only then.
+template <int FMT>
+__device__ inline float with_nan_scales(float v, const void* scales, size_t bytes) {
+  if constexpr (FMT == kMXFP4) {
+    if (!__builtin_isfinite(v)) {
+      const uint8_t* sp = reinterpret_cast<const uint8_t*>(scales);
+      for (size_t i = 0; i < bytes; ++i)
+        if (sp[i] == 255u) v = __uint_as_float(0x7FC00000u);
+    }
+  }
+  return v;
+}
+
 template <int DIR, int FMT, int XT, int NT, int KW>
 __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 4 : 2) moe_kernel(MoeArgs a) {
   constexpr uint32_t RT = 8 / KW;
   constexpr int KC = is_g128(FMT) ? 128 : 64;  // weights per block
   constexpr uint32_t QC = 256 / KC;
-  constexpr int STEPS = KC / 32;
   constexpr bool kMX = FMT == kMXFP4;
   constexpr bool kTable = FMT == kNF4;
   constexpr uint32_t SB = FMT == kINT4 || kMX ? 2 : 4;
@@ -253,20 +432,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 4 : 2) moe_kernel(MoeAr
     const uint32_t at = (uint32_t)(lane >> 2) * spitch + (q + 2u * (uint32_t)(lane & 3)) * (QC * SB);
     const uint32_t off = offset_or_oob(q * QC < nblocks, at & ~3u);
     const __amdgpu_buffer_rsrc_t rs = tile_rsrc(a.scales, st, spitch);
-    if constexpr (FMT == kINT4) {
-      const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, (int)off, 0, 0);
-      d.v[0] = v[0];
-      d.v[1] = v[1];
-      d.v[2] = buffer_load32(rs, off + 8u);
-    } else {
-      const uint4 v = buffer_load16(rs, off);
-      d.v[0] = v.x; d.v[1] = v.y; d.v[2] = v.z; d.v[3] = v.w;
-      if constexpr (kMX) d.v[4] = buffer_load32(rs, off + 16u);
-      if constexpr (Sc::kPer == 4) {
-        const uint4 u = buffer_load16(rs, off + 16u);
-        d.v[4] = u.x; d.v[5] = u.y; d.v[6] = u.z; d.v[7] = u.w;
-      }
-    }
+    load_scale_window<FMT>(d, rs, off);
     if (++sj == nsw) {
       sj = 0;
       st += gridDim.x * RT;
@@ -276,8 +442,6 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 4 : 2) moe_kernel(MoeAr
   // a tile starts on a multiple of 32 bytes)
   const uint32_t sshift = ((uint32_t)(lane >> 2) * spitch & 2u) * 8u;
 
-  const uint32_t laneoff = (uint32_t)(lane & 15) * 16u;
-  const char* tabc = reinterpret_cast<const char*>(tab);
   const uint32_t rpitch = a.qpw * 512u;  // bytes of a window row: its quads
   const uint32_t per = a.qpw / KW;       // quads of a K group per window
   // This lane's A row in each column tile, as its window offset, and its piece of a block's first
@@ -367,130 +531,14 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 4 : 2) moe_kernel(MoeAr
     for (int t = 0; t < NT; ++t) acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
 
     // Multiply the quad held in d: quad j of this K group, at window quad wq (of this K group).
-    auto compute = [&](uint32_t j, uint32_t wq, const MoeQuad& d) __attribute__((always_inline)) {
-      // The quad's scales of row m: from lane 4 m + (pair of quads), the quad's half of its dwords.  Those
-      // of blocks past K are the next row's: zeros instead.
-      const uint32_t jw = j % Sc::kQuads, qb = (kg * qpk + j) * QC;
-      const int from = (4 * m + (int)(jw >> 1)) * 4;
-      uint32_t sw[Sc::kPer];
-#pragma unroll
-      for (int i = 0; i < Sc::kPer; ++i)
-        sw[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)(jw & 1u ? held_scales.v[Sc::kPer + i] : held_scales.v[i]));
-      if (qb + QC > nblocks) {
-        const uint32_t left = qb < nblocks ? (nblocks - qb) * SB : 0u;  // bytes of scales inside K
-#pragma unroll
-        for (int i = 0; i < Sc::kPer; ++i)
-          sw[i] = 4u * i + 4u <= left ? sw[i] : 4u * i < left ? sw[i] & 0xFFFFu : 0u;
-      }
-      // (Opaque copies: offsets derived from these are recomputed per quad, an operation each, instead of
-      // being held across the loop in registers that the loads in flight need.)
-      uint32_t ap[NT];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        ap[t] = apiece[t];
-        asm volatile("" : "+v"(ap[t]));
-      }
-      const uint8_t* wbase = win + wq * 512u;
-      // chunks g and g + 4 of row m: lanes m < 8 hold (row m, g) in load 0 and need (row m, g + 4) of
-      // lane m + 8; lanes m >= 8 hold (row m, g + 4) in load 1 and need (row m, g) of lane m - 8
-      uint32_t wh[2][4], wb[QC][STEPS];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        wh[0][i] = (uint32_t)__builtin_amdgcn_update_dpp((int)d.w[0][i], (int)d.w[1][i], 0x118, 0xF, 0xC, false);
-        wh[1][i] = (uint32_t)__builtin_amdgcn_update_dpp((int)d.w[1][i], (int)d.w[0][i], 0x108, 0xF, 0x3, false);
-      }
-      if constexpr (is_g128(FMT)) {
-#pragma unroll
-        for (int c = 0; c < (int)QC; ++c)
-#pragma unroll
-          for (int s = 0; s < STEPS; ++s) wb[c][s] = wh[c][s];
-      } else {
-        // 64-weight blocks: chunks 2 c, 2 c + 1 of the half quad to every lane group, two dwords
-        // each; MXFP4: one more swap gives step s the dwords of the 32-weight block s.
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const auto s0 = __builtin_amdgcn_permlane32_swap(wh[h][0], wh[h][2], false, false);
-          const auto s1 = __builtin_amdgcn_permlane32_swap(wh[h][1], wh[h][3], false, false);
-          wb[2 * h][0] = s0[0];
-          wb[2 * h][1] = s1[0];
-          wb[2 * h + 1][0] = s0[1];
-          wb[2 * h + 1][1] = s1[1];
-        }
-        if constexpr (kMX) {
-#pragma unroll
-          for (int c = 0; c < (int)QC; ++c) {
-            const auto t = __builtin_amdgcn_permlane16_swap(wb[c][0], wb[c][1], false, false);
-            wb[c][0] = t[0];
-            wb[c][1] = t[1];
-          }
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < (int)QC; ++c) {
-        float4_t dd[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) dd[t] = float4_t{0.f, 0.f, 0.f, 0.f};
-        // Integer codes decode as q + 16; a column of -(16 + z) takes the offset off (z = 8: INT4).
-        uint4 zcol = make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (is_g128(FMT)) {
-          const float zn = FMT == kINT4 ? -24.0f : -16.0f - (float)((sw[c % Sc::kPer] >> 16) & 15u);
-          const uint32_t h = XT == kF16 ? f16_bits(zn) : (__float_as_uint(zn) >> 16);
-          zcol = make_uint4(h | (h << 16), h | (h << 16), h | (h << 16), h | (h << 16));
-        }
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-          constexpr uint32_t kPieces = KC / 8;  // of a block
-          const uint32_t at = (c * kPieces + s * (kMX ? 4u : 1u)) * 16u;
-          uint4 xv[NT];
-#pragma unroll
-          for (int t = 0; t < NT; ++t) xv[t] = *reinterpret_cast<const uint4*>(wbase + arow[t] + (ap[t] ^ at));
-          uint4 b1, b2;
-          if constexpr (kTable) {
-            uint2 tv[4];
-#pragma unroll
-            for (int kb = 0; kb < 4; ++kb) {
-              // LDS byte address = byte * 128 + lane offset: byte * 256 + 2 * lane offset, halved
-              const uint32_t addr =
-                  __builtin_amdgcn_perm(wb[c][s], laneoff, 0x0C0C0000u | ((4u + (uint32_t)kb) << 8)) >> 1;
-              tv[kb] = *reinterpret_cast<const uint2*>(tabc + addr);
-            }
-            b1 = make_uint4(tv[0].x, tv[1].x, tv[2].x, tv[3].x);
-            b2 = make_uint4(tv[0].y, tv[1].y, tv[2].y, tv[3].y);
-          } else {
-            b1 = decode8<FMT, XT>(wb[c][s]);
-          }
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            dd[t] = mfma<XT>(xv[t], b1, dd[t]);
-            if constexpr (kTable) dd[t] = mfma<XT>(xv[t], b2, dd[t]);
-            if constexpr (is_g128(FMT)) dd[t] = mfma<XT>(xv[t], zcol, dd[t]);
-          }
-          if constexpr (kMX) {
-            // 2^(e - 127); e = 255 gives an infinity here, which `finish` tells apart
-            const float sc = ldexpf(__uint_as_float(0x00400000u), (int)((sw[c >> 1] >> (16 * (c & 1) + 8 * s)) & 0xFFu));
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(dd[t][i], sc, acc[t][i]);
-              dd[t] = float4_t{0.f, 0.f, 0.f, 0.f};
-            }
-          }
-        }
-        if constexpr (!kMX) {
-          const float sc = __uint_as_float(FMT == kINT4    ? (c == 0 ? sw[0] << 16 : sw[0] & 0xFFFF0000u)
-                                           : FMT == kINT4A ? sw[c % Sc::kPer] << 16 : sw[c % Sc::kPer]);
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(dd[t][i], sc, acc[t][i]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
+    auto compute = [&](uint32_t j, uint32_t wq, const MoeQuad& d, auto odd) __attribute__((always_inline)) {
+      const uint32_t qb = (kg * qpk + j) * QC;
+      const uint32_t left = qb < nblocks ? (nblocks - qb) * SB : 0u;
+      quad_product<FMT, XT, NT, decltype(odd)::value>(acc, d, held_scales, j % Sc::kQuads, left, win + wq * 512u, arow, apiece, tab, lane);
     };
 
     // A tile's value for (row n, A row 4 g + i of column tile t): its K groups' sums, in group order.
-    // Waves hold theirs as [t][i][16 g + n].  An MXFP4 scale byte of 255 is NaN: it made its row's
-    // sums infinite or NaN, so a row is looked through for it only then.
+    // Waves hold theirs as [t][i][16 g + n].
     auto tile_value = [&](const float* buf, uint32_t tile, uint32_t n, uint32_t t, uint32_t r)
                           __attribute__((always_inline)) {
       float v = 0.0f;
@@ -500,14 +548,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 4 : 2) moe_kernel(MoeAr
       return kTable ? v * (1.0f / kNf4Factor) : v;
     };
     auto with_nan = [&](float v, uint32_t row) __attribute__((always_inline)) {
-      if constexpr (kMX) {
-        if (!__builtin_isfinite(v)) {
-          const uint8_t* sp = reinterpret_cast<const uint8_t*>(a.scales) + ((size_t)e * a.n + row) * spitch;
-          for (uint32_t i = 0; i < spitch; ++i)
-            if (sp[i] == 255u) v = __uint_as_float(0x7FC00000u);
-        }
-      }
-      return v;
+      return with_nan_scales<FMT>(v, reinterpret_cast<const uint8_t*>(a.scales) + ((size_t)e * a.n + row) * spitch, spitch);
     };
 
     uint32_t held = 0xFFFFFFFFu;  // first quad (of each K group) of the window in LDS
@@ -522,19 +563,12 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 4 : 2) moe_kernel(MoeAr
           __syncthreads();
         }
         if (j % Sc::kQuads == 0) {  // the next scale window: shifted into place, the one after it requested
-#pragma unroll
-          for (int i = 0; i < 2 * Sc::kPer; ++i) {
-            if constexpr (Sc::kShift) {
-              held_scales.v[i] = __builtin_amdgcn_alignbit(next_scales.v[i + 1], next_scales.v[i], sshift);
-            } else {
-              held_scales.v[i] = next_scales.v[i];
-            }
-          }
+          place_scales<FMT>(held_scales, next_scales, sshift);
           load_scales(next_scales);
         }
-        compute(j, j - w0, W0);
+        compute(j, j - w0, W0, std::integral_constant<int, 0>{});
         load_quad(W0);
-        if (j + 1 < qpk) compute(j + 1, j + 1 - w0, W1);
+        if (j + 1 < qpk) compute(j + 1, j + 1 - w0, W1, std::integral_constant<int, 1>{});
         load_quad(W1);
       }
 
@@ -583,6 +617,161 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 4 : 2) moe_kernel(MoeAr
     }
     if (c0 + cols < count) __syncthreads();  // the window and the sums have been read
   }
+}
+
+// Down products of a few tokens, combined in the same launch: a workgroup takes 16 rows of y of one
+// token, each wave the product with one of the token's experts (SL = 8 / KW slots at a time, K in KW
+// ranges), scaled by its routing weight and added up in LDS in a fixed order.  No partial results in
+// memory and no third launch; tokens that share an expert read its weights again (mostly from L2),
+// so it serves calls whose pairs are few beside the experts.  A wave's window holds the three planes
+// of its own pair alone: nothing is shared until the sums, and no barrier stands in the way.
+constexpr uint32_t kTokenQuads = 6;  // quads of a wave's window
+
+template <int FMT, int KW>
+__global__ void __launch_bounds__(kMoeThreads, 4) moe_token_kernel(MoeArgs a) {
+  constexpr uint32_t SL = 8 / KW;
+  constexpr int KC = is_g128(FMT) ? 128 : 64;
+  constexpr uint32_t QC = 256 / KC;
+  constexpr bool kMX = FMT == kMXFP4;
+  constexpr bool kTable = FMT == kNF4;
+  constexpr uint32_t SB = FMT == kINT4 || kMX ? 2 : 4;
+  using Sc = MoeScales<FMT>;
+  __shared__ __align__(16) uint32_t tab[kTable ? kTableBytes / 4 : 4];
+  __shared__ float sums[8][16];
+  extern __shared__ __align__(16) uint8_t smem[];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint32_t sl = (uint32_t)wave % SL, kg = (uint32_t)wave / SL;
+  const int g = lane >> 4, m = lane & 15;
+  const uint32_t token = blockIdx.y;
+  const bool slot_lane = (uint32_t)lane < a.top_k;
+  const int id = slot_lane ? a.ids[token * a.top_k + (uint32_t)lane] : -1;
+  const float weight = slot_lane ? a.weights[token * a.top_k + (uint32_t)lane] : 0.0f;
+  if constexpr (kTable) {
+    fill_moe_table<kBF16>(tab);
+    __syncthreads();
+  }
+
+  const uint32_t qpk = a.qpk;
+  const uint32_t pitch = a.k >> 1;
+  const uint32_t nblocks = a.k / KC;
+  const uint32_t spitch = nblocks * SB;
+  const uint32_t nchunks = a.k >> 5;
+  const uint32_t per = min(qpk, kTokenQuads);  // quads of a window
+  uint8_t* win = smem + (uint32_t)wave * (3u * per * 512u);
+  const uint32_t chunk = (uint32_t)g + 4u * (uint32_t)(m >> 3);
+  const uint32_t wlane = (uint32_t)(m & 7) * pitch + chunk * 16u;
+  const uint32_t sshift = ((uint32_t)(lane >> 2) * spitch & 2u) * 8u;
+  const uint32_t plane = (uint32_t)min(m, 2);  // A row m is plane m (rows 3 .. 15 repeat the last)
+  const uint32_t arow[1] = {plane * (per * 512u)};
+  const uint32_t piece = kMX ? g : is_g128(FMT) ? 4 * g : 4 * (g & 1) + 2 * (g >> 1);
+  const uint32_t apiece[1] = {(piece ^ plane) * 16u};
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, 3u * a.pairs * a.k * 2u);
+  const uint32_t tile = blockIdx.x;
+
+  float y = 0.0f;  // lanes 0 .. 15: this wave's share of row 16 tile + lane
+  for (uint32_t slot = sl; slot < a.top_k; slot += SL) {
+    const int e = __builtin_amdgcn_readlane(id, (int)slot);
+    if ((uint32_t)e >= a.experts) continue;
+    const size_t row0 = (size_t)e * a.n + tile * 16u;
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.packed + row0 * pitch, 16u * pitch);
+    const __amdgpu_buffer_rsrc_t rs =
+        make_rsrc(reinterpret_cast<const char*>(a.scales) + row0 * spitch, 16u * spitch);
+    auto load_quad = [&](uint32_t j, MoeQuad& d) __attribute__((always_inline)) {
+      const uint32_t q = kg * qpk + j;
+      const bool in = j < qpk && q * 8 + chunk < nchunks;
+      const uint4 v0 = buffer_load16_stream(rw, offset_or_oob(in, wlane + q * 128u));
+      const uint4 v1 = buffer_load16_stream(rw, offset_or_oob(in, wlane + q * 128u + 8u * pitch));
+      d.w[0][0] = v0.x; d.w[0][1] = v0.y; d.w[0][2] = v0.z; d.w[0][3] = v0.w;
+      d.w[1][0] = v1.x; d.w[1][1] = v1.y; d.w[1][2] = v1.z; d.w[1][3] = v1.w;
+    };
+    auto load_scales = [&](uint32_t j, Sc& d) __attribute__((always_inline)) {
+      const uint32_t q = kg * qpk + j;
+      const uint32_t at = (uint32_t)(lane >> 2) * spitch + (q + 2u * (uint32_t)(lane & 3)) * (QC * SB);
+      load_scale_window<FMT>(d, rs, offset_or_oob(j < qpk && q * QC < nblocks, at & ~3u));
+    };
+    const uint32_t pair = token * a.top_k + slot;
+
+    MoeQuad W0, W1;
+    Sc held, next;
+    float4_t acc[1] = {float4_t{0.f, 0.f, 0.f, 0.f}};
+    for (uint32_t j0 = 0; j0 < qpk; j0 += per) {
+      // The window: quads j0 .. j0 + per - 1 of this K range, 32 pieces of a plane's quad
+      uint4 v[3][kTokenQuads / 2];
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (uint32_t i = 0; i < kTokenQuads / 2; ++i) {
+          const uint32_t ql = 2u * i + (uint32_t)(lane >> 5), jq = j0 + ql;
+          const uint32_t kpos = (kg * qpk + jq) * 256u + ((((uint32_t)lane & 31u) ^ (uint32_t)p) * 8u);
+          if (2u * i < per)
+            v[p][i] = buffer_load16(rx, offset_or_oob(ql < per && jq < qpk && kpos < a.k,
+                                                      (((uint32_t)p * a.pairs + pair) * a.k + kpos) * 2u));
+        }
+      auto store_window = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (uint32_t i = 0; i < kTokenQuads / 2; ++i) {
+            const uint32_t ql = 2u * i + (uint32_t)(lane >> 5);
+            if (2u * i < per && ql < per)
+              *reinterpret_cast<uint4*>(win + ((uint32_t)p * per + 2u * i) * 512u + (uint32_t)lane * 16u) = arranged<FMT>(v[p][i]);
+          }
+      };
+      // (the stores stand in both branches: behind a join they would wait for the weights too)
+      if (j0 == 0) {
+        load_scales(0, next);
+        load_quad(0, W0);
+        load_quad(1, W1);
+        store_window();
+      } else {
+        store_window();
+      }
+      const uint32_t end = min(qpk, j0 + per);
+      for (uint32_t j = j0; j < end; j += 2) {
+        if (j % Sc::kQuads == 0) {
+          place_scales<FMT>(held, next, sshift);
+          load_scales(j + Sc::kQuads, next);
+        }
+        auto product = [&](uint32_t jj, const MoeQuad& d, auto odd) __attribute__((always_inline)) {
+          const uint32_t qb = (kg * qpk + jj) * QC;
+          quad_product<FMT, kBF16, 1, decltype(odd)::value>(acc, d, held, jj % Sc::kQuads, qb < nblocks ? (nblocks - qb) * SB : 0u,
+                                      win + (jj - j0) * 512u, arow, apiece, tab, lane);
+        };
+        product(j, W0, std::integral_constant<int, 0>{});
+        load_quad(j + 2, W0);
+        if (j + 1 < end) product(j + 1, W1, std::integral_constant<int, 1>{});
+        load_quad(j + 3, W1);
+      }
+    }
+    // rows 0, 1, 2 of D are the planes' products: lanes 0 .. 15, i = 0, 1, 2
+    float v = acc[0][0] + (acc[0][1] + acc[0][2]);
+    if constexpr (kTable) v *= 1.0f / kNf4Factor;
+    if (lane < 16)
+      v = with_nan_scales<FMT>(v, reinterpret_cast<const uint8_t*>(a.scales) + (row0 + (uint32_t)m) * spitch, spitch);
+    const float w = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(weight), (int)slot));
+    y = __builtin_fmaf(w, v, y);
+  }
+  if (lane < 16) sums[wave][lane] = y;
+  __syncthreads();
+  if (tid < 16) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v += sums[w][tid];
+    a.y[(size_t)token * a.n + tile * 16u + (uint32_t)tid] = v;
+  }
+}
+
+template <int FMT, int KW>
+hipError_t launch_moe_token_one(const MoeArgs& a, uint32_t tokens, hipStream_t s) {
+  constexpr uint32_t kMost = 8 * 3 * kTokenQuads * 512;
+  static const hipError_t raised = hipFuncSetAttribute(reinterpret_cast<const void*>(&moe_token_kernel<FMT, KW>),
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, kMost);
+  if (raised != hipSuccess) return raised;
+  const uint32_t per = a.qpk < kTokenQuads ? a.qpk : kTokenQuads;
+  hipLaunchKernelGGL((moe_token_kernel<FMT, KW>), dim3(a.tiles, tokens), dim3(kMoeThreads), 8u * 3u * per * 512u, s, a);
+  return hipGetLastError();
 }
 
 template <int DIR, int FMT, int XT, int NT, int KW>
