@@ -36,6 +36,8 @@ constexpr int kMoePacked = 4;      // pairs of a down chunk whose three planes s
 // pairs a chunk, 3: up to 16, a tile per plane).  grid.y = slots (see moe_kernel).
 hipError_t launch_moe_up_f16(int weight, int kw, const MoeArgs& a, uint32_t slots, hipStream_t s);
 hipError_t launch_moe_up_bf16(int weight, int kw, const MoeArgs& a, uint32_t slots, hipStream_t s);
+hipError_t launch_moe_pair_f16(int weight, int kw, const MoeArgs& a, uint32_t tokens, hipStream_t s);
+hipError_t launch_moe_pair_bf16(int weight, int kw, const MoeArgs& a, uint32_t tokens, hipStream_t s);
 hipError_t launch_moe_token(int weight, int kw, const MoeArgs& a, uint32_t tokens, hipStream_t s);
 hipError_t launch_moe_down(int weight, int kw, int tiles, const MoeArgs& a, uint32_t slots,
                            hipStream_t s);

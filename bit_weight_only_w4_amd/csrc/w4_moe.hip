@@ -4,6 +4,12 @@
 
 #include "w4_moe.h"
 
+#ifndef MOE_PAIR_KW
+#define MOE_PAIR_KW 8
+#endif
+#ifndef MOE_PAIR_WAVES
+#define MOE_PAIR_WAVES 2048
+#endif
 #ifndef MOE_TOKEN_PAIRS
 #define MOE_TOKEN_PAIRS 64
 #endif
@@ -216,6 +222,28 @@ hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const floa
   a.n = (uint32_t)(2 * inter);
   a.k = (uint32_t)hidden;
   a.tiles = (uint32_t)(inter / 8);
+  // A few tokens, mostly with experts of their own: two launches, a wave per pair in each.
+  if (tokens == 1 || (pairs <= MOE_TOKEN_PAIRS && 2 * pairs <= experts)) {
+    const int64_t units = inter / 16 * pairs;
+    int kw = 1;
+    while (kw < MOE_PAIR_KW && 2 * kw <= (hidden + 255) / 256 && units * kw < MOE_PAIR_WAVES) kw *= 2;
+    a.qpk = (uint32_t)(((hidden + 255) / 256 + kw - 1) / kw);
+    hipError_t e = fmt_xtype(fmt) == kF16 ? launch_moe_pair_f16(weight, kw, a, (uint32_t)tokens, s)
+                                          : launch_moe_pair_bf16(weight, kw, a, (uint32_t)tokens, s);
+    if (e != hipSuccess) return e;
+    a.packed = down;
+    a.scales = down_scales;
+    a.x = a.h;
+    a.n = (uint32_t)hidden;
+    a.k = (uint32_t)inter;
+    a.tiles = (uint32_t)(hidden / 16);
+    a.weights = weights;
+    a.y = y;
+    kw = top_k > 4 ? 1 : top_k > 2 ? 2 : 4;
+    while (kw > 1 && kw > (inter + 255) / 256) kw /= 2;
+    a.qpk = (uint32_t)(((inter + 255) / 256 + kw - 1) / kw);
+    return launch_moe_token(weight, kw, a, (uint32_t)tokens, s);
+  }
   uint32_t cols = (uint32_t)std::min<int64_t>(16, tokens);
   int kw = moe_kw(a.tiles, slots, hidden, cols);
   a.grid = (uint32_t)std::max<int64_t>(1, 2 * device_cu_count() / slots);
@@ -230,15 +258,6 @@ hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const floa
   a.n = (uint32_t)hidden;
   a.k = (uint32_t)inter;
   a.tiles = (uint32_t)(hidden / 16);
-  // A few tokens, mostly with experts of their own: the combination inside the down launch.
-  if (tokens == 1 || (pairs <= MOE_TOKEN_PAIRS && 2 * pairs <= experts)) {
-    a.weights = weights;
-    a.y = y;
-    kw = top_k > 4 ? 1 : top_k > 2 ? 2 : 4;
-    while (kw > 1 && kw > (inter + 255) / 256) kw /= 2;
-    a.qpk = (uint32_t)(((inter + 255) / 256 + kw - 1) / kw);
-    return launch_moe_token(weight, kw, a, (uint32_t)tokens, s);
-  }
   const int tiles = pairs <= 2 * experts ? 1 : 3;
   cols = (uint32_t)std::min<int64_t>(tiles == 1 ? kMoePacked : 16, tokens);
   kw = moe_kw(a.tiles, slots, inter, 3 * cols);

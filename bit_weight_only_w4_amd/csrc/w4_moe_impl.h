@@ -356,6 +356,19 @@ __device__ inline float with_nan_scales(float v, const void* scales, size_t byte
   return v;
 }
 
+// h = silu(gate) up of one row and pair, as three bf16 planes.
+__device__ inline void store_h(const MoeArgs& a, uint32_t pair, uint32_t row, uint32_t inter, float gate, float up) {
+  const float v = gate / (1.0f + expf(-gate)) * up;
+  const uint32_t b1 = __float_as_uint(v) & 0xFFFF0000u;
+  const float r1 = __builtin_isinf(v) ? 0.0f : v - __uint_as_float(b1);
+  const uint32_t b2 = __float_as_uint(r1) & 0xFFFF0000u;
+  const float r2 = r1 - __uint_as_float(b2);  // cut: a contracted r1 may be longer
+  const size_t at = (size_t)pair * inter + row, plane = (size_t)a.pairs * inter;
+  a.h[at] = (uint16_t)(b1 >> 16);
+  a.h[at + plane] = (uint16_t)(b2 >> 16);
+  a.h[at + 2 * plane] = (uint16_t)(__float_as_uint(r2) >> 16);
+}
+
 template <int DIR, int FMT, int XT, int NT, int KW>
 __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 4 : 2) moe_kernel(MoeArgs a) {
   constexpr uint32_t RT = 8 / KW;
@@ -590,15 +603,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 4 : 2) moe_kernel(MoeAr
           const int pair = __shfl(list, (int)j);  // (rows * have is a multiple of 16: lanes 0 .. 15 take part)
           const float gate = with_nan(tile_value(buf, tile, n, j / 16u, j & 15u), row0 + row);
           const float up = with_nan(tile_value(buf, tile + 1u, n, j / 16u, j & 15u), inter + row0 + row);
-          const float v = gate / (1.0f + expf(-gate)) * up;
-          const uint32_t b1 = __float_as_uint(v) & 0xFFFF0000u;
-          const float r1 = __builtin_isinf(v) ? 0.0f : v - __uint_as_float(b1);
-          const uint32_t b2 = __float_as_uint(r1) & 0xFFFF0000u;
-          const float r2 = r1 - __uint_as_float(b2);  // cut: a contracted r1 may be longer
-          const size_t at = (size_t)(uint32_t)pair * inter + row0 + row, plane = (size_t)a.pairs * inter;
-          a.h[at] = (uint16_t)(b1 >> 16);
-          a.h[at + plane] = (uint16_t)(b2 >> 16);
-          a.h[at + 2 * plane] = (uint16_t)(__float_as_uint(r2) >> 16);
+          store_h(a, (uint32_t)pair, row0 + row, inter, gate, up);
         }
       } else {
         const uint32_t row0 = tile0 * 16u, rows = tiles * 16u;
@@ -619,12 +624,180 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 4 : 2) moe_kernel(MoeAr
   }
 }
 
-// Down products of a few tokens, combined in the same launch: a workgroup takes 16 rows of y of one
-// token, each wave the product with one of the token's experts (SL = 8 / KW slots at a time, K in KW
-// ranges), scaled by its routing weight and added up in LDS in a fixed order.  No partial results in
-// memory and no third launch; tokens that share an expert read its weights again (mostly from L2),
-// so it serves calls whose pairs are few beside the experts.  A wave's window holds the three planes
-// of its own pair alone: nothing is shared until the sums, and no barrier stands in the way.
+// The products of a few tokens, whose pairs are few beside the experts: no list of an expert's pairs and no
+// window that waves share.  A wave takes one pair; tokens that share an expert read its weights
+// again, mostly from L2.  SL = 8 / KW pairs side by side in a workgroup, K in KW ranges; a wave's
+// window holds what it needs itself, and no barrier stands before the sums.
+
+// Up: 16 rows of h of SL slots of one token; a wave multiplies its expert's gate and up tile by x.
+constexpr uint32_t kPairQuads = 8;  // quads of a wave's window
+
+template <int FMT, int XT, int KW>
+__global__ void __launch_bounds__(kMoeThreads, 4) moe_pair_kernel(MoeArgs a) {
+  constexpr uint32_t SL = 8 / KW;
+  constexpr int KC = is_g128(FMT) ? 128 : 64;
+  constexpr uint32_t QC = 256 / KC;
+  constexpr bool kMX = FMT == kMXFP4;
+  constexpr bool kTable = FMT == kNF4;
+  constexpr uint32_t SB = FMT == kINT4 || kMX ? 2 : 4;
+  using Sc = MoeScales<FMT>;
+  __shared__ __align__(16) uint32_t tab[kTable ? kTableBytes / 4 : 4];
+  __shared__ float sums[8][2][16];
+  __shared__ __align__(16) uint8_t window[8][kPairQuads * 512];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint32_t sl = (uint32_t)wave % SL, kg = (uint32_t)wave / SL;
+  const int g = lane >> 4, m = lane & 15;
+  const uint32_t rounds = (a.top_k + SL - 1) / SL;
+  const uint32_t token = blockIdx.y / rounds, slot0 = (blockIdx.y - token * rounds) * SL;
+  const bool have = slot0 + sl < a.top_k;
+  const uint32_t pair = token * a.top_k + slot0 + sl;
+  const int e = have ? a.ids[pair] : -1;
+
+  const uint32_t qpk = a.qpk;
+  const uint32_t tile = blockIdx.x, inter = a.n >> 1;
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (size_t)token * a.k, a.k * 2u);
+  uint8_t* win = window[wave];
+  // quads j0 .. j0 + 7 of this K range, 32 pieces each
+  uint4 v[kPairQuads / 2];
+  auto load_window = [&](uint32_t j0) __attribute__((always_inline)) {
+#pragma unroll
+    for (uint32_t i = 0; i < kPairQuads / 2; ++i) {
+      const uint32_t jq = j0 + 2u * i + (uint32_t)(lane >> 5), kpos = (kg * qpk + jq) * 256u + ((uint32_t)lane & 31u) * 8u;
+      if (j0 + 2u * i < qpk) v[i] = buffer_load16(rx, offset_or_oob(jq < qpk && kpos < a.k, kpos * 2u));
+    }
+  };
+  auto store_window = [&](uint32_t j0) __attribute__((always_inline)) {
+#pragma unroll
+    for (uint32_t i = 0; i < kPairQuads / 2; ++i)
+      if (j0 + 2u * i < qpk) *reinterpret_cast<uint4*>(win + i * 1024u + (uint32_t)lane * 16u) = arranged<FMT>(v[i]);
+  };
+  load_window(0);  // x does not wait for the ids
+  if constexpr (kTable) {
+    fill_moe_table<XT>(tab);
+    __syncthreads();
+  }
+
+  const uint32_t pitch = a.k >> 1;
+  const uint32_t nblocks = a.k / KC;
+  const uint32_t spitch = nblocks * SB;
+  const uint32_t nchunks = a.k >> 5;
+  const uint32_t chunk = (uint32_t)g + 4u * (uint32_t)(m >> 3);
+  const uint32_t wlane = (uint32_t)(m & 7) * pitch + chunk * 16u;
+  const uint32_t sshift = ((uint32_t)(lane >> 2) * spitch & 2u) * 8u;
+  const uint32_t arow[1] = {0};  // every A row is x
+  const uint32_t apiece[1] = {(uint32_t)(kMX ? g : is_g128(FMT) ? 4 * g : 4 * (g & 1) + 2 * (g >> 1)) * 16u};
+
+  if ((uint32_t)e < a.experts) {
+    __amdgpu_buffer_rsrc_t rw[2], rs[2];
+    size_t row0[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      row0[r] = (size_t)e * a.n + (r ? inter : 0u) + tile * 16u;
+      rw[r] = make_rsrc(a.packed + row0[r] * pitch, 16u * pitch);
+      rs[r] = make_rsrc(reinterpret_cast<const char*>(a.scales) + row0[r] * spitch, 16u * spitch);
+    }
+    auto load_quad = [&](uint32_t j, MoeQuad (&d)[2]) __attribute__((always_inline)) {
+      const uint32_t q = kg * qpk + j;
+      const bool in = j < qpk && q * 8 + chunk < nchunks;
+      const uint32_t o0 = offset_or_oob(in, wlane + q * 128u), o1 = offset_or_oob(in, wlane + q * 128u + 8u * pitch);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint4 v0 = buffer_load16_stream(rw[r], o0);
+        const uint4 v1 = buffer_load16_stream(rw[r], o1);
+        d[r].w[0][0] = v0.x; d[r].w[0][1] = v0.y; d[r].w[0][2] = v0.z; d[r].w[0][3] = v0.w;
+        d[r].w[1][0] = v1.x; d[r].w[1][1] = v1.y; d[r].w[1][2] = v1.z; d[r].w[1][3] = v1.w;
+      }
+    };
+    Sc raw[2], held[2];
+    auto load_scales = [&](uint32_t j) __attribute__((always_inline)) {
+      const uint32_t q = kg * qpk + j;
+      const uint32_t at = (uint32_t)(lane >> 2) * spitch + (q + 2u * (uint32_t)(lane & 3)) * (QC * SB);
+      const uint32_t off = offset_or_oob(j < qpk && q * QC < nblocks, at & ~3u);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) load_scale_window<FMT>(raw[r], rs[r], off);
+    };
+    MoeQuad W0[2], W1[2];
+    load_scales(0);
+    load_quad(0, W0);
+    load_quad(1, W1);
+    store_window(0);
+    float4_t acc[2][1] = {{float4_t{0.f, 0.f, 0.f, 0.f}}, {float4_t{0.f, 0.f, 0.f, 0.f}}};
+    for (uint32_t j = 0; j < qpk; j += 2) {
+      if (j > 0 && j % kPairQuads == 0) {
+        load_window(j);
+        store_window(j);
+      }
+      if (j % Sc::kQuads == 0) {  // (past the first window the scales are waited for: few ranges are so long)
+        if (j > 0) load_scales(j);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) place_scales<FMT>(held[r], raw[r], sshift);
+      }
+      auto product = [&](uint32_t jj, const MoeQuad (&d)[2], auto odd) __attribute__((always_inline)) {
+        const uint32_t qb = (kg * qpk + jj) * QC, left = qb < nblocks ? (nblocks - qb) * SB : 0u;
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          quad_product<FMT, XT, 1, decltype(odd)::value>(acc[r], d[r], held[r], jj % Sc::kQuads, left,
+                                                         win + (jj % kPairQuads) * 512u, arow, apiece, tab, lane);
+      };
+      product(j, W0, std::integral_constant<int, 0>{});
+      load_quad(j + 2, W0);
+      if (j + 1 < qpk) product(j + 1, W1, std::integral_constant<int, 1>{});
+      load_quad(j + 3, W1);
+    }
+    if (lane < 16) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float s = acc[r][0][0];  // all of D's rows are alike
+        if constexpr (kTable) s *= 1.0f / kNf4Factor;
+        sums[wave][r][lane] = with_nan_scales<FMT>(
+            s, reinterpret_cast<const uint8_t*>(a.scales) + (row0[r] + (uint32_t)lane) * spitch, spitch);
+      }
+    }
+  }
+  __syncthreads();
+  if (kg == 0 && lane < 16 && (uint32_t)e < a.experts) {
+    float gate = 0.0f, up = 0.0f;
+#pragma unroll
+    for (uint32_t w = 0; w < (uint32_t)KW; ++w) {
+      gate += sums[w * SL + sl][0][lane];
+      up += sums[w * SL + sl][1][lane];
+    }
+    store_h(a, pair, tile * 16u + (uint32_t)lane, inter, gate, up);
+  }
+}
+
+template <int FMT, int XT, int KW>
+hipError_t launch_moe_pair_one(const MoeArgs& a, uint32_t tokens, hipStream_t s) {
+  constexpr uint32_t SL = 8 / KW;
+  hipLaunchKernelGGL((moe_pair_kernel<FMT, XT, KW>), dim3(a.tiles / 2, tokens * ((a.top_k + SL - 1) / SL)),
+                     dim3(kMoeThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int XT>
+hipError_t launch_moe_pair_weight(int weight, int kw, const MoeArgs& a, uint32_t tokens, hipStream_t s) {
+#define W4_PAIR(F)                                                                    \
+  case F:                                                                             \
+    return kw == 1   ? launch_moe_pair_one<F, XT, 1>(a, tokens, s)                    \
+           : kw == 2 ? launch_moe_pair_one<F, XT, 2>(a, tokens, s)                    \
+           : kw == 4 ? launch_moe_pair_one<F, XT, 4>(a, tokens, s)                    \
+           : kw == 8 ? launch_moe_pair_one<F, XT, 8>(a, tokens, s) : hipErrorInvalidValue;
+  switch (weight) {
+    W4_PAIR(kNF4)
+    W4_PAIR(kINT4)
+    W4_PAIR(kFP4)
+    W4_PAIR(kINT4A)
+    W4_PAIR(kMXFP4)
+  }
+#undef W4_PAIR
+  return hipErrorInvalidValue;
+}
+
+// Down, combined in the same launch: 16 rows of y of one token, each wave the product with one of the
+// token's experts (SL slots at a time), scaled by its routing weight and added up in LDS in a fixed order.
+// No partial results in memory and no third launch.
 constexpr uint32_t kTokenQuads = 6;  // quads of a wave's window
 
 template <int FMT, int KW>
