@@ -24,7 +24,7 @@ struct MoeArgs {
   uint32_t qpk;            // quads (256 weights) per K group
   uint32_t qpw;            // quads per activation window, a multiple of the K groups
   uint32_t cols;           // pairs of a chunk: at most 16 per column tile (down with one tile: 4)
-  uint32_t grid;           // workgroups of a slot, at most one per group of tiles
+  uint32_t grid;           // workgroups of an expert, at most one per group of tiles
   uint32_t win_bytes;      // LDS bytes of a window: rows * qpw * 512
 };
 
@@ -33,13 +33,13 @@ constexpr uint32_t kMoeMaxWindow = 81920;  // LDS bytes of a window
 constexpr int kMoePacked = 4;      // pairs of a down chunk whose three planes share one tile
 
 // kw K groups (1, 2, 4) in a workgroup of 8 / kw row tiles; down also: tiles (1: up to kMoePacked
-// pairs a chunk, 3: up to 16, a tile per plane).  grid.y = slots (see moe_kernel).
-hipError_t launch_moe_up_f16(int weight, int kw, const MoeArgs& a, uint32_t slots, hipStream_t s);
-hipError_t launch_moe_up_bf16(int weight, int kw, const MoeArgs& a, uint32_t slots, hipStream_t s);
+// pairs a chunk, 3: up to 16, a tile per plane).
+hipError_t launch_moe_up_f16(int weight, int kw, const MoeArgs& a, hipStream_t s);
+hipError_t launch_moe_up_bf16(int weight, int kw, const MoeArgs& a, hipStream_t s);
 hipError_t launch_moe_pair_f16(int weight, int kw, const MoeArgs& a, uint32_t tokens, hipStream_t s);
 hipError_t launch_moe_pair_bf16(int weight, int kw, const MoeArgs& a, uint32_t tokens, hipStream_t s);
 hipError_t launch_moe_token(int weight, int kw, const MoeArgs& a, uint32_t tokens, hipStream_t s);
-hipError_t launch_moe_down(int weight, int kw, int tiles, const MoeArgs& a, uint32_t slots,
+hipError_t launch_moe_down(int weight, int kw, int tiles, const MoeArgs& a,
                            hipStream_t s);
 
 // The layer (arguments as w4_moe, already validated).

@@ -4,15 +4,6 @@
 
 #include "w4_moe.h"
 
-#ifndef MOE_PAIR_KW
-#define MOE_PAIR_KW 8
-#endif
-#ifndef MOE_PAIR_WAVES
-#define MOE_PAIR_WAVES 2048
-#endif
-#ifndef MOE_TOKEN_PAIRS
-#define MOE_TOKEN_PAIRS 64
-#endif
 namespace w4 {
 namespace {
 
@@ -132,7 +123,8 @@ hipError_t route_type(const void* logits, uint32_t tokens, uint32_t experts, uin
 }
 
 // y[t] = sum over slots j, in order, of weights[t, j] * part[t * top_k + j]; absent slots add
-// nothing (their rows of `part` were never written), a token without experts gets zeros.
+// nothing (their rows of `part` were never written), a token without experts gets zeros.  Bound by the
+// latency of one load after another, so a thread has four slots' loads in flight.
 __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ part,
                                                       const int32_t* __restrict__ ids,
                                                       const float* __restrict__ weights, uint32_t hidden,
@@ -142,26 +134,35 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
   const uint32_t n = blockIdx.x * 256 + threadIdx.x;
   if (n >= hidden) return;
   float v = 0.0f;
-  for (uint32_t j = 0; j < top_k; ++j) {
-    const uint32_t p = t * top_k + j;
-    if ((uint32_t)ids[p] < experts) v = __builtin_fmaf(weights[p], part[(size_t)p * hidden + n], v);
+  // four slots' loads together; what an absent slot's row holds is loaded too, and left out
+  for (uint32_t j0 = 0; j0 < top_k; j0 += 4) {
+    float x[4], w[4];
+    bool have[4];
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+      const uint32_t p = t * top_k + min(j0 + i, top_k - 1u);
+      x[i] = part[(size_t)p * hidden + n];
+      w[i] = weights[p];
+      have[i] = j0 + i < top_k && (uint32_t)ids[p] < experts;
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) v = have[i] ? __builtin_fmaf(w[i], x[i], v) : v;
   }
   y[(size_t)t * hidden + n] = v;
 }
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Workgroups of a slot (MoeArgs::grid): as many as give the possible experts in use two per CU together,
-// what fits; each then walks the expert's tile groups with its loads running ahead and one window
+// Workgroups of an expert (MoeArgs::grid): as many as give the experts two per CU together, what fits; each then walks the expert's tile groups with its loads running ahead and one window
 // of activations.  Measured on MI355X (32 tokens, 8 of 128 experts, 2048 x 768, MXFP4): 4 workgroups of each expert
 // and direction 83.5 us, one per tile group 92.
 // K groups: the fewest whose workgroups give every CU two, at most one per quad, and two quads of
 // `rows` window rows for each inside the largest window.
-int moe_kw(int64_t tiles, int64_t slots, int64_t k, int64_t rows) {
+int moe_kw(int64_t tiles, int64_t experts, int64_t k, int64_t rows) {
   const int64_t quads = (k + 255) / 256;
   int kw = 1;
   while (kw < 4 && 2 * kw <= quads && rows * 1024 * 2 * kw <= kMoeMaxWindow &&
-         (tiles + 8 / kw - 1) / (8 / kw) * slots < 2 * device_cu_count())
+         (tiles + 8 / kw - 1) / (8 / kw) * experts < 2 * device_cu_count())
     kw *= 2;
   return kw;
 }
@@ -206,7 +207,6 @@ hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const floa
                       const void* down_scales, int64_t tokens, int64_t hidden, int64_t inter,
                       int64_t experts, int64_t top_k, float* y, void* ws, hipStream_t s) {
   const int64_t pairs = tokens * top_k;
-  const uint32_t slots = (uint32_t)std::min(pairs, experts);
   const int weight = fmt_weight(fmt);
   MoeArgs a{};
   a.ids = ids;
@@ -222,11 +222,17 @@ hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const floa
   a.n = (uint32_t)(2 * inter);
   a.k = (uint32_t)hidden;
   a.tiles = (uint32_t)(inter / 8);
-  // A few tokens, mostly with experts of their own: two launches, a wave per pair in each.
-  if (tokens == 1 || (pairs <= MOE_TOKEN_PAIRS && 2 * pairs <= experts)) {
+  // Fewer pairs than experts: a wave per pair in both launches, the second combining.  Measured on MI355X
+  // against the shared products and their third launch (us): 8 of 128 experts, 2048 x 768, MXFP4, at 2 / 4 /
+  // 8 / 12 / 16 / 32 tokens 18.2 / 26.8 / 45.8 / 63.6 / 77.6 / 143.7 against 24.3 / 32.2 / 48.7 / 66.2 / 77.4 /
+  // 86.5; 4 of 64, 1536 x 1408, INT4, at 4 / 8 / 12 / 16 tokens 23.1 / 35.5 / 51.4 / 63.1 against 30.0 /
+  // 41.3 / 52.2 / 59.5.
+  if (tokens == 1 || pairs < experts) {
+    const int least = top_k > 4 ? 1 : top_k > 2 ? 2 : top_k > 1 ? 4 : 8;  // no wave without a slot
+    // up: K ranges until the waves number two per SIMD
     const int64_t units = inter / 16 * pairs;
-    int kw = 1;
-    while (kw < MOE_PAIR_KW && 2 * kw <= (hidden + 255) / 256 && units * kw < MOE_PAIR_WAVES) kw *= 2;
+    int kw = least;
+    while (kw < 8 && 2 * kw <= (hidden + 255) / 256 && units * kw < 8 * device_cu_count()) kw *= 2;
     a.qpk = (uint32_t)(((hidden + 255) / 256 + kw - 1) / kw);
     hipError_t e = fmt_xtype(fmt) == kF16 ? launch_moe_pair_f16(weight, kw, a, (uint32_t)tokens, s)
                                           : launch_moe_pair_bf16(weight, kw, a, (uint32_t)tokens, s);
@@ -239,17 +245,16 @@ hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const floa
     a.tiles = (uint32_t)(hidden / 16);
     a.weights = weights;
     a.y = y;
-    kw = top_k > 4 ? 1 : top_k > 2 ? 2 : 4;
-    while (kw > 1 && kw > (inter + 255) / 256) kw /= 2;
+    kw = least;
     a.qpk = (uint32_t)(((inter + 255) / 256 + kw - 1) / kw);
     return launch_moe_token(weight, kw, a, (uint32_t)tokens, s);
   }
   uint32_t cols = (uint32_t)std::min<int64_t>(16, tokens);
-  int kw = moe_kw(a.tiles, slots, hidden, cols);
-  a.grid = (uint32_t)std::max<int64_t>(1, 2 * device_cu_count() / slots);
+  int kw = moe_kw(a.tiles, experts, hidden, cols);
+  a.grid = (uint32_t)std::max<int64_t>(1, 2 * device_cu_count() / experts);
   moe_window(hidden, kw, cols, 1, &a);
-  hipError_t e = fmt_xtype(fmt) == kF16 ? launch_moe_up_f16(weight, kw, a, slots, s)
-                                        : launch_moe_up_bf16(weight, kw, a, slots, s);
+  hipError_t e = fmt_xtype(fmt) == kF16 ? launch_moe_up_f16(weight, kw, a, s)
+                                        : launch_moe_up_bf16(weight, kw, a, s);
   if (e != hipSuccess) return e;
 
   a.packed = down;
@@ -260,9 +265,9 @@ hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const floa
   a.tiles = (uint32_t)(hidden / 16);
   const int tiles = pairs <= 2 * experts ? 1 : 3;
   cols = (uint32_t)std::min<int64_t>(tiles == 1 ? kMoePacked : 16, tokens);
-  kw = moe_kw(a.tiles, slots, inter, 3 * cols);
+  kw = moe_kw(a.tiles, experts, inter, 3 * cols);
   moe_window(inter, kw, cols, 3, &a);
-  e = launch_moe_down(weight, kw, tiles, a, slots, s);
+  e = launch_moe_down(weight, kw, tiles, a, s);
   if (e != hipSuccess) return e;
 
   hipLaunchKernelGGL(combine_kernel, dim3((unsigned)((hidden + 255) / 256), (unsigned)tokens), dim3(256), 0,

@@ -2,9 +2,9 @@
 #include "w4_moe_impl.h"
 
 namespace w4 {
-hipError_t launch_moe_down(int weight, int kw, int tiles, const MoeArgs& a, uint32_t slots, hipStream_t s) {
-  return tiles == 1 ? launch_moe_weight<kDown, kBF16, 1>(weight, kw, a, slots, s)
-                    : launch_moe_weight<kDown, kBF16, 3>(weight, kw, a, slots, s);
+hipError_t launch_moe_down(int weight, int kw, int tiles, const MoeArgs& a, hipStream_t s) {
+  return tiles == 1 ? launch_moe_weight<kDown, kBF16, 1>(weight, kw, a, s)
+                    : launch_moe_weight<kDown, kBF16, 3>(weight, kw, a, s);
 }
 
 namespace {
@@ -14,6 +14,7 @@ hipError_t token_kw(int kw, const MoeArgs& a, uint32_t tokens, hipStream_t s) {
     case 1: return launch_moe_token_one<FMT, 1>(a, tokens, s);
     case 2: return launch_moe_token_one<FMT, 2>(a, tokens, s);
     case 4: return launch_moe_token_one<FMT, 4>(a, tokens, s);
+    case 8: return launch_moe_token_one<FMT, 8>(a, tokens, s);
   }
   return hipErrorInvalidValue;
 }

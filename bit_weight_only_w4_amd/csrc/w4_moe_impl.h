@@ -6,9 +6,9 @@
 // products; the up kernel writes h for every pair, the down kernel one row of partial results per
 // pair, and the combine kernel adds a token's pairs in slot order, scaled by their routing weights.
 //
-// Which experts are in use is known on the device alone.  grid.y gives each possible expert in use
-// a slot: with fewer pairs than experts slot s is pair s, whose workgroups take all pairs of the
-// pair's expert if no earlier pair has it (and end otherwise); else slot s is expert s.  Every wave finds
+// Which experts are in use is known on the device alone.  With fewer pairs than experts (and for one token)
+// a wave takes one pair (moe_pair_kernel, moe_token_kernel).  With more, the pairs of an expert share its
+// weights: grid.y is the expert, whose workgroups end at once if no pair has it.  Every wave finds
 // its expert's pairs itself, 64 ids at a time (a ballot, and a lane permutation that hands the r-th
 // pair to lane r): no launch, memory or barrier for a sorted list.
 //
@@ -121,13 +121,11 @@ __device__ inline uint4 arranged(uint4 v) {
   }
 }
 
-// The pairs of expert e in pair order: returns their number and the first of them, and in lane r
-// (r < ncol <= 63) the pair of rank c0 + r, or -1.  `id0` holds the first 64 ids, one a lane (-1 past
-// the last).  Every lane of the wave takes part.
-__device__ inline uint32_t scan_pairs(const int32_t* __restrict__ ids, uint32_t pairs, int id0, int e,
-                                      uint32_t c0, uint32_t ncol, int lane, uint32_t& first, int& mine) {
+// The pairs of expert e in pair order: returns their number, and in lane r (r < ncol <= 63) the pair of
+// rank c0 + r, or -1.  Every lane of the wave takes part.
+__device__ inline uint32_t scan_pairs(const int32_t* __restrict__ ids, uint32_t pairs, int e, uint32_t c0,
+                                      uint32_t ncol, int lane, int& mine) {
   uint32_t total = 0;
-  first = 0xFFFFFFFFu;
   mine = -1;
   auto batch = [&](uint32_t base, int id) __attribute__((always_inline)) {
     const bool match = id == e;
@@ -139,12 +137,10 @@ __device__ inline uint32_t scan_pairs(const int32_t* __restrict__ ids, uint32_t 
     const uint32_t to = match && rank - c0 < ncol ? rank - c0 : 63u;
     const int got = __builtin_amdgcn_ds_permute((int)(to * 4u), (int)(base + (uint32_t)lane + 1u));
     if (lane < (int)ncol && got > 0) mine = got - 1;
-    if (first == 0xFFFFFFFFu) first = base + (uint32_t)__builtin_ctzll(mask);
     total += (uint32_t)__builtin_popcountll(mask);
   };
-  batch(0, id0);
-  // then eight batches at a time: their loads are in flight together
-  for (uint32_t base = 64; base < pairs; base += 512) {
+  // eight batches at a time: their loads are in flight together
+  for (uint32_t base = 0; base < pairs; base += 512) {
     int id[8];
 #pragma unroll
     for (int b = 0; b < 8; ++b) {
@@ -387,14 +383,8 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 4 : 2) moe_kernel(MoeAr
   const uint32_t rt = (uint32_t)wave % RT, kg = (uint32_t)wave / RT;
   const int g = lane >> 4, m = lane & 15;
 
-  // This slot's expert, and the first 64 ids, before any other vector load: loads complete in order,
-  // and what waits for the ids must not wait for weights.
-  const bool by_pair = a.pairs < a.experts;
-  const int id0 = (uint32_t)lane < a.pairs ? a.ids[lane] : -1;
+  const int e = (int)blockIdx.y;  // the expert
   if constexpr (kTable) fill_moe_table<XT>(tab);
-  const int e = !by_pair ? (int)blockIdx.y
-                : blockIdx.y < 64 ? __builtin_amdgcn_readlane(id0, (int)blockIdx.y) : a.ids[blockIdx.y];
-  if ((uint32_t)e >= a.experts) return;
   const uint32_t cols = a.cols;  // pairs of a chunk
 
   const uint32_t qpk = a.qpk;
@@ -477,11 +467,11 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 4 : 2) moe_kernel(MoeAr
   Sc held_scales, next_scales;
   uint32_t count = 1;
   for (uint32_t c0 = 0; c0 < count; c0 += cols) {
-    uint32_t first;
+    // The expert's pairs, before any other vector load of the chunk: loads complete in order, and what
+    // waits for the ids must not wait for weights.
     int list;
-    count = scan_pairs(a.ids, a.pairs, id0, e, c0, cols, lane, first, list);
-    // without pairs, or another slot has this expert: every wave sees the same count
-    if (count == 0 || (by_pair && first != blockIdx.y)) return;
+    count = scan_pairs(a.ids, a.pairs, e, c0, cols, lane, list);
+    if (count == 0) return;  // (every wave sees the same count)
     const uint32_t have = min(cols, count - c0);
     lt = st = blockIdx.x * RT + rt;
     lj = sj = 0;
@@ -783,7 +773,8 @@ hipError_t launch_moe_pair_weight(int weight, int kw, const MoeArgs& a, uint32_t
     return kw == 1   ? launch_moe_pair_one<F, XT, 1>(a, tokens, s)                    \
            : kw == 2 ? launch_moe_pair_one<F, XT, 2>(a, tokens, s)                    \
            : kw == 4 ? launch_moe_pair_one<F, XT, 4>(a, tokens, s)                    \
-           : kw == 8 ? launch_moe_pair_one<F, XT, 8>(a, tokens, s) : hipErrorInvalidValue;
+           : kw == 8 ? launch_moe_pair_one<F, XT, 8>(a, tokens, s)                    \
+                     : hipErrorInvalidValue;
   switch (weight) {
     W4_PAIR(kNF4)
     W4_PAIR(kINT4)
@@ -948,7 +939,7 @@ hipError_t launch_moe_token_one(const MoeArgs& a, uint32_t tokens, hipStream_t s
 }
 
 template <int DIR, int FMT, int XT, int NT, int KW>
-hipError_t launch_moe_one(const MoeArgs& a, uint32_t slots, hipStream_t s) {
+hipError_t launch_moe_one(const MoeArgs& a, hipStream_t s) {
   constexpr uint32_t RT = 8 / KW, kSums = 2 * 8 * NT * 1024;
   // the limit on dynamic LDS, raised once per instantiation and process
   static const hipError_t raised = hipFuncSetAttribute(
@@ -957,29 +948,29 @@ hipError_t launch_moe_one(const MoeArgs& a, uint32_t slots, hipStream_t s) {
   if (raised != hipSuccess) return raised;
   if (a.win_bytes > kMoeMaxWindow) return hipErrorInvalidValue;
   const uint32_t ngroups = (a.tiles + RT - 1) / RT;
-  hipLaunchKernelGGL((moe_kernel<DIR, FMT, XT, NT, KW>), dim3(a.grid < ngroups ? a.grid : ngroups, slots),
+  hipLaunchKernelGGL((moe_kernel<DIR, FMT, XT, NT, KW>), dim3(a.grid < ngroups ? a.grid : ngroups, a.experts),
                      dim3(kMoeThreads), a.win_bytes + kSums, s, a);
   return hipGetLastError();
 }
 
 template <int DIR, int FMT, int XT, int NT>
-hipError_t launch_moe_kw(int kw, const MoeArgs& a, uint32_t slots, hipStream_t s) {
+hipError_t launch_moe_kw(int kw, const MoeArgs& a, hipStream_t s) {
   switch (kw) {
-    case 1: return launch_moe_one<DIR, FMT, XT, NT, 1>(a, slots, s);
-    case 2: return launch_moe_one<DIR, FMT, XT, NT, 2>(a, slots, s);
-    case 4: return launch_moe_one<DIR, FMT, XT, NT, 4>(a, slots, s);
+    case 1: return launch_moe_one<DIR, FMT, XT, NT, 1>(a, s);
+    case 2: return launch_moe_one<DIR, FMT, XT, NT, 2>(a, s);
+    case 4: return launch_moe_one<DIR, FMT, XT, NT, 4>(a, s);
   }
   return hipErrorInvalidValue;
 }
 
 template <int DIR, int XT, int NT>
-hipError_t launch_moe_weight(int weight, int kw, const MoeArgs& a, uint32_t slots, hipStream_t s) {
+hipError_t launch_moe_weight(int weight, int kw, const MoeArgs& a, hipStream_t s) {
   switch (weight) {
-    case kNF4: return launch_moe_kw<DIR, kNF4, XT, NT>(kw, a, slots, s);
-    case kINT4: return launch_moe_kw<DIR, kINT4, XT, NT>(kw, a, slots, s);
-    case kFP4: return launch_moe_kw<DIR, kFP4, XT, NT>(kw, a, slots, s);
-    case kINT4A: return launch_moe_kw<DIR, kINT4A, XT, NT>(kw, a, slots, s);
-    case kMXFP4: return launch_moe_kw<DIR, kMXFP4, XT, NT>(kw, a, slots, s);
+    case kNF4: return launch_moe_kw<DIR, kNF4, XT, NT>(kw, a, s);
+    case kINT4: return launch_moe_kw<DIR, kINT4, XT, NT>(kw, a, s);
+    case kFP4: return launch_moe_kw<DIR, kFP4, XT, NT>(kw, a, s);
+    case kINT4A: return launch_moe_kw<DIR, kINT4A, XT, NT>(kw, a, s);
+    case kMXFP4: return launch_moe_kw<DIR, kMXFP4, XT, NT>(kw, a, s);
   }
   return hipErrorInvalidValue;
 }
