@@ -1128,7 +1128,7 @@ int moe_shape(int fmt, int64_t tokens, int64_t hidden, int64_t inter, int64_t ex
 size_t w4_moe_workspace_bytes(int fmt, int64_t tokens, int64_t hidden, int64_t inter, int64_t experts,
                               int64_t top_k) {
   if (moe_shape(fmt, tokens, hidden, inter, experts, top_k) != W4_OK) return 0;
-  return moe_workspace(tokens * top_k, hidden, inter);
+  return moe_workspace(tokens * top_k, hidden, inter, experts);
 }
 
 int w4_moe(const void* x, const int32_t* ids, const float* weights, const uint8_t* gate_up,
@@ -1144,7 +1144,7 @@ int w4_moe(const void* x, const int32_t* ids, const float* weights, const uint8_
   if (!aligned(x, 16) || !aligned(gate_up, 16) || !aligned(down, 16) || !aligned(gate_up_scales, 4) ||
       !aligned(down_scales, 4) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(y, 4))
     return W4_ERR_ALIGN;
-  const size_t used = moe_workspace(tokens * top_k, hidden, inter);
+  const size_t used = moe_workspace(tokens * top_k, hidden, inter, experts);
   if (!workspace || workspace_bytes < used) return W4_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return W4_ERR_ALIGN;
   const size_t pairs = (size_t)(tokens * top_k), per = (size_t)hidden * (size_t)inter;  // weights a matrix

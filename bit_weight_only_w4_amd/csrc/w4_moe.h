@@ -10,6 +10,8 @@ struct MoeArgs {
   const uint8_t* packed;   // [E, N, K/2]; up: N = 2 inter, gate rows first
   const void* scales;      // [E, N, scales of K]
   const uint16_t* x;       // up: x [tokens, K]; down: the three planes of h [3, pairs, K]
+  const int32_t* order;    // many tokens: the pairs sorted by expert
+  const int32_t* start;    // ... and the first position of each expert, [experts + 1]
   const int32_t* ids;      // [pairs], pair = token * top_k + slot; outside [0, experts): absent
   uint16_t* h;             // up: planes of h [3, pairs, inter]
   float* part;             // down: [pairs, N]
@@ -39,6 +41,8 @@ hipError_t launch_moe_up_bf16(int weight, int kw, const MoeArgs& a, hipStream_t 
 hipError_t launch_moe_pair_f16(int weight, int kw, const MoeArgs& a, uint32_t tokens, hipStream_t s);
 hipError_t launch_moe_pair_bf16(int weight, int kw, const MoeArgs& a, uint32_t tokens, hipStream_t s);
 hipError_t launch_moe_token(int weight, int kw, const MoeArgs& a, uint32_t tokens, hipStream_t s);
+hipError_t launch_moe_wide_up(int weight, int xtype, const MoeArgs& a, hipStream_t s);
+hipError_t launch_moe_wide_down(int weight, const MoeArgs& a, hipStream_t s);
 hipError_t launch_moe_down(int weight, int kw, int tiles, const MoeArgs& a,
                            hipStream_t s);
 
@@ -47,7 +51,7 @@ hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const floa
                       const uint8_t* gate_up, const void* gate_up_scales, const uint8_t* down,
                       const void* down_scales, int64_t tokens, int64_t hidden, int64_t inter,
                       int64_t experts, int64_t top_k, float* y, void* ws, hipStream_t s);
-size_t moe_workspace(int64_t pairs, int64_t hidden, int64_t inter);
+size_t moe_workspace(int64_t pairs, int64_t hidden, int64_t inter, int64_t experts);
 hipError_t launch_moe_route(const void* logits, int type, int64_t tokens, int64_t experts, int64_t top_k,
                             bool renormalize, int32_t* ids, float* weights, hipStream_t s);
 

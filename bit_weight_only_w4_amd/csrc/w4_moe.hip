@@ -151,10 +151,56 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
   y[(size_t)t * hidden + n] = v;
 }
 
+// Pairs sorted by expert, in pair order: workgroup e counts the valid ids below e and writes the pairs of
+// e behind them, start[e] being their number.  Batches of 1024 ids, one a thread; ranks by ballots.
+constexpr uint32_t kOrderThreads = 1024;
+
+__global__ void __launch_bounds__(kOrderThreads) order_kernel(const int32_t* __restrict__ ids, uint32_t pairs,
+                                                              uint32_t experts, int32_t* __restrict__ order,
+                                                              int32_t* __restrict__ start) {
+  __shared__ uint32_t below_s[16], match_s[2][16];
+  const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
+  const int e = (int)blockIdx.x;  // e == experts: the number of valid pairs alone
+  uint32_t below = 0;
+  for (uint32_t i = tid; i < pairs; i += kOrderThreads) {
+    const int id = ids[i];
+    below += id >= 0 && id < e ? 1u : 0u;
+  }
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) below += (uint32_t)__shfl_xor((int)below, off);
+  if (lane == 0) below_s[wave] = below;
+  __syncthreads();
+  uint32_t at = 0;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) at += below_s[w];
+  if (tid == 0) start[e] = (int32_t)at;
+  if ((uint32_t)e == experts) return;
+  uint32_t flip = 0;
+  for (uint32_t base = 0; base < pairs; base += kOrderThreads, flip ^= 1u) {
+    const uint32_t i = base + tid;
+    const bool match = i < pairs && ids[i] == e;
+    const uint64_t mask = __ballot(match);
+    if (lane == 0) match_s[flip][wave] = (uint32_t)__builtin_popcountll(mask);
+    __syncthreads();  // (the other buffer is read no more when it is written again)
+    uint32_t before = 0, all = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < 16; ++w) {
+      const uint32_t c = match_s[flip][w];
+      before += w < wave ? c : 0u;
+      all += c;
+    }
+    if (match)
+      order[at + before + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                                    __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0))] = (int32_t)i;
+    at += all;
+  }
+}
+
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Workgroups of an expert (MoeArgs::grid): as many as give the experts two per CU together, what fits; each then walks the expert's tile groups with its loads running ahead and one window
-// of activations.  Measured on MI355X (32 tokens, 8 of 128 experts, 2048 x 768, MXFP4): 4 workgroups of each expert
+// Workgroups of an expert (MoeArgs::grid): as many as give the experts two per CU together, what fits;
+// each then walks the expert's tile groups with its loads running ahead and one window of activations.
+// Measured on MI355X (32 tokens, 8 of 128 experts, 2048 x 768, MXFP4): 4 workgroups of each expert
 // and direction 83.5 us, one per tile group 92.
 // K groups: the fewest whose workgroups give every CU two, at most one per quad, and two quads of
 // `rows` window rows for each inside the largest window.
@@ -197,9 +243,23 @@ hipError_t launch_moe_route(const void* logits, int type, int64_t tokens, int64_
   return hipErrorInvalidValue;
 }
 
-// The planes of h (three bf16 values per pair and row), then the partial results.
-size_t moe_workspace(int64_t pairs, int64_t hidden, int64_t inter) {
-  return align256((size_t)pairs * (size_t)inter * 6) + (size_t)pairs * (size_t)hidden * 4;
+// Many tokens: from three pairs an expert on, and from eight where the experts are too few to fill the
+// card without K groups (down: a workgroup has 128 rows).  Measured on MI355X against the kernels with K
+// groups (us for the layer): 8 of 128 experts, 2048 x 768, MXFP4, at 2 / 4 / 8 / 16 pairs an expert 96 / 98 /
+// 104 / 144 against 84 / 113 / 145 / 251; 1 of 32, 2048 x 2048, FP4, 66 / 71 / 73 / 98 against 59 / 72 / 79 /
+// 146.  Few experts: 2 of 8, 1024 x 768, FP4, at 4 / 8 / 16 pairs 21 / 21 / 29 against 19 / 23 / 37; 2 of 4,
+// 2048 x 2048, NF4, 47 / 47 / 50 against 29 / 46 / 75; one expert of 2048 x 4096, INT4, 48 / 49 / 49 against
+// 25 / 37 / 60.
+static bool moe_wide(int64_t pairs, int64_t experts, int64_t hidden) {
+  const bool fills = 4 * (hidden / 128) * experts >= 3 * device_cu_count();
+  return pairs >= (fills ? 3 : 8) * experts;
+}
+
+// The planes of h (three bf16 values per pair and row), the partial results, the sorted pairs and the
+// experts' first positions among them.
+size_t moe_workspace(int64_t pairs, int64_t hidden, int64_t inter, int64_t experts) {
+  return align256((size_t)pairs * (size_t)inter * 6) + align256((size_t)pairs * (size_t)hidden * 4) +
+         align256((size_t)pairs * 4) + ((size_t)experts + 1) * 4;
 }
 
 hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const float* weights,
@@ -209,6 +269,20 @@ hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const floa
   const int64_t pairs = tokens * top_k;
   const int weight = fmt_weight(fmt);
   MoeArgs a{};
+  auto combine = [&]() {
+    hipLaunchKernelGGL(combine_kernel, dim3((unsigned)((hidden + 255) / 256), (unsigned)tokens), dim3(256), 0, s,
+                       a.part, ids, weights, (uint32_t)hidden, (uint32_t)experts, (uint32_t)top_k, y);
+    return hipGetLastError();
+  };
+  // the second product's operands
+  auto turn_down = [&]() {
+    a.packed = down;
+    a.scales = down_scales;
+    a.x = a.h;
+    a.n = (uint32_t)hidden;
+    a.k = (uint32_t)inter;
+    a.tiles = (uint32_t)(hidden / 16);
+  };
   a.ids = ids;
   a.h = reinterpret_cast<uint16_t*>(ws);
   a.part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + align256((size_t)pairs * (size_t)inter * 6));
@@ -227,27 +301,45 @@ hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const floa
   // 8 / 12 / 16 / 32 tokens 18.2 / 26.8 / 45.8 / 63.6 / 77.6 / 143.7 against 24.3 / 32.2 / 48.7 / 66.2 / 77.4 /
   // 86.5; 4 of 64, 1536 x 1408, INT4, at 4 / 8 / 12 / 16 tokens 23.1 / 35.5 / 51.4 / 63.1 against 30.0 /
   // 41.3 / 52.2 / 59.5.
-  if (tokens == 1 || pairs < experts) {
-    const int least = top_k > 4 ? 1 : top_k > 2 ? 2 : top_k > 1 ? 4 : 8;  // no wave without a slot
-    // up: K ranges until the waves number two per SIMD
+  // One slot a token pays up to half as many pairs as experts: 1 of 32, 2048 x 2048, FP4, at 12 / 16 / 24 tokens
+  // 33.1 / 42.6 / 60.0 against 38.4 / 43.2 / 44.7; 1 of 64, 1024 x 1024, INT4, at 24 / 32 / 48 25.9 / 32.4 / 45.0
+  // against 30.2 / 31.0 / 31.5.
+  if (tokens == 1 || (pairs < experts && (top_k > 1 || 2 * pairs <= experts))) {
+    const int least = top_k > 4 ? 1 : top_k > 2 ? 2 : top_k > 1 ? 4 : 8;  // no wave without a slot ...
+    // ... or without a quad (1 token, 2 of 8, 512 x 256, NF4: 9.2 against 10.2); up: then K ranges until the waves
+    // number two per SIMD
     const int64_t units = inter / 16 * pairs;
     int kw = least;
+    while (kw > 1 && kw > (hidden + 255) / 256) kw /= 2;
     while (kw < 8 && 2 * kw <= (hidden + 255) / 256 && units * kw < 8 * device_cu_count()) kw *= 2;
     a.qpk = (uint32_t)(((hidden + 255) / 256 + kw - 1) / kw);
     hipError_t e = fmt_xtype(fmt) == kF16 ? launch_moe_pair_f16(weight, kw, a, (uint32_t)tokens, s)
                                           : launch_moe_pair_bf16(weight, kw, a, (uint32_t)tokens, s);
     if (e != hipSuccess) return e;
-    a.packed = down;
-    a.scales = down_scales;
-    a.x = a.h;
-    a.n = (uint32_t)hidden;
-    a.k = (uint32_t)inter;
-    a.tiles = (uint32_t)(hidden / 16);
+    turn_down();
     a.weights = weights;
     a.y = y;
     kw = least;
+    while (kw > 1 && kw > (inter + 255) / 256) kw /= 2;
     a.qpk = (uint32_t)(((inter + 255) / 256 + kw - 1) / kw);
     return launch_moe_token(weight, kw, a, (uint32_t)tokens, s);
+  }
+  if (moe_wide(pairs, experts, hidden)) {
+    char* at = reinterpret_cast<char*>(a.part) + align256((size_t)pairs * (size_t)hidden * 4);
+    int32_t* order = reinterpret_cast<int32_t*>(at);
+    int32_t* start = reinterpret_cast<int32_t*>(at + align256((size_t)pairs * 4));
+    hipLaunchKernelGGL(order_kernel, dim3((unsigned)experts + 1), dim3(kOrderThreads), 0, s, ids, (uint32_t)pairs,
+                       (uint32_t)experts, order, start);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.order = order;
+    a.start = start;
+    e = launch_moe_wide_up(weight, fmt_xtype(fmt), a, s);
+    if (e != hipSuccess) return e;
+    turn_down();
+    e = launch_moe_wide_down(weight, a, s);
+    if (e != hipSuccess) return e;
+    return combine();
   }
   uint32_t cols = (uint32_t)std::min<int64_t>(16, tokens);
   int kw = moe_kw(a.tiles, experts, hidden, cols);
@@ -257,12 +349,7 @@ hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const floa
                                         : launch_moe_up_bf16(weight, kw, a, s);
   if (e != hipSuccess) return e;
 
-  a.packed = down;
-  a.scales = down_scales;
-  a.x = a.h;
-  a.n = (uint32_t)hidden;
-  a.k = (uint32_t)inter;
-  a.tiles = (uint32_t)(hidden / 16);
+  turn_down();
   const int tiles = pairs <= 2 * experts ? 1 : 3;
   cols = (uint32_t)std::min<int64_t>(tiles == 1 ? kMoePacked : 16, tokens);
   kw = moe_kw(a.tiles, experts, inter, 3 * cols);
@@ -270,9 +357,7 @@ hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const floa
   e = launch_moe_down(weight, kw, tiles, a, s);
   if (e != hipSuccess) return e;
 
-  hipLaunchKernelGGL(combine_kernel, dim3((unsigned)((hidden + 255) / 256), (unsigned)tokens), dim3(256), 0,
-                     s, a.part, ids, weights, (uint32_t)hidden, (uint32_t)experts, (uint32_t)top_k, y);
-  return hipGetLastError();
+  return combine();
 }
 
 }  // namespace w4

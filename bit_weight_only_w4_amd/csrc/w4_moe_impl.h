@@ -10,7 +10,8 @@
 // a wave takes one pair (moe_pair_kernel, moe_token_kernel).  With more, the pairs of an expert share its
 // weights: grid.y is the expert, whose workgroups end at once if no pair has it.  Every wave finds
 // its expert's pairs itself, 64 ids at a time (a ballot, and a lane permutation that hands the r-th
-// pair to lane r): no launch, memory or barrier for a sorted list.
+// pair to lane r): no launch, memory or barrier for a sorted list.  With
+// several pairs an expert, the kernels of w4_moe_wide_impl.h take over.
 //
 // Inside a workgroup 8 waves are RT row tiles (16 weight rows each) x KW K groups; the tiles of the
 // up direction alternate between a gate tile and the up tile of the same rows.  K runs in quads (256
@@ -51,7 +52,7 @@ constexpr float kNf4Factor = 1.4376f;
 
 // NF4's byte -> decoded pair table: 16 copies of each 8-byte entry (first terms, second terms), lane L
 // reading copy L % 16.
-template <int XT>
+template <int XT, int THREADS = kMoeThreads>
 __device__ inline void fill_moe_table(uint32_t* tab) {
   const float c = __uint_as_float(codes_in_lanes<kNF4>()) * kNf4Factor;
   uint32_t v1, v2;
@@ -68,8 +69,8 @@ __device__ inline void fill_moe_table(uint32_t* tab) {
   const uint32_t lo1 = (uint32_t)__shfl((int)v1, (tid >> 3) & 15) << 16;
   const uint32_t lo2 = (uint32_t)__shfl((int)v2, (tid >> 3) & 15) << 16;
 #pragma unroll
-  for (int j = 0; j < kTableBytes / 16 / kMoeThreads; ++j) {
-    const int i = tid + kMoeThreads * j;
+  for (int j = 0; j < kTableBytes / 16 / THREADS; ++j) {
+    const int i = tid + THREADS * j;
     const int hi = __builtin_amdgcn_readfirstlane(i >> 7);
     const uint32_t p1 = (uint32_t)__builtin_amdgcn_readlane((int)v1, hi) | lo1;
     const uint32_t p2 = (uint32_t)__builtin_amdgcn_readlane((int)v2, hi) | lo2;
@@ -172,6 +173,50 @@ struct MoeScales {
   uint32_t v[kRaw];
 };
 
+// A quad's dwords as the B operands of its steps: wb[block][step] holds 8 weights of row m, k order inside a
+// block permuted as the activations' pieces are read.
+template <int FMT>
+__device__ __attribute__((always_inline)) inline void quad_steps(
+    const MoeQuad& d, uint32_t (&wb)[is_g128(FMT) ? 2 : 4][is_g128(FMT) ? 4 : 2]) {
+  constexpr uint32_t QC = is_g128(FMT) ? 2 : 4;
+  constexpr int STEPS = is_g128(FMT) ? 4 : 2;
+  constexpr bool kMX = FMT == kMXFP4;
+  // chunks g and g + 4 of row m: lanes m < 8 hold (row m, g) in load 0 and need (row m, g + 4) of
+  // lane m + 8; lanes m >= 8 hold (row m, g + 4) in load 1 and need (row m, g) of lane m - 8
+  uint32_t wh[2][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    wh[0][i] = (uint32_t)__builtin_amdgcn_update_dpp((int)d.w[0][i], (int)d.w[1][i], 0x118, 0xF, 0xC, false);
+    wh[1][i] = (uint32_t)__builtin_amdgcn_update_dpp((int)d.w[1][i], (int)d.w[0][i], 0x108, 0xF, 0x3, false);
+  }
+  if constexpr (is_g128(FMT)) {
+#pragma unroll
+    for (int c = 0; c < (int)QC; ++c)
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) wb[c][s] = wh[c][s];
+  } else {
+    // 64-weight blocks: chunks 2 c, 2 c + 1 of the half quad to every lane group, two dwords
+    // each; MXFP4: one more swap gives step s the dwords of the 32-weight block s.
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const auto s0 = __builtin_amdgcn_permlane32_swap(wh[h][0], wh[h][2], false, false);
+      const auto s1 = __builtin_amdgcn_permlane32_swap(wh[h][1], wh[h][3], false, false);
+      wb[2 * h][0] = s0[0];
+      wb[2 * h][1] = s1[0];
+      wb[2 * h + 1][0] = s0[1];
+      wb[2 * h + 1][1] = s1[1];
+    }
+    if constexpr (kMX) {
+#pragma unroll
+      for (int c = 0; c < (int)QC; ++c) {
+        const auto t = __builtin_amdgcn_permlane16_swap(wb[c][0], wb[c][1], false, false);
+        wb[c][0] = t[0];
+        wb[c][1] = t[1];
+      }
+    }
+  }
+}
+
 // acc += the product of the quad held in d (B) and 256 k of the window (A).  The quad is the jw-th of the
 // scales' eight, ODD its parity; `left` is the bytes of its row's scales that lie inside K; its first piece of A row r
 // of column tile t stands at wbase + arow[t].
@@ -209,40 +254,8 @@ __device__ __attribute__((always_inline)) inline void quad_product(
     ap[t] = apiece[t];
     asm volatile("" : "+v"(ap[t]));
   }
-  // chunks g and g + 4 of row m: lanes m < 8 hold (row m, g) in load 0 and need (row m, g + 4) of
-  // lane m + 8; lanes m >= 8 hold (row m, g + 4) in load 1 and need (row m, g) of lane m - 8
-  uint32_t wh[2][4], wb[QC][STEPS];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    wh[0][i] = (uint32_t)__builtin_amdgcn_update_dpp((int)d.w[0][i], (int)d.w[1][i], 0x118, 0xF, 0xC, false);
-    wh[1][i] = (uint32_t)__builtin_amdgcn_update_dpp((int)d.w[1][i], (int)d.w[0][i], 0x108, 0xF, 0x3, false);
-  }
-  if constexpr (is_g128(FMT)) {
-#pragma unroll
-    for (int c = 0; c < (int)QC; ++c)
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s) wb[c][s] = wh[c][s];
-  } else {
-    // 64-weight blocks: chunks 2 c, 2 c + 1 of the half quad to every lane group, two dwords
-    // each; MXFP4: one more swap gives step s the dwords of the 32-weight block s.
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const auto s0 = __builtin_amdgcn_permlane32_swap(wh[h][0], wh[h][2], false, false);
-      const auto s1 = __builtin_amdgcn_permlane32_swap(wh[h][1], wh[h][3], false, false);
-      wb[2 * h][0] = s0[0];
-      wb[2 * h][1] = s1[0];
-      wb[2 * h + 1][0] = s0[1];
-      wb[2 * h + 1][1] = s1[1];
-    }
-    if constexpr (kMX) {
-#pragma unroll
-      for (int c = 0; c < (int)QC; ++c) {
-        const auto t = __builtin_amdgcn_permlane16_swap(wb[c][0], wb[c][1], false, false);
-        wb[c][0] = t[0];
-        wb[c][1] = t[1];
-      }
-    }
-  }
+  uint32_t wb[QC][STEPS];
+  quad_steps<FMT>(d, wb);
 #pragma unroll
   for (int c = 0; c < (int)QC; ++c) {
     float4_t dd[NT];

@@ -2,6 +2,7 @@
 import numpy as np
 import pytest
 
+import oracle
 import synth_inputs
 from tests import gpu_util as g
 from tests import moe_util as mu
@@ -256,3 +257,206 @@ def test_router_and_layer_together_match_the_plain_layer():
                dp.view(experts, hidden, -1), ds.view(experts, hidden, -1), fmt)
     c["ids"], c["weights"] = ids.cpu().numpy(), w.cpu().numpy()
     mu.check(y, c)
+
+
+# ---- every way of launching the products: a wave per pair, shared products with K groups, many tokens
+
+LAUNCHES = [(7, 128, 128, 8, 1), (4, 128, 192, 8, 2), (3, 192, 128, 7, 2),    # around as many pairs as experts
+            (16, 320, 128, 3, 1), (9, 128, 320, 4, 3),                         # K groups, up to 8 pairs an expert
+            (20, 384, 256, 4, 2), (96, 128, 128, 192, 6), (130, 256, 192, 3, 2)]  # many tokens
+
+
+@pytest.mark.parametrize("fmt", ["nf4_bf16", "int4_f16", "fp4_bf16", "int4a_bf16", "mxfp4_f16"])
+@pytest.mark.parametrize("tokens,hidden,inter,experts,top_k", LAUNCHES)
+def test_launches(fmt, tokens, hidden, inter, experts, top_k):
+    if fmt.startswith("int4"):
+        hidden, inter = (hidden + 127) // 128 * 128, (inter + 127) // 128 * 128
+    c = mu.case(fmt, tokens, hidden, inter, experts, top_k, seed=tokens + experts)
+    mu.check(_run(c), c)
+
+
+@pytest.mark.parametrize("fmt", ["nf4_f16", "int4_bf16", "int4a_f16", "mxfp4_bf16", "fp4_f16"])
+@pytest.mark.parametrize("tokens,hidden,inter,experts,top_k", [
+    (1, 16768, 128, 2, 2),   # a wave's window of the up product more than once
+    (1, 128, 1664, 6, 5),    # and of the down product
+    (16, 4224, 128, 4, 1), (16, 128, 4224, 4, 1),   # windows that waves share
+    (5, 4224, 2432, 2, 1),
+    (40, 2432, 4224, 2, 1), (70, 4224, 640, 1, 1)])  # scale windows, odd numbers of quads
+def test_long_rows(fmt, tokens, hidden, inter, experts, top_k):
+    c = mu.case(fmt, tokens, hidden, inter, experts, top_k, seed=tokens + hidden)
+    mu.check(_run(c), c)
+
+
+@pytest.mark.parametrize("tokens,experts,top_k", [(2, 40, 16), (1, 1, 16), (9, 1, 1), (3, 1024, 2), (300, 1024, 4),
+                                                  (900, 1024, 4)])
+def test_most_slots_and_experts(tokens, experts, top_k):
+    c = mu.case("mxfp4_bf16", tokens, 64, 64, experts, top_k, seed=experts + tokens)
+    mu.check(_run(c), c)
+
+
+@pytest.mark.parametrize("tokens,experts,top_k", [(1, 4, 2), (8, 4, 2), (40, 4, 2)])
+def test_nan_scale_bytes_reach_their_rows_alone(tokens, experts, top_k):
+    """A scale byte of 255 in a down row makes that output NaN for the tokens of its expert; in a gate or up row
+    it makes that h NaN, and with it every output of its expert's tokens."""
+    import torch
+
+    import bit_weight_only_w4_amd as w4
+
+    c = mu.case("mxfp4_bf16", tokens, 320, 192, experts, top_k, seed=6)
+    has = (c["ids"] == 2).any(1)
+    if not has.any():
+        c["ids"][0, 0], has[0] = 2, True
+    args = list(mu.to_device(c, g.device()))
+    clean = w4.moe(*args)
+    scales = args[6].clone()
+    scales[2, 77, 5] = 255
+    y = w4.moe(*args[:6], scales, args[7])
+    want = torch.zeros_like(y, dtype=torch.bool)
+    want[torch.from_numpy(has).to(y.device), 77] = True
+    assert torch.equal(torch.isnan(y), want) and torch.equal(y[~want], clean[~want])
+    for row in (33, 192 + 60):
+        scales = args[4].clone()
+        scales[2, row, 9] = 255
+        y = w4.moe(*args[:4], scales, *args[5:])
+        want = torch.from_numpy(has).to(y.device)
+        assert torch.isnan(y[want]).all() and torch.equal(y[~want], clean[~want])
+
+
+@pytest.mark.parametrize("tokens", [2, 12, 60])
+def test_operands_off_by_one_element(tokens):
+    """ids, weights, scales and y need 4-byte alignment alone; what lies around y stays."""
+    import torch
+
+    import bit_weight_only_w4_amd as w4
+
+    for fmt in ("mxfp4_f16", "nf4_bf16"):
+        c = mu.case(fmt, tokens, 192, 128, 6, 2, seed=7)
+        args = list(mu.to_device(c, g.device()))
+
+        def shifted(t):
+            n = 4 // t.element_size()
+            buf = torch.empty(t.numel() + n, dtype=t.dtype, device=t.device)
+            buf[n:] = t.reshape(-1)
+            return buf[n:].view(t.shape)
+
+        want = w4.moe(*args)
+        for i in (1, 2, 4, 6):
+            args[i] = shifted(args[i])
+        buf = torch.full((tokens * 192 + 2,), 3.0, device=g.device())
+        w4.moe(*args, y=buf[1:-1].view(tokens, 192))
+        assert torch.equal(buf[1:-1].view(tokens, 192), want)
+        assert float(buf[0]) == 3.0 and float(buf[-1]) == 3.0
+
+
+@pytest.mark.parametrize("tokens", [4, 60])
+def test_two_streams_at_once(tokens):
+    import torch
+
+    import bit_weight_only_w4_amd as w4
+
+    cases = [mu.case("int4_bf16", tokens, 256, 256, 6, 2, seed=s) for s in (1, 2)]
+    args = [mu.to_device(c, g.device()) for c in cases]
+    want = [w4.moe(*a) for a in args]
+    size = w4.moe_workspace_bytes("int4_bf16", tokens, 256, 256, 6, 2)
+    ws = [torch.empty(size, dtype=torch.uint8, device=g.device()) for _ in args]
+    ys = [torch.empty_like(w) for w in want]
+    streams = [torch.cuda.Stream() for _ in args]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for a, y, b, s in zip(args, ys, ws, streams):
+            w4.moe(*a, y=y, workspace=b, stream=s)
+    torch.cuda.synchronize()
+    for y, w in zip(ys, want):
+        assert torch.equal(y, w)
+
+
+@pytest.mark.parametrize("fmt", ["int4a_f16", "mxfp4_bf16"])
+def test_capture_of_many_tokens(fmt):
+    """The sorted pairs are made anew by every replay."""
+    import torch
+
+    import bit_weight_only_w4_amd as w4
+
+    dev = g.device()
+    tokens, hidden, inter, experts, top_k = 70, 256, 128, 5, 2
+    c = mu.case(fmt, tokens, hidden, inter, experts, top_k, seed=4)
+    args = list(mu.to_device(c, dev))
+    out = torch.empty(tokens, hidden, device=dev)
+    ws = torch.empty(w4.moe_workspace_bytes(fmt, tokens, hidden, inter, experts, top_k), dtype=torch.uint8, device=dev)
+    w4.moe(*args, y=out, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        w4.moe(*args, y=out, workspace=ws)
+    rng = np.random.default_rng(3)
+    for i in range(4):
+        c["ids"] = rng.integers(-1, experts + 1 if i % 2 else 2, size=(tokens, top_k)).astype(np.int32)
+        args[1].copy_(torch.from_numpy(c["ids"]))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(w4.moe(*args), out), i
+        mu.check(out, c)
+
+
+def test_experts_past_4_gib():
+    """The last expert of weights that pass 32-bit offsets."""
+    import torch
+
+    import bit_weight_only_w4_amd as w4
+
+    dev = g.device()
+    experts, hidden, inter = 1024, 2304, 2048
+    gen = torch.Generator(device=dev).manual_seed(1)
+
+    def matrix(n, k):
+        p = torch.randint(0, 256, (experts, n, k // 2), dtype=torch.uint8, device=dev, generator=gen)
+        s = torch.randint(0x3C00, 0x3C80, (experts, n, k // 128), dtype=torch.int16, device=dev, generator=gen)
+        return p, s
+
+    gu, dn = matrix(2 * inter, hidden), matrix(hidden, inter)
+    assert gu[0].numel() > 2 ** 32
+    last = []
+    for p, sc in (gu, dn):
+        p, sc = p[-1].cpu().numpy(), sc[-1].cpu().numpy().view(np.uint16)
+        hat = oracle.dequant("int4", p, sc)
+        mag = hat + 48 * np.repeat(oracle.bf16_bits_to_f64(sc), 128, axis=1)
+        last.append((None, None, hat[None], mag[None]))
+    for tokens in (1, 3500):
+        x = (torch.randn(tokens, hidden, device=dev, generator=gen) / 16).half()
+        ids = torch.full((tokens, 1), experts - 1, dtype=torch.int32, device=dev)
+        weights = torch.rand(tokens, 1, device=dev, generator=gen)
+        y = w4.moe(x, ids, weights, *gu, *dn, "int4_f16")
+        rows = [0, tokens // 2, tokens - 1]
+        mu.check(y[rows], dict(fmt="int4_f16", x=x[rows].cpu().numpy().view(np.uint16), ids=np.zeros((3, 1), np.int32),
+                               weights=weights[rows].cpu().numpy(), gu=last[0], dn=last[1]))
+
+
+def test_refusals_of_device_tensors():
+    import torch
+
+    import bit_weight_only_w4_amd as w4
+
+    args = list(mu.to_device(mu.case("fp4_f16", 4, 128, 64, 4, 2, seed=1), g.device()))
+    wrong = {0: [args[0].t().contiguous().t(), args[0].bfloat16(), args[0][:3], args[0][:, :64].contiguous()],
+             1: [args[1].long(), args[1].t().contiguous().t(), args[1][:2]],
+             2: [args[2].half(), args[2][:, :1]],
+             3: [args[3][:, :64], args[3].view(torch.int8), args[3][0]],
+             4: [args[4][:, :, :1], args[4].double()],
+             5: [args[5][:3], args[5].transpose(1, 2)],
+             6: [args[6][:3]]}
+    for i, bad in wrong.items():
+        for b in bad:
+            with pytest.raises((ValueError, TypeError, w4.W4Error)):
+                w4.moe(*args[:i], b, *args[i + 1:])
+    for y in (torch.empty(4, 64, device=g.device()), torch.empty(4, 128, device=g.device()).half(),
+              torch.empty(4, 128)):
+        with pytest.raises((ValueError, TypeError, w4.W4Error)):
+            w4.moe(*args, y=y)
+    with pytest.raises((ValueError, TypeError, w4.W4Error)):
+        w4.moe(*args, workspace=torch.empty(64, dtype=torch.uint8, device=g.device()))
+    with pytest.raises((ValueError, TypeError, w4.W4Error)):
+        w4.moe(*args, y=args[0].view(torch.float32))  # x itself: too small, and the wrong shape
+    big = torch.zeros(4 * 128 * 4 + 4 * 128 * 2, dtype=torch.uint8, device=g.device())
+    x = big[:4 * 128 * 2].view(torch.float16).view(4, 128)
+    y = big[512:512 + 4 * 128 * 4].view(torch.float32).view(4, 128)
+    with pytest.raises((ValueError, TypeError, w4.W4Error)):
+        w4.moe(x, *args[1:], y=y)  # y over x
