@@ -7,16 +7,19 @@
 // chunk's activations one quad (256 k) at a time, in two LDS buffers: while one is multiplied, the next
 // quad is in registers on its way into the other, and one barrier a quad suffices.  Two or three
 // workgroups fit a CU, whose waves compute while the others' wait.
-//   * Integer codes decode as q + 16.  The offset's part, sum(x) of a block, comes from one MFMA with a
-//     matrix of ones, which both row tiles share: acc += scale * (D - (16 + z) sum(x)).
+//   * Integer codes decode as q + 16, and an MFMA with a column of -(16 + z) takes the offset off inside each
+//     step, so that sums keep the size of the result's terms.  (Taken off a block at a time, by one MFMA with
+//     ones for both tiles, the layer's error at 150 tokens, 1920 x 2432, INT4A, was 1.5e-6 of the largest output
+//     against 5.1e-7, for 73 us against 77.)
 //   * Down: the three planes of a column are summands of one value, so their MFMAs add to the same
-//     sums (a plane as a column tile of its own: 162 against 143 us at the size below).
+//     sums (a plane as a column tile of its own: 162 against 143 us
+//     for 512 tokens, 4 of 64 experts, 1536 x 1408, INT4).
 //   * Weights keep to the caches' ordinary policy: several chunks read them (173 against 163 us with the
 //     streaming hint).
 //   * The pairs come sorted by expert (order_kernel); a chunk's columns are cut to what it has, in
 //     tiles of 16.
-// Measured on MI355X, 512 tokens, 4 of 64 experts, 1536 x 1408, INT4: up 69 us (256 TFLOP/s), down 82 us
-// (108 TFLOP/s of the layer's, 325 with the planes).  Bound by waiting, not by the matrix units: the
+// Measured on MI355X, 512 tokens, 6 of 64 experts, 1536 x 1408, FP4: up 73 us (365 TFLOP/s), down 117 us
+// (114 TFLOP/s of the layer's, 341 with the planes).  Bound by waiting, not by the matrix units: the
 // registers of two row tiles in flight leave a SIMD two waves, which do not cover LDS and barrier
 // latencies.
 #pragma once
@@ -68,12 +71,19 @@ __device__ __attribute__((always_inline)) inline void wide_product(
   }
 #pragma unroll
   for (int c = 0; c < (int)QC; ++c) {
-    float4_t dd[2][NT], xs[NT];
+    float4_t dd[2][NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      xs[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int r = 0; r < 2; ++r) dd[r][t] = float4_t{0.f, 0.f, 0.f, 0.f};
+    uint4 zcol[2];
+    if constexpr (kInt) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float zn = FMT == kINT4 ? -24.0f : -16.0f - (float)((sw[r][c % Sc::kPer] >> 16) & 15u);
+        const uint32_t h = XT == kF16 ? f16_bits(zn) : (__float_as_uint(zn) >> 16);
+        zcol[r] = make_uint4(h | (h << 16), h | (h << 16), h | (h << 16), h | (h << 16));
+      }
     }
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
@@ -108,14 +118,8 @@ __device__ __attribute__((always_inline)) inline void wide_product(
           for (int p = 0; p < NP; ++p) {
             dd[r][t] = mfma<XT>(xv[t][p], b1, dd[r][t]);
             if constexpr (kTable) dd[r][t] = mfma<XT>(xv[t][p], b2, dd[r][t]);
+            if constexpr (kInt) dd[r][t] = mfma<XT>(xv[t][p], zcol[r], dd[r][t]);
           }
-      }
-      if constexpr (kInt) {
-        constexpr uint32_t kOne = XT == kF16 ? 0x3C003C00u : 0x3F803F80u;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int p = 0; p < NP; ++p) xs[t] = mfma<XT>(xv[t][p], make_uint4(kOne, kOne, kOne, kOne), xs[t]);
       }
       if constexpr (kMX) {
 #pragma unroll
@@ -137,14 +141,10 @@ __device__ __attribute__((always_inline)) inline void wide_product(
         const float sc = __uint_as_float(FMT == kINT4    ? (c == 0 ? sw[r][0] << 16 : sw[r][0] & 0xFFFF0000u)
                                          : FMT == kINT4A ? sw[r][c % Sc::kPer] << 16
                                                          : sw[r][c % Sc::kPer]);
-        const float zn = FMT == kINT4 ? -24.0f : -16.0f - (float)((sw[r][c % Sc::kPer] >> 16) & 15u);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float v = kInt ? __builtin_fmaf(xs[t][i], zn, dd[r][t][i]) : dd[r][t][i];
-            acc[r][t][i] = __builtin_fmaf(v, sc, acc[r][t][i]);
-          }
+          for (int i = 0; i < 4; ++i) acc[r][t][i] = __builtin_fmaf(dd[r][t][i], sc, acc[r][t][i]);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
