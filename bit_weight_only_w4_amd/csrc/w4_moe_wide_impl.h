@@ -27,12 +27,6 @@
 
 #include "w4_moe_impl.h"
 
-#ifndef WEXTRA
-#define WEXTRA 1
-#endif
-#ifndef WDOWN
-#define WDOWN 2
-#endif
 namespace w4 {
 namespace {
 
