@@ -87,17 +87,22 @@ bool plan_slice(const int64_t* ns, int groups, int64_t k, int64_t b, int t, int 
   return true;
 }
 
-// Batch tiles per slice: the largest T (8, 4, 2, 1; at most what B needs) whose launch has at
+// MXFP4's scaling step by step leaves no registers for eight batch tiles (28672 x 8192 at B = 128: 715 us with
+// their spills, 161 in two slices of four).
+int most_tiles(int fmt) { return fmt_weight(fmt) == kMXFP4 ? 4 : kMaxTiles; }
+
+// Batch tiles per slice: the largest T (8, 4, 2, 1; at most `most` and what B needs) whose launch has at
 // least half a row tile per CU; slices beyond the first re-read the weights (mostly from L2).
 // Offsets are 32-bit: a slice's activations (16 T K 2 bytes) and K itself are bounded below.
-bool plan_mfma(const int64_t* ns, int groups, int64_t k, int64_t b, int splits, MfmaPlan* out) {
+bool plan_mfma(const int64_t* ns, int groups, int64_t k, int64_t b, int splits, int most,
+               MfmaPlan* out) {
   int64_t n_total = 0;
   for (int g = 0; g < groups; ++g) n_total += ns[g];
   if (b < 1 || b > W4_MAX_BATCH || k >= ((int64_t)1 << 22) || n_total >= ((int64_t)1 << 31) ||
       16 * kMaxTiles * k * 2 >= ((int64_t)1 << 31))
     return false;
   const int64_t cus = device_cu_count();
-  const int need = (int)std::min<int64_t>((b + 15) / 16, kMaxTiles);
+  const int need = (int)std::min<int64_t>((b + 15) / 16, most);
   const int tmax = need <= 1 ? 1 : need <= 2 ? 2 : need <= 4 ? 4 : 8;
   bool found = false;
   MfmaPlan best{};
@@ -126,7 +131,7 @@ hipError_t launch_mfma_members(int fmt, const uint16_t* x, int groups, const uin
   if (splits > 1 && (groups != 1 || ws == nullptr)) return hipErrorInvalidValue;
   if (splits > 1 && b * ns[0] >= ((int64_t)1 << 32)) return hipErrorNotSupported;  // 32-bit planes
   MfmaPlan p;
-  if (!plan_mfma(ns, groups, k, b, splits, &p)) return hipErrorNotSupported;
+  if (!plan_mfma(ns, groups, k, b, splits, most_tiles(fmt), &p)) return hipErrorNotSupported;
   MfmaArgs a;
   memset(&a, 0, sizeof(a));
   const int64_t rows = 16 * (8 / p.kw);
@@ -179,7 +184,7 @@ hipError_t launch_mfma(int fmt, const uint16_t* x, const uint8_t* packed, const 
 int mfma_splits_used(int64_t n, int64_t k, int64_t b, int splits) {
   if (splits <= 1) return 1;
   MfmaPlan p;
-  if (!plan_mfma(&n, 1, k, b, splits, &p)) return 0;
+  if (!plan_mfma(&n, 1, k, b, splits, kMaxTiles, &p)) return 0;
   return p.splits;
 }
 

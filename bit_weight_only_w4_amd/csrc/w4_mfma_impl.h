@@ -100,8 +100,8 @@ template <int FMT>
 struct Quad {
   static constexpr int QC = is_g128(FMT) ? 2 : 4;  // scale blocks per quad
   uint32_t w[2][4];
-  uint32_t s[QC];  // fp32 bits (INT4: bf16 bits in the low half; INT4A: its word; MXFP4: the
-                   // block pair's two E8M0 bytes)
+  uint32_t s[QC];  // fp32 bits (INT4: bf16 bits in the low half; INT4A: its word; MXFP4: the three
+                   // dwords that hold the quad's eight E8M0 bytes, and in a group Cursor::odd)
 };
 
 // The four E2M1 pairs of a packed dword in memory order (high nibble first) as 16-bit pairs.  The
@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, min_waves(T)) mfma_kernel(MfmaArgs a
   struct Cursor {
     int ti, q;
     __amdgpu_buffer_rsrc_t rw, rs;
+    uint32_t odd;  // MXFP4: 2 where the scales start inside a dword (rs then starts at that dword)
   };
   // The member that owns global tile t (uniform), by selects over the fixed member slots so that
   // the argument block is never indexed dynamically.
@@ -198,7 +199,13 @@ __global__ void __launch_bounds__(kThreads, min_waves(T)) mfma_kernel(MfmaArgs a
     const uint32_t rows_left = c.ti < ntiles && row_base < mm.n ? mm.n - row_base : 0u;
     const uint32_t rows = rows_left >= 16u ? 16u : rows_left;
     c.rw = make_rsrc(mm.packed + (size_t)row_base * pitch, rows * pitch);
-    c.rs = make_rsrc(reinterpret_cast<const char*>(mm.scales) + (size_t)row_base * spitch, rows * spitch);
+    const char* sp = reinterpret_cast<const char*>(mm.scales) + (size_t)row_base * spitch;
+    if constexpr (kMX) {  // whole dwords
+      c.odd = (uint32_t)(reinterpret_cast<uintptr_t>(sp) & 2u);
+      c.rs = make_rsrc(sp - c.odd, (rows * spitch + c.odd + 3u) & ~3u);
+    } else {
+      c.rs = make_rsrc(sp, rows * spitch);
+    }
   };
   // The resources change only at a new tile (a uniform branch).
   auto advance = [&](Cursor& c) __attribute__((always_inline)) {
@@ -230,8 +237,17 @@ __global__ void __launch_bounds__(kThreads, min_waves(T)) mfma_kernel(MfmaArgs a
     // 16-byte load; of a quad that ends past K, the blocks past K are zeroed when the quad is
     // multiplied (inside the matrix their bytes are the next row's; zeroing them here would make
     // the loop wait for the load).  INT4: two bf16 scales, 2-byte aligned, two loads, moved to the
-    // high half when multiplied (for the same reason).
-    if constexpr (!is_g128(FMT) && !kMX) {
+    // high half when multiplied (for the same reason).  MXFP4: eight bytes, 2-byte aligned, as the
+    // three dwords around them in one load (28672 x 8192, B = 8 / 16 / 32: 45 / 50 / 64 us; four 2-byte
+    // loads, which touch the same 16 lines each, 60 / 77 / 66).
+    if constexpr (kMX) {
+      const uint32_t off = offset_or_oob(qb < nblocks, (sbase + cur.odd) & ~3u);
+      const auto sv = __builtin_amdgcn_raw_buffer_load_b96(cur.rs, (int)off, 0, 0);
+      d.s[0] = sv[0];
+      d.s[1] = sv[1];
+      d.s[2] = sv[2];
+      if constexpr (GROUPED) d.s[3] = cur.odd;
+    } else if constexpr (!is_g128(FMT)) {
       const uint4 sv = buffer_load16(cur.rs, offset_or_oob(qb < nblocks, sbase));
       d.s[0] = sv.x;
       d.s[1] = sv.y;
@@ -364,6 +380,21 @@ __global__ void __launch_bounds__(kThreads, min_waves(T)) mfma_kernel(MfmaArgs a
         for (int s = 0; s < STEPS; ++s) wb[c][s] = wh[c][s];
       }
     }
+    // MXFP4: the quad's scale bytes moved into place, those of blocks past K (the next row's) zeroed.
+    uint32_t sx[2] = {0u, 0u};
+    if constexpr (kMX) {
+      const uint32_t odd = GROUPED ? d.s[3] : (uint32_t)(reinterpret_cast<uintptr_t>(a.m[0].scales) & 2u);
+      uint32_t shift = slane;  // (opaque: recomputed per quad, not held across the loop)
+      asm volatile("" : "+v"(shift));
+      shift = ((shift + odd) & 2u) * 8u;
+      sx[0] = __builtin_amdgcn_alignbit(d.s[1], d.s[0], shift);
+      sx[1] = __builtin_amdgcn_alignbit(d.s[2], d.s[1], shift);
+      const int left = (int)nblocks - (int)qb;
+      if (left < QC) {
+        sx[0] = left >= 2 ? sx[0] : left == 1 ? sx[0] & 0xFFFFu : 0u;
+        sx[1] = left == 3 ? sx[1] & 0xFFFFu : 0u;
+      }
+    }
     const uint8_t* xq = xw + (wq * kQuad + klane) * 2;
     // This lane's B rows: activation row 16 t + m of the slice, or the last one held when the
     // slice is shorter (those columns of D are never stored).  Recomputed per quad (the opaque
@@ -392,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, min_waves(T)) mfma_kernel(MfmaArgs a
       for (int s = 0; s < STEPS; ++s) {
         if constexpr (kMX) {
           const uint4 a1 = e2m1_pairs<XT>(wb[c][s]);
-          const uint32_t sraw = __float_as_uint(e8m0_value((d.s[c] >> (8 * s)) & 0xFFu));
+          const uint32_t sraw = __float_as_uint(e8m0_value((sx[c >> 1] >> (16 * (c & 1) + 8 * s)) & 0xFFu));
           const float sc[4] = {row_bcast<0>(sraw), row_bcast<1>(sraw), row_bcast<2>(sraw),
                                row_bcast<3>(sraw)};
 #pragma unroll
@@ -597,7 +628,8 @@ hipError_t dispatch_fx(int op, const MfmaArgs& a, int tiles, int kw, int lds, in
     case 1: return dispatch_t<FMT, XT, 1, GROUPED>(op, a, kw, lds, grid, slices, out, s);
     case 2: return dispatch_t<FMT, XT, 2, GROUPED>(op, a, kw, lds, grid, slices, out, s);
     case 4: return dispatch_t<FMT, XT, 4, GROUPED>(op, a, kw, lds, grid, slices, out, s);
-    case 8: return dispatch_t<FMT, XT, 8, GROUPED>(op, a, kw, lds, grid, slices, out, s);
+    case 8:
+      if constexpr (FMT != kMXFP4) return dispatch_t<FMT, XT, 8, GROUPED>(op, a, kw, lds, grid, slices, out, s);
   }
   return hipErrorInvalidValue;
 }

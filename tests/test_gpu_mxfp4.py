@@ -185,3 +185,31 @@ def test_noalloc_split(fmt):
                                              w4.FORMATS[fmt], 300, 1536, 3, vp(y.data_ptr()), 4, None) == 0
     torch.cuda.synchronize()
     _check(y, x, fmt, pr, sr)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n,k,b", [(33, 64, 16), (17, 1088, 5), (50, 320, 70), (300, 192, 2), (40, 4160, 130)])
+def test_scales_that_start_inside_a_dword(fmt, n, k, b):
+    """Rows 1 .. n of a matrix whose rows hold an odd number of scale pairs: the scales of the part start two bytes
+    into a dword.  The bytes around them are 255 and must not be used.  Alone, and in a group beside a
+    matrix whose scales start on a dword."""
+    import torch
+
+    import bit_weight_only_w4_amd as w4
+
+    assert (k // 32) % 4 == 2
+    x, xd, p, s, pr, sr = _case(fmt, n + 2, k, b, seed=n + k, spread=3)
+    clean = s.clone()
+    s[0] = 255
+    s[-1] = 255
+    part, scales = p[1:-1], s[1:-1]
+    assert scales.data_ptr() % 4 == 2
+    paths = ["mfma"] + (["gemv"] if b <= 8 else [])
+    for path in paths:
+        _check(w4.matmul_ex(xd, part, scales, fmt, path=path), x, fmt, pr[1:-1], sr[1:-1])
+    _check(w4.gemm_smallbatch(xd, part, scales, fmt), x, fmt, pr[1:-1], sr[1:-1])
+    torch.cuda.synchronize()
+    ys = w4.gemm_smallbatch_grouped(xd, [part, p, part], [scales, clean, scales], fmt)
+    _check(ys[0], x, fmt, pr[1:-1], sr[1:-1])
+    _check(ys[1], x, fmt, pr, sr)
+    _check(ys[2], x, fmt, pr[1:-1], sr[1:-1])
