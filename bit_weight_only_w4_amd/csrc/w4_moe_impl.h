@@ -175,42 +175,33 @@ struct MoeScales {
   uint32_t v[kRaw];
 };
 
-// A quad's dwords as the B operands of its steps: wb[block][step] holds 8 weights of row m, k order inside a
-// block permuted as the activations' pieces are read.
-template <int FMT>
-__device__ __attribute__((always_inline)) inline void quad_steps(
-    const MoeQuad& d, uint32_t (&wb)[is_g128(FMT) ? 2 : 4][is_g128(FMT) ? 4 : 2]) {
-  constexpr uint32_t QC = is_g128(FMT) ? 2 : 4;
-  constexpr int STEPS = is_g128(FMT) ? 4 : 2;
-  constexpr bool kMX = FMT == kMXFP4;
+// A half quad's dwords as the B operands of its steps: wb[block][step] holds 8 weights of row m, k order inside
+// a block permuted as the activations' pieces are read.
+template <int FMT, int H>
+__device__ __attribute__((always_inline)) inline void half_steps(
+    const MoeQuad& d, uint32_t (&wb)[is_g128(FMT) ? 1 : 2][is_g128(FMT) ? 4 : 2]) {
   // chunks g and g + 4 of row m: lanes m < 8 hold (row m, g) in load 0 and need (row m, g + 4) of
   // lane m + 8; lanes m >= 8 hold (row m, g + 4) in load 1 and need (row m, g) of lane m - 8
-  uint32_t wh[2][4];
+  uint32_t wh[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    wh[0][i] = (uint32_t)__builtin_amdgcn_update_dpp((int)d.w[0][i], (int)d.w[1][i], 0x118, 0xF, 0xC, false);
-    wh[1][i] = (uint32_t)__builtin_amdgcn_update_dpp((int)d.w[1][i], (int)d.w[0][i], 0x108, 0xF, 0x3, false);
-  }
+  for (int i = 0; i < 4; ++i)
+    wh[i] = H == 0 ? (uint32_t)__builtin_amdgcn_update_dpp((int)d.w[0][i], (int)d.w[1][i], 0x118, 0xF, 0xC, false)
+                   : (uint32_t)__builtin_amdgcn_update_dpp((int)d.w[1][i], (int)d.w[0][i], 0x108, 0xF, 0x3, false);
   if constexpr (is_g128(FMT)) {
 #pragma unroll
-    for (int c = 0; c < (int)QC; ++c)
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s) wb[c][s] = wh[c][s];
+    for (int s = 0; s < 4; ++s) wb[0][s] = wh[s];
   } else {
     // 64-weight blocks: chunks 2 c, 2 c + 1 of the half quad to every lane group, two dwords
     // each; MXFP4: one more swap gives step s the dwords of the 32-weight block s.
+    const auto s0 = __builtin_amdgcn_permlane32_swap(wh[0], wh[2], false, false);
+    const auto s1 = __builtin_amdgcn_permlane32_swap(wh[1], wh[3], false, false);
+    wb[0][0] = s0[0];
+    wb[0][1] = s1[0];
+    wb[1][0] = s0[1];
+    wb[1][1] = s1[1];
+    if constexpr (FMT == kMXFP4) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const auto s0 = __builtin_amdgcn_permlane32_swap(wh[h][0], wh[h][2], false, false);
-      const auto s1 = __builtin_amdgcn_permlane32_swap(wh[h][1], wh[h][3], false, false);
-      wb[2 * h][0] = s0[0];
-      wb[2 * h][1] = s1[0];
-      wb[2 * h + 1][0] = s0[1];
-      wb[2 * h + 1][1] = s1[1];
-    }
-    if constexpr (kMX) {
-#pragma unroll
-      for (int c = 0; c < (int)QC; ++c) {
+      for (int c = 0; c < 2; ++c) {
         const auto t = __builtin_amdgcn_permlane16_swap(wb[c][0], wb[c][1], false, false);
         wb[c][0] = t[0];
         wb[c][1] = t[1];
@@ -256,8 +247,13 @@ __device__ __attribute__((always_inline)) inline void quad_product(
     ap[t] = apiece[t];
     asm volatile("" : "+v"(ap[t]));
   }
-  uint32_t wb[QC][STEPS];
-  quad_steps<FMT>(d, wb);
+  uint32_t wb[QC][STEPS], half[2][QC / 2][STEPS];
+  half_steps<FMT, 0>(d, half[0]);
+  half_steps<FMT, 1>(d, half[1]);
+#pragma unroll
+  for (int c = 0; c < (int)QC; ++c)
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) wb[c][s] = half[c / (QC / 2)][c % (QC / 2)][s];
 #pragma unroll
   for (int c = 0; c < (int)QC; ++c) {
     float4_t dd[NT];

@@ -1,12 +1,14 @@
-// Expert products of many tokens (kernel template): chunks of up to 64 pairs of an expert (down: 16), its
+// Expert products of many tokens (kernel template): chunks of up to 64 pairs of an expert (down: 32), its
 // weights decoded once for all of them.
 //
 // The products, formats and decoders are those of w4_moe_impl.h.  A wave takes two row tiles (up: the
 // gate tile and the up tile of 16 rows of h; down: 32 rows), so that each piece of activations read from
 // LDS feeds two MFMAs and no sum has to leave the wave.  A workgroup's four waves share the
-// chunk's activations one quad (256 k) at a time, in two LDS buffers: while one is multiplied, the next
-// quad is in registers on its way into the other, and one barrier a quad suffices.  Two or three
-// workgroups fit a CU, whose waves compute while the others' wait.
+// chunk's activations, a quad (256 k; down: half of one) at a time, in two LDS buffers: while one is multiplied,
+// the next is in registers on its way into the other, and one barrier a buffer suffices.  Two or three
+// workgroups fit a CU, whose waves compute while the others' wait.  (Whole quads in the down product too would
+// leave a CU one workgroup with the planes of 32 pairs; halves in the up product: 206 against 178 us for 512
+// tokens, 8 of 128 experts, 2048 x 768, MXFP4.)
 //   * Integer codes decode as q + 16, and an MFMA with a column of -(16 + z) takes the offset off inside each
 //     step, so that sums keep the size of the result's terms.  (Taken off a block at a time, by one MFMA with
 //     ones for both tiles, the layer's error at 150 tokens, 1920 x 2432, INT4A, was 1.5e-6 of the largest output
@@ -18,8 +20,8 @@
 //     streaming hint).
 //   * The pairs come sorted by expert (order_kernel); a chunk's columns are cut to what it has, in
 //     tiles of 16.
-// Measured on MI355X, 512 tokens, 6 of 64 experts, 1536 x 1408, FP4: up 73 us (365 TFLOP/s), down 117 us
-// (114 TFLOP/s of the layer's, 341 with the planes).  Bound by waiting, not by the matrix units: the
+// Measured on MI355X, 512 tokens, 6 of 64 experts, 1536 x 1408, FP4: up 81 us (328 TFLOP/s), down 90 us
+// (148 TFLOP/s of the layer's, 443 with the planes).  Bound by waiting, not by the matrix units: the
 // registers of two row tiles in flight leave a SIMD two waves, which do not cover LDS and barrier
 // latencies.
 #pragma once
@@ -32,39 +34,46 @@ namespace {
 
 constexpr int kWideWaves = 4, kWideThreads = 64 * kWideWaves;
 
-// acc[r][t] += the quads of both row tiles times 256 k of the window, whose column tile t is NP planes to be
-// added up; see quad_product.
-template <int FMT, int XT, int NT, int NP, int ODD>
+// acc[r][t] += half H of the quads of both row tiles times the 128 k of the window, whose column tile t is NP
+// planes to be added up; see quad_product.
+template <int FMT, int XT, int NT, int NP, int ODD, int H>
 __device__ __attribute__((always_inline)) inline void wide_product(
     float4_t (&acc)[2][NT], const MoeQuad (&d)[2], const MoeScales<FMT> (&scales)[2], uint32_t jw, uint32_t left,
     const uint8_t* wbase, uint32_t apiece, const uint32_t* tab, int lane) {
   using Sc = MoeScales<FMT>;
   constexpr int KC = is_g128(FMT) ? 128 : 64;  // weights per block
-  constexpr uint32_t QC = 256 / KC;
+  constexpr int QH = 128 / KC;                 // blocks of a half
   constexpr int STEPS = KC / 32;
   constexpr bool kMX = FMT == kMXFP4;
   constexpr bool kTable = FMT == kNF4;
   constexpr bool kInt = is_g128(FMT);
   constexpr uint32_t SB = FMT == kINT4 || kMX ? 2 : 4;
+  constexpr int kDwords = Sc::kPer == 4 ? 2 : 1;               // of scales of a half
+  constexpr int kFirst = Sc::kPer == 1 ? 0 : H * kDwords;      // ... among the quad's
   const int m = lane & 15;
   const uint32_t laneoff = (uint32_t)m * 16u;
   const char* tabc = reinterpret_cast<const char*>(tab);
   const int from = (4 * m + (int)(jw >> 1)) * 4;
-  uint32_t sw[2][Sc::kPer], wb[2][QC][STEPS];
+  // (an opaque copy: the pieces' offsets are recomputed, an operation each, not held across the loop)
+  uint32_t ap = apiece;
+  asm volatile("" : "+v"(ap));
+  uint32_t sw[2][kDwords], wb[2][QH][STEPS];
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
 #pragma unroll
-    for (int i = 0; i < Sc::kPer; ++i)
-      sw[r][i] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)scales[r].v[ODD * Sc::kPer + i]);
-    if (left < QC * SB) {
+    for (int i = 0; i < kDwords; ++i)
+      sw[r][i] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)scales[r].v[ODD * Sc::kPer + kFirst + i]);
+    if (left < 256u / KC * SB) {
 #pragma unroll
-      for (int i = 0; i < Sc::kPer; ++i)
-        sw[r][i] = 4u * i + 4u <= left ? sw[r][i] : 4u * i < left ? sw[r][i] & 0xFFFFu : 0u;
+      for (int i = 0; i < kDwords; ++i) {
+        const uint32_t at = 4u * (kFirst + i);
+        sw[r][i] = at + 4u <= left ? sw[r][i] : at < left ? sw[r][i] & 0xFFFFu : 0u;
+      }
     }
-    quad_steps<FMT>(d[r], wb[r]);
+    half_steps<FMT, H>(d[r], wb[r]);
   }
 #pragma unroll
-  for (int c = 0; c < (int)QC; ++c) {
+  for (int c = 0; c < QH; ++c) {
     float4_t dd[2][NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -74,7 +83,7 @@ __device__ __attribute__((always_inline)) inline void wide_product(
     if constexpr (kInt) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float zn = FMT == kINT4 ? -24.0f : -16.0f - (float)((sw[r][c % Sc::kPer] >> 16) & 15u);
+        const float zn = FMT == kINT4 ? -24.0f : -16.0f - (float)((sw[r][0] >> 16) & 15u);
         const uint32_t h = XT == kF16 ? f16_bits(zn) : (__float_as_uint(zn) >> 16);
         zcol[r] = make_uint4(h | (h << 16), h | (h << 16), h | (h << 16), h | (h << 16));
       }
@@ -83,13 +92,12 @@ __device__ __attribute__((always_inline)) inline void wide_product(
     for (int s = 0; s < STEPS; ++s) {
       constexpr uint32_t kPieces = KC / 8;  // of a block
       const uint32_t at = (c * kPieces + s * (kMX ? 4u : 1u)) * 16u;
-      // (the exclusive or touches the low 256 bytes alone: half a quad further is an immediate offset)
-      const uint8_t* xp = wbase + (apiece ^ (at & 255u)) + (at & 256u);
+      const uint8_t* xp = wbase + (ap ^ at);
       uint4 xv[NT][NP];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int p = 0; p < NP; ++p) xv[t][p] = *reinterpret_cast<const uint4*>(xp + (t * NP + p) * 8192u);
+        for (int p = 0; p < NP; ++p) xv[t][p] = *reinterpret_cast<const uint4*>(xp + (t * NP + p) * 4096u);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         uint4 b1, b2;
@@ -119,7 +127,7 @@ __device__ __attribute__((always_inline)) inline void wide_product(
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const float sc =
-              ldexpf(__uint_as_float(0x00400000u), (int)((sw[r][c >> 1] >> (16 * (c & 1) + 8 * s)) & 0xFFu));
+              ldexpf(__uint_as_float(0x00400000u), (int)((sw[r][0] >> (16 * c + 8 * s)) & 0xFFu));
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -132,9 +140,9 @@ __device__ __attribute__((always_inline)) inline void wide_product(
     if constexpr (!kMX) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float sc = __uint_as_float(FMT == kINT4    ? (c == 0 ? sw[r][0] << 16 : sw[r][0] & 0xFFFF0000u)
-                                         : FMT == kINT4A ? sw[r][c % Sc::kPer] << 16
-                                                         : sw[r][c % Sc::kPer]);
+        const float sc = __uint_as_float(FMT == kINT4    ? (H == 0 ? sw[r][0] << 16 : sw[r][0] & 0xFFFF0000u)
+                                         : FMT == kINT4A ? sw[r][0] << 16
+                                                         : sw[r][c % kDwords]);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -151,8 +159,10 @@ struct MoeWide {
   static constexpr uint32_t QC = 256 / KC;
   static constexpr uint32_t SB = FMT == kINT4 || FMT == kMXFP4 ? 2 : 4;
   static constexpr int NP = DIR == kUp ? 1 : 3;              // planes
-  static constexpr uint32_t kBuffer = NT * NP * 16u * 512u;  // bytes of an LDS buffer
-  static constexpr uint32_t kPieces = NT * NP * 16u * 32u / kWideThreads;  // of a thread
+  static constexpr uint32_t kBuffer = NT * NP * 16u * 256u;  // bytes of half a quad in LDS
+  static constexpr uint32_t kHalves = DIR == kUp ? 2 : 1;    // halves of a buffer, and of a barrier
+  static constexpr uint32_t kPieces = NT * NP;               // of a thread
+  static_assert(kWideThreads == 16 * 16, "a thread takes one piece of each 16 window rows");
 
   // 32 rows a wave (unit `unit`) of expert e, on the chunk's pairs: `list` holds them in lanes, `have` of
   // them.
@@ -194,38 +204,43 @@ struct MoeWide {
     };
     const uint32_t sshift = ((uint32_t)(lane >> 2) * spitch & 2u) * 8u;
 
-    // Activations: piece s of a thread belongs to window row 8 s + tid / 32, at position tid % 32.  Rows
+    // Activations: piece s of a thread belongs to window row 16 s + tid / 16, at position tid % 16.  Rows
     // without a pair read as zeros.
     const __amdgpu_buffer_rsrc_t rx =
         make_rsrc(a.x, (DIR == kUp ? a.pairs / a.top_k : 3u * a.pairs) * a.k * 2u);
-    const uint32_t wrow = (uint32_t)tid >> 5, slot = (uint32_t)tid & 31u;
+    const uint32_t wrow = (uint32_t)tid >> 4, slot = (uint32_t)tid & 15u;
+    const uint32_t xpiece = slot ^ wrow;  // in the half quad
     uint32_t xoff[kPieces];
 #pragma unroll
     for (uint32_t s = 0; s < kPieces; ++s) {
-      const uint32_t r = 8u * s + wrow;
-      const uint32_t col = (r >> 4) / NP * 16u + (r & 15u), plane = (r >> 4) % NP;
+      const uint32_t col = s / NP * 16u + wrow, plane = s % NP;
       const uint32_t p = (uint32_t)__shfl(list, (int)col);
       const uint32_t base = (DIR == kUp ? p / a.top_k : plane * a.pairs + p) * a.k * 2u;
-      xoff[s] = offset_or_oob(col < have, base + ((slot ^ (r & 15u)) * 16u));
+      xoff[s] = offset_or_oob(col < have, base + xpiece * 16u);
     }
-    uint4 xv[kPieces];
-    auto load_x = [&](uint32_t q) __attribute__((always_inline)) {
+    uint4 xv[kHalves][kPieces];
+    auto load_x = [&](uint32_t u) __attribute__((always_inline)) {  // buffer u's halves
 #pragma unroll
-      for (uint32_t s = 0; s < kPieces; ++s) {
-        const uint32_t piece = slot ^ ((8u * s + wrow) & 15u);
-        // (an offset past the buffer stays past it: the sum does not wrap)
-        xv[s] = buffer_load16(rx, offset_or_oob(q * 32u + piece < a.k >> 3 && xoff[s] != kOutOfRange, xoff[s] + q * 512u));
-      }
+      for (uint32_t h = 0; h < kHalves; ++h)
+#pragma unroll
+        for (uint32_t s = 0; s < kPieces; ++s) {
+          const uint32_t at = u * kHalves + h;
+          // (an offset past the buffer stays past it: the sum does not wrap)
+          xv[h][s] = buffer_load16(rx, offset_or_oob(at * 16u + xpiece < a.k >> 3 && xoff[s] != kOutOfRange, xoff[s] + at * 256u));
+        }
     };
     auto store_x = [&](uint32_t b) __attribute__((always_inline)) {
 #pragma unroll
-      for (uint32_t s = 0; s < kPieces; ++s)
-        *reinterpret_cast<uint4*>(smem + b * kBuffer + (8u * s + wrow) * 512u + slot * 16u) = arranged<FMT>(xv[s]);
+      for (uint32_t h = 0; h < kHalves; ++h)
+#pragma unroll
+        for (uint32_t s = 0; s < kPieces; ++s)
+          *reinterpret_cast<uint4*>(smem + (b * kHalves + h) * kBuffer + (16u * s + wrow) * 256u + slot * 16u) =
+              arranged<FMT>(xv[h][s]);
     };
 
     const uint32_t piece0 = FMT == kMXFP4 ? g : is_g128(FMT) ? 4 * g : 4 * (g & 1) + 2 * (g >> 1);
     const uint32_t apiece = (piece0 ^ (uint32_t)m) * 16u;
-    const uint8_t* arow = smem + (uint32_t)m * 512u;
+    const uint8_t* arow = smem + (uint32_t)m * 256u;
 
     float4_t acc[2][NT];
 #pragma unroll
@@ -242,16 +257,23 @@ struct MoeWide {
     load_x(1);
     load_quad(1, W1);
     __syncthreads();
-    auto step = [&](uint32_t q, MoeQuad (&d)[2], auto odd) __attribute__((always_inline)) {
-      constexpr int ODD = decltype(odd)::value;
-      if (q + 1 < nq) {
-        store_x(1u - ODD);
-        load_x(q + 2);
+    auto half = [&](uint32_t q, MoeQuad (&d)[2], auto odd, auto which) __attribute__((always_inline)) {
+      constexpr int ODD = decltype(odd)::value, H = decltype(which)::value;
+      constexpr uint32_t B = kHalves == 2 ? ODD : H;  // the buffer multiplied
+      const uint32_t u = kHalves == 2 ? q : 2u * q + H;
+      if ((kHalves == 1 || H == 0) && u + 1 < 2u / kHalves * nq) {
+        store_x(1u - B);
+        load_x(u + 2);
       }
       const uint32_t left = (nblocks - q * QC) * SB;
-      wide_product<FMT, XT, NT, NP, ODD>(acc, d, held, q % Sc::kQuads, left, arow + ODD * kBuffer, apiece, tab, lane);
-      load_quad(q + 2, d);
-      __syncthreads();
+      wide_product<FMT, XT, NT, NP, ODD, H>(acc, d, held, q % Sc::kQuads, left,
+                                            arow + (kHalves == 2 ? 2u * B + H : B) * kBuffer, apiece, tab, lane);
+      if (H == 1) load_quad(q + 2, d);
+      if (kHalves == 1 || H == 1) __syncthreads();
+    };
+    auto step = [&](uint32_t q, MoeQuad (&d)[2], auto odd) __attribute__((always_inline)) {
+      half(q, d, odd, std::integral_constant<int, 0>{});
+      half(q, d, odd, std::integral_constant<int, 1>{});
     };
     for (uint32_t q = 0; q < nq; q += 2) {
       if (q % Sc::kQuads == 0) {
@@ -317,7 +339,7 @@ __global__ void __launch_bounds__(kWideThreads, DIR == kUp && NT == 1 ? 3 : 2) m
 
 template <int DIR, int FMT, int XT, int NT>
 hipError_t launch_moe_wide_one(const MoeArgs& a, hipStream_t s) {
-  constexpr int kLds = 2 * MoeWide<DIR, FMT, XT, NT>::kBuffer;
+  constexpr int kLds = 2 * MoeWide<DIR, FMT, XT, NT>::kHalves * MoeWide<DIR, FMT, XT, NT>::kBuffer;
   static const hipError_t raised =
       hipFuncSetAttribute(reinterpret_cast<const void*>(&moe_wide_kernel<DIR, FMT, XT, NT>),
                           hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
@@ -337,12 +359,16 @@ hipError_t launch_moe_wide_one(const MoeArgs& a, hipStream_t s) {
 // MI355X (us for the layer, 16 columns against 64): 8 of 128 experts, 2048 x 768, MXFP4, at 4 / 8 / 16 / 32
 // pairs an expert 98 / 104 / 154 / 234 against 109 / 118 / 144 / 200; 4 of 64, 1536 x 1408, INT4, 72 / 78 /
 // 116 / 173 against 79 / 85 / 109 / 145.  NF4, whose table takes 32 KiB: 32 columns always.
-// Down: 16 pairs, the three planes of 32 would take a CU's LDS for one workgroup (or, in one buffer,
-// more registers than there are: 143 -> 157 us).
+// Down: 16 pairs a chunk up to 12 pairs an expert, or where chunks of 32 would leave CUs without one; else
+// 32.  Measured (16 against 32): 6 of 64, 1536 x 1408, FP4, at 24 / 48 pairs an expert 136 / 195 against 122 /
+// 171; 8 of 128, 2048 x 768, MXFP4, at 16 / 32 pairs 167 / 220 against 149 / 203; 2 of 8, 1536 x 2048, NF4,
+// at 16 / 32 / 64 / 128 pairs 48 / 56 / 71 / 114 against 56 / 58 / 75 / 104.
 template <int DIR, int FMT, int XT>
 hipError_t launch_moe_wide_cols(const MoeArgs& a, hipStream_t s) {
   if constexpr (DIR == kDown) {
-    return launch_moe_wide_one<DIR, FMT, XT, 1>(a, s);
+    const bool fills = (uint64_t)(a.pairs / 32u) * (a.n / 128u) >= (uint64_t)device_cu_count();
+    return a.pairs > 12u * a.experts && fills ? launch_moe_wide_one<DIR, FMT, XT, 2>(a, s)
+                                              : launch_moe_wide_one<DIR, FMT, XT, 1>(a, s);
   } else if constexpr (FMT == kNF4) {
     return launch_moe_wide_one<DIR, FMT, XT, 2>(a, s);
   } else {
