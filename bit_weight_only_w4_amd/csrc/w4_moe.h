@@ -41,10 +41,10 @@ hipError_t launch_moe_up_bf16(int weight, int kw, const MoeArgs& a, hipStream_t 
 hipError_t launch_moe_pair_f16(int weight, int kw, const MoeArgs& a, uint32_t tokens, hipStream_t s);
 hipError_t launch_moe_pair_bf16(int weight, int kw, const MoeArgs& a, uint32_t tokens, hipStream_t s);
 hipError_t launch_moe_token(int weight, int kw, const MoeArgs& a, uint32_t tokens, hipStream_t s);
+hipError_t launch_moe_down(int weight, int kw, int tiles, const MoeArgs& a, hipStream_t s);
+// Many tokens (the pairs sorted by expert).
 hipError_t launch_moe_wide_up(int weight, int xtype, const MoeArgs& a, hipStream_t s);
 hipError_t launch_moe_wide_down(int weight, const MoeArgs& a, hipStream_t s);
-hipError_t launch_moe_down(int weight, int kw, int tiles, const MoeArgs& a,
-                           hipStream_t s);
 
 // The layer (arguments as w4_moe, already validated).
 hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const float* weights,

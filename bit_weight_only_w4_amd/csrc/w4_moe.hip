@@ -246,8 +246,8 @@ hipError_t launch_moe_route(const void* logits, int type, int64_t tokens, int64_
 
 // Many tokens: from three pairs an expert on, and from eight where the experts are too few to fill the
 // card without K groups (down: a workgroup has 128 rows).  Measured on MI355X against the kernels with K
-// groups (us for the layer): 8 of 128 experts, 2048 x 768, MXFP4, at 2 / 4 / 8 / 16 pairs an expert 96 / 98 /
-// 104 / 144 against 84 / 113 / 145 / 251; 1 of 32, 2048 x 2048, FP4, 66 / 71 / 73 / 98 against 59 / 72 / 79 /
+// groups (us for the layer): 8 of 128 experts, 2048 x 768, MXFP4, at 2 / 4 / 8 / 16 pairs an expert 96 / 105 /
+// 106 / 131 against 84 / 113 / 145 / 251; 1 of 32, 2048 x 2048, FP4, 66 / 72 / 74 / 92 against 59 / 72 / 79 /
 // 146.  Few experts: 2 of 8, 1024 x 768, FP4, at 4 / 8 / 16 pairs 21 / 21 / 29 against 19 / 23 / 37; 2 of 4,
 // 2048 x 2048, NF4, 47 / 47 / 50 against 29 / 46 / 75; one expert of 2048 x 4096, INT4, 48 / 49 / 49 against
 // 25 / 37 / 60.

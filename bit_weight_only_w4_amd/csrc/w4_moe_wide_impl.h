@@ -356,7 +356,7 @@ hipError_t launch_moe_wide_one(const MoeArgs& a, hipStream_t s) {
 }
 
 // Up: 16 columns a chunk, three workgroups to a CU, up to 12 pairs an expert, else up to 64.  Measured on
-// MI355X (us for the layer, 16 columns against 64): 8 of 128 experts, 2048 x 768, MXFP4, at 4 / 8 / 16 / 32
+// MI355X (us for the layer with 16 pairs a down chunk, 16 columns against 64): 8 of 128 experts, 2048 x 768, MXFP4, at 4 / 8 / 16 / 32
 // pairs an expert 98 / 104 / 154 / 234 against 109 / 118 / 144 / 200; 4 of 64, 1536 x 1408, INT4, 72 / 78 /
 // 116 / 173 against 79 / 85 / 109 / 145.  NF4, whose table takes 32 KiB: 32 columns always.
 // Down: 16 pairs a chunk up to 12 pairs an expert, or where chunks of 32 would leave CUs without one; else
