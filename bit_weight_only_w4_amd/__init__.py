@@ -77,6 +77,7 @@ def lib() -> ctypes.CDLL:
         L.w4_auto_path.argtypes = [ci, i64, i64, i64, sz, ctypes.POINTER(ci)]
         ip = ctypes.POINTER(ci)
         L.w4_gemv_plan.argtypes = [ci, i64, i64, i64, ci, ip, ip, ip, ip, ip]
+        L.w4_moe_plan.argtypes = [ci, i64, i64, i64, i64, i64, ip, ip, ip, ip, ip]
         L.w4_nf4_codebook.restype = ctypes.POINTER(ctypes.c_float)
         L.w4_status_string.argtypes = [ci]
         L.w4_status_string.restype = ctypes.c_char_p
@@ -99,7 +100,7 @@ def lib() -> ctypes.CDLL:
                      "w4_gptq_quantize", "w4_sparse24_compress", "w4_sparse24_gemv",
                      "w4_sparse24_gemv_grouped", "w4_set_path", "w4_get_path",
                      "w4_matmul_splitk_noalloc",
-                     "w4_set_workspace", "w4_moe_route", "w4_moe"):
+                     "w4_set_workspace", "w4_moe_route", "w4_moe", "w4_moe_plan"):
             getattr(L, name).restype = ci
         _lib = L
     return _lib
@@ -586,6 +587,15 @@ def moe_route(logits, top_k, renormalize=True, ids=None, weights=None, stream=No
 
 def moe_workspace_bytes(fmt, tokens, hidden, inter, experts, top_k) -> int:
     return int(lib().w4_moe_workspace_bytes(_fmt(fmt), tokens, hidden, inter, experts, top_k))
+
+
+def moe_plan(fmt, tokens, hidden, inter, experts, top_k):
+    """dict(kind, up_groups, down_groups, up_window, down_window) of a layer's launches: kind 0 a wave per
+    (token, slot) pair, 1 products that an expert's pairs share, 2 the same with the pairs sorted first."""
+    vals = [ctypes.c_int(0) for _ in range(5)]
+    check(lib().w4_moe_plan(_fmt(fmt), tokens, hidden, inter, experts, top_k, *[ctypes.byref(v) for v in vals]),
+          "w4_moe_plan")
+    return dict(zip(("kind", "up_groups", "down_groups", "up_window", "down_window"), (v.value for v in vals)))
 
 
 def moe(x, ids, weights, gate_up, gate_up_scales, down, down_scales, fmt, y=None, workspace=None,

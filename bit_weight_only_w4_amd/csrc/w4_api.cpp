@@ -1131,6 +1131,20 @@ size_t w4_moe_workspace_bytes(int fmt, int64_t tokens, int64_t hidden, int64_t i
   return moe_workspace(tokens * top_k, hidden, inter, experts);
 }
 
+int w4_moe_plan(int fmt, int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k, int* kind,
+                int* up_groups, int* down_groups, int* up_window, int* down_window) {
+  const int st = moe_shape(fmt, tokens, hidden, inter, experts, top_k);
+  if (st != W4_OK) return st;
+  MoePlan p;
+  if (!plan_moe(tokens, hidden, inter, experts, top_k, &p)) return W4_ERR_PATH;
+  if (kind) *kind = p.kind;
+  if (up_groups) *up_groups = p.up.kw;
+  if (down_groups) *down_groups = p.down.kw;
+  if (up_window) *up_window = (int)p.up.win_bytes;
+  if (down_window) *down_window = (int)p.down.win_bytes;
+  return W4_OK;
+}
+
 int w4_moe(const void* x, const int32_t* ids, const float* weights, const uint8_t* gate_up,
            const void* gate_up_scales, const uint8_t* down, const void* down_scales, int fmt,
            int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k, float* y,
@@ -1155,7 +1169,9 @@ int w4_moe(const void* x, const int32_t* ids, const float* weights, const uint8_
   for (int i = 0; i < 7; ++i)
     if (overlaps(y, yb, in[i], bytes[i]) || overlaps(workspace, used, in[i], bytes[i])) return W4_ERR_ALIAS;
   if (overlaps(y, yb, workspace, used)) return W4_ERR_ALIAS;
-  return launch_moe(fmt, reinterpret_cast<const uint16_t*>(x), ids, weights, gate_up, gate_up_scales, down,
+  MoePlan plan;
+  if (!plan_moe(tokens, hidden, inter, experts, top_k, &plan)) return W4_ERR_PATH;
+  return launch_moe(fmt, plan, reinterpret_cast<const uint16_t*>(x), ids, weights, gate_up, gate_up_scales, down,
                     down_scales, tokens, hidden, inter, experts, top_k, y, workspace,
                     reinterpret_cast<hipStream_t>(stream)) == hipSuccess
              ? W4_OK

@@ -46,10 +46,24 @@ hipError_t launch_moe_down(int weight, int kw, int tiles, const MoeArgs& a, hipS
 hipError_t launch_moe_wide_up(int weight, int xtype, const MoeArgs& a, hipStream_t s);
 hipError_t launch_moe_wide_down(int weight, const MoeArgs& a, hipStream_t s);
 
+// The launches of a layer, chosen on its sizes before the first of them.
+enum MoeKind { kMoePerPair = 0, kMoeShared = 1, kMoeSorted = 2 };
+struct MoeProduct {  // of the shared products; a wave per pair: kw and qpk alone
+  int kw;            // K groups
+  uint32_t qpk, qpw, cols, win_bytes;  // as in MoeArgs
+};
+struct MoePlan {
+  int kind;
+  int tiles;  // shared products, down: see launch_moe_down
+  MoeProduct up, down;
+};
+// False if a window would not fit LDS.
+bool plan_moe(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k, MoePlan* out);
+
 // The layer (arguments as w4_moe, already validated).
-hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const float* weights,
-                      const uint8_t* gate_up, const void* gate_up_scales, const uint8_t* down,
-                      const void* down_scales, int64_t tokens, int64_t hidden, int64_t inter,
+hipError_t launch_moe(int fmt, const MoePlan& plan, const uint16_t* x, const int32_t* ids,
+                      const float* weights, const uint8_t* gate_up, const void* gate_up_scales,
+                      const uint8_t* down, const void* down_scales, int64_t tokens, int64_t hidden, int64_t inter,
                       int64_t experts, int64_t top_k, float* y, void* ws, hipStream_t s);
 size_t moe_workspace(int64_t pairs, int64_t hidden, int64_t inter, int64_t experts);
 hipError_t launch_moe_route(const void* logits, int type, int64_t tokens, int64_t experts, int64_t top_k,

@@ -215,20 +215,28 @@ int moe_kw(int64_t tiles, int64_t experts, int64_t k, int64_t rows) {
 }
 
 // Quads, window and chunk of a product over K with kw K groups: `cols` pairs a chunk of `planes`
-// rows each, and as many quads a window as fit kWindowBytes (all of K if it fits).
+// rows each, and as many quads a window as fit kWindowBytes: all of K if it fits, else an even number of
+// quads of each K group (the loop takes two at a time), so that evening out the windows cannot pass what fits.
+// Two quads of each always do: moe_kw leaves room for them in kMoeMaxWindow.
 constexpr int64_t kWindowBytes = 65536;
 
-void moe_window(int64_t k, int kw, uint32_t cols, uint32_t planes, MoeArgs* a) {
+MoeProduct moe_window(int64_t k, int kw, uint32_t cols, uint32_t planes) {
   const int64_t qpk = ((k + 255) / 256 + kw - 1) / kw;
   const int64_t rows = (int64_t)cols * planes;
-  const int64_t fit = std::max<int64_t>(1, kWindowBytes / (rows * 512 * kw));
-  // (windows of an even number of quads of a K group: the loop takes two at a time)
-  const int64_t windows = (qpk + fit - 1) / fit;
-  const int64_t per = windows == 1 ? qpk : std::max<int64_t>(2, ((qpk + windows - 1) / windows + 1) / 2 * 2);
-  a->qpk = (uint32_t)qpk;
-  a->qpw = (uint32_t)(per * kw);
-  a->cols = cols;
-  a->win_bytes = (uint32_t)rows * a->qpw * 512u;
+  const int64_t fit = kWindowBytes / (rows * 512 * kw);
+  int64_t per = qpk;
+  if (per > fit) {
+    const int64_t most = std::max<int64_t>(2, fit / 2 * 2);
+    const int64_t windows = (qpk + most - 1) / most;
+    per = ((qpk + windows - 1) / windows + 1) / 2 * 2;
+  }
+  MoeProduct p;
+  p.kw = kw;
+  p.cols = cols;
+  p.qpk = (uint32_t)qpk;
+  p.qpw = (uint32_t)(per * kw);
+  p.win_bytes = (uint32_t)rows * p.qpw * 512u;
+  return p;
 }
 
 }  // namespace
@@ -263,7 +271,53 @@ size_t moe_workspace(int64_t pairs, int64_t hidden, int64_t inter, int64_t exper
          align256((size_t)pairs * 4) + ((size_t)experts + 1) * 4;
 }
 
-hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const float* weights,
+// Fewer pairs than experts: a wave per pair in both launches, the second combining.  Measured on MI355X
+// against the shared products and their third launch (us): 8 of 128 experts, 2048 x 768, MXFP4, at 2 / 4 /
+// 8 / 12 / 16 / 32 tokens 18.2 / 26.8 / 45.8 / 63.6 / 77.6 / 143.7 against 24.3 / 32.2 / 48.7 / 66.2 / 77.4 /
+// 86.5; 4 of 64, 1536 x 1408, INT4, at 4 / 8 / 12 / 16 tokens 23.1 / 35.5 / 51.4 / 63.1 against 30.0 /
+// 41.3 / 52.2 / 59.5.
+// One slot a token pays up to half as many pairs as experts: 1 of 32, 2048 x 2048, FP4, at 12 / 16 / 24 tokens
+// 33.1 / 42.6 / 60.0 against 38.4 / 43.2 / 44.7; 1 of 64, 1024 x 1024, INT4, at 24 / 32 / 48 25.9 / 32.4 / 45.0
+// against 30.2 / 31.0 / 31.5.
+static bool moe_per_pair(int64_t tokens, int64_t experts, int64_t top_k) {
+  const int64_t pairs = tokens * top_k;
+  return tokens == 1 || (pairs < experts && (top_k > 1 || 2 * pairs <= experts));
+}
+
+bool plan_moe(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k, MoePlan* out) {
+  const int64_t pairs = tokens * top_k;
+  MoePlan p{};
+  if (moe_per_pair(tokens, experts, top_k)) {
+    p.kind = kMoePerPair;
+    const int least = top_k > 4 ? 1 : top_k > 2 ? 2 : top_k > 1 ? 4 : 8;  // no wave without a slot ...
+    // ... or without a quad (1 token, 2 of 8, 512 x 256, NF4: 9.2 against 10.2); up: then K ranges until the waves
+    // number two per SIMD
+    const int64_t units = inter / 16 * pairs;
+    int kw = least;
+    while (kw > 1 && kw > (hidden + 255) / 256) kw /= 2;
+    while (kw < 8 && 2 * kw <= (hidden + 255) / 256 && units * kw < 8 * device_cu_count()) kw *= 2;
+    p.up.kw = kw;
+    p.up.qpk = (uint32_t)(((hidden + 255) / 256 + kw - 1) / kw);
+    kw = least;
+    while (kw > 1 && kw > (inter + 255) / 256) kw /= 2;
+    p.down.kw = kw;
+    p.down.qpk = (uint32_t)(((inter + 255) / 256 + kw - 1) / kw);
+  } else if (moe_wide(pairs, experts, hidden)) {
+    p.kind = kMoeSorted;
+  } else {
+    p.kind = kMoeShared;
+    uint32_t cols = (uint32_t)std::min<int64_t>(16, tokens);
+    p.up = moe_window(hidden, moe_kw(inter / 8, experts, hidden, cols), cols, 1);
+    p.tiles = pairs <= 2 * experts ? 1 : 3;
+    cols = (uint32_t)std::min<int64_t>(p.tiles == 1 ? kMoePacked : 16, tokens);
+    p.down = moe_window(inter, moe_kw(hidden / 16, experts, inter, 3 * cols), cols, 3);
+    if (p.up.win_bytes > kMoeMaxWindow || p.down.win_bytes > kMoeMaxWindow) return false;
+  }
+  *out = p;
+  return true;
+}
+
+hipError_t launch_moe(int fmt, const MoePlan& plan, const uint16_t* x, const int32_t* ids, const float* weights,
                       const uint8_t* gate_up, const void* gate_up_scales, const uint8_t* down,
                       const void* down_scales, int64_t tokens, int64_t hidden, int64_t inter,
                       int64_t experts, int64_t top_k, float* y, void* ws, hipStream_t s) {
@@ -275,6 +329,12 @@ hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const floa
                        a.part, ids, weights, (uint32_t)hidden, (uint32_t)experts, (uint32_t)top_k, y);
     return hipGetLastError();
   };
+  auto set = [&](const MoeProduct& p) {
+    a.qpk = p.qpk;
+    a.qpw = p.qpw;
+    a.cols = p.cols;
+    a.win_bytes = p.win_bytes;
+  };
   // the second product's operands
   auto turn_down = [&]() {
     a.packed = down;
@@ -283,6 +343,7 @@ hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const floa
     a.n = (uint32_t)hidden;
     a.k = (uint32_t)inter;
     a.tiles = (uint32_t)(hidden / 16);
+    set(plan.down);
   };
   a.ids = ids;
   a.h = reinterpret_cast<uint16_t*>(ws);
@@ -297,35 +358,17 @@ hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const floa
   a.n = (uint32_t)(2 * inter);
   a.k = (uint32_t)hidden;
   a.tiles = (uint32_t)(inter / 8);
-  // Fewer pairs than experts: a wave per pair in both launches, the second combining.  Measured on MI355X
-  // against the shared products and their third launch (us): 8 of 128 experts, 2048 x 768, MXFP4, at 2 / 4 /
-  // 8 / 12 / 16 / 32 tokens 18.2 / 26.8 / 45.8 / 63.6 / 77.6 / 143.7 against 24.3 / 32.2 / 48.7 / 66.2 / 77.4 /
-  // 86.5; 4 of 64, 1536 x 1408, INT4, at 4 / 8 / 12 / 16 tokens 23.1 / 35.5 / 51.4 / 63.1 against 30.0 /
-  // 41.3 / 52.2 / 59.5.
-  // One slot a token pays up to half as many pairs as experts: 1 of 32, 2048 x 2048, FP4, at 12 / 16 / 24 tokens
-  // 33.1 / 42.6 / 60.0 against 38.4 / 43.2 / 44.7; 1 of 64, 1024 x 1024, INT4, at 24 / 32 / 48 25.9 / 32.4 / 45.0
-  // against 30.2 / 31.0 / 31.5.
-  if (tokens == 1 || (pairs < experts && (top_k > 1 || 2 * pairs <= experts))) {
-    const int least = top_k > 4 ? 1 : top_k > 2 ? 2 : top_k > 1 ? 4 : 8;  // no wave without a slot ...
-    // ... or without a quad (1 token, 2 of 8, 512 x 256, NF4: 9.2 against 10.2); up: then K ranges until the waves
-    // number two per SIMD
-    const int64_t units = inter / 16 * pairs;
-    int kw = least;
-    while (kw > 1 && kw > (hidden + 255) / 256) kw /= 2;
-    while (kw < 8 && 2 * kw <= (hidden + 255) / 256 && units * kw < 8 * device_cu_count()) kw *= 2;
-    a.qpk = (uint32_t)(((hidden + 255) / 256 + kw - 1) / kw);
-    hipError_t e = fmt_xtype(fmt) == kF16 ? launch_moe_pair_f16(weight, kw, a, (uint32_t)tokens, s)
-                                          : launch_moe_pair_bf16(weight, kw, a, (uint32_t)tokens, s);
+  set(plan.up);
+  if (plan.kind == kMoePerPair) {
+    hipError_t e = fmt_xtype(fmt) == kF16 ? launch_moe_pair_f16(weight, plan.up.kw, a, (uint32_t)tokens, s)
+                                          : launch_moe_pair_bf16(weight, plan.up.kw, a, (uint32_t)tokens, s);
     if (e != hipSuccess) return e;
     turn_down();
     a.weights = weights;
     a.y = y;
-    kw = least;
-    while (kw > 1 && kw > (inter + 255) / 256) kw /= 2;
-    a.qpk = (uint32_t)(((inter + 255) / 256 + kw - 1) / kw);
-    return launch_moe_token(weight, kw, a, (uint32_t)tokens, s);
+    return launch_moe_token(weight, plan.down.kw, a, (uint32_t)tokens, s);
   }
-  if (moe_wide(pairs, experts, hidden)) {
+  if (plan.kind == kMoeSorted) {
     char* at = reinterpret_cast<char*>(a.part) + align256((size_t)pairs * (size_t)hidden * 4);
     int32_t* order = reinterpret_cast<int32_t*>(at);
     int32_t* start = reinterpret_cast<int32_t*>(at + align256((size_t)pairs * 4));
@@ -342,22 +385,13 @@ hipError_t launch_moe(int fmt, const uint16_t* x, const int32_t* ids, const floa
     if (e != hipSuccess) return e;
     return combine();
   }
-  uint32_t cols = (uint32_t)std::min<int64_t>(16, tokens);
-  int kw = moe_kw(a.tiles, experts, hidden, cols);
   a.grid = (uint32_t)std::max<int64_t>(1, 2 * device_cu_count() / experts);
-  moe_window(hidden, kw, cols, 1, &a);
-  hipError_t e = fmt_xtype(fmt) == kF16 ? launch_moe_up_f16(weight, kw, a, s)
-                                        : launch_moe_up_bf16(weight, kw, a, s);
+  hipError_t e = fmt_xtype(fmt) == kF16 ? launch_moe_up_f16(weight, plan.up.kw, a, s)
+                                        : launch_moe_up_bf16(weight, plan.up.kw, a, s);
   if (e != hipSuccess) return e;
-
   turn_down();
-  const int tiles = pairs <= 2 * experts ? 1 : 3;
-  cols = (uint32_t)std::min<int64_t>(tiles == 1 ? kMoePacked : 16, tokens);
-  kw = moe_kw(a.tiles, experts, inter, 3 * cols);
-  moe_window(inter, kw, cols, 3, &a);
-  e = launch_moe_down(weight, kw, tiles, a, s);
+  e = launch_moe_down(weight, plan.down.kw, plan.tiles, a, s);
   if (e != hipSuccess) return e;
-
   return combine();
 }
 

@@ -572,6 +572,13 @@ int w4_moe(const void* x, const int32_t* ids, const float* weights, const uint8_
 size_t w4_moe_workspace_bytes(int fmt, int64_t tokens, int64_t hidden, int64_t inter, int64_t experts,
                               int64_t top_k);
 
+/* How w4_moe launches these sizes: kind 0, a wave per (token, slot) pair; 1, products shared by the
+ * pairs of an expert; 2, the same with the pairs sorted by expert first.  Kinds 0 and 1: the K groups of
+ * the up and the down product; kind 1: the bytes of LDS that each keeps activations in (0 otherwise).
+ * Any output pointer may be NULL.  Returns W4_OK, or the error w4_moe gives for these sizes. */
+int w4_moe_plan(int fmt, int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k, int* kind,
+                int* up_groups, int* down_groups, int* up_window, int* down_window);
+
 /* ------------------------------------------------------------------ measurement probes ------ */
 
 /* Streaming-read ceiling probe: reads `bytes` (multiple of 16) from device `src` with 128-bit
