@@ -51,6 +51,8 @@ namespace {
 
 constexpr int kUp = 0, kDown = 1;
 constexpr float kNf4Factor = 1.4376f;
+__constant__ uint32_t c_moe_nf4[16] = W4_NF4_CODE_BITS;
+__constant__ uint32_t c_moe_fp4[16] = W4_FP4_CODE_BITS;
 
 // NF4's byte -> decoded pair table: 16 copies of each 8-byte entry (first terms, second terms), lane L
 // reading copy L % 16.
@@ -295,7 +297,7 @@ __device__ __attribute__((always_inline)) inline void quad_product(
         if constexpr (is_g128(FMT)) dd[t] = mfma<XT>(xv[t], zcol, dd[t]);
       }
       if constexpr (kMX) {
-        // 2^(e - 127); e = 255 gives an infinity here, which `finish` tells apart
+        // 2^(e - 127); e = 255 gives an infinity here, and its sums are looked at again (defined_sum)
         const float sc = ldexpf(__uint_as_float(0x00400000u), (int)((sw[c >> 1] >> (16 * (c & 1) + 8 * s)) & 0xFFu));
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -349,20 +351,6 @@ __device__ inline void place_scales(MoeScales<FMT>& held, const MoeScales<FMT>& 
   }
 }
 
-// v, or NaN if the MXFP4 row at `scales` (bytes of them) holds a scale byte of 255.  Such a byte makes
-// its row's sums infinite or NaN, so a row is looked through only then.
-template <int FMT>
-__device__ inline float with_nan_scales(float v, const void* scales, size_t bytes) {
-  if constexpr (FMT == kMXFP4) {
-    if (!__builtin_isfinite(v)) {
-      const uint8_t* sp = reinterpret_cast<const uint8_t*>(scales);
-      for (size_t i = 0; i < bytes; ++i)
-        if (sp[i] == 255u) v = __uint_as_float(0x7FC00000u);
-    }
-  }
-  return v;
-}
-
 // h = silu(gate) up of one row and pair, as three bf16 planes.
 __device__ inline void store_h(const MoeArgs& a, uint32_t pair, uint32_t row, uint32_t inter, float gate, float up) {
   const float v = gate / (1.0f + expf(-gate)) * up;
@@ -374,6 +362,93 @@ __device__ inline void store_h(const MoeArgs& a, uint32_t pair, uint32_t row, ui
   a.h[at] = (uint16_t)(b1 >> 16);
   a.h[at + plane] = (uint16_t)(b2 >> 16);
   a.h[at + 2 * plane] = (uint16_t)(__float_as_uint(r2) >> 16);
+}
+
+// Sums that are not finite, computed again from the definition.  The kernels' arithmetic leaves it there:
+// integer codes are taken as q + 16 with an offset taken off beside and NF4's as two terms, so an infinite operand
+// meets terms of both signs (a NaN where the definition has an infinity), sums of such terms may
+// overflow early, and an MXFP4 scale byte of 255 multiplies as an infinity.  A kernel marks that one of its sums
+// was not finite and looks at what it stored; a wave with none passes by.  One row over k0 .. k1 - 1 in 64
+// bits: code scale x, x the value whose NP planes (bf16) or one value (XT) stand in its row.
+template <int FMT, int XT, int NP>
+__device__ __attribute__((always_inline)) inline float defined_sum(const MoeArgs& a, int e, uint32_t row, uint32_t xrow,
+                                                                   uint32_t k0, uint32_t k1) {
+  constexpr uint32_t KC = FMT == kMXFP4 ? 32 : is_g128(FMT) ? 128 : 64;
+  constexpr uint32_t SB = FMT == kMXFP4 ? 1 : FMT == kINT4 ? 2 : 4;
+  const size_t at = (size_t)e * a.n + row;
+  const uint8_t* packed = a.packed + at * (a.k >> 1);
+  const char* scales = reinterpret_cast<const char*>(a.scales) + at * (a.k / KC * SB);
+  const uint16_t* x = a.x + (size_t)xrow * a.k;
+  const size_t plane = (size_t)a.pairs * a.k;
+  double sum = 0.0;
+#pragma unroll 1
+  for (uint32_t k = k0; k < k1 && sum == sum; k += 8) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(packed + (k >> 1));
+    const char* sp = scales + k / KC * SB;
+    float scale, zero = FMT == kINT4 ? 8.0f : 0.0f;
+    if constexpr (FMT == kMXFP4) {
+      scale = e8m0_value(*reinterpret_cast<const uint8_t*>(sp));
+    } else if constexpr (FMT == kINT4) {
+      scale = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(sp) << 16);
+    } else {
+      const uint32_t word = *reinterpret_cast<const uint32_t*>(sp);
+      scale = __uint_as_float(FMT == kINT4A ? word << 16 : word);
+      if constexpr (FMT == kINT4A) zero = (float)((word >> 16) & 15u);
+    }
+#pragma unroll 1
+    for (uint32_t i = 0; i < 8; ++i) {
+      const uint32_t nibble = (w >> (4u * (i ^ 1u))) & 15u;  // the high nibble first
+      float code;
+      if constexpr (is_g128(FMT)) {
+        code = (float)nibble - zero;
+      } else {
+        code = __uint_as_float(FMT == kNF4 ? c_moe_nf4[nibble] : c_moe_fp4[nibble]);
+      }
+      float v;
+      if constexpr (XT == kF16) {
+        v = (float)reinterpret_cast<const _Float16*>(x)[k + i];
+      } else {
+        v = __uint_as_float((uint32_t)x[k + i] << 16);
+        if constexpr (NP == 3)
+          v += __uint_as_float((uint32_t)x[plane + k + i] << 16) + __uint_as_float((uint32_t)x[2 * plane + k + i] << 16);
+      }
+      sum += (double)code * scale * v;
+    }
+  }
+  return (float)sum;
+}
+
+// NaN into `odd` if v is not finite.
+__device__ inline void watch(float& odd, float v) { odd = __builtin_fmaf(v, 0.0f, odd); }
+
+// The launch's arguments read anew from memory: what looks at results again holds no register for it before.
+__device__ __attribute__((always_inline)) inline MoeArgs args_again() {
+  uint64_t p = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  MoeArgs a;
+  __builtin_memcpy(&a, (const MoeArgs*)reinterpret_cast<const __attribute__((address_space(4))) MoeArgs*>(p), sizeof(a));
+  return a;
+}
+
+// h of one row and pair, and a partial result, looked at again.  (h is not finite where gate or up is not.)
+template <int FMT, int XT>
+__device__ __attribute__((always_inline)) inline void settle_h(const MoeArgs& a, int e, uint32_t pair, uint32_t row) {
+  const uint32_t inter = a.n >> 1;
+  if ((a.h[(size_t)pair * inter + row] & 0x7F80u) != 0x7F80u) return;
+  float gate = 0.0f, up = 0.0f;
+#pragma unroll 1
+  for (uint32_t r = 0; r < 2; ++r) {
+    const float v = defined_sum<FMT, XT, 1>(a, e, r * inter + row, pair / a.top_k, 0, a.k);
+    gate = r == 0 ? v : gate;
+    up = v;
+  }
+  store_h(a, pair, row, inter, gate, up);
+}
+
+template <int FMT>
+__device__ __attribute__((always_inline)) inline void settle_part(const MoeArgs& a, int e, uint32_t pair, uint32_t row) {
+  float* p = a.part + (size_t)pair * a.n + row;
+  if (!__builtin_isfinite(*p)) *p = defined_sum<FMT, kBF16, 3>(a, e, row, pair, 0, a.k);
 }
 
 template <int DIR, int FMT, int XT, int NT, int KW>
@@ -476,6 +551,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 4 : 2) moe_kernel(MoeAr
 
   MoeQuad W0, W1;
   Sc held_scales, next_scales;
+  float odd_sum = 0.0f;  // NaN: a sum of this thread's was not finite
   uint32_t count = 1;
   for (uint32_t c0 = 0; c0 < count; c0 += cols) {
     // The expert's pairs, before any other vector load of the chunk: loads complete in order, and what
@@ -561,10 +637,6 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 4 : 2) moe_kernel(MoeAr
       for (uint32_t w = 0; w < (uint32_t)KW; ++w) v += buf[(w * RT + tile % RT) * (NT * 256u) + at];
       return kTable ? v * (1.0f / kNf4Factor) : v;
     };
-    auto with_nan = [&](float v, uint32_t row) __attribute__((always_inline)) {
-      return with_nan_scales<FMT>(v, reinterpret_cast<const uint8_t*>(a.scales) + ((size_t)e * a.n + row) * spitch, spitch);
-    };
-
     uint32_t held = 0xFFFFFFFFu;  // first quad (of each K group) of the window in LDS
     uint32_t buffer = 0;
     for (uint32_t ug = blockIdx.x; ug < ngroups; ug += gridDim.x) {
@@ -602,8 +674,10 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 4 : 2) moe_kernel(MoeAr
         for (uint32_t i = (uint32_t)tid; i < rows * have; i += kMoeThreads) {
           const uint32_t j = i / rows, row = i - j * rows, tile = row / 16u * 2u, n = row & 15u;
           const int pair = __shfl(list, (int)j);  // (rows * have is a multiple of 16: lanes 0 .. 15 take part)
-          const float gate = with_nan(tile_value(buf, tile, n, j / 16u, j & 15u), row0 + row);
-          const float up = with_nan(tile_value(buf, tile + 1u, n, j / 16u, j & 15u), inter + row0 + row);
+          const float gate = tile_value(buf, tile, n, j / 16u, j & 15u);
+          const float up = tile_value(buf, tile + 1u, n, j / 16u, j & 15u);
+          watch(odd_sum, gate);
+          watch(odd_sum, up);
           store_h(a, (uint32_t)pair, row0 + row, inter, gate, up);
         }
       } else {
@@ -617,11 +691,38 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 4 : 2) moe_kernel(MoeAr
           } else {
             v = tile_value(buf, tile, n, 0, j) + (tile_value(buf, tile, n, 1, j) + tile_value(buf, tile, n, 2, j));
           }
-          a.part[(size_t)(uint32_t)pair * a.n + row0 + row] = with_nan(v, row0 + row);
+          watch(odd_sum, v);
+          a.part[(size_t)(uint32_t)pair * a.n + row0 + row] = v;
         }
       }
     }
     if (c0 + cols < count) __syncthreads();  // the window and the sums have been read
+  }
+  if (__any(odd_sum != odd_sum)) {  // this wave's results once more, walked as above
+    const MoeArgs b = args_again();
+    const uint32_t ngroups = (b.tiles + RT - 1) / RT;
+    int list;
+    count = 1;
+#pragma unroll 1
+    for (uint32_t c0 = 0; c0 < count; c0 += b.cols) {
+      count = scan_pairs(b.ids, b.pairs, (int)blockIdx.y, c0, b.cols, lane, list);
+      const uint32_t have = min(b.cols, count - c0);
+#pragma unroll 1
+      for (uint32_t ug = blockIdx.x; ug < ngroups; ug += gridDim.x) {
+        constexpr uint32_t kHeight = DIR == kUp ? 8u : 16u;  // result rows of a tile
+        const uint32_t tile0 = ug * RT, row0 = tile0 * kHeight, rows = min(RT, b.tiles - tile0) * kHeight;
+#pragma unroll 1
+        for (uint32_t i = (uint32_t)tid; i < rows * have; i += kMoeThreads) {
+          const uint32_t j = i / rows, row = row0 + i - j * rows;
+          const uint32_t pair = (uint32_t)__shfl(list, (int)j);
+          if constexpr (DIR == kUp) {
+            settle_h<FMT, XT>(b, (int)blockIdx.y, pair, row);
+          } else {
+            settle_part<FMT>(b, (int)blockIdx.y, pair, row);
+          }
+        }
+      }
+    }
   }
 }
 
@@ -754,8 +855,7 @@ __global__ void __launch_bounds__(kMoeThreads, 4) moe_pair_kernel(MoeArgs a) {
       for (int r = 0; r < 2; ++r) {
         float s = acc[r][0][0];  // all of D's rows are alike
         if constexpr (kTable) s *= 1.0f / kNf4Factor;
-        sums[wave][r][lane] = with_nan_scales<FMT>(
-            s, reinterpret_cast<const uint8_t*>(a.scales) + (row0[r] + (uint32_t)lane) * spitch, spitch);
+        sums[wave][r][lane] = s;
       }
     }
   }
@@ -768,6 +868,7 @@ __global__ void __launch_bounds__(kMoeThreads, 4) moe_pair_kernel(MoeArgs a) {
       up += sums[w * SL + sl][1][lane];
     }
     store_h(a, pair, tile * 16u + (uint32_t)lane, inter, gate, up);
+    if (!__builtin_isfinite(gate) || !__builtin_isfinite(up)) settle_h<FMT, XT>(args_again(), e, pair, tile * 16u + (uint32_t)lane);
   }
 }
 
@@ -848,6 +949,7 @@ __global__ void __launch_bounds__(kMoeThreads, 4) moe_token_kernel(MoeArgs a) {
   const uint32_t tile = blockIdx.x;
 
   float y = 0.0f;  // lanes 0 .. 15: this wave's share of row 16 tile + lane
+  float odd_sum = 0.0f;  // NaN: one of its products was not finite
   for (uint32_t slot = sl; slot < a.top_k; slot += SL) {
     const int e = __builtin_amdgcn_readlane(id, (int)slot);
     if ((uint32_t)e >= a.experts) continue;
@@ -925,10 +1027,22 @@ __global__ void __launch_bounds__(kMoeThreads, 4) moe_token_kernel(MoeArgs a) {
     // rows 0, 1, 2 of D are the planes' products: lanes 0 .. 15, i = 0, 1, 2
     float v = acc[0][0] + (acc[0][1] + acc[0][2]);
     if constexpr (kTable) v *= 1.0f / kNf4Factor;
-    if (lane < 16)
-      v = with_nan_scales<FMT>(v, reinterpret_cast<const uint8_t*>(a.scales) + (row0 + (uint32_t)m) * spitch, spitch);
+    watch(odd_sum, v);
     const float w = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(weight), (int)slot));
     y = __builtin_fmaf(w, v, y);
+  }
+  if (lane < 16 && odd_sum != odd_sum) {  // this wave's slots and K range once more
+    const MoeArgs b = args_again();
+    const uint32_t wave2 = threadIdx.x >> 6, k0 = min(b.k, wave2 / SL * b.qpk * 256u);
+    y = 0.0f;
+#pragma unroll 1
+    for (uint32_t slot = wave2 % SL; slot < b.top_k; slot += SL) {
+      const uint32_t pair = blockIdx.y * b.top_k + slot;
+      const int e = b.ids[pair];
+      if ((uint32_t)e < b.experts)
+        y = __builtin_fmaf(b.weights[pair], defined_sum<FMT, kBF16, 3>(b, e, blockIdx.x * 16u + (uint32_t)lane, pair, k0,
+                                                                       min(b.k, k0 + b.qpk * 256u)), y);
+    }
   }
   if (lane < 16) sums[wave][lane] = y;
   __syncthreads();

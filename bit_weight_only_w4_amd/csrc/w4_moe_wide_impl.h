@@ -165,9 +165,10 @@ struct MoeWide {
   static_assert(kWideThreads == 16 * 16, "a thread takes one piece of each 16 window rows");
 
   // 32 rows a wave (unit `unit`) of expert e, on the chunk's pairs: `list` holds them in lanes, `have` of
-  // them.
+  // them.  odd_sum becomes NaN if a sum of this lane's is not finite.
   static __device__ __attribute__((always_inline)) inline void run(const MoeArgs& a, int e, uint32_t unit, int list,
-                                                                   uint32_t have, uint8_t* smem, const uint32_t* tab) {
+                                                                   uint32_t have, uint8_t* smem, const uint32_t* tab,
+                                                                   float& odd_sum) {
     using Sc = MoeScales<FMT>;
     const int tid = threadIdx.x, lane = tid & 63;
     const int g = lane >> 4, m = lane & 15;
@@ -285,10 +286,10 @@ struct MoeWide {
       if (q + 1 < nq) step(q + 1, W1, std::integral_constant<int, 1>{});
     }
 
-    auto finished = [&](float v, int r) __attribute__((always_inline)) {
+    auto finished = [&](float v) __attribute__((always_inline)) {
       if constexpr (FMT == kNF4) v *= 1.0f / kNf4Factor;
-      const uint32_t row = row0[r] + (uint32_t)m;
-      return with_nan_scales<FMT>(v, reinterpret_cast<const uint8_t*>(a.scales) + ((size_t)e * a.n + row) * spitch, spitch);
+      watch(odd_sum, v);
+      return v;
     };
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -298,11 +299,12 @@ struct MoeWide {
         const uint32_t pair = (uint32_t)__shfl(list, (int)col);
         if (live && col < have) {
           if constexpr (DIR == kUp) {
-            store_h(a, pair, row0[0] + (uint32_t)m, a.n >> 1, finished(acc[0][t][i], 0), finished(acc[1][t][i], 1));
+            const float gate = finished(acc[0][t][i]);
+            store_h(a, pair, row0[0] + (uint32_t)m, a.n >> 1, gate, finished(acc[1][t][i]));
           } else {
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-              a.part[(size_t)pair * a.n + row0[r] + (uint32_t)m] = finished(acc[r][t][i], r);
+              a.part[(size_t)pair * a.n + row0[r] + (uint32_t)m] = finished(acc[r][t][i]);
           }
         }
       }
@@ -322,17 +324,40 @@ __global__ void __launch_bounds__(kWideThreads, DIR == kUp && NT == 1 ? 3 : 2) m
   if constexpr (kTable) fill_moe_table<XT, kWideThreads>(tab);
   const uint32_t lane = threadIdx.x & 63u;
   const uint32_t unit = blockIdx.x * kWideWaves + (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  float odd_sum = 0.0f;
   for (uint32_t c0 = blockIdx.z * kCols; c0 < count; c0 += gridDim.z * kCols) {
     const uint32_t have = min(kCols, count - c0);
     const int list = lane < have ? a.order[first + c0 + lane] : 0;
     if (NT > 3 && have > 48) {
-      MoeWide<DIR, FMT, XT, NT>::run(a, e, unit, list, have, smem, tab);
+      MoeWide<DIR, FMT, XT, NT>::run(a, e, unit, list, have, smem, tab, odd_sum);
     } else if (NT > 2 && have > 32) {
-      MoeWide<DIR, FMT, XT, NT < 3 ? NT : 3>::run(a, e, unit, list, have, smem, tab);
+      MoeWide<DIR, FMT, XT, NT < 3 ? NT : 3>::run(a, e, unit, list, have, smem, tab, odd_sum);
     } else if (NT > 1 && have > 16) {
-      MoeWide<DIR, FMT, XT, NT < 2 ? NT : 2>::run(a, e, unit, list, have, smem, tab);
+      MoeWide<DIR, FMT, XT, NT < 2 ? NT : 2>::run(a, e, unit, list, have, smem, tab, odd_sum);
     } else {
-      MoeWide<DIR, FMT, XT, 1>::run(a, e, unit, list, have, smem, tab);
+      MoeWide<DIR, FMT, XT, 1>::run(a, e, unit, list, have, smem, tab, odd_sum);
+    }
+  }
+  if (__any(odd_sum != odd_sum)) {  // this wave's results once more, each by the lane that stored it
+    const MoeArgs b = args_again();
+    const uint32_t base = (uint32_t)b.start[blockIdx.y], pairs = (uint32_t)b.start[blockIdx.y + 1] - base;
+    const uint32_t u = blockIdx.x * kWideWaves + (threadIdx.x >> 6), m = threadIdx.x & 15u;
+    if (u < b.tiles / 2) {
+#pragma unroll 1
+      for (uint32_t c0 = blockIdx.z * kCols; c0 < pairs; c0 += gridDim.z * kCols) {
+#pragma unroll 1
+        for (uint32_t i = 0; i < 4u * NT; ++i) {
+          const uint32_t col = c0 + 16u * (i >> 2) + 4u * ((threadIdx.x & 63u) >> 4) + (i & 3u);
+          if (col >= pairs) continue;
+          const uint32_t pair = (uint32_t)b.order[base + col];
+          if constexpr (DIR == kUp) {
+            settle_h<FMT, XT>(b, (int)blockIdx.y, pair, u * 16u + m);
+          } else {
+#pragma unroll 1
+            for (uint32_t r = 0; r < 2; ++r) settle_part<FMT>(b, (int)blockIdx.y, pair, u * 32u + 16u * r + m);
+          }
+        }
+      }
     }
   }
 }

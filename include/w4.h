@@ -560,9 +560,10 @@ int w4_moe_route(const void* logits, int logits_type, int64_t tokens, int64_t ex
  *   workspace  device memory of at least w4_moe_workspace_bytes(...) bytes, 16-byte aligned; scratch
  *            on entry and exit; must not overlap an input; two calls in flight must not share it
  * fp32 accumulation; the products between the two matrices are kept to 24 bits, so y is exact up
- * to fp32 sums (NF4: codes to 4e-7 of their rms).  INT4 and INT4A codes are multiplied as q + 16 with the
- * offset taken off beside, so bf16 activations beyond 2^115 in magnitude may overflow where the
- * sum itself would not.  The order of every sum is fixed: the same call gives the same bits.  Asynchronous on `stream`. */
+ * to fp32 sums (NF4: codes to 4e-7 of their rms).  Infinities and NaN of the activations, of a
+ * product between the matrices that leaves fp32's range and of MXFP4's scale byte 255 come out where the
+ * formula has them: a product's sum that is not finite in fp32 is computed again, in 64 bits, which takes longer.
+ * The order of every sum is fixed: the same call gives the same bits.  Asynchronous on `stream`. */
 int w4_moe(const void* x, const int32_t* ids, const float* weights, const uint8_t* gate_up,
            const void* gate_up_scales, const uint8_t* down, const void* down_scales, int fmt,
            int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k, float* y,
