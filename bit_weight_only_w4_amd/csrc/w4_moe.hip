@@ -252,16 +252,20 @@ hipError_t launch_moe_route(const void* logits, int type, int64_t tokens, int64_
   return hipErrorInvalidValue;
 }
 
-// Many tokens: from three pairs an expert on, and from eight where the experts are too few to fill the
-// card without K groups (down: a workgroup has 128 rows).  Measured on MI355X against the kernels with K
-// groups (us for the layer): 8 of 128 experts, 2048 x 768, MXFP4, at 2 / 4 / 8 / 16 pairs an expert 96 / 105 /
-// 106 / 131 against 84 / 113 / 145 / 251; 1 of 32, 2048 x 2048, FP4, 66 / 72 / 74 / 92 against 59 / 72 / 79 /
-// 146.  Few experts: 2 of 8, 1024 x 768, FP4, at 4 / 8 / 16 pairs 21 / 21 / 29 against 19 / 23 / 37; 2 of 4,
-// 2048 x 2048, NF4, 47 / 47 / 50 against 29 / 46 / 75; one expert of 2048 x 4096, INT4, 48 / 49 / 49 against
-// 25 / 37 / 60.
+// Many tokens: from three pairs an expert on where the experts fill the card without K groups (down: a workgroup has
+// 128 rows).  Measured on MI355X against the kernels with K groups (us for the layer): 8 of 128 experts, 2048 x 768,
+// MXFP4, at 2 / 4 / 8 / 16 pairs an expert 96 / 105 / 106 / 131 against 84 / 113 / 145 / 251; 1 of 32, 2048 x 2048,
+// FP4, 66 / 72 / 74 / 92 against 59 / 72 / 79 / 146.
+// Else from eight pairs on: 2 of 8, 1024 x 768, FP4, at 6 / 8 / 12 / 16 pairs 21 / 21 / 22 / 24 against 20 / 22 / 27 /
+// 35; 2 of 8, 1536 x 2048, NF4, 45 / 45 / 47 / 48 against 46 / 48 / 68 / 83; 4 of 16, 1024 x 512, INT4, 21 / 21 / 21 /
+// 24 against 19 / 20 / 27 / 33.  With fewer than eight experts the sorted kernels have too few workgroups for longer,
+// and start at 14: at 8 / 12 / 14 / 16 / 20 pairs one expert of 2048 x 4096, INT4, 50 / 50 / 50 / 50 / 53 against 35 /
+// 40 / 54 / 56 / 91; one of 4096 x 1408, MXFP4, 39 / 39 / 40 / 40 / 45 against 25 / 29 / 32 / 34 / 52; 1 of 2, 4096 x
+// 2048, NF4, 61 / 63 / 65 / 66 / 66 against 40 / 53 / 63 / 73 / 76; 2 of 4, 2048 x 2048, NF4, 48 / 48 / 48 / 50 / 51
+// against 44 / 48 / 50 / 74 / 82.
 static bool moe_wide(int64_t pairs, int64_t experts, int64_t hidden) {
   const bool fills = 4 * (hidden / 128) * experts >= 3 * device_cu_count();
-  return pairs >= (fills ? 3 : 8) * experts;
+  return pairs >= (fills ? 3 : experts < 8 ? 14 : 8) * experts;
 }
 
 // The planes of h (three bf16 values per pair and row), the partial results, the sorted pairs and the

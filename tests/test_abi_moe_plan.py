@@ -70,3 +70,12 @@ def test_refusals():
         w4.moe_plan("int4_f16", 1, 64, 128, 1, 1)
     assert w4.lib().w4_moe_plan(9, 1, 64, 64, 1, 1, None, None, None, None, None) == -4
     assert w4.lib().w4_moe_plan(1, 1, 64, 64, 1, 1, None, None, None, None, None) == 0
+
+
+@pytest.mark.parametrize("tokens,experts,top_k,kind", [
+    (8, 1, 1, 1), (13, 1, 1, 1), (14, 1, 1, 2), (16, 2, 1, 1), (27, 2, 1, 1), (28, 2, 1, 2), (16, 4, 2, 1),
+    (27, 4, 2, 1), (28, 4, 2, 2), (31, 8, 2, 1), (32, 8, 2, 2), (15, 16, 8, 1), (16, 16, 8, 2), (95, 256, 8, 1),
+    (96, 256, 8, 2)])
+def test_sorted_pairs_start_where_they_were_measured_to_pay(tokens, experts, top_k, kind):
+    """2048 x 2048: fewer than eight experts from 14 pairs each, more from eight, those that fill the card from three."""
+    assert _w4().moe_plan("int4_f16", tokens, 1024 if experts == 16 else 2048, 2048, experts, top_k)["kind"] == kind

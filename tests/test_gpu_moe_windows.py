@@ -22,3 +22,16 @@ def test_windows_of_three_planes(fmt, tokens, hidden, inter, experts, top_k):
     assert p["down_window"] < 3 * tokens * quads * 512  # more than one window
     c = mu.case(fmt, tokens, hidden, inter, experts, top_k, seed=tokens + inter)
     mu.check(w4.moe(*mu.to_device(c, dev)), c)
+
+
+@pytest.mark.parametrize("fmt", ["nf4_bf16", "int4a_f16", "mxfp4_f16"])
+@pytest.mark.parametrize("tokens,hidden,inter,experts,top_k,kind", [
+    (8, 512, 640, 1, 1, 1), (13, 2304, 1280, 1, 1, 1), (14, 512, 640, 1, 1, 2), (27, 256, 640, 2, 1, 1),
+    (28, 256, 640, 2, 1, 2), (26, 384, 2304, 4, 2, 1), (6, 640, 384, 1, 2, 1), (7, 640, 384, 1, 2, 2)])
+def test_few_experts_around_the_rule(fmt, tokens, hidden, inter, experts, top_k, kind):
+    import bit_weight_only_w4_amd as w4
+
+    dev = g.device()
+    assert w4.moe_plan(fmt, tokens, hidden, inter, experts, top_k)["kind"] == kind
+    c = mu.case(fmt, tokens, hidden, inter, experts, top_k, seed=tokens + inter)
+    mu.check(w4.moe(*mu.to_device(c, dev)), c)
