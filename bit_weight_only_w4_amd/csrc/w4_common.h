@@ -198,7 +198,7 @@ hipError_t launch_dense_gemv(int fmt, const uint16_t* x, const uint16_t* w_hat, 
                              int64_t k, int64_t b, float* y, hipStream_t s);
 // MFMA path.  splits > 1 (one member only): K in `splits` ranges of whole quads (fewer when the
 // quads do not fill them), each range's partial sums in ws[split][B][N] (fp32), then the
-// fixed-order reduction into y; mfma_splits_used gives the number of ranges (0: no plan).
+// fixed-order reduction into y.
 hipError_t launch_mfma(int fmt, const uint16_t* x, const uint8_t* packed, const void* scales,
                        int64_t n, int64_t k, int64_t b, float* y, hipStream_t s, int splits = 1,
                        float* ws = nullptr);
@@ -206,7 +206,6 @@ hipError_t launch_mfma_members(int fmt, const uint16_t* x, int groups, const uin
                                const void* const* scales, const int64_t* ns, float* const* y,
                                int64_t k, int64_t b, hipStream_t s, int splits = 1,
                                float* ws = nullptr);
-int mfma_splits_used(int64_t n, int64_t k, int64_t b, int splits);
 // Tiled GEMM.  splits > 1: K in up to `splits` ranges of whole 64-weight blocks on grid.y
 // (gemm_splits_used gives how many), each range's partial sums in ws[range][M][N] (fp32), then the
 // fixed-order reduction into y.

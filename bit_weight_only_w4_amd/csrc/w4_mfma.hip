@@ -181,11 +181,4 @@ hipError_t launch_mfma(int fmt, const uint16_t* x, const uint8_t* packed, const 
   return launch_mfma_members(fmt, x, 1, &packed, &scales, &n, &y, k, b, s, splits, ws);
 }
 
-int mfma_splits_used(int64_t n, int64_t k, int64_t b, int splits) {
-  if (splits <= 1) return 1;
-  MfmaPlan p;
-  if (!plan_mfma(&n, 1, k, b, splits, kMaxTiles, &p)) return 0;
-  return p.splits;
-}
-
 }  // namespace w4

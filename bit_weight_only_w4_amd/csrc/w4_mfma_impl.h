@@ -433,7 +433,6 @@ __global__ void __launch_bounds__(kThreads, min_waves(T)) mfma_kernel(MfmaArgs a
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(one[i], sc[i], acc[t][i]);
           }
-          if constexpr (T == 8) __builtin_amdgcn_sched_barrier(0);
           continue;
         }
         uint32_t p1[4], p2[4];
