@@ -104,8 +104,8 @@ __global__ void __launch_bounds__(256) route_kernel(const void* __restrict__ log
 }
 
 template <int TYPE>
-hipError_t route_type(const void* logits, uint32_t tokens, uint32_t experts, uint32_t top_k,
-                      int renorm, int32_t* ids, float* weights, hipStream_t s) {
+hipError_t route_slice(const void* logits, uint32_t tokens, uint32_t experts, uint32_t top_k,
+                       int renorm, int32_t* ids, float* weights, hipStream_t s) {
   const uint32_t waves = tokens < 4 ? tokens : 4;
   const dim3 grid((tokens + waves - 1) / waves), block(64 * waves);
 #define W4_ROUTE(NV)                                                                              \
@@ -121,6 +121,21 @@ hipError_t route_type(const void* logits, uint32_t tokens, uint32_t experts, uin
   W4_ROUTE(16)
 #undef W4_ROUTE
   return hipErrorInvalidValue;
+}
+
+// A launch's threads, 64 a token, have to number fewer than 2^32: slices of 2^25 tokens.
+template <int TYPE>
+hipError_t route_type(const void* logits, uint32_t tokens, uint32_t experts, uint32_t top_k,
+                      int renorm, int32_t* ids, float* weights, hipStream_t s) {
+  constexpr uint32_t kSlice = 1u << 25;
+  constexpr size_t kBytes = TYPE == W4_LOGITS_F32 ? 4 : 2;
+  for (uint32_t t = 0; t < tokens; t += kSlice) {
+    const hipError_t e = route_slice<TYPE>(reinterpret_cast<const char*>(logits) + (size_t)t * experts * kBytes,
+                                           std::min(kSlice, tokens - t), experts, top_k, renorm,
+                                           ids + (size_t)t * top_k, weights + (size_t)t * top_k, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // y[t] = sum over slots j, in order, of weights[t, j] * part[t * top_k + j]; absent slots add
