@@ -182,6 +182,7 @@ bool plan_gemv(int64_t n, int64_t k, int b, int splits, GemvPlan* out, bool grou
   } else {
     team = std::max(64, next_pow2((cps + 2) / 3));
   }
+  team = std::min(team, kGemvMaxThreads);  // rows past 3 chunks a lane: more chunks a lane instead
   while (team < kGemvMaxThreads && (cps + team - 1) / team > itmax) team *= 2;
   const int iters = (cps + team - 1) / team;
   if (iters > itmax) return false;
