@@ -395,25 +395,33 @@ __device__ __attribute__((always_inline)) inline float defined_sum(const MoeArgs
       scale = __uint_as_float(FMT == kINT4A ? word << 16 : word);
       if constexpr (FMT == kINT4A) zero = (float)((word >> 16) & 15u);
     }
-#pragma unroll 1
-    for (uint32_t i = 0; i < 8; ++i) {
-      const uint32_t nibble = (w >> (4u * (i ^ 1u))) & 15u;  // the high nibble first
-      float code;
-      if constexpr (is_g128(FMT)) {
-        code = (float)nibble - zero;
-      } else {
-        code = __uint_as_float(FMT == kNF4 ? c_moe_nf4[nibble] : c_moe_fp4[nibble]);
+    float v[8], code[8];
+    auto halves = [&](const uint16_t* p, auto add) __attribute__((always_inline)) {
+      const uint4 q = *reinterpret_cast<const uint4*>(p + k);
+      const uint32_t d[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) add(v[i], (d[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
+    };
+    if constexpr (XT == kF16) {
+      halves(x, [](float& o, uint32_t b) { o = (float)__builtin_bit_cast(_Float16, (uint16_t)b); });
+    } else {
+      halves(x, [](float& o, uint32_t b) { o = __uint_as_float(b << 16); });
+      if constexpr (NP == 3) {
+        halves(x + plane, [](float& o, uint32_t b) { o += __uint_as_float(b << 16); });
+        halves(x + 2 * plane, [](float& o, uint32_t b) { o += __uint_as_float(b << 16); });
       }
-      float v;
-      if constexpr (XT == kF16) {
-        v = (float)reinterpret_cast<const _Float16*>(x)[k + i];
-      } else {
-        v = __uint_as_float((uint32_t)x[k + i] << 16);
-        if constexpr (NP == 3)
-          v += __uint_as_float((uint32_t)x[plane + k + i] << 16) + __uint_as_float((uint32_t)x[2 * plane + k + i] << 16);
-      }
-      sum += (double)code * scale * v;
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t nibble = (w >> (4 * (i ^ 1))) & 15u;  // the high nibble first
+      if constexpr (is_g128(FMT)) {
+        code[i] = (float)nibble - zero;
+      } else {
+        code[i] = __uint_as_float(FMT == kNF4 ? c_moe_nf4[nibble] : c_moe_fp4[nibble]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += (double)code[i] * scale * v[i];
   }
   return (float)sum;
 }
