@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, min_waves(T)) mfma_kernel(MfmaArgs a
     // multiplied (inside the matrix their bytes are the next row's; zeroing them here would make
     // the loop wait for the load).  INT4: two bf16 scales, 2-byte aligned, two loads, moved to the
     // high half when multiplied (for the same reason).  MXFP4: eight bytes, 2-byte aligned, as the
-    // three dwords around them in one load (28672 x 8192, B = 8 / 16 / 32: 45 / 50 / 64 us; four 2-byte
+    // three dwords around them in one load (28672 x 8192, B = 8 / 16 / 32: 42 / 49 / 64 us; four 2-byte
     // loads, which touch the same 16 lines each, 60 / 77 / 66).
     if constexpr (kMX) {
       const uint32_t off = offset_or_oob(qb < nblocks, (sbase + cur.odd) & ~3u);

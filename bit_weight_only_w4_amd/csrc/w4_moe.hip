@@ -269,8 +269,8 @@ hipError_t launch_moe_route(const void* logits, int type, int64_t tokens, int64_
 
 // Many tokens: from three pairs an expert on where the experts fill the card without K groups (down: a workgroup has
 // 128 rows).  Measured on MI355X against the kernels with K groups (us for the layer): 8 of 128 experts, 2048 x 768,
-// MXFP4, at 2 / 4 / 8 / 16 pairs an expert 96 / 105 / 106 / 131 against 84 / 113 / 145 / 251; 1 of 32, 2048 x 2048,
-// FP4, 66 / 72 / 74 / 92 against 59 / 72 / 79 / 146.
+// MXFP4, at 2 / 4 / 8 / 16 pairs an expert 95 / 99 / 104 / 130 against 83 / 109 / 140 / 239; 1 of 32, 2048 x 2048,
+// FP4, 68 / 72 / 74 / 93 against 58 / 68 / 78 / 140.
 // Else from eight pairs on: 2 of 8, 1024 x 768, FP4, at 6 / 8 / 12 / 16 pairs 21 / 21 / 22 / 24 against 20 / 22 / 27 /
 // 35; 2 of 8, 1536 x 2048, NF4, 45 / 45 / 47 / 48 against 46 / 48 / 68 / 83; 4 of 16, 1024 x 512, INT4, 21 / 21 / 21 /
 // 24 against 19 / 20 / 27 / 33.  With fewer than eight experts the sorted kernels have too few workgroups for longer,
@@ -292,12 +292,10 @@ size_t moe_workspace(int64_t pairs, int64_t hidden, int64_t inter, int64_t exper
 
 // Fewer pairs than experts: a wave per pair in both launches, the second combining.  Measured on MI355X
 // against the shared products and their third launch (us): 8 of 128 experts, 2048 x 768, MXFP4, at 2 / 4 /
-// 8 / 12 / 16 / 32 tokens 18.2 / 26.8 / 45.8 / 63.6 / 77.6 / 143.7 against 24.3 / 32.2 / 48.7 / 66.2 / 77.4 /
-// 86.5; 4 of 64, 1536 x 1408, INT4, at 4 / 8 / 12 / 16 tokens 23.1 / 35.5 / 51.4 / 63.1 against 30.0 /
-// 41.3 / 52.2 / 59.5.
+// 8 / 12 / 16 / 32 tokens 18 / 27 / 48 / 63 / 78 / 140 against 54 / 60 / 64 / 66 / 75 / 83; 4 of 64, 1536 x 1408,
+// INT4, at 4 / 8 / 12 / 16 tokens 23 / 34 / 49 / 60 against 54 / 55 / 58 / 59.
 // One slot a token pays up to half as many pairs as experts: 1 of 32, 2048 x 2048, FP4, at 12 / 16 / 24 tokens
-// 33.1 / 42.6 / 60.0 against 38.4 / 43.2 / 44.7; 1 of 64, 1024 x 1024, INT4, at 24 / 32 / 48 25.9 / 32.4 / 45.0
-// against 30.2 / 31.0 / 31.5.
+// 33 / 42 / 60 against 38 / 43 / 44; 1 of 64, 1024 x 1024, INT4, at 24 / 32 / 48 26 / 33 / 46 against 30 / 31 / 32.
 static bool moe_per_pair(int64_t tokens, int64_t experts, int64_t top_k) {
   const int64_t pairs = tokens * top_k;
   return tokens == 1 || (pairs < experts && (top_k > 1 || 2 * pairs <= experts));

@@ -38,8 +38,8 @@
 //     tokens nothing; from five tokens on a plane is a tile of its own.
 //   * A group's sums go through LDS, where every thread takes its share of the results: the K groups
 //     are added in group order, gate meets up, and a row's values are stored side by side.
-// Measured on MI355X, 32 tokens, 8 of 128 experts, 2048 x 768, MXFP4 (280 MB of weights): up 42 us (4.4 TB/s),
-// down 36 us (2.6 TB/s: rows of three quads leave little to run ahead with), where a copy reaches 4.8 TB/s.
+// Measured on MI355X, 32 tokens, 8 of 128 experts, 2048 x 768, MXFP4 (280 MB of weights): up 44 us (4.3 TB/s),
+// down 39 us (2.4 TB/s: rows of three quads leave little to run ahead with), where a copy reaches 4.8 TB/s.
 #pragma once
 #include <type_traits>
 
@@ -738,8 +738,8 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 4 : 2) moe_kernel(MoeAr
 // window that waves share.  A wave takes one pair; tokens that share an expert read its weights
 // again, mostly from L2.  SL = 8 / KW pairs side by side in a workgroup, K in KW ranges; a wave's
 // window holds what it needs itself, and no barrier stands before the sums.  Measured on MI355X, 1 token, 8 of 64
-// experts, 2048 x 1024, INT4: up 8.1 us (2.1 TB/s), down 6.6 us (1.3 TB/s); 5 tokens, 4 of 60, 1536 x 1408,
-// NF4: 15.9 and 10.3 us.  Bound by one load's latency after another: arguments, ids, weights.
+// experts, 2048 x 1024, INT4: up 8.6 us (2.0 TB/s), down 7.5 us (1.2 TB/s); 5 tokens, 4 of 60, 1536 x 1408,
+// NF4: 17.3 and 10.8 us.  Bound by one load's latency after another: arguments, ids, weights.
 
 // Up: 16 rows of h of SL slots of one token; a wave multiplies its expert's gate and up tile by x.
 constexpr uint32_t kPairQuads = 8;  // quads of a wave's window

@@ -20,8 +20,8 @@
 //     streaming hint).
 //   * The pairs come sorted by expert (order_kernel); a chunk's columns are cut to what it has, in
 //     tiles of 16.
-// Measured on MI355X, 512 tokens, 6 of 64 experts, 1536 x 1408, FP4: up 81 us (328 TFLOP/s), down 90 us
-// (148 TFLOP/s of the layer's, 443 with the planes).  Bound by waiting, not by the matrix units: the
+// Measured on MI355X, 512 tokens, 6 of 64 experts, 1536 x 1408, FP4: up 84 us (315 TFLOP/s), down 93 us
+// (142 TFLOP/s of the layer's, 427 with the planes).  Bound by waiting, not by the matrix units: the
 // registers of two row tiles in flight leave a SIMD two waves, which do not cover LDS and barrier
 // latencies.
 #pragma once
@@ -382,12 +382,12 @@ hipError_t launch_moe_wide_one(const MoeArgs& a, hipStream_t s) {
 
 // Up: 16 columns a chunk, three workgroups to a CU, up to 12 pairs an expert, else up to 64.  Measured on
 // MI355X (us for the layer with 16 pairs a down chunk, 16 columns against 64): 8 of 128 experts, 2048 x 768, MXFP4, at 4 / 8 / 16 / 32
-// pairs an expert 98 / 104 / 154 / 234 against 109 / 118 / 144 / 200; 4 of 64, 1536 x 1408, INT4, 72 / 78 /
-// 116 / 173 against 79 / 85 / 109 / 145.  NF4, whose table takes 32 KiB: 32 columns always.
+// pairs an expert 110 / 110 / 161 / 244 against 114 / 113 / 152 / 200; 4 of 64, 1536 x 1408, INT4, 77 / 83 /
+// 123 / 190 against 82 / 86 / 112 / 155.  NF4, whose table takes 32 KiB: 32 columns always.
 // Down: 16 pairs a chunk up to 12 pairs an expert, or where chunks of 32 would leave CUs without one; else
-// 32.  Measured (16 against 32): 6 of 64, 1536 x 1408, FP4, at 24 / 48 pairs an expert 136 / 195 against 122 /
-// 171; 8 of 128, 2048 x 768, MXFP4, at 16 / 32 pairs 167 / 220 against 149 / 203; 2 of 8, 1536 x 2048, NF4,
-// at 16 / 32 / 64 / 128 pairs 48 / 56 / 71 / 114 against 56 / 58 / 75 / 104.
+// 32.  Measured (16 against 32): 6 of 64, 1536 x 1408, FP4, at 24 / 48 pairs an expert 138 / 201 against 124 /
+// 177; 8 of 128, 2048 x 768, MXFP4, at 16 / 32 pairs 152 / 200 against 132 / 178; 2 of 8, 1536 x 2048, NF4,
+// at 16 / 32 / 64 / 128 pairs 48 / 57 / 72 / 115 against 56 / 59 / 75 / 104.
 template <int DIR, int FMT, int XT>
 hipError_t launch_moe_wide_cols(const MoeArgs& a, hipStream_t s) {
   if constexpr (DIR == kDown) {
