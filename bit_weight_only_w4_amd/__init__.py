@@ -50,6 +50,10 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(
                 f"W4 HIP library not built ({LIB_PATH} missing); run "
                 "`python -m bit_weight_only_w4_amd.build` on a machine with ROCm")
+        try:
+            import torch  # noqa: F401  (its HIP runtime first: torch sees no GPU through another one)
+        except ImportError:
+            pass
         L = ctypes.CDLL(LIB_PATH)
         i64, vp, sz, ci = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
         L.w4_quantize_nf4.argtypes = [vp, i64, i64, vp, vp, vp]
