@@ -70,6 +70,16 @@ def lib() -> ctypes.CDLL:
         L.w4_sparse24_gemv_grouped.argtypes = [vp, ci, vp, vp, vp, ci, i64, i64, vp, vp]
         L.w4_moe_route.argtypes = [vp, ci, i64, i64, i64, ci, vp, vp, vp]
         L.w4_moe.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, i64, i64, i64, i64, i64, vp, vp, sz, vp]
+        L.w4_gated.argtypes = [vp, vp, vp, ci, ci, i64, i64, i64, vp, vp, vp, sz, vp]
+        L.w4_gated_workspace_bytes.argtypes = [ci, i64, i64, i64]
+        L.w4_gated_workspace_bytes.restype = sz
+        L.w4_gated_grad.argtypes = [vp, vp, ci, ci, i64, i64, vp, vp]
+        L.w4_gemm_grad.argtypes = [vp, vp, vp, ci, i64, i64, i64, vp, vp, sz, vp]
+        L.w4_gemm_grad_workspace_bytes.argtypes = [ci, i64, i64, i64]
+        L.w4_gemm_grad_workspace_bytes.restype = sz
+        L.w4_quantize_int8.argtypes = [vp, ci, i64, i64, vp, vp, vp]
+        L.w4_gemm_int8.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, ci, vp]
+        L.w4_gated_int8.argtypes = [vp, vp, vp, vp, ci, i64, i64, i64, vp, vp, ci, vp]
         L.w4_moe_workspace_bytes.argtypes = [ci, i64, i64, i64, i64, i64]
         L.w4_moe_workspace_bytes.restype = sz
         L.w4_gemv.argtypes = [vp, vp, vp, ci, i64, i64, i64, vp, vp]
@@ -104,7 +114,9 @@ def lib() -> ctypes.CDLL:
                      "w4_gptq_quantize", "w4_sparse24_compress", "w4_sparse24_gemv",
                      "w4_sparse24_gemv_grouped", "w4_set_path", "w4_get_path",
                      "w4_matmul_splitk_noalloc",
-                     "w4_set_workspace", "w4_moe_route", "w4_moe", "w4_moe_plan"):
+                     "w4_set_workspace", "w4_moe_route", "w4_moe", "w4_moe_plan",
+                     "w4_gated", "w4_gated_grad", "w4_gemm_grad", "w4_quantize_int8", "w4_gemm_int8",
+                     "w4_gated_int8"):
             getattr(L, name).restype = ci
         _lib = L
     return _lib
@@ -656,3 +668,271 @@ def moe(x, ids, weights, gate_up, gate_up_scales, down, down_scales, fmt, y=None
     if status:
         check(status, "w4_moe")
     return y
+
+
+ACTS = {"silu": 0, "gelu_tanh": 1}
+
+
+def _act(act) -> int:
+    code = ACTS.get(act)
+    if code is None:
+        raise ValueError(f"unknown activation {act!r}; expected one of {sorted(ACTS)}")
+    return code
+
+
+def _type16(name, dtype) -> int:
+    import torch
+
+    if dtype is torch.float16:
+        return 1
+    if dtype is torch.bfloat16:
+        return 2
+    raise ValueError(f"{name} must be float16 or bfloat16")
+
+
+def _rows(name, x, what):
+    """The GPU index of a contiguous 2-D GPU tensor."""
+    index = x.get_device()
+    if x.dim() != 2 or index < 0 or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 2-D GPU tensor {what}")
+    return index
+
+
+def _weights(name, packed, scales, fmt, k, index):
+    """(format code, rows) of 4-bit weights [N, K/2] with their scales, which must be on GPU `index`."""
+    import torch
+
+    code = FORMATS.get(fmt)
+    if code is None:
+        raise ValueError(f"unknown format {fmt!r}; expected one of {sorted(FORMATS)}")
+    if packed.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D uint8 tensor [N, K/2]")
+    n = packed.shape[0]
+    dtype, group = _MOE_SCALES[fmt.split("_")[0]]
+    _expect(name, packed, (n, k // 2), torch.uint8, index)
+    _expect(f"{name} scales", scales, (n, k // group), getattr(torch, dtype), index)
+    return code, n
+
+
+def _scratch(workspace, size, device, index):
+    """A workspace of `size` bytes, allocated if not given: (tensor or None, its bytes)."""
+    import torch
+
+    if workspace is None:
+        return (torch.empty(size, dtype=torch.uint8, device=device), size) if size else (None, 0)
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the first tensor's GPU")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _block_outputs(t, i, dtype, device, index, h, products, save):
+    """h [t, i] and, where wanted, products [t, 2 i], allocated if not given."""
+    import torch
+
+    if h is None:
+        h = torch.empty((t, i), dtype=dtype, device=device)
+    else:
+        _expect("h", h, (t, i), dtype, index)
+    if products is not None:
+        _expect("products", products, (t, 2 * i), dtype, index)
+    elif save:
+        products = torch.empty((t, 2 * i), dtype=dtype, device=device)
+    return h, products
+
+
+def gated_workspace_bytes(fmt, tokens, hidden, inter) -> int:
+    return int(lib().w4_gated_workspace_bytes(_fmt(fmt), tokens, hidden, inter))
+
+
+def gated(x, gate_up, gate_up_scales, fmt, act="silu", save=False, h=None, products=None, workspace=None,
+          stream=None):
+    """The first half of a gated feed-forward block over 4-bit weights, in one call: h [T, I] of x's type with
+    h = act(g) * u, g = x . Wg^T, u = x . Wu^T ("silu" or "gelu_tanh").
+
+    x [T, H] of the format's activation type; gate_up uint8 [2 I, H/2] (gate rows, then up rows) with the
+    format's scales [2 I, H/g].  With save=True (or `products` given) it returns (h, products), products [T, 2 I] of x's type
+    holding g | u, which gated_grad takes.  `workspace` is a uint8 tensor of gated_workspace_bytes(...),
+    allocated by the call if not given and needed."""
+    index = _rows("x", x, "[T, H]")
+    t, k = x.shape
+    code, n = _weights("gate_up", gate_up, gate_up_scales, fmt, k, index)
+    if _type16("x", x.dtype) != (1 if fmt.endswith("_f16") else 2):
+        raise ValueError(f"x must be of the activation type of {fmt!r}")
+    if n % 2:
+        raise ValueError("gate_up must hold as many gate rows as up rows")
+    a = _act(act)
+    context = _on_device(index, stream)
+    if context is not None:
+        with context:
+            return gated(x, gate_up, gate_up_scales, fmt, act, save, h, products, workspace)
+    import torch
+
+    L = lib()
+    h, products = _block_outputs(t, n // 2, x.dtype, x.device, index, h, products, save)
+    workspace, size = _scratch(workspace, L.w4_gated_workspace_bytes(code, t, k, n // 2), x.device, index)
+    status = L.w4_gated(x.data_ptr(), gate_up.data_ptr(), gate_up_scales.data_ptr(), code, a, t, k, n // 2,
+                        h.data_ptr(), _ptr(products), _ptr(workspace), size, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        check(status, "w4_gated")
+    return h if products is None else (h, products)
+
+
+def gated_grad(dh, products, act="silu", d_products=None, stream=None):
+    """The gradients of a gated block's products from that of its output: d_products [T, 2 I] = dg | du with
+    dg = dh * u * act'(g), du = dh * act(g), from dh [T, I] and products [T, 2 I] = g | u (fp16 or bf16)."""
+    import torch
+
+    index = _rows("dh", dh, "[T, I]")
+    kind, a = _type16("dh", dh.dtype), _act(act)
+    t, i = dh.shape
+    _expect("products", products, (t, 2 * i), dh.dtype, index)
+    context = _on_device(index, stream)
+    if context is not None:
+        with context:
+            return gated_grad(dh, products, act, d_products)
+    if d_products is None:
+        d_products = torch.empty((t, 2 * i), dtype=dh.dtype, device=dh.device)
+    else:
+        _expect("d_products", d_products, (t, 2 * i), dh.dtype, index)
+    status = lib().w4_gated_grad(dh.data_ptr(), products.data_ptr(), kind, a, t, i, d_products.data_ptr(),
+                                 torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        check(status, "w4_gated_grad")
+    return d_products
+
+
+def gemm_grad_workspace_bytes(fmt, n, k, b) -> int:
+    return int(lib().w4_gemm_grad_workspace_bytes(_fmt(fmt), n, k, b))
+
+
+def gemm_grad(d, packed, scales, fmt, dx=None, workspace=None, stream=None):
+    """The input gradient of a product with frozen 4-bit weights: dx [B, K] = d [B, N] . W_hat, of d's type (the
+    format's activation type).  `workspace` is a uint8 tensor of gemm_grad_workspace_bytes(...), allocated by the
+    call if not given and needed."""
+    import torch
+
+    index = _rows("d", d, "[B, N]")
+    b, n = d.shape
+    if packed.dim() != 2:
+        raise ValueError("packed must be a 2-D uint8 tensor [N, K/2]")
+    k = packed.shape[1] * 2
+    code, rows = _weights("packed", packed, scales, fmt, k, index)
+    if rows != n:
+        raise ValueError("d must have a column for each weight row")
+    if _type16("d", d.dtype) != (1 if fmt.endswith("_f16") else 2):
+        raise ValueError(f"d must be of the activation type of {fmt!r}")
+    context = _on_device(index, stream)
+    if context is not None:
+        with context:
+            return gemm_grad(d, packed, scales, fmt, dx, workspace)
+    L = lib()
+    if dx is None:
+        dx = torch.empty((b, k), dtype=d.dtype, device=d.device)
+    else:
+        _expect("dx", dx, (b, k), d.dtype, index)
+    workspace, size = _scratch(workspace, L.w4_gemm_grad_workspace_bytes(code, n, k, b), d.device, index)
+    status = L.w4_gemm_grad(d.data_ptr(), packed.data_ptr(), scales.data_ptr(), code, n, k, b, dx.data_ptr(),
+                            _ptr(workspace), size, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        check(status, "w4_gemm_grad")
+    return dx
+
+
+INT8_MAX_K = 131008
+
+
+def _type(dtype) -> int:
+    import torch
+
+    return 0 if dtype is torch.float32 else _type16("the type", dtype)
+
+
+def quantize_int8(x, codes=None, scales=None, stream=None):
+    """Rows to 8 bits (tokens, or the channels of a weight matrix): x [R, K] fp32, fp16 or bf16 -> (codes int8
+    [R, K], scales fp32 [R]), scale max|x| / 127, code the integer nearest to x / scale (ties to even).  A row
+    that holds an infinity or NaN gets scale NaN."""
+    import torch
+
+    index = _rows("x", x, "[R, K]")
+    kind = _type(x.dtype)
+    context = _on_device(index, stream)
+    if context is not None:
+        with context:
+            return quantize_int8(x, codes, scales)
+    r, k = x.shape
+    if codes is None:
+        codes = torch.empty((r, k), dtype=torch.int8, device=x.device)
+    else:
+        _expect("codes", codes, (r, k), torch.int8, index)
+    if scales is None:
+        scales = torch.empty(r, dtype=torch.float32, device=x.device)
+    else:
+        _expect("scales", scales, (r,), torch.float32, index)
+    status = lib().w4_quantize_int8(x.data_ptr(), kind, r, k, codes.data_ptr(), scales.data_ptr(),
+                                    torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        check(status, "w4_quantize_int8")
+    return codes, scales
+
+
+def _int8_operands(xq, xs, wq, ws):
+    """(GPU index, tokens, K, weight rows) of the operands of an 8-bit product."""
+    import torch
+
+    index = _rows("xq", xq, "[B, K]")
+    b, k = xq.shape
+    if wq.dim() != 2:
+        raise ValueError("wq must be a 2-D int8 tensor [N, K]")
+    n = wq.shape[0]
+    _expect("xq", xq, (b, k), torch.int8, index)
+    _expect("xs", xs, (b,), torch.float32, index)
+    _expect("wq", wq, (n, k), torch.int8, index)
+    _expect("ws", ws, (n,), torch.float32, index)
+    return index, b, k, n
+
+
+def gemm_int8(xq, xs, wq, ws, dtype=None, y=None, stream=None):
+    """y [B, N] = (xq . wq^T) * xs * ws: 8-bit codes xq int8 [B, K] and wq int8 [N, K] with a scale for each token
+    and each channel (as quantize_int8 gives them), exact int32 sums.  dtype: float32 (default), float16 or bfloat16."""
+    import torch
+
+    index, b, k, n = _int8_operands(xq, xs, wq, ws)
+    if dtype is None:
+        dtype = torch.float32 if y is None else y.dtype
+    kind = _type(dtype)
+    context = _on_device(index, stream)
+    if context is not None:
+        with context:
+            return gemm_int8(xq, xs, wq, ws, dtype, y)
+    if y is None:
+        y = torch.empty((b, n), dtype=dtype, device=xq.device)
+    else:
+        _expect("y", y, (b, n), dtype, index)
+    status = lib().w4_gemm_int8(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), n, k, b, y.data_ptr(), kind,
+                                torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        check(status, "w4_gemm_int8")
+    return y
+
+
+def gated_int8(xq, xs, wq, ws, act="silu", dtype=None, save=False, h=None, products=None, stream=None):
+    """gated over 8-bit tokens and weights: wq int8 [2 I, K] (gate rows, then up rows), ws [2 I]; h and products are
+    of `dtype` (bfloat16, the default, or float16)."""
+    import torch
+
+    index, t, k, n = _int8_operands(xq, xs, wq, ws)
+    if n % 2:
+        raise ValueError("wq must hold as many gate rows as up rows")
+    if dtype is None:
+        dtype = torch.bfloat16 if h is None else h.dtype
+    kind, a = _type16("the type", dtype), _act(act)
+    context = _on_device(index, stream)
+    if context is not None:
+        with context:
+            return gated_int8(xq, xs, wq, ws, act, dtype, save, h, products)
+    h, products = _block_outputs(t, n // 2, dtype, xq.device, index, h, products, save)
+    status = lib().w4_gated_int8(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), a, t, k, n // 2,
+                                 h.data_ptr(), _ptr(products), kind, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        check(status, "w4_gated_int8")
+    return h if products is None else (h, products)

@@ -5,9 +5,11 @@
 #include <string.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <mutex>
 
 #include "w4_common.h"
+#include "w4_ffn.h"
 #include "w4_moe.h"
 
 namespace w4 {
@@ -1246,6 +1248,179 @@ int w4_sparse24_gemv_grouped(const uint16_t* x, int groups, const uint16_t* cons
   const hipError_t e = launch_sparse24_gemv(xtype, x, groups, vps, meta, N, y, k, b,
                                             reinterpret_cast<hipStream_t>(stream));
   return e == hipSuccess ? W4_OK : W4_ERR_HIP;
+}
+
+namespace {
+
+bool valid_act(int act) { return act == W4_ACT_SILU || act == W4_ACT_GELU_TANH; }
+bool valid_type(int type) { return type == W4_F32 || type == W4_F16 || type == W4_BF16; }
+size_t type_bytes(int type) { return type == W4_F32 ? 4 : 2; }
+
+struct Range {
+  const void* p;
+  size_t bytes;
+};
+// Whether an output meets an input or another output.
+bool any_overlap(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
+  for (const Range* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Range& i : ins)
+      if (overlaps(o->p, o->bytes, i.p, i.bytes)) return true;
+    for (const Range* q = o + 1; q != outs.end(); ++q)
+      if (overlaps(o->p, o->bytes, q->p, q->bytes)) return true;
+  }
+  return false;
+}
+
+// The limits keep the 32-bit offsets inside a tile of the dense kernel in range: rows of less than 2^22 bytes.
+int gated_shape(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
+  if (!valid_fmt(fmt)) return W4_ERR_FORMAT;
+  const int64_t g = fmt_group(fmt);
+  if (tokens < 1 || tokens > W4_MAX_BATCH || hidden < g || hidden % g || hidden >= ((int64_t)1 << 21) || inter < 1 ||
+      inter >= ((int64_t)1 << 24))
+    return W4_ERR_SHAPE;
+  return W4_OK;
+}
+
+int grad_shape(int fmt, int64_t n, int64_t k, int64_t b) {
+  if (!valid_fmt(fmt)) return W4_ERR_FORMAT;
+  const int64_t g = fmt_group(fmt);
+  if (b < 1 || b > W4_MAX_BATCH || k < g || k % g || k >= ((int64_t)1 << 22) || n < 1 || n >= ((int64_t)1 << 21))
+    return W4_ERR_SHAPE;
+  return W4_OK;
+}
+
+}  // namespace
+
+size_t w4_gated_workspace_bytes(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
+  return gated_shape(fmt, tokens, hidden, inter) == W4_OK ? gated_workspace(fmt, tokens, hidden, inter) : 0;
+}
+
+int w4_gated(const void* x, const uint8_t* gate_up, const void* gate_up_scales, int fmt, int act, int64_t tokens,
+             int64_t hidden, int64_t inter, void* h, void* products, void* workspace, size_t workspace_bytes,
+             void* stream) {
+  const int st = gated_shape(fmt, tokens, hidden, inter);
+  if (st == W4_ERR_FORMAT || !valid_act(act)) return W4_ERR_FORMAT;
+  if (!x || !gate_up || !gate_up_scales || !h) return W4_ERR_NULL;
+  if (st != W4_OK) return st;
+  if (!aligned(x, 16) || !aligned(gate_up, 16) || !aligned(gate_up_scales, 4) || !aligned(h, 2) ||
+      (products && !aligned(products, 2)))
+    return W4_ERR_ALIGN;
+  const size_t used = gated_workspace(fmt, tokens, hidden, inter);
+  if (used && (!workspace || workspace_bytes < used)) return W4_ERR_WORKSPACE;
+  if (used && !aligned(workspace, 16)) return W4_ERR_ALIGN;
+  const size_t weights = (size_t)(2 * inter) * (size_t)hidden, hb = (size_t)(tokens * inter) * 2;
+  if (any_overlap({{h, hb}, {products, 2 * hb}, {workspace, used}},
+                  {{x, (size_t)(tokens * hidden) * 2},
+                   {gate_up, weights / 2},
+                   {gate_up_scales, weights / (size_t)fmt_group(fmt) * fmt_scale_bytes(fmt)}}))
+    return W4_ERR_ALIAS;
+  return launch_gated(fmt, act, reinterpret_cast<const uint16_t*>(x), gate_up, gate_up_scales, tokens, hidden, inter,
+                      reinterpret_cast<uint16_t*>(h), reinterpret_cast<uint16_t*>(products), workspace,
+                      reinterpret_cast<hipStream_t>(stream)) == hipSuccess
+             ? W4_OK
+             : W4_ERR_HIP;
+}
+
+int w4_gated_grad(const void* dh, const void* products, int type, int act, int64_t tokens, int64_t inter,
+                  void* d_products, void* stream) {
+  if ((type != W4_F16 && type != W4_BF16) || !valid_act(act)) return W4_ERR_FORMAT;
+  if (!dh || !products || !d_products) return W4_ERR_NULL;
+  const int64_t limit = (int64_t)1 << 38;
+  if (tokens < 1 || inter < 1 || tokens >= limit || inter >= limit / tokens) return W4_ERR_SHAPE;
+  if (!aligned(dh, 2) || !aligned(products, 2) || !aligned(d_products, 2)) return W4_ERR_ALIGN;
+  const size_t hb = (size_t)(tokens * inter) * 2;
+  if (any_overlap({{d_products, 2 * hb}}, {{dh, hb}, {products, 2 * hb}})) return W4_ERR_ALIAS;
+  return launch_gated_grad(type == W4_F16 ? kF16 : kBF16, act, reinterpret_cast<const uint16_t*>(dh),
+                           reinterpret_cast<const uint16_t*>(products), tokens, inter,
+                           reinterpret_cast<uint16_t*>(d_products), reinterpret_cast<hipStream_t>(stream)) == hipSuccess
+             ? W4_OK
+             : W4_ERR_HIP;
+}
+
+size_t w4_gemm_grad_workspace_bytes(int fmt, int64_t N, int64_t K, int64_t B) {
+  return grad_shape(fmt, N, K, B) == W4_OK ? gemm_grad_workspace(fmt, N, K, B) : 0;
+}
+
+int w4_gemm_grad(const void* d, const uint8_t* packed, const void* scales, int fmt, int64_t N, int64_t K, int64_t B,
+                 void* dx, void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = grad_shape(fmt, N, K, B);
+  if (st == W4_ERR_FORMAT) return st;
+  if (!d || !packed || !scales || !dx) return W4_ERR_NULL;
+  if (st != W4_OK) return st;
+  if (!aligned(d, 2) || !aligned(packed, 16) || !aligned(scales, fmt_scale_bytes(fmt)) || !aligned(dx, 2))
+    return W4_ERR_ALIGN;
+  const size_t used = gemm_grad_workspace(fmt, N, K, B);
+  if (used && (!workspace || workspace_bytes < used)) return W4_ERR_WORKSPACE;
+  if (used && !aligned(workspace, 16)) return W4_ERR_ALIGN;
+  const size_t weights = (size_t)N * (size_t)K;
+  if (any_overlap({{dx, (size_t)(B * K) * 2}, {workspace, used}},
+                  {{d, (size_t)(B * N) * 2},
+                   {packed, weights / 2},
+                   {scales, weights / (size_t)fmt_group(fmt) * fmt_scale_bytes(fmt)}}))
+    return W4_ERR_ALIAS;
+  return launch_gemm_grad(fmt, reinterpret_cast<const uint16_t*>(d), packed, scales, N, K, B,
+                          reinterpret_cast<uint16_t*>(dx), workspace,
+                          reinterpret_cast<hipStream_t>(stream)) == hipSuccess
+             ? W4_OK
+             : W4_ERR_HIP;
+}
+
+int w4_quantize_int8(const void* x, int type, int64_t rows, int64_t K, int8_t* codes, float* scales, void* stream) {
+  if (!valid_type(type)) return W4_ERR_FORMAT;
+  if (!x || !codes || !scales) return W4_ERR_NULL;
+  if (rows < 1 || rows >= kMaxDim || K < 1 || K >= ((int64_t)1 << 24)) return W4_ERR_SHAPE;
+  if (!aligned(x, type_bytes(type)) || !aligned(scales, 4)) return W4_ERR_ALIGN;
+  const size_t count = (size_t)rows * (size_t)K;
+  if (any_overlap({{codes, count}, {scales, (size_t)rows * 4}}, {{x, count * type_bytes(type)}})) return W4_ERR_ALIAS;
+  return launch_quantize_int8(type, x, rows, K, codes, scales, reinterpret_cast<hipStream_t>(stream)) == hipSuccess
+             ? W4_OK
+             : W4_ERR_HIP;
+}
+
+namespace {
+
+// Shared checks of the 8-bit products (`rows` weight rows; outputs h or y, and products or null), and their launch.
+int int8_call(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws, bool gated, int act, int64_t n,
+              int64_t k, int64_t b, void* out, void* products, int type, void* stream) {
+  if (!xq || !xs || !wq || !ws || !out) return W4_ERR_NULL;
+  if (b < 1 || b >= ((int64_t)1 << 20) || k < 64 || k % 64 || k > W4_INT8_MAX_K || n < 1 ||
+      n >= (gated ? (int64_t)1 << 24 : kMaxDim))
+    return W4_ERR_SHAPE;
+  const size_t esz = type_bytes(type);
+  if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(xs, 4) || !aligned(ws, 4) || !aligned(out, esz) ||
+      (products && !aligned(products, esz)))
+    return W4_ERR_ALIGN;
+  const size_t rows = (size_t)n * (gated ? 2 : 1), ob = (size_t)b * (size_t)n * esz;
+  if (any_overlap({{out, ob}, {products, 2 * ob}},
+                  {{xq, (size_t)(b * k)}, {xs, (size_t)b * 4}, {wq, rows * (size_t)k}, {ws, rows * 4}}))
+    return W4_ERR_ALIAS;
+  DenseArgs a{};
+  a.a = reinterpret_cast<const uint8_t*>(xq);
+  a.b = reinterpret_cast<const uint8_t*>(wq);
+  a.m = (uint32_t)b;
+  a.n = (uint32_t)n;
+  a.pitch = (uint32_t)k;
+  a.row_scale = xs;
+  a.col_scale = ws;
+  a.out = out;
+  a.products = products;
+  a.out_type = (uint32_t)type;
+  a.act = (uint32_t)act;
+  return launch_int8(gated, a, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? W4_OK : W4_ERR_HIP;
+}
+
+}  // namespace
+
+int w4_gemm_int8(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws, int64_t N, int64_t K, int64_t B,
+                 void* y, int type, void* stream) {
+  if (!valid_type(type)) return W4_ERR_FORMAT;
+  return int8_call(xq, xs, wq, ws, false, W4_ACT_SILU, N, K, B, y, nullptr, type, stream);
+}
+
+int w4_gated_int8(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws, int act, int64_t tokens,
+                  int64_t K, int64_t inter, void* h, void* products, int type, void* stream) {
+  if ((type != W4_F16 && type != W4_BF16) || !valid_act(act)) return W4_ERR_FORMAT;
+  return int8_call(xq, xs, wq, ws, true, act, inter, K, tokens, h, products, type, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,46 @@
+// Internal declarations of the gated feed-forward block, its gradients and the 8-bit products.
+#pragma once
+#include "w4_common.h"
+
+namespace w4 {
+
+// The operand types of the dense kernel (w4_dense.h).
+enum DenseType { kDenseF16 = 0, kDenseBF16 = 1, kDenseI8 = 2 };
+
+// One dense product C[m, n] = sum_k A[m, k] B[n, k], both operands with K contiguous, and what becomes of it.
+struct DenseArgs {
+  const uint8_t* a;  // [M, pitch] rows of operand bytes, 16-byte aligned
+  const uint8_t* b;  // [N, pitch]; gated: [2 N, pitch], gate rows, then up rows
+  uint32_t m, n;     // outputs (gated: N is the width of h)
+  uint32_t pitch;    // bytes of a row of either operand (its K elements), a multiple of 64, below 2^23
+  const float* row_scale;   // 8 bits: s[m]
+  const float* col_scale;   // 8 bits: s[n]
+  const int* row_exp;       // 16 bits: a row stands for its values times 2^row_exp[m]; may be null
+  const int* col_exp;       // 16 bits: the same for B's rows; may be null
+  const int* exp;           // 16 bits: one exponent for all of B; may be null
+  void* out;         // [M, N]
+  void* products;    // gated: [M, 2 N] or null
+  uint32_t out_type;  // 0 fp32, 1 fp16, 2 bf16
+  uint32_t act;
+};
+
+hipError_t launch_dense(int type, bool gated, const DenseArgs& a, hipStream_t s);
+
+// ---- gated block over 4-bit weights
+size_t gated_workspace(int fmt, int64_t tokens, int64_t hidden, int64_t inter);
+hipError_t launch_gated(int fmt, int act, const uint16_t* x, const uint8_t* packed, const void* scales, int64_t tokens,
+                        int64_t hidden, int64_t inter, uint16_t* h, uint16_t* products, void* ws, hipStream_t s);
+hipError_t launch_gated_grad(int xt, int act, const uint16_t* dh, const uint16_t* products, int64_t tokens,
+                             int64_t inter, uint16_t* dp, hipStream_t s);
+
+// ---- input gradient of a 4-bit product
+size_t gemm_grad_workspace(int fmt, int64_t n, int64_t k, int64_t b);
+hipError_t launch_gemm_grad(int fmt, const uint16_t* d, const uint8_t* packed, const void* scales, int64_t n, int64_t k,
+                            int64_t b, uint16_t* dx, void* ws, hipStream_t s);
+
+// ---- 8 bits
+hipError_t launch_quantize_int8(int type, const void* x, int64_t rows, int64_t k, int8_t* codes, float* scales,
+                                hipStream_t s);
+hipError_t launch_int8(bool gated, const DenseArgs& a, hipStream_t s);
+
+}  // namespace w4

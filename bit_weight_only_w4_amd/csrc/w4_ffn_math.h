@@ -1,0 +1,90 @@
+// Activations of the gated block, and what its kernels share.
+//   silu(g)      = g p,  p = 1 / (1 + exp(-g));        silu'(g) = p (1 + g (1 - p))
+//   gelu_tanh(g) = g / 2 (1 + tanh(v)) = g p,  p = 1 / (1 + exp(-2 v)),  v = sqrt(2/pi) (g + 0.044715 g^3);
+//                  gelu_tanh'(g) = p + g 2 v' p (1 - p),  v' = sqrt(2/pi) (1 + 3 * 0.044715 g^2)
+// The logistic form has no difference of near-equal numbers where tanh is close to -1.  exp and the reciprocal
+// are the hardware's (a few units of 2^-24, times |g| for exp; p below 2^-126 reads 0): the results are rounded to
+// 16 bits.
+#pragma once
+#include "w4_common.h"
+
+namespace w4 {
+namespace {
+
+__device__ inline float logistic(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
+
+// 2 v(g) and its derivative.  g is held to +-30 (where p is 0 or 1 in fp32), so that g^3 stays in range and
+// p (1 - p) = 0 meets a finite factor; a NaN passes.
+__device__ inline float gelu_arg(float g, float* slope) {
+  const float c = g > 30.0f ? 30.0f : g < -30.0f ? -30.0f : g;
+  *slope = 1.5957691216057308f * (1.0f + 0.134145f * c * c);
+  return 1.5957691216057308f * (c + 0.044715f * c * c * c);
+}
+
+template <int ACT>
+__device__ inline float act_value(float g) {
+  if constexpr (ACT == W4_ACT_SILU) {
+    return g * logistic(g);
+  } else {
+    float d;
+    return g * logistic(gelu_arg(g, &d));
+  }
+}
+
+// act(g), and act'(g) in *slope.
+template <int ACT>
+__device__ inline float act_slope(float g, float* slope) {
+  if constexpr (ACT == W4_ACT_SILU) {
+    const float p = logistic(g);
+    *slope = p * (1.0f + g * (1.0f - p));
+    return g * p;
+  } else {
+    float d;
+    const float p = logistic(gelu_arg(g, &d));
+    *slope = p + g * (p * (1.0f - p)) * d;  // in this order: g d alone may leave the range
+    return g * p;
+  }
+}
+
+// 16-bit values as fp32 and back (to nearest, ties to even).
+template <int XT>
+__device__ inline float from16(uint32_t bits) {
+  if constexpr (XT == kF16) return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+  return __uint_as_float(bits << 16);
+}
+template <int XT>
+__device__ inline uint32_t to16(float v) {
+  if constexpr (XT == kF16) return __builtin_bit_cast(uint16_t, (_Float16)v);
+  return __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+
+// Weight j (0 .. 7) of a packed dword, as its code's value: byte j / 2, high nibble first.  E2M1 and NF4 through
+// the fp32 table `codes`; INT4 as q - 8, asymmetric INT4 as q - z.
+__device__ inline uint32_t nibble(uint32_t w, int j) { return (w >> (8 * (j >> 1) + ((j & 1) ? 0 : 4))) & 15u; }
+
+// A block's scale as fp32 from its stored form (INT4A: the low half of its word).
+template <int FMT>
+__device__ inline float scale_of(const void* scales, size_t i) {
+  if constexpr (FMT == kNF4 || FMT == kFP4) return reinterpret_cast<const float*>(scales)[i];
+  if constexpr (FMT == kINT4) return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(scales)[i] << 16);
+  if constexpr (FMT == kINT4A) return __uint_as_float(reinterpret_cast<const uint32_t*>(scales)[i] << 16);
+  return e8m0_value(reinterpret_cast<const uint8_t*>(scales)[i]);
+}
+template <int FMT>
+constexpr int weights_per_scale() { return is_g128(FMT) ? 128 : FMT == kMXFP4 ? 32 : 64; }
+
+// Exponent e with |s code| 2^-e < 2^15 for every code of the format: the largest fp16 binade.
+template <int FMT>
+__device__ inline int fold_exponent(float s) {
+  constexpr int c = FMT == kNF4 ? 0 : FMT == kINT4A ? 4 : 3;  // |code| <= 2^c
+  return s > 0.0f ? ilogbf(s) + 1 + c - 15 : 0;
+}
+
+__device__ inline float wave_max(float v) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+  return v;
+}
+
+}  // namespace
+}  // namespace w4

@@ -1,0 +1,214 @@
+// Gated feed-forward block over 4-bit weights: h = act(x Wg^T) * (x Wu^T), and the gradients of its two products.
+//
+// Many tokens: the weights are decoded once to fp16 rows in the workspace and the dense kernel (w4_dense.h)
+// multiplies them.  A weight row is held as w 2^-f with one exponent f a row that puts its largest scale into the
+// top of fp16's range, bf16 tokens as x 2^-e with one e a token; both come off exactly in the epilogue.  fp16 has
+// 11 significant bits where bf16 has 8, so a weight is rounded by at most 2^-11 of itself (INT4 and MXFP4: not at
+// all) and a bf16 token not at all; what lies more than 2^29 below its row's largest is rounded by at most 2^-39
+// of that.
+#include "w4_ffn.h"
+#include "w4_ffn_math.h"
+
+namespace w4 {
+namespace {
+
+constexpr int kDecodeThreads = 256;
+
+struct DecodeArgs {
+  const uint8_t* packed;  // [N, K/2]
+  const void* scales;
+  uint16_t* w;   // [N, K] fp16
+  int* w_exp;    // [N]
+  uint32_t n, k;
+  const uint16_t* x;  // [T, K] bf16, null: no tokens to convert
+  uint16_t* xh;       // [T, K] fp16
+  int* x_exp;         // [T]
+  uint32_t t;
+};
+
+// A wave a row: weight rows first, then token rows.
+template <int FMT>
+__global__ void __launch_bounds__(kDecodeThreads) decode_rows_kernel(DecodeArgs p) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t row = blockIdx.x * (kDecodeThreads / 64) + (threadIdx.x >> 6);
+  constexpr uint32_t G = weights_per_scale<FMT>();
+  constexpr uint32_t kn[16] = W4_NF4_CODE_BITS;
+  constexpr uint32_t kf[16] = W4_FP4_CODE_BITS;
+  __shared__ float table[16];
+  if (threadIdx.x < 16) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) bits = (int)threadIdx.x == q ? (FMT == kNF4 ? kn[q] : kf[q]) : bits;
+    table[threadIdx.x] = is_g128(FMT) ? (float)((int)threadIdx.x - 8) : __uint_as_float(bits);
+  }
+  __syncthreads();
+  if (row < p.n) {
+    const uint32_t groups = p.k / G;
+    const size_t s0 = (size_t)row * groups;
+    float top = 0.0f;
+    for (uint32_t i = lane; i < groups; i += 64) {
+      const float s = fabsf(scale_of<FMT>(p.scales, s0 + i));
+      top = s < __builtin_inff() ? fmaxf(top, s) : top;  // infinities and NaN have no binade
+    }
+    const int f = fold_exponent<FMT>(wave_max(top));
+    if (lane == 0) p.w_exp[row] = f;
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(p.packed + (size_t)row * (p.k / 2));
+    uint4* dst = reinterpret_cast<uint4*>(p.w + (size_t)row * p.k);
+    for (uint32_t i = lane; i < p.k / 8; i += 64) {
+      const uint32_t v = src[i];
+      const float s = ldexpf(scale_of<FMT>(p.scales, s0 + i * 8 / G), -f);
+      float shift = 0.0f;
+      if constexpr (FMT == kINT4A)
+        shift = 8.0f - (float)((reinterpret_cast<const uint32_t*>(p.scales)[s0 + i * 8 / G] >> 16) & 15u);
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float a = (table[nibble(v, 2 * j)] + shift) * s, b = (table[nibble(v, 2 * j + 1)] + shift) * s;
+        o[j] = to16<kF16>(a) | (to16<kF16>(b) << 16);
+      }
+      dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    return;
+  }
+  const uint32_t t = row - p.n;
+  if (!p.x || t >= p.t) return;
+  const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)t * p.k);
+  uint4* dst = reinterpret_cast<uint4*>(p.xh + (size_t)t * p.k);
+  uint32_t top = 0;  // the largest finite magnitude, as bits
+  for (uint32_t i = lane; i < p.k / 8; i += 64) {
+    const uint4 v = src[i];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t a = w[j] & 0x7FFFu, b = (w[j] >> 16) & 0x7FFFu;
+      top = a < 0x7F80u ? max(top, a) : top;
+      top = b < 0x7F80u ? max(top, b) : top;
+    }
+  }
+  const float m = wave_max(__uint_as_float(top << 16));
+  const int e = m > 0.0f ? ilogbf(m) - 14 : 0;
+  if (lane == 0) p.x_exp[t] = e;
+  for (uint32_t i = lane; i < p.k / 8; i += 64) {
+    const uint4 v = src[i];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      o[j] = to16<kF16>(ldexpf(__uint_as_float(w[j] << 16), -e)) |
+             (to16<kF16>(ldexpf(__uint_as_float(w[j] & 0xFFFF0000u), -e)) << 16);
+    dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+size_t up16(size_t v) { return (v + 15) & ~(size_t)15; }
+
+struct GatedSpace {
+  size_t w, w_exp, xh, x_exp, bytes;
+};
+GatedSpace gated_space(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
+  GatedSpace g;
+  g.w = 0;
+  g.w_exp = up16((size_t)(2 * inter * hidden) * 2);
+  g.xh = g.w_exp + up16((size_t)(2 * inter) * 4);
+  g.x_exp = g.xh;
+  g.bytes = g.xh;
+  if (fmt_xtype(fmt) == kBF16) {
+    g.x_exp = g.xh + up16((size_t)(tokens * hidden) * 2);
+    g.bytes = g.x_exp + up16((size_t)tokens * 4);
+  }
+  return g;
+}
+
+// Gradients of g | u from that of h, element by element: six bytes read and four written a channel, which is all
+// that bounds it.  V channels a thread: 8 where rows and pointers allow 16-byte accesses, else 1.
+template <int XT, int ACT, int V>
+__global__ void __launch_bounds__(256) gated_grad_kernel(const uint16_t* dh, const uint16_t* pr, uint16_t* dp,
+                                                         int64_t total, int64_t inter) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;  // channel of dh, row-major
+  if (i >= total) return;
+  const int64_t t = i / inter, at = i + t * inter;  // g at 2 inter t + channel, u inter further
+  uint16_t d[V], g[V], u[V], og[V], ou[V];
+  __builtin_memcpy(d, dh + i, sizeof d);
+  __builtin_memcpy(g, pr + at, sizeof g);
+  __builtin_memcpy(u, pr + at + inter, sizeof u);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    float slope;
+    const float y = act_slope<ACT>(from16<XT>(g[j]), &slope), f = from16<XT>(d[j]);
+    og[j] = (uint16_t)to16<XT>(f * from16<XT>(u[j]) * slope);
+    ou[j] = (uint16_t)to16<XT>(f * y);
+  }
+  __builtin_memcpy(dp + at, og, sizeof og);
+  __builtin_memcpy(dp + at + inter, ou, sizeof ou);
+}
+
+template <int XT, int ACT>
+hipError_t grad_launch(const uint16_t* dh, const uint16_t* pr, uint16_t* dp, int64_t tokens, int64_t inter,
+                       hipStream_t s) {
+  const int64_t total = tokens * inter;
+  const bool wide = inter % 8 == 0 && ((uintptr_t)dh | (uintptr_t)pr | (uintptr_t)dp) % 16 == 0;
+  if (wide)
+    gated_grad_kernel<XT, ACT, 8><<<dim3((uint32_t)((total / 8 + 255) / 256)), dim3(256), 0, s>>>(dh, pr, dp, total,
+                                                                                                inter);
+  else
+    gated_grad_kernel<XT, ACT, 1><<<dim3((uint32_t)((total + 255) / 256)), dim3(256), 0, s>>>(dh, pr, dp, total, inter);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t gated_workspace(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
+  return gated_space(fmt, tokens, hidden, inter).bytes;
+}
+
+hipError_t launch_gated(int fmt, int act, const uint16_t* x, const uint8_t* packed, const void* scales, int64_t tokens,
+                        int64_t hidden, int64_t inter, uint16_t* h, uint16_t* products, void* ws, hipStream_t s) {
+  const GatedSpace g = gated_space(fmt, tokens, hidden, inter);
+  uint8_t* base = reinterpret_cast<uint8_t*>(ws);
+  const bool convert = fmt_xtype(fmt) == kBF16;
+  DecodeArgs d;
+  d.packed = packed;
+  d.scales = scales;
+  d.w = reinterpret_cast<uint16_t*>(base + g.w);
+  d.w_exp = reinterpret_cast<int*>(base + g.w_exp);
+  d.n = (uint32_t)(2 * inter);
+  d.k = (uint32_t)hidden;
+  d.x = convert ? x : nullptr;
+  d.xh = reinterpret_cast<uint16_t*>(base + g.xh);
+  d.x_exp = reinterpret_cast<int*>(base + g.x_exp);
+  d.t = (uint32_t)tokens;
+  const uint32_t rows = d.n + (convert ? d.t : 0), per = kDecodeThreads / 64;
+  const dim3 grid((rows + per - 1) / per), block(kDecodeThreads);
+  switch (fmt_weight(fmt)) {
+    case kNF4: decode_rows_kernel<kNF4><<<grid, block, 0, s>>>(d); break;
+    case kINT4: decode_rows_kernel<kINT4><<<grid, block, 0, s>>>(d); break;
+    case kFP4: decode_rows_kernel<kFP4><<<grid, block, 0, s>>>(d); break;
+    case kINT4A: decode_rows_kernel<kINT4A><<<grid, block, 0, s>>>(d); break;
+    default: decode_rows_kernel<kMXFP4><<<grid, block, 0, s>>>(d); break;
+  }
+  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  DenseArgs a{};
+  a.a = reinterpret_cast<const uint8_t*>(convert ? d.xh : x);
+  a.b = reinterpret_cast<const uint8_t*>(d.w);
+  a.m = (uint32_t)tokens;
+  a.n = (uint32_t)inter;
+  a.pitch = (uint32_t)(2 * hidden);
+  a.row_exp = convert ? d.x_exp : nullptr;
+  a.col_exp = d.w_exp;
+  a.out = h;
+  a.products = products;
+  a.out_type = convert ? 2 : 1;
+  a.act = (uint32_t)act;
+  return launch_dense(kDenseF16, true, a, s);
+}
+
+hipError_t launch_gated_grad(int xt, int act, const uint16_t* dh, const uint16_t* products, int64_t tokens,
+                             int64_t inter, uint16_t* dp, hipStream_t s) {
+  if (xt == kF16)
+    return act == W4_ACT_SILU ? grad_launch<kF16, W4_ACT_SILU>(dh, products, dp, tokens, inter, s)
+                              : grad_launch<kF16, W4_ACT_GELU_TANH>(dh, products, dp, tokens, inter, s);
+  return act == W4_ACT_SILU ? grad_launch<kBF16, W4_ACT_SILU>(dh, products, dp, tokens, inter, s)
+                            : grad_launch<kBF16, W4_ACT_GELU_TANH>(dh, products, dp, tokens, inter, s);
+}
+
+}  // namespace w4

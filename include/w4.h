@@ -580,6 +580,116 @@ size_t w4_moe_workspace_bytes(int fmt, int64_t tokens, int64_t hidden, int64_t i
 int w4_moe_plan(int fmt, int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k, int* kind,
                 int* up_groups, int* down_groups, int* up_window, int* down_window);
 
+/* ------------------------------------------------------------------ gated feed-forward ----- */
+
+/* Activation of a gated block: silu(g) = g / (1 + exp(-g)); gelu_tanh(g) =
+ * g / 2 (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))). */
+typedef enum { W4_ACT_SILU = 0, W4_ACT_GELU_TANH = 1 } w4_act_t;
+
+/* Element types of the calls below. */
+typedef enum { W4_F32 = 0, W4_F16 = 1, W4_BF16 = 2 } w4_type_t;
+
+/* w4_gated: the first half of a dense gated feed-forward block over 4-bit weights, both products, the
+ * activation and the product of the two in one call:
+ *   g = x . Wg^T,  u = x . Wu^T,  h = act(g) * u.
+ *   x         device [tokens, hidden] fp16 or bf16 (per fmt); 16-byte aligned
+ *   gate_up   device uint8[2 * inter, hidden / 2]: the gate rows, then the up rows, packed as for w4_gemv;
+ *             16-byte aligned
+ *   gate_up_scales  the format's scales [2 * inter, ...]; 4-byte aligned
+ *   fmt       any w4_format_t
+ *   act       w4_act_t
+ *   tokens    1 <= tokens <= W4_MAX_BATCH
+ *   hidden    as K for the format, below 2^21
+ *   inter     1 <= inter < 2^24
+ *   h         device [tokens, inter] of x's type, fully overwritten; 2-byte aligned
+ *   products  device [tokens, 2 * inter] of x's type, or NULL: g and u of each token, which w4_gated_grad takes;
+ *             2-byte aligned
+ *   workspace device memory of at least w4_gated_workspace_bytes(...) bytes, 16-byte aligned; may be NULL when
+ *             that is 0; scratch on entry and exit; two calls in flight must not share it
+ * No output may overlap an input, the other output or the workspace, nor the workspace an input.  fp32
+ * accumulation, g and u rounded to x's type for `products` alone.  From many tokens on (see w4_gated_workspace_bytes) the
+ * weights enter as fp16 numbers of a common exponent a row (at most 2^-11 of themselves off; INT4 and MXFP4 exact) and
+ * bf16 tokens as fp16 numbers of a common exponent a token (exact), in both what lies more than 2^29 below the
+ * row's largest by at most 2^-39 of that.  The order of every sum is fixed.  Asynchronous on `stream`. */
+int w4_gated(const void* x, const uint8_t* gate_up, const void* gate_up_scales, int fmt, int act, int64_t tokens,
+             int64_t hidden, int64_t inter, void* h, void* products, void* workspace, size_t workspace_bytes,
+             void* stream);
+
+/* Bytes of workspace w4_gated needs for these sizes (0: none); 0 for invalid ones. */
+size_t w4_gated_workspace_bytes(int fmt, int64_t tokens, int64_t hidden, int64_t inter);
+
+/* w4_gated_grad: the gradients of a gated block's products from that of h:
+ *   dg = dh * u * act'(g),  du = dh * act(g).
+ *   dh          device [tokens, inter] of `type` (W4_F16 or W4_BF16); 2-byte aligned
+ *   products    device [tokens, 2 * inter]: g and u of each token, as w4_gated writes them; 2-byte aligned
+ *   act         w4_act_t
+ *   tokens, inter   at least 1, tokens * inter < 2^38
+ *   d_products  device [tokens, 2 * inter], fully overwritten: dg and du of each token; 2-byte aligned; must not
+ *               overlap an input
+ * fp32 in between, one rounding at the end.  No workspace.  Asynchronous on `stream`. */
+int w4_gated_grad(const void* dh, const void* products, int type, int act, int64_t tokens, int64_t inter,
+                  void* d_products, void* stream);
+
+/* w4_gemm_grad: the input gradient of a product with frozen 4-bit weights (y = x . W_hat^T, as w4_gemv and its
+ * kin compute it), dx[b, k] = sum_n d[b, n] * W_hat[n, k].
+ *   d        device [B, N] fp16 or bf16 (per fmt); 2-byte aligned (16-byte aligned rows are read in place)
+ *   packed, scales, fmt, K   as for w4_gemv
+ *   N        1 <= N < 2^21
+ *   K        below 2^22
+ *   B        1 <= B <= W4_MAX_BATCH
+ *   dx       device [B, K] of d's type, fully overwritten; 2-byte aligned; must not overlap an input or the
+ *            workspace
+ *   workspace  device memory of at least w4_gemm_grad_workspace_bytes(...) bytes, 16-byte aligned; scratch on
+ *            entry and exit; must not overlap an input; two calls in flight must not share it
+ * A weight is rounded once to d's type (bf16 2^-8, fp16 2^-11 of itself, fp16 with one exponent for all of W: what
+ * lies more than 2^29 below the largest scale by at most 2^-39 of that), the sums are fp32 in a fixed order, dx is rounded once.
+ * Asynchronous on `stream`. */
+int w4_gemm_grad(const void* d, const uint8_t* packed, const void* scales, int fmt, int64_t N, int64_t K, int64_t B,
+                 void* dx, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace w4_gemm_grad needs for these sizes; 0 for invalid ones. */
+size_t w4_gemm_grad_workspace_bytes(int fmt, int64_t N, int64_t K, int64_t B);
+
+/* ------------------------------------------------------------------ 8-bit products --------- */
+
+#define W4_INT8_MAX_K 131008 /* int32 sums of 8-bit products stay in range */
+
+/* w4_quantize_int8: rows to 8 bits, tokens (in a step) or the channels of a weight matrix (beforehand).  Per row
+ * s = fp32(max |x| / 127), q = rint(x / s) of the exact quotient, ties to even, held to +-127; a row whose s is 0
+ * gets codes 0.  A row that holds an infinity or NaN gets s = NaN and codes 0, so what is multiplied with it
+ * comes out NaN.
+ *   x       device [rows, K] of `type` (w4_type_t), read only; aligned to its element
+ *   rows    1 <= rows < 2^31
+ *   K       1 <= K < 2^24
+ *   codes   device int8[rows, K], written
+ *   scales  device float[rows], written; 4-byte aligned
+ * No output may overlap the input or the other output.  Asynchronous on `stream`; no workspace, and unlike the
+ * 4-bit quantizers no synchronization. */
+int w4_quantize_int8(const void* x, int type, int64_t rows, int64_t K, int8_t* codes, float* scales, void* stream);
+
+/* w4_gemm_int8: y[b, n] = (sum_k xq[b, k] * wq[n, k]) * xs[b] * ws[n], the sum exact, then fp32.
+ *   xq      device int8[B, K] (any values, -128 too); 16-byte aligned
+ *   xs      device float[B]; 4-byte aligned
+ *   wq      device int8[N, K]; 16-byte aligned
+ *   ws      device float[N]; 4-byte aligned
+ *   N       1 <= N < 2^31
+ *   K       a positive multiple of 64, at most W4_INT8_MAX_K
+ *   B       1 <= B < 2^20
+ *   y       device [B, N] of `type` (w4_type_t), fully overwritten; aligned to its element; must not overlap an
+ *           input
+ * No workspace.  Asynchronous on `stream`. */
+int w4_gemm_int8(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws, int64_t N, int64_t K, int64_t B,
+                 void* y, int type, void* stream);
+
+/* w4_gated_int8: w4_gated over 8-bit tokens and weights: g and u are w4_gemm_int8's products with the gate rows and
+ * the up rows of wq [2 * inter, K], ws [2 * inter].
+ *   type    of h and products: W4_F16 or W4_BF16
+ *   tokens  1 <= tokens < 2^20
+ *   inter   1 <= inter < 2^24
+ * The rest as there.  No workspace.  Asynchronous on `stream`. */
+int w4_gated_int8(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws, int act, int64_t tokens,
+                  int64_t K, int64_t inter, void* h, void* products, int type, void* stream);
+
 /* ------------------------------------------------------------------ measurement probes ------ */
 
 /* Streaming-read ceiling probe: reads `bytes` (multiple of 16) from device `src` with 128-bit
