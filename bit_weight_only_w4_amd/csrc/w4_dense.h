@@ -3,15 +3,18 @@
 // fragment is 16 bytes in every type, so one kernel moves bytes and only the matrix instruction differs.
 //
 // Work layout.  A workgroup of WM x WN waves owns a tile of TM = 32 MT WM rows of A by TN = 32 NT WN rows of B and
-// walks K in steps of 128 bytes.  Both operand tiles of a step come straight from memory into LDS (buffer loads
-// with the LDS destination), two stages, the next one in flight while one is multiplied.
-//   * Stage layout: 128 bytes a row, the 16-byte chunk c of row r in slot c XOR (r / 2 mod 8): the sixteen rows that
+// walks K in steps of 64 bytes through a ring of four stages.  Both operand tiles of a step come straight from
+// memory into LDS (buffer loads with the LDS destination), three steps ahead.  One barrier a step: before it a wave
+// waits for its own copies of the next step (those of the one after stay in flight) and for its LDS reads, so that
+// behind it every wave finds the next stage whole and the stage before this one free for new copies.  A wave's
+// fragments are one half step ahead of its matrix instructions, across the barrier too.
+//   * Stage layout: 64 bytes a row, the 16-byte chunk c of row r in slot c XOR (r / 4 mod 4): the sixteen rows that
 //     a 16-lane group of a 128-bit LDS read takes then lie in distinct banks.
-//   * A (32 rows x 32 bytes): lane 32 h + c takes row c, bytes 16 h .. 16 h + 15 of the step.  B the same.
+//   * A (32 rows x 32 bytes): lane 32 h + c takes row c, bytes 16 h .. 16 h + 15 of the half step.  B the same.
 //   * D (32 x 32): lane 32 h + c holds column c (a row of B), rows 8 (e / 4) + 4 h + e % 4 (register e).
 //   * Gated: the B tile holds TN / 2 gate rows, then the up rows of the same channels; a wave's even column tiles
 //     are gate, its odd ones the up of the same channels, so the activation and the product happen in registers.
-//   * Rows past M or N and chunks past K are read at an offset outside the buffer, which gives zeros.
+//   * Rows past M or N and steps past K are read at an offset outside the buffer, which gives zeros.
 #pragma once
 #include "w4_ffn.h"
 #include "w4_ffn_math.h"
@@ -47,6 +50,28 @@ __device__ inline typename DenseAcc<TYPE>::type dense_mfma(const uint4& a, const
                                                   0);
 }
 
+// A raw buffer resource as four scalars (make_rsrc's form, for the copies below).
+__device__ inline i32x4 dense_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  i32x4 r;
+  r.x = __builtin_amdgcn_readfirstlane((int)(uint32_t)b);
+  r.y = __builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32));
+  r.z = __builtin_amdgcn_readfirstlane((int)bytes);
+  r.w = 0x00020000;
+  return r;
+}
+
+// Copies 16 bytes a lane from offset `off` of the resource to LDS, lane l's to `to` + 16 l (`to` uniform).  By hand,
+// because the compiler makes an LDS read wait for copies that it cannot tell from the one that filled what is read;
+// here the kernel's own waits say which have landed.  It has no result register; its address is read as it issues.
+__device__ inline void dense_copy(i32x4 r, const uint8_t* to, uint32_t off) {
+  const uint32_t lds = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)to;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(
+                   __builtin_amdgcn_readfirstlane((int)lds)),
+               "v"(off), "s"(r)
+               : "memory");  // m0 holds nothing else: the compiler sets it right before each use of its own
+}
+
 __device__ inline void store_typed(void* out, size_t i, float v, uint32_t type) {
   if (type == 0)
     reinterpret_cast<float*>(out)[i] = v;
@@ -58,10 +83,10 @@ template <int TYPE, bool GATED, int WM, int WN, int MT, int NT>
 __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
   constexpr int W = WM * WN, TM = 32 * MT * WM, TN = 32 * NT * WN;
   constexpr int ROWS = TM + TN;             // rows of a stage
-  constexpr int COPIES = ROWS / 8 / W;      // copies of 8 rows a wave makes for a stage
-  static_assert(ROWS % (8 * W) == 0 && TM % 8 == 0, "whole copies");
+  constexpr int COPIES = ROWS / 16 / W;     // copies of 16 rows a wave makes for a stage
+  static_assert(TM % (16 * W) == 0 && (GATED ? TN / 2 : TN) % (16 * W) == 0, "a round of copies fills one operand");
   static_assert(!GATED || NT % 2 == 0, "gate and up in one wave");
-  __shared__ __align__(16) uint8_t st0[ROWS * 128], st1[ROWS * 128];
+  __shared__ __align__(16) uint8_t ring[4][ROWS * 64];
   using Acc = typename DenseAcc<TYPE>::type;
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -79,35 +104,35 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
   constexpr uint32_t CN = GATED ? TN / 2 : TN;  // channels of a tile
   const uint32_t n0 = (tile / mt) * CN;
 
-  const __amdgpu_buffer_rsrc_t ra =
-      make_rsrc(p.a + (size_t)m0 * p.pitch, min((uint32_t)TM, p.m - m0) * p.pitch);
   const uint32_t nrows = min(CN, p.n - n0);
-  const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.b + (size_t)n0 * p.pitch, nrows * p.pitch);
-  const __amdgpu_buffer_rsrc_t ru =
-      make_rsrc(p.b + (size_t)(GATED ? p.n + n0 : 0) * p.pitch, GATED ? nrows * p.pitch : 0u);
+  const i32x4 ra = dense_rsrc(p.a + (size_t)m0 * p.pitch, min((uint32_t)TM, p.m - m0) * p.pitch);
+  const i32x4 rb = dense_rsrc(p.b + (size_t)n0 * p.pitch, nrows * p.pitch);
+  const i32x4 ru = dense_rsrc(p.b + (size_t)(GATED ? p.n + n0 : 0) * p.pitch, GATED ? nrows * p.pitch : 0u);
 
-  // Copy j of this wave fills rows 8 (W j + wave) .. + 7 of a stage: lane l slot l % 8 of row l / 8.  Its offsets:
-  uint32_t off[COPIES], col[COPIES];
+  // Copy j of this wave fills rows 16 (W j + wave) .. + 15 of a stage: lane l slot l % 4 of row l / 4.  Its offsets:
+  uint32_t off[COPIES];
 #pragma unroll
   for (int j = 0; j < COPIES; ++j) {
-    const uint32_t r0 = 8u * (uint32_t)(W * j + wave);  // uniform
-    const uint32_t r = r0 + ((uint32_t)lane >> 3);
-    const uint32_t ch = ((uint32_t)lane & 7u) ^ ((r >> 1) & 7u);
+    const uint32_t r = 16u * (uint32_t)(W * j + wave) + ((uint32_t)lane >> 2);
+    const uint32_t ch = ((uint32_t)lane & 3u) ^ ((r >> 2) & 3u);
     const uint32_t row = r < (uint32_t)TM ? r : (r - TM) % CN;
     const uint32_t rows = r < (uint32_t)TM ? min((uint32_t)TM, p.m - m0) : nrows;
-    col[j] = ch * 16;
     off[j] = row < rows ? row * p.pitch + ch * 16 : kOutOfRange - p.pitch;
   }
-  auto copy = [&](uint8_t* st, uint32_t k) __attribute__((always_inline)) {
+  const uint32_t steps = p.pitch / 64;
+  // The copies of step t; past the last step they are made all the same, from outside the buffers, so that the
+  // number of copies in flight is the same in every step.
+  auto copy = [&](const uint8_t* st, uint32_t t) __attribute__((always_inline)) {
+    const uint32_t k = t < steps ? t * 64 : 0x40000000u;
 #pragma unroll
     for (int j = 0; j < COPIES; ++j) {
-      const uint32_t r0 = 8u * (uint32_t)(W * j + wave);
-      const __amdgpu_buffer_rsrc_t r = r0 < (uint32_t)TM ? ra : !GATED || r0 < (uint32_t)TM + CN ? rb : ru;
-      uint32_t o = off[j] + k;
-      if constexpr (TYPE == kDenseI8) o = k + col[j] < p.pitch ? o : kOutOfRange;  // rows of 64 bytes times an odd number
-      asm volatile("" : "+v"(o));
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          r, (__attribute__((address_space(3))) void*)(st + r0 * 128), 16, (int)o, 0, 0, 0);
+      const uint8_t* to = st + 16 * (W * j + wave) * 64;
+      if (16 * W * j < TM)  // known when compiled
+        dense_copy(ra, to, off[j] + k);
+      else if (!GATED || 16 * W * j < TM + (int)CN)
+        dense_copy(rb, to, off[j] + k);
+      else
+        dense_copy(ru, to, off[j] + k);
     }
   };
 
@@ -119,51 +144,60 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
-  const uint32_t key = ((uint32_t)c >> 1) & 7u;  // every fragment row is c modulo 32
-  auto frag = [&](const uint8_t* st, int row, int s) __attribute__((always_inline)) {
-    const uint32_t slot = (uint32_t)(2 * s + h) ^ key;
-    return *reinterpret_cast<const uint4*>(st + (row + c) * 128 + slot * 16);
+  const uint32_t key = ((uint32_t)c >> 2) & 3u;  // every fragment row is c modulo 32
+  struct Frags {
+    uint4 a[MT], b[NT];
   };
-  auto multiply = [&](const uint8_t* st) __attribute__((always_inline)) {
+  auto load = [&](Frags& f, const uint8_t* st, int s) __attribute__((always_inline)) {
+    const uint32_t slot = ((uint32_t)(2 * s + h) ^ key) * 16 + c * 64;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      uint4 a[MT], b[NT];
+    for (int i = 0; i < MT; ++i) f.a[i] = *reinterpret_cast<const uint4*>(st + 32 * (MT * wm + i) * 64 + slot);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) a[i] = frag(st, 32 * (MT * wm + i), s);
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        b[j] = frag(st, TM + (GATED ? (j & 1) * (int)CN + 32 * (NT / 2 * wn + j / 2) : 32 * (NT * wn + j)), s);
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = dense_mfma<TYPE>(a[i], b[j], acc[i][j]);
+    for (int j = 0; j < NT; ++j) {
+      const int row = TM + (GATED ? (j & 1) * (int)CN + 32 * (NT / 2 * wn + j / 2) : 32 * (NT * wn + j));
+      f.b[j] = *reinterpret_cast<const uint4*>(st + row * 64 + slot);
     }
   };
-
-  // Two stages.  A stage's copies are waited for by the wave that made them, then the barrier hands the stage over;
-  // a second barrier, after it is read, frees it for the copies of the step after the next.
-  const uint32_t steps = (p.pitch + 127) / 128;
-  auto landed = [&](bool more) __attribute__((always_inline)) {
-    if (more)
-      __builtin_amdgcn_s_waitcnt(0x0F70 | (COPIES & 15) | ((COPIES >> 4) << 14));  // all but the next stage's
-    else
-      wait_all_vector_loads();
-    __syncthreads();
+  auto multiply = [&](const Frags& f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] = dense_mfma<TYPE>(f.a[i], f.b[j], acc[i][j]);
   };
-  copy(st0, 0);
-  if (steps > 1) copy(st1, 128);
-  for (uint32_t t = 0; t < steps; t += 2) {
-    landed(t + 1 < steps);
-    multiply(st0);
-    __syncthreads();
-    if (t + 2 < steps) copy(st0, (t + 2) * 128);
-    if (t + 1 < steps) {
-      landed(t + 2 < steps);
-      multiply(st1);
-      __syncthreads();
-      if (t + 3 < steps) copy(st1, (t + 3) * 128);
+  // A half step: the fragments of the next one are requested between this one's matrix instructions.
+  auto half = [&](Frags& next, const uint8_t* st, int s, const Frags& f) __attribute__((always_inline)) {
+    load(next, st, s);
+    multiply(f);
+#pragma unroll
+    for (int i = 0; i < MT * NT; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a matrix instruction
+      if (i < MT + NT) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // an LDS read
     }
+  };
+  Frags f0, f1;
+  copy(ring[0], 0);
+  copy(ring[1], 1);
+  copy(ring[2], 2);
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(2 * COPIES) : "memory");
+  load(f0, ring[0], 0);
+  auto step = [&](uint8_t* st, uint8_t* next, uint8_t* free, uint32_t t) __attribute__((always_inline)) {
+    // by hand: the compiler's own barrier waits for every copy in flight
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(COPIES) : "memory");
+    copy(free, t + 3);
+    half(f1, st, 1, f0);
+    half(f0, next, 0, f1);
+  };
+  for (uint32_t t = 0;;) {
+    step(ring[0], ring[1], ring[3], t);
+    if (++t == steps) break;
+    step(ring[1], ring[2], ring[0], t);
+    if (++t == steps) break;
+    step(ring[2], ring[3], ring[1], t);
+    if (++t == steps) break;
+    step(ring[3], ring[0], ring[2], t);
+    if (++t == steps) break;
   }
+  wait_all_vector_loads();  // no copy outlives the workgroup
 
   // Epilogue.  16 bits: the exponents come off exactly (ldexp).  8 bits: the int32 sum is rounded to fp32 and
   // multiplied by its token's and its channel's scale, at most 2^-24 each.

@@ -14,7 +14,7 @@ hipError_t dense_pick(const DenseArgs& a, hipStream_t s) {
   const int64_t cus = device_cu_count();
   if (a.m > 32 && tiles(256, 256) >= cus) return dense_launch<TYPE, GATED, 2, 4, 4, 2>(a, s);
   if (a.m > 32) return dense_launch<TYPE, GATED, 2, 2, 2, 2>(a, s);
-  return dense_launch<TYPE, GATED, 1, 4, 1, 2>(a, s);
+  return dense_launch<TYPE, GATED, 1, 2, 1, 2>(a, s);
 }
 
 }  // namespace
