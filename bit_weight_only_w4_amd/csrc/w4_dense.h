@@ -72,11 +72,9 @@ __device__ inline void dense_copy(i32x4 r, const uint8_t* to, uint32_t off) {
                : "memory");  // m0 holds nothing else: the compiler sets it right before each use of its own
 }
 
-__device__ inline void store_typed(void* out, size_t i, float v, uint32_t type) {
-  if (type == 0)
-    reinterpret_cast<float*>(out)[i] = v;
-  else
-    reinterpret_cast<uint16_t*>(out)[i] = (uint16_t)(type == 1 ? to16<kF16>(v) : to16<kBF16>(v));
+__device__ inline __amdgpu_buffer_rsrc_t dense_buffer(i32x4 r) {
+  return __builtin_amdgcn_make_buffer_rsrc(
+      reinterpret_cast<void*>((uint64_t)(uint32_t)r.x | ((uint64_t)(uint32_t)r.y << 32)), (short)0, r.z, r.w);
 }
 
 template <int TYPE, bool GATED, int WM, int WN, int MT, int NT>
@@ -200,43 +198,103 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
   wait_all_vector_loads();  // no copy outlives the workgroup
 
   // Epilogue.  16 bits: the exponents come off exactly (ldexp).  8 bits: the int32 sum is rounded to fp32 and
-  // multiplied by its token's and its channel's scale, at most 2^-24 each.
+  // multiplied by its token's and its channel's scale, at most 2^-24 each.  16-bit results of 32 rows go through LDS
+  // (the ring is free: a part of it for each wave), so that a store writes whole 16-byte pieces of a row; fp32
+  // results are stored from the registers, 128 bytes a row.
+  __syncthreads();
+  constexpr int CT = GATED ? NT / 2 : NT;   // column tiles of an output
+  constexpr int CW = 32 * CT;               // its columns in this wave
+  uint16_t* stage = reinterpret_cast<uint16_t*>(&ring[0][0]) + wave * 32 * CW;
+  const uint32_t nw = n0 + (uint32_t)wn * CW;  // first column
+  const void* rows_of = TYPE == kDenseI8 ? (const void*)p.row_scale : (const void*)p.row_exp;
+  const void* cols_of = TYPE == kDenseI8 ? (const void*)p.col_scale : (const void*)p.col_exp;
+  const i32x4 rr = dense_rsrc(reinterpret_cast<const uint32_t*>(rows_of) + m0, rows_of ? min((uint32_t)TM, p.m - m0) * 4 : 0u);
+  uint32_t cv[NT];  // this lane's channels
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const uint32_t n = nw + 32 * (GATED ? j / 2 : j) + c;
+    cv[j] = cols_of && n < p.n ? reinterpret_cast<const uint32_t*>(cols_of)[(GATED && (j & 1) ? p.n : 0u) + n] : 0u;
+  }
+  int all = 0;
+  if constexpr (TYPE != kDenseI8) all = p.exp ? *p.exp : 0;
+  // One output's 32 rows from row `mw` on, in LDS, to memory.
+  auto flush = [&](void* out, uint32_t pitch, uint32_t n, uint32_t nend, uint32_t mw) __attribute__((always_inline)) {
+    __builtin_amdgcn_wave_barrier();
+    uint16_t* o = reinterpret_cast<uint16_t*>(out);
+    if (p.wide) {
+      constexpr int PER = CW / 8;  // pieces a row
+#pragma unroll
+      for (int q = 0; q < 32 * PER / 64; ++q) {
+        const int at = q * 64 + lane, r = at / PER, piece = at % PER;
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + r * CW + piece * 8);
+        if (mw + r < p.m && n + piece * 8 < nend)
+          *reinterpret_cast<uint4*>(o + (size_t)(mw + r) * pitch + n + piece * 8) = v;
+      }
+    } else {
+#pragma unroll 4
+      for (int q = 0; q < 32 * CW / 64; ++q) {
+        const int at = q * 64 + lane, r = at / CW, col = at % CW;
+        if (mw + r < p.m && n + col < nend) o[(size_t)(mw + r) * pitch + n + col] = stage[r * CW + col];
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  };
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
+    const uint32_t mw = m0 + 32 * (MT * wm + i);
+    uint32_t rv[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const uint32_t m = m0 + 32 * (MT * wm + i) + 8 * (e / 4) + 4 * h + e % 4;
-      if (m >= p.m) continue;
-      float rs = 1.0f;
-      int re = 0;
+    for (int q = 0; q < 4; ++q) {
+      const u32x4 v = __builtin_bit_cast(
+          u32x4, __builtin_amdgcn_raw_buffer_load_b128(dense_buffer(rr), (32 * (MT * wm + i) + 8 * q + 4 * h) * 4, 0, 0));
+      rv[4 * q] = v.x, rv[4 * q + 1] = v.y, rv[4 * q + 2] = v.z, rv[4 * q + 3] = v.w;
+    }
+    auto value = [&](int j, int e) __attribute__((always_inline)) {
       if constexpr (TYPE == kDenseI8)
-        rs = p.row_scale[m];
+        return (float)acc[i][j][e] * __uint_as_float(rv[e]) * __uint_as_float(cv[j]);
       else
-        re = (p.row_exp ? p.row_exp[m] : 0) + (p.exp ? *p.exp : 0);
-      auto value = [&](auto v, uint32_t n) __attribute__((always_inline)) {
-        if constexpr (TYPE == kDenseI8)
-          return (float)v * rs * p.col_scale[n];
-        else
-          return ldexpf(v, re + (p.col_exp ? p.col_exp[n] : 0));
-      };
+        return ldexpf(acc[i][j][e], (int)rv[e] + (int)cv[j] + all);
+    };
+    auto put = [&](int e, int j, float v) __attribute__((always_inline)) {
+      stage[(8 * (e / 4) + 4 * h + e % 4) * CW + 32 * j + c] =
+          (uint16_t)(p.out_type == W4_F16 ? to16<kF16>(v) : to16<kBF16>(v));
+    };
+    if constexpr (GATED) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        if constexpr (GATED) {
-          if (j & 1) continue;
-          const uint32_t n = n0 + 32 * (NT / 2 * wn + j / 2) + c;
-          if (n >= p.n) continue;
-          const float g = value(acc[i][j][e], n), u = value(acc[i][j + 1][e], p.n + n);
+      for (int e = 0; e < 16; ++e)
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+          const float g = value(2 * j, e);
           const float y = p.act == W4_ACT_SILU ? act_value<W4_ACT_SILU>(g) : act_value<W4_ACT_GELU_TANH>(g);
-          store_typed(p.out, (size_t)m * p.n + n, y * u, p.out_type);
-          if (p.products) {
-            store_typed(p.products, (size_t)m * 2 * p.n + n, g, p.out_type);
-            store_typed(p.products, (size_t)m * 2 * p.n + p.n + n, u, p.out_type);
-          }
-        } else {
-          const uint32_t n = n0 + 32 * (NT * wn + j) + c;
-          if (n < p.n) store_typed(p.out, (size_t)m * p.n + n, value(acc[i][j][e], n), p.out_type);
+          put(e, j, y * value(2 * j + 1, e));
+        }
+      flush(p.out, p.n, nw, p.n, mw);
+      if (p.products) {
+#pragma unroll
+        for (int half_of = 0; half_of < 2; ++half_of) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+#pragma unroll
+            for (int j = 0; j < CT; ++j) put(e, j, value(2 * j + half_of, e));
+          flush(p.products, 2 * p.n, nw + (half_of ? p.n : 0u), half_of ? 2 * p.n : p.n, mw);
         }
       }
+    } else if (p.out_type == W4_F32) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const uint32_t m = mw + 8 * (e / 4) + 4 * h + e % 4;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const uint32_t n = nw + 32 * j + c;
+          if (m < p.m && n < p.n) reinterpret_cast<float*>(p.out)[(size_t)m * p.n + n] = value(j, e);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) put(e, j, value(j, e));
+      flush(p.out, p.n, nw, p.n, mw);
     }
   }
 }

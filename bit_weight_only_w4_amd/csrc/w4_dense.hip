@@ -19,7 +19,9 @@ hipError_t dense_pick(const DenseArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_dense(int type, bool gated, const DenseArgs& a, hipStream_t s) {
+hipError_t launch_dense(int type, bool gated, const DenseArgs& args, hipStream_t s) {
+  DenseArgs a = args;
+  a.wide = a.n % 8 == 0 && ((uintptr_t)a.out | (uintptr_t)a.products) % 16 == 0;
   if (type == kDenseF16) return gated ? dense_pick<kDenseF16, true>(a, s) : dense_pick<kDenseF16, false>(a, s);
   if (type == kDenseBF16) return gated ? hipErrorInvalidValue : dense_pick<kDenseBF16, false>(a, s);
   return gated ? dense_pick<kDenseI8, true>(a, s) : dense_pick<kDenseI8, false>(a, s);

@@ -20,8 +20,9 @@ struct DenseArgs {
   const int* exp;           // 16 bits: one exponent for all of B; may be null
   void* out;         // [M, N]
   void* products;    // gated: [M, 2 N] or null
-  uint32_t out_type;  // 0 fp32, 1 fp16, 2 bf16
+  uint32_t out_type;  // w4_type_t; fp32 for 8-bit products without a gate alone
   uint32_t act;
+  uint32_t wide;      // set by launch_dense: rows of the outputs are whole, aligned 16-byte pieces
 };
 
 hipError_t launch_dense(int type, bool gated, const DenseArgs& a, hipStream_t s);
