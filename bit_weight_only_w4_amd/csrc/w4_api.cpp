@@ -1281,6 +1281,40 @@ int gated_shape(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
   return W4_OK;
 }
 
+// w4_gated in one launch: the fused GEMV for one token where it has a launch shape, else the MFMA kernel.
+hipError_t run_gated_few(int fmt, int act, const uint16_t* x, const uint8_t* packed, const void* scales, int64_t tokens,
+                         int64_t hidden, int64_t inter, uint16_t* h, uint16_t* products, hipStream_t s) {
+  GemvGatedArgs a;
+  memset(&a, 0, sizeof(a));
+  const size_t bytes = (size_t)inter * (size_t)hidden / 2;
+  const size_t sbytes = (size_t)inter * (size_t)(hidden / fmt_group(fmt)) * fmt_scale_bytes(fmt);
+  for (int q = 0; q < 2; ++q) {
+    a.m[q].packed = packed + q * bytes;
+    a.m[q].scales = reinterpret_cast<const uint8_t*>(scales) + q * sbytes;
+    a.m[q].n = (uint32_t)inter;
+  }
+  a.x = x;
+  a.h = h;
+  a.products = products;
+  a.act = (uint32_t)act;
+  GemvPlan p;
+  if (tokens > 1 || !plan_gemv(2 * inter, hidden, 1, 1, &p) || p.iters > 3)
+    return launch_gated_mfma(fmt, a, hidden, tokens, s);
+  const int64_t per = p.threads / p.team, blocks = (inter + per - 1) / per;
+  const int64_t grid = std::min<int64_t>(blocks, p.cap);
+  a.m[0].nrb = (uint32_t)blocks;
+  a.m[0].grid = (uint32_t)grid;
+  p.grid_x = (int)grid;
+  a.k = hidden;
+  a.cpr = (int)(hidden / 32);
+  a.cps = p.cps;
+  a.team = p.team;
+  a.iters = p.iters;
+  a.small_table = fmt_weight(fmt) != kNF4 || blocks <= grid || p.threads == 256 ? 1 : 0;  // as run_gemv_members
+  return fmt_xtype(fmt) == kF16 ? launch_gated_gemv_f16(fmt_weight(fmt), a, p, s)
+                                : launch_gated_gemv_bf16(fmt_weight(fmt), a, p, s);
+}
+
 int grad_shape(int fmt, int64_t n, int64_t k, int64_t b) {
   if (!valid_fmt(fmt)) return W4_ERR_FORMAT;
   const int64_t g = fmt_group(fmt);
@@ -1314,6 +1348,12 @@ int w4_gated(const void* x, const uint8_t* gate_up, const void* gate_up_scales, 
                    {gate_up, weights / 2},
                    {gate_up_scales, weights / (size_t)fmt_group(fmt) * fmt_scale_bytes(fmt)}}))
     return W4_ERR_ALIAS;
+  if (gated_few(fmt, tokens, hidden, inter))
+    return run_gated_few(fmt, act, reinterpret_cast<const uint16_t*>(x), gate_up, gate_up_scales, tokens, hidden, inter,
+                         reinterpret_cast<uint16_t*>(h), reinterpret_cast<uint16_t*>(products),
+                         reinterpret_cast<hipStream_t>(stream)) == hipSuccess
+               ? W4_OK
+               : W4_ERR_HIP;
   return launch_gated(fmt, act, reinterpret_cast<const uint16_t*>(x), gate_up, gate_up_scales, tokens, hidden, inter,
                       reinterpret_cast<uint16_t*>(h), reinterpret_cast<uint16_t*>(products), workspace,
                       reinterpret_cast<hipStream_t>(stream)) == hipSuccess

@@ -161,6 +161,13 @@ struct GemvArgsT {
 };
 using GemvArgs = GemvArgsT<kMaxGroup>;
 
+// A gated launch: members 0 (gate) and 1 (up) of the same rows, h and, where wanted, the products.
+struct GemvGatedArgs : GemvArgsT<2> {
+  uint16_t* h;         // [B, N]
+  uint16_t* products;  // [B, 2 N] or null
+  uint32_t act;
+};
+
 constexpr int kGemvMaxThreads = 512;
 constexpr int kMaxGemvBatch = 8;
 

@@ -28,21 +28,16 @@ struct DenseArgs {
 hipError_t launch_dense(int type, bool gated, const DenseArgs& a, hipStream_t s);
 
 // ---- gated block over 4-bit weights
+bool gated_few(int fmt, int64_t tokens, int64_t hidden, int64_t inter);
 size_t gated_workspace(int fmt, int64_t tokens, int64_t hidden, int64_t inter);
 hipError_t launch_gated(int fmt, int act, const uint16_t* x, const uint8_t* packed, const void* scales, int64_t tokens,
                         int64_t hidden, int64_t inter, uint16_t* h, uint16_t* products, void* ws, hipStream_t s);
-// The same for a few tokens, in one launch without a workspace (w4_gated_few.h), for up to kFewTokens.
-constexpr int kFewTokens = 32;
-struct GatedFewArgs {
-  const uint8_t* packed;  // [2 inter, K/2]
-  const void* scales;
-  const uint16_t* x;      // [T, K]
-  uint16_t* h;            // [T, inter]
-  uint16_t* products;     // [T, 2 inter] or null
-  uint32_t t, k, inter, act;
-};
-hipError_t launch_gated_few_f16(int weight, const GatedFewArgs& a, hipStream_t s);
-hipError_t launch_gated_few_bf16(int weight, const GatedFewArgs& a, hipStream_t s);
+// The same for a few tokens, in one launch without a workspace: the fused GEMV's gated launch for one token, the MFMA
+// kernel's for more (gated_mfma_fits: whether it has a launch shape).
+hipError_t launch_gated_gemv_f16(int weight, const GemvGatedArgs& a, const GemvPlan& p, hipStream_t s);
+hipError_t launch_gated_gemv_bf16(int weight, const GemvGatedArgs& a, const GemvPlan& p, hipStream_t s);
+bool gated_mfma_fits(int fmt, int64_t inter, int64_t k, int64_t b);
+hipError_t launch_gated_mfma(int fmt, const GemvGatedArgs& a, int64_t k, int64_t b, hipStream_t s);
 hipError_t launch_gated_grad(int xt, int act, const uint16_t* dh, const uint16_t* products, int64_t tokens,
                              int64_t inter, uint16_t* dp, hipStream_t s);
 

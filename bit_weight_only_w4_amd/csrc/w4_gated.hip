@@ -13,6 +13,7 @@ namespace w4 {
 namespace {
 
 constexpr int kDecodeThreads = 256;
+constexpr int kFewTokens = 128;
 
 struct DecodeArgs {
   const uint8_t* packed;  // [N, K/2]
@@ -157,17 +158,17 @@ hipError_t grad_launch(const uint16_t* dh, const uint16_t* pr, uint16_t* dp, int
 
 }  // namespace
 
+// Whether the weights are streamed once and decoded on chip (no workspace).
+bool gated_few(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
+  return tokens <= kFewTokens && gated_mfma_fits(fmt, inter, hidden, tokens);
+}
+
 size_t gated_workspace(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
-  return tokens <= kFewTokens ? 0 : gated_space(fmt, tokens, hidden, inter).bytes;
+  return gated_few(fmt, tokens, hidden, inter) ? 0 : gated_space(fmt, tokens, hidden, inter).bytes;
 }
 
 hipError_t launch_gated(int fmt, int act, const uint16_t* x, const uint8_t* packed, const void* scales, int64_t tokens,
                         int64_t hidden, int64_t inter, uint16_t* h, uint16_t* products, void* ws, hipStream_t s) {
-  if (tokens <= kFewTokens) {
-    const GatedFewArgs f{packed, scales, x, h, products, (uint32_t)tokens, (uint32_t)hidden, (uint32_t)inter, (uint32_t)act};
-    return fmt_xtype(fmt) == kF16 ? launch_gated_few_f16(fmt_weight(fmt), f, s)
-                                  : launch_gated_few_bf16(fmt_weight(fmt), f, s);
-  }
   const GatedSpace g = gated_space(fmt, tokens, hidden, inter);
   uint8_t* base = reinterpret_cast<uint8_t*>(ws);
   const bool convert = fmt_xtype(fmt) == kBF16;

@@ -34,7 +34,10 @@
 //   * Reduction over a team: DPP within 16 lanes, cross-row shuffles up to 64, and an LDS exchange
 //     between the waves of a team wider than one wave.
 #pragma once
+#include <type_traits>
+
 #include "w4_common.h"
+#include "w4_ffn_math.h"
 
 namespace w4 {
 namespace {
@@ -69,6 +72,13 @@ __device__ inline uint32_t codes_in_lanes() {
 // The decoded 16-bit value(s) of nibble (lane & 15), meaningful in lanes 0..15: the fp16 code
 // (NF4 x fp16), the bf16 hi/lo split of the code (NF4 x bf16), the FP4 code (exact in both 16-bit
 // types), or q - 8 in the activation type (INT4, exact).
+// Whether a code is held as the sum of two 16-bit terms: NF4 with bf16 activations, and in a gated launch with fp16
+// too (its results are rounded to fp16: a code rounded there as well would cost as much accuracy again).
+template <int FMT, int XT, bool GATED>
+constexpr bool split_code() {
+  return FMT == kNF4 && (XT == kBF16 || GATED);
+}
+
 template <int FMT, int XT>
 __device__ inline void lane_decode(uint32_t& v1, uint32_t& v2) {
   v2 = 0;
@@ -79,6 +89,7 @@ __device__ inline void lane_decode(uint32_t& v1, uint32_t& v2) {
     const float c = __uint_as_float(codes_in_lanes<kNF4>());
     if (XT == kF16) {
       v1 = f16_bits(c);
+      v2 = f16_bits(c - (float)__builtin_bit_cast(_Float16, (uint16_t)v1));  // taken by gated launches
     } else {
       v1 = bf16_rne_bits(c);
       v2 = bf16_rne_bits(c - __uint_as_float(v1 << 16));
@@ -96,12 +107,12 @@ __device__ inline void lane_decode(uint32_t& v1, uint32_t& v2) {
 // bank).  Thread t writes slots t, t + NT, ...; slot i belongs to entry i / SPE, whose high nibble
 // (i / 16 SPE) is the same for the whole wave (read with v_readlane) and whose low nibble
 // ((i / SPE) & 15) is fixed per lane when NT >= 256.
-template <int FMT, int XT, int NT, int SPE>
+template <int FMT, int XT, int NT, int SPE, bool GATED = false>
 __device__ inline void fill_table(uint32_t* tab) {
   constexpr int kShift = SPE == 16 ? 4 : 2;  // log2(SPE)
   uint32_t v1, v2;
   lane_decode<FMT, XT>(v1, v2);
-  constexpr bool kSplit = (FMT == kNF4 && XT == kBF16);
+  constexpr bool kSplit = split_code<FMT, XT, GATED>();
   uint4* t4 = reinterpret_cast<uint4*>(tab);
   const int tid = threadIdx.x;
   uint32_t lo1 = 0, lo2 = 0;
@@ -228,12 +239,16 @@ __device__ inline uint32_t fp4_pair(uint32_t w) {
   }
 }
 
-template <int FMT, int XT, int B, int ITM, int NT, bool GROUPED>
+// GATED (w4_gated for a few tokens): the launch has two members of the same rows, gate and up; a workgroup
+// walks the row blocks of both at once, so that a team holds the sums of a channel's gate row and up row and
+// stores act(gate) * up in x's type.  Everything else, the prefetch too, is as for one member, in pairs.
+template <int FMT, int XT, int B, int ITM, int NT, bool GROUPED, bool GATED = false>
 __global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 2)))
-gemv_kernel(GemvArgsT<GROUPED ? kMaxGroup : 1> a) {
+gemv_kernel(typename std::conditional<GATED, GemvGatedArgs, GemvArgsT<GROUPED ? kMaxGroup : 1>>::type a) {
+  static_assert(!(GATED && GROUPED), "a gated launch has its two members");
   constexpr bool kTable = !table_free<FMT>();
   __shared__ __align__(16) uint32_t tab[kTable ? kTableBytes / 4 : 4];
-  __shared__ float xwave[NT / 64][B];
+  __shared__ float xwave[NT / 64][GATED ? 2 * B : B];
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -304,12 +319,15 @@ gemv_kernel(GemvArgsT<GROUPED ? kMaxGroup : 1> a) {
   // without touching memory, and need no clamping or branch.
   const uint32_t pitch = (uint32_t)(k >> 1);  // packed bytes per row
   const uint32_t spitch = scale_pitch<FMT>(k);
-  auto load_rb = [&](uint32_t rbv, uint4 (&p)[ITM], ScaleSlot<FMT> (&s)[ITM], bool clamp = true) {
+  auto load_rb = [&](uint32_t rbv, uint4 (&p)[ITM], ScaleSlot<FMT> (&s)[ITM], bool clamp = true, bool up = false) {
     // A prefetch past this workgroup's last row block re-reads that block (an L2 hit) rather
     // than switching the resource off, which would need a per-block select of its size.  The
     // first row block needs no clamp (rb0 <= rb_last), so its loads do not wait for the trip
     // count's division.
-    const Where w = where(!clamp || rbv < rb_last ? rbv : rb_last);
+    Where w = where(!clamp || rbv < rb_last ? rbv : rb_last);
+    if constexpr (GATED) {
+      if (up) w.packed = a.m[1].packed, w.scales = a.m[1].scales;
+    }
     uint32_t rows = w.n - w.row0;  // w.row0 < w.n: every row block up to rb_last exists
     rows = rows < (uint32_t)teams_per_wg ? rows : (uint32_t)teams_per_wg;
     const __amdgpu_buffer_rsrc_t rp = make_rsrc(w.packed + (int64_t)w.row0 * pitch, rows * pitch);
@@ -329,7 +347,11 @@ gemv_kernel(GemvArgsT<GROUPED ? kMaxGroup : 1> a) {
   // --- first row block, then this lane's activations, then the second row block
   uint4 pA[ITM], pB[ITM], pC[ITM];
   ScaleSlot<FMT> sA[ITM], sB[ITM], sC[ITM];
+  constexpr int UP = GATED ? ITM : 1;  // the up rows' buffers (unused otherwise)
+  uint4 qA[UP], qB[UP], qC[UP];
+  ScaleSlot<FMT> tA[UP], tB[UP], tC[UP];
   load_rb(rb0, pA, sA, false);
+  if constexpr (GATED) load_rb(rb0, qA, tA, false, true);
   uint32_t xr[ITM][B][16];
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, (uint32_t)(B * k * 2));
 #pragma unroll
@@ -361,14 +383,14 @@ gemv_kernel(GemvArgsT<GROUPED ? kMaxGroup : 1> a) {
   count = (nrb - 1u - rb0) / grid + 1u;
   rb_last = rb0 + grid * (count - 1u);
   load_rb(rb0 + grid, pB, sB);
-
+  if constexpr (GATED) load_rb(rb0 + grid, qB, tB, true, true);
 
   // --- decode table, written while the loads above are in flight
   if constexpr (kTable) {
     if (a.small_table) {
-      fill_table<FMT, XT, NT, 4>(tab);
+      fill_table<FMT, XT, NT, 4, GATED>(tab);
     } else {
-      fill_table<FMT, XT, NT, 16>(tab);
+      fill_table<FMT, XT, NT, 16, GATED>(tab);
     }
     __syncthreads();
   }
@@ -412,7 +434,7 @@ gemv_kernel(GemvArgsT<GROUPED ? kMaxGroup : 1> a) {
     }
   }
 
-  constexpr bool kSplitCode = (FMT == kNF4 && XT == kBF16);
+  constexpr bool kSplitCode = split_code<FMT, XT, GATED>();
   // copy of this lane (see fill_table): 64 / 32 copies, or 16 / 8 in the small table
   const uint32_t cmask = a.small_table ? (kSplitCode ? 7u : 15u) : (kSplitCode ? 31u : 63u);
   const uint32_t laneoff = ((uint32_t)lane & cmask) * (kSplitCode ? 8u : 4u);
@@ -420,8 +442,8 @@ gemv_kernel(GemvArgsT<GROUPED ? kMaxGroup : 1> a) {
   const int wave = tid >> 6;
   const int waves_per_team = team > 64 ? team >> 6 : 1;
 
-  auto compute_store = [&](uint32_t rbv, const uint4 (&pk)[ITM], const ScaleSlot<FMT> (&sc)[ITM]) {
-    float acc[B];
+  // This lane's share of its team's row sums.
+  auto sums = [&](const uint4 (&pk)[ITM], const ScaleSlot<FMT> (&sc)[ITM], float (&acc)[B]) __attribute__((always_inline)) {
 #pragma unroll
     for (int b = 0; b < B; ++b) acc[b] = 0.0f;
 #pragma unroll
@@ -463,6 +485,12 @@ gemv_kernel(GemvArgsT<GROUPED ? kMaxGroup : 1> a) {
 #pragma unroll
               for (int b = 0; b < B; ++b) {
                 const bf162_t xv = __builtin_bit_cast(bf162_t, xr[i][b][m]);
+                if constexpr (XT == kF16) {
+                  const half2_t xh = __builtin_bit_cast(half2_t, xr[i][b][m]);
+                  d[b] = __builtin_amdgcn_fdot2(__builtin_bit_cast(half2_t, t.x), xh, d[b], false);
+                  d[b] = __builtin_amdgcn_fdot2(__builtin_bit_cast(half2_t, t.y), xh, d[b], false);
+                  continue;
+                }
                 d[b] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf162_t, t.x), xv, d[b], false);
                 d[b] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf162_t, t.y), xv, d[b], false);
               }
@@ -497,6 +525,10 @@ gemv_kernel(GemvArgsT<GROUPED ? kMaxGroup : 1> a) {
       }
     }
 
+  };
+  auto compute_store = [&](uint32_t rbv, const uint4 (&pk)[ITM], const ScaleSlot<FMT> (&sc)[ITM]) {
+    float acc[B];
+    sums(pk, sc, acc);
     const Where w = where(rbv);
     const uint32_t row = w.row0 + (uint32_t)team_id;
     const int64_t n = w.n;
@@ -525,6 +557,73 @@ gemv_kernel(GemvArgsT<GROUPED ? kMaxGroup : 1> a) {
       __syncthreads();
     }
   };
+
+  if constexpr (GATED) {
+    auto pair = [&](uint32_t rbv, const uint4 (&pg)[ITM], const ScaleSlot<FMT> (&sg)[ITM], const uint4 (&pu)[ITM],
+                    const ScaleSlot<FMT> (&su)[ITM]) {
+      float gate[B], up[B];
+      sums(pg, sg, gate);
+      sums(pu, su, up);
+      const uint32_t row = rbv * (uint32_t)teams_per_wg + (uint32_t)team_id;
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        gate[b] = team_sum_wave(gate[b], team);
+        up[b] = team_sum_wave(up[b], team);
+      }
+      if (waves_per_team > 1) {
+        if (lane == 0) {
+#pragma unroll
+          for (int b = 0; b < B; ++b) {
+            xwave[wave][b] = gate[b];
+            xwave[wave][B + b] = up[b];
+          }
+        }
+        __syncthreads();
+        if (tl == 0) {
+#pragma unroll
+          for (int b = 0; b < B; ++b) {
+            gate[b] = 0.0f;
+            up[b] = 0.0f;
+            for (int w = 0; w < waves_per_team; ++w) {
+              gate[b] += xwave[wave + w][b];
+              up[b] += xwave[wave + w][B + b];
+            }
+          }
+        }
+        __syncthreads();
+      }
+      if (tl == 0 && row < mm.n) {
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          const float y = a.act == W4_ACT_SILU ? act_value<W4_ACT_SILU>(gate[b]) : act_value<W4_ACT_GELU_TANH>(gate[b]);
+          a.h[(size_t)b * mm.n + row] = (uint16_t)to16<XT>(y * up[b]);
+          if (a.products) {
+            uint16_t* o = a.products + (size_t)b * 2 * mm.n + row;
+            o[0] = (uint16_t)to16<XT>(gate[b]);
+            o[mm.n] = (uint16_t)to16<XT>(up[b]);
+          }
+        }
+      }
+    };
+    auto load_pair = [&](uint32_t rbv, uint4 (&pg)[ITM], ScaleSlot<FMT> (&sg)[ITM], uint4 (&pu)[ITM],
+                         ScaleSlot<FMT> (&su)[ITM]) __attribute__((always_inline)) {
+      load_rb(rbv, pg, sg);
+      load_rb(rbv, pu, su, true, true);
+    };
+    uint32_t rb = rb0, t = 0;
+    for (; t + 3 <= count; t += 3) {
+      load_pair(rb + 2 * grid, pC, sC, qC, tC);
+      pair(rb, pA, sA, qA, tA);
+      load_pair(rb + 3 * grid, pA, sA, qA, tA);
+      pair(rb + grid, pB, sB, qB, tB);
+      load_pair(rb + 4 * grid, pB, sB, qB, tB);
+      pair(rb + 2 * grid, pC, sC, qC, tC);
+      rb += 3 * grid;
+    }
+    if (t < count) pair(rb, pA, sA, qA, tA);
+    if (t + 1 < count) pair(rb + grid, pB, sB, qB, tB);
+    return;
+  }
 
   // --- main loop: three row blocks per trip, buffers rotating A -> B -> C, two row blocks in
   // flight behind the one being computed, no early exit; the last one or two row blocks are
@@ -599,6 +698,28 @@ hipError_t launch_fx(int b, const GemvArgs& a, int groups, const GemvPlan& p, hi
     case 6: return launch_b<FMT, XT, 6, GROUPED>(a, groups, p, s);
     case 7: return launch_b<FMT, XT, 7, GROUPED>(a, groups, p, s);
     case 8: return launch_b<FMT, XT, 8, GROUPED>(a, groups, p, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+// Gated launches: batches of up to kGatedGemvBatch rows, rows of up to 3 chunks a lane.
+template <int FMT, int XT, int B, int ITM>
+hipError_t launch_gated_one(const GemvGatedArgs& a, const GemvPlan& p, hipStream_t s) {
+  if (p.threads == 256)
+    gemv_kernel<FMT, XT, B, ITM, 256, false, true><<<dim3(p.grid_x), dim3(256), 0, s>>>(a);
+  else if (p.threads == 512)
+    gemv_kernel<FMT, XT, B, ITM, 512, false, true><<<dim3(p.grid_x), dim3(512), 0, s>>>(a);
+  else
+    return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+template <int FMT, int XT, int B>
+hipError_t launch_gated_b(const GemvGatedArgs& a, const GemvPlan& p, hipStream_t s) {
+  switch (p.iters) {
+    case 1: return launch_gated_one<FMT, XT, B, 1>(a, p, s);
+    case 2: return launch_gated_one<FMT, XT, B, 2>(a, p, s);
+    case 3: return launch_gated_one<FMT, XT, B, 3>(a, p, s);
   }
   return hipErrorInvalidValue;
 }

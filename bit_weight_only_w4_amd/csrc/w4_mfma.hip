@@ -22,14 +22,17 @@ int64_t member_tiles(const int64_t* ns, int groups, int64_t rows) {
   return t;
 }
 
+// gated: ns[0] is the rows of gate and up together, which share a workgroup: at most four K groups, and LDS for the
+// up sums where there are no K groups.
 bool plan_slice(const int64_t* ns, int groups, int64_t k, int64_t b, int t, int splits,
-                MfmaPlan* p) {
+                MfmaPlan* p, bool gated = false) {
   // With split-K the rules below see one split's quads and count every split's workgroups.
   const int64_t quads_all = (k + kQuad - 1) / kQuad;
   splits = (int)std::max<int64_t>(1, std::min<int64_t>(splits, quads_all));
   const int64_t quads = (quads_all + splits - 1) / splits;
   const int64_t cus = device_cu_count();
   const int slices = (int)((b + 16 * t - 1) / (16 * t)) * splits;
+  const int most_kw = std::min(max_kw(t), gated ? 4 : 8);
   const int64_t rows_held = std::min<int64_t>(16 * t, b);
   int kw = 1;
   if (quads <= 12 && splits == 1) {
@@ -40,9 +43,9 @@ bool plan_slice(const int64_t* ns, int groups, int64_t k, int64_t b, int t, int 
     // batch tiles (one workgroup per CU), the most K groups whose tiles still fit one round of
     // resident workgroups (a second, partial round costs more than the shorter waves save).
     if (t == 1) {
-      kw = member_tiles(ns, groups, 16 * 8) * slices >= 2 * 2 * cus ? 1 : 8;
+      kw = member_tiles(ns, groups, 16 * 8) * slices >= 2 * 2 * cus ? 1 : most_kw;
     } else {
-      for (int c = max_kw(t); c >= 1; c /= 2) {
+      for (int c = most_kw; c >= 1; c /= 2) {
         kw = c;
         if (member_tiles(ns, groups, 16 * (8 / c)) * slices <= cus) break;
       }
@@ -51,14 +54,14 @@ bool plan_slice(const int64_t* ns, int groups, int64_t k, int64_t b, int t, int 
     // Longer rows, or split-K (whose splits already supply the parallelism): the fewest K groups
     // that give every CU a row tile, which keeps row tiles tall and each activation loaded into
     // the window serving the most weight rows.
-    for (int c = 1; c <= max_kw(t); c *= 2) {
+    for (int c = 1; c <= most_kw; c *= 2) {
       if (c > quads) break;
       kw = c;
       if (member_tiles(ns, groups, 16 * (8 / c)) * slices >= cus) break;
     }
   }
   const int64_t qpk = (quads + kw - 1) / kw;
-  const int64_t red = kw > 1 ? (int64_t)(kw - 1) * (8 / kw) * t * 1024 : 0;
+  const int64_t red = kw > 1 ? (int64_t)(kw - 1) * (8 / kw) * t * 1024 : gated ? 4 * t * 1024 : 0;
   const int64_t budget = kLdsBytes - kTableBytes - red;  // the table is static LDS
   int64_t qpp = qpk;
   // Window bytes, rounded up to whole rounds of 512 16-byte slots (each thread's last load may land
@@ -78,7 +81,7 @@ bool plan_slice(const int64_t* ns, int groups, int64_t k, int64_t b, int t, int 
   p->xrow = (int)(((int64_t)kw * 32 * qpp + 1) * 16);
   p->red = (int)red;
   p->lds = (int)(red + window(qpp));  // dynamic LDS
-  p->ntiles = (int)member_tiles(ns, groups, 16 * (8 / kw));
+  p->ntiles = gated ? (int)((ns[0] / 2 + 64 / kw - 1) / (64 / kw)) : (int)member_tiles(ns, groups, 16 * (8 / kw));
   p->slices = slices / splits;
   // Split z owns quads [z qps, (z + 1) qps); the last one may run past K (reads zeros), none is
   // empty.
@@ -95,7 +98,7 @@ int most_tiles(int fmt) { return fmt_weight(fmt) == kMXFP4 ? 4 : kMaxTiles; }
 // least half a row tile per CU; slices beyond the first re-read the weights (mostly from L2).
 // Offsets are 32-bit: a slice's activations (16 T K 2 bytes) and K itself are bounded below.
 bool plan_mfma(const int64_t* ns, int groups, int64_t k, int64_t b, int splits, int most,
-               MfmaPlan* out) {
+               MfmaPlan* out, bool gated = false) {
   int64_t n_total = 0;
   for (int g = 0; g < groups; ++g) n_total += ns[g];
   if (b < 1 || b > W4_MAX_BATCH || k >= ((int64_t)1 << 22) || n_total >= ((int64_t)1 << 31) ||
@@ -108,7 +111,7 @@ bool plan_mfma(const int64_t* ns, int groups, int64_t k, int64_t b, int splits, 
   MfmaPlan best{};
   for (int t = tmax; t >= 1; t /= 2) {
     MfmaPlan p;
-    if (!plan_slice(ns, groups, k, b, t, splits, &p)) continue;
+    if (!plan_slice(ns, groups, k, b, t, splits, &p, gated)) continue;
     if (!found || (int64_t)p.ntiles * p.slices > (int64_t)best.ntiles * best.slices) {
       best = p;
       found = true;
@@ -173,6 +176,48 @@ hipError_t launch_mfma_members(int fmt, const uint16_t* x, int groups, const uin
   if (e != hipSuccess || p.splits == 1) return e;
   // the splits' partial sums, added in split order (bitwise reproducible), overwrite y
   return launch_splitk_reduce(ws, y[0], b * ns[0], p.splits, s);
+}
+
+// One gated launch (w4_gated): as above with the gate and the up matrix in a workgroup.
+bool gated_mfma_fits(int fmt, int64_t inter, int64_t k, int64_t b) {
+  MfmaPlan p;
+  const int64_t rows = 2 * inter;
+  return plan_mfma(&rows, 1, k, b, 1, most_tiles(fmt), &p, true);
+}
+
+hipError_t launch_gated_mfma(int fmt, const GemvGatedArgs& args, int64_t k, int64_t b, hipStream_t s) {
+  MfmaPlan p;
+  const int64_t rows = 2 * (int64_t)args.m[0].n;
+  if (!plan_mfma(&rows, 1, k, b, 1, most_tiles(fmt), &p, true)) return hipErrorNotSupported;
+  MfmaGatedArgs a;
+  memset(&a, 0, sizeof(a));
+  for (int q = 0; q < 2; ++q) {
+    a.m[q].packed = args.m[q].packed;
+    a.m[q].scales = args.m[q].scales;
+    a.m[q].n = args.m[0].n;
+  }
+  a.x = args.x;
+  a.groups = 1;
+  a.k = (uint32_t)k;
+  a.b = (uint32_t)b;
+  a.qpk = (uint32_t)p.qpk;
+  a.qpp = (uint32_t)p.qpp;
+  a.xrow = (uint32_t)p.xrow;
+  a.red_bytes = (uint32_t)p.red;
+  a.tiles = (uint32_t)p.ntiles;
+  a.h = args.h;
+  a.products = args.products;
+  a.act = args.act;
+  const auto run = fmt_xtype(fmt) == kF16 ? mfma_dispatch_gated_f16 : mfma_dispatch_gated_bf16;
+  int resident = 0;
+  hipError_t e = run(0, fmt_weight(fmt), a, p.tiles, p.kw, p.lds, 0, p.slices, &resident, s);
+  if (e != hipSuccess) return e;
+  if (resident < 1) return hipErrorNotSupported;
+  const int64_t fit = std::max<int64_t>(1, (int64_t)device_cu_count() * resident / p.slices);
+  const int grid = (int)std::min<int64_t>(p.ntiles, fit);
+  a.tiles_base = (uint32_t)(p.ntiles / grid);
+  a.tiles_rem = (uint32_t)(p.ntiles % grid);
+  return run(1, fmt_weight(fmt), a, p.tiles, p.kw, p.lds, grid, p.slices, nullptr, s);
 }
 
 hipError_t launch_mfma(int fmt, const uint16_t* x, const uint8_t* packed, const void* scales,

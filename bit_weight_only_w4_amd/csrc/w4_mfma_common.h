@@ -41,7 +41,8 @@ __device__ inline uint32_t codes_in_lanes() {
 // (16 of each 8-byte NF4 x bf16 entry): 128 bytes per entry, lane L reading copy L % 32 (L % 16).
 // Half the GEMV's LDS, which leaves room for larger activation tiles.  Filled by all THREADS
 // threads of a workgroup; the caller synchronizes before the first lookup.
-template <int FMT, int XT, int THREADS>
+// SPLIT: 8-byte entries, each code as the sum of two 16-bit terms (NF4).
+template <int FMT, int XT, int THREADS, bool SPLIT = FMT == kNF4 && XT == kBF16>
 __device__ inline void fill_table(uint32_t* tab) {
   uint32_t v1, v2 = 0;
   if (FMT == kFP4) {
@@ -51,6 +52,7 @@ __device__ inline void fill_table(uint32_t* tab) {
     const float c = __uint_as_float(codes_in_lanes<kNF4>());
     if (XT == kF16) {
       v1 = f16_bits(c);
+      if (SPLIT) v2 = f16_bits(c - (float)__builtin_bit_cast(_Float16, (uint16_t)v1));
     } else {
       v1 = bf16_rne_bits(c);
       v2 = bf16_rne_bits(c - __uint_as_float(v1 << 16));
@@ -59,7 +61,7 @@ __device__ inline void fill_table(uint32_t* tab) {
     const float v = (float)((int)(threadIdx.x & 15u) - 8);
     v1 = XT == kF16 ? f16_bits(v) : (__float_as_uint(v) >> 16);
   }
-  constexpr bool kSplit = (FMT == kNF4 && XT == kBF16);
+  constexpr bool kSplit = SPLIT;
   uint4* t4 = reinterpret_cast<uint4*>(tab);
   const int tid = threadIdx.x;
   // 16-byte slot i belongs to entry i >> 3: high nibble i >> 7 (uniform over a wave), low nibble

@@ -32,6 +32,10 @@
 //   * NF4 x bf16 uses the two-term bf16 split of each code (two MFMAs per step); INT4 codes q - 8
 //     are exact in both 16-bit types.  Asymmetric INT4 decodes q - 8 the same way and adds one
 //     MFMA per step whose A rows hold -(z - 8), which makes D the block's sum of (q - z) x.
+//   * Gated launches (w4_gated): members 0 and 1 are the gate and the up matrix of the same rows; even row groups
+//     take 16 gate rows, the odd ones next to them the same 16 up rows, and after the K groups are added the up
+//     sums go through LDS to the gate waves, which store act(g) * u in x's type.  NF4 codes have two terms in fp16
+//     too: one alone would be off by as much as the rounding of h.
 //   * MXFP4 moves through the registers as NF4's 64-weight blocks; one more swap of 16-lane rows
 //     (v_permlane16_swap) gathers the lane groups' dwords so that each MFMA step is one 32-weight
 //     block with one scale, applied in fp32 after the step.  Its codes come from the hardware
@@ -41,7 +45,9 @@
 #include <string.h>
 
 #include <algorithm>
+#include <type_traits>
 
+#include "w4_ffn_math.h"
 #include "w4_mfma_common.h"
 
 namespace w4 {
@@ -73,6 +79,13 @@ struct MfmaArgs {
   uint32_t qps;        // split-K (grid.z > 1): quads per split, KW * qpk; split z owns quads
                        // [z qps, (z + 1) qps) and writes its partial sums to y + z * ysplit
   uint32_t ysplit;     // floats between the partial planes of consecutive splits (B * N)
+};
+
+// A gated launch: members 0 (gate) and 1 (up), n the channels of each.
+struct MfmaGatedArgs : MfmaArgs {
+  uint16_t* h;         // [B, n]
+  uint16_t* products;  // [B, 2 n] or null
+  uint32_t act;
 };
 
 namespace {
@@ -126,15 +139,17 @@ __device__ inline uint4 e2m1_pairs(uint32_t w) {
 // batch tile, two above.
 constexpr int min_waves(int t) { return t == 1 ? 4 : 2; }
 
-template <int FMT, int XT, int T, int KW, bool GROUPED>
-__global__ void __launch_bounds__(kThreads, min_waves(T)) mfma_kernel(MfmaArgs a) {
+template <int FMT, int XT, int T, int KW, bool GROUPED, bool GATED = false>
+__global__ void __launch_bounds__(kThreads, min_waves(T))
+mfma_kernel(typename std::conditional<GATED, MfmaGatedArgs, MfmaArgs>::type a) {
   constexpr int RW = 8 / KW;
+  static_assert(!GATED || (RW >= 2 && !GROUPED), "a gate and an up row group in a workgroup");
   constexpr int KC = is_g128(FMT) ? 128 : 64;  // weights per scale block
   constexpr int QC = kQuad / KC;              // blocks per quad
   constexpr int STEPS = KC / 32;              // MFMA steps per block
   constexpr bool kMX = FMT == kMXFP4;          // a scale per step, no table
   constexpr int SB = FMT == kINT4 || kMX ? 2 : 4;  // bytes of scale per block
-  constexpr bool kSplit = (FMT == kNF4 && XT == kBF16);
+  constexpr bool kSplit = FMT == kNF4 && (XT == kBF16 || GATED);
   // LDS: the decode table (static, at address 0, so a lookup address needs no base), then the
   // dynamic part: the K-group reduction area and the x window.
   __shared__ __align__(16) uint32_t tab[kMX ? 4 : kTableBytes / 4];
@@ -194,8 +209,12 @@ __global__ void __launch_bounds__(kThreads, min_waves(T)) mfma_kernel(MfmaArgs a
   };
   auto set_tile = [&](Cursor& c) __attribute__((always_inline)) {
     const uint32_t tg = blockIdx.x + (uint32_t)c.ti * gridDim.x;
-    const MfmaMember mm = member(tg);
-    const uint32_t row_base = ((tg - mm.tile0) * RW + rg) * 16u;
+    MfmaMember mm = member(tg);
+    uint32_t row_base = ((tg - mm.tile0) * RW + rg) * 16u;
+    if constexpr (GATED) {
+      row_base = (tg * (RW / 2) + rg / 2) * 16u;
+      if (rg & 1) mm.packed = a.m[1].packed, mm.scales = a.m[1].scales;
+    }
     const uint32_t rows_left = c.ti < ntiles && row_base < mm.n ? mm.n - row_base : 0u;
     const uint32_t rows = rows_left >= 16u ? 16u : rows_left;
     c.rw = make_rsrc(mm.packed + (size_t)row_base * pitch, rows * pitch);
@@ -246,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, min_waves(T)) mfma_kernel(MfmaArgs a
       d.s[0] = sv[0];
       d.s[1] = sv[1];
       d.s[2] = sv[2];
-      if constexpr (GROUPED) d.s[3] = cur.odd;
+      if constexpr (GROUPED || GATED) d.s[3] = cur.odd;
     } else if constexpr (!is_g128(FMT)) {
       const uint4 sv = buffer_load16(cur.rs, offset_or_oob(qb < nblocks, sbase));
       d.s[0] = sv.x;
@@ -316,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, min_waves(T)) mfma_kernel(MfmaArgs a
   advance(ld);
   load_quad(ld, P1);
   advance(ld);
-  if constexpr (!kMX) fill_table<FMT, XT, kThreads>(tab);
+  if constexpr (!kMX) fill_table<FMT, XT, kThreads, kSplit>(tab);
   if constexpr (R == 4) {
     load_quad(ld, P2);
     advance(ld);
@@ -383,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, min_waves(T)) mfma_kernel(MfmaArgs a
     // MXFP4: the quad's scale bytes moved into place, those of blocks past K (the next row's) zeroed.
     uint32_t sx[2] = {0u, 0u};
     if constexpr (kMX) {
-      const uint32_t odd = GROUPED ? d.s[3] : (uint32_t)(reinterpret_cast<uintptr_t>(a.m[0].scales) & 2u);
+      const uint32_t odd = GROUPED || GATED ? d.s[3] : (uint32_t)(reinterpret_cast<uintptr_t>(a.m[0].scales) & 2u);
       uint32_t shift = slane;  // (opaque: recomputed per quad, not held across the loop)
       asm volatile("" : "+v"(shift));
       shift = ((shift + odd) & 2u) * 8u;
@@ -500,7 +519,38 @@ __global__ void __launch_bounds__(kThreads, min_waves(T)) mfma_kernel(MfmaArgs a
         }
       }
     }
-    if (kg == 0) {
+    if constexpr (GATED) {
+      // A K group's slots are free once its own wave has added them; without K groups the area is the up waves'.
+      const int slot = KW > 1 ? rg | 1 : rg >> 1;
+      if (KW == 1) __syncthreads();  // the previous tile's sums have been read
+      if (kg == 0 && (rg & 1)) {
+#pragma unroll
+        for (int t = 0; t < T; ++t) red[(slot * T + t) * 64 + lane] = acc[t];
+      }
+      __syncthreads();
+      if (kg == 0 && !(rg & 1)) {
+        const uint32_t c0 = (tg * (RW / 2) + rg / 2) * 16u + 4u * g;  // lane's four channels
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+          const float4_t up = red[(slot * T + t) * 64 + lane];
+          const uint32_t b = 16u * t + m;
+          if (b >= bsl) continue;
+          uint16_t* hr = a.h + (size_t)(b0 + b) * n;
+          uint16_t* pr = a.products ? a.products + (size_t)(b0 + b) * 2 * n : nullptr;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (c0 + i >= n) continue;
+            const float gate = acc[t][i];
+            const float v = a.act == W4_ACT_SILU ? act_value<W4_ACT_SILU>(gate) : act_value<W4_ACT_GELU_TANH>(gate);
+            hr[c0 + i] = (uint16_t)to16<XT>(v * up[i]);
+            if (pr) {
+              pr[c0 + i] = (uint16_t)to16<XT>(gate);
+              pr[n + c0 + i] = (uint16_t)to16<XT>(up[i]);
+            }
+          }
+        }
+      }
+    } else if (kg == 0) {
 #pragma unroll
       for (int t = 0; t < T; ++t) {
         const uint32_t b = 16u * t + m;
@@ -651,11 +701,65 @@ hipError_t dispatch(int op, int fmt, const MfmaArgs& a, int tiles, int kw, int l
   return hipErrorInvalidValue;
 }
 
+// Gated launches: resident workgroups per CU (op 0) or the launch (op 1), K groups of up to four.
+template <int FMT, int XT, int T, int KW>
+hipError_t gated_kw(int op, const MfmaGatedArgs& a, int lds, int grid, int slices, int* out, hipStream_t s) {
+  const void* f = reinterpret_cast<const void*>(&mfma_kernel<FMT, XT, T, KW, false, true>);
+  if (op == 0) {
+    static bool raised = false;
+    if (!raised) {
+      (void)hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kLdsBytes - kTableBytes);
+      raised = true;
+    }
+    return hipOccupancyMaxActiveBlocksPerMultiprocessor(out, f, kThreads, lds);
+  }
+  mfma_kernel<FMT, XT, T, KW, false, true>
+      <<<dim3((unsigned)grid, (unsigned)slices), dim3(kThreads), (unsigned)lds, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int FMT, int XT>
+hipError_t gated_fx(int op, const MfmaGatedArgs& a, int tiles, int kw, int lds, int grid, int slices, int* out,
+                    hipStream_t s) {
+#define W4_GATED_KW(TV, KWV)      \
+  if (tiles == TV && kw == KWV)   \
+    return gated_kw<FMT, XT, TV, KWV>(op, a, lds, grid, slices, out, s);
+  W4_GATED_KW(1, 1)
+  W4_GATED_KW(1, 2)
+  W4_GATED_KW(1, 4)
+  W4_GATED_KW(2, 1)
+  W4_GATED_KW(2, 2)
+  W4_GATED_KW(2, 4)
+  W4_GATED_KW(4, 1)
+  W4_GATED_KW(4, 2)
+  if constexpr (FMT != kMXFP4) {
+    W4_GATED_KW(8, 1)
+  }
+#undef W4_GATED_KW
+  return hipErrorInvalidValue;
+}
+
+template <int XT>
+hipError_t gated_dispatch(int op, int weight, const MfmaGatedArgs& a, int tiles, int kw, int lds, int grid, int slices,
+                          int* out, hipStream_t s) {
+  switch (weight) {
+    case kNF4: return gated_fx<kNF4, XT>(op, a, tiles, kw, lds, grid, slices, out, s);
+    case kINT4: return gated_fx<kINT4, XT>(op, a, tiles, kw, lds, grid, slices, out, s);
+    case kFP4: return gated_fx<kFP4, XT>(op, a, tiles, kw, lds, grid, slices, out, s);
+    case kINT4A: return gated_fx<kINT4A, XT>(op, a, tiles, kw, lds, grid, slices, out, s);
+    default: return gated_fx<kMXFP4, XT>(op, a, tiles, kw, lds, grid, slices, out, s);
+  }
+}
+
 }  // namespace
 
 // Op 0 (resident workgroups per CU) or op 1 (launch) of the grouped instantiations, which live in
 // their own translation unit.
 hipError_t mfma_dispatch_grouped(int op, int fmt, const MfmaArgs& a, int tiles, int kw, int lds,
                                  int grid, int slices, int* out, hipStream_t s);
+hipError_t mfma_dispatch_gated_f16(int op, int weight, const MfmaGatedArgs& a, int tiles, int kw, int lds, int grid,
+                                   int slices, int* out, hipStream_t s);
+hipError_t mfma_dispatch_gated_bf16(int op, int weight, const MfmaGatedArgs& a, int tiles, int kw, int lds, int grid,
+                                    int slices, int* out, hipStream_t s);
 
 }  // namespace w4
