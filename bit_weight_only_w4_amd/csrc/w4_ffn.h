@@ -46,6 +46,19 @@ size_t gemm_grad_workspace(int fmt, int64_t n, int64_t k, int64_t b);
 hipError_t launch_gemm_grad(int fmt, const uint16_t* d, const uint8_t* packed, const void* scales, int64_t n, int64_t k,
                             int64_t b, uint16_t* dx, void* ws, hipStream_t s);
 
+// The same for a few tokens, without decoded rows (w4_grad_few.h).
+struct GradFewArgs {
+  const uint16_t* d;      // [B, N]
+  const uint8_t* packed;  // [N, K/2]
+  const void* scales;
+  uint16_t* dx;           // [B, K]
+  float* partial;         // [splits, B, K] where N is split over workgroups, else null
+  uint32_t n, k, b;
+  uint32_t per;           // steps of 32 rows in a split
+};
+hipError_t launch_grad_few_f16(int weight, const GradFewArgs& a, uint32_t splits, hipStream_t s);
+hipError_t launch_grad_few_bf16(int weight, const GradFewArgs& a, uint32_t splits, hipStream_t s);
+
 // ---- 8 bits
 hipError_t launch_quantize_int8(int type, const void* x, int64_t rows, int64_t k, int8_t* codes, float* scales,
                                 hipStream_t s);

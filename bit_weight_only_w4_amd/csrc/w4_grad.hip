@@ -100,6 +100,17 @@ __global__ void __launch_bounds__(256) pad_kernel(const uint16_t* d, uint16_t* t
   to[t * np + c] = c < n ? d[t * n + c] : (uint16_t)0;
 }
 
+constexpr int kFewTokens = 64;
+
+// Splits of N for a few tokens: as many as give every CU a workgroup of 128 columns, each at least a step of 32 rows
+// for each of its eight waves.
+uint32_t few_splits(int64_t n, int64_t k) {
+  const int64_t groups = (k + 127) / 128, rounds = ((n + 31) / 32 + 7) / 8;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(rounds, device_cu_count() / groups));
+  const int64_t per = (rounds + want - 1) / want;  // rounds a split
+  return (uint32_t)((rounds + per - 1) / per);
+}
+
 size_t up16(size_t v) { return (v + 15) & ~(size_t)15; }
 
 struct GradSpace {
@@ -145,13 +156,26 @@ hipError_t prepare(int xt, const uint8_t* packed, const void* scales, int64_t n,
 
 }  // namespace
 
-size_t gemm_grad_workspace(int, int64_t n, int64_t k, int64_t b) { return grad_space(n, k, b).bytes; }
+size_t gemm_grad_workspace(int, int64_t n, int64_t k, int64_t b) {
+  if (b <= kFewTokens) {
+    const uint32_t splits = few_splits(n, k);
+    return splits > 1 ? up16((size_t)splits * (size_t)(b * k) * 4) : 0;
+  }
+  return grad_space(n, k, b).bytes;
+}
 
 hipError_t launch_gemm_grad(int fmt, const uint16_t* d, const uint8_t* packed, const void* scales, int64_t n, int64_t k,
                             int64_t b, uint16_t* dx, void* ws, hipStream_t s) {
+  const int xt = fmt_xtype(fmt);
+  if (b <= kFewTokens) {
+    const uint32_t splits = few_splits(n, k), steps = (uint32_t)((n + 31) / 32);
+    const GradFewArgs f{d, packed, scales, dx, splits > 1 ? reinterpret_cast<float*>(ws) : nullptr,
+                        (uint32_t)n, (uint32_t)k, (uint32_t)b, (steps + splits - 1) / splits};
+    return xt == kF16 ? launch_grad_few_f16(fmt_weight(fmt), f, splits, s)
+                      : launch_grad_few_bf16(fmt_weight(fmt), f, splits, s);
+  }
   const GradSpace g = grad_space(n, k, b);
   uint8_t* base = reinterpret_cast<uint8_t*>(ws);
-  const int xt = fmt_xtype(fmt);
   hipError_t e;
   switch (fmt_weight(fmt)) {
     case kNF4: e = prepare<kNF4>(xt, packed, scales, n, k, base, g, s); break;

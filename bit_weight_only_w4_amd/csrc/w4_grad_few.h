@@ -1,0 +1,279 @@
+// Input gradient of a 4-bit product for a few tokens: dx[t, k] = sum_n d[t, n] W_hat[n, k], the packed weights
+// streamed once and decoded in registers.
+//
+// Work layout.  A workgroup of eight waves owns 128 columns; N runs in steps of 32 rows, wave w of split z takes every
+// eighth step of the split.  The sum runs along the rows, so an operand of the matrix cores (16x16x32) needs eight
+// consecutive rows of one column in a lane, while a packed dword holds eight columns of one row.  Lane 16 g + m
+// therefore loads the dwords of columns 8 m .. 8 m + 7 of rows 8 g .. 8 g + 7 and runs eight products: product j has
+// column 8 m + j where it says column m.  No exchange between lanes, and a lane ends with eight consecutive columns of
+// tokens 4 g .. 4 g + 3.
+//   * Scales: lane 16 g + m loads one, of row 8 g + (m & 7) and the column half m >> 3 (groups of 128: of the row;
+//     blocks of 32: the two bytes of that half); lane r of each half row hands it to the others when row r is decoded.
+//   * Weights are decoded to fp32, scaled and rounded to bf16 operands, bf16 d: one term (2^-8 of the weight, as the
+//     decoded rows of the other path).  fp16 d: d as the sum of two bf16 numbers (exact), the weight as the sum of two
+//     (2^-16), three products; bf16 has fp32's range, so no common exponent is needed.
+//   * The waves' sums are added in LDS, the splits' by a second kernel, both in a fixed order.
+#pragma once
+#include <type_traits>
+
+#include "w4_ffn.h"
+#include "w4_ffn_math.h"
+#include "w4_mfma_common.h"
+
+namespace w4 {
+namespace {
+
+constexpr int kGradWaves = 8;
+
+struct GradStep {
+  uint32_t w[8], s;
+};
+
+template <int FMT, int XT, int NT>
+__global__ void __launch_bounds__(64 * kGradWaves) grad_few_kernel(GradFewArgs p) {
+  constexpr bool kMX = FMT == kMXFP4;
+  __shared__ __align__(16) float4_t red[kGradWaves * 8 * 64];
+  __shared__ float table[FMT == kNF4 ? 16 * 64 : 1];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, m = lane & 15;
+  const uint32_t k0 = blockIdx.x * 128u, k = p.k, n = p.n, pitch = k / 2;
+  constexpr uint32_t G = weights_per_scale<FMT>();
+  constexpr uint32_t SB = FMT == kINT4 ? 2 : kMX ? 1 : 4;
+  const uint32_t spitch = k / G * SB;
+  const uint32_t steps = (n + 31) / 32;
+  const uint32_t first = blockIdx.y * p.per, last = min(first + p.per, steps);
+
+  const bool have = k0 + 8 * m < k;
+  uint32_t woff[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) woff[r] = offset_or_oob(have, (8 * g + r) * pitch + k0 / 2 + 4 * m);
+  // the scale's column: of the half m >> 3 (64 columns), or of the whole group
+  const uint32_t scol = is_g128(FMT) ? k0 / 128 : kMX ? k0 / 32 + 2 * (m >> 3) : k0 / 64 + (m >> 3);
+  const uint32_t soff = offset_or_oob(scol * G < k, (uint32_t)(8 * g + (m & 7)) * spitch + scol * SB);
+  auto load_step = [&](uint32_t st, GradStep& d) __attribute__((always_inline)) {
+    const uint32_t n0 = st * 32, rows = st < last ? min(32u, n - n0) : 0u;
+    const size_t at = st < last ? n0 : 0;
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.packed + at * pitch, rows * pitch);
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(reinterpret_cast<const uint8_t*>(p.scales) + at * spitch, rows * spitch);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) d.w[r] = buffer_load32(rw, woff[r]);
+    d.s = FMT == kINT4 || kMX ? buffer_load16bit(rs, soff) : buffer_load32(rs, soff);
+  };
+  // d of token m of a tile: eight rows' values, zero past N.
+  auto load_d = [&](uint32_t st, uint4 (&d)[NT]) __attribute__((always_inline)) {
+    const uint32_t n0 = st * 32 + 8 * g;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const uint16_t* row = p.d + (size_t)min((uint32_t)(16 * t + m), p.b - 1) * n;
+      uint32_t v[4] = {0, 0, 0, 0};
+      if (st < last && n0 + 8 <= n) {
+        __builtin_memcpy(v, row + n0, 16);
+      } else if (st < last) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (n0 + j < n) v[j >> 1] |= (uint32_t)row[n0 + j] << (16 * (j & 1));
+      }
+      d[t] = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  };
+
+  float4_t acc[NT][8];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[t][j] = float4_t{0.f, 0.f, 0.f, 0.f};
+
+  // The scale of row r of this lane's eight (as stored), from the lane that loaded it.
+  auto scale_bits = [&](uint32_t s, auto r) __attribute__((always_inline)) {
+    const uint32_t lo = __float_as_uint(row_bcast<decltype(r)::value>(s));
+    if constexpr (is_g128(FMT)) return lo;
+    const uint32_t hi = __float_as_uint(row_bcast<8 + decltype(r)::value>(s));
+    return m < 8 ? lo : hi;
+  };
+  auto compute = [&](const GradStep& st, const uint4 (&d)[NT]) __attribute__((always_inline)) {
+    uint4 dh[NT], dl[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if constexpr (XT == kBF16) {
+        dh[t] = d[t];
+      } else {
+        const uint32_t v[4] = {d[t].x, d[t].y, d[t].z, d[t].w};
+        uint32_t a[4], b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x = from16<kF16>(v[j] & 0xFFFFu), y = from16<kF16>(v[j] >> 16);
+          const uint32_t xh = bf16_rne_bits(x), yh = bf16_rne_bits(y);
+          a[j] = xh | (yh << 16);
+          // an infinity or NaN stays in the first term alone
+          const float xl = x - __uint_as_float(xh << 16), yl = y - __uint_as_float(yh << 16);
+          b[j] = (xl == xl ? __float_as_uint(xl) >> 16 : 0u) | (yl == yl ? __float_as_uint(yl) & 0xFFFF0000u : 0u);
+        }
+        dh[t] = make_uint4(a[0], a[1], a[2], a[3]);
+        dl[t] = make_uint4(b[0], b[1], b[2], b[3]);
+      }
+    }
+    float s[8], o[8];  // scales; asymmetric and symmetric INT4: what the code's offset comes to
+    auto one = [&](auto r) __attribute__((always_inline)) {
+      constexpr int R = decltype(r)::value;
+      const uint32_t bits = scale_bits(st.s, r);
+      if constexpr (kMX) {
+        s[R] = e8m0_value((bits >> (2 * (m & 4))) & 255u);
+      } else if constexpr (is_g128(FMT)) {
+        s[R] = __uint_as_float(bits << 16);
+        o[R] = FMT == kINT4 ? -8.0f : -(float)((bits >> 16) & 15u);
+      } else {
+        s[R] = __uint_as_float(bits);
+      }
+    };
+    one(std::integral_constant<int, 0>{});
+    one(std::integral_constant<int, 1>{});
+    one(std::integral_constant<int, 2>{});
+    one(std::integral_constant<int, 3>{});
+    one(std::integral_constant<int, 4>{});
+    one(std::integral_constant<int, 5>{});
+    one(std::integral_constant<int, 6>{});
+    one(std::integral_constant<int, 7>{});
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {  // byte b: columns 2 b (high nibble) and 2 b + 1
+      float w[2][8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const uint32_t v = st.w[r];
+        if constexpr (FMT == kNF4) {
+          const uint32_t hi = (v >> (8 * b + 4)) & 15u, lo = (v >> (8 * b)) & 15u;
+          w[0][r] = table[hi * 64 + lane] * s[r];
+          w[1][r] = table[lo * 64 + lane] * s[r];
+        } else if constexpr (FMT == kFP4 || kMX) {
+          const auto c = b == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 0)
+                         : b == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 1)
+                         : b == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 2)
+                                  : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 3);
+          w[0][r] = c[1] * s[r];
+          w[1][r] = c[0] * s[r];
+        } else {
+          w[0][r] = ((float)((v >> (8 * b + 4)) & 15u) + o[r]) * s[r];
+          w[1][r] = ((float)((v >> (8 * b)) & 15u) + o[r]) * s[r];
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = w[q][2 * i], y = w[q][2 * i + 1];
+          h[i] = to16<kBF16>(x) | (to16<kBF16>(y) << 16);
+          if constexpr (XT == kF16) {
+            const float xl = x - __uint_as_float(h[i] << 16), yl = y - __uint_as_float(h[i] & 0xFFFF0000u);
+            l[i] = to16<kBF16>(xl == xl ? xl : 0.0f) | (to16<kBF16>(yl == yl ? yl : 0.0f) << 16);
+          }
+        }
+        const uint4 oh = make_uint4(h[0], h[1], h[2], h[3]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          if constexpr (XT == kF16) {
+            const uint4 ol = make_uint4(l[0], l[1], l[2], l[3]);
+            acc[t][2 * b + q] = mfma<kBF16>(dl[t], oh, acc[t][2 * b + q]);
+            acc[t][2 * b + q] = mfma<kBF16>(dh[t], ol, acc[t][2 * b + q]);
+          }
+          acc[t][2 * b + q] = mfma<kBF16>(dh[t], oh, acc[t][2 * b + q]);
+        }
+      }
+    }
+  };
+
+  GradStep sa, sb;
+  uint4 da[NT], db[NT];
+  uint32_t st = first + wave;
+  load_step(st, sa);
+  load_d(st, da);
+  load_step(st + kGradWaves, sb);
+  load_d(st + kGradWaves, db);
+  if constexpr (FMT == kNF4) {
+    const float c = __uint_as_float(codes_in_lanes<kNF4>());
+    for (int i = wave; i < 16; i += kGradWaves) table[i * 64 + lane] = __shfl(c, i);
+    __syncthreads();
+  }
+  for (; st < last; st += 2 * kGradWaves) {
+    compute(sa, da);
+    load_step(st + 2 * kGradWaves, sa);
+    load_d(st + 2 * kGradWaves, da);
+    if (st + kGradWaves < last) {
+      compute(sb, db);
+      load_step(st + 3 * kGradWaves, sb);
+      load_d(st + 3 * kGradWaves, db);
+    }
+  }
+
+  // A tile at a time: [wave][product][lane]; then half a token's group of eight columns a thread.
+  const float* f = reinterpret_cast<const float*>(red);
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) red[(wave * 8 + j) * 64 + lane] = acc[t][j];
+    __syncthreads();
+    const int half = tid & 1, column = (tid >> 1) & 15, token = tid >> 5;  // 16 tokens
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kGradWaves; ++w)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += f[((w * 8 + 4 * half + j) * 64 + (token >> 2) * 16 + column) * 4 + (token & 3)];
+    const uint32_t row = 16 * t + token, col = k0 + 8 * column + 4 * half;
+    if (row < p.b && col < k) {
+      if (p.partial) {
+        float* to = p.partial + ((size_t)blockIdx.y * p.b + row) * k + col;
+        *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
+      } else {
+        uint16_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = (uint16_t)to16<XT>(v[j]);
+        __builtin_memcpy(p.dx + (size_t)row * k + col, o, 8);
+      }
+    }
+  }
+}
+
+template <int XT>
+__global__ void __launch_bounds__(256) grad_sum_kernel(const float* partial, uint16_t* dx, int64_t count, uint32_t splits) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= count) return;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (uint32_t s = 0; s < splits; ++s) {
+    const float4 q = *reinterpret_cast<const float4*>(partial + (int64_t)s * count + i);
+    v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
+  }
+  const uint16_t o[4] = {(uint16_t)to16<XT>(v.x), (uint16_t)to16<XT>(v.y), (uint16_t)to16<XT>(v.z),
+                         (uint16_t)to16<XT>(v.w)};
+  __builtin_memcpy(dx + i, o, 8);
+}
+
+template <int FMT, int XT>
+hipError_t grad_few_launch(const GradFewArgs& a, uint32_t splits, hipStream_t s) {
+  const dim3 grid((a.k + 127) / 128, splits), block(64 * kGradWaves);
+  if (a.b <= 16)
+    grad_few_kernel<FMT, XT, 1><<<grid, block, 0, s>>>(a);
+  else if (a.b <= 32)
+    grad_few_kernel<FMT, XT, 2><<<grid, block, 0, s>>>(a);
+  else
+    grad_few_kernel<FMT, XT, 4><<<grid, block, 0, s>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits == 1) return e;
+  const int64_t count = (int64_t)a.b * a.k;
+  grad_sum_kernel<XT><<<dim3((uint32_t)((count / 4 + 255) / 256)), dim3(256), 0, s>>>(a.partial, a.dx, count, splits);
+  return hipGetLastError();
+}
+
+template <int XT>
+hipError_t grad_few_dispatch(int weight, const GradFewArgs& a, uint32_t splits, hipStream_t s) {
+  switch (weight) {
+    case kNF4: return grad_few_launch<kNF4, XT>(a, splits, s);
+    case kINT4: return grad_few_launch<kINT4, XT>(a, splits, s);
+    case kFP4: return grad_few_launch<kFP4, XT>(a, splits, s);
+    case kINT4A: return grad_few_launch<kINT4A, XT>(a, splits, s);
+    default: return grad_few_launch<kMXFP4, XT>(a, splits, s);
+  }
+}
+
+}  // namespace
+}  // namespace w4
