@@ -78,8 +78,10 @@ def lib() -> ctypes.CDLL:
         L.w4_gemm_grad_workspace_bytes.argtypes = [ci, i64, i64, i64]
         L.w4_gemm_grad_workspace_bytes.restype = sz
         L.w4_quantize_int8.argtypes = [vp, ci, i64, i64, vp, vp, vp]
-        L.w4_gemm_int8.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, ci, vp]
-        L.w4_gated_int8.argtypes = [vp, vp, vp, vp, ci, i64, i64, i64, vp, vp, ci, vp]
+        L.w4_gemm_int8.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, ci, vp, sz, vp]
+        L.w4_gated_int8.argtypes = [vp, vp, vp, vp, ci, i64, i64, i64, vp, vp, ci, vp, sz, vp]
+        L.w4_int8_workspace_bytes.argtypes = [i64, i64, i64, ci]
+        L.w4_int8_workspace_bytes.restype = sz
         L.w4_moe_workspace_bytes.argtypes = [ci, i64, i64, i64, i64, i64]
         L.w4_moe_workspace_bytes.restype = sz
         L.w4_gemv.argtypes = [vp, vp, vp, ci, i64, i64, i64, vp, vp]
@@ -891,9 +893,14 @@ def _int8_operands(xq, xs, wq, ws):
     return index, b, k, n
 
 
-def gemm_int8(xq, xs, wq, ws, dtype=None, y=None, stream=None):
+def int8_workspace_bytes(n, k, b, gated=False) -> int:
+    return int(lib().w4_int8_workspace_bytes(n, k, b, 1 if gated else 0))
+
+
+def gemm_int8(xq, xs, wq, ws, dtype=None, y=None, workspace=None, stream=None):
     """y [B, N] = (xq . wq^T) * xs * ws: 8-bit codes xq int8 [B, K] and wq int8 [N, K] with a scale for each token
-    and each channel (as quantize_int8 gives them), exact int32 sums.  dtype: float32 (default), float16 or bfloat16."""
+    and each channel (as quantize_int8 gives them), exact int32 sums.  dtype: float32 (default), float16 or bfloat16.
+    `workspace` is a uint8 tensor of int8_workspace_bytes(...), allocated by the call if not given and needed."""
     import torch
 
     index, b, k, n = _int8_operands(xq, xs, wq, ws)
@@ -903,21 +910,24 @@ def gemm_int8(xq, xs, wq, ws, dtype=None, y=None, stream=None):
     context = _on_device(index, stream)
     if context is not None:
         with context:
-            return gemm_int8(xq, xs, wq, ws, dtype, y)
+            return gemm_int8(xq, xs, wq, ws, dtype, y, workspace)
+    L = lib()
     if y is None:
         y = torch.empty((b, n), dtype=dtype, device=xq.device)
     else:
         _expect("y", y, (b, n), dtype, index)
-    status = lib().w4_gemm_int8(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), n, k, b, y.data_ptr(), kind,
-                                torch._C._cuda_getCurrentRawStream(index))
+    workspace, size = _scratch(workspace, L.w4_int8_workspace_bytes(n, k, b, 0), xq.device, index)
+    status = L.w4_gemm_int8(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), n, k, b, y.data_ptr(), kind,
+                            _ptr(workspace), size, torch._C._cuda_getCurrentRawStream(index))
     if status:
         check(status, "w4_gemm_int8")
     return y
 
 
-def gated_int8(xq, xs, wq, ws, act="silu", dtype=None, save=False, h=None, products=None, stream=None):
+def gated_int8(xq, xs, wq, ws, act="silu", dtype=None, save=False, h=None, products=None, workspace=None,
+               stream=None):
     """gated over 8-bit tokens and weights: wq int8 [2 I, K] (gate rows, then up rows), ws [2 I]; h and products are
-    of `dtype` (bfloat16, the default, or float16)."""
+    of `dtype` (bfloat16, the default, or float16); `workspace` of int8_workspace_bytes(I, K, T, gated=True)."""
     import torch
 
     index, t, k, n = _int8_operands(xq, xs, wq, ws)
@@ -929,10 +939,13 @@ def gated_int8(xq, xs, wq, ws, act="silu", dtype=None, save=False, h=None, produ
     context = _on_device(index, stream)
     if context is not None:
         with context:
-            return gated_int8(xq, xs, wq, ws, act, dtype, save, h, products)
+            return gated_int8(xq, xs, wq, ws, act, dtype, save, h, products, workspace)
+    L = lib()
     h, products = _block_outputs(t, n // 2, dtype, xq.device, index, h, products, save)
-    status = lib().w4_gated_int8(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), a, t, k, n // 2,
-                                 h.data_ptr(), _ptr(products), kind, torch._C._cuda_getCurrentRawStream(index))
+    workspace, size = _scratch(workspace, L.w4_int8_workspace_bytes(n // 2, k, t, 1), xq.device, index)
+    status = L.w4_gated_int8(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), a, t, k, n // 2,
+                             h.data_ptr(), _ptr(products), kind, _ptr(workspace), size,
+                             torch._C._cuda_getCurrentRawStream(index))
     if status:
         check(status, "w4_gated_int8")
     return h if products is None else (h, products)

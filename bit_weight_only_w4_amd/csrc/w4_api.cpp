@@ -1419,19 +1419,28 @@ int w4_quantize_int8(const void* x, int type, int64_t rows, int64_t K, int8_t* c
 
 namespace {
 
+int int8_shape(bool gated, int64_t n, int64_t k, int64_t b) {
+  return b < 1 || b >= ((int64_t)1 << 16) || k < 64 || k % 64 || k > W4_INT8_MAX_K || n < 1 || n >= ((int64_t)1 << 24) ||
+                 b * n >= ((int64_t)1 << (gated ? 36 : 37))
+             ? W4_ERR_SHAPE
+             : W4_OK;
+}
+
 // Shared checks of the 8-bit products (`rows` weight rows; outputs h or y, and products or null), and their launch.
 int int8_call(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws, bool gated, int act, int64_t n,
-              int64_t k, int64_t b, void* out, void* products, int type, void* stream) {
+              int64_t k, int64_t b, void* out, void* products, int type, void* workspace, size_t workspace_bytes,
+              void* stream) {
   if (!xq || !xs || !wq || !ws || !out) return W4_ERR_NULL;
-  if (b < 1 || b >= ((int64_t)1 << 20) || k < 64 || k % 64 || k > W4_INT8_MAX_K || n < 1 ||
-      n >= (gated ? (int64_t)1 << 24 : kMaxDim))
-    return W4_ERR_SHAPE;
+  if (int8_shape(gated, n, k, b) != W4_OK) return W4_ERR_SHAPE;
   const size_t esz = type_bytes(type);
   if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(xs, 4) || !aligned(ws, 4) || !aligned(out, esz) ||
       (products && !aligned(products, esz)))
     return W4_ERR_ALIGN;
+  const size_t used = dense_bytes(gated, b, n, k);
+  if (used && (!workspace || workspace_bytes < used)) return W4_ERR_WORKSPACE;
+  if (used && !aligned(workspace, 16)) return W4_ERR_ALIGN;
   const size_t rows = (size_t)n * (gated ? 2 : 1), ob = (size_t)b * (size_t)n * esz;
-  if (any_overlap({{out, ob}, {products, 2 * ob}},
+  if (any_overlap({{out, ob}, {products, 2 * ob}, {workspace, used}},
                   {{xq, (size_t)(b * k)}, {xs, (size_t)b * 4}, {wq, rows * (size_t)k}, {ws, rows * 4}}))
     return W4_ERR_ALIAS;
   DenseArgs a{};
@@ -1444,23 +1453,29 @@ int int8_call(const int8_t* xq, const float* xs, const int8_t* wq, const float* 
   a.col_scale = ws;
   a.out = out;
   a.products = products;
+  a.partial = reinterpret_cast<uint32_t*>(workspace);
   a.out_type = (uint32_t)type;
   a.act = (uint32_t)act;
-  return launch_int8(gated, a, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? W4_OK : W4_ERR_HIP;
+  return launch_dense(kDenseI8, gated, a, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? W4_OK : W4_ERR_HIP;
 }
 
 }  // namespace
 
+size_t w4_int8_workspace_bytes(int64_t N, int64_t K, int64_t B, int gated) {
+  return int8_shape(gated != 0, N, K, B) == W4_OK ? dense_bytes(gated != 0, B, N, K) : 0;
+}
+
 int w4_gemm_int8(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws, int64_t N, int64_t K, int64_t B,
-                 void* y, int type, void* stream) {
+                 void* y, int type, void* workspace, size_t workspace_bytes, void* stream) {
   if (!valid_type(type)) return W4_ERR_FORMAT;
-  return int8_call(xq, xs, wq, ws, false, W4_ACT_SILU, N, K, B, y, nullptr, type, stream);
+  return int8_call(xq, xs, wq, ws, false, W4_ACT_SILU, N, K, B, y, nullptr, type, workspace, workspace_bytes, stream);
 }
 
 int w4_gated_int8(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws, int act, int64_t tokens,
-                  int64_t K, int64_t inter, void* h, void* products, int type, void* stream) {
+                  int64_t K, int64_t inter, void* h, void* products, int type, void* workspace,
+                  size_t workspace_bytes, void* stream) {
   if ((type != W4_F16 && type != W4_BF16) || !valid_act(act)) return W4_ERR_FORMAT;
-  return int8_call(xq, xs, wq, ws, true, act, inter, K, tokens, h, products, type, stream);
+  return int8_call(xq, xs, wq, ws, true, act, inter, K, tokens, h, products, type, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

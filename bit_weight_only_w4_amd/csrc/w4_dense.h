@@ -16,6 +16,8 @@
 //     are gate, its odd ones the up of the same channels, so the activation and the product happen in registers.
 //   * Rows past M or N and steps past K are read at an offset outside the buffer, which gives zeros.
 #pragma once
+#include <type_traits>
+
 #include "w4_ffn.h"
 #include "w4_ffn_math.h"
 #include "w4_mfma_common.h"
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
     const uint32_t rows = r < (uint32_t)TM ? min((uint32_t)TM, p.m - m0) : nrows;
     off[j] = row < rows ? row * p.pitch + ch * 16 : kOutOfRange - p.pitch;
   }
-  const uint32_t steps = p.pitch / 64;
+  const uint32_t first = blockIdx.y * p.per, steps = min(first + p.per, p.pitch / 64);  // this split's
   // The copies of step t; past the last step they are made all the same, from outside the buffers, so that the
   // number of copies in flight is the same in every step.
   auto copy = [&](const uint8_t* st, uint32_t t) __attribute__((always_inline)) {
@@ -173,9 +175,9 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
     }
   };
   Frags f0, f1;
-  copy(ring[0], 0);
-  copy(ring[1], 1);
-  copy(ring[2], 2);
+  copy(ring[0], first);
+  copy(ring[1], first + 1);
+  copy(ring[2], first + 2);
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(2 * COPIES) : "memory");
   load(f0, ring[0], 0);
   auto step = [&](uint8_t* st, uint8_t* next, uint8_t* free, uint32_t t) __attribute__((always_inline)) {
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
     half(f1, st, 1, f0);
     half(f0, next, 0, f1);
   };
-  for (uint32_t t = 0;;) {
+  for (uint32_t t = first;;) {
     step(ring[0], ring[1], ring[3], t);
     if (++t == steps) break;
     step(ring[1], ring[2], ring[0], t);
@@ -206,6 +208,24 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
   constexpr int CW = 32 * CT;               // its columns in this wave
   uint16_t* stage = reinterpret_cast<uint16_t*>(&ring[0][0]) + wave * 32 * CW;
   const uint32_t nw = n0 + (uint32_t)wn * CW;  // first column
+  if (p.partial) {  // a split's sums as they are; dense_sum_kernel adds them
+    const uint32_t width = GATED ? 2 * p.n : p.n;
+    uint32_t* plane = p.partial + (size_t)blockIdx.y * p.m * width;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const uint32_t m = m0 + 32 * (MT * wm + i) + 8 * (e / 4) + 4 * h + e % 4;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const uint32_t n = nw + 32 * (GATED ? j / 2 : j) + c;
+          const auto v = acc[i][j][e];  // (a value: the cast of a vector's element itself takes another one)
+          if (m < p.m && n < p.n)
+            plane[(size_t)m * width + (GATED && (j & 1) ? p.n : 0u) + n] = __builtin_bit_cast(uint32_t, v);
+        }
+      }
+    return;
+  }
   const void* rows_of = TYPE == kDenseI8 ? (const void*)p.row_scale : (const void*)p.row_exp;
   const void* cols_of = TYPE == kDenseI8 ? (const void*)p.col_scale : (const void*)p.col_exp;
   const i32x4 rr = dense_rsrc(reinterpret_cast<const uint32_t*>(rows_of) + m0, rows_of ? min((uint32_t)TM, p.m - m0) * 4 : 0u);
@@ -299,12 +319,73 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
   }
 }
 
+// Adds the splits' sums in split order and makes of them what the epilogue above does.  V columns a thread.
+template <int TYPE, bool GATED, int V>
+__global__ void __launch_bounds__(256) dense_sum_kernel(DenseArgs p) {
+  const uint32_t n = (blockIdx.x * 256 + threadIdx.x) * V, m = blockIdx.y;
+  if (n >= p.n) return;
+  using T = typename std::conditional<TYPE == kDenseI8, int, float>::type;
+  const uint32_t width = GATED ? 2 * p.n : p.n;
+  const size_t plane = (size_t)p.m * width;
+  T sum[GATED ? 2 : 1][V] = {};
+#pragma unroll
+  for (int q = 0; q < (GATED ? 2 : 1); ++q) {
+    const T* at = reinterpret_cast<const T*>(p.partial) + (size_t)m * width + q * p.n + n;
+#pragma unroll 4
+    for (uint32_t z = 0; z < p.splits; ++z) {
+      T v[V];
+      __builtin_memcpy(v, at + z * plane, sizeof v);
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum[q][i] += v[i];
+    }
+  }
+  const float rs = TYPE == kDenseI8 ? p.row_scale[m] : 0.0f;
+  const int re = TYPE == kDenseI8 ? 0 : (p.row_exp ? p.row_exp[m] : 0) + (p.exp ? *p.exp : 0);
+  float v[3][V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+#pragma unroll
+    for (int q = 0; q < (GATED ? 2 : 1); ++q) {
+      const uint32_t c = q * p.n + n + i;
+      if constexpr (TYPE == kDenseI8)
+        v[q][i] = (float)sum[q][i] * rs * p.col_scale[c];
+      else
+        v[q][i] = ldexpf(sum[q][i], re + (p.col_exp ? p.col_exp[c] : 0));
+    }
+    if constexpr (GATED)
+      v[2][i] = v[1][i] * (p.act == W4_ACT_SILU ? act_value<W4_ACT_SILU>(v[0][i]) : act_value<W4_ACT_GELU_TANH>(v[0][i]));
+  }
+  auto store = [&](void* out, size_t at, const float(&w)[V]) __attribute__((always_inline)) {
+    if (p.out_type == W4_F32) {
+      __builtin_memcpy(reinterpret_cast<float*>(out) + at, w, sizeof w);
+    } else {
+      uint16_t o[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = (uint16_t)(p.out_type == W4_F16 ? to16<kF16>(w[i]) : to16<kBF16>(w[i]));
+      __builtin_memcpy(reinterpret_cast<uint16_t*>(out) + at, o, sizeof o);
+    }
+  };
+  store(p.out, (size_t)m * p.n + n, v[GATED ? 2 : 0]);
+  if constexpr (GATED) {
+    if (p.products) {
+      store(p.products, (size_t)m * width + n, v[0]);
+      store(p.products, (size_t)m * width + p.n + n, v[1]);
+    }
+  }
+}
+
 template <int TYPE, bool GATED, int WM, int WN, int MT, int NT>
 hipError_t dense_launch(const DenseArgs& a, hipStream_t s) {
   constexpr uint32_t TM = 32 * MT * WM, CN = 32 * NT * WN / (GATED ? 2 : 1);
   const uint64_t tiles = (uint64_t)((a.m + TM - 1) / TM) * ((a.n + CN - 1) / CN);
   if (tiles >= ((uint64_t)1 << 31)) return hipErrorInvalidValue;
-  dense_kernel<TYPE, GATED, WM, WN, MT, NT><<<dim3((uint32_t)tiles), dim3(64 * WM * WN), 0, s>>>(a);
+  dense_kernel<TYPE, GATED, WM, WN, MT, NT><<<dim3((uint32_t)tiles, a.splits), dim3(64 * WM * WN), 0, s>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  if (a.wide)
+    dense_sum_kernel<TYPE, GATED, 4><<<dim3((a.n + 1023) / 1024, a.m), dim3(256), 0, s>>>(a);
+  else
+    dense_sum_kernel<TYPE, GATED, 1><<<dim3((a.n + 255) / 256, a.m), dim3(256), 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -22,10 +22,14 @@ struct DenseArgs {
   void* products;    // gated: [M, 2 N] or null
   uint32_t out_type;  // w4_type_t; fp32 for 8-bit products without a gate alone
   uint32_t act;
+  uint32_t* partial;  // scratch for dense_bytes() bytes, null where that is 0
+  uint32_t splits, per;  // set by launch_dense: K split over workgroups, steps of 64 bytes in a split
   uint32_t wide;      // set by launch_dense: rows of the outputs are whole, aligned 16-byte pieces
 };
 
 hipError_t launch_dense(int type, bool gated, const DenseArgs& a, hipStream_t s);
+// Scratch that a product of these sizes needs (its K split over workgroups): [splits, M, N or 2 N] of 4 bytes.
+size_t dense_bytes(bool gated, int64_t m, int64_t n, int64_t pitch);
 
 // ---- gated block over 4-bit weights
 bool gated_few(int fmt, int64_t tokens, int64_t hidden, int64_t inter);
@@ -62,6 +66,5 @@ hipError_t launch_grad_few_bf16(int weight, const GradFewArgs& a, uint32_t split
 // ---- 8 bits
 hipError_t launch_quantize_int8(int type, const void* x, int64_t rows, int64_t k, int8_t* codes, float* scales,
                                 hipStream_t s);
-hipError_t launch_int8(bool gated, const DenseArgs& a, hipStream_t s);
 
 }  // namespace w4

@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_rows_kernel(DecodeArgs 
 size_t up16(size_t v) { return (v + 15) & ~(size_t)15; }
 
 struct GatedSpace {
-  size_t w, w_exp, xh, x_exp, bytes;
+  size_t w, w_exp, xh, x_exp, partial, bytes;
 };
 GatedSpace gated_space(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
   GatedSpace g;
@@ -112,11 +112,12 @@ GatedSpace gated_space(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
   g.w_exp = up16((size_t)(2 * inter * hidden) * 2);
   g.xh = g.w_exp + up16((size_t)(2 * inter) * 4);
   g.x_exp = g.xh;
-  g.bytes = g.xh;
+  g.partial = g.xh;
   if (fmt_xtype(fmt) == kBF16) {
     g.x_exp = g.xh + up16((size_t)(tokens * hidden) * 2);
-    g.bytes = g.x_exp + up16((size_t)tokens * 4);
+    g.partial = g.x_exp + up16((size_t)tokens * 4);
   }
+  g.bytes = g.partial + up16(dense_bytes(true, tokens, inter, 2 * hidden));
   return g;
 }
 
@@ -201,6 +202,7 @@ hipError_t launch_gated(int fmt, int act, const uint16_t* x, const uint8_t* pack
   a.pitch = (uint32_t)(2 * hidden);
   a.row_exp = convert ? d.x_exp : nullptr;
   a.col_exp = d.w_exp;
+  a.partial = reinterpret_cast<uint32_t*>(base + g.partial);
   a.out = h;
   a.products = products;
   a.out_type = convert ? 2 : 1;

@@ -115,7 +115,7 @@ size_t up16(size_t v) { return (v + 15) & ~(size_t)15; }
 
 struct GradSpace {
   uint32_t np;
-  size_t wt, d, parts, exp, bytes;
+  size_t wt, d, parts, exp, partial, bytes;
 };
 GradSpace grad_space(int64_t n, int64_t k, int64_t b) {
   GradSpace g;
@@ -124,7 +124,8 @@ GradSpace grad_space(int64_t n, int64_t k, int64_t b) {
   g.d = up16((size_t)k * g.np * 2);
   g.parts = g.d + up16((size_t)b * g.np * 2);
   g.exp = g.parts + kMaxParts * 4;
-  g.bytes = g.exp + 16;
+  g.partial = g.exp + 16;
+  g.bytes = g.partial + up16(dense_bytes(false, b, k, (int64_t)g.np * 2));
   return g;
 }
 
@@ -198,6 +199,7 @@ hipError_t launch_gemm_grad(int fmt, const uint16_t* d, const uint8_t* packed, c
   a.n = (uint32_t)k;
   a.pitch = g.np * 2;
   a.exp = xt == kF16 ? reinterpret_cast<const int*>(base + g.exp) : nullptr;
+  a.partial = reinterpret_cast<uint32_t*>(base + g.partial);
   a.out = dx;
   a.out_type = xt == kF16 ? 1 : 2;
   return launch_dense(xt == kF16 ? kDenseF16 : kDenseBF16, false, a, s);

@@ -157,6 +157,4 @@ hipError_t launch_quantize_int8(int type, const void* x, int64_t rows, int64_t k
   return hipGetLastError();
 }
 
-hipError_t launch_int8(bool gated, const DenseArgs& a, hipStream_t s) { return launch_dense(kDenseI8, gated, a, s); }
-
 }  // namespace w4

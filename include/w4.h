@@ -672,23 +672,30 @@ int w4_quantize_int8(const void* x, int type, int64_t rows, int64_t K, int8_t* c
  *   xs      device float[B]; 4-byte aligned
  *   wq      device int8[N, K]; 16-byte aligned
  *   ws      device float[N]; 4-byte aligned
- *   N       1 <= N < 2^31
+ *   N       1 <= N < 2^24
  *   K       a positive multiple of 64, at most W4_INT8_MAX_K
- *   B       1 <= B < 2^20
+ *   B       1 <= B < 2^16, B * N < 2^37
  *   y       device [B, N] of `type` (w4_type_t), fully overwritten; aligned to its element; must not overlap an
- *           input
- * No workspace.  Asynchronous on `stream`. */
+ *           input or the workspace
+ *   workspace  device memory of at least w4_int8_workspace_bytes(...) bytes, 16-byte aligned; may be NULL when that
+ *           is 0; scratch on entry and exit; must not overlap an input; two calls in flight must not share it
+ * Asynchronous on `stream`. */
 int w4_gemm_int8(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws, int64_t N, int64_t K, int64_t B,
-                 void* y, int type, void* stream);
+                 void* y, int type, void* workspace, size_t workspace_bytes, void* stream);
 
 /* w4_gated_int8: w4_gated over 8-bit tokens and weights: g and u are w4_gemm_int8's products with the gate rows and
  * the up rows of wq [2 * inter, K], ws [2 * inter].
  *   type    of h and products: W4_F16 or W4_BF16
- *   tokens  1 <= tokens < 2^20
- *   inter   1 <= inter < 2^24
- * The rest as there.  No workspace.  Asynchronous on `stream`. */
+ *   tokens  1 <= tokens < 2^16
+ *   inter   1 <= inter < 2^24, tokens * inter < 2^36
+ * The rest as there.  Asynchronous on `stream`. */
 int w4_gated_int8(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws, int act, int64_t tokens,
-                  int64_t K, int64_t inter, void* h, void* products, int type, void* stream);
+                  int64_t K, int64_t inter, void* h, void* products, int type, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace w4_gemm_int8 (gated = 0) or w4_gated_int8 (gated != 0, N = inter) needs for these sizes (0:
+ * none); 0 for invalid ones. */
+size_t w4_int8_workspace_bytes(int64_t N, int64_t K, int64_t B, int gated);
 
 /* ------------------------------------------------------------------ measurement probes ------ */
 

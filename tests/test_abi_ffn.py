@@ -109,13 +109,16 @@ def test_quantize_int8_refusals():
     assert call(c=FAKE) == -9 and call(s=FAKE + 476) == -9 and call(s=FAKE * 2 + 116) == -9
 
 
-def _int8(L, gated=False, type=1, act=0, n=30, k=128, b=5, **p):
-    a = dict(xq=FAKE, xs=FAKE * 2, wq=FAKE * 3, ws=FAKE * 4, out=FAKE * 5, pr=FAKE * 6)
+def _int8(L, gated=False, type=1, act=0, n=30, k=128, b=5, work=FAKE * 900, wsb=None, **p):
+    a = dict(xq=FAKE, xs=FAKE * 2, wq=FAKE * 3, ws=FAKE * 400, out=FAKE * 500, pr=FAKE * 600)
     a.update(p)
     v = {q: vp(z) for q, z in a.items()}
+    if wsb is None:
+        wsb = L.w4_int8_workspace_bytes(n, k, b, int(gated))
     if gated:
-        return L.w4_gated_int8(v["xq"], v["xs"], v["wq"], v["ws"], act, b, k, n, v["out"], v["pr"], type, None)
-    return L.w4_gemm_int8(v["xq"], v["xs"], v["wq"], v["ws"], n, k, b, v["out"], type, None)
+        return L.w4_gated_int8(v["xq"], v["xs"], v["wq"], v["ws"], act, b, k, n, v["out"], v["pr"], type, vp(work), wsb,
+                               None)
+    return L.w4_gemm_int8(v["xq"], v["xs"], v["wq"], v["ws"], n, k, b, v["out"], type, vp(work), wsb, None)
 
 
 @pytest.mark.parametrize("gated", [False, True])
@@ -127,19 +130,27 @@ def test_int8_refusals(gated):
     assert _int8(L, gated, type=3) == -4 and _int8(L, gated, type=-1) == -4
     if gated:
         assert _int8(L, gated, type=0) == -4 and _int8(L, gated, act=2) == -4
-    for bad in (dict(b=0), dict(b=1 << 20), dict(k=0), dict(k=96), dict(k=131072), dict(n=0),
-                dict(n=1 << (24 if gated else 31))):
-        assert _int8(L, gated, **bad) == -2, bad
-    for bad in (dict(xq=FAKE + 8), dict(xs=FAKE * 2 + 2), dict(wq=FAKE * 3 + 4), dict(ws=FAKE * 4 + 1),
-                dict(out=FAKE * 5 + 1)):
+    for bad in (dict(b=0), dict(b=1 << 16), dict(k=0), dict(k=96), dict(k=131072), dict(n=0), dict(n=1 << 24),
+                dict(b=1 << 15, n=1 << (21 if gated else 22))):
+        assert _int8(L, gated, wsb=1 << 60, **bad) == -2, bad
+        assert L.w4_int8_workspace_bytes(bad.get("n", 30), bad.get("k", 128), bad.get("b", 5), int(gated)) == 0
+    for bad in (dict(xq=FAKE + 8), dict(xs=FAKE * 2 + 2), dict(wq=FAKE * 3 + 4), dict(ws=FAKE * 400 + 1),
+                dict(out=FAKE * 500 + 1)):
         assert _int8(L, gated, **bad) == -3, bad
-    for name, at in (("xq", FAKE), ("xs", FAKE * 2), ("wq", FAKE * 3), ("ws", FAKE * 4)):
+    long = dict(n=40, k=131008, b=64)  # few results of long rows: K is split
+    used = L.w4_int8_workspace_bytes(40, 131008, 64, int(gated))
+    assert used and used % (64 * 40 * (8 if gated else 4)) == 0
+    assert _int8(L, gated, work=0, **long) == -6 and _int8(L, gated, wsb=used - 1, **long) == -6
+    assert _int8(L, gated, work=FAKE * 900 + 8, **long) == -3
+    for at in (FAKE, FAKE * 2, FAKE * 3, FAKE * 400, FAKE * 500):
+        assert _int8(L, gated, work=at, **long) == -9, at
+    for name, at in (("xq", FAKE), ("xs", FAKE * 2), ("wq", FAKE * 3), ("ws", FAKE * 400)):
         assert _int8(L, gated, out=at) == -9, name
         if gated:
             assert _int8(L, gated, pr=at) == -9, name
     assert _int8(L, gated, out=FAKE * 3 + 128 * 30 * (2 if gated else 1) - 2) == -9
     if gated:
-        assert _int8(L, gated, pr=FAKE * 5) == -9 and _int8(L, gated, pr=FAKE * 6 + 1) == -3
+        assert _int8(L, gated, pr=FAKE * 500) == -9 and _int8(L, gated, pr=FAKE * 600 + 1) == -3
 
 
 def test_binding_refuses_host_tensors():
