@@ -3,18 +3,19 @@
 // fragment is 16 bytes in every type, so one kernel moves bytes and only the matrix instruction differs.
 //
 // Work layout.  A workgroup of WM x WN waves owns a tile of TM = 32 MT WM rows of A by TN = 32 NT WN rows of B and
-// walks K in steps of 64 bytes through a ring of four stages.  Both operand tiles of a step come straight from
-// memory into LDS (buffer loads with the LDS destination), three steps ahead.  One barrier a step: before it a wave
-// waits for its own copies of the next step (those of the one after stay in flight) and for its LDS reads, so that
-// behind it every wave finds the next stage whole and the stage before this one free for new copies.  A wave's
-// fragments are one half step ahead of its matrix instructions, across the barrier too.
-//   * Stage layout: 64 bytes a row, the 16-byte chunk c of row r in slot c XOR (r / 4 mod 4): the sixteen rows that
+// walks K in steps of 128 bytes (whole cache lines: steps of 64 asked the L2 for each line twice, two thirds of the
+// requests it can serve) through a ring of STAGES stages.  Both operand tiles of a step come straight from memory
+// into LDS (buffer loads with the LDS destination).  One barrier a step, before its last quarter: by then a wave has
+// read its last fragments of the stage, and waits for its own copies of the next one; behind it every wave finds the
+// next stage whole and this one free for the copies of the step STAGES further.  A wave's fragments are a quarter
+// ahead of its matrix instructions, across the barrier too.
+//   * Stage layout: 128 bytes a row, the 16-byte chunk c of row r in slot c XOR (r / 2 mod 8): the sixteen rows that
 //     a 16-lane group of a 128-bit LDS read takes then lie in distinct banks.
-//   * A (32 rows x 32 bytes): lane 32 h + c takes row c, bytes 16 h .. 16 h + 15 of the half step.  B the same.
+//   * A (32 rows x 32 bytes): lane 32 h + c takes row c, bytes 16 h .. 16 h + 15 of the quarter.  B the same.
 //   * D (32 x 32): lane 32 h + c holds column c (a row of B), rows 8 (e / 4) + 4 h + e % 4 (register e).
 //   * Gated: the B tile holds TN / 2 gate rows, then the up rows of the same channels; a wave's even column tiles
 //     are gate, its odd ones the up of the same channels, so the activation and the product happen in registers.
-//   * Rows past M or N and steps past K are read at an offset outside the buffer, which gives zeros.
+//   * Rows past M or N and bytes past K are read at an offset outside the buffer, which gives zeros.
 #pragma once
 #include <type_traits>
 
@@ -65,13 +66,14 @@ __device__ inline i32x4 dense_rsrc(const void* base, uint32_t bytes) {
 
 // Copies 16 bytes a lane from offset `off` of the resource to LDS, lane l's to `to` + 16 l (`to` uniform).  By hand,
 // because the compiler makes an LDS read wait for copies that it cannot tell from the one that filled what is read;
-// here the kernel's own waits say which have landed.  It has no result register; its address is read as it issues.
+// here the kernel's own waits say which have landed.  It has no result register; its address is read as it issues; m0
+// holds nothing else (the compiler sets it right before each use of its own).  No memory clobber: copies keep their
+// order to each other and to the barriers, and only to those.
 __device__ inline void dense_copy(i32x4 r, const uint8_t* to, uint32_t off) {
   const uint32_t lds = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)to;
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(
                    __builtin_amdgcn_readfirstlane((int)lds)),
-               "v"(off), "s"(r)
-               : "memory");  // m0 holds nothing else: the compiler sets it right before each use of its own
+               "v"(off), "s"(r));
 }
 
 __device__ inline __amdgpu_buffer_rsrc_t dense_buffer(i32x4 r) {
@@ -79,14 +81,14 @@ __device__ inline __amdgpu_buffer_rsrc_t dense_buffer(i32x4 r) {
       reinterpret_cast<void*>((uint64_t)(uint32_t)r.x | ((uint64_t)(uint32_t)r.y << 32)), (short)0, r.z, r.w);
 }
 
-template <int TYPE, bool GATED, int WM, int WN, int MT, int NT>
+template <int TYPE, bool GATED, int WM, int WN, int MT, int NT, int STAGES>
 __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
   constexpr int W = WM * WN, TM = 32 * MT * WM, TN = 32 * NT * WN;
   constexpr int ROWS = TM + TN;             // rows of a stage
-  constexpr int COPIES = ROWS / 16 / W;     // copies of 16 rows a wave makes for a stage
-  static_assert(TM % (16 * W) == 0 && (GATED ? TN / 2 : TN) % (16 * W) == 0, "a round of copies fills one operand");
+  constexpr int COPIES = ROWS / 8 / W;      // copies of 8 rows a wave makes for a stage
+  static_assert(TM % (8 * W) == 0 && (GATED ? TN / 2 : TN) % (8 * W) == 0, "a round of copies fills one operand");
   static_assert(!GATED || NT % 2 == 0, "gate and up in one wave");
-  __shared__ __align__(16) uint8_t ring[4][ROWS * 64];
+  __shared__ __align__(16) uint8_t ring[STAGES][ROWS * 128];
   using Acc = typename DenseAcc<TYPE>::type;
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -94,46 +96,46 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
   const int wm = wave / WN, wn = wave % WN;
   const int c = lane & 31, h = lane >> 5;
 
-  // Every eighth workgroup runs on one XCD: those take consecutive tiles, the tiles of a column of B first, so that
-  // a B tile is read from memory by one XCD.
+  // Every eighth workgroup runs on one XCD: those take consecutive tiles, in blocks of up to eight tiles along M and as
+  // many columns of B as are in work at once, so that both operands are read by few XCDs.
   const uint32_t mt = (p.m + TM - 1) / TM;
-  const uint32_t tiles = gridDim.x, per = tiles / 8, rem = tiles % 8;
+  const uint32_t tiles = gridDim.x, share = tiles / 8, rem = tiles % 8;
   const uint32_t xcd = blockIdx.x % 8, at = blockIdx.x / 8;
-  const uint32_t tile = xcd * per + min(xcd, rem) + at;
-  const uint32_t m0 = (tile % mt) * TM;
+  const uint32_t tile = xcd * share + min(xcd, rem) + at;
   constexpr uint32_t CN = GATED ? TN / 2 : TN;  // channels of a tile
-  const uint32_t n0 = (tile / mt) * CN;
+  const uint32_t nt = (p.n + CN - 1) / CN;
+  const uint32_t band = tile / (8 * nt), in_band = tile % (8 * nt), high = min(8u, mt - 8 * band);
+  const uint32_t m0 = (8 * band + in_band % high) * TM, n0 = in_band / high * CN;
 
   const uint32_t nrows = min(CN, p.n - n0);
   const i32x4 ra = dense_rsrc(p.a + (size_t)m0 * p.pitch, min((uint32_t)TM, p.m - m0) * p.pitch);
   const i32x4 rb = dense_rsrc(p.b + (size_t)n0 * p.pitch, nrows * p.pitch);
   const i32x4 ru = dense_rsrc(p.b + (size_t)(GATED ? p.n + n0 : 0) * p.pitch, GATED ? nrows * p.pitch : 0u);
 
-  // Copy j of this wave fills rows 16 (W j + wave) .. + 15 of a stage: lane l slot l % 4 of row l / 4.  Its offsets:
+  // Copy j of this wave fills rows 8 (W j + wave) .. + 7 of a stage: lane l slot l % 8 of row l / 8.  Its offsets:
   uint32_t off[COPIES];
+  const uint32_t mine = (((uint32_t)lane & 7u) ^ ((4u * wave + ((uint32_t)lane >> 4)) & 7u)) * 16;  // the chunk, for W even
+  static_assert(W % 2 == 0, "the same chunk in every copy");
 #pragma unroll
   for (int j = 0; j < COPIES; ++j) {
-    const uint32_t r = 16u * (uint32_t)(W * j + wave) + ((uint32_t)lane >> 2);
-    const uint32_t ch = ((uint32_t)lane & 3u) ^ ((r >> 2) & 3u);
+    const uint32_t r = 8u * (uint32_t)(W * j + wave) + ((uint32_t)lane >> 3);
     const uint32_t row = r < (uint32_t)TM ? r : (r - TM) % CN;
     const uint32_t rows = r < (uint32_t)TM ? min((uint32_t)TM, p.m - m0) : nrows;
-    off[j] = row < rows ? row * p.pitch + ch * 16 : kOutOfRange - p.pitch;
+    off[j] = row < rows ? row * p.pitch + mine : kOutOfRange - p.pitch;
   }
-  const uint32_t first = blockIdx.y * p.per, steps = min(first + p.per, p.pitch / 64);  // this split's
-  // The copies of step t; past the last step they are made all the same, from outside the buffers, so that the
-  // number of copies in flight is the same in every step.
-  auto copy = [&](const uint8_t* st, uint32_t t) __attribute__((always_inline)) {
-    const uint32_t k = t < steps ? t * 64 : 0x40000000u;
-#pragma unroll
-    for (int j = 0; j < COPIES; ++j) {
-      const uint8_t* to = st + 16 * (W * j + wave) * 64;
-      if (16 * W * j < TM)  // known when compiled
-        dense_copy(ra, to, off[j] + k);
-      else if (!GATED || 16 * W * j < TM + (int)CN)
-        dense_copy(rb, to, off[j] + k);
-      else
-        dense_copy(ru, to, off[j] + k);
-    }
+  const uint32_t first = blockIdx.y * p.per, steps = min(first + p.per, (p.pitch + 127) / 128);  // this split's
+  // Copy j of step t; past the last step copies are made all the same, from outside the buffers, so that the number
+  // of copies in flight is the same in every step.
+  auto copy = [&](const uint8_t* st, uint32_t t, int j) __attribute__((always_inline)) {
+    uint32_t k = t < steps ? t * 128 : 0x40000000u;
+    if constexpr (TYPE == kDenseI8) k = k + mine < p.pitch ? k : 0x40000000u;  // rows may end in the middle of a step
+    const uint8_t* to = st + 8 * (W * j + wave) * 128;
+    if (8 * W * j < TM)  // known when compiled
+      dense_copy(ra, to, off[j] + k);
+    else if (!GATED || 8 * W * j < TM + (int)CN)
+      dense_copy(rb, to, off[j] + k);
+    else
+      dense_copy(ru, to, off[j] + k);
   };
 
   Acc acc[MT][NT];
@@ -144,58 +146,66 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
-  const uint32_t key = ((uint32_t)c >> 2) & 3u;  // every fragment row is c modulo 32
+  const uint32_t key = ((uint32_t)c >> 1) & 7u;  // every fragment row is c modulo 32
   struct Frags {
     uint4 a[MT], b[NT];
   };
-  auto load = [&](Frags& f, const uint8_t* st, int s) __attribute__((always_inline)) {
-    const uint32_t slot = ((uint32_t)(2 * s + h) ^ key) * 16 + c * 64;
-#pragma unroll
-    for (int i = 0; i < MT; ++i) f.a[i] = *reinterpret_cast<const uint4*>(st + 32 * (MT * wm + i) * 64 + slot);
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int row = TM + (GATED ? (j & 1) * (int)CN + 32 * (NT / 2 * wn + j / 2) : 32 * (NT * wn + j));
-      f.b[j] = *reinterpret_cast<const uint4*>(st + row * 64 + slot);
-    }
+  // Quarter s of the stage at byte `st` of the ring.
+  const uint32_t base = (((uint32_t)h ^ key) * 16) + c * 128;
+  auto fetch = [&](Frags& f, const uint8_t* at, int i) __attribute__((always_inline)) {  // fragment i of a quarter
+    const int j = i - MT;
+    const int row = i < MT ? 32 * (MT * wm + i)
+                           : TM + (GATED ? (j & 1) * (int)CN + 32 * (NT / 2 * wn + j / 2) : 32 * (NT * wn + j));
+    const uint4 v = *reinterpret_cast<const uint4*>(at + row * 128);
+    if (i < MT)
+      f.a[i] = v;
+    else
+      f.b[j] = v;
   };
-  auto multiply = [&](const Frags& f) __attribute__((always_inline)) {
+  constexpr uint32_t SIZE = ROWS * 128;
+  // The copies of a step are spread over the quarters in which its stage is free, the last of this step and the first
+  // ones of the next (two stages: only the first, so that they have half a step to arrive): in one burst behind the
+  // barrier they kept the waves from issuing matrix instructions.
+  constexpr int C3 = STAGES == 2 ? (COPIES + 1) / 2 : (COPIES + 3) / 4;  // up to the end of quarter 3, 0, 1, 2
+  constexpr int C0 = STAGES == 2 ? COPIES : COPIES < 2 * C3 ? COPIES : 2 * C3;
+  constexpr int C1 = COPIES < 3 * C3 ? COPIES : 3 * C3;
+  // A quarter: after each matrix instruction one of the next quarter's fragments is requested, and a copy now and then.
+  auto quarter = [&](Frags& next, uint32_t st, int s, const Frags& f, uint32_t to, uint32_t t, auto from, auto end)
+      __attribute__((always_inline)) {
+    constexpr int A = decltype(from)::value, Z = decltype(end)::value, ALL = MT * NT;
+    const uint8_t* at = &ring[0][0] + ((base + st) ^ (uint32_t)(s * 32));
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int q = 0; q < ALL; ++q) {
+      acc[q / NT][q % NT] = dense_mfma<TYPE>(f.a[q / NT], f.b[q % NT], acc[q / NT][q % NT]);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = dense_mfma<TYPE>(f.a[i], f.b[j], acc[i][j]);
-  };
-  // A half step: the fragments of the next one are requested between this one's matrix instructions.
-  auto half = [&](Frags& next, const uint8_t* st, int s, const Frags& f) __attribute__((always_inline)) {
-    load(next, st, s);
-    multiply(f);
+      for (int i = 0; i < MT + NT; ++i)
+        if (i * ALL / (MT + NT) == q) fetch(next, at, i);
 #pragma unroll
-    for (int i = 0; i < MT * NT; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a matrix instruction
-      if (i < MT + NT) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // an LDS read
+      for (int j = A; j < Z; ++j)
+        if ((j - A) * ALL / (Z - A > 0 ? Z - A : 1) == q) copy(&ring[0][0] + to, t, j);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
   Frags f0, f1;
-  copy(ring[0], first);
-  copy(ring[1], first + 1);
-  copy(ring[2], first + 2);
-  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(2 * COPIES) : "memory");
-  load(f0, ring[0], 0);
-  auto step = [&](uint8_t* st, uint8_t* next, uint8_t* free, uint32_t t) __attribute__((always_inline)) {
+#pragma unroll
+  for (int i = 0; i < STAGES; ++i)
+#pragma unroll
+    for (int j = 0; j < (i == STAGES - 1 ? C3 : COPIES); ++j) copy(&ring[i][0], first + i, j);
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((STAGES - 2) * COPIES + C3) : "memory");
+#pragma unroll
+  for (int i = 0; i < MT + NT; ++i) fetch(f0, &ring[0][0] + base, i);
+  uint32_t now = 0, spare = (STAGES - 1) * SIZE;  // the step's stage, and the last step's
+  using std::integral_constant;
+  for (uint32_t t = first; t < steps; ++t) {
+    const uint32_t u = t + STAGES - 1;
+    quarter(f1, now, 1, f0, spare, u, integral_constant<int, C3>{}, integral_constant<int, C0>{});
+    quarter(f0, now, 2, f1, spare, u, integral_constant<int, C0>{}, integral_constant<int, C1>{});
+    quarter(f1, now, 3, f0, spare, u, integral_constant<int, C1>{}, integral_constant<int, COPIES>{});
     // by hand: the compiler's own barrier waits for every copy in flight
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(COPIES) : "memory");
-    copy(free, t + 3);
-    half(f1, st, 1, f0);
-    half(f0, next, 0, f1);
-  };
-  for (uint32_t t = first;;) {
-    step(ring[0], ring[1], ring[3], t);
-    if (++t == steps) break;
-    step(ring[1], ring[2], ring[0], t);
-    if (++t == steps) break;
-    step(ring[2], ring[3], ring[1], t);
-    if (++t == steps) break;
-    step(ring[3], ring[0], ring[2], t);
-    if (++t == steps) break;
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * COPIES) : "memory");
+    spare = now;
+    now = now + SIZE == STAGES * SIZE ? 0 : now + SIZE;
+    quarter(f0, now, 0, f1, spare, u + 1, integral_constant<int, 0>{}, integral_constant<int, C3>{});
   }
   wait_all_vector_loads();  // no copy outlives the workgroup
 
@@ -374,12 +384,12 @@ __global__ void __launch_bounds__(256) dense_sum_kernel(DenseArgs p) {
   }
 }
 
-template <int TYPE, bool GATED, int WM, int WN, int MT, int NT>
+template <int TYPE, bool GATED, int WM, int WN, int MT, int NT, int STAGES>
 hipError_t dense_launch(const DenseArgs& a, hipStream_t s) {
   constexpr uint32_t TM = 32 * MT * WM, CN = 32 * NT * WN / (GATED ? 2 : 1);
   const uint64_t tiles = (uint64_t)((a.m + TM - 1) / TM) * ((a.n + CN - 1) / CN);
   if (tiles >= ((uint64_t)1 << 31)) return hipErrorInvalidValue;
-  dense_kernel<TYPE, GATED, WM, WN, MT, NT><<<dim3((uint32_t)tiles, a.splits), dim3(64 * WM * WN), 0, s>>>(a);
+  dense_kernel<TYPE, GATED, WM, WN, MT, NT, STAGES><<<dim3((uint32_t)tiles, a.splits), dim3(64 * WM * WN), 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   if (a.wide)

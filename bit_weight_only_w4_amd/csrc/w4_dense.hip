@@ -25,7 +25,7 @@ struct DensePlan {
 // latency); a CU's workgroups share both.  Each round of workgroups pays its start and end; a split K
 // pays for writing and reading its sums.
 DensePlan plan_dense(bool gated, int64_t m, int64_t n, int64_t pitch) {
-  const int64_t cus = device_cu_count(), steps = pitch / 64;
+  const int64_t cus = device_cu_count(), steps = (pitch + 127) / 128;
   const int64_t width = gated ? 2 * n : n;
   DensePlan best{0, 1, (uint32_t)steps};
   double least = 0;
@@ -33,12 +33,12 @@ DensePlan plan_dense(bool gated, int64_t m, int64_t n, int64_t pitch) {
     const Tile& t = kTiles[i];
     const int64_t tm = 32 * t.mt * t.wm, tn = 32 * t.nt * t.wn;
     const int64_t tiles = ((m + tm - 1) / tm) * ((width + tn - 1) / tn);
-    const double step = std::max(tm * tn / 64.0, (tm + tn) * 64 / 48.0);
-    for (int64_t s = 1; s <= 32 && s * 8 <= std::max<int64_t>(steps, 8); ++s) {
+    const double step = std::max(tm * tn / 32.0, (tm + tn) * 128 / 48.0);
+    for (int64_t s = 1; s <= 32 && s * 4 <= std::max<int64_t>(steps, 4); ++s) {
       const int64_t per = (steps + s - 1) / s;
       if ((s - 1) * per >= steps) continue;  // an empty split
       const int64_t on_cu = (tiles * s + cus - 1) / cus;  // workgroups of the busiest CU
-      const double lonely = std::max(step, 650.0 / std::min<int64_t>(on_cu, t.fit));  // the copies' latency over three steps
+      const double lonely = std::max(step, 1300.0 / std::min<int64_t>(on_cu, t.fit));  // the copies' latency over three steps
       double clocks = on_cu * per * lonely + (double)((on_cu + t.fit - 1) / t.fit) * 4000 + on_cu * tm * tn / 24.0;
       if (s > 1) clocks += 7000 + (double)s * m * width * 8 / 1600;
       if (least == 0 || clocks < least) {
@@ -53,10 +53,10 @@ DensePlan plan_dense(bool gated, int64_t m, int64_t n, int64_t pitch) {
 template <int TYPE, bool GATED>
 hipError_t dense_pick(int tile, const DenseArgs& a, hipStream_t s) {
   switch (tile) {
-    case 0: return dense_launch<TYPE, GATED, 2, 4, 4, 2>(a, s);
-    case 1: return dense_launch<TYPE, GATED, 2, 2, 2, 2>(a, s);
-    case 2: return dense_launch<TYPE, GATED, 2, 2, 1, 2>(a, s);
-    default: return dense_launch<TYPE, GATED, 1, 2, 1, 2>(a, s);
+    case 0: return dense_launch<TYPE, GATED, 2, 4, 4, 2, 2>(a, s);
+    case 1: return dense_launch<TYPE, GATED, 2, 2, 2, 2, 2>(a, s);
+    case 2: return dense_launch<TYPE, GATED, 2, 2, 1, 2, 2>(a, s);
+    default: return dense_launch<TYPE, GATED, 1, 2, 1, 2, 2>(a, s);
   }
 }
 
