@@ -7,12 +7,15 @@ namespace w4 {
 
 namespace {
 
-// The tiles, largest first: waves along M and N, 32-row tiles of a wave along M and N, and how many workgroups a CU
-// holds (LDS: four stages).
+// The tiles, largest first: waves along M and N, 32-row tiles of a wave along M and N, stages; how many workgroups of it
+// a CU holds (LDS), and what was measured (MI355X, over twelve shapes of 1 to 4096 rows, fp16 and int8): microseconds
+// a step of 128 bytes when alone on a CU and when the CU is full, and a round's start and end.
 struct Tile {
-  int wm, wn, mt, nt, fit;
+  int tm, tn, fit;
+  double alone, full, ends;
 };
-constexpr Tile kTiles[] = {{2, 4, 4, 2, 1}, {2, 2, 2, 2, 2}, {2, 2, 1, 2, 3}, {1, 2, 1, 2, 4}};
+constexpr Tile kTiles[] = {{256, 256, 1, 1.85, 1.85, 5}, {128, 256, 1, 0.92, 0.92, 4}, {64, 128, 2, 0.34, 0.50, 3},
+                           {32, 128, 2, 0.33, 0.42, 3}};
 constexpr int kTileCount = 4;
 
 struct DensePlan {
@@ -20,10 +23,11 @@ struct DensePlan {
   uint32_t splits, per;
 };
 
-// Tile and splits by an estimate in clocks.  A step of a tile takes the matrix cores TM TN / 64 clocks and (TM + TN) 64
-// bytes through the caches, at about 48 bytes a clock and CU (what three stages in flight carry over the memory's
-// latency); a CU's workgroups share both.  Each round of workgroups pays its start and end; a split K
-// pays for writing and reading its sums.
+// Tile and K splits by an estimate in microseconds: rounds of workgroups over the CUs, each operand's bytes at 5.5 TB/s
+// where that takes longer, and for a split the second kernel and its sums' way through memory.  Against the best of
+// 4 tiles and 1 to 20 splits it is within 7% on those shapes (64 x 128 tiles for 40 x 28672 x 8192 int8: 36 us, its
+// weights at 6.5 TB/s; 128 x 256 for 1000 x 17920 x 1536 fp16: 78 us, 256 x 256 there 87; five splits of 256 x 256
+// for 2048 x 1536 x 17920 fp16: 129 us, unsplit 128 x 256 tiles 262).
 DensePlan plan_dense(bool gated, int64_t m, int64_t n, int64_t pitch) {
   const int64_t cus = device_cu_count(), steps = (pitch + 127) / 128;
   const int64_t width = gated ? 2 * n : n;
@@ -31,18 +35,17 @@ DensePlan plan_dense(bool gated, int64_t m, int64_t n, int64_t pitch) {
   double least = 0;
   for (int i = 0; i < kTileCount; ++i) {
     const Tile& t = kTiles[i];
-    const int64_t tm = 32 * t.mt * t.wm, tn = 32 * t.nt * t.wn;
-    const int64_t tiles = ((m + tm - 1) / tm) * ((width + tn - 1) / tn);
-    const double step = std::max(tm * tn / 32.0, (tm + tn) * 128 / 48.0);
-    for (int64_t s = 1; s <= 32 && s * 4 <= std::max<int64_t>(steps, 4); ++s) {
+    const int64_t tiles = ((m + t.tm - 1) / t.tm) * ((width + t.tn - 1) / t.tn);
+    for (int64_t s = 1; s <= 20 && s * 4 <= std::max<int64_t>(steps, 4); ++s) {
       const int64_t per = (steps + s - 1) / s;
       if ((s - 1) * per >= steps) continue;  // an empty split
-      const int64_t on_cu = (tiles * s + cus - 1) / cus;  // workgroups of the busiest CU
-      const double lonely = std::max(step, 1300.0 / std::min<int64_t>(on_cu, t.fit));  // the copies' latency over three steps
-      double clocks = on_cu * per * lonely + (double)((on_cu + t.fit - 1) / t.fit) * 4000 + on_cu * tm * tn / 24.0;
-      if (s > 1) clocks += 7000 + (double)s * m * width * 8 / 1600;
-      if (least == 0 || clocks < least) {
-        least = clocks;
+      const int64_t rounds = (tiles * s + cus * t.fit - 1) / (cus * t.fit);
+      const double work = rounds * (per * (tiles * s <= cus ? t.alone : t.full) + t.ends);
+      const double bytes = (double)(m + width) * pitch / 5.5e6;
+      double us = std::max(work, bytes) + 0.1 * std::min(work, bytes);
+      if (s > 1) us += 3 + (double)s * m * width * 8 / 5e6;
+      if (least == 0 || us < least) {
+        least = us;
         best = DensePlan{i, (uint32_t)s, (uint32_t)per};
       }
     }
@@ -54,9 +57,9 @@ template <int TYPE, bool GATED>
 hipError_t dense_pick(int tile, const DenseArgs& a, hipStream_t s) {
   switch (tile) {
     case 0: return dense_launch<TYPE, GATED, 2, 4, 4, 2, 2>(a, s);
-    case 1: return dense_launch<TYPE, GATED, 2, 2, 2, 2, 2>(a, s);
-    case 2: return dense_launch<TYPE, GATED, 2, 2, 1, 2, 2>(a, s);
-    default: return dense_launch<TYPE, GATED, 1, 2, 1, 2, 2>(a, s);
+    case 1: return dense_launch<TYPE, GATED, 2, 4, 2, 2, 3>(a, s);
+    case 2: return dense_launch<TYPE, GATED, 2, 2, 1, 2, 3>(a, s);
+    default: return dense_launch<TYPE, GATED, 1, 2, 1, 2, 4>(a, s);
   }
 }
 

@@ -66,8 +66,5 @@ hipError_t launch_grad_few_bf16(int weight, const GradFewArgs& a, uint32_t split
 // ---- 8 bits
 hipError_t launch_quantize_int8(int type, const void* x, int64_t rows, int64_t k, int8_t* codes, float* scales,
                                 hipStream_t s);
-hipError_t launch_int8(bool gated, const DenseArgs& a, hipStream_t s);
-// Scratch that the product needs.
-size_t int8_bytes(bool gated, int64_t b, int64_t n, int64_t k);
 
 }  // namespace w4

@@ -1,5 +1,4 @@
-// 8-bit rows and products: the quantizer, and the launches of the products (kernels in w4_int8_few.h and
-// w4_dense.h).
+// 8-bit rows: the quantizer (the products are launches of the dense kernel, w4_dense.h).
 //
 // A row's scale is s = fp32(max|x| / 127) and its codes q = rint(x / s), ties to even, held to +-127 (a subnormal
 // scale may be rounded so far down that the quotient passes 127).  The nearest integer of the exact quotient:
@@ -8,7 +7,6 @@
 // scale NaN and codes 0, so its products are NaN.
 #include "w4_ffn.h"
 #include "w4_ffn_math.h"
-#include "w4_int8_few.h"
 
 namespace w4 {
 namespace {
@@ -157,17 +155,6 @@ hipError_t launch_quantize_int8(int type, const void* x, int64_t rows, int64_t k
   else
     quantize_typed<2>(x, rows, k, codes, scales, s);
   return hipGetLastError();
-}
-
-// Up to 32 tokens stream the weights (32-bit offsets hold their rows: K < 2^17); more go through the dense kernel.
-bool int8_few(int64_t b) { return b <= 32; }
-
-size_t int8_bytes(bool gated, int64_t b, int64_t n, int64_t k) { return int8_few(b) ? 0 : dense_bytes(gated, b, n, k); }
-
-hipError_t launch_int8(bool gated, const DenseArgs& a, hipStream_t s) {
-  if (!int8_few(a.m)) return launch_dense(kDenseI8, gated, a, s);
-  if (a.m <= 16) return gated ? int8_few_launch<true, 1>(a, s) : int8_few_launch<false, 1>(a, s);
-  return gated ? int8_few_launch<true, 2>(a, s) : int8_few_launch<false, 2>(a, s);
 }
 
 }  // namespace w4
