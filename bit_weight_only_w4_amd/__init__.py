@@ -716,15 +716,23 @@ def _weights(name, packed, scales, fmt, k, index):
     return code, n
 
 
-def _scratch(workspace, size, device, index):
-    """A workspace of `size` bytes, allocated if not given: (tensor or None, its bytes)."""
+def _with_workspace(entry, head, workspace, size_of, device, index):
+    """Calls a library entry whose last arguments are a workspace, its bytes and the stream.  Without one given, the
+    first try goes without: an entry that needs none runs, one that does says so before it launches anything."""
     import torch
 
+    stream = torch._C._cuda_getCurrentRawStream(index)
     if workspace is None:
-        return (torch.empty(size, dtype=torch.uint8, device=device), size) if size else (None, 0)
-    if workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the first tensor's GPU")
-    return workspace, workspace.numel() * workspace.element_size()
+        status = entry(*head, None, 0, stream)
+        if status != -6:
+            return status
+        size = size_of()
+        workspace = torch.empty(size, dtype=torch.uint8, device=device)
+    else:
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the first tensor's GPU")
+        size = workspace.numel() * workspace.element_size()
+    return entry(*head, workspace.data_ptr(), size, stream)
 
 
 def _block_outputs(t, i, dtype, device, index, h, products, save):
@@ -771,9 +779,9 @@ def gated(x, gate_up, gate_up_scales, fmt, act="silu", save=False, h=None, produ
 
     L = lib()
     h, products = _block_outputs(t, n // 2, x.dtype, x.device, index, h, products, save)
-    workspace, size = _scratch(workspace, L.w4_gated_workspace_bytes(code, t, k, n // 2), x.device, index)
-    status = L.w4_gated(x.data_ptr(), gate_up.data_ptr(), gate_up_scales.data_ptr(), code, a, t, k, n // 2,
-                        h.data_ptr(), _ptr(products), _ptr(workspace), size, torch._C._cuda_getCurrentRawStream(index))
+    status = _with_workspace(L.w4_gated, (x.data_ptr(), gate_up.data_ptr(), gate_up_scales.data_ptr(), code, a, t, k,
+                                          n // 2, h.data_ptr(), _ptr(products)), workspace,
+                             lambda: L.w4_gated_workspace_bytes(code, t, k, n // 2), x.device, index)
     if status:
         check(status, "w4_gated")
     return h if products is None else (h, products)
@@ -832,9 +840,9 @@ def gemm_grad(d, packed, scales, fmt, dx=None, workspace=None, stream=None):
         dx = torch.empty((b, k), dtype=d.dtype, device=d.device)
     else:
         _expect("dx", dx, (b, k), d.dtype, index)
-    workspace, size = _scratch(workspace, L.w4_gemm_grad_workspace_bytes(code, n, k, b), d.device, index)
-    status = L.w4_gemm_grad(d.data_ptr(), packed.data_ptr(), scales.data_ptr(), code, n, k, b, dx.data_ptr(),
-                            _ptr(workspace), size, torch._C._cuda_getCurrentRawStream(index))
+    status = _with_workspace(L.w4_gemm_grad, (d.data_ptr(), packed.data_ptr(), scales.data_ptr(), code, n, k, b,
+                                              dx.data_ptr()), workspace,
+                             lambda: L.w4_gemm_grad_workspace_bytes(code, n, k, b), d.device, index)
     if status:
         check(status, "w4_gemm_grad")
     return dx
@@ -881,15 +889,17 @@ def _int8_operands(xq, xs, wq, ws):
     """(GPU index, tokens, K, weight rows) of the operands of an 8-bit product."""
     import torch
 
-    index = _rows("xq", xq, "[B, K]")
+    index = xq.get_device()
+    if xq.dim() != 2 or wq.dim() != 2 or index < 0:
+        raise ValueError("xq must be [B, K] and wq [N, K], on the GPU")
     b, k = xq.shape
-    if wq.dim() != 2:
-        raise ValueError("wq must be a 2-D int8 tensor [N, K]")
     n = wq.shape[0]
-    _expect("xq", xq, (b, k), torch.int8, index)
-    _expect("xs", xs, (b,), torch.float32, index)
-    _expect("wq", wq, (n, k), torch.int8, index)
-    _expect("ws", ws, (n,), torch.float32, index)
+    i8, f32 = torch.int8, torch.float32
+    if not (xq.dtype is i8 and wq.dtype is i8 and xs.dtype is f32 and ws.dtype is f32 and wq.shape[1] == k
+            and xs.shape == (b,) and ws.shape == (n,) and wq.get_device() == index and xs.get_device() == index
+            and ws.get_device() == index and xq.is_contiguous() and wq.is_contiguous() and xs.is_contiguous()
+            and ws.is_contiguous()):
+        raise ValueError("xq int8 [B, K], xs float32 [B], wq int8 [N, K] and ws float32 [N] must be contiguous, on one GPU")
     return index, b, k, n
 
 
@@ -916,9 +926,9 @@ def gemm_int8(xq, xs, wq, ws, dtype=None, y=None, workspace=None, stream=None):
         y = torch.empty((b, n), dtype=dtype, device=xq.device)
     else:
         _expect("y", y, (b, n), dtype, index)
-    workspace, size = _scratch(workspace, L.w4_int8_workspace_bytes(n, k, b, 0), xq.device, index)
-    status = L.w4_gemm_int8(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), n, k, b, y.data_ptr(), kind,
-                            _ptr(workspace), size, torch._C._cuda_getCurrentRawStream(index))
+    status = _with_workspace(L.w4_gemm_int8, (xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), n, k, b,
+                                              y.data_ptr(), kind), workspace,
+                             lambda: L.w4_int8_workspace_bytes(n, k, b, 0), xq.device, index)
     if status:
         check(status, "w4_gemm_int8")
     return y
@@ -942,10 +952,9 @@ def gated_int8(xq, xs, wq, ws, act="silu", dtype=None, save=False, h=None, produ
             return gated_int8(xq, xs, wq, ws, act, dtype, save, h, products, workspace)
     L = lib()
     h, products = _block_outputs(t, n // 2, dtype, xq.device, index, h, products, save)
-    workspace, size = _scratch(workspace, L.w4_int8_workspace_bytes(n // 2, k, t, 1), xq.device, index)
-    status = L.w4_gated_int8(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), a, t, k, n // 2,
-                             h.data_ptr(), _ptr(products), kind, _ptr(workspace), size,
-                             torch._C._cuda_getCurrentRawStream(index))
+    status = _with_workspace(L.w4_gated_int8, (xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), a, t, k,
+                                               n // 2, h.data_ptr(), _ptr(products), kind), workspace,
+                             lambda: L.w4_int8_workspace_bytes(n // 2, k, t, 1), xq.device, index)
     if status:
         check(status, "w4_gated_int8")
     return h if products is None else (h, products)
