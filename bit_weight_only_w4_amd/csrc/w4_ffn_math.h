@@ -58,10 +58,6 @@ __device__ inline uint32_t to16(float v) {
   return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
-// Weight j (0 .. 7) of a packed dword, as its code's value: byte j / 2, high nibble first.  E2M1 and NF4 through
-// the fp32 table `codes`; INT4 as q - 8, asymmetric INT4 as q - z.
-__device__ inline uint32_t nibble(uint32_t w, int j) { return (w >> (8 * (j >> 1) + ((j & 1) ? 0 : 4))) & 15u; }
-
 // A block's scale as fp32 from its stored form (INT4A: the low half of its word).
 template <int FMT>
 __device__ inline float scale_of(const void* scales, size_t i) {
@@ -72,6 +68,50 @@ __device__ inline float scale_of(const void* scales, size_t i) {
 }
 template <int FMT>
 constexpr int weights_per_scale() { return is_g128(FMT) ? 128 : FMT == kMXFP4 ? 32 : 64; }
+
+// A block's scale and what its codes' offset is (INT4 8, asymmetric INT4 its zero point).
+struct BlockScale {
+  float s, zero;
+};
+template <int FMT>
+__device__ inline BlockScale block_scale(const void* scales, size_t i) {
+  BlockScale b;
+  b.s = scale_of<FMT>(scales, i);
+  b.zero = FMT == kINT4A ? (float)((reinterpret_cast<const uint32_t*>(scales)[i] >> 16) & 15u) : 8.0f;
+  return b;
+}
+
+// The fp32 codes of NF4, by the first sixteen threads of a workgroup (other formats need none).
+template <int FMT>
+__device__ inline void code_table(float* table) {
+  constexpr uint32_t kn[16] = W4_NF4_CODE_BITS;
+  if (FMT == kNF4 && threadIdx.x < 16) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) bits = (int)threadIdx.x == q ? kn[q] : bits;
+    table[threadIdx.x] = __uint_as_float(bits);
+  }
+}
+
+// The two weights of byte j of a packed dword in fp32, code times scale, the high nibble's (the earlier k) first:
+// NF4 through the table, E2M1 by the hardware's conversion, integers less their offset (exact) times the scale.
+template <int FMT>
+__device__ inline void decode_pair(uint32_t v, int j, const float* table, BlockScale b, float* first, float* second) {
+  if constexpr (FMT == kNF4) {
+    *first = table[(v >> (8 * j + 4)) & 15u] * b.s;
+    *second = table[(v >> (8 * j)) & 15u] * b.s;
+  } else if constexpr (FMT == kFP4 || FMT == kMXFP4) {
+    const auto c = j == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 0)
+                   : j == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 1)
+                   : j == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 2)
+                            : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 3);
+    *first = c[1] * b.s;
+    *second = c[0] * b.s;
+  } else {
+    *first = ((float)((v >> (8 * j + 4)) & 15u) - b.zero) * b.s;
+    *second = ((float)((v >> (8 * j)) & 15u) - b.zero) * b.s;
+  }
+}
 
 // Exponent e with |s code| 2^-e < 2^15 for every code of the format: the largest fp16 binade.
 template <int FMT>

@@ -27,48 +27,60 @@ struct DecodeArgs {
   uint32_t t;
 };
 
-// A wave a row: weight rows first, then token rows.
+// A wave a row: weight rows first, then token rows.  A lane takes 8 consecutive weights of every 512 (so that a store
+// of the wave is 1 KiB in one piece), the first kHeld rounds with their scales in flight at once; the largest of
+// these scales is the row's unless the row is longer.
+constexpr int kHeld = 4;
+
 template <int FMT>
 __global__ void __launch_bounds__(kDecodeThreads) decode_rows_kernel(DecodeArgs p) {
   const int lane = threadIdx.x & 63;
   const uint32_t row = blockIdx.x * (kDecodeThreads / 64) + (threadIdx.x >> 6);
   constexpr uint32_t G = weights_per_scale<FMT>();
-  constexpr uint32_t kn[16] = W4_NF4_CODE_BITS;
-  constexpr uint32_t kf[16] = W4_FP4_CODE_BITS;
   __shared__ float table[16];
-  if (threadIdx.x < 16) {
-    uint32_t bits = 0;
-#pragma unroll
-    for (int q = 0; q < 16; ++q) bits = (int)threadIdx.x == q ? (FMT == kNF4 ? kn[q] : kf[q]) : bits;
-    table[threadIdx.x] = is_g128(FMT) ? (float)((int)threadIdx.x - 8) : __uint_as_float(bits);
-  }
+  code_table<FMT>(table);
   __syncthreads();
   if (row < p.n) {
-    const uint32_t groups = p.k / G;
+    const uint32_t groups = p.k / G, chunks = p.k / 8;
     const size_t s0 = (size_t)row * groups;
-    float top = 0.0f;
-    for (uint32_t i = lane; i < groups; i += 64) {
-      const float s = fabsf(scale_of<FMT>(p.scales, s0 + i));
-      top = s < __builtin_inff() ? fmaxf(top, s) : top;  // infinities and NaN have no binade
-    }
-    const int f = fold_exponent<FMT>(wave_max(top));
-    if (lane == 0) p.w_exp[row] = f;
     const uint32_t* src = reinterpret_cast<const uint32_t*>(p.packed + (size_t)row * (p.k / 2));
     uint4* dst = reinterpret_cast<uint4*>(p.w + (size_t)row * p.k);
-    for (uint32_t i = lane; i < p.k / 8; i += 64) {
-      const uint32_t v = src[i];
-      const float s = ldexpf(scale_of<FMT>(p.scales, s0 + i * 8 / G), -f);
-      float shift = 0.0f;
-      if constexpr (FMT == kINT4A)
-        shift = 8.0f - (float)((reinterpret_cast<const uint32_t*>(p.scales)[s0 + i * 8 / G] >> 16) & 15u);
+    uint32_t v[kHeld];
+    BlockScale s[kHeld];
+    float top = 0.0f;
+    auto fold = [&](float x) __attribute__((always_inline)) {
+      const float a = fabsf(x);
+      top = a < __builtin_inff() ? fmaxf(top, a) : top;  // infinities and NaN have no binade
+    };
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      const uint32_t i = j * 64 + lane;
+      if (i < chunks) {
+        v[j] = src[i];
+        s[j] = block_scale<FMT>(p.scales, s0 + i * 8 / G);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j)
+      if (j * 64 + lane < chunks) fold(s[j].s);
+    for (uint32_t i = kHeld * 512 / G + lane; i < groups; i += 64) fold(scale_of<FMT>(p.scales, s0 + i));
+    const int f = fold_exponent<FMT>(wave_max(top));
+    if (lane == 0) p.w_exp[row] = f;
+    auto put = [&](uint32_t i, uint32_t w, BlockScale b) __attribute__((always_inline)) {
+      b.s = ldexpf(b.s, -f);
       uint32_t o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float a = (table[nibble(v, 2 * j)] + shift) * s, b = (table[nibble(v, 2 * j + 1)] + shift) * s;
-        o[j] = to16<kF16>(a) | (to16<kF16>(b) << 16);
+        float lo, hi;
+        decode_pair<FMT>(w, j, table, b, &lo, &hi);
+        o[j] = to16<kF16>(lo) | (to16<kF16>(hi) << 16);
       }
       dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
-    }
+    };
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j)
+      if (j * 64 + lane < chunks) put(j * 64 + lane, v[j], s[j]);
+    for (uint32_t i = kHeld * 64 + lane; i < chunks; i += 64) put(i, src[i], block_scale<FMT>(p.scales, s0 + i * 8 / G));
     return;
   }
   const uint32_t t = row - p.n;

@@ -1,7 +1,7 @@
 // Input gradient of a product with frozen 4-bit weights: dx[t, k] = sum_n d[t, n] W_hat[n, k].
 //
 // The sum runs over the weight rows, along which a packed byte holds nothing: the weights are decoded once into
-// W_hat^T rows of 16 bits in the workspace (through LDS, 64 x 64 weights a workgroup), which the dense kernel
+// W_hat^T rows of 16 bits in the workspace (through LDS), which the dense kernel
 // multiplies with d.  A weight is rounded once to d's type (2^-8 of itself in bf16, 2^-11 in fp16; fp16 with one
 // exponent for the whole matrix, taken from its largest scale, so that neither large nor small weights leave its
 // range).  Rows of W_hat^T are padded with zeros to whole steps of the dense kernel, and so is d where its rows do
@@ -14,7 +14,7 @@
 namespace w4 {
 namespace {
 
-constexpr int kTile = 64;       // weights of a tile along either axis
+constexpr int kTile = 64;       // weight rows of a tile
 constexpr int kMaxParts = 256;  // workgroups of the scale scan
 
 template <int FMT>
@@ -39,65 +39,70 @@ struct TransposeArgs {
   const float* parts;     // the scan's maxima, null for bf16
   uint32_t nparts;
   int* exp;               // the exponent that they give
+  uint32_t tiles;         // workgroups that transpose; those after them copy d
+  const uint16_t* d;      // [B, N]
+  uint16_t* padded;       // [B, NP]
 };
+
+// A tile of 64 rows x 256 columns a workgroup, whole cache lines of the packed rows: a thread decodes 32 columns of two
+// rows, writes them to LDS as pairs along n, and stores 16 bytes of rows of W_hat^T.  In LDS column 32 part + j is at
+// row 8 j + part of 40 dwords: the 64 pairs that a wave writes at once then lie in 64 banks.  Neighbouring workgroups
+// take neighbouring rows, whose pieces of W_hat^T are one after another.
+constexpr int kColumns = 256;
 
 template <int FMT, int XT>
 __global__ void __launch_bounds__(256) transpose_kernel(TransposeArgs p) {
   constexpr uint32_t G = weights_per_scale<FMT>();
-  constexpr uint32_t kn[16] = W4_NF4_CODE_BITS;
-  constexpr uint32_t kf[16] = W4_FP4_CODE_BITS;
-  __shared__ float table[16];
-  __shared__ uint16_t tile[kTile][kTile + 2];  // [k][n]
-  const int tid = threadIdx.x;
-  if (tid < 16) {
-    uint32_t bits = 0;
-#pragma unroll
-    for (int q = 0; q < 16; ++q) bits = tid == q ? (FMT == kNF4 ? kn[q] : kf[q]) : bits;
-    table[tid] = is_g128(FMT) ? (float)(tid - 8) : __uint_as_float(bits);
+  constexpr int PITCH = 40;
+  const uint32_t tid = threadIdx.x;
+  if (blockIdx.x >= p.tiles) {  // a row of d, zeros after its end
+    const size_t t = blockIdx.x - p.tiles;
+    for (uint32_t c = tid; c < p.np; c += 256) p.padded[t * p.np + c] = c < p.n ? p.d[t * p.n + c] : (uint16_t)0;
+    return;
   }
-  int f = 0;
+  __shared__ float table[16];
+  __shared__ __align__(16) uint32_t tile[kColumns * PITCH];
+  const uint32_t along = p.np / kTile;
+  const uint32_t n0 = blockIdx.x % along * kTile, k0 = blockIdx.x / along * kColumns;
+  const uint32_t rp = tid >> 3, part = tid & 7;  // rows n0 + 2 rp and the next, columns k0 + 32 part ..
+  const uint32_t kt = k0 + 32 * part;
+  uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  BlockScale s[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t n = n0 + 2 * rp + q;
+    if (n < p.n && kt < p.k) {
+      v[q] = *reinterpret_cast<const uint4*>(p.packed + ((size_t)n * p.k + kt) / 2);
+      s[q] = block_scale<FMT>(p.scales, (size_t)n * (p.k / G) + kt / G);
+    }
+  }
+  code_table<FMT>(table);
   if constexpr (XT == kF16) {  // every wave for itself: at most 256 values
     float top = 0.0f;
     for (uint32_t i = tid & 63; i < p.nparts; i += 64) top = fmaxf(top, p.parts[i]);
-    f = fold_exponent<FMT>(wave_max(top));
-    if (tid == 0 && blockIdx.x == 0 && blockIdx.y == 0) *p.exp = f;
+    const int f = fold_exponent<FMT>(wave_max(top));
+    if (tid == 0 && blockIdx.x == 0) *p.exp = f;
+    s[0].s = ldexpf(s[0].s, -f);
+    s[1].s = ldexpf(s[1].s, -f);
   }
   __syncthreads();
-  const uint32_t n0 = blockIdx.x * kTile, k0 = blockIdx.y * kTile;
-  {
-    const uint32_t r = tid >> 2, part = tid & 3;  // row of the tile, 16 weights of it
-    const uint32_t n = n0 + r, k = k0 + part * 16;
-    if (n < p.n) {
-      const uint2 v = *reinterpret_cast<const uint2*>(p.packed + ((size_t)n * p.k + k) / 2);
-      const size_t at = (size_t)n * (p.k / G) + k / G;
-      const float s = ldexpf(scale_of<FMT>(p.scales, at), -f);
-      float shift = 0.0f;
-      if constexpr (FMT == kINT4A)
-        shift = 8.0f - (float)((reinterpret_cast<const uint32_t*>(p.scales)[at] >> 16) & 15u);
+  const uint32_t w0[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, w1[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        tile[part * 16 + j][r] = (uint16_t)to16<XT>((table[nibble(j < 8 ? v.x : v.y, j & 7)] + shift) * s);
-    } else {
+  for (int j = 0; j < 16; ++j) {
+    float a[2], b[2];  // rows past N have scale 0 and finite codes: zeros
+    decode_pair<FMT>(w0[j >> 2], j & 3, table, s[0], &a[0], &a[1]);
+    decode_pair<FMT>(w1[j >> 2], j & 3, table, s[1], &b[0], &b[1]);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) tile[part * 16 + j][r] = 0;
-    }
+    for (int q = 0; q < 2; ++q)
+      tile[(8 * (2 * j + q) + part) * PITCH + rp] = to16<XT>(a[q]) | (to16<XT>(b[q]) << 16);
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t k = (uint32_t)(tid >> 3) + 32u * i, c = tid & 7;
-    uint32_t o[4];
-    __builtin_memcpy(o, &tile[k][c * 8], 16);
-    *reinterpret_cast<uint4*>(p.wt + (size_t)(k0 + k) * p.np + n0 + c * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t k = (tid >> 3) + 32u * i, c = tid & 7;
+    const uint4 o = *reinterpret_cast<const uint4*>(tile + (8 * (k & 31) + (k >> 5)) * PITCH + 4 * c);
+    if (k0 + k < p.k) *reinterpret_cast<uint4*>(p.wt + (size_t)(k0 + k) * p.np + n0 + c * 8) = o;
   }
-}
-
-// d's rows padded with zeros: [B, N] -> [B, NP].
-__global__ void __launch_bounds__(256) pad_kernel(const uint16_t* d, uint16_t* to, uint32_t n, uint32_t np) {
-  const uint32_t c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= np) return;
-  const size_t t = blockIdx.y;
-  to[t * np + c] = c < n ? d[t * n + c] : (uint16_t)0;
 }
 
 constexpr int kFewTokens = 64;
@@ -130,8 +135,8 @@ GradSpace grad_space(int64_t n, int64_t k, int64_t b) {
 }
 
 template <int FMT>
-hipError_t prepare(int xt, const uint8_t* packed, const void* scales, int64_t n, int64_t k, uint8_t* ws,
-                   const GradSpace& g, hipStream_t s) {
+hipError_t prepare(int xt, const uint16_t* d, int64_t pad_rows, const uint8_t* packed, const void* scales, int64_t n,
+                   int64_t k, uint8_t* ws, const GradSpace& g, hipStream_t s) {
   TransposeArgs p;
   p.packed = packed;
   p.scales = scales;
@@ -142,7 +147,10 @@ hipError_t prepare(int xt, const uint8_t* packed, const void* scales, int64_t n,
   p.parts = reinterpret_cast<const float*>(ws + g.parts);
   p.exp = reinterpret_cast<int*>(ws + g.exp);
   p.nparts = 0;
-  const dim3 grid(g.np / kTile, (uint32_t)(k / kTile));
+  p.tiles = (uint32_t)((int64_t)(g.np / kTile) * ((k + kColumns - 1) / kColumns));
+  p.d = d;
+  p.padded = reinterpret_cast<uint16_t*>(ws + g.d);
+  const dim3 grid(p.tiles + (uint32_t)pad_rows);
   if (xt == kF16) {
     const int64_t count = n * (k / weights_per_scale<FMT>());
     p.nparts = (uint32_t)std::min<int64_t>(kMaxParts, (count + 1023) / 1024);
@@ -177,21 +185,18 @@ hipError_t launch_gemm_grad(int fmt, const uint16_t* d, const uint8_t* packed, c
   }
   const GradSpace g = grad_space(n, k, b);
   uint8_t* base = reinterpret_cast<uint8_t*>(ws);
+  const bool pad = (int64_t)g.np != n || (uintptr_t)d % 16;
+  const int64_t pr = pad ? b : 0;
   hipError_t e;
   switch (fmt_weight(fmt)) {
-    case kNF4: e = prepare<kNF4>(xt, packed, scales, n, k, base, g, s); break;
-    case kINT4: e = prepare<kINT4>(xt, packed, scales, n, k, base, g, s); break;
-    case kFP4: e = prepare<kFP4>(xt, packed, scales, n, k, base, g, s); break;
-    case kINT4A: e = prepare<kINT4A>(xt, packed, scales, n, k, base, g, s); break;
-    default: e = prepare<kMXFP4>(xt, packed, scales, n, k, base, g, s); break;
+    case kNF4: e = prepare<kNF4>(xt, d, pr, packed, scales, n, k, base, g, s); break;
+    case kINT4: e = prepare<kINT4>(xt, d, pr, packed, scales, n, k, base, g, s); break;
+    case kFP4: e = prepare<kFP4>(xt, d, pr, packed, scales, n, k, base, g, s); break;
+    case kINT4A: e = prepare<kINT4A>(xt, d, pr, packed, scales, n, k, base, g, s); break;
+    default: e = prepare<kMXFP4>(xt, d, pr, packed, scales, n, k, base, g, s); break;
   }
   if (e != hipSuccess) return e;
-  if ((int64_t)g.np != n || (uintptr_t)d % 16) {
-    uint16_t* pad = reinterpret_cast<uint16_t*>(base + g.d);
-    pad_kernel<<<dim3((g.np + 255) / 256, (uint32_t)b), dim3(256), 0, s>>>(d, pad, (uint32_t)n, g.np);
-    if (e = hipGetLastError(); e != hipSuccess) return e;
-    d = pad;
-  }
+  if (pad) d = reinterpret_cast<const uint16_t*>(base + g.d);
   DenseArgs a{};
   a.a = reinterpret_cast<const uint8_t*>(d);
   a.b = base + g.wt;
