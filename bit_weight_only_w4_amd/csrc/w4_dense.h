@@ -98,14 +98,16 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
 
   // Every eighth workgroup runs on one XCD: those take consecutive tiles, in blocks of up to eight tiles along M and as
   // many columns of B as are in work at once, so that both operands are read by few XCDs.
-  const uint32_t mt = (p.m + TM - 1) / TM;
-  const uint32_t tiles = gridDim.x, share = tiles / 8, rem = tiles % 8;
-  const uint32_t xcd = blockIdx.x % 8, at = blockIdx.x / 8;
-  const uint32_t tile = xcd * share + min(xcd, rem) + at;
+  // (A launch may cover the last tiles of a larger size with its own smaller ones.)
   constexpr uint32_t CN = GATED ? TN / 2 : TN;  // channels of a tile
-  const uint32_t nt = (p.n + CN - 1) / CN;
+  const uint32_t mt = (p.m + p.bm - 1) / p.bm, nt = (p.n + p.bn - 1) / p.bn;
+  const uint32_t tiles = gridDim.x, share = tiles / 8, rem = tiles % 8;
+  const uint32_t xcd = blockIdx.x % 8, at = xcd * share + min(xcd, rem) + blockIdx.x / 8;
+  const uint32_t sm = p.bm / TM, parts = sm * (p.bn / CN);
+  const uint32_t tile = p.tile0 + at / parts, part = at % parts;
   const uint32_t band = tile / (8 * nt), in_band = tile % (8 * nt), high = min(8u, mt - 8 * band);
-  const uint32_t m0 = (8 * band + in_band % high) * TM, n0 = in_band / high * CN;
+  const uint32_t m0 = (8 * band + in_band % high) * p.bm + part % sm * TM, n0 = in_band / high * p.bn + part / sm * CN;
+  if (m0 >= p.m || n0 >= p.n) return;  // uniform; a part of a larger tile past the end
 
   const uint32_t nrows = min(CN, p.n - n0);
   const i32x4 ra = dense_rsrc(p.a + (size_t)m0 * p.pitch, min((uint32_t)TM, p.m - m0) * p.pitch);
@@ -384,14 +386,20 @@ __global__ void __launch_bounds__(256) dense_sum_kernel(DenseArgs p) {
   }
 }
 
+// One launch over `count` tiles of bm x bn channels from tile0 on.
 template <int TYPE, bool GATED, int WM, int WN, int MT, int NT, int STAGES>
-hipError_t dense_launch(const DenseArgs& a, hipStream_t s) {
+hipError_t dense_launch(DenseArgs a, uint32_t tile0, uint32_t count, uint32_t bm, uint32_t bn, hipStream_t s) {
   constexpr uint32_t TM = 32 * MT * WM, CN = 32 * NT * WN / (GATED ? 2 : 1);
-  const uint64_t tiles = (uint64_t)((a.m + TM - 1) / TM) * ((a.n + CN - 1) / CN);
-  if (tiles >= ((uint64_t)1 << 31)) return hipErrorInvalidValue;
-  dense_kernel<TYPE, GATED, WM, WN, MT, NT, STAGES><<<dim3((uint32_t)tiles, a.splits), dim3(64 * WM * WN), 0, s>>>(a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1) return e;
+  a.tile0 = tile0;
+  a.bm = bm;
+  a.bn = bn;
+  dense_kernel<TYPE, GATED, WM, WN, MT, NT, STAGES>
+      <<<dim3(count * (bm / TM) * (bn / CN), a.splits), dim3(64 * WM * WN), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int TYPE, bool GATED>
+hipError_t dense_sum(const DenseArgs& a, hipStream_t s) {
   if (a.wide)
     dense_sum_kernel<TYPE, GATED, 4><<<dim3((a.n + 1023) / 1024, a.m), dim3(256), 0, s>>>(a);
   else

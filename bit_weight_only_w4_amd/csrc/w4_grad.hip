@@ -57,7 +57,16 @@ __global__ void __launch_bounds__(256) transpose_kernel(TransposeArgs p) {
   const uint32_t tid = threadIdx.x;
   if (blockIdx.x >= p.tiles) {  // a row of d, zeros after its end
     const size_t t = blockIdx.x - p.tiles;
-    for (uint32_t c = tid; c < p.np; c += 256) p.padded[t * p.np + c] = c < p.n ? p.d[t * p.n + c] : (uint16_t)0;
+    const uint16_t* from = p.d + t * p.n;
+    for (uint32_t c = tid * 8; c < p.np; c += 256 * 8) {
+      uint32_t v[4] = {0, 0, 0, 0};
+      if (c + 8 <= p.n) {
+        __builtin_memcpy(v, from + c, 16);
+      } else {
+        for (uint32_t j = 0; c + j < p.n; ++j) v[j >> 1] |= (uint32_t)from[c + j] << (16 * (j & 1));
+      }
+      *reinterpret_cast<uint4*>(p.padded + t * p.np + c) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
     return;
   }
   __shared__ float table[16];
