@@ -700,22 +700,6 @@ def _rows(name, x, what):
     return index
 
 
-def _weights(name, packed, scales, fmt, k, index):
-    """(format code, rows) of 4-bit weights [N, K/2] with their scales, which must be on GPU `index`."""
-    import torch
-
-    code = FORMATS.get(fmt)
-    if code is None:
-        raise ValueError(f"unknown format {fmt!r}; expected one of {sorted(FORMATS)}")
-    if packed.dim() != 2:
-        raise ValueError(f"{name} must be a 2-D uint8 tensor [N, K/2]")
-    n = packed.shape[0]
-    dtype, group = _MOE_SCALES[fmt.split("_")[0]]
-    _expect(name, packed, (n, k // 2), torch.uint8, index)
-    _expect(f"{name} scales", scales, (n, k // group), getattr(torch, dtype), index)
-    return code, n
-
-
 def _with_workspace(entry, head, workspace, size_of, device, index):
     """Calls a library entry whose last arguments are a workspace, its bytes and the stream.  Without one given, the
     first try goes without: an entry that needs none runs, one that does says so before it launches anything."""
@@ -735,19 +719,33 @@ def _with_workspace(entry, head, workspace, size_of, device, index):
     return entry(*head, workspace.data_ptr(), size, stream)
 
 
-def _block_outputs(t, i, dtype, device, index, h, products, save):
-    """h [t, i] and, where wanted, products [t, 2 i], allocated if not given."""
-    import torch
-
+def _block_outputs(t, i, dtype, like, index, h, products, save):
+    """h [t, i] and, where wanted, products [t, 2 i], allocated like `like` if not given."""
     if h is None:
-        h = torch.empty((t, i), dtype=dtype, device=device)
+        h = like.new_empty((t, i), dtype=dtype)
     else:
         _expect("h", h, (t, i), dtype, index)
     if products is not None:
         _expect("products", products, (t, 2 * i), dtype, index)
     elif save:
-        products = torch.empty((t, 2 * i), dtype=dtype, device=device)
+        products = like.new_empty((t, 2 * i), dtype=dtype)
     return h, products
+
+
+_FORMAT_SPECS = {}
+
+
+def _format_spec(fmt):
+    """(code, activation type, scale type, weights a scale) of a format name, kept in _FORMAT_SPECS."""
+    import torch
+
+    if fmt not in FORMATS:
+        raise ValueError(f"unknown format {fmt!r}; expected one of {sorted(FORMATS)}")
+    weight, xtype = fmt.split("_")
+    stype, group = _MOE_SCALES[weight]
+    spec = (FORMATS[fmt], torch.float16 if xtype == "f16" else torch.bfloat16, getattr(torch, stype), group)
+    _FORMAT_SPECS[fmt] = spec
+    return spec
 
 
 def gated_workspace_bytes(fmt, tokens, hidden, inter) -> int:
@@ -763,25 +761,33 @@ def gated(x, gate_up, gate_up_scales, fmt, act="silu", save=False, h=None, produ
     format's scales [2 I, H/g].  With save=True (or `products` given) it returns (h, products), products [T, 2 I] of x's type
     holding g | u, which gated_grad takes.  `workspace` is a uint8 tensor of gated_workspace_bytes(...),
     allocated by the call if not given and needed."""
-    index = _rows("x", x, "[T, H]")
+    import torch
+
+    a = ACTS.get(act)
+    spec = _FORMAT_SPECS.get(fmt) or _format_spec(fmt)
+    index = x.get_device()
+    if a is None:
+        raise ValueError(f"unknown activation {act!r}; expected one of {sorted(ACTS)}")
+    if x.dim() != 2 or gate_up.dim() != 2 or index < 0:
+        raise ValueError("x must be [T, H] and gate_up [2 I, H/2], on the GPU")
+    code, dtype, stype, group = spec
     t, k = x.shape
-    code, n = _weights("gate_up", gate_up, gate_up_scales, fmt, k, index)
-    if _type16("x", x.dtype) != (1 if fmt.endswith("_f16") else 2):
-        raise ValueError(f"x must be of the activation type of {fmt!r}")
-    if n % 2:
-        raise ValueError("gate_up must hold as many gate rows as up rows")
-    a = _act(act)
+    n = gate_up.shape[0]
+    if not (x.dtype is dtype and gate_up.dtype is torch.uint8 and gate_up_scales.dtype is stype and n % 2 == 0
+            and gate_up.shape[1] * 2 == k and gate_up_scales.shape == (n, k // group)
+            and gate_up.get_device() == index and gate_up_scales.get_device() == index
+            and x.is_contiguous() and gate_up.is_contiguous() and gate_up_scales.is_contiguous()):
+        raise ValueError(f"{fmt!r} takes contiguous x [T, H] {dtype}, gate_up [2 I, H/2] uint8 and its scales "
+                         f"[2 I, H/{group}] {stype}, on one GPU")
     context = _on_device(index, stream)
     if context is not None:
         with context:
             return gated(x, gate_up, gate_up_scales, fmt, act, save, h, products, workspace)
-    import torch
-
     L = lib()
-    h, products = _block_outputs(t, n // 2, x.dtype, x.device, index, h, products, save)
+    h, products = _block_outputs(t, n // 2, dtype, x, index, h, products, save)
     status = _with_workspace(L.w4_gated, (x.data_ptr(), gate_up.data_ptr(), gate_up_scales.data_ptr(), code, a, t, k,
-                                          n // 2, h.data_ptr(), _ptr(products)), workspace,
-                             lambda: L.w4_gated_workspace_bytes(code, t, k, n // 2), x.device, index)
+                                          n // 2, h.data_ptr(), None if products is None else products.data_ptr()),
+                             workspace, lambda: L.w4_gated_workspace_bytes(code, t, k, n // 2), x.device, index)
     if status:
         check(status, "w4_gated")
     return h if products is None else (h, products)
@@ -792,16 +798,22 @@ def gated_grad(dh, products, act="silu", d_products=None, stream=None):
     dg = dh * u * act'(g), du = dh * act(g), from dh [T, I] and products [T, 2 I] = g | u (fp16 or bf16)."""
     import torch
 
-    index = _rows("dh", dh, "[T, I]")
-    kind, a = _type16("dh", dh.dtype), _act(act)
+    kind, a = _type16("dh", dh.dtype), ACTS.get(act)
+    index = dh.get_device()
+    if a is None:
+        raise ValueError(f"unknown activation {act!r}; expected one of {sorted(ACTS)}")
+    if dh.dim() != 2 or index < 0:
+        raise ValueError("dh must be [T, I], on the GPU")
     t, i = dh.shape
-    _expect("products", products, (t, 2 * i), dh.dtype, index)
+    if not (products.dtype is dh.dtype and products.shape == (t, 2 * i) and products.get_device() == index
+            and dh.is_contiguous() and products.is_contiguous()):
+        raise ValueError("dh [T, I] and products [T, 2 I] must be contiguous and of one type, on one GPU")
     context = _on_device(index, stream)
     if context is not None:
         with context:
             return gated_grad(dh, products, act, d_products)
     if d_products is None:
-        d_products = torch.empty((t, 2 * i), dtype=dh.dtype, device=dh.device)
+        d_products = torch.empty_like(products)
     else:
         _expect("d_products", d_products, (t, 2 * i), dh.dtype, index)
     status = lib().w4_gated_grad(dh.data_ptr(), products.data_ptr(), kind, a, t, i, d_products.data_ptr(),
@@ -821,25 +833,26 @@ def gemm_grad(d, packed, scales, fmt, dx=None, workspace=None, stream=None):
     call if not given and needed."""
     import torch
 
-    index = _rows("d", d, "[B, N]")
+    code, dtype, stype, group = _FORMAT_SPECS.get(fmt) or _format_spec(fmt)
+    index = d.get_device()
+    if d.dim() != 2 or packed.dim() != 2 or index < 0:
+        raise ValueError("d must be [B, N] and packed [N, K/2], on the GPU")
     b, n = d.shape
-    if packed.dim() != 2:
-        raise ValueError("packed must be a 2-D uint8 tensor [N, K/2]")
     k = packed.shape[1] * 2
-    code, rows = _weights("packed", packed, scales, fmt, k, index)
-    if rows != n:
-        raise ValueError("d must have a column for each weight row")
-    if _type16("d", d.dtype) != (1 if fmt.endswith("_f16") else 2):
-        raise ValueError(f"d must be of the activation type of {fmt!r}")
+    if not (d.dtype is dtype and packed.dtype is torch.uint8 and scales.dtype is stype and packed.shape[0] == n
+            and scales.shape == (n, k // group) and packed.get_device() == index and scales.get_device() == index
+            and d.is_contiguous() and packed.is_contiguous() and scales.is_contiguous()):
+        raise ValueError(f"{fmt!r} takes contiguous d [B, N] {dtype}, packed [N, K/2] uint8 and its scales "
+                         f"[N, K/{group}] {stype}, on one GPU")
     context = _on_device(index, stream)
     if context is not None:
         with context:
             return gemm_grad(d, packed, scales, fmt, dx, workspace)
     L = lib()
     if dx is None:
-        dx = torch.empty((b, k), dtype=d.dtype, device=d.device)
+        dx = d.new_empty((b, k))
     else:
-        _expect("dx", dx, (b, k), d.dtype, index)
+        _expect("dx", dx, (b, k), dtype, index)
     status = _with_workspace(L.w4_gemm_grad, (d.data_ptr(), packed.data_ptr(), scales.data_ptr(), code, n, k, b,
                                               dx.data_ptr()), workspace,
                              lambda: L.w4_gemm_grad_workspace_bytes(code, n, k, b), d.device, index)
@@ -871,11 +884,11 @@ def quantize_int8(x, codes=None, scales=None, stream=None):
             return quantize_int8(x, codes, scales)
     r, k = x.shape
     if codes is None:
-        codes = torch.empty((r, k), dtype=torch.int8, device=x.device)
+        codes = torch.empty_like(x, dtype=torch.int8)
     else:
         _expect("codes", codes, (r, k), torch.int8, index)
     if scales is None:
-        scales = torch.empty(r, dtype=torch.float32, device=x.device)
+        scales = x.new_empty(r, dtype=torch.float32)
     else:
         _expect("scales", scales, (r,), torch.float32, index)
     status = lib().w4_quantize_int8(x.data_ptr(), kind, r, k, codes.data_ptr(), scales.data_ptr(),
@@ -923,7 +936,7 @@ def gemm_int8(xq, xs, wq, ws, dtype=None, y=None, workspace=None, stream=None):
             return gemm_int8(xq, xs, wq, ws, dtype, y, workspace)
     L = lib()
     if y is None:
-        y = torch.empty((b, n), dtype=dtype, device=xq.device)
+        y = xs.new_empty((b, n), dtype=dtype)
     else:
         _expect("y", y, (b, n), dtype, index)
     status = _with_workspace(L.w4_gemm_int8, (xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), n, k, b,
@@ -951,7 +964,7 @@ def gated_int8(xq, xs, wq, ws, act="silu", dtype=None, save=False, h=None, produ
         with context:
             return gated_int8(xq, xs, wq, ws, act, dtype, save, h, products, workspace)
     L = lib()
-    h, products = _block_outputs(t, n // 2, dtype, xq.device, index, h, products, save)
+    h, products = _block_outputs(t, n // 2, dtype, xq, index, h, products, save)
     status = _with_workspace(L.w4_gated_int8, (xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), a, t, k,
                                                n // 2, h.data_ptr(), _ptr(products), kind), workspace,
                              lambda: L.w4_int8_workspace_bytes(n // 2, k, t, 1), xq.device, index)

@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
   if constexpr (TYPE != kDenseI8) all = p.exp ? *p.exp : 0;
   // One output's 32 rows from row `mw` on, in LDS, to memory.
   auto flush = [&](void* out, uint32_t pitch, uint32_t n, uint32_t nend, uint32_t mw) __attribute__((always_inline)) {
-    __builtin_amdgcn_wave_barrier();
+    asm volatile("" ::: "memory");  // a wave's LDS accesses keep their order; the compiler's must too
     uint16_t* o = reinterpret_cast<uint16_t*>(out);
     if (p.wide) {
       constexpr int PER = CW / 8;  // pieces a row
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
         if (mw + r < p.m && n + col < nend) o[(size_t)(mw + r) * pitch + n + col] = stage[r * CW + col];
       }
     }
-    __builtin_amdgcn_wave_barrier();
+    asm volatile("" ::: "memory");
   };
 #pragma unroll
   for (int i = 0; i < MT; ++i) {

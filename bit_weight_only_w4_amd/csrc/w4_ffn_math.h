@@ -58,6 +58,22 @@ __device__ inline uint32_t to16(float v) {
   return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
+// The two 16-bit terms of an NF4 code in a gated launch: the first cut towards zero (and one step short of a code that it
+// would hold whole), so that both have the code's sign and neither is 0 unless the code is: an infinite activation
+// then gives what it gives with the code itself.  Together they are off by at most 2^-15 of the code (bf16), 2^-21 (fp16).
+template <int XT>
+__device__ inline void signed_terms(float c, uint32_t& v1, uint32_t& v2) {
+  if constexpr (XT == kF16) {
+    v1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(c, 0.0f)) & 0xFFFFu;
+    if (c != 0.0f && (float)__builtin_bit_cast(_Float16, (uint16_t)v1) == c) v1 -= 1;
+    v2 = to16<kF16>(c - (float)__builtin_bit_cast(_Float16, (uint16_t)v1));
+  } else {
+    v1 = __float_as_uint(c) >> 16;
+    if (c != 0.0f && __uint_as_float(v1 << 16) == c) v1 -= 1;
+    v2 = to16<kBF16>(c - __uint_as_float(v1 << 16));
+  }
+}
+
 // A block's scale as fp32 from its stored form (INT4A: the low half of its word).
 template <int FMT>
 __device__ inline float scale_of(const void* scales, size_t i) {

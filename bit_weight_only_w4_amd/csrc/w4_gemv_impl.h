@@ -79,7 +79,7 @@ constexpr bool split_code() {
   return FMT == kNF4 && (XT == kBF16 || GATED);
 }
 
-template <int FMT, int XT>
+template <int FMT, int XT, bool GATED>
 __device__ inline void lane_decode(uint32_t& v1, uint32_t& v2) {
   v2 = 0;
   if (FMT == kFP4) {
@@ -87,9 +87,10 @@ __device__ inline void lane_decode(uint32_t& v1, uint32_t& v2) {
     v1 = XT == kF16 ? f16_bits(c) : (__float_as_uint(c) >> 16);
   } else if (FMT == kNF4) {
     const float c = __uint_as_float(codes_in_lanes<kNF4>());
-    if (XT == kF16) {
+    if constexpr (GATED) {
+      signed_terms<XT>(c, v1, v2);
+    } else if (XT == kF16) {
       v1 = f16_bits(c);
-      v2 = f16_bits(c - (float)__builtin_bit_cast(_Float16, (uint16_t)v1));  // taken by gated launches
     } else {
       v1 = bf16_rne_bits(c);
       v2 = bf16_rne_bits(c - __uint_as_float(v1 << 16));
@@ -111,7 +112,7 @@ template <int FMT, int XT, int NT, int SPE, bool GATED = false>
 __device__ inline void fill_table(uint32_t* tab) {
   constexpr int kShift = SPE == 16 ? 4 : 2;  // log2(SPE)
   uint32_t v1, v2;
-  lane_decode<FMT, XT>(v1, v2);
+  lane_decode<FMT, XT, GATED>(v1, v2);
   constexpr bool kSplit = split_code<FMT, XT, GATED>();
   uint4* t4 = reinterpret_cast<uint4*>(tab);
   const int tid = threadIdx.x;

@@ -103,25 +103,27 @@ __global__ void __launch_bounds__(64 * kGradWaves) grad_few_kernel(GradFewArgs p
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float x = from16<kF16>(v[j] & 0xFFFFu), y = from16<kF16>(v[j] >> 16);
-          const uint32_t xh = bf16_rne_bits(x), yh = bf16_rne_bits(y);
-          a[j] = xh | (yh << 16);
-          // an infinity or NaN stays in the first term alone
-          const float xl = x - __uint_as_float(xh << 16), yl = y - __uint_as_float(yh << 16);
-          b[j] = (xl == xl ? __float_as_uint(xl) >> 16 : 0u) | (yl == yl ? __float_as_uint(yl) & 0xFFFF0000u : 0u);
+          // An infinity or NaN is the second term, which meets the weights' first term alone: with their second ones,
+          // zeros among them, it would make NaN of an infinity.
+          a[j] = to16<kBF16>(fabsf(x) < __builtin_inff() ? x : 0.0f) |
+                 (to16<kBF16>(fabsf(y) < __builtin_inff() ? y : 0.0f) << 16);
+          const float xl = x - __uint_as_float(a[j] << 16), yl = y - __uint_as_float(a[j] & 0xFFFF0000u);  // at most 3 bits
+          b[j] = (__float_as_uint(xl) >> 16) | (__float_as_uint(yl) & 0xFFFF0000u);
         }
         dh[t] = make_uint4(a[0], a[1], a[2], a[3]);
         dl[t] = make_uint4(b[0], b[1], b[2], b[3]);
       }
     }
-    float s[8], o[8];  // scales; asymmetric and symmetric INT4: what the code's offset comes to
+    float s[8], o[8];  // scales and the offsets of integer codes
     auto one = [&](auto r) __attribute__((always_inline)) {
       constexpr int R = decltype(r)::value;
       const uint32_t bits = scale_bits(st.s, r);
+      o[R] = 8.0f;
       if constexpr (kMX) {
         s[R] = e8m0_value((bits >> (2 * (m & 4))) & 255u);
       } else if constexpr (is_g128(FMT)) {
         s[R] = __uint_as_float(bits << 16);
-        o[R] = FMT == kINT4 ? -8.0f : -(float)((bits >> 16) & 15u);
+        if constexpr (FMT == kINT4A) o[R] = (float)((bits >> 16) & 15u);
       } else {
         s[R] = __uint_as_float(bits);
       }
@@ -144,16 +146,8 @@ __global__ void __launch_bounds__(64 * kGradWaves) grad_few_kernel(GradFewArgs p
           const uint32_t hi = (v >> (8 * b + 4)) & 15u, lo = (v >> (8 * b)) & 15u;
           w[0][r] = table[hi * 64 + lane] * s[r];
           w[1][r] = table[lo * 64 + lane] * s[r];
-        } else if constexpr (FMT == kFP4 || kMX) {
-          const auto c = b == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 0)
-                         : b == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 1)
-                         : b == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 2)
-                                  : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 3);
-          w[0][r] = c[1] * s[r];
-          w[1][r] = c[0] * s[r];
         } else {
-          w[0][r] = ((float)((v >> (8 * b + 4)) & 15u) + o[r]) * s[r];
-          w[1][r] = ((float)((v >> (8 * b)) & 15u) + o[r]) * s[r];
+          decode_pair<FMT>(v, b, nullptr, BlockScale{s[r], o[r]}, &w[0][r], &w[1][r]);
         }
       }
 #pragma unroll
@@ -165,23 +159,23 @@ __global__ void __launch_bounds__(64 * kGradWaves) grad_few_kernel(GradFewArgs p
           h[i] = to16<kBF16>(x) | (to16<kBF16>(y) << 16);
           if constexpr (XT == kF16) {
             const float xl = x - __uint_as_float(h[i] << 16), yl = y - __uint_as_float(h[i] & 0xFFFF0000u);
-            l[i] = to16<kBF16>(xl == xl ? xl : 0.0f) | (to16<kBF16>(yl == yl ? yl : 0.0f) << 16);
+            l[i] = to16<kBF16>(xl) | (to16<kBF16>(yl) << 16);
           }
         }
         const uint4 oh = make_uint4(h[0], h[1], h[2], h[3]);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
+          float4_t& c = acc[t][2 * b + q];
           if constexpr (XT == kF16) {
             const uint4 ol = make_uint4(l[0], l[1], l[2], l[3]);
-            acc[t][2 * b + q] = mfma<kBF16>(dl[t], oh, acc[t][2 * b + q]);
-            acc[t][2 * b + q] = mfma<kBF16>(dh[t], ol, acc[t][2 * b + q]);
+            c = mfma<kBF16>(dl[t], oh, c);
+            c = mfma<kBF16>(dh[t], ol, c);
           }
-          acc[t][2 * b + q] = mfma<kBF16>(dh[t], oh, acc[t][2 * b + q]);
+          c = mfma<kBF16>(dh[t], oh, c);
         }
       }
     }
   };
-
   GradStep sa, sb;
   uint4 da[NT], db[NT];
   uint32_t st = first + wave;

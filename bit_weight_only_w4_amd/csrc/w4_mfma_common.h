@@ -5,6 +5,7 @@
 // turns one packed byte into both of its weights with one LDS read.
 #pragma once
 #include "w4_common.h"
+#include "w4_ffn_math.h"
 
 namespace w4 {
 namespace {
@@ -41,18 +42,20 @@ __device__ inline uint32_t codes_in_lanes() {
 // (16 of each 8-byte NF4 x bf16 entry): 128 bytes per entry, lane L reading copy L % 32 (L % 16).
 // Half the GEMV's LDS, which leaves room for larger activation tiles.  Filled by all THREADS
 // threads of a workgroup; the caller synchronizes before the first lookup.
-// SPLIT: 8-byte entries, each code as the sum of two 16-bit terms (NF4).
-template <int FMT, int XT, int THREADS, bool SPLIT = FMT == kNF4 && XT == kBF16>
+// GATED: NF4 in two terms of one sign in either type (signed_terms), 8-byte entries.
+template <int FMT, int XT, int THREADS, bool GATED = false>
 __device__ inline void fill_table(uint32_t* tab) {
+  constexpr bool SPLIT = FMT == kNF4 && (XT == kBF16 || GATED);
   uint32_t v1, v2 = 0;
   if (FMT == kFP4) {
     const float c = __uint_as_float(codes_in_lanes<kFP4>());  // exact in both 16-bit types
     v1 = XT == kF16 ? f16_bits(c) : (__float_as_uint(c) >> 16);
   } else if (FMT == kNF4) {
     const float c = __uint_as_float(codes_in_lanes<kNF4>());
-    if (XT == kF16) {
+    if constexpr (GATED) {
+      signed_terms<XT>(c, v1, v2);
+    } else if (XT == kF16) {
       v1 = f16_bits(c);
-      if (SPLIT) v2 = f16_bits(c - (float)__builtin_bit_cast(_Float16, (uint16_t)v1));
     } else {
       v1 = bf16_rne_bits(c);
       v2 = bf16_rne_bits(c - __uint_as_float(v1 << 16));

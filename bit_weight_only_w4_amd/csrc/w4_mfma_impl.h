@@ -335,7 +335,7 @@ mfma_kernel(typename std::conditional<GATED, MfmaGatedArgs, MfmaArgs>::type a) {
   advance(ld);
   load_quad(ld, P1);
   advance(ld);
-  if constexpr (!kMX) fill_table<FMT, XT, kThreads, kSplit>(tab);
+  if constexpr (!kMX) fill_table<FMT, XT, kThreads, GATED>(tab);
   if constexpr (R == 4) {
     load_quad(ld, P2);
     advance(ld);

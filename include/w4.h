@@ -610,7 +610,9 @@ typedef enum { W4_F32 = 0, W4_F16 = 1, W4_BF16 = 2 } w4_type_t;
  * accumulation, g and u rounded to x's type for `products` alone.  From many tokens on (see w4_gated_workspace_bytes) the
  * weights enter as fp16 numbers of a common exponent a row (at most 2^-11 of themselves off; INT4 and MXFP4 exact) and
  * bf16 tokens as fp16 numbers of a common exponent a token (exact), in both what lies more than 2^29 below the
- * row's largest by at most 2^-39 of that.  The order of every sum is fixed.  Asynchronous on `stream`. */
+ * row's largest by at most 2^-39 of that.  Infinities and NaN stay in their token's (a scale's: in its channel's) results,
+ * where the formula has them; without a workspace an infinite token of asymmetric INT4 gives NaN for some of its infinite
+ * products (its zero points are taken off as z times the token's sum).  The order of every sum is fixed.  Asynchronous on `stream`. */
 int w4_gated(const void* x, const uint8_t* gate_up, const void* gate_up_scales, int fmt, int act, int64_t tokens,
              int64_t hidden, int64_t inter, void* h, void* products, void* workspace, size_t workspace_bytes,
              void* stream);
@@ -643,7 +645,8 @@ int w4_gated_grad(const void* dh, const void* products, int type, int act, int64
  *            entry and exit; must not overlap an input; two calls in flight must not share it
  * A weight is rounded once to d's type (bf16 2^-8, fp16 2^-11 of itself, fp16 with one exponent for all of W: what
  * lies more than 2^29 below the largest scale by at most 2^-39 of that), the sums are fp32 in a fixed order, dx is rounded once.
- * Asynchronous on `stream`. */
+ * Infinities and NaN of d stay in their row, where the formula has them; what an infinite or NaN scale gives stays in its
+ * block's columns (NaN, or the formula's infinity).  Asynchronous on `stream`. */
 int w4_gemm_grad(const void* d, const uint8_t* packed, const void* scales, int fmt, int64_t N, int64_t K, int64_t B,
                  void* dx, void* workspace, size_t workspace_bytes, void* stream);
 

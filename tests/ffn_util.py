@@ -164,3 +164,19 @@ class Guarded:
 
     def whole(self):
         return bool((self.flat[:self.pad] == 77).all() and (self.flat[-self.pad:] == 77).all())
+
+
+def formula_finite(x, w):
+    """Where x . w^T of the formula is finite, where it is +-inf (sign) and where NaN, with infinities and NaN in x and w
+    (a sum of infinities of one sign is that infinity, of both signs, or 0 times one, NaN)."""
+    t = x.unsqueeze(1) * w.unsqueeze(0)
+    return t.sum(2)
+
+
+def assert_like(got, ref):
+    """got is NaN where ref is, the same infinity where ref is one, finite elsewhere."""
+    got = got.cpu().double()
+    assert torch.equal(torch.isnan(got), torch.isnan(ref)), (torch.isnan(got) != torch.isnan(ref)).nonzero()[:5]
+    inf = torch.isinf(ref)
+    assert torch.equal(got[inf], ref[inf])
+    assert torch.isfinite(got[torch.isfinite(ref)]).all()
