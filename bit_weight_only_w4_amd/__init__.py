@@ -12,6 +12,7 @@ int16 tensor ``[N, K/128]`` for INT4.  ``"fp4_*"`` (E2M1, NF4's layout), ``"int4
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -700,23 +701,25 @@ def _rows(name, x, what):
     return index
 
 
-def _with_workspace(entry, head, workspace, size_of, device, index):
-    """Calls a library entry whose last arguments are a workspace, its bytes and the stream.  Without one given, the
-    first try goes without: an entry that needs none runs, one that does says so before it launches anything."""
+@functools.lru_cache(maxsize=4096)
+def _scratch_bytes(index, entry, *sizes):
+    """A workspace size of the library (a function of the sizes and of the current device, `index`)."""
+    return int(getattr(lib(), entry)(*sizes))
+
+
+def _scratch(workspace, size, like, index):
+    """(address, bytes, tensor) of a call's workspace: the one given, else `size` bytes allocated on `like`'s GPU."""
     import torch
 
-    stream = torch._C._cuda_getCurrentRawStream(index)
     if workspace is None:
-        status = entry(*head, None, 0, stream)
-        if status != -6:
-            return status
-        size = size_of()
-        workspace = torch.empty(size, dtype=torch.uint8, device=device)
+        if not size:
+            return None, 0, None
+        workspace = like.new_empty(size, dtype=torch.uint8)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the first tensor's GPU")
     else:
-        if workspace.get_device() != index or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the first tensor's GPU")
         size = workspace.numel() * workspace.element_size()
-    return entry(*head, workspace.data_ptr(), size, stream)
+    return workspace.data_ptr(), size, workspace
 
 
 def _block_outputs(t, i, dtype, like, index, h, products, save):
@@ -785,9 +788,11 @@ def gated(x, gate_up, gate_up_scales, fmt, act="silu", save=False, h=None, produ
             return gated(x, gate_up, gate_up_scales, fmt, act, save, h, products, workspace)
     L = lib()
     h, products = _block_outputs(t, n // 2, dtype, x, index, h, products, save)
-    status = _with_workspace(L.w4_gated, (x.data_ptr(), gate_up.data_ptr(), gate_up_scales.data_ptr(), code, a, t, k,
-                                          n // 2, h.data_ptr(), None if products is None else products.data_ptr()),
-                             workspace, lambda: L.w4_gated_workspace_bytes(code, t, k, n // 2), x.device, index)
+    address, size, workspace = _scratch(workspace, _scratch_bytes(index, "w4_gated_workspace_bytes", code, t, k, n // 2),
+                                        x, index)
+    status = L.w4_gated(x.data_ptr(), gate_up.data_ptr(), gate_up_scales.data_ptr(), code, a, t, k, n // 2, h.data_ptr(),
+                        None if products is None else products.data_ptr(), address, size,
+                        torch._C._cuda_getCurrentRawStream(index))
     if status:
         check(status, "w4_gated")
     return h if products is None else (h, products)
@@ -853,9 +858,10 @@ def gemm_grad(d, packed, scales, fmt, dx=None, workspace=None, stream=None):
         dx = d.new_empty((b, k))
     else:
         _expect("dx", dx, (b, k), dtype, index)
-    status = _with_workspace(L.w4_gemm_grad, (d.data_ptr(), packed.data_ptr(), scales.data_ptr(), code, n, k, b,
-                                              dx.data_ptr()), workspace,
-                             lambda: L.w4_gemm_grad_workspace_bytes(code, n, k, b), d.device, index)
+    address, size, workspace = _scratch(workspace, _scratch_bytes(index, "w4_gemm_grad_workspace_bytes", code, n, k, b),
+                                        d, index)
+    status = L.w4_gemm_grad(d.data_ptr(), packed.data_ptr(), scales.data_ptr(), code, n, k, b, dx.data_ptr(), address,
+                            size, torch._C._cuda_getCurrentRawStream(index))
     if status:
         check(status, "w4_gemm_grad")
     return dx
@@ -939,9 +945,9 @@ def gemm_int8(xq, xs, wq, ws, dtype=None, y=None, workspace=None, stream=None):
         y = xs.new_empty((b, n), dtype=dtype)
     else:
         _expect("y", y, (b, n), dtype, index)
-    status = _with_workspace(L.w4_gemm_int8, (xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), n, k, b,
-                                              y.data_ptr(), kind), workspace,
-                             lambda: L.w4_int8_workspace_bytes(n, k, b, 0), xq.device, index)
+    address, size, workspace = _scratch(workspace, _scratch_bytes(index, "w4_int8_workspace_bytes", n, k, b, 0), xq, index)
+    status = L.w4_gemm_int8(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), n, k, b, y.data_ptr(), kind,
+                            address, size, torch._C._cuda_getCurrentRawStream(index))
     if status:
         check(status, "w4_gemm_int8")
     return y
@@ -965,9 +971,10 @@ def gated_int8(xq, xs, wq, ws, act="silu", dtype=None, save=False, h=None, produ
             return gated_int8(xq, xs, wq, ws, act, dtype, save, h, products, workspace)
     L = lib()
     h, products = _block_outputs(t, n // 2, dtype, xq, index, h, products, save)
-    status = _with_workspace(L.w4_gated_int8, (xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), a, t, k,
-                                               n // 2, h.data_ptr(), _ptr(products), kind), workspace,
-                             lambda: L.w4_int8_workspace_bytes(n // 2, k, t, 1), xq.device, index)
+    address, size, workspace = _scratch(workspace, _scratch_bytes(index, "w4_int8_workspace_bytes", n // 2, k, t, 1), xq,
+                                        index)
+    status = L.w4_gated_int8(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), a, t, k, n // 2, h.data_ptr(),
+                             _ptr(products), kind, address, size, torch._C._cuda_getCurrentRawStream(index))
     if status:
         check(status, "w4_gated_int8")
     return h if products is None else (h, products)
