@@ -31,6 +31,7 @@ MAX_SPLIT_K = 64
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
 _lib = None
+_torch = None  # torch, once a call has loaded it: an import statement in each of them costs as much as their checks
 
 
 class W4Error(RuntimeError):
@@ -567,7 +568,8 @@ def _on_device(index, stream):
         if stream.device.index != index:
             raise ValueError("stream and tensors must be on one device")
         return torch.cuda.stream(stream)
-    return None if torch.cuda.current_device() == index else torch.cuda.device(index)
+    # (torch.cuda.current_device() without its check that CUDA is initialized: a tensor on the GPU is)
+    return None if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
 
 
 def moe_route(logits, top_k, renormalize=True, ids=None, weights=None, stream=None):
@@ -676,6 +678,14 @@ def moe(x, ids, weights, gate_up, gate_up_scales, down, down_scales, fmt, y=None
 ACTS = {"silu": 0, "gelu_tanh": 1}
 
 
+def _load_torch():
+    global _torch
+    import torch
+
+    _torch = torch
+    return torch
+
+
 def _act(act) -> int:
     code = ACTS.get(act)
     if code is None:
@@ -684,8 +694,7 @@ def _act(act) -> int:
 
 
 def _type16(name, dtype) -> int:
-    import torch
-
+    torch = _torch or _load_torch()
     if dtype is torch.float16:
         return 1
     if dtype is torch.bfloat16:
@@ -709,8 +718,7 @@ def _scratch_bytes(index, entry, *sizes):
 
 def _scratch(workspace, size, like, index):
     """(address, bytes, tensor) of a call's workspace: the one given, else `size` bytes allocated on `like`'s GPU."""
-    import torch
-
+    torch = _torch or _load_torch()
     if workspace is None:
         if not size:
             return None, 0, None
@@ -740,8 +748,7 @@ _FORMAT_SPECS = {}
 
 def _format_spec(fmt):
     """(code, activation type, scale type, weights a scale) of a format name, kept in _FORMAT_SPECS."""
-    import torch
-
+    torch = _torch or _load_torch()
     if fmt not in FORMATS:
         raise ValueError(f"unknown format {fmt!r}; expected one of {sorted(FORMATS)}")
     weight, xtype = fmt.split("_")
@@ -764,8 +771,7 @@ def gated(x, gate_up, gate_up_scales, fmt, act="silu", save=False, h=None, produ
     format's scales [2 I, H/g].  With save=True (or `products` given) it returns (h, products), products [T, 2 I] of x's type
     holding g | u, which gated_grad takes.  `workspace` is a uint8 tensor of gated_workspace_bytes(...),
     allocated by the call if not given and needed."""
-    import torch
-
+    torch = _torch or _load_torch()
     a = ACTS.get(act)
     spec = _FORMAT_SPECS.get(fmt) or _format_spec(fmt)
     index = x.get_device()
@@ -801,8 +807,7 @@ def gated(x, gate_up, gate_up_scales, fmt, act="silu", save=False, h=None, produ
 def gated_grad(dh, products, act="silu", d_products=None, stream=None):
     """The gradients of a gated block's products from that of its output: d_products [T, 2 I] = dg | du with
     dg = dh * u * act'(g), du = dh * act(g), from dh [T, I] and products [T, 2 I] = g | u (fp16 or bf16)."""
-    import torch
-
+    torch = _torch or _load_torch()
     kind, a = _type16("dh", dh.dtype), ACTS.get(act)
     index = dh.get_device()
     if a is None:
@@ -836,8 +841,7 @@ def gemm_grad(d, packed, scales, fmt, dx=None, workspace=None, stream=None):
     """The input gradient of a product with frozen 4-bit weights: dx [B, K] = d [B, N] . W_hat, of d's type (the
     format's activation type).  `workspace` is a uint8 tensor of gemm_grad_workspace_bytes(...), allocated by the
     call if not given and needed."""
-    import torch
-
+    torch = _torch or _load_torch()
     code, dtype, stype, group = _FORMAT_SPECS.get(fmt) or _format_spec(fmt)
     index = d.get_device()
     if d.dim() != 2 or packed.dim() != 2 or index < 0:
@@ -871,8 +875,7 @@ INT8_MAX_K = 131008
 
 
 def _type(dtype) -> int:
-    import torch
-
+    torch = _torch or _load_torch()
     return 0 if dtype is torch.float32 else _type16("the type", dtype)
 
 
@@ -880,8 +883,7 @@ def quantize_int8(x, codes=None, scales=None, stream=None):
     """Rows to 8 bits (tokens, or the channels of a weight matrix): x [R, K] fp32, fp16 or bf16 -> (codes int8
     [R, K], scales fp32 [R]), scale max|x| / 127, code the integer nearest to x / scale (ties to even).  A row
     that holds an infinity or NaN gets scale NaN."""
-    import torch
-
+    torch = _torch or _load_torch()
     index = _rows("x", x, "[R, K]")
     kind = _type(x.dtype)
     context = _on_device(index, stream)
@@ -906,8 +908,7 @@ def quantize_int8(x, codes=None, scales=None, stream=None):
 
 def _int8_operands(xq, xs, wq, ws):
     """(GPU index, tokens, K, weight rows) of the operands of an 8-bit product."""
-    import torch
-
+    torch = _torch or _load_torch()
     index = xq.get_device()
     if xq.dim() != 2 or wq.dim() != 2 or index < 0:
         raise ValueError("xq must be [B, K] and wq [N, K], on the GPU")
@@ -930,8 +931,7 @@ def gemm_int8(xq, xs, wq, ws, dtype=None, y=None, workspace=None, stream=None):
     """y [B, N] = (xq . wq^T) * xs * ws: 8-bit codes xq int8 [B, K] and wq int8 [N, K] with a scale for each token
     and each channel (as quantize_int8 gives them), exact int32 sums.  dtype: float32 (default), float16 or bfloat16.
     `workspace` is a uint8 tensor of int8_workspace_bytes(...), allocated by the call if not given and needed."""
-    import torch
-
+    torch = _torch or _load_torch()
     index, b, k, n = _int8_operands(xq, xs, wq, ws)
     if dtype is None:
         dtype = torch.float32 if y is None else y.dtype
@@ -957,8 +957,7 @@ def gated_int8(xq, xs, wq, ws, act="silu", dtype=None, save=False, h=None, produ
                stream=None):
     """gated over 8-bit tokens and weights: wq int8 [2 I, K] (gate rows, then up rows), ws [2 I]; h and products are
     of `dtype` (bfloat16, the default, or float16); `workspace` of int8_workspace_bytes(I, K, T, gated=True)."""
-    import torch
-
+    torch = _torch or _load_torch()
     index, t, k, n = _int8_operands(xq, xs, wq, ws)
     if n % 2:
         raise ValueError("wq must hold as many gate rows as up rows")
