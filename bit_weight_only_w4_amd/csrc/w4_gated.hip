@@ -6,6 +6,8 @@
 // 11 significant bits where bf16 has 8, so a weight is rounded by at most 2^-11 of itself (INT4 and MXFP4: not at
 // all) and a bf16 token not at all; what lies more than 2^29 below its row's largest is rounded by at most 2^-39
 // of that.
+#include <algorithm>
+
 #include "w4_ffn.h"
 #include "w4_ffn_math.h"
 
@@ -137,8 +139,8 @@ GatedSpace gated_space(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
 // that bounds it.  V channels a thread: 8 where rows and pointers allow 16-byte accesses, else 1.
 template <int XT, int ACT, int V>
 __global__ void __launch_bounds__(256) gated_grad_kernel(const uint16_t* dh, const uint16_t* pr, uint16_t* dp,
-                                                         int64_t total, int64_t inter) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;  // channel of dh, row-major
+                                                         int64_t first, int64_t total, int64_t inter) {
+  const int64_t i = first + ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;  // channel of dh, row-major
   if (i >= total) return;
   const int64_t t = i / inter, at = i + t * inter;  // g at 2 inter t + channel, u inter further
   uint16_t d[V], g[V], u[V], og[V], ou[V];
@@ -161,11 +163,14 @@ hipError_t grad_launch(const uint16_t* dh, const uint16_t* pr, uint16_t* dp, int
                        hipStream_t s) {
   const int64_t total = tokens * inter;
   const bool wide = inter % 8 == 0 && ((uintptr_t)dh | (uintptr_t)pr | (uintptr_t)dp) % 16 == 0;
-  if (wide)
-    gated_grad_kernel<XT, ACT, 8><<<dim3((uint32_t)((total / 8 + 255) / 256)), dim3(256), 0, s>>>(dh, pr, dp, total,
-                                                                                                inter);
-  else
-    gated_grad_kernel<XT, ACT, 1><<<dim3((uint32_t)((total + 255) / 256)), dim3(256), 0, s>>>(dh, pr, dp, total, inter);
+  const int64_t v = wide ? 8 : 1, most = ((int64_t)1 << 31) * v;  // a launch has fewer than 2^32 threads
+  for (int64_t first = 0; first < total; first += most) {
+    const dim3 grid((uint32_t)((std::min(total - first, most) / v + 255) / 256)), block(256);
+    if (wide)
+      gated_grad_kernel<XT, ACT, 8><<<grid, block, 0, s>>>(dh, pr, dp, first, total, inter);
+    else
+      gated_grad_kernel<XT, ACT, 1><<<grid, block, 0, s>>>(dh, pr, dp, first, total, inter);
+  }
   return hipGetLastError();
 }
 

@@ -444,3 +444,51 @@ def test_gated_grad_past_32_bits():
     assert int((dp != 0).sum()) == 2
     p = 1 / (1 + math.exp(-1))
     assert abs(float(dp[-1, inter - 1]) - 6 * p * (2 - p)) < 0.05 and abs(float(dp[-1, -1]) - 2 * p) < 0.01
+
+
+def test_more_rows_than_one_launch_holds():
+    """2^26 rows of one value: 2^32 threads."""
+    w4, dev = _w4(), f.device()
+    rows = (1 << 26) + 3
+    x = (torch.arange(rows, dtype=torch.int32, device=dev) % 5 - 2).to(torch.bfloat16).view(rows, 1)
+    codes, scales = w4.quantize_int8(x)
+    assert torch.equal(codes.view(-1), (x.view(-1).sign() * 127).to(torch.int8))
+    assert torch.equal(scales, x.view(-1).abs().float() / 127.0)
+
+
+def test_gated_grad_of_more_than_2_32_single_channels():
+    w4, dev = _w4(), f.device()
+    tokens = (1 << 32) + 5
+    pr = torch.zeros(tokens, 2, dtype=torch.bfloat16, device=dev)
+    dh = torch.zeros(tokens, 1, dtype=torch.bfloat16, device=dev)
+    at = [0, (1 << 31) - 1, 1 << 31, 1 << 32, tokens - 1]
+    for t in at:
+        pr[t, 0], pr[t, 1], dh[t, 0] = 1.0, 3.0, 2.0
+    dp = w4.gated_grad(dh, pr)
+    assert int((dp != 0).sum()) == 2 * len(at)
+    p = 1 / (1 + math.exp(-1))
+    for t in at:
+        assert abs(float(dp[t, 0]) - 6 * p * (2 - p)) < 0.05 and abs(float(dp[t, 1]) - 2 * p) < 0.01
+
+
+@pytest.mark.parametrize("rows,k", [(2048, 1536), (2049, 1535), (2047, 1536), (2050, 1544), (513, 2056), (512, 2056), (3, 2049),
+                                    (600, 10250), (2, 16400), (5, 16384)])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_quantize_int8_launches(dtype, rows, k):
+    """Both sides of each bound of the launch's rule, rows that a workgroup does not hold, and quotients on and next to
+    the borders between two codes."""
+    w4, dev = _w4(), f.device()
+    dt = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[dtype]
+    g = torch.Generator().manual_seed(rows + k)
+    x = torch.randn(rows, k, generator=g)
+    half = torch.randint(-254, 255, (rows, k), generator=g).float() / 2
+    half[:, 0] = 127.0  # scale 1: the others lie on integers and borders
+    x[1::2] = half[1::2]
+    if dtype == "f32":
+        nudge = torch.randint(0, 3, (rows, k), generator=g)
+        x = torch.where(nudge == 1, torch.nextafter(x, torch.zeros(())), x)
+        x[1::2, 0] = 127.0
+    x = x.to(dt)
+    codes, scales = w4.quantize_int8(x.to(dev))
+    q, s = f.int8_rows(x)
+    assert torch.equal(scales.cpu(), s) and torch.equal(codes.cpu(), q)
