@@ -1436,7 +1436,7 @@ int int8_call(const int8_t* xq, const float* xs, const int8_t* wq, const float* 
   if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(xs, 4) || !aligned(ws, 4) || !aligned(out, esz) ||
       (products && !aligned(products, esz)))
     return W4_ERR_ALIGN;
-  const size_t used = dense_bytes(gated, b, n, k);
+  const size_t used = int8_few(b) ? 0 : dense_bytes(gated, b, n, k);
   if (used && (!workspace || workspace_bytes < used)) return W4_ERR_WORKSPACE;
   if (used && !aligned(workspace, 16)) return W4_ERR_ALIGN;
   const size_t rows = (size_t)n * (gated ? 2 : 1), ob = (size_t)b * (size_t)n * esz;
@@ -1456,13 +1456,15 @@ int int8_call(const int8_t* xq, const float* xs, const int8_t* wq, const float* 
   a.partial = reinterpret_cast<uint32_t*>(workspace);
   a.out_type = (uint32_t)type;
   a.act = (uint32_t)act;
-  return launch_dense(kDenseI8, gated, a, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? W4_OK : W4_ERR_HIP;
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  return (int8_few(b) ? launch_int8_rows(gated, a, st) : launch_dense(kDenseI8, gated, a, st)) == hipSuccess ? W4_OK
+                                                                                                          : W4_ERR_HIP;
 }
 
 }  // namespace
 
 size_t w4_int8_workspace_bytes(int64_t N, int64_t K, int64_t B, int gated) {
-  return int8_shape(gated != 0, N, K, B) == W4_OK ? dense_bytes(gated != 0, B, N, K) : 0;
+  return int8_shape(gated != 0, N, K, B) == W4_OK && !int8_few(B) ? dense_bytes(gated != 0, B, N, K) : 0;
 }
 
 int w4_gemm_int8(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws, int64_t N, int64_t K, int64_t B,

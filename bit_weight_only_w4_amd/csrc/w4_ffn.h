@@ -65,6 +65,9 @@ hipError_t launch_grad_few_f16(int weight, const GradFewArgs& a, uint32_t splits
 hipError_t launch_grad_few_bf16(int weight, const GradFewArgs& a, uint32_t splits, hipStream_t s);
 
 // ---- 8 bits
+// Products of a few tokens, without scratch (w4_int8_rows.hip); args as for launch_dense.
+bool int8_few(int64_t b);
+hipError_t launch_int8_rows(bool gated, const DenseArgs& a, hipStream_t s);
 hipError_t launch_quantize_int8(int type, const void* x, int64_t rows, int64_t k, int8_t* codes, float* scales,
                                 hipStream_t s);
 

@@ -234,6 +234,16 @@ def test_gated_int8(tokens, n, k, out):
     _int8_case(tokens, n, k, out, gated=True, act=ACTS[n % 2], seed=tokens)
 
 
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("n,k", [(1, 64), (7, 1024), (30, 1088), (129, 4160), (17, 896), (2, 9024)])
+@pytest.mark.parametrize("tokens", [1, 2, 3, 4, 5])
+def test_int8_few_tokens(tokens, n, k, gated, out):
+    """Around the bounds of the launches: tokens held, rows of a wave, rows of a KiB and more."""
+    if not (gated and out == "f32"):
+        _int8_case(tokens, n, k, out, gated=gated, act=ACTS[n % 2], seed=tokens + n)
+
+
 def test_int8_many_tiles():
     _int8_case(1030, 4400, 128, "bf16", seed=3)
     _int8_case(1030, 8800, 192, "bf16", gated=True, seed=4)
