@@ -16,6 +16,14 @@
 //   * Gated: the B tile holds TN / 2 gate rows, then the up rows of the same channels; a wave's even column tiles
 //     are gate, its odd ones the up of the same channels, so the activation and the product happen in registers.
 //   * Rows past M or N and bytes past K are read at an offset outside the buffer, which gives zeros.
+//   * B in four bits (gated, fp16): a wave's 32 rows of packed weights and their scales come to LDS of its own a step
+//     ahead, and between the matrix instructions it decodes them, scales them, rounds them to fp16 and writes them into
+//     the stage where the copies would have put them.
+//
+// What bounds it is the matrix cores under the card's power limit: its rate depends on the data.  4096 x 8192 x 8192: int8
+// 245 to 260 us (2110 to 2240 Tops/s; the library's product 2090), fp16 1160 TFLOP/s (1250).  One wave of every SIMD waits
+// while the other issues: with the copies in one burst behind the barrier, or with steps of 64 bytes, int8 took 300 us and
+// more.
 #pragma once
 #include <type_traits>
 
@@ -24,7 +32,29 @@
 #include "w4_mfma_common.h"
 
 namespace w4 {
+
+struct DensePlan {
+  int tile;
+  uint32_t splits, per;
+  uint32_t tiles, rest;  // tiles in all, and how many of the last are covered with 64 x 128 tiles by a second launch
+};
+DensePlan plan_dense(bool gated, int64_t m, int64_t n, int64_t pitch, bool packed);
+// Sets what a launch of the plan needs; false where it has too many tiles.
+bool dense_prepare(const DensePlan& p, DenseArgs* a);
+
 namespace {
+
+// The tiles, largest first: waves along M and N, 32-row tiles of a wave along M and N, stages; how many workgroups of it
+// a CU holds (LDS), and what was measured (MI355X, over twelve shapes of 1 to 4096 rows, fp16 and int8): microseconds
+// a step of 128 bytes when alone on a CU and when the CU is full, and a round's start and end.
+struct Tile {
+  int tm, tn, fit;
+  double alone, full, ends;
+};
+constexpr Tile kTiles[] = {{256, 256, 1, 1.85, 1.85, 5}, {128, 256, 1, 0.95, 0.95, 4.5}, {64, 128, 2, 0.34, 0.72, 3},
+                           {32, 128, 2, 0.33, 0.60, 3}};
+constexpr int kTileCount = 4;  // (four bits: without the last, whose waves would hold 64 rows of B)
+constexpr int kRestTile = 2;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
@@ -76,19 +106,95 @@ __device__ inline void dense_copy(i32x4 r, const uint8_t* to, uint32_t off) {
                "v"(off), "s"(r));
 }
 
+// The same for 4 bytes a lane.
+__device__ inline void dense_copy4(i32x4 r, const uint8_t* to, uint32_t off) {
+  const uint32_t lds = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)to;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(
+                   __builtin_amdgcn_readfirstlane((int)lds)),
+               "v"(off), "s"(r));
+}
+
 __device__ inline __amdgpu_buffer_rsrc_t dense_buffer(i32x4 r) {
   return __builtin_amdgcn_make_buffer_rsrc(
       reinterpret_cast<void*>((uint64_t)(uint32_t)r.x | ((uint64_t)(uint32_t)r.y << 32)), (short)0, r.z, r.w);
 }
 
-template <int TYPE, bool GATED, int WM, int WN, int MT, int NT, int STAGES>
+// a * s rounded to fp32 and to fp16, two of them in a dword: a in fp16 (the halves of c) or in fp32.
+__device__ inline uint32_t scaled_halves(uint32_t c, float s) {
+  uint32_t d;
+  asm("v_fma_mixlo_f16 %0, %1, %2, 0 op_sel_hi:[1,0,0]" : "=v"(d) : "v"(c), "v"(s));
+  asm("v_fma_mixhi_f16 %0, %1, %2, 0 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "+v"(d) : "v"(c), "v"(s));
+  return d;
+}
+__device__ inline uint32_t scaled_pair(float a, float b, float s) {
+  uint32_t d;
+  asm("v_fma_mixlo_f16 %0, %1, %2, 0" : "=v"(d) : "v"(a), "v"(s));
+  asm("v_fma_mixhi_f16 %0, %1, %2, 0" : "+v"(d) : "v"(b), "v"(s));
+  return d;
+}
+
+// Four bits: the weights of a packed dword, two of them at a time, in fp16: code (exact) times scale.
+//   * E2M1: the hardware's conversion to fp16, which takes the low nibble first: the nibbles are swapped before.
+//     MXFP4's scales are powers of two, which it applies itself (NaN too).
+//   * INT4: the nibbles as bytes below 0x64, which is 1024 + q in fp16, less 1024 + the offset.
+//   * NF4: fp32 codes from a table in LDS, sixteen banks of it, so lanes never wait for each other.
+template <int FMT>
+struct DenseDecoder {
+  uint32_t a, b;
+  float s;
+  uint32_t bias;
+  float code[8];  // NF4: asked for some matrix instructions before they are used
+  template <int J>
+  __device__ inline void look(const float* table) {
+    const uint8_t* t = reinterpret_cast<const uint8_t*>(table);
+    code[2 * J] = *reinterpret_cast<const float*>(t + ((a >> (8 * J)) & 0xFFu));
+    code[2 * J + 1] = *reinterpret_cast<const float*>(t + ((b >> (8 * J)) & 0xFFu));
+  }
+  __device__ inline void set(uint32_t w, BlockScale k) {
+    s = k.s;
+    if constexpr (FMT == kFP4 || FMT == kMXFP4) {
+      a = ((w >> 4) & 0x0F0F0F0Fu) | ((w & 0x0F0F0F0Fu) << 4);
+    } else if constexpr (FMT == kNF4) {
+      a = (w >> 2) & 0x3C3C3C3Cu;  // byte offsets of the first nibbles' codes, and of the second's
+      b = (w << 2) & 0x3C3C3C3Cu;
+    } else {
+      const uint32_t h = (w >> 4) & 0x0F0F0F0Fu, l = w & 0x0F0F0F0Fu;
+      a = __builtin_amdgcn_perm(h, l, 0x01050004u);  // codes 0 1 2 3 of this dword's eight as bytes, then 4 5 6 7
+      b = __builtin_amdgcn_perm(h, l, 0x03070206u);
+      const _Float16 z = (_Float16)(1024.0f + k.zero);
+      bias = (uint32_t)__builtin_bit_cast(uint16_t, z) * 0x10001u;
+    }
+  }
+  template <int J>
+  __device__ inline uint32_t pair() const {
+    if constexpr (FMT == kMXFP4) {
+      return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(a, s, J));
+    } else if constexpr (FMT == kFP4) {
+      return scaled_halves(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(a, 1.0f, J)), s);
+    } else if constexpr (FMT == kNF4) {
+      return scaled_pair(code[2 * J], code[2 * J + 1], s);
+    } else {
+      typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+      const uint32_t q = __builtin_amdgcn_perm(0x64646464u, J < 2 ? a : b, J & 1 ? 0x04030402u : 0x04010400u);
+      return scaled_halves(
+          __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, q) - __builtin_bit_cast(half2_t, bias)), s);
+    }
+  }
+};
+
+template <int TYPE, bool GATED, int FMT, int WM, int WN, int MT, int NT, int STAGES>
 __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
   constexpr int W = WM * WN, TM = 32 * MT * WM, TN = 32 * NT * WN;
   constexpr int ROWS = TM + TN;             // rows of a stage
-  constexpr int COPIES = ROWS / 8 / W;      // copies of 8 rows a wave makes for a stage
-  static_assert(TM % (8 * W) == 0 && (GATED ? TN / 2 : TN) % (8 * W) == 0, "a round of copies fills one operand");
+  constexpr bool PACKED = FMT >= 0;         // B in four bits
+  constexpr int COPIES = (PACKED ? TM : ROWS) / 8 / W;  // copies of 8 rows a wave makes for a stage
+  static_assert(TM % (8 * W) == 0 && (PACKED || (GATED ? TN / 2 : TN) % (8 * W) == 0), "a round of copies fills one operand");
+  static_assert(!PACKED || TN == 32 * W, "32 rows of B a wave");
   static_assert(!GATED || NT % 2 == 0, "gate and up in one wave");
   __shared__ __align__(16) uint8_t ring[STAGES][ROWS * 128];
+  constexpr int RAW = 64 * 16 + 64 * 4;     // a step's packed bytes and scales of a wave's rows of B
+  __shared__ __align__(16) uint8_t raw[PACKED ? W * RAW : 16];
+  __shared__ float table[16];
   using Acc = typename DenseAcc<TYPE>::type;
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -111,8 +217,17 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
 
   const uint32_t nrows = min(CN, p.n - n0);
   const i32x4 ra = dense_rsrc(p.a + (size_t)m0 * p.pitch, min((uint32_t)TM, p.m - m0) * p.pitch);
-  const i32x4 rb = dense_rsrc(p.b + (size_t)n0 * p.pitch, nrows * p.pitch);
-  const i32x4 ru = dense_rsrc(p.b + (size_t)(GATED ? p.n + n0 : 0) * p.pitch, GATED ? nrows * p.pitch : 0u);
+  i32x4 rb{}, ru{};  // B, gated: its gate and up rows; four bits: a wave's packed rows and their scales
+  if constexpr (PACKED) {
+    const uint32_t r = 32 * wave, up = GATED && r >= CN ? 1u : 0u, at = r - (up ? CN : 0u);
+    const size_t row = (size_t)(up ? p.n : 0u) + n0 + at;
+    const uint32_t rows = at < nrows ? min(32u, nrows - at) : 0u;
+    rb = dense_rsrc(p.b + row * (p.pitch / 4), rows * (p.pitch / 4));
+    ru = dense_rsrc(reinterpret_cast<const uint8_t*>(p.scales) + row * (p.pitch / 16), rows * (p.pitch / 16));
+  } else {
+    rb = dense_rsrc(p.b + (size_t)n0 * p.pitch, nrows * p.pitch);
+    ru = dense_rsrc(p.b + (size_t)(GATED ? p.n + n0 : 0) * p.pitch, GATED ? nrows * p.pitch : 0u);
+  }
 
   // Copy j of this wave fills rows 8 (W j + wave) .. + 7 of a stage: lane l slot l % 8 of row l / 8.  Its offsets:
   uint32_t off[COPIES];
@@ -171,10 +286,56 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
   constexpr int C3 = STAGES == 2 ? (COPIES + 1) / 2 : (COPIES + 3) / 4;  // up to the end of quarter 3, 0, 1, 2
   constexpr int C0 = STAGES == 2 ? COPIES : COPIES < 2 * C3 ? COPIES : 2 * C3;
   constexpr int C1 = COPIES < 3 * C3 ? COPIES : 3 * C3;
+  using std::integral_constant;
+  // Four bits: this wave's 32 rows of the B tile, a lane 32 weights of row lane / 2 in a step.  Their packed bytes and
+  // scales come to LDS of the wave's own (which leaves the counting of loads in flight to this kernel), a step ahead
+  // of their use; a quarter of them is decoded, scaled, rounded to fp16 and written into the stage in each quarter.
+  uint8_t* const own = raw + (PACKED ? wave * RAW : 0);
+  const uint32_t raw_row = (uint32_t)lane >> 1, raw_half = (uint32_t)lane & 1u;
+  const uint32_t woff = raw_row * (p.pitch / 4) + raw_half * 16, soff = raw_row * (p.pitch / 16) + raw_half * 4;
+  const uint32_t wput = (TM + 32u * wave + raw_row) * 128 + ((4u * raw_half) ^ ((raw_row >> 1) & 7u)) * 16;
+  struct Raw {
+    uint4 w;
+    float s;
+  } held{};
+  BlockScale hs{0.0f, 0.0f};
+  auto copy_raw = [&](uint32_t t) __attribute__((always_inline)) {  // past the last step: from outside the buffers
+    dense_copy(rb, own, woff + (t < steps ? t * 32 : 0x40000000u));
+    dense_copy4(ru, own + 1024, soff + (t < steps ? t * 8 : 0x40000000u));
+  };
+  auto take_raw = [&]() __attribute__((always_inline)) {
+    held.w = *reinterpret_cast<const uint4*>(own + lane * 16);
+    held.s = *reinterpret_cast<const float*>(own + 1024 + lane * 4);
+  };
+  auto scale_raw = [&]() __attribute__((always_inline)) {
+    hs = BlockScale{held.s, 8.0f};
+    if constexpr (FMT == kINT4A) {  // the pair's first lane has the scale, its second the zero point
+      const float other = __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(held.s), 0xB1, 0xF,
+                                                                              0xF, true));
+      hs = raw_half ? BlockScale{other, held.s} : BlockScale{held.s, other};
+    }
+  };
+  uint32_t made[4];
+  DenseDecoder<PACKED ? FMT : kFP4> dec;
+  auto look = [&](int quarter_of, auto pair) __attribute__((always_inline)) {
+    constexpr int P = decltype(pair)::value;
+    const uint32_t w[4] = {held.w.x, held.w.y, held.w.z, held.w.w};
+    if (P == 0) dec.set(w[quarter_of], hs);
+    if constexpr (FMT == kNF4) dec.template look<P>(table);
+  };
+  auto decode = [&](uint32_t stage_at, int quarter_of, auto pair) __attribute__((always_inline)) {
+    constexpr int P = decltype(pair)::value;
+    made[P] = dec.template pair<P>();
+    if (P == 3)
+      *reinterpret_cast<uint4*>(&ring[0][0] + ((wput + stage_at) ^ (uint32_t)(quarter_of * 16))) =
+          make_uint4(made[0], made[1], made[2], made[3]);
+  };
   // A quarter: after each matrix instruction one of the next quarter's fragments is requested, and a copy now and then.
-  auto quarter = [&](Frags& next, uint32_t st, int s, const Frags& f, uint32_t to, uint32_t t, auto from, auto end)
+  auto quarter = [&](Frags& next, uint32_t st, auto which, const Frags& f, uint32_t to, uint32_t t, auto from, auto end)
       __attribute__((always_inline)) {
     constexpr int A = decltype(from)::value, Z = decltype(end)::value, ALL = MT * NT;
+    constexpr int s = decltype(which)::value;  // the quarter whose fragments are requested
+    constexpr int D0 = PACKED && s == 0 ? 1 : 0;
     const uint8_t* at = &ring[0][0] + ((base + st) ^ (uint32_t)(s * 32));
 #pragma unroll
     for (int q = 0; q < ALL; ++q) {
@@ -182,32 +343,92 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
 #pragma unroll
       for (int i = 0; i < MT + NT; ++i)
         if (i * ALL / (MT + NT) == q) fetch(next, at, i);
+      if constexpr (PACKED) {
+        if (D0 && q == 1) {  // the packed bytes are in registers before the next ones are asked for
+          asm volatile("" : "+v"(held.w.x), "+v"(held.w.y), "+v"(held.w.z), "+v"(held.w.w), "+v"(held.s));
+          scale_raw();
+          copy_raw(t + 1);
+        }
+        constexpr integral_constant<int, 0> p0;
+        constexpr integral_constant<int, 1> p1;
+        constexpr integral_constant<int, 2> p2;
+        constexpr integral_constant<int, 3> p3;
+        if constexpr (FMT == kNF4) {
+          if (D0 == q) look(s, p0), look(s, p1);
+          if (D0 + (ALL - D0) / 3 == q) decode(to, s, p0), decode(to, s, p1), look(s, p2), look(s, p3);
+          if (D0 + 2 * (ALL - D0) / 3 == q) decode(to, s, p2), decode(to, s, p3);
+        } else {
+          if (D0 == q) look(s, p0), decode(to, s, p0);
+          if (D0 + (ALL - D0) / 4 == q) decode(to, s, p1);
+          if (D0 + 2 * (ALL - D0) / 4 == q) decode(to, s, p2);
+          if (D0 + 3 * (ALL - D0) / 4 == q) decode(to, s, p3);
+        }
+      }
 #pragma unroll
       for (int j = A; j < Z; ++j)
-        if ((j - A) * ALL / (Z - A > 0 ? Z - A : 1) == q) copy(&ring[0][0] + to, t, j);
+        if (D0 + (j - A) * (ALL - D0) / (Z - A > 0 ? Z - A : 1) == q) copy(&ring[0][0] + to, t, j);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
   Frags f0, f1;
+  if constexpr (PACKED) {
+    code_table<FMT>(table);
+    Raw ahead[STAGES];
+    const __amdgpu_buffer_rsrc_t bw = dense_buffer(rb), bs = dense_buffer(ru);
 #pragma unroll
-  for (int i = 0; i < STAGES; ++i)
+    for (int i = 0; i < STAGES; ++i) {
+      const uint32_t t = first + i;
+      ahead[i].w = __builtin_bit_cast(
+          uint4, __builtin_amdgcn_raw_buffer_load_b128(bw, woff + (t < steps ? t * 32 : 0x40000000u), 0, 0));
+      ahead[i].s = __uint_as_float(
+          __builtin_amdgcn_raw_buffer_load_b32(bs, soff + (t < steps ? t * 8 : 0x40000000u), 0, 0));
+    }
+    __syncthreads();  // the table
 #pragma unroll
-    for (int j = 0; j < (i == STAGES - 1 ? C3 : COPIES); ++j) copy(&ring[i][0], first + i, j);
-  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((STAGES - 2) * COPIES + C3) : "memory");
+    for (int i = 0; i < STAGES - 1; ++i)
+#pragma unroll
+      for (int j = 0; j < COPIES; ++j) copy(&ring[i][0], first + i, j);
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) {
+      held = ahead[i];
+      scale_raw();
+#pragma unroll
+      for (int q = 0; q < (i == STAGES - 1 ? 1 : 4); ++q) {
+        look(q, integral_constant<int, 0>{});
+        decode(i * SIZE, q, integral_constant<int, 0>{});
+        look(q, integral_constant<int, 1>{});
+        decode(i * SIZE, q, integral_constant<int, 1>{});
+        look(q, integral_constant<int, 2>{});
+        decode(i * SIZE, q, integral_constant<int, 2>{});
+        look(q, integral_constant<int, 3>{});
+        decode(i * SIZE, q, integral_constant<int, 3>{});
+      }
+    }
+    copy_raw(first + STAGES);
+#pragma unroll
+    for (int j = 0; j < C3; ++j) copy(&ring[STAGES - 1][0], first + STAGES - 1, j);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 + C3) : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i)
+#pragma unroll
+      for (int j = 0; j < (i == STAGES - 1 ? C3 : COPIES); ++j) copy(&ring[i][0], first + i, j);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((STAGES - 2) * COPIES + C3) : "memory");
+  }
 #pragma unroll
   for (int i = 0; i < MT + NT; ++i) fetch(f0, &ring[0][0] + base, i);
   uint32_t now = 0, spare = (STAGES - 1) * SIZE;  // the step's stage, and the last step's
-  using std::integral_constant;
   for (uint32_t t = first; t < steps; ++t) {
     const uint32_t u = t + STAGES - 1;
-    quarter(f1, now, 1, f0, spare, u, integral_constant<int, C3>{}, integral_constant<int, C0>{});
-    quarter(f0, now, 2, f1, spare, u, integral_constant<int, C0>{}, integral_constant<int, C1>{});
-    quarter(f1, now, 3, f0, spare, u, integral_constant<int, C1>{}, integral_constant<int, COPIES>{});
+    quarter(f1, now, integral_constant<int, 1>{}, f0, spare, u, integral_constant<int, C3>{}, integral_constant<int, C0>{});
+    quarter(f0, now, integral_constant<int, 2>{}, f1, spare, u, integral_constant<int, C0>{}, integral_constant<int, C1>{});
+    quarter(f1, now, integral_constant<int, 3>{}, f0, spare, u, integral_constant<int, C1>{}, integral_constant<int, COPIES>{});
     // by hand: the compiler's own barrier waits for every copy in flight
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * COPIES) : "memory");
     spare = now;
     now = now + SIZE == STAGES * SIZE ? 0 : now + SIZE;
-    quarter(f0, now, 0, f1, spare, u + 1, integral_constant<int, 0>{}, integral_constant<int, C3>{});
+    if constexpr (PACKED) take_raw();
+    quarter(f0, now, integral_constant<int, 0>{}, f1, spare, u + 1, integral_constant<int, 0>{}, integral_constant<int, C3>{});
   }
   wait_all_vector_loads();  // no copy outlives the workgroup
 
@@ -387,13 +608,13 @@ __global__ void __launch_bounds__(256) dense_sum_kernel(DenseArgs p) {
 }
 
 // One launch over `count` tiles of bm x bn channels from tile0 on.
-template <int TYPE, bool GATED, int WM, int WN, int MT, int NT, int STAGES>
+template <int TYPE, bool GATED, int FMT, int WM, int WN, int MT, int NT, int STAGES>
 hipError_t dense_launch(DenseArgs a, uint32_t tile0, uint32_t count, uint32_t bm, uint32_t bn, hipStream_t s) {
   constexpr uint32_t TM = 32 * MT * WM, CN = 32 * NT * WN / (GATED ? 2 : 1);
   a.tile0 = tile0;
   a.bm = bm;
   a.bn = bn;
-  dense_kernel<TYPE, GATED, WM, WN, MT, NT, STAGES>
+  dense_kernel<TYPE, GATED, FMT, WM, WN, MT, NT, STAGES>
       <<<dim3(count * (bm / TM) * (bn / CN), a.splits), dim3(64 * WM * WN), 0, s>>>(a);
   return hipGetLastError();
 }
@@ -405,6 +626,25 @@ hipError_t dense_sum(const DenseArgs& a, hipStream_t s) {
   else
     dense_sum_kernel<TYPE, GATED, 1><<<dim3((a.n + 255) / 256, a.m), dim3(256), 0, s>>>(a);
   return hipGetLastError();
+}
+
+template <int TYPE, bool GATED, int FMT>
+hipError_t dense_tiles(int tile, const DenseArgs& a, uint32_t tile0, uint32_t count, int of, hipStream_t s) {
+  const uint32_t bm = kTiles[of].tm, bn = kTiles[of].tn / (GATED ? 2 : 1);
+  if (tile == 0) return dense_launch<TYPE, GATED, FMT, 2, 4, 4, 2, 2>(a, tile0, count, bm, bn, s);
+  if (tile == 1) return dense_launch<TYPE, GATED, FMT, 2, 4, 2, 2, 3>(a, tile0, count, bm, bn, s);
+  if (tile == 2) return dense_launch<TYPE, GATED, FMT, 2, 2, 1, 2, 3>(a, tile0, count, bm, bn, s);
+  if constexpr (FMT < 0) return dense_launch<TYPE, GATED, FMT, 1, 2, 1, 2, 4>(a, tile0, count, bm, bn, s);
+  return hipErrorInvalidValue;
+}
+
+template <int TYPE, bool GATED, int FMT>
+hipError_t dense_run(const DensePlan& p, const DenseArgs& a, hipStream_t s) {
+  hipError_t e = dense_tiles<TYPE, GATED, FMT>(p.tile, a, 0, p.tiles - p.rest, p.tile, s);
+  if (e == hipSuccess && p.rest)
+    e = dense_tiles<TYPE, GATED, FMT>(kRestTile, a, p.tiles - p.rest, p.rest, p.tile, s);
+  if (e == hipSuccess && p.splits > 1) e = dense_sum<TYPE, GATED>(a, s);
+  return e;
 }
 
 }  // namespace

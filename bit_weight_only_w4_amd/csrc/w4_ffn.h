@@ -11,6 +11,7 @@ enum DenseType { kDenseF16 = 0, kDenseBF16 = 1, kDenseI8 = 2 };
 struct DenseArgs {
   const uint8_t* a;  // [M, pitch] rows of operand bytes, 16-byte aligned
   const uint8_t* b;  // [N, pitch]; gated: [2 N, pitch], gate rows, then up rows
+  const float* scales;  // four bits: [rows of B, K / 64, 2] (w4_gated.hip); b then holds packed rows, four times shorter
   uint32_t m, n;     // outputs (gated: N is the width of h)
   uint32_t pitch;    // bytes of a row of either operand (its K elements), a multiple of 64, below 2^23
   const float* row_scale;   // 8 bits: s[m]
@@ -30,7 +31,12 @@ struct DenseArgs {
 
 hipError_t launch_dense(int type, bool gated, const DenseArgs& a, hipStream_t s);
 // Scratch that a product of these sizes needs (its K split over workgroups): [splits, M, N or 2 N] of 4 bytes.
-size_t dense_bytes(bool gated, int64_t m, int64_t n, int64_t pitch);
+size_t dense_bytes(bool gated, int64_t m, int64_t n, int64_t pitch, bool packed = false);
+// The gated product with B in four bits: A fp16.
+hipError_t launch_dense_nf4(const DenseArgs& a, hipStream_t s);
+hipError_t launch_dense_fp4(const DenseArgs& a, hipStream_t s);
+hipError_t launch_dense_mxfp4(const DenseArgs& a, hipStream_t s);
+hipError_t launch_dense_int4(const DenseArgs& a, hipStream_t s);
 
 // ---- gated block over 4-bit weights
 bool gated_few(int fmt, int64_t tokens, int64_t hidden, int64_t inter);

@@ -1,12 +1,13 @@
 // Gated feed-forward block over 4-bit weights: h = act(x Wg^T) * (x Wu^T), and the gradients of its two products.
 //
-// Many tokens: the weights are decoded once to fp16 rows in the workspace and the dense kernel (w4_dense.h)
-// multiplies them.  A weight row is held as w 2^-f with one exponent f a row that puts its largest scale into the
+// Many tokens: the dense kernel (w4_dense.h) multiplies fp16 rows with fp16 weights, which are decoded once into the
+// workspace or, where they meet few tiles of tokens, by the dense kernel as they arrive.  A weight row is held as w 2^-f with one exponent f a row that puts its largest scale into the
 // top of fp16's range, bf16 tokens as x 2^-e with one e a token; both come off exactly in the epilogue.  fp16 has
 // 11 significant bits where bf16 has 8, so a weight is rounded by at most 2^-11 of itself (INT4 and MXFP4: not at
 // all) and a bf16 token not at all; what lies more than 2^29 below its row's largest is rounded by at most 2^-39
 // of that.
 #include <algorithm>
+#include <type_traits>
 
 #include "w4_ffn.h"
 #include "w4_ffn_math.h"
@@ -15,12 +16,17 @@ namespace w4 {
 namespace {
 
 constexpr int kDecodeThreads = 256;
+// Up to here the weights are streamed past the tokens and decoded in registers (run_gated_few).  Microseconds against
+// the dense kernel: 64 tokens NF4 1536 -> 8960 21 / 32, 4096 -> 14336 INT4 53 / 115; 128 tokens NF4 42 / 41, 91 / 132, INT4
+// 31 / 37, 71 / 138, MXFP4 41 / 37, 92 / 140; 192 tokens (a second pass) NF4 78 / 39, INT4 57 / 38, 132 / 143.
 constexpr int kFewTokens = 128;
 
 struct DecodeArgs {
   const uint8_t* packed;  // [N, K/2]
   const void* scales;
-  uint16_t* w;   // [N, K] fp16
+  uint16_t* w;   // [N, K] fp16: decoded rows
+  float2* fold;  // [N, K / 64], in place of w: what the dense kernel takes for 64 packed weights, the scales 2^-f of
+                 // their halves, for integer formats the scale 2^-f and the codes' offset
   int* w_exp;    // [N]
   uint32_t n, k;
   const uint16_t* x;  // [T, K] bf16, null: no tokens to convert
@@ -30,30 +36,45 @@ struct DecodeArgs {
 };
 
 // A wave a row: weight rows first, then token rows.  A lane takes 8 consecutive weights of every 512 (so that a store
-// of the wave is 1 KiB in one piece), the first kHeld rounds with their scales in flight at once; the largest of
+// of the wave is 1 KiB in one piece; 27.5 million weights take 16 us, 4.3 TB/s), the first kHeld rounds with their scales in flight at once; the largest of
 // these scales is the row's unless the row is longer.
 constexpr int kHeld = 4;
 
-template <int FMT>
+// FOLD: its scales alone.
+template <int FMT, bool FOLD>
 __global__ void __launch_bounds__(kDecodeThreads) decode_rows_kernel(DecodeArgs p) {
   const int lane = threadIdx.x & 63;
   const uint32_t row = blockIdx.x * (kDecodeThreads / 64) + (threadIdx.x >> 6);
   constexpr uint32_t G = weights_per_scale<FMT>();
   __shared__ float table[16];
-  code_table<FMT>(table);
-  __syncthreads();
+  if constexpr (!FOLD) {
+    code_table<FMT>(table);
+    __syncthreads();
+  }
   if (row < p.n) {
     const uint32_t groups = p.k / G, chunks = p.k / 8;
     const size_t s0 = (size_t)row * groups;
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(p.packed + (size_t)row * (p.k / 2));
-    uint4* dst = reinterpret_cast<uint4*>(p.w + (size_t)row * p.k);
-    uint32_t v[kHeld];
-    BlockScale s[kHeld];
     float top = 0.0f;
     auto fold = [&](float x) __attribute__((always_inline)) {
       const float a = fabsf(x);
       top = a < __builtin_inff() ? fmaxf(top, a) : top;  // infinities and NaN have no binade
     };
+    if constexpr (FOLD) {
+      for (uint32_t i = lane; i < groups; i += 64) fold(scale_of<FMT>(p.scales, s0 + i));
+      const int f = fold_exponent<FMT>(wave_max(top));
+      if (lane == 0) p.w_exp[row] = f;
+      for (uint32_t i = lane; i < p.k / 64; i += 64) {
+        const BlockScale b = block_scale<FMT>(p.scales, s0 + 64 * i / G);
+        float second = FMT == kINT4 || FMT == kINT4A ? b.zero : ldexpf(b.s, -f);
+        if constexpr (FMT == kMXFP4) second = ldexpf(scale_of<FMT>(p.scales, s0 + 2 * i + 1), -f);
+        p.fold[(size_t)row * (p.k / 64) + i] = make_float2(ldexpf(b.s, -f), second);
+      }
+      return;
+    }
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(p.packed + (size_t)row * (p.k / 2));
+    uint4* dst = reinterpret_cast<uint4*>(p.w + (size_t)row * p.k);
+    uint32_t v[kHeld];
+    BlockScale s[kHeld];
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
       const uint32_t i = j * 64 + lane;
@@ -117,13 +138,26 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_rows_kernel(DecodeArgs 
 
 size_t up16(size_t v) { return (v + 15) & ~(size_t)15; }
 
+// Whether the dense kernel decodes the packed weights itself.  It does so once for every tile of up to 256 tokens, which
+// costs it 10 to 35% of its time (MXFP4, whose scales the conversion applies, 5 to 15); the other way the weights go
+// through memory once more, at four times their size.  Microseconds for 256 tokens, decoded first / by the dense kernel:
+// INT4 2048 -> 8192 50 / 46, 4096 -> 11008 126 / 92, 8192 -> 28672 504 / 299; NF4 48 / 54, 99 / 103, 519 / 339 (4096 ->
+// 14336 138 / 118); FP4 50 / 43, 121 / 87, 536 / 308; MXFP4 46 / 40, 99 / 86, 527 / 283.  512 tokens: INT4 61 / 56, 161 /
+// 164, 739 / 712; NF4 60 / 65, 150 / 190, 735 / 782; MXFP4 57 / 51, 147 / 145, 740 / 602.  MXFP4 at 1000: 83 / 78, 209 /
+// 220, 1065 / 1031; at 4096 (1536 -> 8960) 242 / 265.
+bool gated_packed(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
+  if (fmt_weight(fmt) == kMXFP4) return tokens <= 1024;
+  return tokens <= 256 && (fmt_weight(fmt) != kNF4 || 2 * inter * hidden >= 100'000'000);
+}
+
 struct GatedSpace {
   size_t w, w_exp, xh, x_exp, partial, bytes;
 };
 GatedSpace gated_space(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
   GatedSpace g;
+  const bool packed = gated_packed(fmt, tokens, hidden, inter);
   g.w = 0;
-  g.w_exp = up16((size_t)(2 * inter * hidden) * 2);
+  g.w_exp = up16(packed ? (size_t)(2 * inter) * (size_t)(hidden / 64) * 8 : (size_t)(2 * inter * hidden) * 2);
   g.xh = g.w_exp + up16((size_t)(2 * inter) * 4);
   g.x_exp = g.xh;
   g.partial = g.xh;
@@ -131,12 +165,13 @@ GatedSpace gated_space(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
     g.x_exp = g.xh + up16((size_t)(tokens * hidden) * 2);
     g.partial = g.x_exp + up16((size_t)tokens * 4);
   }
-  g.bytes = g.partial + up16(dense_bytes(true, tokens, inter, 2 * hidden));
+  g.bytes = g.partial + up16(dense_bytes(true, tokens, inter, 2 * hidden, packed));
   return g;
 }
 
 // Gradients of g | u from that of h, element by element: six bytes read and four written a channel, which is all
-// that bounds it.  V channels a thread: 8 where rows and pointers allow 16-byte accesses, else 1.
+// that bounds it (bf16, 4096 x 8960: 65 us, 5.6 TB/s).  V channels a thread: 8 where rows and pointers allow 16-byte
+// accesses, else 1 (4096 x 8961: 95 us).
 template <int XT, int ACT, int V>
 __global__ void __launch_bounds__(256) gated_grad_kernel(const uint16_t* dh, const uint16_t* pr, uint16_t* dp,
                                                          int64_t first, int64_t total, int64_t inter) {
@@ -194,6 +229,7 @@ hipError_t launch_gated(int fmt, int act, const uint16_t* x, const uint8_t* pack
   d.packed = packed;
   d.scales = scales;
   d.w = reinterpret_cast<uint16_t*>(base + g.w);
+  d.fold = reinterpret_cast<float2*>(base + g.w);
   d.w_exp = reinterpret_cast<int*>(base + g.w_exp);
   d.n = (uint32_t)(2 * inter);
   d.k = (uint32_t)hidden;
@@ -202,18 +238,28 @@ hipError_t launch_gated(int fmt, int act, const uint16_t* x, const uint8_t* pack
   d.x_exp = reinterpret_cast<int*>(base + g.x_exp);
   d.t = (uint32_t)tokens;
   const uint32_t rows = d.n + (convert ? d.t : 0), per = kDecodeThreads / 64;
+  const bool fold = gated_packed(fmt, tokens, hidden, inter);
   const dim3 grid((rows + per - 1) / per), block(kDecodeThreads);
+  auto decode = [&](auto format) {
+    constexpr int F = decltype(format)::value;
+    if (fold)
+      decode_rows_kernel<F, true><<<grid, block, 0, s>>>(d);
+    else
+      decode_rows_kernel<F, false><<<grid, block, 0, s>>>(d);
+  };
+  using std::integral_constant;
   switch (fmt_weight(fmt)) {
-    case kNF4: decode_rows_kernel<kNF4><<<grid, block, 0, s>>>(d); break;
-    case kINT4: decode_rows_kernel<kINT4><<<grid, block, 0, s>>>(d); break;
-    case kFP4: decode_rows_kernel<kFP4><<<grid, block, 0, s>>>(d); break;
-    case kINT4A: decode_rows_kernel<kINT4A><<<grid, block, 0, s>>>(d); break;
-    default: decode_rows_kernel<kMXFP4><<<grid, block, 0, s>>>(d); break;
+    case kNF4: decode(integral_constant<int, kNF4>{}); break;
+    case kINT4: decode(integral_constant<int, kINT4>{}); break;
+    case kFP4: decode(integral_constant<int, kFP4>{}); break;
+    case kINT4A: decode(integral_constant<int, kINT4A>{}); break;
+    default: decode(integral_constant<int, kMXFP4>{}); break;
   }
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   DenseArgs a{};
   a.a = reinterpret_cast<const uint8_t*>(convert ? d.xh : x);
-  a.b = reinterpret_cast<const uint8_t*>(d.w);
+  a.b = fold ? packed : reinterpret_cast<const uint8_t*>(d.w);
+  a.scales = fold ? reinterpret_cast<const float*>(d.fold) : nullptr;
   a.m = (uint32_t)tokens;
   a.n = (uint32_t)inter;
   a.pitch = (uint32_t)(2 * hidden);
@@ -224,7 +270,13 @@ hipError_t launch_gated(int fmt, int act, const uint16_t* x, const uint8_t* pack
   a.products = products;
   a.out_type = convert ? 2 : 1;
   a.act = (uint32_t)act;
-  return launch_dense(kDenseF16, true, a, s);
+  if (!fold) return launch_dense(kDenseF16, true, a, s);
+  switch (fmt_weight(fmt)) {
+    case kNF4: return launch_dense_nf4(a, s);
+    case kFP4: return launch_dense_fp4(a, s);
+    case kMXFP4: return launch_dense_mxfp4(a, s);
+    default: return launch_dense_int4(a, s);
+  }
 }
 
 hipError_t launch_gated_grad(int xt, int act, const uint16_t* dh, const uint16_t* products, int64_t tokens,

@@ -1,8 +1,8 @@
 // Input gradient of a product with frozen 4-bit weights: dx[t, k] = sum_n d[t, n] W_hat[n, k].
 //
 // The sum runs over the weight rows, along which a packed byte holds nothing: the weights are decoded once into
-// W_hat^T rows of 16 bits in the workspace (through LDS), which the dense kernel
-// multiplies with d.  A weight is rounded once to d's type (2^-8 of itself in bf16, 2^-11 in fp16; fp16 with one
+// W_hat^T rows of 16 bits in the workspace (through LDS), which the dense kernel multiplies with d.  Of 143 us for 2048
+// tokens of INT4 17920 x 1536 the product takes 109 (1030 TFLOP/s), the sum of its five splits 12, decoding 22.  A weight is rounded once to d's type (2^-8 of itself in bf16, 2^-11 in fp16; fp16 with one
 // exponent for the whole matrix, taken from its largest scale, so that neither large nor small weights leave its
 // range).  Rows of W_hat^T are padded with zeros to whole steps of the dense kernel, and so is d where its rows do
 // not end on one or are not aligned.
@@ -46,7 +46,8 @@ struct TransposeArgs {
 
 // A tile of 64 rows x 256 columns a workgroup, whole cache lines of the packed rows: a thread decodes 32 columns of two
 // rows, writes them to LDS as pairs along n, and stores 16 bytes of rows of W_hat^T.  In LDS column 32 part + j is at
-// row 8 j + part of 40 dwords: the 64 pairs that a wave writes at once then lie in 64 banks.  Neighbouring workgroups
+// row 8 j + part of 40 dwords: the 64 pairs that a wave writes at once then lie in 64 banks (27.5 million weights: 17 us,
+// 4 TB/s).  Neighbouring workgroups
 // take neighbouring rows, whose pieces of W_hat^T are one after another.
 constexpr int kColumns = 256;
 
@@ -114,10 +115,13 @@ __global__ void __launch_bounds__(256) transpose_kernel(TransposeArgs p) {
   }
 }
 
+// Up to here the packed weights are decoded in registers (w4_grad_few.h).  Microseconds at 64 tokens there, at 65 here:
+// NF4 bf16 1536 x 8960 20.7 / 28, INT4 fp16 17920 x 1536 26.3 / 38.8.
 constexpr int kFewTokens = 64;
 
 // Splits of N for a few tokens: as many as give every CU a workgroup of 128 columns, each at least a step of 32 rows
-// for each of its eight waves.
+// for each of its eight waves.  Twice and half as many took 15.2 and 15.2 us for 16 tokens of NF4 1536 x 8960 (12.8 so),
+// 29.2 and 22.9 for 64 (20.7).
 uint32_t few_splits(int64_t n, int64_t k) {
   const int64_t groups = (k + 127) / 128, rounds = ((n + 31) / 32 + 7) / 8;
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(rounds, device_cu_count() / groups));

@@ -492,3 +492,64 @@ def test_quantize_int8_launches(dtype, rows, k):
     codes, scales = w4.quantize_int8(x.to(dev))
     q, s = f.int8_rows(x)
     assert torch.equal(scales.cpu(), s) and torch.equal(codes.cpu(), q)
+
+
+# ---- weights decoded by the product itself
+
+@pytest.mark.parametrize("fmt", f.FMTS)
+@pytest.mark.parametrize("tokens,steps,inter", [(129, 1, 1), (256, 9, 333), (144, 4, 1030), (256, 40, 129)])
+def test_gated_decoded_in_the_product(fmt, tokens, steps, inter):
+    """Up to 256 tokens: one step and many, ragged channels, one row of tiles, K split over workgroups."""
+    _gated_case(fmt, tokens, steps * f.group(fmt), inter, ACTS[inter % 2], seed=steps)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4_f16", "mxfp4_bf16"])
+@pytest.mark.parametrize("tokens,hidden,inter", [(1024, 320, 700), (1025, 320, 700), (700, 128, 9100), (511, 64, 4500)])
+def test_gated_mxfp4_tiles(fmt, tokens, hidden, inter):
+    _gated_case(fmt, tokens, hidden, inter, "silu", seed=hidden)
+
+
+@pytest.mark.parametrize("fmt", ["nf4_f16", "nf4_bf16"])
+@pytest.mark.parametrize("tokens", [129, 256, 257])
+def test_gated_many_weights(fmt, tokens):
+    """100 million NF4 weights, a sample of whose channels is compared."""
+    w4, dev, dtype = _w4(), f.device(), f.DTYPES[fmt.split("_")[1]]
+    hidden, inter = 1024, 48900
+    g = torch.Generator(device=dev).manual_seed(tokens)
+    p = torch.randint(0, 256, (2 * inter, hidden // 2), dtype=torch.uint8, device=dev, generator=g)
+    s = torch.rand((2 * inter, hidden // 64), device=dev, generator=g) * 0.1
+    x = f.normal((tokens, hidden), dtype, 3)
+    h, pr = w4.gated(x.to(dev), p, s, fmt, "silu", save=True)
+    at = torch.cat((torch.arange(0, inter, 1511), torch.tensor([inter - 1])))
+    rows = torch.cat((at, at + inter))
+    _, _, hat = f.as_operands(fmt, p[rows.to(dev)].cpu().numpy(), s[rows.to(dev)].cpu().numpy())
+    ref, eh, both, ep = f.gated_bound(x, hat, "silu", dtype)
+    f.check(pr[:, rows.to(dev)], both, ep)
+    f.check(h[:, at.to(dev)], ref, eh)
+
+
+@pytest.mark.parametrize("fmt", f.FMTS)
+@pytest.mark.parametrize("tokens", [1, 20, 200, 300])
+def test_gated_nonfinite_scales(fmt, tokens):
+    """An infinite or NaN scale of a gate or up row gives no finite product of its row and leaves the others alone."""
+    w4, dev, dtype = _w4(), f.device(), f.DTYPES[fmt.split("_")[1]]
+    hidden, inter = 256, 70
+    p, s, hat = f.weights(fmt, 2 * inter, hidden, 31)
+    bad = [3, 64, inter + 5, 2 * inter - 1]
+    weight = fmt.split("_")[0]
+    s = s.clone()
+    raw = s.view({"mxfp4": torch.uint8, "int4": torch.int16}.get(weight, torch.int32))
+    for i, row in enumerate(bad):
+        nan = i % 2 or weight == "mxfp4"
+        raw[row, 1] = {"mxfp4": 255, "int4": 0x7FC0 if nan else 0x7F80,
+                       "int4a": (0x7FC0 if nan else 0x7F80) | 3 << 16}.get(weight, 0x7FC00000 if nan else 0x7F800000)
+    x = f.normal((tokens, hidden), dtype, 32)
+    x = torch.where(x == 0, torch.ones_like(x), x)
+    h, pr = w4.gated(x.to(dev), p.to(dev), s.to(dev), fmt, "silu", save=True)
+    ref, eh, both, ep = f.gated_bound(x, hat, "silu", dtype)
+    good = torch.ones(2 * inter, dtype=torch.bool)
+    good[bad] = False
+    f.check(pr.cpu()[:, good], both[:, good], ep[:, good])
+    assert not torch.isfinite(pr.cpu()[:, ~good]).any()
+    good = good[:inter] & good[inter:]
+    f.check(h.cpu()[:, good], ref[:, good], eh[:, good])
