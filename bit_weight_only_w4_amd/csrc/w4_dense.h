@@ -38,7 +38,7 @@ struct DensePlan {
   uint32_t splits, per;
   uint32_t tiles, rest;  // tiles in all, and how many of the last are covered with 64 x 128 tiles by a second launch
 };
-DensePlan plan_dense(bool gated, int64_t m, int64_t n, int64_t pitch, bool packed);
+DensePlan plan_dense(bool gated, int64_t m, int64_t n, int64_t pitch, int packed);
 // Sets what a launch of the plan needs; false where it has too many tiles.
 bool dense_prepare(const DensePlan& p, DenseArgs* a);
 

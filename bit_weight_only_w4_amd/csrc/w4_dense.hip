@@ -11,20 +11,30 @@ namespace w4 {
 // weights at 6.5 TB/s; 128 x 256 for 1000 x 17920 x 1536 fp16: 78 us, 256 x 256 there 87; five splits of 256 x 256
 // for 2048 x 1536 x 17920 fp16: 129 us, unsplit 128 x 256 tiles 262).  Where a last round of large tiles would leave
 // most CUs idle, its tiles are covered by smaller ones in a second launch.
-DensePlan plan_dense(bool gated, int64_t m, int64_t n, int64_t pitch, bool packed) {
+//
+// Four bits: decoding makes a step of the largest tile take 1.0 (MXFP4), 1.19 (FP4, INT4) or 1.3 (NF4) times as long, of
+// the others, whose rows of B meet fewer of A, 1.18 times that (160 and 256 tokens of 1536 -> 8960 to 8192 -> 28672).
+DensePlan plan_dense(bool gated, int64_t m, int64_t n, int64_t pitch, int packed) {
+  const double slow = packed < 0 || packed == kMXFP4 ? 1.0 : packed == kNF4 ? 1.3 : 1.19;
   const int64_t cus = device_cu_count(), steps = (pitch + 127) / 128;
   const int64_t width = gated ? 2 * n : n;
   DensePlan best{0, 1, (uint32_t)steps, 0, 0};
   double least = 0;
-  for (int i = 0; i < (packed ? kTileCount - 1 : kTileCount); ++i) {
-    const Tile& t = kTiles[i];
+  for (int i = 0; i < (packed < 0 ? kTileCount : kTileCount - 1); ++i) {
+    auto tile_of = [&](int j) {
+      Tile t = kTiles[j];
+      const double f = packed < 0 ? 1.0 : j ? 1.18 * slow : slow;
+      t.alone *= f, t.full *= f;
+      return t;
+    };
+    const Tile t = tile_of(i);
     const int64_t tiles = ((m + t.tm - 1) / t.tm) * ((width + t.tn - 1) / t.tn);
     for (int64_t s = 1; s <= 20 && s * 4 <= std::max<int64_t>(steps, 4); ++s) {
       const int64_t per = (steps + s - 1) / s;
       if ((s - 1) * per >= steps) continue;  // an empty split
       const int64_t rounds = (tiles * s + cus * t.fit - 1) / (cus * t.fit);
       const double work = rounds * (per * (tiles * s <= cus ? t.alone : t.full) + t.ends);
-      const double bytes = ((double)m + (packed ? 0.3125 : 1.0) * width) * pitch / 5.5e6;
+      const double bytes = ((double)m + (packed < 0 ? 1.0 : 0.3125) * width) * pitch / 5.5e6;
       auto offer = [&](double w, int64_t rest) {
         double us = std::max(w, bytes) + 0.1 * std::min(w, bytes);
         if (s > 1) us += 3 + (double)s * m * width * 8 / 5e6;
@@ -36,7 +46,7 @@ DensePlan plan_dense(bool gated, int64_t m, int64_t n, int64_t pitch, bool packe
       offer(work, 0);
       const int64_t rest = tiles % cus;
       if (t.fit == 1 && s == 1 && tiles > cus && rest) {
-        const Tile& r = kTiles[kRestTile];
+        const Tile r = tile_of(kRestTile);
         const int64_t small = rest * (t.tm / r.tm) * (t.tn / r.tn);
         offer(tiles / cus * (per * t.alone + t.ends) + 2 + (small + cus * r.fit - 1) / (cus * r.fit) *
                   (per * (small <= cus ? r.alone : r.full) + r.ends),
@@ -56,14 +66,14 @@ bool dense_prepare(const DensePlan& p, DenseArgs* a) {
   return true;
 }
 
-size_t dense_bytes(bool gated, int64_t m, int64_t n, int64_t pitch, bool packed) {
+size_t dense_bytes(bool gated, int64_t m, int64_t n, int64_t pitch, int packed) {
   const DensePlan p = plan_dense(gated, m, n, pitch, packed);
   return p.splits > 1 ? (size_t)p.splits * (size_t)m * (size_t)(gated ? 2 * n : n) * 4 : 0;
 }
 
 hipError_t launch_dense(int type, bool gated, const DenseArgs& args, hipStream_t s) {
   DenseArgs a = args;
-  const DensePlan p = plan_dense(gated, a.m, a.n, a.pitch, false);
+  const DensePlan p = plan_dense(gated, a.m, a.n, a.pitch, -1);
   if (!dense_prepare(p, &a)) return hipErrorInvalidValue;
   if (type == kDenseF16)
     return gated ? dense_run<kDenseF16, true, -1>(p, a, s) : dense_run<kDenseF16, false, -1>(p, a, s);

@@ -31,7 +31,8 @@ struct DenseArgs {
 
 hipError_t launch_dense(int type, bool gated, const DenseArgs& a, hipStream_t s);
 // Scratch that a product of these sizes needs (its K split over workgroups): [splits, M, N or 2 N] of 4 bytes.
-size_t dense_bytes(bool gated, int64_t m, int64_t n, int64_t pitch, bool packed = false);
+// `packed`: the weight format of B in four bits, else -1.
+size_t dense_bytes(bool gated, int64_t m, int64_t n, int64_t pitch, int packed = -1);
 // The gated product with B in four bits: A fp16.
 hipError_t launch_dense_nf4(const DenseArgs& a, hipStream_t s);
 hipError_t launch_dense_fp4(const DenseArgs& a, hipStream_t s);

@@ -35,22 +35,93 @@ struct DecodeArgs {
   uint32_t t;
 };
 
-// A wave a row: weight rows first, then token rows.  A lane takes 8 consecutive weights of every 512 (so that a store
-// of the wave is 1 KiB in one piece; 27.5 million weights take 16 us, 4.3 TB/s), the first kHeld rounds with their scales in flight at once; the largest of
-// these scales is the row's unless the row is longer.
+// Token rows to fp16, a wave each: a lane takes 8 consecutive values of every 512 and keeps those of the first kHeld
+// rounds between the pass for the largest and the one that writes.
 constexpr int kHeld = 4;
 
-// FOLD: its scales alone.
-template <int FMT, bool FOLD>
+__device__ inline void token_row(const DecodeArgs& p, uint32_t t, int lane) {
+  const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)t * p.k);
+  uint4* dst = reinterpret_cast<uint4*>(p.xh + (size_t)t * p.k);
+  const uint32_t chunks = p.k / 8;
+  uint32_t top = 0;  // the largest finite magnitude, as bits
+  auto fold = [&](const uint4& v) __attribute__((always_inline)) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t a = w[j] & 0x7FFFu, b = (w[j] >> 16) & 0x7FFFu;
+      top = a < 0x7F80u ? max(top, a) : top;
+      top = b < 0x7F80u ? max(top, b) : top;
+    }
+  };
+  uint4 held[kHeld];
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) held[j] = j * 64 + lane < chunks ? src[j * 64 + lane] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) fold(held[j]);
+  for (uint32_t i = kHeld * 64 + lane; i < chunks; i += 64) fold(src[i]);
+  const float m = wave_max(__uint_as_float(top << 16));
+  const int e = m > 0.0f ? ilogbf(m) - 14 : 0;
+  if (lane == 0) p.x_exp[t] = e;
+  auto put = [&](uint32_t i, const uint4& v) __attribute__((always_inline)) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      o[j] = to16<kF16>(ldexpf(__uint_as_float(w[j] << 16), -e)) |
+             (to16<kF16>(ldexpf(__uint_as_float(w[j] & 0xFFFF0000u), -e)) << 16);
+    dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+  };
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j)
+    if (j * 64 + lane < chunks) put(j * 64 + lane, held[j]);
+  for (uint32_t i = kHeld * 64 + lane; i < chunks; i += 64) put(i, src[i]);
+}
+
+// The scales of weight rows for the kernel that decodes them itself, sixteen lanes a row; token rows in the first
+// workgroups, whose two passes take longest (27.5 million MXFP4 weights and 1000 tokens 7 us).
+constexpr int kFoldRows = kDecodeThreads / 16;
+
+template <int FMT>
+__global__ void __launch_bounds__(kDecodeThreads) fold_rows_kernel(DecodeArgs p) {
+  const uint32_t before = p.x ? (p.t + kDecodeThreads / 64 - 1) / (kDecodeThreads / 64) : 0u;
+  if (blockIdx.x < before) {
+    const uint32_t t = blockIdx.x * (kDecodeThreads / 64) + (threadIdx.x >> 6);
+    if (t < p.t) token_row(p, t, threadIdx.x & 63);
+    return;
+  }
+  const uint32_t lane = threadIdx.x & 15, row = (blockIdx.x - before) * kFoldRows + (threadIdx.x >> 4);
+  if (row >= p.n) return;  // sixteen lanes at once
+  constexpr uint32_t G = weights_per_scale<FMT>();
+  const uint32_t groups = p.k / G, blocks = p.k / 64;
+  const size_t s0 = (size_t)row * groups;
+  float top = 0.0f;
+  for (uint32_t i = lane; i < groups; i += 16) {
+    const float a = fabsf(scale_of<FMT>(p.scales, s0 + i));
+    top = a < __builtin_inff() ? fmaxf(top, a) : top;  // infinities and NaN have no binade
+  }
+#pragma unroll
+  for (int d = 8; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+  const int f = fold_exponent<FMT>(top);
+  if (lane == 0) p.w_exp[row] = f;
+  for (uint32_t i = lane; i < blocks; i += 16) {
+    const BlockScale b = block_scale<FMT>(p.scales, s0 + 64 * i / G);
+    float second = FMT == kINT4 || FMT == kINT4A ? b.zero : ldexpf(b.s, -f);
+    if constexpr (FMT == kMXFP4) second = ldexpf(scale_of<FMT>(p.scales, s0 + 2 * i + 1), -f);
+    p.fold[(size_t)row * blocks + i] = make_float2(ldexpf(b.s, -f), second);
+  }
+}
+
+// Weight rows decoded, a wave each, then token rows.  A lane takes 8 consecutive weights of every 512 (so that a store
+// of the wave is 1 KiB in one piece; 27.5 million weights take 16 us, 4.3 TB/s), the first kHeld rounds with their scales
+// in flight at once; the largest of these scales is the row's unless the row is longer.
+template <int FMT>
 __global__ void __launch_bounds__(kDecodeThreads) decode_rows_kernel(DecodeArgs p) {
   const int lane = threadIdx.x & 63;
   const uint32_t row = blockIdx.x * (kDecodeThreads / 64) + (threadIdx.x >> 6);
   constexpr uint32_t G = weights_per_scale<FMT>();
   __shared__ float table[16];
-  if constexpr (!FOLD) {
-    code_table<FMT>(table);
-    __syncthreads();
-  }
+  code_table<FMT>(table);
+  __syncthreads();
   if (row < p.n) {
     const uint32_t groups = p.k / G, chunks = p.k / 8;
     const size_t s0 = (size_t)row * groups;
@@ -59,18 +130,6 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_rows_kernel(DecodeArgs 
       const float a = fabsf(x);
       top = a < __builtin_inff() ? fmaxf(top, a) : top;  // infinities and NaN have no binade
     };
-    if constexpr (FOLD) {
-      for (uint32_t i = lane; i < groups; i += 64) fold(scale_of<FMT>(p.scales, s0 + i));
-      const int f = fold_exponent<FMT>(wave_max(top));
-      if (lane == 0) p.w_exp[row] = f;
-      for (uint32_t i = lane; i < p.k / 64; i += 64) {
-        const BlockScale b = block_scale<FMT>(p.scales, s0 + 64 * i / G);
-        float second = FMT == kINT4 || FMT == kINT4A ? b.zero : ldexpf(b.s, -f);
-        if constexpr (FMT == kMXFP4) second = ldexpf(scale_of<FMT>(p.scales, s0 + 2 * i + 1), -f);
-        p.fold[(size_t)row * (p.k / 64) + i] = make_float2(ldexpf(b.s, -f), second);
-      }
-      return;
-    }
     const uint32_t* src = reinterpret_cast<const uint32_t*>(p.packed + (size_t)row * (p.k / 2));
     uint4* dst = reinterpret_cast<uint4*>(p.w + (size_t)row * p.k);
     uint32_t v[kHeld];
@@ -107,47 +166,25 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_rows_kernel(DecodeArgs 
     return;
   }
   const uint32_t t = row - p.n;
-  if (!p.x || t >= p.t) return;
-  const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)t * p.k);
-  uint4* dst = reinterpret_cast<uint4*>(p.xh + (size_t)t * p.k);
-  uint32_t top = 0;  // the largest finite magnitude, as bits
-  for (uint32_t i = lane; i < p.k / 8; i += 64) {
-    const uint4 v = src[i];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t a = w[j] & 0x7FFFu, b = (w[j] >> 16) & 0x7FFFu;
-      top = a < 0x7F80u ? max(top, a) : top;
-      top = b < 0x7F80u ? max(top, b) : top;
-    }
-  }
-  const float m = wave_max(__uint_as_float(top << 16));
-  const int e = m > 0.0f ? ilogbf(m) - 14 : 0;
-  if (lane == 0) p.x_exp[t] = e;
-  for (uint32_t i = lane; i < p.k / 8; i += 64) {
-    const uint4 v = src[i];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      o[j] = to16<kF16>(ldexpf(__uint_as_float(w[j] << 16), -e)) |
-             (to16<kF16>(ldexpf(__uint_as_float(w[j] & 0xFFFF0000u), -e)) << 16);
-    dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
-  }
+  if (p.x && t < p.t) token_row(p, t, lane);
 }
 
 size_t up16(size_t v) { return (v + 15) & ~(size_t)15; }
 
 // Whether the dense kernel decodes the packed weights itself.  It does so once for every tile of up to 256 tokens, which
-// costs it 10 to 35% of its time (MXFP4, whose scales the conversion applies, 5 to 15); the other way the weights go
-// through memory once more, at four times their size.  Microseconds for 256 tokens, decoded first / by the dense kernel:
-// INT4 2048 -> 8192 50 / 46, 4096 -> 11008 126 / 92, 8192 -> 28672 504 / 299; NF4 48 / 54, 99 / 103, 519 / 339 (4096 ->
-// 14336 138 / 118); FP4 50 / 43, 121 / 87, 536 / 308; MXFP4 46 / 40, 99 / 86, 527 / 283.  512 tokens: INT4 61 / 56, 161 /
-// 164, 739 / 712; NF4 60 / 65, 150 / 190, 735 / 782; MXFP4 57 / 51, 147 / 145, 740 / 602.  MXFP4 at 1000: 83 / 78, 209 /
-// 220, 1065 / 1031; at 4096 (1536 -> 8960) 242 / 265.
-bool gated_packed(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
-  if (fmt_weight(fmt) == kMXFP4) return tokens <= 1024;
-  return tokens <= 256 && (fmt_weight(fmt) != kNF4 || 2 * inter * hidden >= 100'000'000);
+// makes its steps up to half as long again (NF4; MXFP4, whose scales the conversion applies, little longer); the other way
+// the weights go through memory once more, at four times their size.  Microseconds, by the dense kernel / decoded first:
+//             2048 -> 8192   4096 -> 11008   8192 -> 28672
+//   NF4  256   46.5 / 48.3     99 / 100        324 / 511     512  61 / 58    135 / 151     577 / 740
+//   NF4  300   54 / 52        156 / 127        573 / 582    1000  91 / 89    283 / 222    1200 / 1106
+//   INT4 256   43 / 50         87 / 123        298 / 524     512  56 / 61    125 / 159     543 / 734   1000  83 / 89
+//                                                                                       255 / 228   1093 / 1097
+//   FP4  256   41 / 48         88 / 117        302 / 519     512  57 / 58    127 / 150     543 / 736   1000  85 / 86
+//                                                                                       248 / 221   1088 / 1110
+//   MXFP4 256  39 / 46         80 / 100        276 / 518    1000  76 / 82 (4096 -> 14336 231 / 275)     957 / 1062
+//   MXFP4 2048 (1536 -> 8960 135 / 134)  364 / 366  1668 / 1770;  4096 (264 / 240)  695 / 669  3288 / 3218
+bool gated_packed(int fmt, int64_t tokens) {
+  return tokens <= (fmt_weight(fmt) == kMXFP4 ? 2048 : fmt_weight(fmt) == kNF4 ? 256 : 512);
 }
 
 struct GatedSpace {
@@ -155,7 +192,7 @@ struct GatedSpace {
 };
 GatedSpace gated_space(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
   GatedSpace g;
-  const bool packed = gated_packed(fmt, tokens, hidden, inter);
+  const bool packed = gated_packed(fmt, tokens);
   g.w = 0;
   g.w_exp = up16(packed ? (size_t)(2 * inter) * (size_t)(hidden / 64) * 8 : (size_t)(2 * inter * hidden) * 2);
   g.xh = g.w_exp + up16((size_t)(2 * inter) * 4);
@@ -165,7 +202,7 @@ GatedSpace gated_space(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
     g.x_exp = g.xh + up16((size_t)(tokens * hidden) * 2);
     g.partial = g.x_exp + up16((size_t)tokens * 4);
   }
-  g.bytes = g.partial + up16(dense_bytes(true, tokens, inter, 2 * hidden, packed));
+  g.bytes = g.partial + up16(dense_bytes(true, tokens, inter, 2 * hidden, packed ? fmt_weight(fmt) : -1));
   return g;
 }
 
@@ -237,15 +274,15 @@ hipError_t launch_gated(int fmt, int act, const uint16_t* x, const uint8_t* pack
   d.xh = reinterpret_cast<uint16_t*>(base + g.xh);
   d.x_exp = reinterpret_cast<int*>(base + g.x_exp);
   d.t = (uint32_t)tokens;
-  const uint32_t rows = d.n + (convert ? d.t : 0), per = kDecodeThreads / 64;
-  const bool fold = gated_packed(fmt, tokens, hidden, inter);
-  const dim3 grid((rows + per - 1) / per), block(kDecodeThreads);
+  const bool fold = gated_packed(fmt, tokens);
+  const uint32_t per = kDecodeThreads / 64, token_rows = convert ? d.t : 0;
+  const dim3 grid(fold ? (token_rows + per - 1) / per + (d.n + kFoldRows - 1) / kFoldRows : (d.n + token_rows + per - 1) / per);
   auto decode = [&](auto format) {
     constexpr int F = decltype(format)::value;
     if (fold)
-      decode_rows_kernel<F, true><<<grid, block, 0, s>>>(d);
+      fold_rows_kernel<F><<<grid, dim3(kDecodeThreads), 0, s>>>(d);
     else
-      decode_rows_kernel<F, false><<<grid, block, 0, s>>>(d);
+      decode_rows_kernel<F><<<grid, dim3(kDecodeThreads), 0, s>>>(d);
   };
   using std::integral_constant;
   switch (fmt_weight(fmt)) {

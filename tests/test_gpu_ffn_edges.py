@@ -497,14 +497,16 @@ def test_quantize_int8_launches(dtype, rows, k):
 # ---- weights decoded by the product itself
 
 @pytest.mark.parametrize("fmt", f.FMTS)
-@pytest.mark.parametrize("tokens,steps,inter", [(129, 1, 1), (256, 9, 333), (144, 4, 1030), (256, 40, 129)])
+@pytest.mark.parametrize("tokens,steps,inter", [(129, 1, 1), (256, 9, 333), (144, 4, 1030), (256, 40, 129), (257, 3, 140),
+                                                (512, 5, 70), (513, 5, 70)])
 def test_gated_decoded_in_the_product(fmt, tokens, steps, inter):
-    """Up to 256 tokens: one step and many, ragged channels, one row of tiles, K split over workgroups."""
+    """One step and many, ragged channels, one row of tiles, K split over workgroups; around each format's last number of
+    tokens."""
     _gated_case(fmt, tokens, steps * f.group(fmt), inter, ACTS[inter % 2], seed=steps)
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4_f16", "mxfp4_bf16"])
-@pytest.mark.parametrize("tokens,hidden,inter", [(1024, 320, 700), (1025, 320, 700), (700, 128, 9100), (511, 64, 4500)])
+@pytest.mark.parametrize("tokens,hidden,inter", [(2048, 320, 700), (2049, 320, 700), (700, 128, 9100), (511, 64, 4500)])
 def test_gated_mxfp4_tiles(fmt, tokens, hidden, inter):
     _gated_case(fmt, tokens, hidden, inter, "silu", seed=hidden)
 
