@@ -1,11 +1,11 @@
 // Gated feed-forward block over 4-bit weights: h = act(x Wg^T) * (x Wu^T), and the gradients of its two products.
 //
 // Many tokens: the dense kernel (w4_dense.h) multiplies fp16 rows with fp16 weights, which are decoded once into the
-// workspace or, where they meet few tiles of tokens, by the dense kernel as they arrive.  A weight row is held as w 2^-f with one exponent f a row that puts its largest scale into the
-// top of fp16's range, bf16 tokens as x 2^-e with one e a token; both come off exactly in the epilogue.  fp16 has
-// 11 significant bits where bf16 has 8, so a weight is rounded by at most 2^-11 of itself (INT4 and MXFP4: not at
-// all) and a bf16 token not at all; what lies more than 2^29 below its row's largest is rounded by at most 2^-39
-// of that.
+// workspace or, where they meet few tiles of tokens, by the dense kernel as they arrive.  A weight row is held as w 2^-f
+// with one exponent f a row that puts its largest scale into the top of fp16's range, bf16 tokens as x 2^-e with one e a
+// token; both come off exactly in the epilogue.  fp16 has 11 significant bits where bf16 has 8, so a weight is rounded by at
+// most 2^-11 of itself (INT4 and MXFP4: not at all) and a bf16 token not at all; what lies more than 2^29 below its row's
+// largest is rounded by at most 2^-39 of that.
 #include <algorithm>
 #include <type_traits>
 

@@ -1,11 +1,11 @@
 // Input gradient of a product with frozen 4-bit weights: dx[t, k] = sum_n d[t, n] W_hat[n, k].
 //
-// The sum runs over the weight rows, along which a packed byte holds nothing: the weights are decoded once into
-// W_hat^T rows of 16 bits in the workspace (through LDS), which the dense kernel multiplies with d.  Of 143 us for 2048
-// tokens of INT4 17920 x 1536 the product takes 109 (1030 TFLOP/s), the sum of its five splits 12, decoding 22.  A weight is rounded once to d's type (2^-8 of itself in bf16, 2^-11 in fp16; fp16 with one
-// exponent for the whole matrix, taken from its largest scale, so that neither large nor small weights leave its
-// range).  Rows of W_hat^T are padded with zeros to whole steps of the dense kernel, and so is d where its rows do
-// not end on one or are not aligned.
+// The sum runs over the weight rows, along which a packed byte holds nothing: the weights are decoded once into W_hat^T
+// rows of 16 bits in the workspace (through LDS), which the dense kernel multiplies with d.  Of 143 us for 2048 tokens of
+// INT4 17920 x 1536 the product takes 109 (1030 TFLOP/s), the sum of its five splits 12, decoding 22.  A weight is rounded
+// once to d's type (2^-8 of itself in bf16, 2^-11 in fp16; fp16 with one exponent for the whole matrix, taken from its
+// largest scale, so that neither large nor small weights leave its range).  Rows of W_hat^T are padded with zeros to whole
+// steps of the dense kernel, and so is d where its rows do not end on one or are not aligned.
 #include <algorithm>
 
 #include "w4_ffn.h"

@@ -12,7 +12,8 @@
  *   - All arrays are dense and row-major; there are no stride arguments.
  *   - `stream` is a hipStream_t passed as void* (NULL = the default stream).  Matmul calls are
  *     asynchronous on it and make no allocation and no synchronization, so they can be captured
- *     in a HIP graph.  Quantize calls synchronize the stream (they report device-detected errors).
+ *     in a HIP graph.  Calls that quantize to 4 bits synchronize the stream (they report device-detected
+ *     errors).
  *   - Arguments are validated on the host before anything is launched; a failing check returns a
  *     negative w4_status_t and launches nothing.  After a launch, a HIP launch error is reported
  *     as W4_ERR_HIP.
@@ -83,7 +84,7 @@ typedef enum {
   W4_ERR_NULL = -1,      /* a required pointer is NULL                                        */
   W4_ERR_SHAPE = -2,     /* N, K or B out of range, or K not a multiple of 64 (NF4, FP4, MXFP4) / 128 (INT4, INT4A) */
   W4_ERR_ALIGN = -3,     /* packed or x not 16-byte aligned, scales or y not element aligned  */
-  W4_ERR_FORMAT = -4,    /* unknown w4_format_t                                               */
+  W4_ERR_FORMAT = -4,    /* unknown w4_format_t, w4_type_t or w4_act_t                        */
   W4_ERR_NONFINITE = -5, /* quantize met a NaN or Inf weight (outputs are then meaningless)   */
   W4_ERR_WORKSPACE = -6, /* workspace missing or smaller than w4_workspace_bytes()            */
   W4_ERR_PATH = -7,      /* unknown path, or a path that does not support this batch size     */
@@ -607,12 +608,13 @@ typedef enum { W4_F32 = 0, W4_F16 = 1, W4_BF16 = 2 } w4_type_t;
  *   workspace device memory of at least w4_gated_workspace_bytes(...) bytes, 16-byte aligned; may be NULL when
  *             that is 0; scratch on entry and exit; two calls in flight must not share it
  * No output may overlap an input, the other output or the workspace, nor the workspace an input.  fp32
- * accumulation, g and u rounded to x's type for `products` alone.  From many tokens on (see w4_gated_workspace_bytes) the
- * weights enter as fp16 numbers of a common exponent a row (at most 2^-11 of themselves off; INT4 and MXFP4 exact) and
- * bf16 tokens as fp16 numbers of a common exponent a token (exact), in both what lies more than 2^29 below the
- * row's largest by at most 2^-39 of that.  Infinities and NaN stay in their token's (a scale's: in its channel's) results,
- * where the formula has them; without a workspace an infinite token of asymmetric INT4 gives NaN for some of its infinite
- * products (its zero points are taken off as z times the token's sum).  The order of every sum is fixed.  Asynchronous on `stream`. */
+ * accumulation, g and u rounded to x's type for `products` alone.  Where a workspace is needed (from 129 tokens
+ * on) the weights enter as fp16 numbers of a common exponent a row (at most 2^-11 of themselves off; INT4 and MXFP4 exact) and bf16 tokens as fp16
+ * numbers of a common exponent a token (exact), in both what lies more than 2^29 below the row's largest by at most
+ * 2^-39 of that.  Infinities and NaN stay in their token's (a scale's: in its channel's) results, where the formula
+ * has them; an infinite token of asymmetric INT4 up to 128 tokens gives NaN for some of its infinite products (its
+ * zero points are taken off as z times the token's sum), as it does for a weight that became 0 under its row's
+ * exponent.  The order of every sum is fixed.  Asynchronous on `stream`. */
 int w4_gated(const void* x, const uint8_t* gate_up, const void* gate_up_scales, int fmt, int act, int64_t tokens,
              int64_t hidden, int64_t inter, void* h, void* products, void* workspace, size_t workspace_bytes,
              void* stream);
@@ -644,9 +646,9 @@ int w4_gated_grad(const void* dh, const void* products, int type, int act, int64
  *   workspace  device memory of at least w4_gemm_grad_workspace_bytes(...) bytes, 16-byte aligned; scratch on
  *            entry and exit; must not overlap an input; two calls in flight must not share it
  * A weight is rounded once to d's type (bf16 2^-8, fp16 2^-11 of itself, fp16 with one exponent for all of W: what
- * lies more than 2^29 below the largest scale by at most 2^-39 of that), the sums are fp32 in a fixed order, dx is rounded once.
- * Infinities and NaN of d stay in their row, where the formula has them; what an infinite or NaN scale gives stays in its
- * block's columns (NaN, or the formula's infinity).  Asynchronous on `stream`. */
+ * lies more than 2^29 below the largest scale by at most 2^-39 of that), the sums are fp32 in a fixed order, dx is
+ * rounded once.  Infinities and NaN of d stay in their row, where the formula has them; what an infinite or NaN scale
+ * gives stays in its block's columns (NaN, or the formula's infinity).  Asynchronous on `stream`. */
 int w4_gemm_grad(const void* d, const uint8_t* packed, const void* scales, int fmt, int64_t N, int64_t K, int64_t B,
                  void* dx, void* workspace, size_t workspace_bytes, void* stream);
 
