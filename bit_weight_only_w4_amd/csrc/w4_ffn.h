@@ -24,7 +24,7 @@ struct DenseArgs {
   uint32_t out_type;  // w4_type_t; fp32 for 8-bit products without a gate alone
   uint32_t act;
   uint32_t* partial;  // scratch for dense_bytes() bytes, null where that is 0
-  uint32_t splits, per;  // set by launch_dense: K split over workgroups, steps of 64 bytes in a split
+  uint32_t splits, per;  // set by launch_dense: K split over workgroups, steps of 128 bytes in a split
   uint32_t tile0, bm, bn;  // set by launch_dense: the launch covers, in its own tiles, tiles of bm x bn from tile0 on
   uint32_t wide;      // set by launch_dense: rows of the outputs are whole, aligned 16-byte pieces
 };

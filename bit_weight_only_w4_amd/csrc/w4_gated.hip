@@ -207,41 +207,44 @@ GatedSpace gated_space(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
 }
 
 // Gradients of g | u from that of h, element by element: six bytes read and four written a channel, which is all
-// that bounds it (bf16, 4096 x 8960: 65 us, 5.6 TB/s).  V channels a thread: 8 where rows and pointers allow 16-byte
-// accesses, else 1 (4096 x 8961: 95 us).
-template <int XT, int ACT, int V>
-__global__ void __launch_bounds__(256) gated_grad_kernel(const uint16_t* dh, const uint16_t* pr, uint16_t* dp,
-                                                         int64_t first, int64_t total, int64_t inter) {
-  const int64_t i = first + ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;  // channel of dh, row-major
-  if (i >= total) return;
-  const int64_t t = i / inter, at = i + t * inter;  // g at 2 inter t + channel, u inter further
-  uint16_t d[V], g[V], u[V], og[V], ou[V];
-  __builtin_memcpy(d, dh + i, sizeof d);
-  __builtin_memcpy(g, pr + at, sizeof g);
-  __builtin_memcpy(u, pr + at + inter, sizeof u);
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
+// that bounds it (bf16, 4096 x 8960: 65 us, 5.6 TB/s; 4096 x 8961, whose rows are not aligned, 66).  A thread takes
+// 8 channels of a row, the last one of a row what is left.
+template <int XT, int ACT>
+__global__ void __launch_bounds__(256) gated_grad_kernel(const uint16_t* dh, const uint16_t* pr, uint16_t* dp, int64_t first,
+                                                         int64_t pieces, int64_t inter) {
+  const int64_t i = first + (int64_t)blockIdx.x * 256 + threadIdx.x;  // piece, row-major
+  if (i >= pieces) return;
+  const int64_t per = (inter + 7) / 8, t = i / per, c = (i - t * per) * 8;
+  const uint16_t* from = dh + t * inter + c;
+  const uint16_t* gu = pr + t * 2 * inter + c;
+  uint16_t* to = dp + t * 2 * inter + c;
+  auto one = [&](uint16_t dv, uint16_t gv, uint16_t uv, uint16_t& og, uint16_t& ou) __attribute__((always_inline)) {
     float slope;
-    const float y = act_slope<ACT>(from16<XT>(g[j]), &slope), f = from16<XT>(d[j]);
-    og[j] = (uint16_t)to16<XT>(f * from16<XT>(u[j]) * slope);
-    ou[j] = (uint16_t)to16<XT>(f * y);
+    const float y = act_slope<ACT>(from16<XT>(gv), &slope), f = from16<XT>(dv);
+    og = (uint16_t)to16<XT>(f * from16<XT>(uv) * slope);
+    ou = (uint16_t)to16<XT>(f * y);
+  };
+  if (c + 8 > inter) {
+    for (int64_t j = 0; c + j < inter; ++j) one(from[j], gu[j], gu[inter + j], to[j], to[inter + j]);
+    return;
   }
-  __builtin_memcpy(dp + at, og, sizeof og);
-  __builtin_memcpy(dp + at + inter, ou, sizeof ou);
+  uint16_t d[8], g[8], u[8], og[8], ou[8];
+  __builtin_memcpy(d, from, 16);
+  __builtin_memcpy(g, gu, 16);
+  __builtin_memcpy(u, gu + inter, 16);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) one(d[j], g[j], u[j], og[j], ou[j]);
+  __builtin_memcpy(to, og, 16);
+  __builtin_memcpy(to + inter, ou, 16);
 }
 
 template <int XT, int ACT>
 hipError_t grad_launch(const uint16_t* dh, const uint16_t* pr, uint16_t* dp, int64_t tokens, int64_t inter,
                        hipStream_t s) {
-  const int64_t total = tokens * inter;
-  const bool wide = inter % 8 == 0 && ((uintptr_t)dh | (uintptr_t)pr | (uintptr_t)dp) % 16 == 0;
-  const int64_t v = wide ? 8 : 1, most = ((int64_t)1 << 31) * v;  // a launch has fewer than 2^32 threads
-  for (int64_t first = 0; first < total; first += most) {
-    const dim3 grid((uint32_t)((std::min(total - first, most) / v + 255) / 256)), block(256);
-    if (wide)
-      gated_grad_kernel<XT, ACT, 8><<<grid, block, 0, s>>>(dh, pr, dp, first, total, inter);
-    else
-      gated_grad_kernel<XT, ACT, 1><<<grid, block, 0, s>>>(dh, pr, dp, first, total, inter);
+  const int64_t pieces = tokens * ((inter + 7) / 8), most = (int64_t)1 << 31;  // a launch has fewer than 2^32 threads
+  for (int64_t first = 0; first < pieces; first += most) {
+    const dim3 grid((uint32_t)((std::min(pieces - first, most) + 255) / 256));
+    gated_grad_kernel<XT, ACT><<<grid, dim3(256), 0, s>>>(dh, pr, dp, first, pieces, inter);
   }
   return hipGetLastError();
 }

@@ -703,7 +703,7 @@ hipError_t launch_fx(int b, const GemvArgs& a, int groups, const GemvPlan& p, hi
   return hipErrorInvalidValue;
 }
 
-// Gated launches: batches of up to kGatedGemvBatch rows, rows of up to 3 chunks a lane.
+// Gated launches: rows of up to 3 chunks a lane.
 template <int FMT, int XT, int B, int ITM>
 hipError_t launch_gated_one(const GemvGatedArgs& a, const GemvPlan& p, hipStream_t s) {
   if (p.threads == 256)
