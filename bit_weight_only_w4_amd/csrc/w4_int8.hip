@@ -15,34 +15,29 @@
 namespace w4 {
 namespace {
 
-// 8 consecutive values of a row as fp32.  TYPE a w4_type_t.
-template <int TYPE, bool ALIGNED>
+// 8 consecutive values of a row as fp32, zeros past the `left` that it still has.  TYPE a w4_type_t.
+template <int TYPE>
 __device__ inline void load8(const void* x, size_t at, uint32_t left, float (&v)[8]) {
-  if constexpr (ALIGNED) {
-    if constexpr (TYPE == W4_F32) {
-      const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(x) + at);
-      const float4 a = q[0], b = q[1];
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  if constexpr (TYPE == W4_F32) {
+    const float* from = reinterpret_cast<const float*>(x) + at;
+    if (left >= 8) {
+      __builtin_memcpy(v, from, 32);
     } else {
-      const uint4 a = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(x) + at);
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = from16<TYPE == W4_F16 ? kF16 : kBF16>(w[j] & 0xFFFFu);
-        v[2 * j + 1] = from16<TYPE == W4_F16 ? kF16 : kBF16>(w[j] >> 16);
-      }
+      for (int j = 0; j < 8; ++j) v[j] = (uint32_t)j < left ? from[j] : 0.0f;
     }
   } else {
+    constexpr int XT = TYPE == W4_F16 ? kF16 : kBF16;
+    const uint16_t* from = reinterpret_cast<const uint16_t*>(x) + at;
+    uint16_t w[8];
+    if (left >= 8) {
+      __builtin_memcpy(w, from, 16);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = 0.0f;
-      if ((uint32_t)j < left) {
-        if constexpr (TYPE == W4_F32)
-          v[j] = reinterpret_cast<const float*>(x)[at + j];
-        else
-          v[j] = from16<TYPE == W4_F16 ? kF16 : kBF16>(reinterpret_cast<const uint16_t*>(x)[at + j]);
-      }
+      for (int j = 0; j < 8; ++j) w[j] = (uint32_t)j < left ? from[j] : (uint16_t)0;
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = from16<XT>(w[j]);
   }
 }
 
@@ -61,7 +56,7 @@ __device__ inline float code_at_border(float x, float s, float c) {
 // maximum and the pass that writes the codes, what is beyond them is read again.  Two or four bytes read and one written a
 // value bound it (65536 x 1024 bf16 45 us, 4.5 TB/s; 4096 x 8192 26 us, 3.8 TB/s), once the border test is left to the
 // few chunks that need it (with it for every value: 54 and 32 us).
-template <int TYPE, bool ALIGNED, int THREADS, int HOLD>
+template <int TYPE, int THREADS, int HOLD>
 __global__ void __launch_bounds__(THREADS) quantize_int8_kernel(const void* x, uint32_t k, int8_t* codes,
                                                                 float* scales) {
   const size_t row = blockIdx.x, base = row * (size_t)k;
@@ -76,13 +71,13 @@ __global__ void __launch_bounds__(THREADS) quantize_int8_kernel(const void* x, u
   for (int i = 0; i < HOLD; ++i) {
     const uint32_t ch = tid + i * THREADS;
     if (ch < chunks) {
-      load8<TYPE, ALIGNED>(x, base + (size_t)ch * 8, k - ch * 8, v[i]);
+      load8<TYPE>(x, base + (size_t)ch * 8, k - ch * 8, v[i]);
       fold(v[i]);
     }
   }
   for (uint32_t ch = tid + HOLD * THREADS; ch < chunks; ch += THREADS) {
     float w[8];
-    load8<TYPE, ALIGNED>(x, base + (size_t)ch * 8, k - ch * 8, w);
+    load8<TYPE>(x, base + (size_t)ch * 8, k - ch * 8, w);
     fold(w);
   }
   float top = wave_max(__uint_as_float(min(most, 0x7F800000u)));
@@ -123,10 +118,12 @@ __global__ void __launch_bounds__(THREADS) quantize_int8_kernel(const void* x, u
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j >> 2] |= ((uint32_t)(int)c[j] & 255u) << (8 * (j & 3));
     int8_t* to = codes + base + (size_t)ch * 8;
-    if constexpr (ALIGNED) {
-      *reinterpret_cast<uint2*>(to) = make_uint2(o[0], o[1]);
+    if (ch * 8 + 8 <= k) {
+      __builtin_memcpy(to, o, 8);
     } else {
-      for (uint32_t j = 0; j < 8 && ch * 8 + j < k; ++j) to[j] = (int8_t)(o[j >> 2] >> (8 * (j & 3)));
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (ch * 8 + j < k) to[j] = (int8_t)(o[j >> 2] >> (8 * (j & 3)));
     }
   };
 #pragma unroll
@@ -136,16 +133,16 @@ __global__ void __launch_bounds__(THREADS) quantize_int8_kernel(const void* x, u
   }
   for (uint32_t ch = tid + HOLD * THREADS; ch < chunks; ch += THREADS) {
     float w[8];
-    load8<TYPE, ALIGNED>(x, base + (size_t)ch * 8, k - ch * 8, w);
+    load8<TYPE>(x, base + (size_t)ch * 8, k - ch * 8, w);
     put(w, ch);
   }
 }
 
-template <int TYPE, bool ALIGNED>
-void quantize_rows(const void* x, int64_t rows, int64_t k, int8_t* codes, float* scales, hipStream_t s) {
+template <int TYPE>
+void quantize_typed(const void* x, int64_t rows, int64_t k, int8_t* codes, float* scales, hipStream_t s) {
   auto run = [&](auto threads, auto hold) {
     constexpr int T = decltype(threads)::value, H = decltype(hold)::value;
-    quantize_int8_kernel<TYPE, ALIGNED, T, H><<<dim3((uint32_t)rows), dim3(T), 0, s>>>(x, (uint32_t)k, codes, scales);
+    quantize_int8_kernel<TYPE, T, H><<<dim3((uint32_t)rows), dim3(T), 0, s>>>(x, (uint32_t)k, codes, scales);
   };
   using std::integral_constant;
   // Microseconds (bf16) with 64, 256 and 1024 threads: 4096 x 512 4.5, 6.4, 17.0; 4096 x 1536 7.9, 8.4, 18.5; 1024 x 1536
@@ -157,15 +154,6 @@ void quantize_rows(const void* x, int64_t rows, int64_t k, int8_t* codes, float*
     run(integral_constant<int, 256>{}, integral_constant<int, 5>{});
   else
     run(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
-}
-
-template <int TYPE>
-void quantize_typed(const void* x, int64_t rows, int64_t k, int8_t* codes, float* scales, hipStream_t s) {
-  const bool aligned = k % 8 == 0 && (uintptr_t)x % 16 == 0 && (uintptr_t)codes % 8 == 0;
-  if (aligned)
-    quantize_rows<TYPE, true>(x, rows, k, codes, scales, s);
-  else
-    quantize_rows<TYPE, false>(x, rows, k, codes, scales, s);
 }
 
 }  // namespace
