@@ -29,7 +29,9 @@ SOURCES = ["w4_api.cpp", "w4_gemv.hip",
            "w4_quant.hip", "w4_twopass.hip", "w4_mfma.hip", "w4_mfma_grouped.hip", "w4_gemm.hip", "w4_gemm_fold.hip",
            "w4_moe.hip", "w4_moe_up_f16.hip", "w4_moe_up_bf16.hip", "w4_moe_down.hip",
            "w4_moe_wide_up.hip", "w4_moe_wide_down.hip",
-           "w4_dense.hip", "w4_dense_nf4.hip", "w4_dense_fp4.hip", "w4_dense_mxfp4.hip", "w4_dense_int4.hip", "w4_gated.hip", "w4_gated_gemv_f16.hip", "w4_gated_gemv_bf16.hip",
+           "w4_dense.hip", "w4_dense_nf4.hip", "w4_dense_fp4.hip", "w4_dense_mxfp4.hip", "w4_dense_int4.hip",
+           "w4_dense_columns_nf4.hip", "w4_dense_columns_fp4.hip", "w4_dense_columns_mxfp4.hip",
+           "w4_dense_columns_int4.hip", "w4_dense_columns_int4a.hip", "w4_gated.hip", "w4_gated_gemv_f16.hip", "w4_gated_gemv_bf16.hip",
            "w4_gated_mfma_f16.hip", "w4_gated_mfma_bf16.hip",
            "w4_grad.hip", "w4_grad_few_f16.hip", "w4_grad_few_bf16.hip", "w4_int8.hip", "w4_int8_rows.hip",
            "w4_gptq.hip", "w4_sparse24.hip", "w4_probe.hip"]

@@ -16,9 +16,9 @@
 //   * Gated: the B tile holds TN / 2 gate rows, then the up rows of the same channels; a wave's even column tiles
 //     are gate, its odd ones the up of the same channels, so the activation and the product happen in registers.
 //   * Rows past M or N and bytes past K are read at an offset outside the buffer, which gives zeros.
-//   * B in four bits (gated, fp16): a wave's 32 rows of packed weights and their scales come to LDS of its own a step
-//     ahead, and between the matrix instructions it decodes them, scales them, rounds them to fp16 and writes them into
-//     the stage where the copies would have put them.
+//   * B in four bits: a wave's packed weights and their scales come to LDS of its own a step ahead, and between the matrix
+//     instructions it decodes them, scales them, rounds them to 16 bits and writes them into the stage where the copies
+//     would have put them: rows of weights for the gated block (PackedRows), columns for a gradient (PackedColumns).
 //
 // What bounds it is the matrix cores under the card's power limit: its rate depends on the data.  4096 x 8192 x 8192: int8
 // 245 to 260 us (2110 to 2240 Tops/s; the library's product 2090), fp16 1160 TFLOP/s (1250).  One wave of every SIMD waits
@@ -34,6 +34,7 @@
 namespace w4 {
 
 struct DensePlan {
+  double us;  // the estimate
   int tile;
   uint32_t splits, per;
   uint32_t tiles, rest;  // tiles in all, and how many of the last are covered with 64 x 128 tiles by a second launch
@@ -106,7 +107,13 @@ __device__ inline void dense_copy(i32x4 r, const uint8_t* to, uint32_t off) {
                "v"(off), "s"(r));
 }
 
-// The same for 4 bytes a lane.
+// The same for 4 bytes a lane, and for 2 (to a dword each).
+__device__ inline void dense_copy2(i32x4 r, const uint8_t* to, uint32_t off) {
+  const uint32_t lds = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)to;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ushort %1, %2, 0 offen lds" ::"s"(
+                   __builtin_amdgcn_readfirstlane((int)lds)),
+               "v"(off), "s"(r));
+}
 __device__ inline void dense_copy4(i32x4 r, const uint8_t* to, uint32_t off) {
   const uint32_t lds = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)to;
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(
@@ -118,6 +125,14 @@ __device__ inline __amdgpu_buffer_rsrc_t dense_buffer(i32x4 r) {
   return __builtin_amdgcn_make_buffer_rsrc(
       reinterpret_cast<void*>((uint64_t)(uint32_t)r.x | ((uint64_t)(uint32_t)r.y << 32)), (short)0, r.z, r.w);
 }
+
+// B in four bits.  A source of the dense kernel's B tile writes the stage that the copies would have filled: the packed
+// bytes and scales of a wave's part come to LDS of its own (which leaves the counting of loads in flight to the kernel) a
+// step ahead of their use, and a quarter of them is decoded, scaled, rounded to 16 bits and written in each quarter of a
+// step.  The kernel calls, a step t: copy(t) asks for its bytes; once they have landed take() reads them, and after
+// settle() the next copy() may overwrite them; then look(q, i), put(stage, q, i) for quarters q and fourths i of them, each
+// look() before its put() (NF4 asks the table some matrix instructions earlier).  first_steps() loads the first ones
+// without LDS.
 
 // a * s rounded to fp32 and to fp16, two of them in a dword: a in fp16 (the halves of c) or in fp32.
 __device__ inline uint32_t scaled_halves(uint32_t c, float s) {
@@ -133,7 +148,7 @@ __device__ inline uint32_t scaled_pair(float a, float b, float s) {
   return d;
 }
 
-// Four bits: the weights of a packed dword, two of them at a time, in fp16: code (exact) times scale.
+// The weights of a packed dword, two of them at a time, in fp16: code (exact) times scale.
 //   * E2M1: the hardware's conversion to fp16, which takes the low nibble first: the nibbles are swapped before.
 //     MXFP4's scales are powers of two, which it applies itself (NaN too).
 //   * INT4: the nibbles as bytes below 0x64, which is 1024 + q in fp16, less 1024 + the offset.
@@ -182,6 +197,261 @@ struct DenseDecoder {
   }
 };
 
+constexpr int kRawBytes = 64 * 16 + 64 * 4;  // a step's packed bytes and scales of a wave
+
+// Rows of packed weights along K (w4_gated): a wave has 32 rows of the tile, a lane 32 weights of row lane / 2 in a step, in
+// chunks of 8.  The scales are folded (w4_gated.hip), two numbers a step.
+template <int FMT, int TM, int TN, int W, int STAGES>
+struct PackedRows {
+  static_assert(TN == 32 * W, "32 rows of B a wave");
+  uint8_t* own;
+  uint8_t* ring;
+  const float* table;
+  i32x4 rw, rs;
+  uint32_t woff, soff, to, steps, half, lane;
+  uint4 w;
+  float s;
+  uint4 ahead_w[STAGES];
+  float ahead_s[STAGES];
+  BlockScale scale;
+  DenseDecoder<FMT> dec;
+  uint32_t made[4];
+
+  // Rows n0 .. of the tile, gate rows first (CN of them, `nrows` exist), then up rows.
+  __device__ inline void init(const DenseArgs& p, uint32_t n0, uint32_t nrows, uint32_t last, uint8_t* raw, uint8_t* stages,
+                              const float* codes, int lane_, int wave) {
+    constexpr uint32_t CN = TN / 2;
+    own = raw + wave * kRawBytes;
+    ring = stages;
+    table = codes;
+    steps = last;
+    lane = (uint32_t)lane_;
+    const uint32_t r = 32 * wave, up = r >= CN ? 1u : 0u, at = r - (up ? CN : 0u);
+    const size_t row = (size_t)(up ? p.n : 0u) + n0 + at;
+    const uint32_t rows = at < nrows ? min(32u, nrows - at) : 0u;
+    rw = dense_rsrc(p.b + row * (p.pitch / 4), rows * (p.pitch / 4));
+    rs = dense_rsrc(reinterpret_cast<const uint8_t*>(p.scales) + row * (p.pitch / 16), rows * (p.pitch / 16));
+    const uint32_t of = lane >> 1;
+    half = lane & 1u;
+    woff = of * (p.pitch / 4) + half * 16;
+    soff = of * (p.pitch / 16) + half * 4;
+    to = (TM + r + of) * 128 + ((4u * half) ^ ((of >> 1) & 7u)) * 16;
+  }
+  __device__ inline void first_steps(uint32_t first) {
+    const __amdgpu_buffer_rsrc_t bw = dense_buffer(rw), bs = dense_buffer(rs);
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) {
+      const uint32_t t = first + i;
+      ahead_w[i] = __builtin_bit_cast(
+          uint4, __builtin_amdgcn_raw_buffer_load_b128(bw, woff + (t < steps ? t * 32 : 0x40000000u), 0, 0));
+      ahead_s[i] =
+          __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bs, soff + (t < steps ? t * 8 : 0x40000000u), 0, 0));
+    }
+  }
+  __device__ inline void use_first(int i) {
+    w = ahead_w[i];
+    s = ahead_s[i];
+    scales();
+  }
+  __device__ inline void copy(uint32_t t) {  // past the last step: from outside the buffers
+    dense_copy(rw, own, woff + (t < steps ? t * 32 : 0x40000000u));
+    dense_copy4(rs, own + 1024, soff + (t < steps ? t * 8 : 0x40000000u));
+  }
+  __device__ inline void take() {
+    w = *reinterpret_cast<const uint4*>(own + lane * 16);
+    s = *reinterpret_cast<const float*>(own + 1024 + lane * 4);
+  }
+  __device__ inline void scales() {
+    scale = BlockScale{s, 8.0f};
+    if constexpr (FMT == kINT4A) {  // the pair's first lane has the scale, its second the zero point
+      const float other =
+          __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(s), 0xB1, 0xF, 0xF, true));
+      scale = half ? BlockScale{other, s} : BlockScale{s, other};
+    }
+  }
+  __device__ inline void settle() {
+    asm volatile("" : "+v"(w.x), "+v"(w.y), "+v"(w.z), "+v"(w.w), "+v"(s));
+    scales();
+  }
+  template <int I>
+  __device__ inline void look(int q) {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    if (I == 0) dec.set(v[q], scale);
+    if constexpr (FMT == kNF4) dec.template look<I>(table);
+  }
+  template <int I>
+  __device__ inline void put(uint32_t stage, int q) {
+    made[I] = dec.template pair<I>();
+    if (I == 3)
+      *reinterpret_cast<uint4*>(ring + ((to + stage) ^ (uint32_t)(q * 16))) = make_uint4(made[0], made[1], made[2], made[3]);
+  }
+};
+
+// Two products rounded to fp32 (with an addend) and to fp16, in a dword.
+__device__ inline uint32_t fma_halves(float a, float s, float add, float b, float t, float more) {
+  uint32_t d;
+  asm("v_fma_mixlo_f16 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(s), "v"(add));
+  asm("v_fma_mixhi_f16 %0, %1, %2, %3" : "+v"(d) : "v"(b), "v"(t), "v"(more));
+  return d;
+}
+
+// Columns of packed weights (w4_gemm_grad): the sum runs along the weight rows, so a step's 64 of them, each with TN / 8
+// dwords of the tile's columns, have to be transposed.  A wave has 64 / W rows, a lane 8 columns (a dword) of four rows 4 a
+// .. 4 a + 3 among them; a quarter is the two columns of a byte, four weights of each, 8 bytes of a stage's row.
+//   * The chunks of stage row r are keyed on (r / 2) xor (r / 8): 32 lanes write to every eighth row, and so to 8 slots; the
+//     rows that a 16-lane group reads still have 8 different keys.
+//   * Scales come in the format's own form: one for each row and 64 or 128 columns; fp16 takes them times 2^-f.
+template <int FMT, int TYPE, int TM, int TN, int W, int STAGES>
+struct PackedColumns {
+  static_assert(TN == 32 * W, "64 rows of weights in the waves of a workgroup");
+  static constexpr uint32_t RPW = 64 / W;        // rows a wave
+  static constexpr uint32_t DW = TN / 8;         // dwords of a row
+  static constexpr uint32_t SU = TN / (is_g128(FMT) ? 128 : 64);  // scale units of a row
+  static constexpr uint32_t SB = FMT == kINT4 || FMT == kMXFP4 ? 2 : 4;
+  uint8_t* own;
+  uint8_t* ring;
+  const float* table;
+  const uint8_t* packed;
+  const uint8_t* scale_rows;
+  uint64_t wstep, sstep;  // bytes of 64 rows
+  uint32_t wbytes, sbytes;  // bytes of a row
+  uint32_t woff, soff, to, n, steps, from, lane, unit, dcol, scol;
+  int f;
+  bool odd;  // MXFP4: the second 32 columns of a unit
+  uint32_t w[4], b[4];
+  uint32_t ahead_w[STAGES][4], ahead_b[STAGES][4];
+  float s[4], add[4];
+  float code[8];
+  uint32_t lo[2], hi[2];
+
+  __device__ inline void init(const DenseArgs& p, uint32_t k0, uint32_t last, int exponent, uint8_t* raw, uint8_t* stages,
+                              const float* codes, int lane_, int wave) {
+    own = raw + wave * kRawBytes;
+    ring = stages;
+    table = codes;
+    lane = (uint32_t)lane_;
+    steps = last;
+    n = p.rows;
+    f = exponent;
+    wbytes = p.n / 2;
+    sbytes = p.n / (is_g128(FMT) ? 128 : 64) * SB;
+    wstep = (uint64_t)wbytes * 64;
+    sstep = (uint64_t)sbytes * 64;
+    packed = p.b;
+    scale_rows = reinterpret_cast<const uint8_t*>(p.scales);
+    const uint32_t first_row = RPW * wave;
+    {  // the copies: 16 bytes of row lane / (DW / 4), a scale of row lane / SU
+      const uint32_t r = lane / (DW / 4), c = lane % (DW / 4), k = k0 + 32 * c;
+      woff = k < p.n ? (first_row + r) * wbytes + k / 2 : kOutOfRange;
+      const uint32_t sr = lane / SU, u = lane % SU, ku = k0 + u * (is_g128(FMT) ? 128 : 64);
+      soff = sr < RPW && ku < p.n ? (first_row + sr) * sbytes + ku / (is_g128(FMT) ? 128 : 64) * SB : kOutOfRange;
+    }
+    const uint32_t c = lane % DW, a = lane / DW;
+    unit = c * 8 / (is_g128(FMT) ? 128 : 64);
+    odd = FMT == kMXFP4 && (c * 8 / 32) % 2;
+    from = (4 * a) * DW + c;  // the first of its four dwords
+    dcol = (first_row + 4 * a) * wbytes + k0 / 2 + 4 * c;
+    scol = (first_row + 4 * a) * sbytes + (k0 + 8 * c) / (is_g128(FMT) ? 128 : 64) * SB;
+    if (k0 + 8 * c >= p.n) dcol = scol = kOutOfRange - 4 * wbytes;
+    const uint32_t chunk = (first_row + 4 * a) / 8, key = (4 * (c & 1)) ^ (c & 7);
+    to = (TM + 8 * c) * 128 + ((chunk ^ key) & 7u) * 16 + 8 * (a & 1);
+  }
+  __device__ inline i32x4 rows_of(const uint8_t* base, uint64_t step, uint32_t bytes, uint32_t t) {
+    const uint32_t left = t < steps ? min(64u, n - 64 * t) : 0u;
+    return dense_rsrc(base + (t < steps ? t * step : 0), left * bytes);
+  }
+  __device__ inline void first_steps(uint32_t first) {
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) {
+      const __amdgpu_buffer_rsrc_t bw = dense_buffer(rows_of(packed, wstep, wbytes, first + i));
+      const __amdgpu_buffer_rsrc_t bs = dense_buffer(rows_of(scale_rows, sstep, sbytes, first + i));
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        ahead_w[i][r] = __builtin_amdgcn_raw_buffer_load_b32(bw, dcol + r * wbytes, 0, 0);
+        const uint32_t so = scol + r * sbytes;
+        ahead_b[i][r] = SB == 2 ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(bs, so, 0, 0)
+                                : __builtin_amdgcn_raw_buffer_load_b32(bs, so, 0, 0);
+      }
+    }
+  }
+  __device__ inline void use_first(int i) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) w[r] = ahead_w[i][r], b[r] = ahead_b[i][r];
+    scales();
+  }
+  __device__ inline void copy(uint32_t t) {
+    dense_copy(rows_of(packed, wstep, wbytes, t), own, woff);
+    const i32x4 rs = rows_of(scale_rows, sstep, sbytes, t);
+    if constexpr (SB == 2)
+      dense_copy2(rs, own + 1024, soff);
+    else
+      dense_copy4(rs, own + 1024, soff);
+  }
+  __device__ inline void take() {
+    const uint32_t* v = reinterpret_cast<const uint32_t*>(own);
+    const uint32_t* u = v + 256 + from / DW * SU + unit;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      w[r] = v[from + r * DW];
+      b[r] = u[r * SU];
+    }
+  }
+  __device__ inline void scales() {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float zero = 8.0f;
+      if constexpr (FMT == kMXFP4)
+        s[r] = e8m0_value((odd ? b[r] >> 8 : b[r]) & 255u);
+      else if constexpr (is_g128(FMT))
+        s[r] = __uint_as_float(b[r] << 16);
+      else
+        s[r] = __uint_as_float(b[r]);
+      if constexpr (FMT == kINT4A) zero = (float)((b[r] >> 16) & 15u);
+      if constexpr (TYPE == kDenseF16) s[r] = ldexpf(s[r], -f);
+      add[r] = is_g128(FMT) ? -zero * s[r] : 0.0f;  // exact: 8 and 4 bits
+    }
+  }
+  __device__ inline void settle() {
+    asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3]), "+v"(b[0]), "+v"(b[1]), "+v"(b[2]), "+v"(b[3]));
+    scales();
+  }
+  // The codes of row I's byte q, the first column's and the second's.
+  template <int I>
+  __device__ inline void look(int q) {
+    if constexpr (FMT == kNF4) {
+      const uint8_t* t = reinterpret_cast<const uint8_t*>(table);
+      const uint32_t v = w[I] >> (8 * q);
+      code[2 * I] = *reinterpret_cast<const float*>(t + ((v >> 2) & 0x3Cu));
+      code[2 * I + 1] = *reinterpret_cast<const float*>(t + ((v << 2) & 0x3Cu));
+    } else if constexpr (FMT == kFP4 || FMT == kMXFP4) {
+      decode_pair<FMT>(w[I], q, nullptr, BlockScale{1.0f, 0.0f}, &code[2 * I], &code[2 * I + 1]);
+    } else {
+      const uint32_t v = w[I] >> (8 * q);
+      code[2 * I] = (float)((v >> 4) & 15u);
+      code[2 * I + 1] = (float)(v & 15u);
+    }
+  }
+  template <int I>
+  __device__ inline void put(uint32_t stage, int q) {
+    if constexpr (I % 2 == 1) {
+      if constexpr (TYPE == kDenseF16) {
+        lo[I / 2] = fma_halves(code[2 * I - 2], s[I - 1], add[I - 1], code[2 * I], s[I], add[I]);
+        hi[I / 2] = fma_halves(code[2 * I - 1], s[I - 1], add[I - 1], code[2 * I + 1], s[I], add[I]);
+      } else {
+        lo[I / 2] = to16<kBF16>(__builtin_fmaf(code[2 * I - 2], s[I - 1], add[I - 1])) |
+                    (to16<kBF16>(__builtin_fmaf(code[2 * I], s[I], add[I])) << 16);
+        hi[I / 2] = to16<kBF16>(__builtin_fmaf(code[2 * I - 1], s[I - 1], add[I - 1])) |
+                    (to16<kBF16>(__builtin_fmaf(code[2 * I + 1], s[I], add[I])) << 16);
+      }
+    }
+    if (I == 3) {
+      uint8_t* at = ring + ((to + stage) ^ (uint32_t)(q * 16)) + 2 * q * 128;
+      *reinterpret_cast<uint2*>(at) = make_uint2(lo[0], lo[1]);
+      *reinterpret_cast<uint2*>(at + 128) = make_uint2(hi[0], hi[1]);
+    }
+  }
+};
+
 template <int TYPE, bool GATED, int FMT, int WM, int WN, int MT, int NT, int STAGES>
 __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
   constexpr int W = WM * WN, TM = 32 * MT * WM, TN = 32 * NT * WN;
@@ -189,11 +459,9 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
   constexpr bool PACKED = FMT >= 0;         // B in four bits
   constexpr int COPIES = (PACKED ? TM : ROWS) / 8 / W;  // copies of 8 rows a wave makes for a stage
   static_assert(TM % (8 * W) == 0 && (PACKED || (GATED ? TN / 2 : TN) % (8 * W) == 0), "a round of copies fills one operand");
-  static_assert(!PACKED || TN == 32 * W, "32 rows of B a wave");
   static_assert(!GATED || NT % 2 == 0, "gate and up in one wave");
   __shared__ __align__(16) uint8_t ring[STAGES][ROWS * 128];
-  constexpr int RAW = 64 * 16 + 64 * 4;     // a step's packed bytes and scales of a wave's rows of B
-  __shared__ __align__(16) uint8_t raw[PACKED ? W * RAW : 16];
+  __shared__ __align__(16) uint8_t raw[PACKED ? W * kRawBytes : 16];
   __shared__ float table[16];
   using Acc = typename DenseAcc<TYPE>::type;
 
@@ -217,14 +485,8 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
 
   const uint32_t nrows = min(CN, p.n - n0);
   const i32x4 ra = dense_rsrc(p.a + (size_t)m0 * p.pitch, min((uint32_t)TM, p.m - m0) * p.pitch);
-  i32x4 rb{}, ru{};  // B, gated: its gate and up rows; four bits: a wave's packed rows and their scales
-  if constexpr (PACKED) {
-    const uint32_t r = 32 * wave, up = GATED && r >= CN ? 1u : 0u, at = r - (up ? CN : 0u);
-    const size_t row = (size_t)(up ? p.n : 0u) + n0 + at;
-    const uint32_t rows = at < nrows ? min(32u, nrows - at) : 0u;
-    rb = dense_rsrc(p.b + row * (p.pitch / 4), rows * (p.pitch / 4));
-    ru = dense_rsrc(reinterpret_cast<const uint8_t*>(p.scales) + row * (p.pitch / 16), rows * (p.pitch / 16));
-  } else {
+  i32x4 rb{}, ru{};  // B, gated: its gate and up rows
+  if constexpr (!PACKED) {
     rb = dense_rsrc(p.b + (size_t)n0 * p.pitch, nrows * p.pitch);
     ru = dense_rsrc(p.b + (size_t)(GATED ? p.n + n0 : 0) * p.pitch, GATED ? nrows * p.pitch : 0u);
   }
@@ -269,11 +531,15 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
   };
   // Quarter s of the stage at byte `st` of the ring.
   const uint32_t base = (((uint32_t)h ^ key) * 16) + c * 128;
-  auto fetch = [&](Frags& f, const uint8_t* at, int i) __attribute__((always_inline)) {  // fragment i of a quarter
+  constexpr bool COLUMNS = PACKED && !GATED;  // B rows are keyed as PackedColumns writes them
+  const uint32_t bdiff = COLUMNS ? (((uint32_t)c >> 3) & 3u) * 16 : 0u;
+  auto fetch = [&](Frags& f, uint32_t at, int i) __attribute__((always_inline)) {  // fragment i of a quarter
     const int j = i - MT;
     const int row = i < MT ? 32 * (MT * wm + i)
                            : TM + (GATED ? (j & 1) * (int)CN + 32 * (NT / 2 * wn + j / 2) : 32 * (NT * wn + j));
-    const uint4 v = *reinterpret_cast<const uint4*>(at + row * 128);
+    static_assert(!COLUMNS || NT % 2 == 0, "a B tile's parity is its column tile's");
+    const uint32_t x = COLUMNS && i >= MT ? bdiff ^ (uint32_t)((j & 1) * 64) : 0u;
+    const uint4 v = *reinterpret_cast<const uint4*>(&ring[0][0] + ((at ^ x) + row * 128));
     if (i < MT)
       f.a[i] = v;
     else
@@ -287,56 +553,27 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
   constexpr int C0 = STAGES == 2 ? COPIES : COPIES < 2 * C3 ? COPIES : 2 * C3;
   constexpr int C1 = COPIES < 3 * C3 ? COPIES : 3 * C3;
   using std::integral_constant;
-  // Four bits: this wave's 32 rows of the B tile, a lane 32 weights of row lane / 2 in a step.  Their packed bytes and
-  // scales come to LDS of the wave's own (which leaves the counting of loads in flight to this kernel), a step ahead
-  // of their use; a quarter of them is decoded, scaled, rounded to fp16 and written into the stage in each quarter.
-  uint8_t* const own = raw + (PACKED ? wave * RAW : 0);
-  const uint32_t raw_row = (uint32_t)lane >> 1, raw_half = (uint32_t)lane & 1u;
-  const uint32_t woff = raw_row * (p.pitch / 4) + raw_half * 16, soff = raw_row * (p.pitch / 16) + raw_half * 4;
-  const uint32_t wput = (TM + 32u * wave + raw_row) * 128 + ((4u * raw_half) ^ ((raw_row >> 1) & 7u)) * 16;
-  struct Raw {
-    uint4 w;
-    float s;
-  } held{};
-  BlockScale hs{0.0f, 0.0f};
-  auto copy_raw = [&](uint32_t t) __attribute__((always_inline)) {  // past the last step: from outside the buffers
-    dense_copy(rb, own, woff + (t < steps ? t * 32 : 0x40000000u));
-    dense_copy4(ru, own + 1024, soff + (t < steps ? t * 8 : 0x40000000u));
-  };
-  auto take_raw = [&]() __attribute__((always_inline)) {
-    held.w = *reinterpret_cast<const uint4*>(own + lane * 16);
-    held.s = *reinterpret_cast<const float*>(own + 1024 + lane * 4);
-  };
-  auto scale_raw = [&]() __attribute__((always_inline)) {
-    hs = BlockScale{held.s, 8.0f};
-    if constexpr (FMT == kINT4A) {  // the pair's first lane has the scale, its second the zero point
-      const float other = __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(held.s), 0xB1, 0xF,
-                                                                              0xF, true));
-      hs = raw_half ? BlockScale{other, held.s} : BlockScale{held.s, other};
+  using Source = typename std::conditional<GATED, PackedRows<PACKED ? FMT : kFP4, TM, PACKED ? TN : 32 * W, W, STAGES>,
+                                           PackedColumns<PACKED ? FMT : kFP4, TYPE, TM, PACKED ? TN : 32 * W, W, STAGES>>::type;
+  Source src;
+  int all = 0;  // the exponent of all of B
+  if constexpr (PACKED && GATED) src.init(p, n0, nrows, steps, raw, &ring[0][0], table, lane, wave);
+  if constexpr (COLUMNS) {
+    if constexpr (TYPE == kDenseF16) {  // from the scan's maxima, every wave for itself
+      float top = 0.0f;
+      for (uint32_t i = lane; i < p.nparts; i += 64) top = fmaxf(top, p.parts[i]);
+      all = fold_exponent<FMT>(wave_max(top));
+      if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *p.exp_out = all;
     }
-  };
-  uint32_t made[4];
-  DenseDecoder<PACKED ? FMT : kFP4> dec;
-  auto look = [&](int quarter_of, auto pair) __attribute__((always_inline)) {
-    constexpr int P = decltype(pair)::value;
-    const uint32_t w[4] = {held.w.x, held.w.y, held.w.z, held.w.w};
-    if (P == 0) dec.set(w[quarter_of], hs);
-    if constexpr (FMT == kNF4) dec.template look<P>(table);
-  };
-  auto decode = [&](uint32_t stage_at, int quarter_of, auto pair) __attribute__((always_inline)) {
-    constexpr int P = decltype(pair)::value;
-    made[P] = dec.template pair<P>();
-    if (P == 3)
-      *reinterpret_cast<uint4*>(&ring[0][0] + ((wput + stage_at) ^ (uint32_t)(quarter_of * 16))) =
-          make_uint4(made[0], made[1], made[2], made[3]);
-  };
+    src.init(p, n0, steps, all, raw, &ring[0][0], table, lane, wave);
+  }
   // A quarter: after each matrix instruction one of the next quarter's fragments is requested, and a copy now and then.
   auto quarter = [&](Frags& next, uint32_t st, auto which, const Frags& f, uint32_t to, uint32_t t, auto from, auto end)
       __attribute__((always_inline)) {
     constexpr int A = decltype(from)::value, Z = decltype(end)::value, ALL = MT * NT;
     constexpr int s = decltype(which)::value;  // the quarter whose fragments are requested
     constexpr int D0 = PACKED && s == 0 ? 1 : 0;
-    const uint8_t* at = &ring[0][0] + ((base + st) ^ (uint32_t)(s * 32));
+    const uint32_t at = (base + st) ^ (uint32_t)(s * 32);
 #pragma unroll
     for (int q = 0; q < ALL; ++q) {
       acc[q / NT][q % NT] = dense_mfma<TYPE>(f.a[q / NT], f.b[q % NT], acc[q / NT][q % NT]);
@@ -345,23 +582,21 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
         if (i * ALL / (MT + NT) == q) fetch(next, at, i);
       if constexpr (PACKED) {
         if (D0 && q == 1) {  // the packed bytes are in registers before the next ones are asked for
-          asm volatile("" : "+v"(held.w.x), "+v"(held.w.y), "+v"(held.w.z), "+v"(held.w.w), "+v"(held.s));
-          scale_raw();
-          copy_raw(t + 1);
+          src.settle();
+          src.copy(t + 1);
         }
-        constexpr integral_constant<int, 0> p0;
-        constexpr integral_constant<int, 1> p1;
-        constexpr integral_constant<int, 2> p2;
-        constexpr integral_constant<int, 3> p3;
         if constexpr (FMT == kNF4) {
-          if (D0 == q) look(s, p0), look(s, p1);
-          if (D0 + (ALL - D0) / 3 == q) decode(to, s, p0), decode(to, s, p1), look(s, p2), look(s, p3);
-          if (D0 + 2 * (ALL - D0) / 3 == q) decode(to, s, p2), decode(to, s, p3);
+          if (D0 == q) src.template look<0>(s), src.template look<1>(s);
+          if (D0 + (ALL - D0) / 3 == q) {
+            src.template put<0>(to, s), src.template put<1>(to, s);
+            src.template look<2>(s), src.template look<3>(s);
+          }
+          if (D0 + 2 * (ALL - D0) / 3 == q) src.template put<2>(to, s), src.template put<3>(to, s);
         } else {
-          if (D0 == q) look(s, p0), decode(to, s, p0);
-          if (D0 + (ALL - D0) / 4 == q) decode(to, s, p1);
-          if (D0 + 2 * (ALL - D0) / 4 == q) decode(to, s, p2);
-          if (D0 + 3 * (ALL - D0) / 4 == q) decode(to, s, p3);
+          if (D0 == q) src.template look<0>(s), src.template put<0>(to, s);
+          if (D0 + (ALL - D0) / 4 == q) src.template look<1>(s), src.template put<1>(to, s);
+          if (D0 + 2 * (ALL - D0) / 4 == q) src.template look<2>(s), src.template put<2>(to, s);
+          if (D0 + 3 * (ALL - D0) / 4 == q) src.template look<3>(s), src.template put<3>(to, s);
         }
       }
 #pragma unroll
@@ -373,16 +608,7 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
   Frags f0, f1;
   if constexpr (PACKED) {
     code_table<FMT>(table);
-    Raw ahead[STAGES];
-    const __amdgpu_buffer_rsrc_t bw = dense_buffer(rb), bs = dense_buffer(ru);
-#pragma unroll
-    for (int i = 0; i < STAGES; ++i) {
-      const uint32_t t = first + i;
-      ahead[i].w = __builtin_bit_cast(
-          uint4, __builtin_amdgcn_raw_buffer_load_b128(bw, woff + (t < steps ? t * 32 : 0x40000000u), 0, 0));
-      ahead[i].s = __uint_as_float(
-          __builtin_amdgcn_raw_buffer_load_b32(bs, soff + (t < steps ? t * 8 : 0x40000000u), 0, 0));
-    }
+    src.first_steps(first);
     __syncthreads();  // the table
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i)
@@ -390,21 +616,16 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
       for (int j = 0; j < COPIES; ++j) copy(&ring[i][0], first + i, j);
 #pragma unroll
     for (int i = 0; i < STAGES; ++i) {
-      held = ahead[i];
-      scale_raw();
+      src.use_first(i);
 #pragma unroll
       for (int q = 0; q < (i == STAGES - 1 ? 1 : 4); ++q) {
-        look(q, integral_constant<int, 0>{});
-        decode(i * SIZE, q, integral_constant<int, 0>{});
-        look(q, integral_constant<int, 1>{});
-        decode(i * SIZE, q, integral_constant<int, 1>{});
-        look(q, integral_constant<int, 2>{});
-        decode(i * SIZE, q, integral_constant<int, 2>{});
-        look(q, integral_constant<int, 3>{});
-        decode(i * SIZE, q, integral_constant<int, 3>{});
+        src.template look<0>(q), src.template put<0>(i * SIZE, q);
+        src.template look<1>(q), src.template put<1>(i * SIZE, q);
+        src.template look<2>(q), src.template put<2>(i * SIZE, q);
+        src.template look<3>(q), src.template put<3>(i * SIZE, q);
       }
     }
-    copy_raw(first + STAGES);
+    src.copy(first + STAGES);
 #pragma unroll
     for (int j = 0; j < C3; ++j) copy(&ring[STAGES - 1][0], first + STAGES - 1, j);
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 + C3) : "memory");
@@ -416,7 +637,7 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((STAGES - 2) * COPIES + C3) : "memory");
   }
 #pragma unroll
-  for (int i = 0; i < MT + NT; ++i) fetch(f0, &ring[0][0] + base, i);
+  for (int i = 0; i < MT + NT; ++i) fetch(f0, base, i);
   uint32_t now = 0, spare = (STAGES - 1) * SIZE;  // the step's stage, and the last step's
   for (uint32_t t = first; t < steps; ++t) {
     const uint32_t u = t + STAGES - 1;
@@ -427,7 +648,7 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * COPIES) : "memory");
     spare = now;
     now = now + SIZE == STAGES * SIZE ? 0 : now + SIZE;
-    if constexpr (PACKED) take_raw();
+    if constexpr (PACKED) src.take();
     quarter(f0, now, integral_constant<int, 0>{}, f1, spare, u + 1, integral_constant<int, 0>{}, integral_constant<int, C3>{});
   }
   wait_all_vector_loads();  // no copy outlives the workgroup
@@ -468,8 +689,7 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
     const uint32_t n = nw + 32 * (GATED ? j / 2 : j) + c;
     cv[j] = cols_of && n < p.n ? reinterpret_cast<const uint32_t*>(cols_of)[(GATED && (j & 1) ? p.n : 0u) + n] : 0u;
   }
-  int all = 0;
-  if constexpr (TYPE != kDenseI8) all = p.exp ? *p.exp : 0;
+  if constexpr (TYPE != kDenseI8 && !COLUMNS) all = p.exp ? *p.exp : 0;
   // One output's 32 rows from row `mw` on, in LDS, to memory.
   auto flush = [&](void* out, uint32_t pitch, uint32_t n, uint32_t nend, uint32_t mw) __attribute__((always_inline)) {
     asm volatile("" ::: "memory");  // a wave's LDS accesses keep their order; the compiler's must too

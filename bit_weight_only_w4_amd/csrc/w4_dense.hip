@@ -14,17 +14,25 @@ namespace w4 {
 //
 // Four bits: decoding makes a step of the largest tile take 1.0 (MXFP4), 1.19 (FP4, INT4) or 1.3 (NF4) times as long, of
 // the others, whose rows of B meet fewer of A, 1.18 times that (160 and 256 tokens of 1536 -> 8960 to 8192 -> 28672).
+// Decoding columns: 1.07 (FP4, INT4), 1.1 (MXFP4) or 1.25 (NF4), 1.12 times that for 128 x 256, 2.2 and 1.62 for 64 x 128
+// (4096 x 2048 weights, 256 and 2048 tokens: a step of 64 x 128 tiles alone 0.71 to 1.07 us, of full CUs 1.14 to 1.5).
 DensePlan plan_dense(bool gated, int64_t m, int64_t n, int64_t pitch, int packed) {
-  const double slow = packed < 0 || packed == kMXFP4 ? 1.0 : packed == kNF4 ? 1.3 : 1.19;
+  const bool columns = packed >= 0 && !gated;
+  const double slow = packed < 0         ? 1.0
+                      : packed == kNF4   ? columns ? 1.25 : 1.3
+                      : packed == kMXFP4 ? columns ? 1.1 : 1.0
+                                         : columns ? 1.07 : 1.19;
   const int64_t cus = device_cu_count(), steps = (pitch + 127) / 128;
   const int64_t width = gated ? 2 * n : n;
-  DensePlan best{0, 1, (uint32_t)steps, 0, 0};
+  DensePlan best{0, 0, 1, (uint32_t)steps, 0, 0};
   double least = 0;
   for (int i = 0; i < (packed < 0 ? kTileCount : kTileCount - 1); ++i) {
     auto tile_of = [&](int j) {
       Tile t = kTiles[j];
-      const double f = packed < 0 ? 1.0 : j ? 1.18 * slow : slow;
-      t.alone *= f, t.full *= f;
+      const double f = packed < 0 || j == 0 ? slow : columns ? 1.12 * slow : 1.18 * slow;
+      t.alone *= columns && j == 2 ? 2.2 * slow : f;
+      t.full *= columns && j == 2 ? 1.62 * slow : f;
+      if (columns) t.ends += 3;  // the first steps are decoded before there is anything to multiply
       return t;
     };
     const Tile t = tile_of(i);
@@ -40,7 +48,7 @@ DensePlan plan_dense(bool gated, int64_t m, int64_t n, int64_t pitch, int packed
         if (s > 1) us += 3 + (double)s * m * width * 8 / 5e6;
         if (least == 0 || us < least) {
           least = us;
-          best = DensePlan{i, (uint32_t)s, (uint32_t)per, (uint32_t)tiles, (uint32_t)rest};
+          best = DensePlan{us, i, (uint32_t)s, (uint32_t)per, (uint32_t)tiles, (uint32_t)rest};
         }
       };
       offer(work, 0);
@@ -65,6 +73,8 @@ bool dense_prepare(const DensePlan& p, DenseArgs* a) {
   a->wide = a->n % 8 == 0 && ((uintptr_t)a->out | (uintptr_t)a->products) % 16 == 0;
   return true;
 }
+
+double dense_us(int64_t m, int64_t n, int64_t pitch, int packed) { return plan_dense(false, m, n, pitch, packed).us; }
 
 size_t dense_bytes(bool gated, int64_t m, int64_t n, int64_t pitch, int packed) {
   const DensePlan p = plan_dense(gated, m, n, pitch, packed);

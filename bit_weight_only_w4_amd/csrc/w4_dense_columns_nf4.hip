@@ -1,0 +1,13 @@
+// The dense product with columns of NF4 weights decoded on chip (w4_dense.h).
+#include "w4_dense.h"
+
+namespace w4 {
+
+hipError_t launch_dense_columns_nf4(int type, const DenseArgs& args, hipStream_t s) {
+  DenseArgs a = args;
+  const DensePlan p = plan_dense(false, a.m, a.n, a.pitch, kNF4);
+  if (!dense_prepare(p, &a)) return hipErrorInvalidValue;
+  return type == kDenseF16 ? dense_run<kDenseF16, false, kNF4>(p, a, s) : dense_run<kDenseBF16, false, kNF4>(p, a, s);
+}
+
+}  // namespace w4

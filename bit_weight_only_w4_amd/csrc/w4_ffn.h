@@ -11,7 +11,13 @@ enum DenseType { kDenseF16 = 0, kDenseBF16 = 1, kDenseI8 = 2 };
 struct DenseArgs {
   const uint8_t* a;  // [M, pitch] rows of operand bytes, 16-byte aligned
   const uint8_t* b;  // [N, pitch]; gated: [2 N, pitch], gate rows, then up rows
-  const float* scales;  // four bits: [rows of B, K / 64, 2] (w4_gated.hip); b then holds packed rows, four times shorter
+  // B in four bits: b holds packed weights.  Gated: B's rows, with the folded scales [rows, K / 64, 2] of w4_gated.hip.
+  // Without a gate: the weights [rows, N / 2] and their scales as they are, transposed; fp16 takes the exponent from parts.
+  const void* scales;
+  uint32_t rows;       // without a gate: weight rows, of which the last step of K may hold fewer than 64
+  const float* parts;  // maxima of the scales
+  uint32_t nparts;
+  int* exp_out;        // where the exponent goes, for dense_sum_kernel (`exp`)
   uint32_t m, n;     // outputs (gated: N is the width of h)
   uint32_t pitch;    // bytes of a row of either operand (its K elements), a multiple of 64, below 2^23
   const float* row_scale;   // 8 bits: s[m]
@@ -33,11 +39,19 @@ hipError_t launch_dense(int type, bool gated, const DenseArgs& a, hipStream_t s)
 // Scratch that a product of these sizes needs (its K split over workgroups): [splits, M, N or 2 N] of 4 bytes.
 // `packed`: the weight format of B in four bits, else -1.
 size_t dense_bytes(bool gated, int64_t m, int64_t n, int64_t pitch, int packed = -1);
+// The estimated time of a product without a gate, in microseconds.
+double dense_us(int64_t m, int64_t n, int64_t pitch, int packed);
 // The gated product with B in four bits: A fp16.
 hipError_t launch_dense_nf4(const DenseArgs& a, hipStream_t s);
 hipError_t launch_dense_fp4(const DenseArgs& a, hipStream_t s);
 hipError_t launch_dense_mxfp4(const DenseArgs& a, hipStream_t s);
 hipError_t launch_dense_int4(const DenseArgs& a, hipStream_t s);
+// The product with B transposed from four bits, of any format; A and the results fp16 or bf16.
+hipError_t launch_dense_columns_nf4(int type, const DenseArgs& a, hipStream_t s);
+hipError_t launch_dense_columns_fp4(int type, const DenseArgs& a, hipStream_t s);
+hipError_t launch_dense_columns_mxfp4(int type, const DenseArgs& a, hipStream_t s);
+hipError_t launch_dense_columns_int4(int type, const DenseArgs& a, hipStream_t s);
+hipError_t launch_dense_columns_int4a(int type, const DenseArgs& a, hipStream_t s);
 
 // ---- gated block over 4-bit weights
 bool gated_few(int fmt, int64_t tokens, int64_t hidden, int64_t inter);

@@ -1,12 +1,13 @@
 // Input gradient of a product with frozen 4-bit weights: dx[t, k] = sum_n d[t, n] W_hat[n, k].
 //
 // The sum runs over the weight rows, along which a packed byte holds nothing: the weights are decoded once into W_hat^T
-// rows of 16 bits in the workspace (through LDS), which the dense kernel multiplies with d.  Of 143 us for 2048 tokens of
-// INT4 17920 x 1536 the product takes 109 (1030 TFLOP/s), the sum of its five splits 12, decoding 22.  A weight is rounded
+// rows of 16 bits in the workspace (through LDS), which the dense kernel multiplies with d, or, where that costs less, the
+// dense kernel decodes and transposes them as they arrive (PackedColumns in w4_dense.h).  A weight is rounded
 // once to d's type (2^-8 of itself in bf16, 2^-11 in fp16; fp16 with one exponent for the whole matrix, taken from its
 // largest scale, so that neither large nor small weights leave its range).  Rows of W_hat^T are padded with zeros to whole
 // steps of the dense kernel, and so is d where its rows do not end on one or are not aligned.
 #include <algorithm>
+#include <type_traits>
 
 #include "w4_ffn.h"
 #include "w4_ffn_math.h"
@@ -18,9 +19,9 @@ constexpr int kTile = 64;       // weight rows of a tile
 constexpr int kMaxParts = 256;  // workgroups of the scale scan
 
 template <int FMT>
-__global__ void __launch_bounds__(256) scale_max_kernel(const void* scales, int64_t count, float* parts) {
+__device__ inline void scale_max(const void* scales, int64_t count, float* parts, uint32_t workgroups) {
   float top = 0.0f;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)workgroups * 256) {
     const float s = fabsf(scale_of<FMT>(scales, (size_t)i));
     top = s < __builtin_inff() ? fmaxf(top, s) : top;
   }
@@ -29,6 +30,34 @@ __global__ void __launch_bounds__(256) scale_max_kernel(const void* scales, int6
   if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = top;
   __syncthreads();
   if (threadIdx.x == 0) parts[blockIdx.x] = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
+}
+
+// A row of d, zeros after its end up to `np`.
+__device__ inline void pad_row(const uint16_t* from, uint16_t* to, uint32_t n, uint32_t np) {
+  for (uint32_t c = threadIdx.x * 8; c < np; c += 256 * 8) {
+    uint32_t v[4] = {0, 0, 0, 0};
+    if (c + 8 <= n) {
+      __builtin_memcpy(v, from + c, 16);
+    } else {
+#pragma unroll
+      for (uint32_t j = 0; j < 8; ++j)
+        if (c + j < n) v[j >> 1] |= (uint32_t)from[c + j] << (16 * (j & 1));
+    }
+    *reinterpret_cast<uint4*>(to + c) = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+// What the product that decodes the weights itself needs before it: the scales' maxima (fp16; `parts` workgroups), and d
+// with whole rows in the workgroups after those.
+template <int FMT>
+__global__ void __launch_bounds__(256) ready_kernel(const void* scales, int64_t count, float* maxima, uint32_t parts,
+                                                    const uint16_t* d, uint16_t* padded, uint32_t n, uint32_t np) {
+  if (blockIdx.x >= parts) {
+    const size_t t = blockIdx.x - parts;
+    pad_row(d + t * n, padded + t * np, n, np);
+    return;
+  }
+  scale_max<FMT>(scales, count, maxima, parts);
 }
 
 struct TransposeArgs {
@@ -58,16 +87,7 @@ __global__ void __launch_bounds__(256) transpose_kernel(TransposeArgs p) {
   const uint32_t tid = threadIdx.x;
   if (blockIdx.x >= p.tiles) {  // a row of d, zeros after its end
     const size_t t = blockIdx.x - p.tiles;
-    const uint16_t* from = p.d + t * p.n;
-    for (uint32_t c = tid * 8; c < p.np; c += 256 * 8) {
-      uint32_t v[4] = {0, 0, 0, 0};
-      if (c + 8 <= p.n) {
-        __builtin_memcpy(v, from + c, 16);
-      } else {
-        for (uint32_t j = 0; c + j < p.n; ++j) v[j >> 1] |= (uint32_t)from[c + j] << (16 * (j & 1));
-      }
-      *reinterpret_cast<uint4*>(p.padded + t * p.np + c) = make_uint4(v[0], v[1], v[2], v[3]);
-    }
+    pad_row(p.d + t * p.n, p.padded + t * p.np, p.n, p.np);
     return;
   }
   __shared__ float table[16];
@@ -131,19 +151,33 @@ uint32_t few_splits(int64_t n, int64_t k) {
 
 size_t up16(size_t v) { return (v + 15) & ~(size_t)15; }
 
+// Whether the product decodes and transposes the weights itself, by the estimates of both: it does so for every tile of up
+// to 256 tokens, and the workgroups of a split start with steps that only decode; the other way all weights are transposed
+// through memory once, 2.5 bytes each at 4 TB/s and a launch.  Microseconds, by the product / transposed first:
+//   FP4 bf16   17920 x 1536: 128 tokens 28 / 40, 512 53 / 64, 1000 88 / 84, 2048 131 / 135;  11008 x 4096: 128 33 / 58, 512
+//              76 / 104, 2048 217 / 179;  28672 x 4096: 80 54 / 134, 512 136 / 187, 2048 465 / 464;  4001 x 2048: 80 19 / 22, 333
+//              29 / 26;  4096 x 4096: 80 22 / 27, 512 38 / 36, 2048 90 / 72, 4096 128 / 118
+//   NF4 bf16   28672 x 4096: 80 60 / 132, 512 148 / 188, 2048 510 / 466;  4001 x 2048: 80 22 / 23, 333 30 / 26
+//   INT4 fp16  28672 x 4096: 80 59 / 152, 512 142 / 203, 2048 478 / 474;  17920 x 1536: 2048 133 / 142
+bool grad_columns(int fmt, int64_t n, int64_t k, int64_t b) {
+  const int64_t pitch = (n + kTile - 1) / kTile * kTile * 2;
+  return b <= 2048 && dense_us(b, k, pitch, fmt_weight(fmt)) < dense_us(b, k, pitch, -1) + 3 + (double)n * k * 2.5 / 4e6;
+}
+
 struct GradSpace {
   uint32_t np;
   size_t wt, d, parts, exp, partial, bytes;
 };
-GradSpace grad_space(int64_t n, int64_t k, int64_t b) {
+GradSpace grad_space(int fmt, int64_t n, int64_t k, int64_t b) {
   GradSpace g;
+  const bool columns = grad_columns(fmt, n, k, b);
   g.np = (uint32_t)((n + kTile - 1) / kTile * kTile);
   g.wt = 0;
-  g.d = up16((size_t)k * g.np * 2);
+  g.d = columns ? 0 : up16((size_t)k * g.np * 2);
   g.parts = g.d + up16((size_t)b * g.np * 2);
   g.exp = g.parts + kMaxParts * 4;
   g.partial = g.exp + 16;
-  g.bytes = g.partial + up16(dense_bytes(false, b, k, (int64_t)g.np * 2));
+  g.bytes = g.partial + up16(dense_bytes(false, b, k, (int64_t)g.np * 2, columns ? fmt_weight(fmt) : -1));
   return g;
 }
 
@@ -167,7 +201,8 @@ hipError_t prepare(int xt, const uint16_t* d, int64_t pad_rows, const uint8_t* p
   if (xt == kF16) {
     const int64_t count = n * (k / weights_per_scale<FMT>());
     p.nparts = (uint32_t)std::min<int64_t>(kMaxParts, (count + 1023) / 1024);
-    scale_max_kernel<FMT><<<dim3(p.nparts), dim3(256), 0, s>>>(scales, count, reinterpret_cast<float*>(ws + g.parts));
+    ready_kernel<FMT><<<dim3(p.nparts), dim3(256), 0, s>>>(scales, count, reinterpret_cast<float*>(ws + g.parts), p.nparts,
+                                                           nullptr, nullptr, 0, 0);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     transpose_kernel<FMT, kF16><<<grid, dim3(256), 0, s>>>(p);
   } else {
@@ -178,12 +213,12 @@ hipError_t prepare(int xt, const uint16_t* d, int64_t pad_rows, const uint8_t* p
 
 }  // namespace
 
-size_t gemm_grad_workspace(int, int64_t n, int64_t k, int64_t b) {
+size_t gemm_grad_workspace(int fmt, int64_t n, int64_t k, int64_t b) {
   if (b <= kFewTokens) {
     const uint32_t splits = few_splits(n, k);
     return splits > 1 ? up16((size_t)splits * (size_t)(b * k) * 4) : 0;
   }
-  return grad_space(n, k, b).bytes;
+  return grad_space(fmt, n, k, b).bytes;
 }
 
 hipError_t launch_gemm_grad(int fmt, const uint16_t* d, const uint8_t* packed, const void* scales, int64_t n, int64_t k,
@@ -196,23 +231,37 @@ hipError_t launch_gemm_grad(int fmt, const uint16_t* d, const uint8_t* packed, c
     return xt == kF16 ? launch_grad_few_f16(fmt_weight(fmt), f, splits, s)
                       : launch_grad_few_bf16(fmt_weight(fmt), f, splits, s);
   }
-  const GradSpace g = grad_space(n, k, b);
+  const GradSpace g = grad_space(fmt, n, k, b);
   uint8_t* base = reinterpret_cast<uint8_t*>(ws);
   const bool pad = (int64_t)g.np != n || (uintptr_t)d % 16;
   const int64_t pr = pad ? b : 0;
+  const bool columns = grad_columns(fmt, n, k, b);
+  uint32_t parts = 0;
+  auto ready = [&](auto format) {
+    constexpr int F = decltype(format)::value;
+    if (!columns) return prepare<F>(xt, d, pr, packed, scales, n, k, base, g, s);
+    const int64_t count = n * (k / weights_per_scale<F>());
+    parts = xt == kF16 ? (uint32_t)std::min<int64_t>(kMaxParts, (count + 1023) / 1024) : 0u;
+    if (parts + pr)
+      ready_kernel<F><<<dim3(parts + (uint32_t)pr), dim3(256), 0, s>>>(
+          scales, count, reinterpret_cast<float*>(base + g.parts), parts, d, reinterpret_cast<uint16_t*>(base + g.d),
+          (uint32_t)n, g.np);
+    return hipGetLastError();
+  };
+  using std::integral_constant;
   hipError_t e;
   switch (fmt_weight(fmt)) {
-    case kNF4: e = prepare<kNF4>(xt, d, pr, packed, scales, n, k, base, g, s); break;
-    case kINT4: e = prepare<kINT4>(xt, d, pr, packed, scales, n, k, base, g, s); break;
-    case kFP4: e = prepare<kFP4>(xt, d, pr, packed, scales, n, k, base, g, s); break;
-    case kINT4A: e = prepare<kINT4A>(xt, d, pr, packed, scales, n, k, base, g, s); break;
-    default: e = prepare<kMXFP4>(xt, d, pr, packed, scales, n, k, base, g, s); break;
+    case kNF4: e = ready(integral_constant<int, kNF4>{}); break;
+    case kINT4: e = ready(integral_constant<int, kINT4>{}); break;
+    case kFP4: e = ready(integral_constant<int, kFP4>{}); break;
+    case kINT4A: e = ready(integral_constant<int, kINT4A>{}); break;
+    default: e = ready(integral_constant<int, kMXFP4>{}); break;
   }
   if (e != hipSuccess) return e;
   if (pad) d = reinterpret_cast<const uint16_t*>(base + g.d);
   DenseArgs a{};
   a.a = reinterpret_cast<const uint8_t*>(d);
-  a.b = base + g.wt;
+  a.b = columns ? packed : base + g.wt;
   a.m = (uint32_t)b;
   a.n = (uint32_t)k;
   a.pitch = g.np * 2;
@@ -220,7 +269,20 @@ hipError_t launch_gemm_grad(int fmt, const uint16_t* d, const uint8_t* packed, c
   a.partial = reinterpret_cast<uint32_t*>(base + g.partial);
   a.out = dx;
   a.out_type = xt == kF16 ? 1 : 2;
-  return launch_dense(xt == kF16 ? kDenseF16 : kDenseBF16, false, a, s);
+  const int type = xt == kF16 ? kDenseF16 : kDenseBF16;
+  if (!columns) return launch_dense(type, false, a, s);
+  a.scales = scales;
+  a.rows = (uint32_t)n;
+  a.parts = reinterpret_cast<const float*>(base + g.parts);
+  a.nparts = parts;
+  a.exp_out = reinterpret_cast<int*>(base + g.exp);
+  switch (fmt_weight(fmt)) {
+    case kNF4: return launch_dense_columns_nf4(type, a, s);
+    case kINT4: return launch_dense_columns_int4(type, a, s);
+    case kFP4: return launch_dense_columns_fp4(type, a, s);
+    case kINT4A: return launch_dense_columns_int4a(type, a, s);
+    default: return launch_dense_columns_mxfp4(type, a, s);
+  }
 }
 
 }  // namespace w4

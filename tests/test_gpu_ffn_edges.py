@@ -555,3 +555,101 @@ def test_gated_nonfinite_scales(fmt, tokens):
     assert not torch.isfinite(pr.cpu()[:, ~good]).any()
     good = good[:inter] & good[inter:]
     f.check(h.cpu()[:, good], ref[:, good], eh[:, good])
+
+
+# ---- gradients whose product decodes and transposes the weights itself: large matrices, a sample of whose columns is compared
+
+def _raw_weights(fmt, n, k, seed):
+    """Random packed weights and scales on the GPU (of about 0.02 to 0.1), as the binding takes them."""
+    dev, weight = f.device(), fmt.split("_")[0]
+    g = torch.Generator(device=dev).manual_seed(seed)
+    p = torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, device=dev, generator=g)
+    if weight == "mxfp4":
+        return p, torch.randint(120, 124, (n, k // 32), dtype=torch.uint8, device=dev, generator=g)
+    s = torch.rand((n, k // (128 if weight.startswith("int4") else 64)), device=dev, generator=g) * 0.08 + 0.02
+    if weight in ("nf4", "fp4"):
+        return p, s
+    bits = s.bfloat16().view(torch.int16)
+    if weight == "int4":
+        return p, bits
+    zero = torch.randint(0, 16, bits.shape, dtype=torch.int32, device=dev, generator=g)
+    return p, bits.int() & 0xFFFF | zero << 16
+
+
+def _columns(fmt, p, s, blocks):
+    """fp64 values of the 128 columns of each of `blocks` (of 128), [n, 128 blocks]."""
+    weight = fmt.split("_")[0]
+    per = {"nf4": 2, "fp4": 2, "mxfp4": 4}.get(weight, 1)
+    out = []
+    for b in blocks:
+        sc = s[:, b * per:(b + 1) * per].contiguous().cpu().numpy()
+        sc = sc.view({"int4": np.uint16, "int4a": np.uint32}.get(weight, sc.dtype))
+        out.append(f.as_operands(fmt, p[:, 64 * b:64 * (b + 1)].contiguous().cpu().numpy(), sc)[2])
+    at = torch.cat([torch.arange(128 * b, 128 * b + 128) for b in blocks])
+    return torch.cat(out, 1), at
+
+
+@pytest.mark.parametrize("fmt", f.FMTS)
+@pytest.mark.parametrize("tokens,n,k", [(65, 8003, 2176), (130, 28000, 1152), (512, 20000, 1664), (333, 11008, 4224),
+                                        (1000, 28672, 4224), (2000, 28000, 4224)])
+def test_gemm_grad_decoded_in_the_product(fmt, tokens, n, k):
+    """Weight rows that end inside a step, an odd number of groups a row (scales on odd halves of a word), columns that end
+    inside a tile, each tile, one and several splits."""
+    w4, dev, dtype = _w4(), f.device(), f.DTYPES[fmt.split("_")[1]]
+    p, s = _raw_weights(fmt, n, k, tokens)
+    d = f.normal((tokens, n), dtype, 3, 0.3)
+    dx = f.Guarded((tokens, k), dtype, dev)
+    w4.gemm_grad(d.to(dev), p, s, fmt, dx=dx.t)
+    torch.cuda.synchronize()
+    assert dx.whole()
+    hat, at = _columns(fmt, p, s, [0, k // 256, k // 128 - 1])
+    few = torch.arange(0, tokens, max(1, tokens // 97))
+    ref, e = f.grad_bound(d[few], hat)
+    f.check(dx.t.cpu()[few][:, at], ref, e)
+    assert torch.isfinite(dx.t).all()
+    again = w4.gemm_grad(d.to(dev), p, s, fmt)
+    assert torch.equal(again, dx.t)
+
+
+@pytest.mark.parametrize("fmt", ["nf4_f16", "fp4_bf16", "int4_f16", "int4a_bf16", "mxfp4_f16", "mxfp4_bf16"])
+def test_gemm_grad_decoded_in_the_product_nonfinite(fmt):
+    """Infinite and NaN gradients stay in their tokens, non-finite scales in their blocks' columns."""
+    w4, dev, dtype = _w4(), f.device(), f.DTYPES[fmt.split("_")[1]]
+    weight, n, k = fmt.split("_")[0], 9001, 1152
+    p, s = _raw_weights(fmt, n, k, 5)
+    d = _poison(f.normal((100, n), dtype, 6, 0.2), [0, 20, 63, 64])
+    dx = w4.gemm_grad(d.to(dev), p, s, fmt).cpu()
+    bad = ~torch.isfinite(d).all(1)
+    hat, at = _columns(fmt, p, s, [0, 8])
+    for t in bad.nonzero().flatten().tolist():  # what an infinity or NaN meets decides: every other term is finite
+        odd = ~torch.isfinite(d[t])
+        ref = (d[t, odd].double().unsqueeze(1) * hat[odd]).sum(0)
+        f.assert_like(dx[t:t + 1, at], ref.unsqueeze(0))
+    ref, e = f.grad_bound(d[~bad], hat)
+    f.check(dx[~bad][:, at], ref, e)
+    raw = s.view({"mxfp4": torch.uint8, "int4": torch.int16}.get(weight, torch.int32))
+    raw[7000, 2] = {"mxfp4": 255, "int4": 0x7FC0, "int4a": 0x7F80}.get(weight, 0x7F800000)
+    raw[9000, raw.shape[1] - 1] = {"mxfp4": 255, "int4": 0x7F80, "int4a": 0x7FC0}.get(weight, 0x7FC00000)
+    d = torch.where(d == 0, torch.ones_like(d), d)
+    dx = w4.gemm_grad(d.to(dev), p, s, fmt).cpu()[~bad]
+    g = k // raw.shape[1]
+    hit = torch.zeros(k, dtype=torch.bool)
+    hit[2 * g:3 * g], hit[k - g:] = True, True
+    assert not torch.isfinite(dx[:, hit]).any() and torch.isfinite(dx[:, ~hit]).all()
+
+
+@pytest.mark.parametrize("xt", ["f16", "bf16"])
+@pytest.mark.parametrize("scale", [2.0 ** -40, 2.0 ** 20])
+def test_gemm_grad_decoded_in_the_product_beyond_fp16(xt, scale):
+    w4, dev, dtype, fmt = _w4(), f.device(), f.DTYPES[xt], f"nf4_{xt}"
+    p, s = _raw_weights(fmt, 9000, 1152, 8)
+    s = s * scale
+    d = (f.normal((80, 9000), torch.float64, 9, 0.3) / (scale if xt == "bf16" else 2.0 ** 14 if scale > 1 else 1)).to(dtype)
+    dx = w4.gemm_grad(d.to(dev), p, s, fmt).cpu()
+    hat, at = _columns(fmt, p, s, [0, 8])
+    ref, e = f.grad_bound(d, hat)
+    if xt == "bf16" or scale < 1:
+        f.check(dx[:, at], ref, e)
+    else:
+        inside = ref.abs() + e < 65504
+        assert inside.any() and bool(((dx[:, at].double() - ref).abs() <= e)[inside].all())
