@@ -135,9 +135,15 @@ __global__ void __launch_bounds__(256) transpose_kernel(TransposeArgs p) {
   }
 }
 
-// Up to here the packed weights are decoded in registers (w4_grad_few.h).  Microseconds at 64 tokens there, at 65 here:
-// NF4 bf16 1536 x 8960 20.7 / 28, INT4 fp16 17920 x 1536 26.3 / 38.8.
-constexpr int kFewTokens = 64;
+// How many tokens take the packed weights decoded in registers (w4_grad_few.h).  Microseconds there / by the dense kernel
+// decoding them itself:  32 tokens FP4 bf16 4096 x 4096 15.8 / 15.5, 28672 x 4096 41 / 47, 896 x 4864 11.3 / 15.5; INT4 fp16 19.1
+// / 19.3, 60 / 55, 12.8 / 19.7.  64 tokens 19.9 / 17.9, 49 / 51, 15.9 / 15.6; INT4 fp16 26 / 22, 76 / 58, 18 / 20.  fp16 with NF4 or
+// FP4 goes on to 64, though up to 15% slower there (NF4 28672 x 4096 80 / 69, 4096 x 4096 26 / 25): two terms keep their
+// weights to 2^-16, the other way they are rounded to 2^-11.
+int64_t few_tokens(int fmt) {
+  const int w = fmt_weight(fmt);
+  return fmt_xtype(fmt) == kF16 && (w == kNF4 || w == kFP4) ? 64 : 32;
+}
 
 // Splits of N for a few tokens: as many as give every CU a workgroup of 128 columns, each at least a step of 32 rows
 // for each of its eight waves.  Twice and half as many took 15.2 and 15.2 us for 16 tokens of NF4 1536 x 8960 (12.8 so),
@@ -214,7 +220,7 @@ hipError_t prepare(int xt, const uint16_t* d, int64_t pad_rows, const uint8_t* p
 }  // namespace
 
 size_t gemm_grad_workspace(int fmt, int64_t n, int64_t k, int64_t b) {
-  if (b <= kFewTokens) {
+  if (b <= few_tokens(fmt)) {
     const uint32_t splits = few_splits(n, k);
     return splits > 1 ? up16((size_t)splits * (size_t)(b * k) * 4) : 0;
   }
@@ -224,7 +230,7 @@ size_t gemm_grad_workspace(int fmt, int64_t n, int64_t k, int64_t b) {
 hipError_t launch_gemm_grad(int fmt, const uint16_t* d, const uint8_t* packed, const void* scales, int64_t n, int64_t k,
                             int64_t b, uint16_t* dx, void* ws, hipStream_t s) {
   const int xt = fmt_xtype(fmt);
-  if (b <= kFewTokens) {
+  if (b <= few_tokens(fmt)) {
     const uint32_t splits = few_splits(n, k), steps = (uint32_t)((n + 31) / 32);
     const GradFewArgs f{d, packed, scales, dx, splits > 1 ? reinterpret_cast<float*>(ws) : nullptr,
                         (uint32_t)n, (uint32_t)k, (uint32_t)b, (steps + splits - 1) / splits};

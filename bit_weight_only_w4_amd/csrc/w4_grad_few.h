@@ -251,8 +251,10 @@ hipError_t grad_few_launch(const GradFewArgs& a, uint32_t splits, hipStream_t s)
     grad_few_kernel<FMT, XT, 1><<<grid, block, 0, s>>>(a);
   else if (a.b <= 32)
     grad_few_kernel<FMT, XT, 2><<<grid, block, 0, s>>>(a);
-  else
+  else if constexpr (XT == kF16 && (FMT == kNF4 || FMT == kFP4))  // up to 64
     grad_few_kernel<FMT, XT, 4><<<grid, block, 0, s>>>(a);
+  else
+    return hipErrorInvalidValue;
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
   const int64_t count = (int64_t)a.b * a.k;

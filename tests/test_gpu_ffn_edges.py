@@ -653,3 +653,21 @@ def test_gemm_grad_decoded_in_the_product_beyond_fp16(xt, scale):
     else:
         inside = ref.abs() + e < 65504
         assert inside.any() and bool(((dx[:, at].double() - ref).abs() <= e)[inside].all())
+
+
+@pytest.mark.parametrize("fmt", f.FMTS)
+@pytest.mark.parametrize("tokens", [31, 32, 33, 49, 64, 65])
+def test_gemm_grad_around_the_last_few_tokens(fmt, tokens):
+    _grad_case(fmt, tokens, 330, 3 * f.group(fmt), seed=tokens)
+
+
+@pytest.mark.parametrize("fmt", ["nf4_bf16", "int4_f16", "int4_bf16", "fp4_bf16", "int4a_f16", "mxfp4_f16", "mxfp4_bf16"])
+@pytest.mark.parametrize("tokens", [33, 48])
+def test_gemm_grad_decoded_in_the_product_few(fmt, tokens):
+    w4, dev, dtype = _w4(), f.device(), f.DTYPES[fmt.split("_")[1]]
+    p, s = _raw_weights(fmt, 9537, 1152, tokens)
+    d = f.normal((tokens, 9537), dtype, 3, 0.3)
+    dx = w4.gemm_grad(d.to(dev), p, s, fmt)
+    hat, at = _columns(fmt, p, s, [0, 4, 8])
+    ref, e = f.grad_bound(d, hat)
+    f.check(dx[:, at.to(dev)], ref, e)
