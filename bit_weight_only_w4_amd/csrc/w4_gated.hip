@@ -16,11 +16,6 @@ namespace w4 {
 namespace {
 
 constexpr int kDecodeThreads = 256;
-// Up to here the weights are streamed past the tokens and decoded in registers (run_gated_few).  Microseconds against
-// the dense kernel: 64 tokens NF4 1536 -> 8960 21 / 32, 4096 -> 14336 INT4 53 / 115; 128 tokens NF4 42 / 41, 91 / 132, INT4
-// 31 / 37, 71 / 138, MXFP4 41 / 37, 92 / 140; 192 tokens (a second pass) NF4 78 / 39, INT4 57 / 38, 132 / 143.
-constexpr int kFewTokens = 128;
-
 struct DecodeArgs {
   const uint8_t* packed;  // [N, K/2]
   const void* scales;
@@ -251,9 +246,22 @@ hipError_t grad_launch(const uint16_t* dh, const uint16_t* pr, uint16_t* dp, int
 
 }  // namespace
 
-// Whether the weights are streamed once and decoded on chip (no workspace).
+// Whether the weights are streamed once past the tokens and decoded in registers (run_gated_few; no workspace).  Microseconds
+// so / by the dense kernel:
+//          1536 -> 8960   4096 -> 11008  8192 -> 28672 |            1536 -> 8960   4096 -> 11008  8192 -> 28672
+//   64 tokens                                          | 128 tokens
+//   INT4    19 / 25        51 / 57       143 / 170     |   INT4      31 / 33        69 / 61       257 / 208
+//   FP4     19 / 24        53 / 56       150 / 171     |   FP4       38 / 32        77 / 61       288 / 211
+//   NF4     22 / 30        61 / 67       187 / 195     |   NF4       42 / 39        88 / 67       328 / 228
+//   MXFP4   21 / 22        64 / 51       180 / 157     |   MXFP4     41 / 29        93 / 60       341 / 189
+// and 896 -> 4864 with 128 tokens 15 / 17, 15 / 17, 18 / 20, 19 / 15.  fp16 with NF4 or FP4 is streamed up to 128 whatever the
+// size: it keeps the weights in two terms or scales their sums, where the dense kernel rounds them to 2^-11.
 bool gated_few(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
-  return tokens <= kFewTokens && gated_mfma_fits(fmt, inter, hidden, tokens);
+  const int w = fmt_weight(fmt);
+  const bool inexact = fmt_xtype(fmt) == kF16 && (w == kNF4 || w == kFP4);
+  const int64_t large = w == kMXFP4 ? 0 : w == kNF4 || w == kFP4 ? (int64_t)1 << 24 : (int64_t)1 << 25;
+  const int64_t most = !inexact && 2 * inter * hidden >= large ? 64 : 128;
+  return tokens <= most && gated_mfma_fits(fmt, inter, hidden, tokens);
 }
 
 size_t gated_workspace(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {

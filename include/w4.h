@@ -608,13 +608,13 @@ typedef enum { W4_F32 = 0, W4_F16 = 1, W4_BF16 = 2 } w4_type_t;
  *   workspace device memory of at least w4_gated_workspace_bytes(...) bytes, 16-byte aligned; may be NULL when
  *             that is 0; scratch on entry and exit; two calls in flight must not share it
  * No output may overlap an input, the other output or the workspace, nor the workspace an input.  fp32
- * accumulation, g and u rounded to x's type for `products` alone.  Where a workspace is needed (from 129 tokens
- * on) the weights enter as fp16 numbers of a common exponent a row (at most 2^-11 of themselves off; INT4 and MXFP4 exact) and bf16 tokens as fp16
- * numbers of a common exponent a token (exact), in both what lies more than 2^29 below the row's largest by at most
- * 2^-39 of that.  Infinities and NaN stay in their token's (a scale's: in its channel's) results, where the formula
- * has them; an infinite token of asymmetric INT4 up to 128 tokens gives NaN for some of its infinite products (its
- * zero points are taken off as z times the token's sum), as it does for a weight that became 0 under its row's
- * exponent.  The order of every sum is fixed.  Asynchronous on `stream`. */
+ * accumulation, g and u rounded to x's type for `products` alone.  Where a workspace is needed (from 65 or 129
+ * tokens on) the weights enter as fp16 numbers of a common exponent a row (at most 2^-11 of themselves off; INT4 and
+ * MXFP4 exact) and bf16 tokens as fp16 numbers of a common exponent a token (exact), in both what lies more than
+ * 2^29 below the row's largest by at most 2^-39 of that.  Infinities and NaN stay in their token's (a scale's: in its channel's) results, where the formula
+ * has them; without a workspace an infinite token of asymmetric INT4 gives NaN for some of its infinite products (its
+ * zero points are taken off as z times the token's sum), with one any does for a weight that became 0 under its
+ * row's exponent.  The order of every sum is fixed.  Asynchronous on `stream`. */
 int w4_gated(const void* x, const uint8_t* gate_up, const void* gate_up_scales, int fmt, int act, int64_t tokens,
              int64_t hidden, int64_t inter, void* h, void* products, void* workspace, size_t workspace_bytes,
              void* stream);

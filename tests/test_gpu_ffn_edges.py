@@ -671,3 +671,21 @@ def test_gemm_grad_decoded_in_the_product_few(fmt, tokens):
     hat, at = _columns(fmt, p, s, [0, 4, 8])
     ref, e = f.grad_bound(d, hat)
     f.check(dx[:, at.to(dev)], ref, e)
+
+
+@pytest.mark.parametrize("fmt", f.FMTS)
+@pytest.mark.parametrize("tokens", [64, 65, 128, 129])
+@pytest.mark.parametrize("steps,inter", [(1, 70), (8, 17000)])
+def test_gated_around_the_last_few_tokens(fmt, tokens, steps, inter):
+    """Small and large matrices (of which a sample of channels is compared)."""
+    w4, dev, dtype = _w4(), f.device(), f.DTYPES[fmt.split("_")[1]]
+    hidden = steps * 128
+    p, s = _raw_weights(fmt, 2 * inter, hidden, tokens)
+    x = f.normal((tokens, hidden), dtype, 3)
+    h, pr = w4.gated(x.to(dev), p, s, fmt, "silu", save=True)
+    at = torch.cat((torch.arange(0, inter, max(1, inter // 37)), torch.tensor([inter - 1])))
+    rows = torch.cat((at, at + inter)).to(dev)
+    hat, _ = _columns(fmt, p[rows], s[rows], range(steps))
+    ref, eh, both, ep = f.gated_bound(x, hat, "silu", dtype)
+    f.check(pr[:, rows], both, ep)
+    f.check(h[:, at.to(dev)], ref, eh)
