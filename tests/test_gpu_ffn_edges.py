@@ -689,3 +689,68 @@ def test_gated_around_the_last_few_tokens(fmt, tokens, steps, inter):
     ref, eh, both, ep = f.gated_bound(x, hat, "silu", dtype)
     f.check(pr[:, rows], both, ep)
     f.check(h[:, at.to(dev)], ref, eh)
+
+
+@pytest.mark.parametrize("fmt", ["nf4_f16", "int4_bf16", "mxfp4_f16"])
+def test_gemm_grad_decoded_in_the_product_in_graphs_and_streams(fmt):
+    """Captured and replayed with new inputs; two calls at once; a dirty workspace of the stated size, and none other."""
+    w4, dev, dtype = _w4(), f.device(), f.DTYPES[fmt.split("_")[1]]
+    tokens, n, k = 90, 9001, 1152
+    p, s = _raw_weights(fmt, n, k, 7)
+    d = [f.normal((tokens, n), dtype, 3 + i, 0.3).to(dev) for i in range(2)]
+    want = [w4.gemm_grad(x, p, s, fmt) for x in d]
+    size = w4.gemm_grad_workspace_bytes(fmt, n, k, tokens)
+    ws = [torch.full((size + 64,), 0xFF, dtype=torch.uint8, device=dev) for _ in d]
+    streams = [torch.cuda.Stream() for _ in d]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = [w4.gemm_grad(x, p, s, fmt, workspace=w[:size], stream=st) for x, w, st in zip(d, ws, streams)]
+        torch.cuda.synchronize()
+        for a, b, w in zip(got, want, ws):
+            assert torch.equal(a, b) and bool((w[size:] == 0xFF).all())
+    with pytest.raises(w4.W4Error):
+        w4.gemm_grad(d[0], p, s, fmt, workspace=ws[0][:size - 16])
+    x = d[0].clone()
+    w4.gemm_grad(x, p, s, fmt)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = w4.gemm_grad(x, p, s, fmt)
+    for i in (1, 0, 1):
+        x.copy_(d[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i])
+        w4.gemm_grad(d[i], p, s, fmt)
+        torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fmt", ["nf4_bf16", "mxfp4_f16", "int4a_bf16", "fp4_f16"])
+def test_gated_decoded_in_the_product_in_graphs_and_streams(fmt):
+    w4, dev, dtype = _w4(), f.device(), f.DTYPES[fmt.split("_")[1]]
+    tokens, hidden, inter = 200, 1024, 1500
+    p, s = _raw_weights(fmt, 2 * inter, hidden, 7)
+    xs = [f.normal((tokens, hidden), dtype, 3 + i).to(dev) for i in range(2)]
+    want = [w4.gated(x, p, s, fmt, save=True) for x in xs]
+    size = w4.gated_workspace_bytes(fmt, tokens, hidden, inter)
+    assert 0 < size < 2 * inter * hidden * 2
+    ws = [torch.full((size + 64,), 0xFF, dtype=torch.uint8, device=dev) for _ in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = [w4.gated(x, p, s, fmt, save=True, workspace=w[:size], stream=st) for x, w, st in zip(xs, ws, streams)]
+        torch.cuda.synchronize()
+        for a, b, w in zip(got, want, ws):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and bool((w[size:] == 0xFF).all())
+    x = xs[0].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = w4.gated(x, p, s, fmt)
+    for i in (1, 0, 1):
+        x.copy_(xs[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i][0])
+        w4.gated(xs[i], p, s, fmt)
+        torch.cuda.synchronize()
