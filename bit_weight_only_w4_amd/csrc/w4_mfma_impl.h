@@ -219,9 +219,9 @@ mfma_kernel(typename std::conditional<GATED, MfmaGatedArgs, MfmaArgs>::type a) {
     const uint32_t rows = rows_left >= 16u ? 16u : rows_left;
     c.rw = make_rsrc(mm.packed + (size_t)row_base * pitch, rows * pitch);
     const char* sp = reinterpret_cast<const char*>(mm.scales) + (size_t)row_base * spitch;
-    if constexpr (kMX) {  // whole dwords
+    if constexpr (kMX) {  // whole dwords; of no rows none (a tile past the stream lies outside the scales)
       c.odd = (uint32_t)(reinterpret_cast<uintptr_t>(sp) & 2u);
-      c.rs = make_rsrc(sp - c.odd, (rows * spitch + c.odd + 3u) & ~3u);
+      c.rs = make_rsrc(sp - c.odd, rows ? (rows * spitch + c.odd + 3u) & ~3u : 0u);
     } else {
       c.rs = make_rsrc(sp, rows * spitch);
     }

@@ -754,3 +754,33 @@ def test_gated_decoded_in_the_product_in_graphs_and_streams(fmt):
         assert torch.equal(out, want[i][0])
         w4.gated(xs[i], p, s, fmt)
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("xt", ["f16", "bf16"])
+@pytest.mark.parametrize("tokens,hidden,inter", [(2, 64, 1), (16, 6720, 781), (16, 192, 4801), (33, 448, 15), (64, 1600, 129),
+                                                 (128, 320, 33)])
+def test_gated_mxfp4_up_scales_inside_a_dword(xt, tokens, hidden, inter):
+    """An odd number of channels times an odd number of 64-weight blocks: the up rows' scales start two bytes into a dword,
+    and the tiles asked for ahead end past them."""
+    _gated_case(f"mxfp4_{xt}", tokens, hidden, inter, "silu", seed=inter)
+
+
+@pytest.mark.parametrize("tokens", [2, 16, 40, 128])
+def test_grouped_mxfp4_scales_inside_a_dword(tokens):
+    """The grouped small-batch product over members whose scales start two bytes into a dword, ragged row counts."""
+    w4, dev, fmt, k = _w4(), f.device(), "mxfp4_f16", 320
+    x = f.normal((tokens, k), torch.float16, 3).to(dev)
+    packed, scales, hats = [], [], []
+    for i, n in enumerate((17, 783, 5)):
+        p, s, hat = f.weights(fmt, n, k, 40 + i)
+        flat = torch.zeros(s.numel() + 8, dtype=torch.uint8, device=dev)
+        flat[2:2 + s.numel()] = s.to(dev).flatten()
+        packed.append(p.to(dev))
+        scales.append(flat[2:2 + s.numel()].view(s.shape))
+        hats.append(hat)
+    ys = w4.gemm_smallbatch_grouped(x, packed, scales, fmt)
+    torch.cuda.synchronize()
+    for y, hat in zip(ys, hats):
+        ref = x.cpu().double() @ hat.t()
+        bound = 2.0 ** -11 * (x.cpu().double().abs() @ hat.t().abs()) + 1e-6
+        assert ((y.cpu().double() - ref).abs() <= bound).all()
