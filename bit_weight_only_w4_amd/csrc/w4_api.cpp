@@ -1302,6 +1302,15 @@ hipError_t run_gated_few(int fmt, int act, const uint16_t* x, const uint8_t* pac
   GemvPlan p;
   if (tokens > 1 || !plan_gemv(2 * inter, hidden, 1, 1, &p) || p.iters > 3)
     return launch_gated_mfma(fmt, a, hidden, tokens, s);
+  // Pairs of rows change how many workgroups serve best.  Two chunks a lane: one per CU (4096 -> 11008 NF4 17.3 to 15.1 us,
+  // INT4 15.4 to 13.5, MXFP4 15.0 to 13.0; with three chunks 5120 -> 13824 would go from 22.9 to 26.1).  Large matrices,
+  // whose plan has one per CU, with a table and teams of two waves and more: twice as many (8192 -> 28672 NF4 60 to 52, INT4
+  // 55 to 48; 4096 -> 28672, teams of a wave, 29 to 31; without a table MXFP4 46 to 49).
+  const int cus = (int)device_cu_count(), w = fmt_weight(fmt);
+  if (p.cap > cus)
+    p.cap = p.iters == 2 ? cus : p.cap;
+  else if (p.team >= 128 && w != kFP4 && w != kMXFP4)
+    p.cap = 2 * p.cap;
   const int64_t per = p.threads / p.team, blocks = (inter + per - 1) / per;
   const int64_t grid = std::min<int64_t>(blocks, p.cap);
   a.m[0].nrb = (uint32_t)blocks;
