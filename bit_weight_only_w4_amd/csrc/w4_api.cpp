@@ -1282,8 +1282,8 @@ int gated_shape(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
 }
 
 // w4_gated in one launch: the fused GEMV for one token where it has a launch shape, else the MFMA kernel.  (One token with
-// the one and the other, us: NF4 1536 -> 8960 7.7 / 10.3, 4096 -> 14336 18.7 / 25.5, 512 -> 256 3.6 / 4.8; INT4 6.8 / 9.6, 16.5 /
-// 19.4; MXFP4 7.0 / 11.9, 16.2 / 25.7.)
+// the one and the other, us: NF4 1536 -> 8960 7.7 / 10.3, 4096 -> 14336 17.2 / 25.5, 512 -> 256 3.6 / 4.8; INT4 6.7 / 9.6, 15.3 /
+// 19.4; MXFP4 6.5 / 11.9, 15.2 / 25.7.)
 hipError_t run_gated_few(int fmt, int act, const uint16_t* x, const uint8_t* packed, const void* scales, int64_t tokens,
                          int64_t hidden, int64_t inter, uint16_t* h, uint16_t* products, hipStream_t s) {
   GemvGatedArgs a;
