@@ -287,7 +287,8 @@ hipError_t launch_gated(int fmt, int act, const uint16_t* x, const uint8_t* pack
   d.t = (uint32_t)tokens;
   const bool fold = gated_packed(fmt, tokens);
   const uint32_t per = kDecodeThreads / 64, token_rows = convert ? d.t : 0;
-  const dim3 grid(fold ? (token_rows + per - 1) / per + (d.n + kFoldRows - 1) / kFoldRows : (d.n + token_rows + per - 1) / per);
+  const dim3 grid(fold ? (token_rows + per - 1) / per + (d.n + kFoldRows - 1) / kFoldRows
+                       : (d.n + token_rows + per - 1) / per);
   auto decode = [&](auto format) {
     constexpr int F = decltype(format)::value;
     if (fold)

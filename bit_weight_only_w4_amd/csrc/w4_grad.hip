@@ -2,7 +2,7 @@
 //
 // The sum runs over the weight rows, along which a packed byte holds nothing: the weights are decoded once into W_hat^T
 // rows of 16 bits in the workspace (through LDS), which the dense kernel multiplies with d, or, where that costs less, the
-// dense kernel decodes and transposes them as they arrive (PackedColumns in w4_dense.h).  A weight is rounded
+// dense kernel decodes and transposes them as they arrive (PackedColumns in w4_dense_sources.h).  A weight is rounded
 // once to d's type (2^-8 of itself in bf16, 2^-11 in fp16; fp16 with one exponent for the whole matrix, taken from its
 // largest scale, so that neither large nor small weights leave its range).  Rows of W_hat^T are padded with zeros to whole
 // steps of the dense kernel, and so is d where its rows do not end on one or are not aligned.
@@ -135,11 +135,15 @@ __global__ void __launch_bounds__(256) transpose_kernel(TransposeArgs p) {
   }
 }
 
-// How many tokens take the packed weights decoded in registers (w4_grad_few.h).  Microseconds there / by the dense kernel
-// decoding them itself:  32 tokens FP4 bf16 4096 x 4096 15.8 / 15.5, 28672 x 4096 41 / 47, 896 x 4864 11.3 / 15.5; INT4 fp16 19.1
-// / 19.3, 60 / 55, 12.8 / 19.7.  64 tokens 19.9 / 17.9, 49 / 51, 15.9 / 15.6; INT4 fp16 26 / 22, 76 / 58, 18 / 20.  fp16 with NF4 or
-// FP4 goes on to 64, though up to 15% slower there (NF4 28672 x 4096 80 / 69, 4096 x 4096 26 / 25): two terms keep their
-// weights to 2^-16, the other way they are rounded to 2^-11.
+// How many tokens take the packed weights decoded in registers (w4_grad_few.h).  Microseconds there / by the dense
+// kernel decoding them itself:
+//                   4096 x 4096   28672 x 4096   896 x 4864
+//   32  FP4 bf16    15.8 / 15.5     41 / 47     11.3 / 15.5
+//       INT4 fp16   19.1 / 19.3     60 / 55     12.8 / 19.7
+//   64  FP4 bf16    19.9 / 17.9     49 / 51     15.9 / 15.6
+//       INT4 fp16   26.0 / 21.8     76 / 58     18.2 / 20.0
+// fp16 with NF4 or FP4 goes on to 64, though up to 15% slower there (NF4 28672 x 4096 80 / 69, 4096 x 4096 26 / 25): two
+// terms keep their weights to 2^-16, the other way they are rounded to 2^-11.
 int64_t few_tokens(int fmt) {
   const int w = fmt_weight(fmt);
   return fmt_xtype(fmt) == kF16 && (w == kNF4 || w == kFP4) ? 64 : 32;
@@ -160,9 +164,10 @@ size_t up16(size_t v) { return (v + 15) & ~(size_t)15; }
 // Whether the product decodes and transposes the weights itself, by the estimates of both: it does so for every tile of up
 // to 256 tokens, and the workgroups of a split start with steps that only decode; the other way all weights are transposed
 // through memory once, 2.5 bytes each at 4 TB/s and a launch.  Microseconds, by the product / transposed first:
-//   FP4 bf16   17920 x 1536: 128 tokens 28 / 40, 512 53 / 64, 1000 88 / 84, 2048 131 / 135;  11008 x 4096: 128 33 / 58, 512
-//              76 / 104, 2048 217 / 179;  28672 x 4096: 80 54 / 134, 512 136 / 187, 2048 465 / 464;  4001 x 2048: 80 19 / 22, 333
-//              29 / 26;  4096 x 4096: 80 22 / 27, 512 38 / 36, 2048 90 / 72, 4096 128 / 118
+//   FP4 bf16   17920 x 1536: 128 tokens 28 / 40, 512 53 / 64, 1000 88 / 84, 2048 131 / 135
+//              11008 x 4096: 128 33 / 58, 512 76 / 104, 2048 217 / 179
+//              28672 x 4096: 80 54 / 134, 512 136 / 187, 2048 465 / 464
+//              4001 x 2048: 80 19 / 22, 333 29 / 26;  4096 x 4096: 80 22 / 27, 512 38 / 36, 2048 90 / 72, 4096 128 / 118
 //   NF4 bf16   28672 x 4096: 80 60 / 132, 512 148 / 188, 2048 510 / 466;  4001 x 2048: 80 22 / 23, 333 30 / 26
 //   INT4 fp16  28672 x 4096: 80 59 / 152, 512 142 / 203, 2048 478 / 474;  17920 x 1536: 2048 133 / 142
 bool grad_columns(int fmt, int64_t n, int64_t k, int64_t b) {
