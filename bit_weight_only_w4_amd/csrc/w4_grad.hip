@@ -138,8 +138,8 @@ __global__ void __launch_bounds__(256) transpose_kernel(TransposeArgs p) {
 // How many tokens take the packed weights decoded in registers (w4_grad_few.h).  Microseconds there / by the dense
 // kernel decoding them itself:
 //                   4096 x 4096   28672 x 4096   896 x 4864
-//   32  FP4 bf16    15.8 / 15.5     41 / 47     11.3 / 15.5
-//       INT4 fp16   19.1 / 19.3     60 / 55     12.8 / 19.7
+//   32  FP4 bf16    14.0 / 15.5     37 / 47     10.7 / 15.5
+//       INT4 fp16   18.0 / 19.3     58 / 55     12.6 / 19.7
 //   64  FP4 bf16    19.9 / 17.9     49 / 51     15.9 / 15.6
 //       INT4 fp16   26.0 / 21.8     76 / 58     18.2 / 20.0
 // fp16 with NF4 or FP4 goes on to 64, though up to 15% slower there (NF4 28672 x 4096 80 / 69, 4096 x 4096 26 / 25): two
@@ -150,8 +150,8 @@ int64_t few_tokens(int fmt) {
 }
 
 // Splits of N for a few tokens: as many as give every CU a workgroup of 128 columns, each at least a step of 32 rows
-// for each of its eight waves.  Twice and half as many took 15.2 and 15.2 us for 16 tokens of NF4 1536 x 8960 (12.8 so),
-// 29.2 and 22.9 for 64 (20.7).
+// for each of its eight waves.  16 tokens of NF4 1536 x 8960 take 11.5 us, with twice and half as many splits 13.8 and 14.9;
+// 17920 x 1536 18.9, 24.3, 21.0; 28672 x 4096 37, 39, 58.
 uint32_t few_splits(int64_t n, int64_t k) {
   const int64_t groups = (k + 127) / 128, rounds = ((n + 31) / 32 + 7) / 8;
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(rounds, device_cu_count() / groups));

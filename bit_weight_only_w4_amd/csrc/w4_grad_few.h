@@ -13,7 +13,7 @@
 //     decoded rows of the other path).  fp16 d: d as the sum of two bf16 numbers (exact), the weight as the sum of two
 //     (2^-16), three products; bf16 has fp32's range, so no common exponent is needed.
 //   * Bound by the chain of loads, decoding and products of a few steps and by the splits' sums on their way through
-//     memory: 16 tokens of NF4 1536 x 8960 10 us (0.8 TB/s) and 2.5 for the sum.
+//     memory: 16 tokens of NF4 1536 x 8960 9 us (0.9 TB/s) and 2.5 for the sum (28672 x 4096 37 us in all, 1.8 TB/s).
 //   * The waves' sums are added in LDS, the splits' by a second kernel, both in a fixed order.
 #pragma once
 #include <type_traits>
@@ -39,12 +39,16 @@ __global__ void __launch_bounds__(64 * kGradWaves) grad_few_kernel(GradFewArgs p
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, m = lane & 15;
-  const uint32_t k0 = blockIdx.x * 128u, k = p.k, n = p.n, pitch = k / 2;
+  // Every eighth workgroup runs on one XCD: those take neighbouring columns, whose 64 bytes of a row share cache lines
+  // (16 tokens FP4 28672 x 4096 37.5 to 32.6 us, 17920 x 1536 19.0 to 16.5).
+  const uint32_t groups = (p.k + 127) / 128, share = gridDim.x / 8, rem = gridDim.x % 8, xcd = blockIdx.x % 8;
+  const uint32_t wg = xcd * share + min(xcd, rem) + blockIdx.x / 8, split = wg / groups;
+  const uint32_t k0 = (wg - split * groups) * 128u, k = p.k, n = p.n, pitch = k / 2;
   constexpr uint32_t G = weights_per_scale<FMT>();
   constexpr uint32_t SB = FMT == kINT4 ? 2 : kMX ? 1 : 4;
   const uint32_t spitch = k / G * SB;
   const uint32_t steps = (n + 31) / 32;
-  const uint32_t first = blockIdx.y * p.per, last = min(first + p.per, steps);
+  const uint32_t first = split * p.per, last = min(first + p.per, steps);
 
   const bool have = k0 + 8 * m < k;
   uint32_t woff[8];
@@ -218,7 +222,7 @@ __global__ void __launch_bounds__(64 * kGradWaves) grad_few_kernel(GradFewArgs p
     const uint32_t row = 16 * t + token, col = k0 + 8 * column + 4 * half;
     if (row < p.b && col < k) {
       if (p.partial) {
-        float* to = p.partial + ((size_t)blockIdx.y * p.b + row) * k + col;
+        float* to = p.partial + ((size_t)split * p.b + row) * k + col;
         *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
       } else {
         uint16_t o[4];
@@ -246,7 +250,7 @@ __global__ void __launch_bounds__(256) grad_sum_kernel(const float* partial, uin
 
 template <int FMT, int XT>
 hipError_t grad_few_launch(const GradFewArgs& a, uint32_t splits, hipStream_t s) {
-  const dim3 grid((a.k + 127) / 128, splits), block(64 * kGradWaves);
+  const dim3 grid((a.k + 127) / 128 * splits), block(64 * kGradWaves);
   if (a.b <= 16)
     grad_few_kernel<FMT, XT, 1><<<grid, block, 0, s>>>(a);
   else if (a.b <= 32)
