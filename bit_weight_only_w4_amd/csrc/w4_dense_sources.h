@@ -59,20 +59,13 @@ __device__ inline __amdgpu_buffer_rsrc_t dense_buffer(i32x4 r) {
 // look() before its put() (NF4 asks the table some matrix instructions earlier).  first_steps() loads the first ones
 // without LDS.
 
-// a * s rounded to fp32 and to fp16, two of them in a dword: a in fp16 (the halves of c) or in fp32.
+// a * s rounded to fp32 and to fp16, two of them in a dword, a in fp16 (the halves of c).  (scaled_pair: a in fp32.)
 __device__ inline uint32_t scaled_halves(uint32_t c, float s) {
   uint32_t d;
   asm("v_fma_mixlo_f16 %0, %1, %2, 0 op_sel_hi:[1,0,0]" : "=v"(d) : "v"(c), "v"(s));
   asm("v_fma_mixhi_f16 %0, %1, %2, 0 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "+v"(d) : "v"(c), "v"(s));
   return d;
 }
-__device__ inline uint32_t scaled_pair(float a, float b, float s) {
-  uint32_t d;
-  asm("v_fma_mixlo_f16 %0, %1, %2, 0" : "=v"(d) : "v"(a), "v"(s));
-  asm("v_fma_mixhi_f16 %0, %1, %2, 0" : "+v"(d) : "v"(b), "v"(s));
-  return d;
-}
-
 // The weights of a packed dword, two of them at a time, in fp16: code (exact) times scale.
 //   * E2M1: the hardware's conversion to fp16, which takes the low nibble first: the nibbles are swapped before.
 //     MXFP4's scales are powers of two, which it applies itself (NaN too).

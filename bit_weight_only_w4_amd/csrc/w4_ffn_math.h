@@ -58,6 +58,14 @@ __device__ inline uint32_t to16(float v) {
   return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
+// a * s and b * s, rounded to fp32 and to fp16, in a dword.
+__device__ inline uint32_t scaled_pair(float a, float b, float s) {
+  uint32_t d;
+  asm("v_fma_mixlo_f16 %0, %1, %2, 0" : "=v"(d) : "v"(a), "v"(s));
+  asm("v_fma_mixhi_f16 %0, %1, %2, 0" : "+v"(d) : "v"(b), "v"(s));
+  return d;
+}
+
 // The two 16-bit terms of an NF4 code in a gated launch: the first cut towards zero (and one step short of a code that it
 // would hold whole), so that both have the code's sign and neither is 0 unless the code is: an infinite activation
 // then gives what it gives with the code itself.  Together they are off by at most 2^-15 of the code (bf16), 2^-21 (fp16).

@@ -69,16 +69,16 @@ __device__ inline uint32_t codes_in_lanes() {
   return v;
 }
 
-// The decoded 16-bit value(s) of nibble (lane & 15), meaningful in lanes 0..15: the fp16 code
-// (NF4 x fp16), the bf16 hi/lo split of the code (NF4 x bf16), the FP4 code (exact in both 16-bit
-// types), or q - 8 in the activation type (INT4, exact).
-// Whether a code is held as the sum of two 16-bit terms: NF4 with bf16 activations, and in a gated launch with fp16
-// too (its results are rounded to fp16: a code rounded there as well would cost as much accuracy again).
+// Whether a table entry has 8 bytes: NF4 with bf16 activations (two 16-bit terms a code), and in a gated launch with
+// either type (the codes in fp32: its results are rounded to 16 bits, and nothing else is).
 template <int FMT, int XT, bool GATED>
 constexpr bool split_code() {
   return FMT == kNF4 && (XT == kBF16 || GATED);
 }
 
+// The decoded value(s) of nibble (lane & 15), meaningful in lanes 0..15: the fp16 code (NF4 x fp16), the bf16 hi/lo
+// split of the code (NF4 x bf16), the fp32 code (NF4, gated), the FP4 code (exact in both 16-bit types), or q - 8 in the
+// activation type (INT4, exact).
 template <int FMT, int XT, bool GATED>
 __device__ inline void lane_decode(uint32_t& v1, uint32_t& v2) {
   v2 = 0;
@@ -88,7 +88,7 @@ __device__ inline void lane_decode(uint32_t& v1, uint32_t& v2) {
   } else if (FMT == kNF4) {
     const float c = __uint_as_float(codes_in_lanes<kNF4>());
     if constexpr (GATED) {
-      signed_terms<XT>(c, v1, v2);
+      v1 = __float_as_uint(c);
     } else if (XT == kF16) {
       v1 = f16_bits(c);
     } else {
@@ -114,11 +114,12 @@ __device__ inline void fill_table(uint32_t* tab) {
   uint32_t v1, v2;
   lane_decode<FMT, XT, GATED>(v1, v2);
   constexpr bool kSplit = split_code<FMT, XT, GATED>();
+  constexpr bool kWide = kSplit && GATED;  // a code a dword
   uint4* t4 = reinterpret_cast<uint4*>(tab);
   const int tid = threadIdx.x;
   uint32_t lo1 = 0, lo2 = 0;
   if (NT >= 256) {
-    lo1 = (uint32_t)__shfl((int)v1, (tid >> kShift) & 15) << 16;
+    lo1 = (uint32_t)__shfl((int)v1, (tid >> kShift) & 15) << (kWide ? 0 : 16);
     if (kSplit) lo2 = (uint32_t)__shfl((int)v2, (tid >> kShift) & 15) << 16;
   }
 #pragma unroll 4
@@ -126,12 +127,14 @@ __device__ inline void fill_table(uint32_t* tab) {
     const int i = tid + NT * j;
     const int hi = __builtin_amdgcn_readfirstlane(i >> (kShift + 4));
     if (NT < 256) {
-      lo1 = (uint32_t)__shfl((int)v1, (i >> kShift) & 15) << 16;
+      lo1 = (uint32_t)__shfl((int)v1, (i >> kShift) & 15) << (kWide ? 0 : 16);
       if (kSplit) lo2 = (uint32_t)__shfl((int)v2, (i >> kShift) & 15) << 16;
     }
-    const uint32_t p1 = (uint32_t)__builtin_amdgcn_readlane((int)v1, hi) | lo1;
+    const uint32_t first = (uint32_t)__builtin_amdgcn_readlane((int)v1, hi), p1 = first | lo1;
     const int slot = SPE == 16 ? i : ((i >> 2) << 4) | (i & 3);
-    if (kSplit) {
+    if (kWide) {
+      t4[slot] = make_uint4(first, lo1, first, lo1);
+    } else if (kSplit) {
       const uint32_t p2 = (uint32_t)__builtin_amdgcn_readlane((int)v2, hi) | lo2;
       t4[slot] = make_uint4(p1, p2, p1, p2);
     } else {
@@ -238,6 +241,40 @@ __device__ inline uint32_t fp4_pair(uint32_t w) {
   } else {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, KB));
   }
+}
+
+// d + first * x + second * x' with two fp16 activations in a dword.  By hand: the compiler would keep the activations
+// of the whole row in fp32, twice the registers and half the waves (8192 -> 28672 59 us against 52).
+__device__ inline float fma_pair(float first, float second, uint32_t x, float d) {
+  asm("v_fma_mix_f32 %0, %1, %2, %0 op_sel_hi:[0,1,0]" : "+v"(d) : "v"(first), "v"(x));
+  asm("v_fma_mix_f32 %0, %1, %2, %0 op_sel:[0,1,0] op_sel_hi:[0,1,0]" : "+v"(d) : "v"(second), "v"(x));
+  return d;
+}
+
+// 32 bf16 activations as fp16 numbers times 2^e, e the result: the largest of them lies in fp16's highest binade but one,
+// what lies more than 2^28 below it is off by at most 2^-39 of it, the others by nothing.  Infinities and NaN stay.
+__device__ inline int chunk_to_fp16(uint32_t (&x)[16]) {
+  typedef uint16_t ushort2_t __attribute__((ext_vector_type(2)));
+  ushort2_t most = {0, 0};
+#pragma unroll
+  for (int m = 0; m < 16; ++m)
+    most = __builtin_elementwise_max(most, __builtin_bit_cast(ushort2_t, x[m] & 0x7FFF7FFFu));
+  uint32_t top = max(most.x, most.y);
+  if (top >= 0x7F80u) {  // the largest finite one
+    top = 0;
+#pragma unroll
+    for (int m = 0; m < 16; ++m) {
+      const uint32_t a = x[m] & 0x7FFFu, b = (x[m] >> 16) & 0x7FFFu;
+      top = max(top, max(a < 0x7F80u ? a : 0u, b < 0x7F80u ? b : 0u));
+    }
+  }
+  // (of subnormal ones the exponent field 0 serves; 2^-e is a normal number)
+  const int e = max((int)(top >> 7) - 127 - 14, -126);
+  const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+  for (int m = 0; m < 16; ++m)
+    x[m] = scaled_pair(__uint_as_float(x[m] << 16), __uint_as_float(x[m] & 0xFFFF0000u), down);
+  return e;
 }
 
 // GATED (w4_gated for a few tokens): the launch has two members of the same rows, gate and up; a workgroup
@@ -399,9 +436,14 @@ gemv_kernel(typename std::conditional<GATED, GemvGatedArgs, GemvArgsT<GROUPED ? 
   // INT4A: the sum of each chunk's 32 activations (per batch row), for the zero-point term
   // -(z - 8) * s * sum(x) of every row this lane meets; computed once per launch.
   constexpr bool kXsum = FMT == kINT4A;
+  // Gated NF4 multiplies fp32 codes with the activations.  bf16 ones: of one chunk a lane the compiler keeps them in fp32
+  // (1536 -> 8960 7.3 us; as below 8.3); of more, whose registers would cost half the waves (8192 -> 28672 61 us), they
+  // become fp16 numbers under an exponent for each chunk, which comes off its sum (55 us).
+  constexpr bool kXexp = GATED && FMT == kNF4 && XT == kBF16 && ITM > 1;
+  int xexp[kXexp ? ITM : 1][B];
   float xsum[kXsum ? ITM : 1][B];
-  if constexpr (kXsum && kTable) {
-    // Keep the sums behind the barrier: computed before it, they made every wave wait for its
+  if constexpr ((kXsum || kXexp) && kTable) {
+    // Keep the sums (and the conversion) behind the barrier: computed before it, they made every wave wait for its
     // activations (and the row block loaded ahead of them) before the barrier, which then waited
     // for the slowest wave's loads (0.3 us per small launch).
 #pragma unroll
@@ -412,6 +454,12 @@ gemv_kernel(typename std::conditional<GATED, GemvGatedArgs, GemvArgsT<GROUPED ? 
         for (int m = 0; m < 16; ++m) asm volatile("" : "+v"(xr[i][b][m]));
       }
     }
+  }
+  if constexpr (kXexp) {
+#pragma unroll
+    for (int i = 0; i < ITM; ++i)
+#pragma unroll
+      for (int b = 0; b < B; ++b) xexp[i][b] = chunk_to_fp16(xr[i][b]);
   }
   if constexpr (kXsum) {
     constexpr uint32_t kOnes = XT == kF16 ? 0x3C003C00u : 0x3F803F80u;
@@ -485,13 +533,16 @@ gemv_kernel(typename std::conditional<GATED, GemvGatedArgs, GemvArgsT<GROUPED ? 
               const uint2 t = *reinterpret_cast<const uint2*>(tabc + addr);
 #pragma unroll
               for (int b = 0; b < B; ++b) {
-                const bf162_t xv = __builtin_bit_cast(bf162_t, xr[i][b][m]);
-                if constexpr (XT == kF16) {
-                  const half2_t xh = __builtin_bit_cast(half2_t, xr[i][b][m]);
-                  d[b] = __builtin_amdgcn_fdot2(__builtin_bit_cast(half2_t, t.x), xh, d[b], false);
-                  d[b] = __builtin_amdgcn_fdot2(__builtin_bit_cast(half2_t, t.y), xh, d[b], false);
+                if constexpr (GATED) {
+                  if constexpr (XT == kF16 || kXexp) {
+                    d[b] = fma_pair(__uint_as_float(t.x), __uint_as_float(t.y), xr[i][b][m], d[b]);
+                  } else {
+                    d[b] = __builtin_fmaf(__uint_as_float(t.x), from16<XT>(xr[i][b][m] & 0xFFFFu), d[b]);
+                    d[b] = __builtin_fmaf(__uint_as_float(t.y), from16<XT>(xr[i][b][m] >> 16), d[b]);
+                  }
                   continue;
                 }
+                const bf162_t xv = __builtin_bit_cast(bf162_t, xr[i][b][m]);
                 d[b] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf162_t, t.x), xv, d[b], false);
                 d[b] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf162_t, t.y), xv, d[b], false);
               }
@@ -520,6 +571,10 @@ gemv_kernel(typename std::conditional<GATED, GemvGatedArgs, GemvArgsT<GROUPED ? 
           for (int b = 0; b < B; ++b) acc[b] = __builtin_fmaf(__builtin_fmaf(-zc, xsum[i][b], d[b]), s, acc[b]);
         } else {
           const float s = scale_value<FMT>(sc[i]);
+          if constexpr (kXexp) {
+#pragma unroll
+            for (int b = 0; b < B; ++b) d[b] = ldexpf(d[b], xexp[i][b]);
+          }
 #pragma unroll
           for (int b = 0; b < B; ++b) acc[b] = __builtin_fmaf(d[b], s, acc[b]);
         }
