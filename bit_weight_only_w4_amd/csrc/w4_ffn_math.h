@@ -66,19 +66,32 @@ __device__ inline uint32_t scaled_pair(float a, float b, float s) {
   return d;
 }
 
-// The two 16-bit terms of an NF4 code in a gated launch: the first cut towards zero (and one step short of a code that it
-// would hold whole), so that both have the code's sign and neither is 0 unless the code is: an infinite activation
-// then gives what it gives with the code itself.  Together they are off by at most 2^-15 of the code (bf16), 2^-21 (fp16).
+// The 16-bit terms of an NF4 code in a gated launch, two fp16 or three bf16 ones: each but the last is what is left cut
+// towards zero (and one step short of it where it would be held whole), so that all have the code's sign and none is 0
+// unless the code is: an infinite activation then gives what it gives with the code itself.  bf16: the sum is the code
+// (24 bits); fp16: it is off by at most 2^-21 of it.
 template <int XT>
-__device__ inline void signed_terms(float c, uint32_t& v1, uint32_t& v2) {
+__device__ inline uint32_t signed_term(float c) {
+  uint32_t v;
   if constexpr (XT == kF16) {
-    v1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(c, 0.0f)) & 0xFFFFu;
-    if (c != 0.0f && (float)__builtin_bit_cast(_Float16, (uint16_t)v1) == c) v1 -= 1;
-    v2 = to16<kF16>(c - (float)__builtin_bit_cast(_Float16, (uint16_t)v1));
+    v = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(c, 0.0f)) & 0xFFFFu;
+    if (c != 0.0f && (float)__builtin_bit_cast(_Float16, (uint16_t)v) == c) v -= 1;
   } else {
-    v1 = __float_as_uint(c) >> 16;
-    if (c != 0.0f && __uint_as_float(v1 << 16) == c) v1 -= 1;
-    v2 = to16<kBF16>(c - __uint_as_float(v1 << 16));
+    v = __float_as_uint(c) >> 16;
+    if (c != 0.0f && __uint_as_float(v << 16) == c) v -= 1;
+  }
+  return v;
+}
+template <int XT>
+__device__ inline void signed_terms(float c, uint32_t& v1, uint32_t& v2, uint32_t& v3) {
+  v1 = signed_term<XT>(c);
+  const float r = c - from16<XT>(v1);
+  if constexpr (XT == kF16) {
+    v2 = to16<kF16>(r);
+    v3 = 0;
+  } else {
+    v2 = signed_term<kBF16>(r);
+    v3 = to16<kBF16>(r - __uint_as_float(v2 << 16));
   }
 }
 

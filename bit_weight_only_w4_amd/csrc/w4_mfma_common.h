@@ -42,18 +42,19 @@ __device__ inline uint32_t codes_in_lanes() {
 // (16 of each 8-byte NF4 x bf16 entry): 128 bytes per entry, lane L reading copy L % 32 (L % 16).
 // Half the GEMV's LDS, which leaves room for larger activation tiles.  Filled by all THREADS
 // threads of a workgroup; the caller synchronizes before the first lookup.
-// GATED: NF4 in two terms of one sign in either type (signed_terms), 8-byte entries.
+// GATED: NF4 in terms of one sign (signed_terms), fp16 in 8-byte entries, bf16 (three terms) in 16-byte ones, eight copies.
 template <int FMT, int XT, int THREADS, bool GATED = false>
 __device__ inline void fill_table(uint32_t* tab) {
   constexpr bool SPLIT = FMT == kNF4 && (XT == kBF16 || GATED);
-  uint32_t v1, v2 = 0;
+  constexpr bool THREE = FMT == kNF4 && XT == kBF16 && GATED;
+  uint32_t v1, v2 = 0, v3 = 0;
   if (FMT == kFP4) {
     const float c = __uint_as_float(codes_in_lanes<kFP4>());  // exact in both 16-bit types
     v1 = XT == kF16 ? f16_bits(c) : (__float_as_uint(c) >> 16);
   } else if (FMT == kNF4) {
     const float c = __uint_as_float(codes_in_lanes<kNF4>());
     if constexpr (GATED) {
-      signed_terms<XT>(c, v1, v2);
+      signed_terms<XT>(c, v1, v2, v3);
     } else if (XT == kF16) {
       v1 = f16_bits(c);
     } else {
@@ -71,6 +72,7 @@ __device__ inline void fill_table(uint32_t* tab) {
   // (i >> 3) & 15 (the same for every slot of a thread).
   const uint32_t lo1 = (uint32_t)__shfl((int)v1, (tid >> 3) & 15) << 16;
   const uint32_t lo2 = kSplit ? (uint32_t)__shfl((int)v2, (tid >> 3) & 15) << 16 : 0u;
+  const uint32_t lo3 = THREE ? (uint32_t)__shfl((int)v3, (tid >> 3) & 15) << 16 : 0u;
 #pragma unroll 4
   for (int j = 0; j < kTableBytes / 16 / THREADS; ++j) {
     const int i = tid + THREADS * j;
@@ -78,7 +80,10 @@ __device__ inline void fill_table(uint32_t* tab) {
     const uint32_t p1 = (uint32_t)__builtin_amdgcn_readlane((int)v1, hi) | lo1;
     if (kSplit) {
       const uint32_t p2 = (uint32_t)__builtin_amdgcn_readlane((int)v2, hi) | lo2;
-      t4[i] = make_uint4(p1, p2, p1, p2);
+      if constexpr (THREE)
+        t4[i] = make_uint4(p1, p2, (uint32_t)__builtin_amdgcn_readlane((int)v3, hi) | lo3, 0u);
+      else
+        t4[i] = make_uint4(p1, p2, p1, p2);
     } else {
       t4[i] = make_uint4(p1, p1, p1, p1);
     }

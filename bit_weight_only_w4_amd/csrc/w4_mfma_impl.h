@@ -35,7 +35,7 @@
 //   * Gated launches (w4_gated): members 0 and 1 are the gate and the up matrix of the same rows; even row groups
 //     take 16 gate rows, the odd ones next to them the same 16 up rows, and after the K groups are added the up
 //     sums go through LDS to the gate waves, which store act(g) * u in x's type.  NF4 codes have two terms in fp16
-//     too: one alone would be off by as much as the rounding of h.
+//     and three in bf16 (2^-21 of a code and nothing are left): one fewer would show in a 16-bit result.
 //   * MXFP4 moves through the registers as NF4's 64-weight blocks; one more swap of 16-lane rows
 //     (v_permlane16_swap) gathers the lane groups' dwords so that each MFMA step is one 32-weight
 //     block with one scale, applied in fp32 after the step.  Its codes come from the hardware
@@ -150,6 +150,7 @@ mfma_kernel(typename std::conditional<GATED, MfmaGatedArgs, MfmaArgs>::type a) {
   constexpr bool kMX = FMT == kMXFP4;          // a scale per step, no table
   constexpr int SB = FMT == kINT4 || kMX ? 2 : 4;  // bytes of scale per block
   constexpr bool kSplit = FMT == kNF4 && (XT == kBF16 || GATED);
+  constexpr bool kThree = FMT == kNF4 && XT == kBF16 && GATED;
   // LDS: the decode table (static, at address 0, so a lookup address needs no base), then the
   // dynamic part: the K-group reduction area and the x window.
   __shared__ __align__(16) uint32_t tab[kMX ? 4 : kTableBytes / 4];
@@ -349,7 +350,8 @@ mfma_kernel(typename std::conditional<GATED, MfmaGatedArgs, MfmaArgs>::type a) {
   for (int t = 0; t < T; ++t) acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
 
   // Twice this lane's byte offset in a table entry (see the lookup below).
-  const uint32_t laneoff = kSplit ? (uint32_t)(lane & 15) * 16u : (uint32_t)(lane & 31) * 8u;
+  const uint32_t laneoff =
+      kThree ? (uint32_t)(lane & 7) * 32u : kSplit ? (uint32_t)(lane & 15) * 16u : (uint32_t)(lane & 31) * 8u;
   const char* tabc = reinterpret_cast<const char*>(tab);
   const uint8_t* xw = xs + (uint32_t)kg * (seg * 16u);  // this K group's part of the window
 
@@ -454,14 +456,19 @@ mfma_kernel(typename std::conditional<GATED, MfmaGatedArgs, MfmaArgs>::type a) {
           }
           continue;
         }
-        uint32_t p1[4], p2[4];
+        uint32_t p1[4], p2[4], p3[4];
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb) {
           // LDS byte address = byte * 128 + lane offset: the perm builds byte * 256 + 2 * lane
           // offset (the packed byte into byte 1), halved by the shift.
           const uint32_t addr =
               __builtin_amdgcn_perm(wb[c][s], laneoff, 0x0C0C0000u | ((4u + (uint32_t)kb) << 8)) >> 1;
-          if (kSplit) {
+          if constexpr (kThree) {
+            const uint4 tv = *reinterpret_cast<const uint4*>(tabc + addr);
+            p1[kb] = tv.x;
+            p2[kb] = tv.y;
+            p3[kb] = tv.z;
+          } else if (kSplit) {
             const uint2 tv = *reinterpret_cast<const uint2*>(tabc + addr);
             p1[kb] = tv.x;
             p2[kb] = tv.y;
@@ -475,6 +482,7 @@ mfma_kernel(typename std::conditional<GATED, MfmaGatedArgs, MfmaArgs>::type a) {
           const uint4 bv = *reinterpret_cast<const uint4*>(xq + xrowoff[t] + (c * KC + s * 8) * 2);
           dd[t] = mfma<XT>(a1, bv, dd[t]);
           if (kSplit) dd[t] = mfma<XT>(make_uint4(p2[0], p2[1], p2[2], p2[3]), bv, dd[t]);
+          if constexpr (kThree) dd[t] = mfma<XT>(make_uint4(p3[0], p3[1], p3[2], p3[3]), bv, dd[t]);
           if (FMT == kINT4A) dd[t] = mfma<XT>(zrow, bv, dd[t]);
         }
         // With 8 tiles, keep each step's B fragments from being fetched ahead of the previous

@@ -76,7 +76,7 @@ def _check(got, ref, terms):
 
 
 @pytest.mark.parametrize("fmt", INEXACT)
-@pytest.mark.parametrize("tokens", [1])
+@pytest.mark.parametrize("tokens", [1, 2, 7, 33, 64, 100, 128])
 def test_gated_products_of_nearly_equal_weights(fmt, tokens):
     """Each token takes one weight of a block less one of the next, in every row."""
     w4, dev, dtype = _w4(), f.device(), f.DTYPES[fmt.split("_")[1]]
@@ -94,7 +94,7 @@ def test_gated_products_of_nearly_equal_weights(fmt, tokens):
 
 
 @pytest.mark.parametrize("fmt", f.FMTS)
-@pytest.mark.parametrize("tokens,hidden,inter", [(1, 384, 40), (1, 4160, 77)])
+@pytest.mark.parametrize("tokens,hidden,inter", [(1, 384, 40), (1, 4160, 77), (5, 640, 33), (64, 384, 100), (128, 1152, 77)])
 def test_gated_products_read_weights_out(fmt, tokens, hidden, inter):
     w4, dev, dtype = _w4(), f.device(), f.DTYPES[fmt.split("_")[1]]
     p, s = _raw_weights(fmt, 2 * inter, hidden, tokens)
