@@ -58,6 +58,13 @@ __device__ inline uint32_t to16(float v) {
   return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
+// Two values as bf16 in a dword, one instruction.
+__device__ inline uint32_t bf16_pair(float a, float b) {
+  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{a, b}), bf2));
+}
+
 // a * s and b * s, rounded to fp32 and to fp16, in a dword.
 __device__ inline uint32_t scaled_pair(float a, float b, float s) {
   uint32_t d;

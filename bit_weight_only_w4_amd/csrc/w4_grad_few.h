@@ -9,9 +9,11 @@
 // tokens 4 g .. 4 g + 3.
 //   * Scales: lane 16 g + m loads one, of row 8 g + (m & 7) and the column half m >> 3 (groups of 128: of the row;
 //     blocks of 32: the two bytes of that half); lane r of each half row hands it to the others when row r is decoded.
-//   * Weights are decoded to fp32, scaled and rounded to bf16 operands, bf16 d: one term (2^-8 of the weight, as the
-//     decoded rows of the other path).  fp16 d: d as the sum of two bf16 numbers (exact), the weight as the sum of two
-//     (2^-16), three products; bf16 has fp32's range, so no common exponent is needed.
+//   * A weight enters as the sum of bf16 numbers, which have fp32's range, so that no common exponent is needed: MXFP4
+//     one (exact), INT4 two (exact, at most 12 bits), NF4 and FP4 three (2^-21).  Every term but the last is rounded from
+//     what is left less 2^-7 of it: so all have the weight's sign and none is 0 unless the weight is, and an infinite
+//     gradient gives what it gives with the weight itself.  fp16 gradients are the sum of two bf16 numbers (exact); of
+//     the products of terms the one below 2^-20 of the whole is left out.
 //   * Bound by the chain of loads, decoding and products of a few steps and by the splits' sums on their way through
 //     memory: 16 tokens of NF4 1536 x 8960 9 us (0.9 TB/s) and 2.5 for the sum (28672 x 4096 37 us in all, 1.8 TB/s).
 //   * The waves' sums are added in LDS, the splits' by a second kernel, both in a fixed order.
@@ -34,6 +36,8 @@ struct GradStep {
 template <int FMT, int XT, int NT>
 __global__ void __launch_bounds__(64 * kGradWaves) grad_few_kernel(GradFewArgs p) {
   constexpr bool kMX = FMT == kMXFP4;
+  constexpr int TERMS = kMX ? 1 : is_g128(FMT) ? 2 : 3;  // of a weight
+  constexpr float kLess = 1.0f - 0x1p-7f;
   __shared__ __align__(16) float4_t red[kGradWaves * 8 * 64];
   __shared__ float table[FMT == kNF4 ? 16 * 64 : 1];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -84,6 +88,7 @@ __global__ void __launch_bounds__(64 * kGradWaves) grad_few_kernel(GradFewArgs p
     }
   };
 
+  const char* codes = reinterpret_cast<const char*>(table);
   float4_t acc[NT][8];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -109,18 +114,17 @@ __global__ void __launch_bounds__(64 * kGradWaves) grad_few_kernel(GradFewArgs p
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float x = from16<kF16>(v[j] & 0xFFFFu), y = from16<kF16>(v[j] >> 16);
-          // An infinity or NaN is the second term, which meets the weights' first term alone: with their second ones,
-          // zeros among them, it would make NaN of an infinity.
-          a[j] = to16<kBF16>(fabsf(x) < __builtin_inff() ? x : 0.0f) |
-                 (to16<kBF16>(fabsf(y) < __builtin_inff() ? y : 0.0f) << 16);
-          const float xl = x - __uint_as_float(a[j] << 16), yl = y - __uint_as_float(a[j] & 0xFFFF0000u);  // at most 3 bits
+          a[j] = bf16_pair(x, y);
+          // at most 3 bits; none of an infinity or NaN
+          const float xl = fabsf(x) < __builtin_inff() ? x - __uint_as_float(a[j] << 16) : 0.0f;
+          const float yl = fabsf(y) < __builtin_inff() ? y - __uint_as_float(a[j] & 0xFFFF0000u) : 0.0f;
           b[j] = (__float_as_uint(xl) >> 16) | (__float_as_uint(yl) & 0xFFFF0000u);
         }
         dh[t] = make_uint4(a[0], a[1], a[2], a[3]);
         dl[t] = make_uint4(b[0], b[1], b[2], b[3]);
       }
     }
-    float s[8], o[8];  // scales and the offsets of integer codes
+    float s[8], o[8], s1[8];  // scales, the offsets of integer codes, and the first term's scales
     auto one = [&](auto r) __attribute__((always_inline)) {
       constexpr int R = decltype(r)::value;
       const uint32_t bits = scale_bits(st.s, r);
@@ -133,6 +137,7 @@ __global__ void __launch_bounds__(64 * kGradWaves) grad_few_kernel(GradFewArgs p
       } else {
         s[R] = __uint_as_float(bits);
       }
+      s1[R] = TERMS > 1 ? s[R] * kLess : s[R];
     };
     one(std::integral_constant<int, 0>{});
     one(std::integral_constant<int, 1>{});
@@ -144,39 +149,49 @@ __global__ void __launch_bounds__(64 * kGradWaves) grad_few_kernel(GradFewArgs p
     one(std::integral_constant<int, 7>{});
 #pragma unroll
     for (int b = 0; b < 4; ++b) {  // byte b: columns 2 b (high nibble) and 2 b + 1
-      float w[2][8];
+      float w[2][8];  // codes, integers less their offset
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
         const uint32_t v = st.w[r];
         if constexpr (FMT == kNF4) {
-          const uint32_t hi = (v >> (8 * b + 4)) & 15u, lo = (v >> (8 * b)) & 15u;
-          w[0][r] = table[hi * 64 + lane] * s[r];
-          w[1][r] = table[lo * 64 + lane] * s[r];
+          // byte offsets of a code's 64 copies, then of this lane's
+          const uint32_t hi = (b < 1 ? v << 4 : v >> (8 * b - 4)) & 0xF00u, lo = (b < 1 ? v << 8 : v >> (8 * b - 8)) & 0xF00u;
+          w[0][r] = *reinterpret_cast<const float*>(codes + (hi | (4u * lane)));
+          w[1][r] = *reinterpret_cast<const float*>(codes + (lo | (4u * lane)));
         } else {
-          decode_pair<FMT>(v, b, nullptr, BlockScale{s[r], o[r]}, &w[0][r], &w[1][r]);
+          decode_pair<FMT>(v, b, nullptr, BlockScale{1.0f, o[r]}, &w[0][r], &w[1][r]);
         }
       }
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        uint32_t h[4], l[4];
+        uint32_t h[4], m2[4], l[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float x = w[q][2 * i], y = w[q][2 * i + 1];
-          h[i] = to16<kBF16>(x) | (to16<kBF16>(y) << 16);
-          if constexpr (XT == kF16) {
-            const float xl = x - __uint_as_float(h[i] << 16), yl = y - __uint_as_float(h[i] & 0xFFFF0000u);
-            l[i] = to16<kBF16>(xl) | (to16<kBF16>(yl) << 16);
+          const int j = 2 * i;
+          const float x = w[q][j], y = w[q][j + 1];
+          h[i] = bf16_pair(x * s1[j], y * s1[j + 1]);
+          if constexpr (TERMS > 1) {
+            const float xl = __builtin_fmaf(x, s[j], -__uint_as_float(h[i] << 16));
+            const float yl = __builtin_fmaf(y, s[j + 1], -__uint_as_float(h[i] & 0xFFFF0000u));
+            if constexpr (TERMS == 2) {
+              m2[i] = bf16_pair(xl, yl);  // exact
+            } else {
+              m2[i] = bf16_pair(xl * kLess, yl * kLess);
+              l[i] = bf16_pair(xl - __uint_as_float(m2[i] << 16), yl - __uint_as_float(m2[i] & 0xFFFF0000u));
+            }
           }
         }
         const uint4 oh = make_uint4(h[0], h[1], h[2], h[3]);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           float4_t& c = acc[t][2 * b + q];
-          if constexpr (XT == kF16) {
-            const uint4 ol = make_uint4(l[0], l[1], l[2], l[3]);
-            c = mfma<kBF16>(dl[t], oh, c);
-            c = mfma<kBF16>(dh[t], ol, c);
+          if constexpr (TERMS == 3) c = mfma<kBF16>(dh[t], make_uint4(l[0], l[1], l[2], l[3]), c);
+          if constexpr (TERMS > 1) {
+            const uint4 om = make_uint4(m2[0], m2[1], m2[2], m2[3]);
+            if constexpr (XT == kF16) c = mfma<kBF16>(dl[t], om, c);
+            c = mfma<kBF16>(dh[t], om, c);
           }
+          if constexpr (XT == kF16) c = mfma<kBF16>(dl[t], oh, c);
           c = mfma<kBF16>(dh[t], oh, c);
         }
       }

@@ -93,6 +93,49 @@ def test_gated_products_of_nearly_equal_weights(fmt, tokens):
     _check(pr, x @ hat.t(), x.abs() @ hat.abs().t())
 
 
+@pytest.mark.parametrize("fmt", INEXACT)
+@pytest.mark.parametrize("tokens,n,steps", [(1, 70, 2), (16, 640, 3), (32, 333, 2)])
+def test_gradient_of_nearly_equal_weights(fmt, tokens, n, steps):
+    """Each token takes the difference of two rows that are nearly equal in every column, the first and the last rows, and
+    rows on both sides of steps among them."""
+    w4, dev, dtype = _w4(), f.device(), f.DTYPES[fmt.split("_")[1]]
+    p, s = _blocks(fmt, steps, 2 * ((n + 1) // 2), n)  # rows and blocks change places
+    g = f.group(fmt)
+    p = p.view(steps, -1, g // 2).transpose(0, 1).reshape(-1, steps * g // 2)[:n].contiguous()
+    s = s.t()[:n].contiguous()
+    hat = _hat(fmt, p, s)
+    pairs = n // 2
+    d = torch.zeros(tokens, n, dtype=torch.float64)
+    terms = torch.zeros(tokens, steps * g, dtype=torch.float64)
+    for t in range(tokens):
+        at = (t // 2 if t % 2 == 0 else pairs - 1 - t // 2) if t % 3 else t * 16 + 15
+        at %= pairs
+        d[t, 2 * at], d[t, 2 * at + 1] = 1.0, -1.0
+        terms[t] = hat[2 * at].abs() + hat[2 * at + 1].abs()
+    dx = w4.gemm_grad(d.to(dtype).to(dev), p.to(dev), s.to(dev), fmt)
+    _check(dx, d @ hat, terms)
+
+
+@pytest.mark.parametrize("fmt", f.FMTS)
+@pytest.mark.parametrize("tokens,n,k", [(1, 40, 384), (16, 1000, 512), (31, 4003, 384), (32, 28672, 1152)])
+def test_gradient_reads_weights_out(fmt, tokens, n, k):
+    """Each token is one number in one row: a row of weights comes back, at one rounding.  The first, the last and the tail
+    rows, rows on both sides of steps, and rows all over; other tokens' rows are far from it in value."""
+    w4, dev, dtype = _w4(), f.device(), f.DTYPES[fmt.split("_")[1]]
+    p, s = _raw_weights(fmt, n, k, tokens)
+    edge = [0, n - 1, n - 2, 63, 64, 31, 32, n // 64 * 64 - 1, n // 64 * 64, n // 64 * 64 + 1, 127, 128, n // 2, n // 4, 3 * n // 4]
+    rows = torch.tensor([(edge[t] if t < len(edge) else t * 7919) % n for t in range(tokens)])
+    value = 2.0 ** (torch.arange(tokens) % 5).double() * (1 - 2 * (torch.arange(tokens) % 2))
+    d = torch.zeros(tokens, n, dtype=dtype)
+    d[torch.arange(tokens), rows] = value.to(dtype)
+    dx = w4.gemm_grad(d.to(dev), p, s, fmt).cpu()
+    at = rows.to(dev)
+    ref = _hat(fmt, p[at], s[at]) * value.unsqueeze(1)
+    if len(torch.unique(rows)) > 3:
+        assert len(torch.unique(ref, dim=0)) > 3
+    _check(dx, ref, ref.abs())
+
+
 @pytest.mark.parametrize("fmt", f.FMTS)
 @pytest.mark.parametrize("tokens,hidden,inter", [(1, 384, 40), (1, 4160, 77), (5, 640, 33), (64, 384, 100), (128, 1152, 77)])
 def test_gated_products_read_weights_out(fmt, tokens, hidden, inter):
