@@ -30,6 +30,7 @@ SOURCES = ["w4_api.cpp", "w4_gemv.hip",
            "w4_moe.hip", "w4_moe_up_f16.hip", "w4_moe_up_bf16.hip", "w4_moe_down.hip",
            "w4_moe_wide_up.hip", "w4_moe_wide_down.hip",
            "w4_dense.hip", "w4_dense_nf4.hip", "w4_dense_fp4.hip", "w4_dense_mxfp4.hip", "w4_dense_int4.hip",
+           "w4_dense_int4a.hip",
            "w4_dense_columns_nf4.hip", "w4_dense_columns_fp4.hip", "w4_dense_columns_mxfp4.hip",
            "w4_dense_columns_int4.hip", "w4_dense_columns_int4a.hip", "w4_gated.hip", "w4_gated_gemv_f16.hip", "w4_gated_gemv_bf16.hip",
            "w4_gated_mfma_f16.hip", "w4_gated_mfma_bf16.hip",

@@ -1447,7 +1447,7 @@ int int8_call(const int8_t* xq, const float* xs, const int8_t* wq, const float* 
   if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(xs, 4) || !aligned(ws, 4) || !aligned(out, esz) ||
       (products && !aligned(products, esz)))
     return W4_ERR_ALIGN;
-  const size_t used = int8_few(b) ? 0 : dense_bytes(gated, b, n, k);
+  const size_t used = int8_few(b) ? 0 : dense_bytes(gated, b, n, k, -1, 1);
   if (used && (!workspace || workspace_bytes < used)) return W4_ERR_WORKSPACE;
   if (used && !aligned(workspace, 16)) return W4_ERR_ALIGN;
   const size_t rows = (size_t)n * (gated ? 2 : 1), ob = (size_t)b * (size_t)n * esz;
@@ -1460,6 +1460,7 @@ int int8_call(const int8_t* xq, const float* xs, const int8_t* wq, const float* 
   a.m = (uint32_t)b;
   a.n = (uint32_t)n;
   a.pitch = (uint32_t)k;
+  a.terms = 1;
   a.row_scale = xs;
   a.col_scale = ws;
   a.out = out;
@@ -1475,7 +1476,7 @@ int int8_call(const int8_t* xq, const float* xs, const int8_t* wq, const float* 
 }  // namespace
 
 size_t w4_int8_workspace_bytes(int64_t N, int64_t K, int64_t B, int gated) {
-  return int8_shape(gated != 0, N, K, B) == W4_OK && !int8_few(B) ? dense_bytes(gated != 0, B, N, K) : 0;
+  return int8_shape(gated != 0, N, K, B) == W4_OK && !int8_few(B) ? dense_bytes(gated != 0, B, N, K, -1, 1) : 0;
 }
 
 int w4_gemm_int8(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws, int64_t N, int64_t K, int64_t B,

@@ -16,6 +16,7 @@
 //   * Gated: the B tile holds TN / 2 gate rows, then the up rows of the same channels; a wave's even column tiles
 //     are gate, its odd ones the up of the same channels, so the activation and the product happen in registers.
 //   * Rows past M or N and bytes past K are read at an offset outside the buffer, which gives zeros.
+//   * B of two terms (fp16, dense_terms): K is twice as long, a step of A's meets one of first and then one of second terms.
 //   * B in four bits: a wave's packed weights and their scales come to LDS of its own a step ahead, and between the matrix
 //     instructions it decodes them, scales them, rounds them to 16 bits and writes them into the stage where the copies
 //     would have put them: rows of weights for the gated block (PackedRows), columns for a gradient (PackedColumns; both
@@ -38,7 +39,7 @@ struct DensePlan {
   uint32_t splits, per;
   uint32_t tiles, rest;  // tiles in all, and how many of the last are covered with 64 x 128 tiles by a second launch
 };
-DensePlan plan_dense(bool gated, int64_t m, int64_t n, int64_t pitch, int packed);
+DensePlan plan_dense(bool gated, int64_t m, int64_t n, int64_t pitch, int packed, int terms);
 // Sets what a launch of the plan needs; false where it has too many tiles.
 bool dense_prepare(const DensePlan& p, DenseArgs* a);
 
@@ -90,6 +91,7 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
   constexpr int W = WM * WN, TM = 32 * MT * WM, TN = 32 * NT * WN;
   constexpr int ROWS = TM + TN;             // rows of a stage
   constexpr bool PACKED = FMT >= 0;         // B in four bits
+  constexpr int TERMS = PACKED && GATED ? dense_terms(FMT) : 1;  // known when compiled
   constexpr int COPIES = (PACKED ? TM : ROWS) / 8 / W;  // copies of 8 rows a wave makes for a stage
   static_assert(TM % (8 * W) == 0 && (PACKED || (GATED ? TN / 2 : TN) % (8 * W) == 0),
                 "a round of copies fills one operand");
@@ -119,10 +121,12 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
 
   const uint32_t nrows = min(CN, p.n - n0);
   const i32x4 ra = dense_rsrc(p.a + (size_t)m0 * p.pitch, min((uint32_t)TM, p.m - m0) * p.pitch);
+  const uint32_t twice = PACKED ? TERMS - 1 : TYPE == kDenseI8 ? 0 : p.terms - 1;  // steps of B to one of A, as a shift
+  const uint32_t bpitch = p.pitch << twice;
   i32x4 rb{}, ru{};  // B, gated: its gate and up rows
   if constexpr (!PACKED) {
-    rb = dense_rsrc(p.b + (size_t)n0 * p.pitch, nrows * p.pitch);
-    ru = dense_rsrc(p.b + (size_t)(GATED ? p.n + n0 : 0) * p.pitch, GATED ? nrows * p.pitch : 0u);
+    rb = dense_rsrc(p.b + (size_t)n0 * bpitch, nrows * bpitch);
+    ru = dense_rsrc(p.b + (size_t)(GATED ? p.n + n0 : 0) * bpitch, GATED ? nrows * bpitch : 0u);
   }
 
   // Copy j of this wave fills rows 8 (W j + wave) .. + 7 of a stage: lane l slot l % 8 of row l / 8.  Its offsets:
@@ -134,13 +138,14 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
     const uint32_t r = 8u * (uint32_t)(W * j + wave) + ((uint32_t)lane >> 3);
     const uint32_t row = r < (uint32_t)TM ? r : (r - TM) % CN;
     const uint32_t rows = r < (uint32_t)TM ? min((uint32_t)TM, p.m - m0) : nrows;
-    off[j] = row < rows ? row * p.pitch + mine : kOutOfRange - p.pitch;
+    // (outside: past 2^31, which no resource of fewer rows than a tile's reaches)
+    off[j] = row < rows ? row * (r < (uint32_t)TM ? p.pitch : bpitch) + mine : 0x80000000u;
   }
-  const uint32_t first = blockIdx.y * p.per, steps = min(first + p.per, (p.pitch + 127) / 128);  // this split's
-  // Copy j of step t; past the last step copies are made all the same, from outside the buffers, so that the number
-  // of copies in flight is the same in every step.
+  const uint32_t first = blockIdx.y * p.per, steps = min(first + p.per, (p.pitch + 127) / 128 << twice);  // this split's
+  // Copy j of step t; past the last step copies are made all the same, of what is never read (mostly from outside the
+  // buffers), so that the number of copies in flight is the same in every step.
   auto copy = [&](const uint8_t* st, uint32_t t, int j) __attribute__((always_inline)) {
-    uint32_t k = t < steps ? t * 128 : 0x40000000u;
+    uint32_t k = t < steps ? (8 * W * j < TM ? t >> twice : t) * 128 : 0x40000000u;
     if constexpr (TYPE == kDenseI8) k = k + mine < p.pitch ? k : 0x40000000u;  // rows may end in the middle of a step
     const uint8_t* to = st + 8 * (W * j + wave) * 128;
     if (8 * W * j < TM)  // known when compiled
@@ -187,7 +192,7 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
   constexpr int C0 = STAGES == 2 ? COPIES : COPIES < 2 * C3 ? COPIES : 2 * C3;
   constexpr int C1 = COPIES < 3 * C3 ? COPIES : 3 * C3;
   constexpr int SF = PACKED ? FMT : kFP4, SN = PACKED ? TN : 32 * W;  // (a source that is never used otherwise)
-  using Source = typename std::conditional<GATED, PackedRows<SF, TM, SN, W, STAGES>,
+  using Source = typename std::conditional<GATED, PackedRows<SF, PACKED ? TERMS : 1, TM, SN, W, STAGES>,
                                            PackedColumns<SF, TYPE, TM, SN, W, STAGES>>::type;
   Source src;
   int all = 0;  // the exponent of all of B
@@ -202,8 +207,10 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
     src.init(p, n0, steps, all, raw, &ring[0][0], table, lane, wave);
   }
   // A quarter: after each matrix instruction one of the next quarter's fragments is requested, and a copy now and then.
-  auto quarter = [&](Frags& next, uint32_t st, auto which, const Frags& f, uint32_t to, uint32_t t, auto from, auto end)
-      __attribute__((always_inline)) {
+  // What it decodes are weights of step t, of their term `of`.
+  auto quarter = [&](Frags& next, uint32_t st, auto which, const Frags& f, uint32_t to, uint32_t t, auto of, auto from,
+                     auto end) __attribute__((always_inline)) {
+    constexpr int T = decltype(of)::value;
     constexpr int A = decltype(from)::value, Z = decltype(end)::value, ALL = MT * NT;
     constexpr int s = decltype(which)::value;  // the quarter whose fragments are requested
     constexpr int D0 = PACKED && s == 0 ? 1 : 0;
@@ -222,15 +229,15 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
         if constexpr (FMT == kNF4) {
           if (D0 == q) src.template look<0>(s), src.template look<1>(s);
           if (D0 + (ALL - D0) / 3 == q) {
-            src.template put<0>(to, s), src.template put<1>(to, s);
+            src.template put<0, T>(to, s), src.template put<1, T>(to, s);
             src.template look<2>(s), src.template look<3>(s);
           }
-          if (D0 + 2 * (ALL - D0) / 3 == q) src.template put<2>(to, s), src.template put<3>(to, s);
+          if (D0 + 2 * (ALL - D0) / 3 == q) src.template put<2, T>(to, s), src.template put<3, T>(to, s);
         } else {
-          if (D0 == q) src.template look<0>(s), src.template put<0>(to, s);
-          if (D0 + (ALL - D0) / 4 == q) src.template look<1>(s), src.template put<1>(to, s);
-          if (D0 + 2 * (ALL - D0) / 4 == q) src.template look<2>(s), src.template put<2>(to, s);
-          if (D0 + 3 * (ALL - D0) / 4 == q) src.template look<3>(s), src.template put<3>(to, s);
+          if (D0 == q) src.template look<0>(s), src.template put<0, T>(to, s);
+          if (D0 + (ALL - D0) / 4 == q) src.template look<1>(s), src.template put<1, T>(to, s);
+          if (D0 + 2 * (ALL - D0) / 4 == q) src.template look<2>(s), src.template put<2, T>(to, s);
+          if (D0 + 3 * (ALL - D0) / 4 == q) src.template look<3>(s), src.template put<3, T>(to, s);
         }
       }
 #pragma unroll
@@ -248,17 +255,21 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
     for (int i = 0; i < STAGES - 1; ++i)
 #pragma unroll
       for (int j = 0; j < COPIES; ++j) copy(&ring[i][0], first + i, j);
-#pragma unroll
-    for (int i = 0; i < STAGES; ++i) {
+    auto decode = [&](auto at, auto of) __attribute__((always_inline)) {
+      constexpr int i = decltype(at)::value, T = decltype(of)::value;
       src.use_first(i);
 #pragma unroll
       for (int q = 0; q < (i == STAGES - 1 ? 1 : 4); ++q) {
-        src.template look<0>(q), src.template put<0>(i * SIZE, q);
-        src.template look<1>(q), src.template put<1>(i * SIZE, q);
-        src.template look<2>(q), src.template put<2>(i * SIZE, q);
-        src.template look<3>(q), src.template put<3>(i * SIZE, q);
+        src.template look<0>(q), src.template put<0, T>(i * SIZE, q);
+        src.template look<1>(q), src.template put<1, T>(i * SIZE, q);
+        src.template look<2>(q), src.template put<2, T>(i * SIZE, q);
+        src.template look<3>(q), src.template put<3, T>(i * SIZE, q);
       }
-    }
+    };
+    static_assert(STAGES == 2 || STAGES == 3, "the stages decoded here");
+    decode(I<0>{}, I<0>{});
+    decode(I<1>{}, I<1 % TERMS>{});
+    if constexpr (STAGES == 3) decode(I<2>{}, I<0>{});
     src.copy(first + STAGES);
 #pragma unroll
     for (int j = 0; j < C3; ++j) copy(&ring[STAGES - 1][0], first + STAGES - 1, j);
@@ -273,17 +284,23 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
 #pragma unroll
   for (int i = 0; i < MT + NT; ++i) fetch(f0, base, i);
   uint32_t now = 0, spare = (STAGES - 1) * SIZE;  // the step's stage, and the last step's
-  for (uint32_t t = first; t < steps; ++t) {
+  auto step = [&](uint32_t t, auto of) __attribute__((always_inline)) {
     const uint32_t u = t + STAGES - 1;
-    quarter(f1, now, I<1>{}, f0, spare, u, I<C3>{}, I<C0>{});
-    quarter(f0, now, I<2>{}, f1, spare, u, I<C0>{}, I<C1>{});
-    quarter(f1, now, I<3>{}, f0, spare, u, I<C1>{}, I<COPIES>{});
+    using Now = I<(decltype(of)::value + STAGES - 1) % TERMS>;  // the term of step u
+    using Next = I<(decltype(of)::value + STAGES) % TERMS>;
+    quarter(f1, now, I<1>{}, f0, spare, u, Now{}, I<C3>{}, I<C0>{});
+    quarter(f0, now, I<2>{}, f1, spare, u, Now{}, I<C0>{}, I<C1>{});
+    quarter(f1, now, I<3>{}, f0, spare, u, Now{}, I<C1>{}, I<COPIES>{});
     // by hand: the compiler's own barrier waits for every copy in flight
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * COPIES) : "memory");
     spare = now;
     now = now + SIZE == STAGES * SIZE ? 0 : now + SIZE;
     if constexpr (PACKED) src.take();
-    quarter(f0, now, I<0>{}, f1, spare, u + 1, I<0>{}, I<C3>{});
+    quarter(f0, now, I<0>{}, f1, spare, u + 1, Next{}, I<0>{}, I<C3>{});
+  };
+  for (uint32_t t = first; t < steps; t += TERMS) {  // (splits begin with a first term)
+    step(t, I<0>{});
+    if constexpr (TERMS == 2) step(t + 1, I<1>{});
   }
   wait_all_vector_loads();  // no copy outlives the workgroup
 

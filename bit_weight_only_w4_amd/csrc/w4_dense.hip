@@ -16,13 +16,13 @@ namespace w4 {
 // the others, whose rows of B meet fewer of A, 1.18 times that (160 and 256 tokens of 1536 -> 8960 to 8192 -> 28672).
 // Decoding columns: 1.07 (FP4, INT4), 1.1 (MXFP4) or 1.25 (NF4), 1.12 times that for 128 x 256, 2.2 and 1.62 for 64 x 128
 // (4096 x 2048 weights, 256 and 2048 tokens: a step of 64 x 128 tiles alone 0.71 to 1.07 us, of full CUs 1.14 to 1.5).
-DensePlan plan_dense(bool gated, int64_t m, int64_t n, int64_t pitch, int packed) {
+DensePlan plan_dense(bool gated, int64_t m, int64_t n, int64_t pitch, int packed, int terms) {
   const bool columns = packed >= 0 && !gated;
   const double slow = packed < 0         ? 1.0
                       : packed == kNF4   ? columns ? 1.25 : 1.3
                       : packed == kMXFP4 ? columns ? 1.1 : 1.0
                                          : columns ? 1.07 : 1.19;
-  const int64_t cus = device_cu_count(), steps = (pitch + 127) / 128;
+  const int64_t cus = device_cu_count(), steps = (pitch + 127) / 128 * terms;
   const int64_t width = gated ? 2 * n : n;
   DensePlan best{0, 0, 1, (uint32_t)steps, 0, 0};
   double least = 0;
@@ -38,11 +38,11 @@ DensePlan plan_dense(bool gated, int64_t m, int64_t n, int64_t pitch, int packed
     const Tile t = tile_of(i);
     const int64_t tiles = ((m + t.tm - 1) / t.tm) * ((width + t.tn - 1) / t.tn);
     for (int64_t s = 1; s <= 20 && s * 4 <= std::max<int64_t>(steps, 4); ++s) {
-      const int64_t per = (steps + s - 1) / s;
+      const int64_t per = (steps / terms + s - 1) / s * terms;
       if ((s - 1) * per >= steps) continue;  // an empty split
       const int64_t rounds = (tiles * s + cus * t.fit - 1) / (cus * t.fit);
       const double work = rounds * (per * (tiles * s <= cus ? t.alone : t.full) + t.ends);
-      const double bytes = ((double)m + (packed < 0 ? 1.0 : 0.3125) * width) * pitch / 5.5e6;
+      const double bytes = ((double)m + (packed < 0 ? terms : 0.3125) * width) * pitch / 5.5e6;
       auto offer = [&](double w, int64_t rest) {
         double us = std::max(w, bytes) + 0.1 * std::min(w, bytes);
         if (s > 1) us += 3 + (double)s * m * width * 8 / 5e6;
@@ -74,16 +74,18 @@ bool dense_prepare(const DensePlan& p, DenseArgs* a) {
   return true;
 }
 
-double dense_us(int64_t m, int64_t n, int64_t pitch, int packed) { return plan_dense(false, m, n, pitch, packed).us; }
+double dense_us(bool gated, int64_t m, int64_t n, int64_t pitch, int packed, int terms) {
+  return plan_dense(gated, m, n, pitch, packed, terms).us;
+}
 
-size_t dense_bytes(bool gated, int64_t m, int64_t n, int64_t pitch, int packed) {
-  const DensePlan p = plan_dense(gated, m, n, pitch, packed);
+size_t dense_bytes(bool gated, int64_t m, int64_t n, int64_t pitch, int packed, int terms) {
+  const DensePlan p = plan_dense(gated, m, n, pitch, packed, terms);
   return p.splits > 1 ? (size_t)p.splits * (size_t)m * (size_t)(gated ? 2 * n : n) * 4 : 0;
 }
 
 hipError_t launch_dense(int type, bool gated, const DenseArgs& args, hipStream_t s) {
   DenseArgs a = args;
-  const DensePlan p = plan_dense(gated, a.m, a.n, a.pitch, -1);
+  const DensePlan p = plan_dense(gated, a.m, a.n, a.pitch, -1, (int)a.terms);
   if (!dense_prepare(p, &a)) return hipErrorInvalidValue;
   if (type == kDenseF16)
     return gated ? dense_run<kDenseF16, true, -1>(p, a, s) : dense_run<kDenseF16, false, -1>(p, a, s);

@@ -5,7 +5,7 @@ namespace w4 {
 
 hipError_t launch_dense_fp4(const DenseArgs& args, hipStream_t s) {
   DenseArgs a = args;
-  const DensePlan p = plan_dense(true, a.m, a.n, a.pitch, kFP4);
+  const DensePlan p = plan_dense(true, a.m, a.n, a.pitch, kFP4, dense_terms(kFP4));
   return dense_prepare(p, &a) ? dense_run<kDenseF16, true, kFP4>(p, a, s) : hipErrorInvalidValue;
 }
 

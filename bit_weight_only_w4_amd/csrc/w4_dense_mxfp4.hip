@@ -5,7 +5,7 @@ namespace w4 {
 
 hipError_t launch_dense_mxfp4(const DenseArgs& args, hipStream_t s) {
   DenseArgs a = args;
-  const DensePlan p = plan_dense(true, a.m, a.n, a.pitch, kMXFP4);
+  const DensePlan p = plan_dense(true, a.m, a.n, a.pitch, kMXFP4, dense_terms(kMXFP4));
   return dense_prepare(p, &a) ? dense_run<kDenseF16, true, kMXFP4>(p, a, s) : hipErrorInvalidValue;
 }
 

@@ -66,15 +66,24 @@ __device__ inline uint32_t scaled_halves(uint32_t c, float s) {
   asm("v_fma_mixhi_f16 %0, %1, %2, 0 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "+v"(d) : "v"(c), "v"(s));
   return d;
 }
-// The weights of a packed dword, two of them at a time, in fp16: code (exact) times scale.
+// a * s - h rounded the same way, h the fp16 halves of a dword: what a first term leaves of a product.
+__device__ inline uint32_t rest_of_halves(uint32_t c, float s, uint32_t h) {
+  uint32_t d;
+  asm("v_fma_mixlo_f16 %0, %1, %2, -%3 op_sel_hi:[1,0,1]" : "=v"(d) : "v"(c), "v"(s), "v"(h));
+  asm("v_fma_mixhi_f16 %0, %1, %2, -%3 op_sel:[1,0,1] op_sel_hi:[1,0,1]" : "+v"(d) : "v"(c), "v"(s), "v"(h));
+  return d;
+}
+
+// The weights of a packed dword, two of them at a time, in fp16: code (exact) times scale, or one of the two terms that
+// such a product is held in (first_term in w4_ffn_math.h).
 //   * E2M1: the hardware's conversion to fp16, which takes the low nibble first: the nibbles are swapped before.
 //     MXFP4's scales are powers of two, which it applies itself (NaN too).
 //   * INT4: the nibbles as bytes below 0x64, which is 1024 + q in fp16, less 1024 + the offset.
 //   * NF4: fp32 codes from a table in LDS, sixteen banks of it, so lanes never wait for each other.
-template <int FMT>
+template <int FMT, int TERMS>
 struct DenseDecoder {
   uint32_t a, b;
-  float s;
+  float s, s1;  // the scale, and the first term's
   uint32_t bias;
   float code[8];  // NF4: asked for some matrix instructions before they are used
   template <int J>
@@ -85,6 +94,7 @@ struct DenseDecoder {
   }
   __device__ inline void set(uint32_t w, BlockScale k) {
     s = k.s;
+    s1 = TERMS == 2 ? first_term(s) : s;
     if constexpr (FMT == kFP4 || FMT == kMXFP4) {
       a = ((w >> 4) & 0x0F0F0F0Fu) | ((w & 0x0F0F0F0Fu) << 4);
     } else if constexpr (FMT == kNF4) {
@@ -98,19 +108,28 @@ struct DenseDecoder {
       bias = (uint32_t)__builtin_bit_cast(uint16_t, z) * 0x10001u;
     }
   }
-  template <int J>
+  // Pair J of the dword, its term T.
+  template <int J, int T>
   __device__ inline uint32_t pair() const {
     if constexpr (FMT == kMXFP4) {
       return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(a, s, J));
-    } else if constexpr (FMT == kFP4) {
-      return scaled_halves(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(a, 1.0f, J)), s);
     } else if constexpr (FMT == kNF4) {
-      return scaled_pair(code[2 * J], code[2 * J + 1], s);
+      const uint32_t h = scaled_pair(code[2 * J], code[2 * J + 1], s1);
+      return T == 0 ? h : rest_of_pair(code[2 * J], code[2 * J + 1], s, h);
+    } else {
+      const uint32_t c = halves<J>(), h = scaled_halves(c, s1);
+      return T == 0 ? h : rest_of_halves(c, s, h);
+    }
+  }
+  // The codes of pair J as fp16 numbers.
+  template <int J>
+  __device__ inline uint32_t halves() const {
+    if constexpr (FMT == kFP4) {
+      return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(a, 1.0f, J));
     } else {
       typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
       const uint32_t q = __builtin_amdgcn_perm(0x64646464u, J < 2 ? a : b, J & 1 ? 0x04030402u : 0x04010400u);
-      return scaled_halves(
-          __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, q) - __builtin_bit_cast(half2_t, bias)), s);
+      return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, q) - __builtin_bit_cast(half2_t, bias));
     }
   }
 };
@@ -119,7 +138,7 @@ constexpr int kRawBytes = 64 * 16 + 64 * 4;  // a step's packed bytes and scales
 
 // Rows of packed weights along K (w4_gated): a wave has 32 rows of the tile, a lane 32 weights of row lane / 2 in a step, in
 // chunks of 8.  The scales are folded (w4_gated.hip), two numbers a step.
-template <int FMT, int TM, int TN, int W, int STAGES>
+template <int FMT, int TERMS, int TM, int TN, int W, int STAGES>
 struct PackedRows {
   static_assert(TN == 32 * W, "32 rows of B a wave");
   uint8_t* own;
@@ -132,7 +151,7 @@ struct PackedRows {
   uint4 ahead_w[STAGES];
   float ahead_s[STAGES];
   BlockScale scale;
-  DenseDecoder<FMT> dec;
+  DenseDecoder<FMT, TERMS> dec;
   uint32_t made[4];
 
   // Rows n0 .. of the tile, gate rows first (CN of them, `nrows` exist), then up rows.
@@ -142,7 +161,7 @@ struct PackedRows {
     own = raw + wave * kRawBytes;
     ring = stages;
     table = codes;
-    steps = last;
+    steps = last / TERMS;  // of A's
     lane = (uint32_t)lane_;
     const uint32_t r = 32 * wave, up = r >= CN ? 1u : 0u, at = r - (up ? CN : 0u);
     const size_t row = (size_t)(up ? p.n : 0u) + n0 + at;
@@ -159,7 +178,7 @@ struct PackedRows {
     const __amdgpu_buffer_rsrc_t bw = dense_buffer(rw), bs = dense_buffer(rs);
 #pragma unroll
     for (int i = 0; i < STAGES; ++i) {
-      const uint32_t t = first + i;
+      const uint32_t t = (first + i) / TERMS;
       ahead_w[i] = __builtin_bit_cast(
           uint4, __builtin_amdgcn_raw_buffer_load_b128(bw, woff + (t < steps ? t * 32 : 0x40000000u), 0, 0));
       ahead_s[i] =
@@ -172,6 +191,7 @@ struct PackedRows {
     scales();
   }
   __device__ inline void copy(uint32_t t) {  // past the last step: from outside the buffers
+    t /= TERMS;
     dense_copy(rw, own, woff + (t < steps ? t * 32 : 0x40000000u));
     dense_copy4(rs, own + 1024, soff + (t < steps ? t * 8 : 0x40000000u));
   }
@@ -181,7 +201,7 @@ struct PackedRows {
   }
   __device__ inline void scales() {
     scale = BlockScale{s, 8.0f};
-    if constexpr (FMT == kINT4A) {  // the pair's first lane has the scale, its second the zero point
+    if constexpr (is_g128(FMT)) {  // the pair's first lane has the scale, its second the zero point
       const float other =
           __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(s), 0xB1, 0xF, 0xF, true));
       scale = half ? BlockScale{other, s} : BlockScale{s, other};
@@ -197,9 +217,9 @@ struct PackedRows {
     if (I == 0) dec.set(v[q], scale);
     if constexpr (FMT == kNF4) dec.template look<I>(table);
   }
-  template <int I>
+  template <int I, int T>
   __device__ inline void put(uint32_t stage, int q) {
-    made[I] = dec.template pair<I>();
+    made[I] = dec.template pair<I, T>();
     if (I == 3)
       *reinterpret_cast<uint4*>(ring + ((to + stage) ^ (uint32_t)(q * 16))) = make_uint4(made[0], made[1], made[2], made[3]);
   }
@@ -349,7 +369,7 @@ struct PackedColumns {
       code[2 * I + 1] = (float)(v & 15u);
     }
   }
-  template <int I>
+  template <int I, int T>
   __device__ inline void put(uint32_t stage, int q) {
     if constexpr (I % 2 == 1) {
       if constexpr (TYPE == kDenseF16) {

@@ -7,6 +7,10 @@ namespace w4 {
 // The operand types of the dense kernel (w4_dense.h).
 enum DenseType { kDenseF16 = 0, kDenseBF16 = 1, kDenseI8 = 2 };
 
+// fp16 terms that a weight of the format is the sum of in the dense kernel: integers and E2M1 times a power of two fit one
+// (at most 11 bits), the others take two, which leave at most 2^-20 of a weight.
+constexpr int dense_terms(int weight) { return weight == kNF4 || weight == kFP4 || weight == kINT4A ? 2 : 1; }
+
 // One dense product C[m, n] = sum_k A[m, k] B[n, k], both operands with K contiguous, and what becomes of it.
 struct DenseArgs {
   const uint8_t* a;  // [M, pitch] rows of operand bytes, 16-byte aligned
@@ -19,7 +23,8 @@ struct DenseArgs {
   uint32_t nparts;
   int* exp_out;        // where the exponent goes, for dense_sum_kernel (`exp`)
   uint32_t m, n;     // outputs (gated: N is the width of h)
-  uint32_t pitch;    // bytes of a row of either operand (its K elements), a multiple of 64, below 2^23
+  uint32_t pitch;    // bytes of a row of A (its K elements), a multiple of 64, below 2^22
+  uint32_t terms;    // B's rows in 16 bits: 1, or 2 where each 128 bytes are followed by 128 of second terms
   const float* row_scale;   // 8 bits: s[m]
   const float* col_scale;   // 8 bits: s[n]
   const int* row_exp;       // 16 bits: a row stands for its values times 2^row_exp[m]; may be null
@@ -37,15 +42,16 @@ struct DenseArgs {
 
 hipError_t launch_dense(int type, bool gated, const DenseArgs& a, hipStream_t s);
 // Scratch that a product of these sizes needs (its K split over workgroups): [splits, M, N or 2 N] of 4 bytes.
-// `packed`: the weight format of B in four bits, else -1.
-size_t dense_bytes(bool gated, int64_t m, int64_t n, int64_t pitch, int packed = -1);
-// The estimated time of a product without a gate, in microseconds.
-double dense_us(int64_t m, int64_t n, int64_t pitch, int packed);
+// `packed`: the weight format of B in four bits, else -1; `terms` of B's rows.
+size_t dense_bytes(bool gated, int64_t m, int64_t n, int64_t pitch, int packed, int terms);
+// The estimated time of a product, in microseconds.
+double dense_us(bool gated, int64_t m, int64_t n, int64_t pitch, int packed, int terms);
 // The gated product with B in four bits: A fp16.
 hipError_t launch_dense_nf4(const DenseArgs& a, hipStream_t s);
 hipError_t launch_dense_fp4(const DenseArgs& a, hipStream_t s);
 hipError_t launch_dense_mxfp4(const DenseArgs& a, hipStream_t s);
 hipError_t launch_dense_int4(const DenseArgs& a, hipStream_t s);
+hipError_t launch_dense_int4a(const DenseArgs& a, hipStream_t s);
 // The product with B transposed from four bits, of any format; A and the results fp16 or bf16.
 hipError_t launch_dense_columns_nf4(int type, const DenseArgs& a, hipStream_t s);
 hipError_t launch_dense_columns_fp4(int type, const DenseArgs& a, hipStream_t s);

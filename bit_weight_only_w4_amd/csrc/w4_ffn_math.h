@@ -73,6 +73,20 @@ __device__ inline uint32_t scaled_pair(float a, float b, float s) {
   return d;
 }
 
+// a * s - h rounded the same way, h the fp16 halves of a dword.
+__device__ inline uint32_t rest_of_pair(float a, float b, float s, uint32_t h) {
+  uint32_t d;
+  asm("v_fma_mixlo_f16 %0, %1, %2, -%3 op_sel_hi:[0,0,1]" : "=v"(d) : "v"(a), "v"(s), "v"(h));
+  asm("v_fma_mixhi_f16 %0, %1, %2, -%3 op_sel:[0,0,1] op_sel_hi:[0,0,1]" : "+v"(d) : "v"(b), "v"(s), "v"(h));
+  return d;
+}
+
+// Two fp16 terms of a weight w = code * s: the first is rounded from code * first_term(s), which is w less 2^-10 of it,
+// the second from what that leaves of w.  It leaves 2^-11 to 1.5 * 2^-10 of w: so both have the weight's sign and neither
+// is 0 unless the weight is (or lies more than 2^28 below fp16's largest), and an infinite activation gives what it gives
+// with the weight itself.  The second is off by at most half its step, 2^-20.4 of w.
+__device__ inline float first_term(float s) { return s * (1.0f - 0x1p-10f); }
+
 // The 16-bit terms of an NF4 code in a gated launch, two fp16 or three bf16 ones: each but the last is what is left cut
 // towards zero (and one step short of it where it would be held whole), so that all have the code's sign and none is 0
 // unless the code is: an infinite activation then gives what it gives with the code itself.  bf16: the sum is the code

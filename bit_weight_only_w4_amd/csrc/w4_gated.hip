@@ -19,7 +19,7 @@ constexpr int kDecodeThreads = 256;
 struct DecodeArgs {
   const uint8_t* packed;  // [N, K/2]
   const void* scales;
-  uint16_t* w;   // [N, K] fp16: decoded rows
+  uint16_t* w;   // [N, K] fp16: decoded rows, or [N, K / 64, 2, 64]: first and second terms
   float2* fold;  // [N, K / 64], in place of w: what the dense kernel takes for 64 packed weights, the scales 2^-f of
                  // their halves, for integer formats the scale 2^-f and the codes' offset
   int* w_exp;    // [N]
@@ -126,7 +126,8 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_rows_kernel(DecodeArgs 
       top = a < __builtin_inff() ? fmaxf(top, a) : top;  // infinities and NaN have no binade
     };
     const uint32_t* src = reinterpret_cast<const uint32_t*>(p.packed + (size_t)row * (p.k / 2));
-    uint4* dst = reinterpret_cast<uint4*>(p.w + (size_t)row * p.k);
+    constexpr int TERMS = dense_terms(FMT);
+    uint4* dst = reinterpret_cast<uint4*>(p.w + (size_t)row * p.k * TERMS);
     uint32_t v[kHeld];
     BlockScale s[kHeld];
 #pragma unroll
@@ -145,14 +146,26 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_rows_kernel(DecodeArgs 
     if (lane == 0) p.w_exp[row] = f;
     auto put = [&](uint32_t i, uint32_t w, BlockScale b) __attribute__((always_inline)) {
       b.s = ldexpf(b.s, -f);
-      uint32_t o[4];
+      uint32_t o[4], r[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         float lo, hi;
-        decode_pair<FMT>(w, j, table, b, &lo, &hi);
-        o[j] = to16<kF16>(lo) | (to16<kF16>(hi) << 16);
+        if constexpr (TERMS == 1) {
+          decode_pair<FMT>(w, j, table, b, &lo, &hi);
+          o[j] = to16<kF16>(lo) | (to16<kF16>(hi) << 16);
+        } else {
+          decode_pair<FMT>(w, j, table, BlockScale{1.0f, b.zero}, &lo, &hi);
+          o[j] = scaled_pair(lo, hi, first_term(b.s));
+          r[j] = rest_of_pair(lo, hi, b.s, o[j]);
+        }
       }
-      dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+      if constexpr (TERMS == 1) {
+        dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+      } else {
+        const uint32_t at = i / 8 * 16 + i % 8;
+        dst[at] = make_uint4(o[0], o[1], o[2], o[3]);
+        dst[at + 8] = make_uint4(r[0], r[1], r[2], r[3]);
+      }
     };
 #pragma unroll
     for (int j = 0; j < kHeld; ++j)
@@ -189,7 +202,7 @@ GatedSpace gated_space(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
   GatedSpace g;
   const bool packed = gated_packed(fmt, tokens);
   g.w = 0;
-  g.w_exp = up16(packed ? (size_t)(2 * inter) * (size_t)(hidden / 64) * 8 : (size_t)(2 * inter * hidden) * 2);
+  g.w_exp = up16(packed ? (size_t)(2 * inter) * (size_t)(hidden / 64) * 8 : (size_t)(2 * inter * hidden) * 2 * dense_terms(fmt_weight(fmt)));
   g.xh = g.w_exp + up16((size_t)(2 * inter) * 4);
   g.x_exp = g.xh;
   g.partial = g.xh;
@@ -197,7 +210,8 @@ GatedSpace gated_space(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
     g.x_exp = g.xh + up16((size_t)(tokens * hidden) * 2);
     g.partial = g.x_exp + up16((size_t)tokens * 4);
   }
-  g.bytes = g.partial + up16(dense_bytes(true, tokens, inter, 2 * hidden, packed ? fmt_weight(fmt) : -1));
+  g.bytes = g.partial + up16(dense_bytes(true, tokens, inter, 2 * hidden, packed ? fmt_weight(fmt) : -1,
+                                       dense_terms(fmt_weight(fmt))));
   return g;
 }
 
@@ -312,6 +326,7 @@ hipError_t launch_gated(int fmt, int act, const uint16_t* x, const uint8_t* pack
   a.m = (uint32_t)tokens;
   a.n = (uint32_t)inter;
   a.pitch = (uint32_t)(2 * hidden);
+  a.terms = (uint32_t)dense_terms(fmt_weight(fmt));
   a.row_exp = convert ? d.x_exp : nullptr;
   a.col_exp = d.w_exp;
   a.partial = reinterpret_cast<uint32_t*>(base + g.partial);
@@ -324,7 +339,8 @@ hipError_t launch_gated(int fmt, int act, const uint16_t* x, const uint8_t* pack
     case kNF4: return launch_dense_nf4(a, s);
     case kFP4: return launch_dense_fp4(a, s);
     case kMXFP4: return launch_dense_mxfp4(a, s);
-    default: return launch_dense_int4(a, s);
+    case kINT4: return launch_dense_int4(a, s);
+    default: return launch_dense_int4a(a, s);
   }
 }
 

@@ -172,7 +172,7 @@ size_t up16(size_t v) { return (v + 15) & ~(size_t)15; }
 //   INT4 fp16  28672 x 4096: 80 59 / 152, 512 142 / 203, 2048 478 / 474;  17920 x 1536: 2048 133 / 142
 bool grad_columns(int fmt, int64_t n, int64_t k, int64_t b) {
   const int64_t pitch = (n + kTile - 1) / kTile * kTile * 2;
-  return b <= 2048 && dense_us(b, k, pitch, fmt_weight(fmt)) < dense_us(b, k, pitch, -1) + 3 + (double)n * k * 2.5 / 4e6;
+  return b <= 2048 && dense_us(false, b, k, pitch, fmt_weight(fmt), 1) < dense_us(false, b, k, pitch, -1, 1) + 3 + (double)n * k * 2.5 / 4e6;
 }
 
 struct GradSpace {
@@ -188,7 +188,7 @@ GradSpace grad_space(int fmt, int64_t n, int64_t k, int64_t b) {
   g.parts = g.d + up16((size_t)b * g.np * 2);
   g.exp = g.parts + kMaxParts * 4;
   g.partial = g.exp + 16;
-  g.bytes = g.partial + up16(dense_bytes(false, b, k, (int64_t)g.np * 2, columns ? fmt_weight(fmt) : -1));
+  g.bytes = g.partial + up16(dense_bytes(false, b, k, (int64_t)g.np * 2, columns ? fmt_weight(fmt) : -1, 1));
   return g;
 }
 
@@ -276,6 +276,7 @@ hipError_t launch_gemm_grad(int fmt, const uint16_t* d, const uint8_t* packed, c
   a.m = (uint32_t)b;
   a.n = (uint32_t)k;
   a.pitch = g.np * 2;
+  a.terms = 1;
   a.exp = xt == kF16 ? reinterpret_cast<const int*>(base + g.exp) : nullptr;
   a.partial = reinterpret_cast<uint32_t*>(base + g.partial);
   a.out = dx;

@@ -76,7 +76,7 @@ def _check(got, ref, terms):
 
 
 @pytest.mark.parametrize("fmt", INEXACT)
-@pytest.mark.parametrize("tokens", [1, 2, 7, 33, 64, 100, 128])
+@pytest.mark.parametrize("tokens", [1, 2, 7, 33, 64, 100, 128, 129, 200, 257, 400, 1100])
 def test_gated_products_of_nearly_equal_weights(fmt, tokens):
     """Each token takes one weight of a block less one of the next, in every row."""
     w4, dev, dtype = _w4(), f.device(), f.DTYPES[fmt.split("_")[1]]
@@ -137,7 +137,8 @@ def test_gradient_reads_weights_out(fmt, tokens, n, k):
 
 
 @pytest.mark.parametrize("fmt", f.FMTS)
-@pytest.mark.parametrize("tokens,hidden,inter", [(1, 384, 40), (1, 4160, 77), (5, 640, 33), (64, 384, 100), (128, 1152, 77)])
+@pytest.mark.parametrize("tokens,hidden,inter", [(1, 384, 40), (1, 4224, 77), (5, 640, 33), (64, 384, 100), (128, 1152, 77), (129, 640, 200),
+                                                 (300, 2176, 333), (512, 4224, 40), (700, 640, 3000), (2049, 384, 90)])
 def test_gated_products_read_weights_out(fmt, tokens, hidden, inter):
     w4, dev, dtype = _w4(), f.device(), f.DTYPES[fmt.split("_")[1]]
     p, s = _raw_weights(fmt, 2 * inter, hidden, tokens)
