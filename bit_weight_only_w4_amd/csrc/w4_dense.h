@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
   constexpr int W = WM * WN, TM = 32 * MT * WM, TN = 32 * NT * WN;
   constexpr int ROWS = TM + TN;             // rows of a stage
   constexpr bool PACKED = FMT >= 0;         // B in four bits
-  constexpr int TERMS = PACKED && GATED ? dense_terms(FMT) : 1;  // known when compiled
+  constexpr int TERMS = PACKED && TYPE == kDenseF16 ? dense_terms(FMT) : 1;  // known when compiled
   constexpr int COPIES = (PACKED ? TM : ROWS) / 8 / W;  // copies of 8 rows a wave makes for a stage
   static_assert(TM % (8 * W) == 0 && (PACKED || (GATED ? TN / 2 : TN) % (8 * W) == 0),
                 "a round of copies fills one operand");
@@ -193,18 +193,21 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
   constexpr int C1 = COPIES < 3 * C3 ? COPIES : 3 * C3;
   constexpr int SF = PACKED ? FMT : kFP4, SN = PACKED ? TN : 32 * W;  // (a source that is never used otherwise)
   using Source = typename std::conditional<GATED, PackedRows<SF, PACKED ? TERMS : 1, TM, SN, W, STAGES>,
-                                           PackedColumns<SF, TYPE, TM, SN, W, STAGES>>::type;
+                                           PackedColumns<SF, PACKED ? TERMS : 1, TYPE, TM, SN, W, STAGES>>::type;
   Source src;
-  int all = 0;  // the exponent of all of B
+  constexpr bool EXPONENTS = COLUMNS && TYPE == kDenseF16;  // of units of columns
+  constexpr int UNIT = column_unit(SF);
+  __shared__ int exps[EXPONENTS ? TN / UNIT : 1];
   if constexpr (PACKED && GATED) src.init(p, n0, nrows, steps, raw, &ring[0][0], table, lane, wave);
   if constexpr (COLUMNS) {
-    if constexpr (TYPE == kDenseF16) {  // from the scan's maxima, every wave for itself
-      float top = 0.0f;
-      for (uint32_t i = lane; i < p.nparts; i += 64) top = fmaxf(top, p.parts[i]);
-      all = fold_exponent<FMT>(wave_max(top));
-      if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *p.exp_out = all;
+    src.init(p, n0, steps, raw, &ring[0][0], table, lane, wave);
+    if constexpr (EXPONENTS) {
+      static_assert(TN / UNIT <= W, "a wave for each unit");
+      if (wave < TN / UNIT) {
+        const int e = unit_exponent<FMT>(p.parts, p.nparts, p.n / UNIT, n0 / UNIT + wave, lane);
+        if (lane == 0) exps[wave] = e;
+      }
     }
-    src.init(p, n0, steps, all, raw, &ring[0][0], table, lane, wave);
   }
   // A quarter: after each matrix instruction one of the next quarter's fragments is requested, and a copy now and then.
   // What it decodes are weights of step t, of their term `of`.
@@ -250,7 +253,11 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
   if constexpr (PACKED) {
     code_table<FMT>(table);
     src.first_steps(first);
-    __syncthreads();  // the table
+    __syncthreads();  // the table and the exponents
+    if constexpr (EXPONENTS) {
+      src.f = exps[src.unit];
+      if (m0 == 0 && blockIdx.y == 0 && tid < TN && n0 + tid < p.n) p.exp_out[n0 + tid] = exps[tid / UNIT];
+    }
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i)
 #pragma unroll
@@ -339,9 +346,11 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const uint32_t n = nw + 32 * (GATED ? j / 2 : j) + c;
-    cv[j] = cols_of && n < p.n ? reinterpret_cast<const uint32_t*>(cols_of)[(GATED && (j & 1) ? p.n : 0u) + n] : 0u;
+    if constexpr (EXPONENTS)
+      cv[j] = (uint32_t)exps[(n - n0) / UNIT];
+    else
+      cv[j] = cols_of && n < p.n ? reinterpret_cast<const uint32_t*>(cols_of)[(GATED && (j & 1) ? p.n : 0u) + n] : 0u;
   }
-  if constexpr (TYPE != kDenseI8 && !COLUMNS) all = p.exp ? *p.exp : 0;
   // One output's 32 rows from row `mw` on, in LDS, to memory.
   auto flush = [&](void* out, uint32_t pitch, uint32_t n, uint32_t nend, uint32_t mw) __attribute__((always_inline)) {
     asm volatile("" ::: "memory");  // a wave's LDS accesses keep their order; the compiler's must too
@@ -378,7 +387,7 @@ __global__ void __launch_bounds__(64 * WM * WN) dense_kernel(DenseArgs p) {
       if constexpr (TYPE == kDenseI8)
         return (float)acc[i][j][e] * __uint_as_float(rv[e]) * __uint_as_float(cv[j]);
       else
-        return ldexpf(acc[i][j][e], (int)rv[e] + (int)cv[j] + all);
+        return ldexpf(acc[i][j][e], (int)rv[e] + (int)cv[j]);
     };
     auto put = [&](int e, int j, float v) __attribute__((always_inline)) {
       stage[(8 * (e / 4) + 4 * h + e % 4) * CW + 32 * j + c] =
@@ -445,7 +454,7 @@ __global__ void __launch_bounds__(256) dense_sum_kernel(DenseArgs p) {
     }
   }
   const float rs = TYPE == kDenseI8 ? p.row_scale[m] : 0.0f;
-  const int re = TYPE == kDenseI8 ? 0 : (p.row_exp ? p.row_exp[m] : 0) + (p.exp ? *p.exp : 0);
+  const int re = TYPE == kDenseI8 || !p.row_exp ? 0 : p.row_exp[m];
   float v[3][V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {

@@ -3,11 +3,10 @@
 
 namespace w4 {
 
-hipError_t launch_dense_columns_fp4(int type, const DenseArgs& args, hipStream_t s) {
+hipError_t launch_dense_columns_fp4(const DenseArgs& args, hipStream_t s) {
   DenseArgs a = args;
-  const DensePlan p = plan_dense(false, a.m, a.n, a.pitch, kFP4, 1);
-  if (!dense_prepare(p, &a)) return hipErrorInvalidValue;
-  return type == kDenseF16 ? dense_run<kDenseF16, false, kFP4>(p, a, s) : dense_run<kDenseBF16, false, kFP4>(p, a, s);
+  const DensePlan p = plan_dense(false, a.m, a.n, a.pitch, kFP4, dense_terms(kFP4));
+  return dense_prepare(p, &a) ? dense_run<kDenseF16, false, kFP4>(p, a, s) : hipErrorInvalidValue;
 }
 
 }  // namespace w4

@@ -3,11 +3,10 @@
 
 namespace w4 {
 
-hipError_t launch_dense_columns_int4a(int type, const DenseArgs& args, hipStream_t s) {
+hipError_t launch_dense_columns_int4a(const DenseArgs& args, hipStream_t s) {
   DenseArgs a = args;
-  const DensePlan p = plan_dense(false, a.m, a.n, a.pitch, kINT4A, 1);
-  if (!dense_prepare(p, &a)) return hipErrorInvalidValue;
-  return type == kDenseF16 ? dense_run<kDenseF16, false, kINT4A>(p, a, s) : dense_run<kDenseBF16, false, kINT4A>(p, a, s);
+  const DensePlan p = plan_dense(false, a.m, a.n, a.pitch, kINT4A, dense_terms(kINT4A));
+  return dense_prepare(p, &a) ? dense_run<kDenseF16, false, kINT4A>(p, a, s) : hipErrorInvalidValue;
 }
 
 }  // namespace w4

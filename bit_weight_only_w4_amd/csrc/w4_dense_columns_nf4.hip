@@ -3,11 +3,10 @@
 
 namespace w4 {
 
-hipError_t launch_dense_columns_nf4(int type, const DenseArgs& args, hipStream_t s) {
+hipError_t launch_dense_columns_nf4(const DenseArgs& args, hipStream_t s) {
   DenseArgs a = args;
-  const DensePlan p = plan_dense(false, a.m, a.n, a.pitch, kNF4, 1);
-  if (!dense_prepare(p, &a)) return hipErrorInvalidValue;
-  return type == kDenseF16 ? dense_run<kDenseF16, false, kNF4>(p, a, s) : dense_run<kDenseBF16, false, kNF4>(p, a, s);
+  const DensePlan p = plan_dense(false, a.m, a.n, a.pitch, kNF4, dense_terms(kNF4));
+  return dense_prepare(p, &a) ? dense_run<kDenseF16, false, kNF4>(p, a, s) : hipErrorInvalidValue;
 }
 
 }  // namespace w4

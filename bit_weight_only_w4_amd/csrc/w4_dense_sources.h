@@ -238,8 +238,9 @@ __device__ inline uint32_t fma_halves(float a, float s, float add, float b, floa
 // .. 4 a + 3 among them; a quarter is the two columns of a byte, four weights of each, 8 bytes of a stage's row.
 //   * The chunks of stage row r are keyed on (r / 2) xor (r / 8): 32 lanes write to every eighth row, and so to 8 slots; the
 //     rows that a 16-lane group reads still have 8 different keys.
-//   * Scales come in the format's own form: one for each row and 64 or 128 columns; fp16 takes them times 2^-f.
-template <int FMT, int TYPE, int TM, int TN, int W, int STAGES>
+//   * Scales come in the format's own form: one for each row and 64 or 128 columns; fp16 takes them times 2^-f, f of a
+//     unit of columns, and where TERMS is 2 a weight in its two terms.
+template <int FMT, int TERMS, int TYPE, int TM, int TN, int W, int STAGES>
 struct PackedColumns {
   static_assert(TN == 32 * W, "64 rows of weights in the waves of a workgroup");
   static constexpr uint32_t RPW = 64 / W;        // rows a wave
@@ -258,19 +259,19 @@ struct PackedColumns {
   bool odd;  // MXFP4: the second 32 columns of a unit
   uint32_t w[4], b[4];
   uint32_t ahead_w[STAGES][4], ahead_b[STAGES][4];
-  float s[4], add[4];
+  float s[4], add[4];    // w = code * s + add
+  float s1[4], add1[4];  // what its first term is rounded from
   float code[8];
   uint32_t lo[2], hi[2];
 
-  __device__ inline void init(const DenseArgs& p, uint32_t k0, uint32_t last, int exponent, uint8_t* raw, uint8_t* stages,
+  __device__ inline void init(const DenseArgs& p, uint32_t k0, uint32_t last, uint8_t* raw, uint8_t* stages,
                               const float* codes, int lane_, int wave) {
     own = raw + wave * kRawBytes;
     ring = stages;
     table = codes;
     lane = (uint32_t)lane_;
-    steps = last;
+    steps = last / TERMS;  // of A's
     n = p.rows;
-    f = exponent;
     wbytes = p.n / 2;
     sbytes = p.n / (is_g128(FMT) ? 128 : 64) * SB;
     wstep = (uint64_t)wbytes * 64;
@@ -301,8 +302,8 @@ struct PackedColumns {
   __device__ inline void first_steps(uint32_t first) {
 #pragma unroll
     for (int i = 0; i < STAGES; ++i) {
-      const __amdgpu_buffer_rsrc_t bw = dense_buffer(rows_of(packed, wstep, wbytes, first + i));
-      const __amdgpu_buffer_rsrc_t bs = dense_buffer(rows_of(scale_rows, sstep, sbytes, first + i));
+      const __amdgpu_buffer_rsrc_t bw = dense_buffer(rows_of(packed, wstep, wbytes, (first + i) / TERMS));
+      const __amdgpu_buffer_rsrc_t bs = dense_buffer(rows_of(scale_rows, sstep, sbytes, (first + i) / TERMS));
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         ahead_w[i][r] = __builtin_amdgcn_raw_buffer_load_b32(bw, dcol + r * wbytes, 0, 0);
@@ -318,6 +319,7 @@ struct PackedColumns {
     scales();
   }
   __device__ inline void copy(uint32_t t) {
+    t /= TERMS;
     dense_copy(rows_of(packed, wstep, wbytes, t), own, woff);
     const i32x4 rs = rows_of(scale_rows, sstep, sbytes, t);
     if constexpr (SB == 2)
@@ -346,7 +348,9 @@ struct PackedColumns {
         s[r] = __uint_as_float(b[r]);
       if constexpr (FMT == kINT4A) zero = (float)((b[r] >> 16) & 15u);
       if constexpr (TYPE == kDenseF16) s[r] = ldexpf(s[r], -f);
+      s1[r] = TERMS == 2 ? first_term(s[r]) : s[r];
       add[r] = is_g128(FMT) ? -zero * s[r] : 0.0f;  // exact: 8 and 4 bits
+      add1[r] = is_g128(FMT) ? -zero * s1[r] : 0.0f;  // exact: 18 and 4
     }
   }
   __device__ inline void settle() {
@@ -369,18 +373,21 @@ struct PackedColumns {
       code[2 * I + 1] = (float)(v & 15u);
     }
   }
+  // Term T of the weights of codes a and b, of rows I - 1 and I.
+  template <int I, int T>
+  __device__ inline uint32_t pair(float a, float b) const {
+    if constexpr (TYPE != kDenseF16) return bf16_pair(a * s[I - 1], b * s[I]);  // (MXFP4: exact)
+    const uint32_t h = fma_halves(a, s1[I - 1], add1[I - 1], b, s1[I], add1[I]);
+    if constexpr (T == 0) return h;
+    if constexpr (is_g128(FMT))  // (the sums are exact: 12 bits)
+      return rest_of_pair(__builtin_fmaf(a, s[I - 1], add[I - 1]), __builtin_fmaf(b, s[I], add[I]), 1.0f, 1.0f, h);
+    return rest_of_pair(a, b, s[I - 1], s[I], h);
+  }
   template <int I, int T>
   __device__ inline void put(uint32_t stage, int q) {
     if constexpr (I % 2 == 1) {
-      if constexpr (TYPE == kDenseF16) {
-        lo[I / 2] = fma_halves(code[2 * I - 2], s[I - 1], add[I - 1], code[2 * I], s[I], add[I]);
-        hi[I / 2] = fma_halves(code[2 * I - 1], s[I - 1], add[I - 1], code[2 * I + 1], s[I], add[I]);
-      } else {
-        lo[I / 2] = to16<kBF16>(__builtin_fmaf(code[2 * I - 2], s[I - 1], add[I - 1])) |
-                    (to16<kBF16>(__builtin_fmaf(code[2 * I], s[I], add[I])) << 16);
-        hi[I / 2] = to16<kBF16>(__builtin_fmaf(code[2 * I - 1], s[I - 1], add[I - 1])) |
-                    (to16<kBF16>(__builtin_fmaf(code[2 * I + 1], s[I], add[I])) << 16);
-      }
+      lo[I / 2] = pair<I, T>(code[2 * I - 2], code[2 * I]);
+      hi[I / 2] = pair<I, T>(code[2 * I - 1], code[2 * I + 1]);
     }
     if (I == 3) {
       uint8_t* at = ring + ((to + stage) ^ (uint32_t)(q * 16)) + 2 * q * 128;

@@ -11,17 +11,21 @@ enum DenseType { kDenseF16 = 0, kDenseBF16 = 1, kDenseI8 = 2 };
 // (at most 11 bits), the others take two, which leave at most 2^-20 of a weight.
 constexpr int dense_terms(int weight) { return weight == kNF4 || weight == kFP4 || weight == kINT4A ? 2 : 1; }
 
+// Columns of W that share an exponent in a gradient's product: one scale of each row, or MXFP4's two.
+constexpr int column_unit(int weight) { return weight == kINT4 || weight == kINT4A ? 128 : 64; }
+
 // One dense product C[m, n] = sum_k A[m, k] B[n, k], both operands with K contiguous, and what becomes of it.
 struct DenseArgs {
   const uint8_t* a;  // [M, pitch] rows of operand bytes, 16-byte aligned
   const uint8_t* b;  // [N, pitch]; gated: [2 N, pitch], gate rows, then up rows
   // B in four bits: b holds packed weights.  Gated: B's rows, with the folded scales [rows, K / 64, 2] of w4_gated.hip.
-  // Without a gate: the weights [rows, N / 2] and their scales as they are, transposed; fp16 takes the exponent from parts.
+  // Without a gate: the weights [rows, N / 2] and their scales as they are, transposed; fp16 takes an exponent for each unit
+  // of columns (column_unit) from parts.
   const void* scales;
   uint32_t rows;       // without a gate: weight rows, of which the last step of K may hold fewer than 64
-  const float* parts;  // maxima of the scales
+  const float* parts;  // [nparts, N / unit]: maxima of the scales
   uint32_t nparts;
-  int* exp_out;        // where the exponent goes, for dense_sum_kernel (`exp`)
+  int* exp_out;        // [N]: where the columns' exponents go, for dense_sum_kernel (`col_exp`)
   uint32_t m, n;     // outputs (gated: N is the width of h)
   uint32_t pitch;    // bytes of a row of A (its K elements), a multiple of 64, below 2^22
   uint32_t terms;    // B's rows in 16 bits: 1, or 2 where each 128 bytes are followed by 128 of second terms
@@ -29,7 +33,6 @@ struct DenseArgs {
   const float* col_scale;   // 8 bits: s[n]
   const int* row_exp;       // 16 bits: a row stands for its values times 2^row_exp[m]; may be null
   const int* col_exp;       // 16 bits: the same for B's rows; may be null
-  const int* exp;           // 16 bits: one exponent for all of B; may be null
   void* out;         // [M, N]
   void* products;    // gated: [M, 2 N] or null
   uint32_t out_type;  // w4_type_t; fp32 for 8-bit products without a gate alone
@@ -52,12 +55,12 @@ hipError_t launch_dense_fp4(const DenseArgs& a, hipStream_t s);
 hipError_t launch_dense_mxfp4(const DenseArgs& a, hipStream_t s);
 hipError_t launch_dense_int4(const DenseArgs& a, hipStream_t s);
 hipError_t launch_dense_int4a(const DenseArgs& a, hipStream_t s);
-// The product with B transposed from four bits, of any format; A and the results fp16 or bf16.
-hipError_t launch_dense_columns_nf4(int type, const DenseArgs& a, hipStream_t s);
-hipError_t launch_dense_columns_fp4(int type, const DenseArgs& a, hipStream_t s);
+// The product with B transposed from four bits: A fp16, for MXFP4 of either type.
+hipError_t launch_dense_columns_nf4(const DenseArgs& a, hipStream_t s);
+hipError_t launch_dense_columns_fp4(const DenseArgs& a, hipStream_t s);
 hipError_t launch_dense_columns_mxfp4(int type, const DenseArgs& a, hipStream_t s);
-hipError_t launch_dense_columns_int4(int type, const DenseArgs& a, hipStream_t s);
-hipError_t launch_dense_columns_int4a(int type, const DenseArgs& a, hipStream_t s);
+hipError_t launch_dense_columns_int4(const DenseArgs& a, hipStream_t s);
+hipError_t launch_dense_columns_int4a(const DenseArgs& a, hipStream_t s);
 
 // ---- gated block over 4-bit weights
 bool gated_few(int fmt, int64_t tokens, int64_t hidden, int64_t inter);

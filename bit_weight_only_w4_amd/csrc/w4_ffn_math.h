@@ -65,21 +65,23 @@ __device__ inline uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{a, b}), bf2));
 }
 
-// a * s and b * s, rounded to fp32 and to fp16, in a dword.
-__device__ inline uint32_t scaled_pair(float a, float b, float s) {
+// a * s and b * t, rounded to fp32 and to fp16, in a dword.
+__device__ inline uint32_t scaled_pair(float a, float b, float s, float t) {
   uint32_t d;
   asm("v_fma_mixlo_f16 %0, %1, %2, 0" : "=v"(d) : "v"(a), "v"(s));
-  asm("v_fma_mixhi_f16 %0, %1, %2, 0" : "+v"(d) : "v"(b), "v"(s));
+  asm("v_fma_mixhi_f16 %0, %1, %2, 0" : "+v"(d) : "v"(b), "v"(t));
   return d;
 }
+__device__ inline uint32_t scaled_pair(float a, float b, float s) { return scaled_pair(a, b, s, s); }
 
-// a * s - h rounded the same way, h the fp16 halves of a dword.
-__device__ inline uint32_t rest_of_pair(float a, float b, float s, uint32_t h) {
+// a * s and b * t less h, rounded the same way, h the fp16 halves of a dword.
+__device__ inline uint32_t rest_of_pair(float a, float b, float s, float t, uint32_t h) {
   uint32_t d;
   asm("v_fma_mixlo_f16 %0, %1, %2, -%3 op_sel_hi:[0,0,1]" : "=v"(d) : "v"(a), "v"(s), "v"(h));
-  asm("v_fma_mixhi_f16 %0, %1, %2, -%3 op_sel:[0,0,1] op_sel_hi:[0,0,1]" : "+v"(d) : "v"(b), "v"(s), "v"(h));
+  asm("v_fma_mixhi_f16 %0, %1, %2, -%3 op_sel:[0,0,1] op_sel_hi:[0,0,1]" : "+v"(d) : "v"(b), "v"(t), "v"(h));
   return d;
 }
+__device__ inline uint32_t rest_of_pair(float a, float b, float s, uint32_t h) { return rest_of_pair(a, b, s, s, h); }
 
 // Two fp16 terms of a weight w = code * s: the first is rounded from code * first_term(s), which is w less 2^-10 of it,
 // the second from what that leaves of w.  It leaves 2^-11 to 1.5 * 2^-10 of w: so both have the weight's sign and neither
@@ -182,6 +184,15 @@ __device__ inline float wave_max(float v) {
 #pragma unroll
   for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
   return v;
+}
+
+// The exponent of unit `unit` (of `units`) of columns from the scan's maxima, by a wave.
+template <int FMT>
+__device__ inline int unit_exponent(const float* parts, uint32_t nparts, uint32_t units, uint32_t unit, int lane) {
+  float top = 0.0f;
+  if (unit < units)
+    for (uint32_t i = lane; i < nparts; i += 64) top = fmaxf(top, parts[(size_t)i * units + unit]);
+  return fold_exponent<FMT>(wave_max(top));
 }
 
 }  // namespace

@@ -94,7 +94,8 @@ def test_gated_products_of_nearly_equal_weights(fmt, tokens):
 
 
 @pytest.mark.parametrize("fmt", INEXACT)
-@pytest.mark.parametrize("tokens,n,steps", [(1, 70, 2), (16, 640, 3), (32, 333, 2)])
+@pytest.mark.parametrize("tokens,n,steps", [(1, 70, 2), (16, 640, 3), (32, 333, 2), (33, 640, 2), (64, 1001, 2), (65, 129, 4),
+                                            (130, 20000, 9), (300, 640, 4), (600, 9000, 9)])
 def test_gradient_of_nearly_equal_weights(fmt, tokens, n, steps):
     """Each token takes the difference of two rows that are nearly equal in every column, the first and the last rows, and
     rows on both sides of steps among them."""
@@ -117,7 +118,9 @@ def test_gradient_of_nearly_equal_weights(fmt, tokens, n, steps):
 
 
 @pytest.mark.parametrize("fmt", f.FMTS)
-@pytest.mark.parametrize("tokens,n,k", [(1, 40, 384), (16, 1000, 512), (31, 4003, 384), (32, 28672, 1152)])
+@pytest.mark.parametrize("tokens,n,k", [(1, 40, 384), (16, 1000, 512), (31, 4003, 384), (32, 28672, 1152), (64, 700, 640),
+                                        (65, 8003, 2176), (130, 28000, 1152), (129, 200, 896), (333, 4001, 640),
+                                        (512, 20000, 1664), (1000, 28672, 4224), (2049, 300, 384)])
 def test_gradient_reads_weights_out(fmt, tokens, n, k):
     """Each token is one number in one row: a row of weights comes back, at one rounding.  The first, the last and the tail
     rows, rows on both sides of steps, and rows all over; other tokens' rows are far from it in value."""
