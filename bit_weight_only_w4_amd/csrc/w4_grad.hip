@@ -16,7 +16,7 @@ namespace w4 {
 namespace {
 
 constexpr int kTile = 64;       // weight rows of a tile
-constexpr int kMaxParts = 256;  // workgroups of the scale scan
+constexpr int kMaxParts = 512;  // workgroups of the scale scan
 
 // The largest finite scale of each unit of columns over rows [first, end), to `parts`.
 template <int FMT>
@@ -35,7 +35,7 @@ __device__ inline void scale_max(const void* scales, uint32_t first, uint32_t en
   if (units > 128) {
     for (uint32_t u = tid; u < units; u += 256) {
       float top = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
       for (uint32_t r = first; r < end; ++r) top = fold(top, r, u);
       parts[u] = top;
     }
@@ -44,7 +44,7 @@ __device__ inline void scale_max(const void* scales, uint32_t first, uint32_t en
   const uint32_t at_once = 256 / units, u = tid % units, r0 = tid / units;  // rows at once
   float top = 0.0f;
   if (r0 < at_once) {
-#pragma unroll 4
+#pragma unroll 8
     for (uint32_t r = first + r0; r < end; r += at_once) top = fold(top, r, u);
   }
   part[tid] = top;
@@ -72,7 +72,7 @@ __device__ inline void pad_row(const uint16_t* from, uint16_t* to, uint32_t n, u
 // A row of bf16 d as fp16 numbers times 2^e, zeros after its end up to `np`: e puts the row's largest into fp16's highest
 // binade but one, so that all that lie within 2^28 below it are exact.  A thread keeps the first kHeld pieces of 8 between
 // the pass for the largest and the one that writes.
-constexpr int kHeld = 2;
+constexpr int kHeld = 4;
 
 __device__ inline void convert_row(const uint16_t* from, uint16_t* to, int* exponent, uint32_t n, uint32_t np) {
   __shared__ uint32_t most[4];
@@ -101,6 +101,7 @@ __device__ inline void convert_row(const uint16_t* from, uint16_t* to, int* expo
     load(c0 + i * 2048, held[i]);
     fold(held[i]);
   }
+#pragma unroll 4
   for (uint32_t c = c0 + kHeld * 2048; c < n; c += 2048) {
     uint32_t v[4];
     load(c, v);
@@ -123,6 +124,7 @@ __device__ inline void convert_row(const uint16_t* from, uint16_t* to, int* expo
 #pragma unroll
   for (int i = 0; i < kHeld; ++i)
     if (c0 + i * 2048 < np) put(c0 + i * 2048, held[i]);
+#pragma unroll 2
   for (uint32_t c = c0 + kHeld * 2048; c < np; c += 2048) {
     uint32_t v[4];
     load(c, v);
