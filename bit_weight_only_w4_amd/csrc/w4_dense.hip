@@ -12,7 +12,7 @@ namespace w4 {
 // for 2048 x 1536 x 17920 fp16: 129 us, unsplit 128 x 256 tiles 262).  Where a last round of large tiles would leave
 // most CUs idle, its tiles are covered by smaller ones in a second launch.
 //
-// Four bits: decoding makes a step of the largest tile take 1.0 (MXFP4), 1.19 (FP4, INT4) or 1.3 (NF4) times as long, of
+// Four bits: decoding makes a step of the largest tile take 1.1 (MXFP4), 1.19 (FP4, INT4) or 1.3 (NF4) times as long, of
 // the others, whose rows of B meet fewer of A, 1.18 times that (160 and 256 tokens of 1536 -> 8960 to 8192 -> 28672).
 // Decoding columns: 1.07 (FP4, INT4), 1.1 (MXFP4) or 1.25 (NF4), 1.12 times that for 128 x 256, 2.2 and 1.62 for 64 x 128
 // (4096 x 2048 weights, 256 and 2048 tokens: a step of 64 x 128 tiles alone 0.71 to 1.07 us, of full CUs 1.14 to 1.5).
@@ -20,7 +20,7 @@ DensePlan plan_dense(bool gated, int64_t m, int64_t n, int64_t pitch, int packed
   const bool columns = packed >= 0 && !gated;
   const double slow = packed < 0         ? 1.0
                       : packed == kNF4   ? columns ? 1.25 : 1.3
-                      : packed == kMXFP4 ? columns ? 1.1 : 1.0
+                      : packed == kMXFP4 ? 1.1
                                          : columns ? 1.07 : 1.19;
   const int64_t cus = device_cu_count(), steps = (pitch + 127) / 128 * terms;
   const int64_t width = gated ? 2 * n : n;

@@ -81,7 +81,10 @@ size_t gemm_grad_workspace(int fmt, int64_t n, int64_t k, int64_t b);
 hipError_t launch_gemm_grad(int fmt, const uint16_t* d, const uint8_t* packed, const void* scales, int64_t n, int64_t k,
                             int64_t b, uint16_t* dx, void* ws, hipStream_t s);
 
-// The same for a few tokens, without decoded rows (w4_grad_few.h).
+// The same for a few tokens, without decoded rows (w4_grad_few.h), and how many those are at most (w4_grad.hip).
+constexpr int grad_few_most(int weight, int xt) {
+  return (weight == kINT4 && xt == kF16) || (weight == kMXFP4 && xt == kBF16) ? 32 : 64;
+}
 struct GradFewArgs {
   const uint16_t* d;      // [B, N]
   const uint8_t* packed;  // [N, K/2]

@@ -179,20 +179,22 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_rows_kernel(DecodeArgs 
 
 size_t up16(size_t v) { return (v + 15) & ~(size_t)15; }
 
-// Whether the dense kernel decodes the packed weights itself.  It does so once for every tile of up to 256 tokens, which
-// makes its steps up to half as long again (NF4; MXFP4, whose scales the conversion applies, little longer); the other way
-// the weights go through memory once more, at four times their size.  Microseconds, by the dense kernel / decoded first:
-//             2048 -> 8192   4096 -> 11008   8192 -> 28672
-//   NF4  256   46.5 / 48.3     99 / 100        324 / 511     512  61 / 58    135 / 151     577 / 740
-//   NF4  300   54 / 52        156 / 127        573 / 582    1000  91 / 89    283 / 222    1200 / 1106
-//   INT4 256   43 / 50         87 / 123        298 / 524     512  56 / 61    125 / 159     543 / 734   1000  83 / 89
-//                                                                                       255 / 228   1093 / 1097
-//   FP4  256   41 / 48         88 / 117        302 / 519     512  57 / 58    127 / 150     543 / 736   1000  85 / 86
-//                                                                                       248 / 221   1088 / 1110
-//   MXFP4 256  39 / 46         80 / 100        276 / 518    1000  76 / 82 (4096 -> 14336 231 / 275)     957 / 1062
-//   MXFP4 2048 (1536 -> 8960 135 / 134)  364 / 366  1668 / 1770;  4096 (264 / 240)  695 / 669  3288 / 3218
-bool gated_packed(int fmt, int64_t tokens) {
-  return tokens <= (fmt_weight(fmt) == kMXFP4 ? 2048 : fmt_weight(fmt) == kNF4 ? 256 : 512);
+// Whether the dense kernel decodes the packed weights itself, by the estimates of both: it decodes them once for every tile
+// of up to 256 tokens, which makes its steps up to half as long again; the other way the weights go through memory once
+// more, at 2 bytes a term and 4 TB/s.  Microseconds, by the dense kernel / decoded first (two terms: NF4, FP4, asymmetric
+// INT4); 70 measured pairs: the rule's way is at most 20% slower than the other (NF4, 2% at the mean of all).
+//                1536 -> 8960   4096 -> 11008   8192 -> 28672
+//   NF4   192      70 / 58       137 / 217       540 / 939      300  79 / 67    309 / 259  1094 / 1130
+//   NF4   512     131 / 95       231 / 313      1032 / 1387    2048 297 / 236   781 / 719  3818 / 3481
+//   FP4   192      56 / 58       126 / 220       503 / 934      512 110 / 94    213 / 313   961 / 1390
+//   INT4  192      34 / 41        87 / 101       284 / 493      300  41 / 46    138 / 141   498 / 594
+//   INT4  512      64 / 63       123 / 155       523 / 720     2048 152 / 141   388 / 370  1905 / 1812
+//   MXFP4 512      57 / 59       111 / 146       466 / 697     1000  78 / 80    213 / 211   924 / 1028
+//   MXFP4 2048    138 / 134      337 / 346      1660 / 1708    4096 254 / 234   681 / 637  3236 / 3119
+bool gated_packed(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
+  const int w = fmt_weight(fmt), terms = dense_terms(w);
+  return dense_us(true, tokens, inter, 2 * hidden, w, terms) <
+         dense_us(true, tokens, inter, 2 * hidden, -1, terms) + (double)(2 * inter) * hidden * (0.5 + 2 * terms) / 4e6;
 }
 
 struct GatedSpace {
@@ -200,7 +202,7 @@ struct GatedSpace {
 };
 GatedSpace gated_space(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
   GatedSpace g;
-  const bool packed = gated_packed(fmt, tokens);
+  const bool packed = gated_packed(fmt, tokens, hidden, inter);
   g.w = 0;
   g.w_exp = up16(packed ? (size_t)(2 * inter) * (size_t)(hidden / 64) * 8 : (size_t)(2 * inter * hidden) * 2 * dense_terms(fmt_weight(fmt)));
   g.xh = g.w_exp + up16((size_t)(2 * inter) * 4);
@@ -262,19 +264,21 @@ hipError_t grad_launch(const uint16_t* dh, const uint16_t* pr, uint16_t* dp, int
 
 // Whether the weights are streamed once past the tokens and decoded in registers (run_gated_few; no workspace).  Microseconds
 // so / by the dense kernel:
-//          1536 -> 8960   4096 -> 11008  8192 -> 28672 |            1536 -> 8960   4096 -> 11008  8192 -> 28672
-//   64 tokens                                          | 128 tokens
-//   INT4    19 / 25        51 / 57       143 / 170     |   INT4      31 / 33        69 / 61       257 / 208
-//   FP4     19 / 24        53 / 56       150 / 171     |   FP4       38 / 32        77 / 61       288 / 211
-//   NF4     22 / 30        61 / 67       187 / 195     |   NF4       42 / 39        88 / 67       328 / 228
-//   MXFP4   21 / 22        64 / 51       180 / 157     |   MXFP4     41 / 29        93 / 60       341 / 189
-// and 896 -> 4864 with 128 tokens 15 / 17, 15 / 17, 18 / 20, 19 / 15.  fp16 with NF4 or FP4 is streamed up to 128 whatever the
-// size: it keeps the weights in two terms or scales their sums, where the dense kernel rounds them to 2^-11.
+//                      896 -> 4864   1536 -> 8960   4096 -> 11008  8192 -> 28672
+//   64 tokens   INT4    11 / 17       18 / 27        51 / 57        142 / 170
+//               FP4     11 / 23       19 / 42        52 / 98        144 / 299
+//               NF4     13 / 26       24 / 53        67 / 124       229 / 354
+//               MXFP4   11 / 15       21 / 24        63 / 50        173 / 157      32 tokens  36 / 50   106 / 149
+//   128 tokens  INT4    15 / 17       30 / 34        67 / 61        252 / 205
+//               FP4     15 / 26       37 / 42        77 / 94        277 / 369
+//               NF4     19 / 33       49 / 46       107 / 111       402 / 414
+//               INT4A   16 / 28       33 / 42        76 / 100       288 / 360
+//               MXFP4   19 / 15       41 / 31        92 / 57        332 / 180      96 tokens  19 / 15    41 / 31 (small ones)
+// (a launch has up to 128 tokens in one pass: 192 tokens of NF4 91 / 70, 208 / 137.)
 bool gated_few(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
   const int w = fmt_weight(fmt);
-  const bool inexact = fmt_xtype(fmt) == kF16 && (w == kNF4 || w == kFP4);
-  const int64_t large = w == kMXFP4 ? 0 : w == kNF4 || w == kFP4 ? (int64_t)1 << 24 : (int64_t)1 << 25;
-  const int64_t most = !inexact && 2 * inter * hidden >= large ? 64 : 128;
+  const bool large = 2 * inter * hidden >= (int64_t)1 << 25;
+  const int64_t most = w == kMXFP4 ? (large ? 32 : 64) : w == kINT4 && large ? 64 : 128;
   return tokens <= most && gated_mfma_fits(fmt, inter, hidden, tokens);
 }
 
@@ -299,7 +303,7 @@ hipError_t launch_gated(int fmt, int act, const uint16_t* x, const uint8_t* pack
   d.xh = reinterpret_cast<uint16_t*>(base + g.xh);
   d.x_exp = reinterpret_cast<int*>(base + g.x_exp);
   d.t = (uint32_t)tokens;
-  const bool fold = gated_packed(fmt, tokens);
+  const bool fold = gated_packed(fmt, tokens, hidden, inter);
   const uint32_t per = kDecodeThreads / 64, token_rows = convert ? d.t : 0;
   const dim3 grid(fold ? (token_rows + per - 1) / per + (d.n + kFoldRows - 1) / kFoldRows
                        : (d.n + token_rows + per - 1) / per);

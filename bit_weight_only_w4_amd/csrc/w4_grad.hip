@@ -255,17 +255,19 @@ __global__ void __launch_bounds__(256) transpose_kernel(TransposeArgs p) {
 
 // How many tokens take the packed weights decoded in registers (w4_grad_few.h).  Microseconds there / by the dense
 // kernel decoding them itself:
-//                   4096 x 4096   28672 x 4096   896 x 4864
-//   32  FP4 bf16    14.0 / 15.5     37 / 47     10.7 / 15.5
-//       INT4 fp16   18.0 / 19.3     58 / 55     12.6 / 19.7
-//   64  FP4 bf16    19.9 / 17.9     49 / 51     15.9 / 15.6
-//       INT4 fp16   26.0 / 21.8     76 / 58     18.2 / 20.0
-// fp16 with NF4 or FP4 goes on to 64, though up to 15% slower there (NF4 28672 x 4096 80 / 69, 4096 x 4096 26 / 25): two
-// terms keep their weights to 2^-16, the other way they are rounded to 2^-11.
-int64_t few_tokens(int fmt) {
-  const int w = fmt_weight(fmt);
-  return fmt_xtype(fmt) == kF16 && (w == kNF4 || w == kFP4) ? 64 : 32;
-}
+//                   4864 x 896   1536 x 8960  4096 x 4096  17920 x 1536  28672 x 4096
+//   33  INT4 fp16    18 / 17      19 / 20      20 / 20      30 / 26       67 / 54
+//       MXFP4 bf16   16 / 13      14 / 16      16 / 15      21 / 21       39 / 45
+//       INT4 bf16    17 / 17      16 / 20      18 / 20      26 / 28       49 / 57
+//   64  INT4 fp16    21 / 17      23 / 22      24 / 22      34 / 26       73 / 56
+//       MXFP4 bf16   18 / 14      18 / 16      20 / 17      25 / 21       44 / 47
+//       MXFP4 fp16   19 / 19      20 / 22      22 / 23      29 / 29       52 / 59
+//       INT4 bf16    19 / 18      20 / 22      22 / 22      29 / 30       53 / 58
+//       INT4A fp16   21 / 21      23 / 30      24 / 29      34 / 39       73 / 93
+//       FP4 fp16     22 / 20      25 / 27      26 / 27      39 / 36       87 / 89
+//       NF4 bf16     21 / 24      23 / 32      25 / 33      35 / 48       71 / 106
+// The first two have one term there and d as it is.  At 17 tokens all are faster here (INT4 fp16 28672 x 4096 51 / 53).
+int64_t few_tokens(int fmt) { return grad_few_most(fmt_weight(fmt), fmt_xtype(fmt)); }
 
 // Splits of N for a few tokens: as many as give every CU a workgroup of 128 columns, each at least a step of 32 rows
 // for each of its eight waves.  16 tokens of NF4 1536 x 8960 take 11.5 us, with twice and half as many splits 13.8 and 14.9;

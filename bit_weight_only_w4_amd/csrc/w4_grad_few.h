@@ -270,7 +270,7 @@ hipError_t grad_few_launch(const GradFewArgs& a, uint32_t splits, hipStream_t s)
     grad_few_kernel<FMT, XT, 1><<<grid, block, 0, s>>>(a);
   else if (a.b <= 32)
     grad_few_kernel<FMT, XT, 2><<<grid, block, 0, s>>>(a);
-  else if constexpr (XT == kF16 && (FMT == kNF4 || FMT == kFP4))  // up to 64
+  else if constexpr (grad_few_most(FMT, XT) > 32)
     grad_few_kernel<FMT, XT, 4><<<grid, block, 0, s>>>(a);
   else
     return hipErrorInvalidValue;
