@@ -231,8 +231,10 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const uint16_t* dh, con
   uint16_t* to = dp + t * 2 * inter + c;
   auto one = [&](uint16_t dv, uint16_t gv, uint16_t uv, uint16_t& og, uint16_t& ou) __attribute__((always_inline)) {
     float slope;
-    const float y = act_slope<ACT>(from16<XT>(gv), &slope), f = from16<XT>(dv);
-    og = (uint16_t)to16<XT>(f * from16<XT>(uv) * slope);
+    const float y = act_slope<ACT>(from16<XT>(gv), &slope), f = from16<XT>(dv), u = from16<XT>(uv);
+    // The slope is at most 1.13: times it first a large u, then f u of a small one, so that neither leaves the range
+    // where the whole does not.
+    og = (uint16_t)to16<XT>(fabsf(u) >= 1.0f ? f * (u * slope) : f * u * slope);
     ou = (uint16_t)to16<XT>(f * y);
   };
   if (c + 8 > inter) {
