@@ -1347,7 +1347,7 @@ int w4_gated(const void* x, const uint8_t* gate_up, const void* gate_up_scales, 
   if (st == W4_ERR_FORMAT || !valid_act(act)) return W4_ERR_FORMAT;
   if (!x || !gate_up || !gate_up_scales || !h) return W4_ERR_NULL;
   if (st != W4_OK) return st;
-  if (!aligned(x, 16) || !aligned(gate_up, 16) || !aligned(gate_up_scales, 4) || !aligned(h, 2) ||
+  if (!aligned(x, 16) || !aligned(gate_up, 16) || !aligned(gate_up_scales, fmt_scale_bytes(fmt)) || !aligned(h, 2) ||
       (products && !aligned(products, 2)))
     return W4_ERR_ALIGN;
   const size_t used = gated_workspace(fmt, tokens, hidden, inter);

@@ -596,7 +596,7 @@ typedef enum { W4_F32 = 0, W4_F16 = 1, W4_BF16 = 2 } w4_type_t;
  *   x         device [tokens, hidden] fp16 or bf16 (per fmt); 16-byte aligned
  *   gate_up   device uint8[2 * inter, hidden / 2]: the gate rows, then the up rows, packed as for w4_gemv;
  *             16-byte aligned
- *   gate_up_scales  the format's scales [2 * inter, ...]; 4-byte aligned
+ *   gate_up_scales  the format's scales [2 * inter, ...]; aligned as for w4_gemv
  *   fmt       any w4_format_t
  *   act       w4_act_t
  *   tokens    1 <= tokens <= W4_MAX_BATCH

@@ -29,3 +29,24 @@ def test_gated_grad_of_large_and_small_factors(act):
     inside = ref.abs() + bound < 3.38e38
     assert ((got - ref).abs() <= bound)[inside].all()
     assert inside.sum() > 600
+
+
+@pytest.mark.parametrize("fmt", ["int4_f16", "int4_bf16", "mxfp4_f16", "mxfp4_bf16"])
+@pytest.mark.parametrize("tokens,steps,inter", [(1, 3, 41), (1, 17, 130), (5, 3, 17), (40, 5, 33), (100, 3, 70), (200, 3, 65),
+                                                (600, 3, 65)])
+def test_gated_scales_two_bytes_into_a_dword(fmt, tokens, steps, inter):
+    """Two-byte scales at an address that is no multiple of four, as every other call takes them."""
+    w4, dev, dtype = _w4(), f.device(), f.DTYPES[fmt.split("_")[1]]
+    p, s, hat = f.weights(fmt, 2 * inter, steps * f.group(fmt), tokens)
+    x = f.normal((tokens, steps * f.group(fmt)), dtype, 2)
+    raw = s.contiguous().view(torch.uint8).flatten()
+    flat = torch.full((raw.numel() + 8,), 255, dtype=torch.uint8, device=dev)
+    flat[2:2 + raw.numel()] = raw.to(dev)
+    at = flat[2:2 + raw.numel()].view(s.dtype).view(s.shape)
+    assert at.data_ptr() % 4 == 2
+    h, pr = w4.gated(x.to(dev), p.to(dev), at, fmt, "silu", save=True)
+    ref, eh, both, ep = f.gated_bound(x, hat, "silu", dtype)
+    f.check(h, ref, eh)
+    f.check(pr, both, ep)
+    h2, pr2 = w4.gated(x.to(dev), p.to(dev), s.to(dev), fmt, "silu", save=True)
+    assert torch.equal(h, h2) and torch.equal(pr, pr2)
