@@ -408,14 +408,13 @@ __global__ void __launch_bounds__(kGroupThreads * KW, 2) gemm_kernel(GemmArgs a)
 
 template <int FMT, int XT, int WN, int WM, int KW, bool GROUPED>
 hipError_t launch_wm(const GemmArgs& a, hipStream_t s) {
-  static bool raised = false;
   constexpr int lds = KW * 2 * stage_bytes<WM>();
   static_assert(KW == 1 || (KW - 1) * 4 * WN * WM * 64 * 16 <= lds, "K-group sums fit the stages");
-  if (!raised) {
-    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&gemm_kernel<FMT, XT, WN, WM, KW, GROUPED>),
-                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-    raised = true;
-  }
+  // once, whichever of several threads comes first
+  static const hipError_t raised =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(&gemm_kernel<FMT, XT, WN, WM, KW, GROUPED>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  (void)raised;
   hipLaunchKernelGGL((gemm_kernel<FMT, XT, WN, WM, KW, GROUPED>),
                      dim3(a.tiles, (a.k / 64 + a.bps - 1) / a.bps), dim3(kGroupThreads * KW), lds, s, a);
   return hipGetLastError();

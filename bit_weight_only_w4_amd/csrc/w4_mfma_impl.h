@@ -627,16 +627,17 @@ mfma_kernel(typename std::conditional<GATED, MfmaGatedArgs, MfmaArgs>::type a) {
 // K groups instantiated for T batch tiles: 8 / 4 / 2 / 1.
 constexpr int max_kw(int t) { return t == 1 ? 8 : t == 2 ? 4 : t == 4 ? 2 : 1; }
 
+inline bool raise_lds_limit(const void* f) {
+  return hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kLdsBytes - kTableBytes) == hipSuccess;
+}
+
 // Workgroups of one instantiation that fit a CU with `lds` bytes of dynamic LDS (registers and
 // LDS), from the runtime; the dynamic LDS limit is raised once per instantiation.
 template <int FMT, int XT, int T, int KW, bool GROUPED>
 int resident_kw(int lds) {
-  static bool raised = false;
-  if (!raised) {
-    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&mfma_kernel<FMT, XT, T, KW, GROUPED>),
-                              hipFuncAttributeMaxDynamicSharedMemorySize, kLdsBytes - kTableBytes);
-    raised = true;
-  }
+  // once, whichever of several threads comes first
+  static const bool raised = raise_lds_limit(reinterpret_cast<const void*>(&mfma_kernel<FMT, XT, T, KW, GROUPED>));
+  (void)raised;
   int nb = 0;
   if (hipOccupancyMaxActiveBlocksPerMultiprocessor(
           &nb, reinterpret_cast<const void*>(&mfma_kernel<FMT, XT, T, KW, GROUPED>), kThreads, lds) !=
@@ -714,11 +715,8 @@ template <int FMT, int XT, int T, int KW>
 hipError_t gated_kw(int op, const MfmaGatedArgs& a, int lds, int grid, int slices, int* out, hipStream_t s) {
   const void* f = reinterpret_cast<const void*>(&mfma_kernel<FMT, XT, T, KW, false, true>);
   if (op == 0) {
-    static bool raised = false;
-    if (!raised) {
-      (void)hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kLdsBytes - kTableBytes);
-      raised = true;
-    }
+    static const bool raised = raise_lds_limit(f);
+    (void)raised;
     return hipOccupancyMaxActiveBlocksPerMultiprocessor(out, f, kThreads, lds);
   }
   mfma_kernel<FMT, XT, T, KW, false, true>

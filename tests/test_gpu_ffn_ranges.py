@@ -1,4 +1,6 @@
 """Gated block and its gradients at the ends of their types' ranges, and operands at addresses of their own."""
+import threading
+
 import pytest
 import torch
 
@@ -50,3 +52,34 @@ def test_gated_scales_two_bytes_into_a_dword(fmt, tokens, steps, inter):
     f.check(pr, both, ep)
     h2, pr2 = w4.gated(x.to(dev), p.to(dev), s.to(dev), fmt, "silu", save=True)
     assert torch.equal(h, h2) and torch.equal(pr, pr2)
+
+
+def test_first_calls_of_several_threads():
+    """Threads that make their first calls at the same time, of sizes that no other test launches."""
+    w4, dev = _w4(), f.device()
+    cases = []
+    for i, (fmt, tokens, steps) in enumerate((("int4a_f16", 9, 2), ("int4a_f16", 30, 2), ("fp4_bf16", 50, 3), ("mxfp4_f16", 13, 1),
+                                              ("nf4_f16", 100, 2), ("nf4_bf16", 19, 4), ("int4_bf16", 61, 5), ("int4_f16", 200, 3))):
+        p, s, hat = f.weights(fmt, 2 * 45, steps * f.group(fmt), i)
+        x = f.normal((tokens, steps * f.group(fmt)), f.DTYPES[fmt.split("_")[1]], i + 1)
+        cases.append((fmt, x, p.to(dev), s.to(dev), hat, x.to(dev)))
+    torch.cuda.synchronize()
+    start, out = threading.Barrier(2 * len(cases)), {}
+
+    def call(k):
+        fmt, _, p, s, _, x = cases[k % len(cases)]
+        stream = torch.cuda.Stream()
+        start.wait()
+        out[k] = w4.gated(x, p, s, fmt, stream=stream)
+        stream.synchronize()
+
+    threads = [threading.Thread(target=call, args=(k,)) for k in range(2 * len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for k in range(len(cases)):
+        fmt, x, _, _, hat, _ = cases[k]
+        ref, eh, _, _ = f.gated_bound(x, hat, "silu", x.dtype)
+        f.check(out[k], ref, eh)
+        assert torch.equal(out[k], out[k + len(cases)])
