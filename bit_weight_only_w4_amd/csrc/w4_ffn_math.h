@@ -173,11 +173,15 @@ __device__ inline void decode_pair(uint32_t v, int j, const float* table, BlockS
   }
 }
 
-// Exponent e with |s code| 2^-e < 2^15 for every code of the format: the largest fp16 binade.
+// Exponent e with s c 2^-e in [2^14, 2^15), c the largest code of the format: fp16's highest binade but one.  What lies
+// within 2^28 below s c is a normal number then; smaller weights are off by at most half of fp16's smallest step, 2^-25,
+// which is 2^-39 of s c at most.
 template <int FMT>
 __device__ inline int fold_exponent(float s) {
-  constexpr int c = FMT == kNF4 ? 0 : FMT == kINT4A ? 4 : 3;  // |code| <= 2^c
-  return s > 0.0f ? ilogbf(s) + 1 + c - 15 : 0;
+  constexpr float c = FMT == kNF4 ? 1.0f : FMT == kINT4 ? 8.0f : FMT == kINT4A ? 15.0f : 6.0f;
+  if (!(s > 0.0f)) return 0;
+  const int e = ilogbf(s);
+  return e + ilogbf(ldexpf(s, -e) * c) - 14;  // (s c itself may leave the range)
 }
 
 __device__ inline float wave_max(float v) {

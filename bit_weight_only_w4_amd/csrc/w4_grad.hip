@@ -2,10 +2,13 @@
 //
 // The sum runs over the weight rows, along which a packed byte holds nothing: the weights are decoded once into W_hat^T
 // rows of 16 bits in the workspace (through LDS), which the dense kernel multiplies with d, or, where that costs less, the
-// dense kernel decodes and transposes them as they arrive (PackedColumns in w4_dense_sources.h).  A weight is rounded
-// once to d's type (2^-8 of itself in bf16, 2^-11 in fp16; fp16 with one exponent for the whole matrix, taken from its
-// largest scale, so that neither large nor small weights leave its range).  Rows of W_hat^T are padded with zeros to whole
-// steps of the dense kernel, and so is d where its rows do not end on one or are not aligned.
+// dense kernel decodes and transposes them as they arrive (PackedColumns in w4_dense_sources.h).  Both types of d are
+// multiplied in fp16, bf16 d as d 2^-e with one e a token (exact), weights as w 2^-f with one f for each unit of 64 columns
+// (128 of the integer formats), taken from its largest scale, so that neither large nor small weights leave fp16's range
+// and no column suffers from another's scales.  INT4 and MXFP4 weights fit one fp16 number, the others are the sum of two
+// (first_term in w4_ffn_math.h); bf16 would hold them to 2^-8 and need three.  MXFP4 with bf16 d is multiplied in bf16,
+// which holds its weights whole and needs no exponents.  Rows of W_hat^T are padded with zeros to whole steps of the
+// dense kernel, and so is d where its rows do not end on one or are not aligned.
 #include <algorithm>
 #include <type_traits>
 

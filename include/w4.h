@@ -608,13 +608,15 @@ typedef enum { W4_F32 = 0, W4_F16 = 1, W4_BF16 = 2 } w4_type_t;
  *   workspace device memory of at least w4_gated_workspace_bytes(...) bytes, 16-byte aligned; may be NULL when
  *             that is 0; scratch on entry and exit; two calls in flight must not share it
  * No output may overlap an input, the other output or the workspace, nor the workspace an input.  fp32
- * accumulation, g and u rounded to x's type for `products` alone.  Where a workspace is needed (from 65 or 129
- * tokens on) the weights enter as fp16 numbers of a common exponent a row (at most 2^-11 of themselves off; INT4 and
- * MXFP4 exact) and bf16 tokens as fp16 numbers of a common exponent a token (exact), in both what lies more than
- * 2^29 below the row's largest by at most 2^-39 of that.  Infinities and NaN stay in their token's (a scale's: in its channel's) results, where the formula
- * has them; without a workspace an infinite token of asymmetric INT4 gives NaN for some of its infinite products (its
- * zero points are taken off as z times the token's sum), with one any does for a weight that became 0 under its
- * row's exponent.  The order of every sum is fixed.  Asynchronous on `stream`. */
+ * accumulation, g and u rounded to x's type for `products` alone.  A weight enters as it is (codes whole, the scale in
+ * fp32 on its block's sum) or, where a workspace is needed (from 33, 65 or 129 tokens on), as one fp16 number (INT4,
+ * MXFP4: exact) or the sum of two (within 2^-20 of itself), all of a row under one exponent; bf16 tokens as fp16 numbers
+ * under one exponent a token there (one token of NF4: for each 32 of its values).  What lies more than 2^28 below the
+ * largest is off by at most 2^-39 of that: of a row, of its largest scale times the format's largest code (NF4 1, E2M1 6,
+ * INT4 8, asymmetric 15), of a token, of its largest value.  Infinities and NaN stay in their token's (a scale's: in its
+ * channel's) results, where the formula has them; without a workspace an infinite token of asymmetric INT4 gives NaN for
+ * some of its infinite products (its zero points are taken off as z times the token's sum), with one any does for a
+ * weight more than 2^28 below its row's largest.  The order of every sum is fixed.  Asynchronous on `stream`. */
 int w4_gated(const void* x, const uint8_t* gate_up, const void* gate_up_scales, int fmt, int act, int64_t tokens,
              int64_t hidden, int64_t inter, void* h, void* products, void* workspace, size_t workspace_bytes,
              void* stream);
@@ -645,10 +647,15 @@ int w4_gated_grad(const void* dh, const void* products, int type, int act, int64
  *            workspace
  *   workspace  device memory of at least w4_gemm_grad_workspace_bytes(...) bytes, 16-byte aligned; scratch on
  *            entry and exit; must not overlap an input; two calls in flight must not share it
- * A weight is rounded once to d's type (bf16 2^-8, fp16 2^-11 of itself, fp16 with one exponent for all of W: what
- * lies more than 2^29 below the largest scale by at most 2^-39 of that), the sums are fp32 in a fixed order, dx is
- * rounded once.  Infinities and NaN of d stay in their row, where the formula has them; what an infinite or NaN scale
- * gives stays in its block's columns (NaN, or the formula's infinity).  Asynchronous on `stream`. */
+ * A weight enters as the sum of one to three bf16 numbers (up to 32 tokens of INT4 with fp16 and of MXFP4 with bf16, 64 of
+ * the others; MXFP4 with bf16 always) or of one or two fp16 numbers under one exponent for each 64 columns (INT4 and
+ * asymmetric INT4 128), with bf16 d as fp16 numbers under one exponent a token.  MXFP4 and INT4 weights (and asymmetric
+ * ones in bf16) are exact so, the others within 2^-20 of themselves; under exponents what lies more than 2^28 below the
+ * largest is off by at most 2^-39 of that: of the columns, of their largest scale times the format's largest code (as for
+ * w4_gated), of a token, of its largest value.  The sums are fp32 in a fixed order, dx is rounded once.  Infinities and
+ * NaN of d stay in their row, where the formula has them (but NaN for an infinite product with a weight more than 2^28
+ * below its columns' largest, where there are exponents); what an infinite or NaN scale gives stays in its block's columns
+ * (NaN, or the formula's infinity).  Asynchronous on `stream`. */
 int w4_gemm_grad(const void* d, const uint8_t* packed, const void* scales, int fmt, int64_t N, int64_t K, int64_t B,
                  void* dx, void* workspace, size_t workspace_bytes, void* stream);
 

@@ -83,3 +83,74 @@ def test_first_calls_of_several_threads():
         ref, eh, _, _ = f.gated_bound(x, hat, "silu", x.dtype)
         f.check(out[k], ref, eh)
         assert torch.equal(out[k], out[k + len(cases)])
+
+
+LARGEST = {"nf4": 1.0, "fp4": 6.0, "mxfp4": 6.0, "int4": 8.0, "int4a": 15.0}
+
+
+def _spread(fmt, rows, blocks, seed):
+    """Random codes; a row's first block has a scale of 1 to 2, block j one 2^(20 + j) times smaller.  Also the largest
+    weight that each row's scales allow."""
+    weight = fmt.split("_")[0]
+    g = f.group(fmt)
+    gen = torch.Generator().manual_seed(seed)
+    p = torch.randint(0, 256, (rows, blocks * g // 2), generator=gen, dtype=torch.uint8)
+    down = torch.arange(blocks).double() + 20
+    down[0] = 0
+    s = (1 + torch.rand(rows, blocks, generator=gen, dtype=torch.float64)) * 2.0 ** -down
+    s = s.float()
+    if weight == "mxfp4":
+        e = (127 - down.long()).expand(rows, blocks).repeat_interleave(2, dim=1)
+        return p, e.to(torch.uint8).contiguous(), torch.full((rows,), 6.0, dtype=torch.float64)
+    if weight.startswith("int4"):
+        bits = s.view(torch.int32) >> 16
+        top = (bits[:, 0] << 16).view(torch.float32).double() * LARGEST[weight]
+        if weight == "int4":
+            return p, bits.to(torch.int16), top
+        return p, bits | torch.randint(0, 16, bits.shape, generator=gen, dtype=torch.int32) << 16, top
+    return p, s, s[:, 0].double() * LARGEST[weight]
+
+
+@pytest.mark.parametrize("weight", ["nf4", "fp4", "mxfp4", "int4", "int4a"])
+@pytest.mark.parametrize("tokens", [192, 700])
+def test_gated_weights_far_below_the_largest(weight, tokens):
+    """Weights read out one by one, down to 2^36 below the row's largest scale: off by at most 2^-20 of themselves, or 2^-39
+    of what the row's largest scale and the format's largest code allow."""
+    w4, dev, fmt = _w4(), f.device(), f"{weight}_bf16"
+    g, blocks, inter = f.group(fmt), 16, 24
+    p, s, top = _spread(fmt, 2 * inter, blocks, tokens)
+    hat = f.as_operands(fmt, p.numpy(), s.numpy().view({"int4": "uint16", "int4a": "uint32"}.get(weight, s.numpy().dtype)))[2]
+    cols = torch.arange(tokens) * 37 % (blocks * g)
+    x = torch.zeros(tokens, blocks * g, dtype=torch.bfloat16)
+    x[torch.arange(tokens), cols] = 1.0
+    _, pr = w4.gated(x.to(dev), p.to(dev), s.to(dev), fmt, save=True)
+    ref = hat.double()[:, cols].t()
+    e = ref.abs() * 2.0 ** -20 + 2.0 ** -39 * top
+    f.check(pr, ref, e + f.rounded(ref.abs() + e, torch.bfloat16))
+
+
+@pytest.mark.parametrize("weight,xt", [("nf4", "bf16"), ("fp4", "bf16"), ("mxfp4", "bf16"), ("int4", "bf16"), ("int4a", "bf16")])
+@pytest.mark.parametrize("tokens,rows", [(100, 40), (70, 16000)])
+def test_gradient_weights_far_below_the_largest(weight, xt, tokens, rows):
+    """The same along the weight rows, which share an exponent with the other rows of their columns only; some columns
+    have small weights alone, and nothing is lost there."""
+    w4, dev, fmt = _w4(), f.device(), f"{weight}_{xt}"
+    g, groups = f.group(fmt), 5
+    p, s, top = _spread(fmt, groups, rows, tokens + 1)
+    p = p.view(groups, rows, g // 2).transpose(0, 1).reshape(rows, groups * g // 2).contiguous()
+    per = s.shape[1] // rows
+    s = s.view(groups, rows, per).transpose(0, 1).reshape(rows, groups * per).contiguous()
+    if rows > 1000:  # (the scales of most rows would be 0)
+        s[40:] = s[torch.arange(40, rows) % 39 + 1]
+    first = {"mxfp4": 60, "int4": 0x2000, "int4a": 0x2000}.get(weight, 2.0 ** -60)
+    s[:, -per:] = first  # the last group's: small in every row
+    top[-1] = LARGEST[weight] * (2.0 ** -67 if weight == "mxfp4" else float(torch.tensor(0x2000 << 16, dtype=torch.int32).view(
+        torch.float32)) if weight.startswith("int4") else 2.0 ** -60)
+    hat = f.as_operands(fmt, p.numpy(), s.numpy().view({"int4": "uint16", "int4a": "uint32"}.get(weight, s.numpy().dtype)))[2]
+    at = torch.arange(tokens) % min(rows, 40) if rows < 1000 else torch.arange(tokens) * 131 % rows
+    d = torch.zeros(tokens, rows, dtype=torch.bfloat16)
+    d[torch.arange(tokens), at] = 1.0
+    dx = w4.gemm_grad(d.to(dev), p.to(dev), s.to(dev), fmt)
+    ref = hat.double()[at]
+    e = ref.abs() * 2.0 ** -20 + 2.0 ** -39 * top.repeat_interleave(g)
+    f.check(dx, ref, e + f.rounded(ref.abs() + e, torch.bfloat16))
