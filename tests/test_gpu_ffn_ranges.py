@@ -154,3 +154,35 @@ def test_gradient_weights_far_below_the_largest(weight, xt, tokens, rows):
     ref = hat.double()[at]
     e = ref.abs() * 2.0 ** -20 + 2.0 ** -39 * top.repeat_interleave(g)
     f.check(dx, ref, e + f.rounded(ref.abs() + e, torch.bfloat16))
+
+
+@pytest.mark.parametrize("tokens", [1, 3, 200])
+@pytest.mark.parametrize("hidden", [1536, 4096, 6144])
+@pytest.mark.parametrize("power", [-127, -118, -60, 90])
+def test_gated_tokens_at_the_ends_of_bf16(tokens, hidden, power):
+    """bf16 tokens near the smallest and the largest of their type, brought back by the weights' scales."""
+    w4, dev, fmt = _w4(), f.device(), "nf4_bf16"
+    p, s, _ = f.weights(fmt, 2 * 20, hidden, 3)
+    s = (s * 2.0 ** min(-power, 120)).contiguous()
+    hat = f.as_operands(fmt, p.numpy(), s.numpy())[2]
+    x = (f.normal((tokens, hidden), torch.float64, 4) * 2.0 ** power).to(torch.bfloat16)
+    h, pr = w4.gated(x.to(dev), p.to(dev), s.to(dev), fmt, "silu", save=True)
+    ref, eh, both, ep = f.gated_bound(x, hat, "silu", torch.bfloat16)
+    f.check(pr, both, ep)
+    f.check(h, ref, eh)
+
+
+def test_gated_tokens_subnormal_chunks_read_out():
+    """One number in the smallest of bf16 in each chunk of a long token: nothing of it is lost."""
+    w4, dev, fmt, hidden = _w4(), f.device(), "nf4_bf16", 4096
+    p, s, _ = f.weights(fmt, 2 * 20, hidden, 5)
+    s = (s * 2.0 ** 120).contiguous()
+    hat = f.as_operands(fmt, p.numpy(), s.numpy())[2].double()
+    for at, value in ((0, 2.0 ** -126), (33, 3 * 2.0 ** -133), (4095, 2.0 ** -120), (64, -2.0 ** -133), (1000, 1.9921875 * 2.0 ** -115)):
+        x = torch.zeros(1, hidden, dtype=torch.bfloat16)
+        x[0, at] = value
+        x[0, at ^ 1] = value * 2.0 ** -6 if value > 2.0 ** -125 else 0.0
+        _, pr = w4.gated(x.to(dev), p.to(dev), s.to(dev), fmt, "silu", save=True)
+        ref = x.double() @ hat.t()
+        e = 2.0 ** -22 * (x.double().abs() @ hat.abs().t())
+        f.check(pr, ref, e + f.rounded(ref.abs() + e, torch.bfloat16))
