@@ -769,8 +769,8 @@ def gated(x, gate_up, gate_up_scales, fmt, act="silu", save=False, h=None, produ
 
     x [T, H] of the format's activation type; gate_up uint8 [2 I, H/2] (gate rows, then up rows) with the
     format's scales [2 I, H/g].  With save=True (or `products` given) it returns (h, products), products [T, 2 I] of x's type
-    holding g | u, which gated_grad takes.  `workspace` is a uint8 tensor of gated_workspace_bytes(...),
-    allocated by the call if not given and needed."""
+    holding g | u, which gated_grad takes; results carry no autograd graph.  `workspace` is a uint8 tensor of
+    gated_workspace_bytes(...), allocated by the call if not given and needed."""
     torch = _torch or _load_torch()
     a = ACTS.get(act)
     spec = _FORMAT_SPECS.get(fmt) or _format_spec(fmt)
@@ -839,7 +839,8 @@ def gemm_grad_workspace_bytes(fmt, n, k, b) -> int:
 
 def gemm_grad(d, packed, scales, fmt, dx=None, workspace=None, stream=None):
     """The input gradient of a product with frozen 4-bit weights: dx [B, K] = d [B, N] . W_hat, of d's type (the
-    format's activation type).  `workspace` is a uint8 tensor of gemm_grad_workspace_bytes(...), allocated by the
+    format's activation type).  The backward pass of gated is gemm_grad(gated_grad(dh, products), gate_up, ...), to be
+    called by the user's autograd function: none of these calls is recorded.  `workspace` is a uint8 tensor of gemm_grad_workspace_bytes(...), allocated by the
     call if not given and needed."""
     torch = _torch or _load_torch()
     code, dtype, stype, group = _FORMAT_SPECS.get(fmt) or _format_spec(fmt)

@@ -1282,7 +1282,7 @@ int gated_shape(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
 }
 
 // w4_gated in one launch: the fused GEMV for one token where it has a launch shape, else the MFMA kernel.  (One token with
-// the one and the other, us: NF4 1536 -> 8960 7.7 / 10.3, 4096 -> 14336 17.2 / 25.5, 512 -> 256 3.6 / 4.8; INT4 6.7 / 9.6, 15.3 /
+// the one and the other, us: NF4 1536 -> 8960 7.2 / 13.0, 4096 -> 14336 18.2 / 30.7, 512 -> 256 3.4 / 5.0; INT4 6.7 / 9.6, 15.3 /
 // 19.4; MXFP4 6.5 / 11.9, 15.2 / 25.7.)
 hipError_t run_gated_few(int fmt, int act, const uint16_t* x, const uint8_t* packed, const void* scales, int64_t tokens,
                          int64_t hidden, int64_t inter, uint16_t* h, uint16_t* products, hipStream_t s) {
@@ -1302,9 +1302,9 @@ hipError_t run_gated_few(int fmt, int act, const uint16_t* x, const uint8_t* pac
   GemvPlan p;
   if (tokens > 1 || !plan_gemv(2 * inter, hidden, 1, 1, &p) || p.iters > 3)
     return launch_gated_mfma(fmt, a, hidden, tokens, s);
-  // Pairs of rows change how many workgroups serve best.  Two chunks a lane: one per CU (4096 -> 11008 NF4 17.3 to 15.1 us,
+  // Pairs of rows change how many workgroups serve best.  Two chunks a lane: one per CU (4096 -> 11008 NF4 18.4 to 16.3 us,
   // INT4 15.4 to 13.5, MXFP4 15.0 to 13.0; with three chunks 5120 -> 13824 would go from 22.9 to 26.1).  Large matrices,
-  // whose plan has one per CU, with a table and teams of two waves and more: twice as many (8192 -> 28672 NF4 60 to 52, INT4
+  // whose plan has one per CU, with a table and teams of two waves and more: twice as many (8192 -> 28672 NF4 59 to 54, INT4
   // 55 to 48; 4096 -> 28672, teams of a wave, 29 to 31; without a table MXFP4 46 to 49).
   const int cus = (int)device_cu_count(), w = fmt_weight(fmt);
   if (p.cap > cus)

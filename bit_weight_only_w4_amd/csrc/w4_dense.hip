@@ -16,6 +16,8 @@ namespace w4 {
 // the others, whose rows of B meet fewer of A, 1.18 times that (160 and 256 tokens of 1536 -> 8960 to 8192 -> 28672).
 // Decoding columns: 1.07 (FP4, INT4), 1.1 (MXFP4) or 1.25 (NF4), 1.12 times that for 128 x 256, 2.2 and 1.62 for 64 x 128
 // (4096 x 2048 weights, 256 and 2048 tokens: a step of 64 x 128 tiles alone 0.71 to 1.07 us, of full CUs 1.14 to 1.5).
+// Measured with weights of one term; of two, a step of second terms takes longer than one of first terms, which together
+// makes NF4 of 256 x 256 tiles 1.02, columns of 128 x 256 1.35 (FP4) and 1.63 (NF4).
 DensePlan plan_dense(bool gated, int64_t m, int64_t n, int64_t pitch, int packed, int terms) {
   const bool columns = packed >= 0 && !gated;
   const double slow = packed < 0         ? 1.0

@@ -109,7 +109,8 @@ __global__ void __launch_bounds__(kDecodeThreads) fold_rows_kernel(DecodeArgs p)
 }
 
 // Weight rows decoded, a wave each, then token rows.  A lane takes 8 consecutive weights of every 512 (so that a store
-// of the wave is 1 KiB in one piece; 27.5 million weights take 16 us, 4.3 TB/s), the first kHeld rounds with their scales
+// of the wave is 1 KiB in one piece; 27.5 million weights take 20 us, in two terms, 128 bytes of each in turn, 24, and 90
+// million 80, 5.1 TB/s), the first kHeld rounds with their scales
 // in flight at once; the largest of these scales is the row's unless the row is longer.
 template <int FMT>
 __global__ void __launch_bounds__(kDecodeThreads) decode_rows_kernel(DecodeArgs p) {
@@ -184,7 +185,7 @@ size_t up16(size_t v) { return (v + 15) & ~(size_t)15; }
 // Whether the dense kernel decodes the packed weights itself, by the estimates of both: it decodes them once for every tile
 // of up to 256 tokens, which makes its steps up to half as long again; the other way the weights go through memory once
 // more, at 2 bytes a term and 4 TB/s.  Microseconds, by the dense kernel / decoded first (two terms: NF4, FP4, asymmetric
-// INT4); 70 measured pairs: the rule's way is at most 20% slower than the other (NF4, 2% at the mean of all).
+// INT4); of 108 measured pairs the rule's way is at most 20% slower than the other (NF4), 1.5% at the mean.
 //                1536 -> 8960   4096 -> 11008   8192 -> 28672
 //   NF4   192      70 / 58       137 / 217       540 / 939      300  79 / 67    309 / 259  1094 / 1130
 //   NF4   512     131 / 95       231 / 313      1032 / 1387    2048 297 / 236   781 / 719  3818 / 3481
@@ -277,7 +278,7 @@ hipError_t grad_launch(const uint16_t* dh, const uint16_t* pr, uint16_t* dp, int
 //               FP4     15 / 26       37 / 42        77 / 94        277 / 369
 //               NF4     19 / 33       49 / 46       107 / 111       402 / 414
 //               INT4A   16 / 28       33 / 42        76 / 100       288 / 360
-//               MXFP4   19 / 15       41 / 31        92 / 57        332 / 180      96 tokens  19 / 15    41 / 31 (small ones)
+//               MXFP4   19 / 15       41 / 31        92 / 57        332 / 180      96 tokens  19 / 15, 41 / 31
 // (a launch has up to 128 tokens in one pass: 192 tokens of NF4 91 / 70, 208 / 137.)
 bool gated_few(int fmt, int64_t tokens, int64_t hidden, int64_t inter) {
   const int w = fmt_weight(fmt);

@@ -74,7 +74,7 @@ __device__ inline void pad_row(const uint16_t* from, uint16_t* to, uint32_t n, u
 
 // A row of bf16 d as fp16 numbers times 2^e, zeros after its end up to `np`: e puts the row's largest into fp16's highest
 // binade but one, so that all that lie within 2^28 below it are exact.  A thread keeps the first kHeld pieces of 8 between
-// the pass for the largest and the one that writes.
+// the pass for the largest and the one that writes (2048 rows of 17920 27 us with the scan beside it, 5.4 TB/s).
 constexpr int kHeld = 4;
 
 __device__ inline void convert_row(const uint16_t* from, uint16_t* to, int* exponent, uint32_t n, uint32_t np) {
@@ -177,7 +177,8 @@ struct TransposeArgs {
 // A tile of 64 rows x 256 columns a workgroup, whole cache lines of the packed rows: a thread decodes 32 columns of two
 // rows, writes them to LDS as pairs along n, and stores 16 bytes of rows of W_hat^T, one term after the other.  In LDS
 // column 32 part + j is at row 8 j + part of 40 dwords: the 64 pairs that a wave writes at once then lie in 64 banks.
-// Neighbouring workgroups take neighbouring rows, whose pieces of W_hat^T are one after another.
+// Neighbouring workgroups take neighbouring rows, whose pieces of W_hat^T are one after another.  27.5 million weights take
+// 21 us, in two terms 34 (3.7 TB/s).
 constexpr int kColumns = 256;
 
 template <int FMT, int XT>
@@ -273,8 +274,8 @@ __global__ void __launch_bounds__(256) transpose_kernel(TransposeArgs p) {
 int64_t few_tokens(int fmt) { return grad_few_most(fmt_weight(fmt), fmt_xtype(fmt)); }
 
 // Splits of N for a few tokens: as many as give every CU a workgroup of 128 columns, each at least a step of 32 rows
-// for each of its eight waves.  16 tokens of NF4 1536 x 8960 take 11.5 us, with twice and half as many splits 13.8 and 14.9;
-// 17920 x 1536 18.9, 24.3, 21.0; 28672 x 4096 37, 39, 58.
+// for each of its eight waves.  16 tokens of NF4 1536 x 8960 take 13.6 us, with twice and half as many splits 16.0 and 21.4;
+// 17920 x 1536 24.4, 28.7, 30.1; 28672 x 4096 54.8, 53.2, 88.4.
 uint32_t few_splits(int64_t n, int64_t k) {
   const int64_t groups = (k + 127) / 128, rounds = ((n + 31) / 32 + 7) / 8;
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(rounds, device_cu_count() / groups));
@@ -291,13 +292,17 @@ size_t up16(size_t v) { return (v + 15) & ~(size_t)15; }
 
 // Whether the product decodes and transposes the weights itself, by the estimates of both: it does so for every tile of up
 // to 256 tokens, and the workgroups of a split start with steps that only decode; the other way all weights are transposed
-// through memory once, 2.5 bytes each at 4 TB/s and a launch.  Microseconds, by the product / transposed first:
-//   FP4 bf16   17920 x 1536: 128 tokens 28 / 40, 512 53 / 64, 1000 88 / 84, 2048 131 / 135
-//              11008 x 4096: 128 33 / 58, 512 76 / 104, 2048 217 / 179
-//              28672 x 4096: 80 54 / 134, 512 136 / 187, 2048 465 / 464
-//              4001 x 2048: 80 19 / 22, 333 29 / 26;  4096 x 4096: 80 22 / 27, 512 38 / 36, 2048 90 / 72, 4096 128 / 118
-//   NF4 bf16   28672 x 4096: 80 60 / 132, 512 148 / 188, 2048 510 / 466;  4001 x 2048: 80 22 / 23, 333 30 / 26
-//   INT4 fp16  28672 x 4096: 80 59 / 152, 512 142 / 203, 2048 478 / 474;  17920 x 1536: 2048 133 / 142
+// through memory once, 2 bytes a term and 0.5 each at 4 TB/s and a launch.  Microseconds, by the product / transposed first:
+//              4096 x 4096   17920 x 1536  11008 x 4096  28672 x 4096
+//   NF4 bf16   80 tokens    34 / 43      62 / 70      55 / 98      109 / 286
+//              512          69 / 69     108 / 121    150 / 154     276 / 400
+//              2048        201 / 150    272 / 265    397 / 378     998 / 987
+//   FP4 fp16   512          59 / 66      87 / 112    126 / 146     242 / 381
+//              2048        162 / 141    228 / 234    352 / 355     856 / 940
+//   INT4 fp16  512          41 / 42      55 / 80      78 / 94      147 / 217
+//              2048         88 / 79     131 / 142    224 / 191     468 / 484
+//   MXFP4 bf16 512          34 / 36      48 / 62      67 / 81      127 / 187
+// Of 276 pairs of six sizes and 80 to 2048 tokens the rule's way is at most 29% slower than the other, 1% at the mean.
 bool grad_columns(int fmt, int64_t n, int64_t k, int64_t b) {
   const int64_t pitch = (n + kTile - 1) / kTile * kTile * 2;
   const int w = fmt_weight(fmt), terms = grad_terms(fmt);

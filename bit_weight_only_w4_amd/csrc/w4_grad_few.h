@@ -14,8 +14,9 @@
 //     what is left less 2^-7 of it: so all have the weight's sign and none is 0 unless the weight is, and an infinite
 //     gradient gives what it gives with the weight itself.  fp16 gradients are the sum of two bf16 numbers (exact); of
 //     the products of terms the one below 2^-20 of the whole is left out.
-//   * Bound by the chain of loads, decoding and products of a few steps and by the splits' sums on their way through
-//     memory: 16 tokens of NF4 1536 x 8960 9 us (0.9 TB/s) and 2.5 for the sum (28672 x 4096 37 us in all, 1.8 TB/s).
+//   * Bound by decoding: a weight of three terms takes some ten vector instructions, of two seven.  16 bf16 tokens of
+//     28672 x 4096, in all: NF4 55 us (1.2 TB/s), FP4 46, INT4 38, MXFP4 31; small ones also by the chain of loads of a few
+//     steps and the splits' sums: NF4 1536 x 8960 11.3 us (0.7 TB/s) and 1.7 for the sum.
 //   * The waves' sums are added in LDS, the splits' by a second kernel, both in a fixed order.
 #pragma once
 #include <type_traits>
@@ -44,7 +45,7 @@ __global__ void __launch_bounds__(64 * kGradWaves) grad_few_kernel(GradFewArgs p
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, m = lane & 15;
   // Every eighth workgroup runs on one XCD: those take neighbouring columns, whose 64 bytes of a row share cache lines
-  // (16 tokens FP4 28672 x 4096 37.5 to 32.6 us, 17920 x 1536 19.0 to 16.5).
+  // (16 tokens FP4 28672 x 4096 49 to 47 us, 17920 x 1536 23.0 to 22.2, NF4 1536 x 8960 14.3 to 13.3).
   const uint32_t groups = (p.k + 127) / 128, share = gridDim.x / 8, rem = gridDim.x % 8, xcd = blockIdx.x % 8;
   const uint32_t wg = xcd * share + min(xcd, rem) + blockIdx.x / 8, split = wg / groups;
   const uint32_t k0 = (wg - split * groups) * 128u, k = p.k, n = p.n, pitch = k / 2;

@@ -608,15 +608,16 @@ typedef enum { W4_F32 = 0, W4_F16 = 1, W4_BF16 = 2 } w4_type_t;
  *   workspace device memory of at least w4_gated_workspace_bytes(...) bytes, 16-byte aligned; may be NULL when
  *             that is 0; scratch on entry and exit; two calls in flight must not share it
  * No output may overlap an input, the other output or the workspace, nor the workspace an input.  fp32
- * accumulation, g and u rounded to x's type for `products` alone.  A weight enters as it is (codes whole, the scale in
- * fp32 on its block's sum) or, where a workspace is needed (from 33, 65 or 129 tokens on), as one fp16 number (INT4,
- * MXFP4: exact) or the sum of two (within 2^-20 of itself), all of a row under one exponent; bf16 tokens as fp16 numbers
- * under one exponent a token there (one token of NF4: for each 32 of its values).  What lies more than 2^28 below the
- * largest is off by at most 2^-39 of that: of a row, of its largest scale times the format's largest code (NF4 1, E2M1 6,
- * INT4 8, asymmetric 15), of a token, of its largest value.  Infinities and NaN stay in their token's (a scale's: in its
- * channel's) results, where the formula has them; without a workspace an infinite token of asymmetric INT4 gives NaN for
- * some of its infinite products (its zero points are taken off as z times the token's sum), with one any does for a
- * weight more than 2^28 below its row's largest.  The order of every sum is fixed.  Asynchronous on `stream`. */
+ * accumulation, g and u rounded to x's type for `products` alone.  A weight enters as it is, the scale in fp32 on its
+ * block's sum (NF4 codes with two and more fp16 tokens within 2^-21), or, where a workspace is needed (from 33, 65 or
+ * 129 tokens on), as one fp16 number (INT4, MXFP4: exact) or the sum of two (within 2^-20 of itself), all of a row
+ * under one exponent; bf16 tokens as fp16 numbers under one exponent a token there (one token of NF4: for each 32 of
+ * its values).  What lies more than 2^28 below the largest is off by at most 2^-39 of that: of a row, of its largest
+ * scale times the format's largest code (NF4 1, E2M1 6, INT4 8, asymmetric 15), of a token, of its largest value.
+ * Infinities and NaN stay in their token's (a scale's: in its channel's) results, where the formula has them; without a
+ * workspace an infinite token of asymmetric INT4 gives NaN for some of its infinite products (its zero points are taken
+ * off as z times the token's sum), with one any does for a weight more than 2^28 below its row's largest.  The order of
+ * every sum is fixed.  Asynchronous on `stream`. */
 int w4_gated(const void* x, const uint8_t* gate_up, const void* gate_up_scales, int fmt, int act, int64_t tokens,
              int64_t hidden, int64_t inter, void* h, void* products, void* workspace, size_t workspace_bytes,
              void* stream);
