@@ -59,7 +59,7 @@ __device__ inline __amdgpu_buffer_rsrc_t dense_buffer(i32x4 r) {
 // look() before its put() (NF4 asks the table some matrix instructions earlier).  first_steps() loads the first ones
 // without LDS.
 
-// a * s rounded to fp32 and to fp16, two of them in a dword, a in fp16 (the halves of c).  (scaled_pair: a in fp32.)
+// a * s rounded to fp32 and to fp16, two of them in a dword, a in fp16 (the halves of c).
 __device__ inline uint32_t scaled_halves(uint32_t c, float s) {
   uint32_t d;
   asm("v_fma_mixlo_f16 %0, %1, %2, 0 op_sel_hi:[1,0,0]" : "=v"(d) : "v"(c), "v"(s));
